@@ -1,0 +1,519 @@
+"""The 8-bit operators on the GPU against plain 64-bit references, at the sizes, masks and values
+where they can go wrong.
+
+Tolerances.  A rounding to type t is off by at most half a step, eps(t)/2 relative to the value:
+H[bf16] = 2^-8, H[f32] = 2^-24, H[e4m3] = 2^-4 (2^-10 absolute below 2^-6, in units of the block's
+factor).  A sum of K exact products accumulated in fp32 in any order is off by at most K eps
+sum|a w| with eps = 2^-23 (one rounding or truncation of the running sum for each term).
+Quantising what is given exactly is exact: compared bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as ref
+
+pytestmark = pytest.mark.gpu
+H = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+EPS32 = 2.0 ** -23
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def fp8():
+    from top_routing_grouped_gb300 import fp8 as m
+    return m
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def np64(t):
+    return t.detach().cpu().to(torch.float64).numpy() if t.dtype != torch.uint8 else t.cpu().numpy().astype(np.int64)
+
+
+def f8(n, *rest):
+    return torch.full((n, *rest), 0x55, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+
+
+def u8(*shape):
+    return torch.full(shape, 0x55, dtype=torch.uint8, device="cuda")
+
+
+def close(got, want, tol, what=""):
+    got, want, tol = np.asarray(got), np.asarray(want), np.broadcast_to(tol, np.shape(want))
+    nan = np.isnan(want)
+    np.testing.assert_array_equal(np.isnan(got), nan, err_msg=what)
+    bad = ~nan & ~(np.abs(got - want) <= tol)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}: " \
+        f"{got[bad][0]} for {want[bad][0]}, allowed {tol[bad][0]}"
+
+
+# ------------------------------------------------------------------ quantisation
+
+def awkward(n, c, dtype, seed):
+    """Values over many magnitudes, with zero blocks, infinities, NaNs, subnormals and maxima at the
+    border of two factors."""
+    x = torch.randn(n, c, generator=gen(seed)) * torch.exp2(torch.randint(-30, 30, (n, 1), generator=gen(seed + 1)).float())
+    x[0] = 0
+    if n > 1:
+        x[1, : c // 2] = 1e-40
+    if n > 2:
+        x[2, c // 2] = float("inf")
+    if n > 3:
+        x[3, c - 1] = float("nan")
+    if n > 4:
+        x[4] = 0.5
+        x[4, 0] = 448.0 * 2.0 ** 3          # exactly the largest value of a factor
+    if n > 5:
+        x[5] = 0.5
+        x[5, c // 3] = -450.0               # the next bf16 above 448
+    if n > 6:
+        x[6, :] = 3e38
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n, c, pad", [(1, 1, 0), (9, 16, 0), (7, 130, 3), (300, 128, 8), (33, 2064, 0), (8, 4096, 64),
+                                       (1000, 1000, 0)])
+def test_quantize_rows_bit_exact(fp8, dtype, n, c, pad):
+    x = awkward(n, c + pad, dtype, 3)[:, :c].cuda() if pad == 0 else awkward(n, c + pad, dtype, 3).cuda()[:, :c]
+    q, s = f8(n, c), u8(n, fp8.scale_cols(c))
+    fp8.quantize(x, q, s)
+    wq, ws = ref.quantize(np64(x))
+    np.testing.assert_array_equal(np64(s), ws)
+    np.testing.assert_array_equal(np64(q), wq)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("E, n, c", [(1, 1, 1), (3, 130, 200), (2, 128, 512), (5, 64, 144)])
+def test_quantize_weights_bit_exact(fp8, dtype, E, n, c):
+    w = awkward(E * n, c, dtype, 5).view(E, n, c).cuda()
+    q, s = f8(E, n, c), u8(E, -(-n // 128), fp8.scale_cols(c))
+    fp8.quantize_weights(w, q, s)
+    wq, ws = ref.quantize_weights(np64(w))
+    np.testing.assert_array_equal(np64(s), ws)
+    np.testing.assert_array_equal(np64(q), wq)
+
+
+def test_zero_rows_do_nothing(fp8):
+    e = torch.empty
+    fp8.quantize(e(0, 64, device="cuda"), f8(0, 64), u8(0, 4))
+    fp8.rmsnorm(e(0, 64, device="cuda"), None, out=e(0, 64, device="cuda"))
+    dw = torch.ones(64, device="cuda")
+    fp8.rmsnorm_backward(e(0, 64, device="cuda"), e(0, 64, device="cuda"), None, e(0, device="cuda"), e(0, 64, device="cuda"), dw,
+                         fp8.rmsnorm_backward_workspace(0, 64))
+    assert not dw.any()  # a sum over no rows
+    b = lambda: e(0, 64, dtype=BF, device="cuda")
+    fp8.checkpoint_save(b(), b(), f8(0, 64), u8(0, 4), f8(0, 64), u8(0, 4))
+    fp8.checkpoint_backward(f8(0, 64), u8(0, 4), f8(0, 64), u8(0, 4), b(), b(), b(), b())
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ norm
+
+def norm_tol(n64, d, dtype):
+    """n = r rstd w in fp32: the mean of d squares is off by at most d eps relative (half of it in
+    rstd), and r rstd w, the square root and the division round a handful of times."""
+    return np.abs(n64) * ((d / 2 + 8) * EPS32 + (H[dtype] if dtype is not None else 0)) + 1e-37
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n, d, pad, residual, weight", [
+    (1, 1, 0, True, True), (1, 4096, 0, True, True), (5, 100, 3, True, True), (129, 2000, 48, False, True),
+    (64, 128, 0, False, False), (700, 512, 8, True, False), (3, 8192, 0, True, True), (2, 12345, 1, True, True),
+    (2, 20000, 0, True, True)])
+def test_rmsnorm(fp8, dtype, n, d, pad, residual, weight):
+    g = gen(11)
+    x = (torch.randn(n, d + pad, generator=g) * 3).to(dtype).cuda()[:, :d]
+    res = torch.randn(n, d + 2 * pad, generator=g).to(dtype).cuda()[:, :d] if residual else None
+    w = (1 + 0.2 * torch.randn(d, generator=g)).cuda() if weight else None
+    e = lambda: torch.empty(n, d, dtype=dtype, device="cuda")
+    r, out, q, s, rstd = e(), e(), f8(n, d), u8(n, fp8.scale_cols(d)), torch.empty(n, device="cuda")
+    fp8.rmsnorm(x, w, residual=res, residual_out=r, out=out, q=q, scales=s, rstd=rstd, eps=1e-5)
+    want_r = (x.float() + res.float()).to(dtype) if residual else x
+    assert torch.equal(r, want_r)
+    v = np64(r)
+    inv = 1 / np.sqrt((v ** 2).mean(1, keepdims=True) + 1e-5)
+    n64 = v * inv * (np64(w) if weight else 1)
+    close(np64(rstd), inv[:, 0], inv[:, 0] * (d / 2 + 4) * EPS32, "rstd")
+    close(np64(out), n64, norm_tol(n64, d, dtype), "out")
+    # the bytes are those of the 64-bit norm unless a maximum lies at a border; the values are
+    # within half an e4m3 step of it in the block's own factor
+    b, wb = np64(s), ref.quantize(n64)[1]
+    kb = -(-d // 128)
+    assert (b[:, kb:] == 0).all()
+    top = np.abs(np.pad(n64, ((0, 0), (0, kb * 128 - d)))).reshape(n, kb, 128).max(2)
+    low, high = ref.scale_byte(top * (1 - d * EPS32)), ref.scale_byte(top * (1 + d * EPS32))
+    assert ((b[:, :kb] >= low) & (b[:, :kb] <= high)).all()
+    f = np.repeat(ref.scale_value(b[:, :kb]), 128, 1)[:, :d]
+    close(np64(q) * f, n64, np.abs(n64) * 2.0 ** -4 + f * 2.0 ** -10 + norm_tol(n64, d, None), "q")
+    assert ((b[:, :kb] == wb[:, :kb]).mean() > 0.99) or b.size < 200
+
+
+def test_rmsnorm_each_output_alone_and_in_place(fp8):
+    g = gen(12)
+    x, res = (torch.randn(40, 384, generator=g).to(BF).cuda() for _ in range(2))
+    w = torch.rand(384, generator=g).cuda()
+    e = lambda: torch.empty(40, 384, dtype=BF, device="cuda")
+    r, out, q, s, rstd = e(), e(), f8(40, 384), u8(40, 4), torch.empty(40, device="cuda")
+    fp8.rmsnorm(x, w, res, r, out, q, s, rstd)
+    for kw in (dict(residual_out=e()), dict(out=e()), dict(q=f8(40, 384), scales=u8(40, 4)), dict(rstd=torch.empty(40, device="cuda"))):
+        fp8.rmsnorm(x, w, res, **kw)
+        for k, t in kw.items():
+            want = dict(residual_out=r, out=out, q=q, scales=s, rstd=rstd)[k]
+            assert torch.equal(t.view(torch.uint8), want.view(torch.uint8)), k
+    for inplace in ("x", "res"):
+        xa, ra = x.clone(), res.clone()
+        o = e()
+        fp8.rmsnorm(xa, w, ra, residual_out=xa if inplace == "x" else ra, out=o)
+        assert torch.equal(xa if inplace == "x" else ra, r) and torch.equal(o, out)
+
+
+def test_rmsnorm_special_rows(fp8):
+    """A row of zeros, of one value, of the largest bf16 values, with an infinity, with a NaN."""
+    x = torch.randn(6, 300, generator=gen(13))
+    x[0] = 0
+    x[1] = -2.5
+    x[2] = 1e30
+    x[3, 7] = float("inf")
+    x[4, 299] = float("nan")
+    x = x.to(BF).cuda()
+    out, q, s = torch.empty_like(x), f8(6, 300), u8(6, 4)
+    fp8.rmsnorm(x, None, out=out, q=q, scales=s, eps=1e-6)
+    o, b = np64(out), np64(s)
+    assert (o[0] == 0).all() and (b[0] == 0).all() and (np64(q)[0] == 0).all()
+    close(o[1], np.full(300, -1.0), 2.0 ** -8 + 1e-6)
+    # the squares of 1e30 leave fp32: the sum is infinite and rstd 0, as the formula in fp32 has it
+    assert (o[2] == 0).all() and (b[2, :3] == 0).all()
+    # an infinity: rstd = 0, 0 * inf = NaN at its place and zeros elsewhere; a NaN spreads over its row
+    assert np.isnan(o[3, 7]) and (np.delete(o[3], 7) == 0).all() and b[3, 0] == 255 and (b[3, 1:3] == 0).all()
+    assert np.isnan(o[4]).all() and (b[4, :3] == 255).all()
+    assert np.isfinite(o[5]).all() and (b[5, :3] < 255).all()
+
+
+@pytest.mark.parametrize("dtype, dout", [(F32, F32), (BF, F32), (BF, BF), (F32, BF)], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("n, d, pad, dres, weight", [(1, 1, 0, False, True), (1, 4096, 0, True, True), (300, 1000, 5, True, True),
+                                                     (2000, 136, 0, False, False), (700, 2048, 8, True, True),
+                                                     (3, 12345, 0, True, True)])
+def test_rmsnorm_backward_against_the_formula(fp8, dtype, dout, n, d, pad, dres, weight):
+    g = gen(14)
+    r = (torch.randn(n, d + pad, generator=g) * 2).to(dtype).cuda()[:, :d]
+    dn = torch.randn(n, d, generator=g).to(dout).cuda()
+    w = (1 + 0.2 * torch.randn(d, generator=g)).cuda() if weight else None
+    dr = torch.randn(n, d, generator=g).to(dtype).cuda() if dres else None
+    rstd = (r.double().square().mean(1) + 1e-5).rsqrt().float()
+    dx, dw = torch.empty(n, d, dtype=dtype, device="cuda"), torch.empty(d, device="cuda")
+    fp8.rmsnorm_backward(dn, r, w, rstd, dx, dw, fp8.rmsnorm_backward_workspace(n, d), dresidual=dr)
+    v, inv, do = np64(r), np64(rstd)[:, None], np64(dn)
+    gw, xh = do * (np64(w) if weight else 1), v * inv
+    m = (gw * xh).mean(1, keepdims=True)
+    want = inv * (gw - xh * m) + (np64(dr) if dres else 0)
+    # the mean of d products is off by at most (d + 4) eps of the mean of their magnitudes
+    mag = np.abs(gw * xh).mean(1, keepdims=True)
+    tol = inv * (8 * EPS32 * (np.abs(gw) + np.abs(xh) * np.abs(m)) + np.abs(xh) * mag * (d + 4) * EPS32)
+    close(np64(dx), want, tol + (H[dtype] + 2 * EPS32) * np.abs(want) + 2 * EPS32 * (np.abs(np64(dr)) if dres else 0), "dx")
+    close(np64(dw), (do * xh).sum(0), (n + 4) * EPS32 * np.abs(do * xh).sum(0), "dweight")
+    dx2, dw2 = torch.empty_like(dx), torch.empty_like(dw)
+    fp8.rmsnorm_backward(dn, r, w, rstd, dx2, dw2, fp8.rmsnorm_backward_workspace(n, d), dresidual=dr)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2), "the same call twice gives the same bits"
+    if dres:  # in place, and without dweight
+        fp8.rmsnorm_backward(dn, r, w, rstd, dr, dresidual=dr)
+        assert torch.equal(dr, dx)
+
+
+def test_rmsnorm_backward_against_differences(fp8):
+    """Central differences of the 64-bit forward, through the kernel's gradients of fp32 inputs.
+    With steps of 1e-4 the differences' own error is about 1e-8 of third derivatives of order one;
+    the gradients are fp32 results of sums over 96 values: 1e-5 covers both many times over."""
+    g = gen(15)
+    n, d = 4, 96
+    x, w, do = torch.randn(n, d, generator=g), 1 + 0.3 * torch.randn(d, generator=g), torch.randn(n, d, generator=g)
+    f = lambda X, W: float((np64(do) * X / np.sqrt((X ** 2).mean(1, keepdims=True) + 1e-5) * W).sum())
+    xc = x.cuda()
+    rstd = torch.empty(n, device="cuda")
+    fp8.rmsnorm(xc, None, rstd=rstd, eps=1e-5)
+    dx, dw = torch.empty(n, d, device="cuda"), torch.empty(d, device="cuda")
+    fp8.rmsnorm_backward(do.cuda(), xc, w.cuda(), rstd, dx, dw, fp8.rmsnorm_backward_workspace(n, d))
+    X, W, h = np64(x), np64(w), 1e-4
+    for i, j in [(0, 0), (1, 17), (2, 95), (3, 40)]:
+        step = np.zeros_like(X)
+        step[i, j] = h
+        assert abs((f(X + step, W) - f(X - step, W)) / (2 * h) - float(dx[i, j])) < 1e-5
+    for j in (0, 50, 95):
+        step = np.zeros_like(W)
+        step[j] = h
+        assert abs((f(X, W + step) - f(X, W - step)) / (2 * h) - float(dw[j])) < 1e-5
+
+
+# ------------------------------------------------------------------ products
+
+def make_rows(n, c, seed, std=1.0):
+    q, s = ref.quantize(np64(torch.randn(n, c, generator=gen(seed)) * std))
+    return q, s
+
+
+def make_weights(E, n, c, seed):
+    return ref.quantize_weights(np64(torch.randn(E, n, c, generator=gen(seed)) * c ** -0.5))
+
+
+PRODUCTS = [  # segments' rows, E, K, N
+    ([1], 1, 16, 16), ([1], 1, 2064, 400), ([128], 1, 128, 256), ([129], 1, 512, 272), ([256], 1, 640, 128),
+    ([300], 1, 1024, 1040), ([2177], 1, 144, 96), ([0, 5, 0, 130, 1], 5, 256, 160), ([0, 0, 0], 3, 64, 64),
+    ([3, 0, 7, 40, 1, 0, 0, 200], 4, 528, 144),  # two sources
+    ([257, 31, 33, 32], 4, 384, 512),
+]
+
+
+@pytest.mark.parametrize("path", ["simt", "auto"])
+@pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("seg, E, K, N", PRODUCTS, ids=lambda v: str(v))
+def test_matmul(fp8, path, out, seg, E, K, N):
+    n = sum(seg) + 3  # rows past the segments stay as they are
+    qa, sa = make_rows(n, K, 21)
+    qw, sw = make_weights(E, N, K, 22)
+    sa[0] = np.where(sa[0] > 0, np.clip(sa[0] + 9, 0, 254), 0)  # a loud row
+    if n > 2:
+        sa[2] = np.where(sa[2] > 0, sa[2] - 20, 0)              # a quiet one
+    plan = fp8.Fp8MatmulPlan(n, K, N, n_experts=E, n_sources=len(seg) // E, out_dtype="bf16" if out is BF else "f32", path=path)
+    ws = torch.full((plan.workspace_bytes,), 0xA5, dtype=torch.uint8, device="cuda")
+    (ta, tsa), (tw, tsw) = ref.to_torch(qa, sa), ref.to_torch(qw, sw)
+    o = torch.full((n, N), 77.0, dtype=out, device="cuda")
+    plan.forward(torch.tensor(seg, dtype=torch.int32, device="cuda"), ta.cuda(), tsa.cuda(), tw.cuda(), tsw.cuda(), o, ws)
+    assert plan.device_status(ws) == 0
+    m = sum(seg)
+    want, mag = ref.matmul(ref.dequantize(qa, sa)[:m], ref.dequantize_w(qw, sw), ref.row_experts(seg, E))
+    close(np64(o)[:m], want, H[out] * np.abs(want) + K * EPS32 * mag, "out")
+    assert (np64(o)[m:] == 77).all(), "rows past the segments are not written"
+
+
+@pytest.mark.parametrize("path", ["simt", "auto"])
+def test_matmul_whole_buffer_without_counts(fp8, path):
+    n, K, N = 200, 256, 320
+    (qa, sa), (qw, sw) = make_rows(n, K, 23), make_weights(1, N, K, 24)
+    plan = fp8.Fp8MatmulPlan(n, K, N, path=path)
+    o = torch.empty(n, N, dtype=BF, device="cuda")
+    t = [x.cuda() for x in (*ref.to_torch(qa, sa), *ref.to_torch(qw, sw))]
+    ws = plan.new_workspace()
+    plan.forward(None, *t, o, ws)
+    assert plan.device_status(ws) == 0
+    want, mag = ref.matmul(ref.dequantize(qa, sa), ref.dequantize_w(qw, sw), np.zeros(n, int))
+    close(np64(o), want, H[BF] * np.abs(want) + K * EPS32 * mag)
+
+
+def test_matmul_any_size_on_the_simt_path(fp8):
+    n, K, N = 37, 131, 77
+    (qa, sa), (qw, sw) = make_rows(n, K, 25), make_weights(2, N, K, 26)
+    plan = fp8.Fp8MatmulPlan(n, K, N, n_experts=2, out_dtype="f32", path="simt")
+    o, ws = torch.empty(n, N, device="cuda"), plan.new_workspace()
+    t = [x.cuda() for x in (*ref.to_torch(qa, sa), *ref.to_torch(qw, sw))]
+    plan.forward(torch.tensor([30, 7], dtype=torch.int32, device="cuda"), *t, o, ws)
+    assert plan.device_status(ws) == 0
+    want, mag = ref.matmul(ref.dequantize(qa, sa), ref.dequantize_w(qw, sw), ref.row_experts([30, 7], 2))
+    close(np64(o), want, H[F32] * np.abs(want) + K * EPS32 * mag)
+
+
+@pytest.mark.parametrize("path", ["simt", "auto"])
+def test_matmul_nan_and_extreme_factors_stay_in_their_rows(fp8, path):
+    """A NaN value or factor makes its own row NaN and no other; the smallest and largest factors
+    give zeros and infinities as fp32 has them."""
+    n, K, N = 140, 256, 64
+    (qa, sa), (qw, sw) = make_rows(n, K, 27), make_weights(1, N, K, 28)
+    ta, tsa = ref.to_torch(qa, sa)
+    ta.view(torch.uint8)[3, 200] = 0x7F
+    tsa[131, 1] = 255
+    tsa[7, :2] = 0
+    plan = fp8.Fp8MatmulPlan(n, K, N, out_dtype="f32", path=path)
+    o, ws = torch.empty(n, N, device="cuda"), plan.new_workspace()
+    tw, tsw = ref.to_torch(qw, sw)
+    plan.forward(None, ta.cuda(), tsa.cuda(), tw.cuda(), tsw.cuda(), o, ws)
+    assert plan.device_status(ws) == 0
+    g = np64(o)
+    assert np.isnan(g[[3, 131]]).all() and np.isfinite(np.delete(g, [3, 131], 0)).all()
+    assert (np.abs(g[7]) < 1e-30).all()
+
+
+@pytest.mark.parametrize("path", ["simt", "auto"])
+@pytest.mark.parametrize("seg", [[5, -1, 3], [60, 30, 11]], ids=["negative", "too many"])
+def test_bad_counts_are_reported_and_compute_nothing(fp8, path, seg):
+    n, K, N = 100, 128, 64
+    (qa, sa), (qw, sw) = make_rows(n, K, 29), make_weights(3, N, K, 30)
+    plan = fp8.Fp8MatmulPlan(n, K, N, n_experts=3, path=path)
+    o, ws = torch.full((n, N), 5.0, dtype=BF, device="cuda"), plan.new_workspace()
+    t = [x.cuda() for x in (*ref.to_torch(qa, sa), *ref.to_torch(qw, sw))]
+    plan.forward(torch.tensor(seg, dtype=torch.int32, device="cuda"), *t, o, ws)
+    from top_routing_grouped_gb300 import moe
+    assert plan.device_status(ws) == moe.MOE_ERR_INTERNAL
+    assert (o == 5).all()
+    plan.forward(torch.tensor([50, 30, 20], dtype=torch.int32, device="cuda"), *t, o, ws)  # the next call is clean
+    assert plan.device_status(ws) == 0
+
+
+EXPERTS = [  # segments' rows, E, d, F
+    ([1], 1, 16, 16), ([1, 1, 0, 1, 1], 5, 512, 256), ([0, 0, 0, 0], 2, 64, 64), ([130, 0, 257, 64], 4, 256, 272),
+    ([33, 128, 0, 3, 300, 1], 3, 400, 144), ([2100], 1, 128, 400), ([20, 31, 32, 33, 0, 200, 90, 64], 8, 1024, 640),
+]
+
+
+@pytest.mark.parametrize("path", ["simt", "auto"])
+@pytest.mark.parametrize("seg, E, d, F", EXPERTS, ids=lambda v: str(v))
+def test_experts(fp8, path, seg, E, d, F):
+    """y = gate * W2 q(silu(W1 x) * W3 x).  The hidden value that is quantised is an fp32 one, off by
+    d eps sum|x w| in either factor, so a value that lies on a border may take the neighbouring
+    e4m3 (a step of at most 2^-3 of it): the reference is given the range of hidden values around its
+    own, and every hidden value within reach of a border adds a step times |w2| to the bound.  A block
+    whose maximum is within reach of a factor's border may be rounded in twice the factor: each of
+    its values is then half a step of either off, again 2^-3 of it at most (2^-8 of the factor below
+    e4m3's normal values)."""
+    m = sum(seg)
+    n = m + 2
+    W = len(seg) // E
+    (qx, sx) = make_rows(n, d, 31)
+    (q1, s1), (q3, s3), (q2, s2) = make_weights(E, F, d, 32), make_weights(E, F, d, 33), make_weights(E, d, F, 34)
+    gates = torch.rand(n, generator=gen(35))
+    plan = fp8.Fp8ExpertPlan(n, d, E, W, F, path=path)
+    ws = torch.full((plan.workspace_bytes,), 0xA5, dtype=torch.uint8, device="cuda")
+    y = torch.full((n, d), 77.0, dtype=BF, device="cuda")
+    t = [x.cuda() for p in ((q1, s1), (q3, s3), (q2, s2)) for x in ref.to_torch(*p)]
+    tx, tsx = ref.to_torch(qx, sx)
+    plan.forward(torch.tensor(seg, dtype=torch.int32, device="cuda"), tx.cuda(), tsx.cuda(), gates.cuda(), *t, y, ws)
+    assert plan.device_status(ws) == 0
+    assert (np64(y)[m:] == 77).all()
+    ex = ref.row_experts(seg, E)
+    x = ref.dequantize(qx, sx)[:m]
+    a, ma = ref.matmul(x, ref.dequantize_w(q1, s1), ex)
+    b, mb = ref.matmul(x, ref.dequantize_w(q3, s3), ex)
+    h = ref.silu(a) * b
+    # |silu'| <= 1.1; exp and the quotient are good to 2^-20
+    dh = 1.1 * d * EPS32 * ma * np.abs(b) + np.abs(ref.silu(a)) * d * EPS32 * mb + 2.0 ** -20 * np.abs(h)
+    if m == 0:
+        return
+    qh, sh = ref.quantize(h)
+    hv = ref.dequantize(qh, sh)
+    f = np.repeat(ref.scale_value(sh), 128, 1)[:, :F]
+    near = ref.round_e4m3((np.abs(h) - dh) / f) != ref.round_e4m3((np.abs(h) + dh) / f)
+    top = np.abs(np.pad(h, ((0, 0), (0, sh.shape[1] * 128 - F)))).reshape(m, -1, 128).max(2)
+    dtop = np.pad(dh, ((0, 0), (0, sh.shape[1] * 128 - F))).reshape(m, -1, 128).max(2)
+    border = np.repeat(ref.scale_byte(top - dtop) != ref.scale_byte(top + dtop), 128, 1)[:, :F]
+    step = (near | border) * np.maximum(np.abs(h) * 2.0 ** -3, f * np.where(border, 2.0 ** -8, 2.0 ** -9))
+    w2 = ref.dequantize_w(q2, s2)
+    want, mag = ref.matmul(hv, w2, ex)
+    slack = ref.matmul(step, np.abs(w2), ex)[0]
+    gt = np64(gates)[:m, None]
+    close(np64(y)[:m], gt * want, (H[BF] + 2 * EPS32) * np.abs(gt * want) + gt * (F * EPS32 * mag + slack), "y")
+
+
+def test_experts_paths_agree_on_a_larger_layer(fp8):
+    """The tensor-core and SIMT paths on 3000 rows of 16 experts: both round the same sums to the
+    same 8 bits but for values at a border, and y to bf16: 2-norm of the difference within 2^-8."""
+    g, E, d, F = torch.Generator("cuda").manual_seed(5), 16, 768, 512
+    seg = torch.tensor([0, 700, 1, 127, 128, 129, 255, 256, 257, 300, 400, 100, 47, 200, 0, 100], dtype=torch.int32)
+    n = int(seg.sum())
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, sx = f8(n, d), u8(n, fp8.scale_cols(d))
+    fp8.quantize(rn(n, d), x, sx)
+    ws = []
+    for r, c in ((F, d), (F, d), (d, F)):
+        q, s = f8(E, r, c), u8(E, -(-r // 128), fp8.scale_cols(c))
+        fp8.quantize_weights(rn(E, r, c) * c ** -0.5, q, s)
+        ws += [q, s]
+    gates, ys = torch.rand(n, generator=g, device="cuda"), []
+    for path in ("auto", "simt"):
+        plan = fp8.Fp8ExpertPlan(n, d, E, 1, F, path=path)
+        y, w = torch.empty(n, d, dtype=BF, device="cuda"), plan.new_workspace()
+        plan.forward(seg.cuda(), x, sx, gates, *ws, y, w)
+        assert plan.device_status(w) == 0
+        ys.append(np64(y))
+    assert np.linalg.norm(ys[0] - ys[1]) <= 2.0 ** -8 * np.linalg.norm(ys[1])
+
+
+# ------------------------------------------------------------------ checkpoints
+
+@pytest.mark.parametrize("n, F", [(1, 16), (1, 2048), (7, 130), (300, 1072), (1000, 1)])
+def test_checkpoint_save_bit_exact(fp8, n, F):
+    a, b = awkward(n, F, BF, 41).cuda(), awkward(n, F, BF, 42).flip(0).cuda()
+    out = [f8(n, F), u8(n, fp8.scale_cols(F)), f8(n, F), u8(n, fp8.scale_cols(F))]
+    fp8.checkpoint_save(a, b, *out)
+    for x, (q, s) in ((a, out[:2]), (b, out[2:])):
+        wq, ws = ref.quantize(np64(x))
+        np.testing.assert_array_equal(np64(s), ws)
+        np.testing.assert_array_equal(np64(q), wq)
+
+
+@pytest.mark.parametrize("n, F", [(1, 16), (1, 2048), (7, 130), (300, 1072), (513, 1)])
+def test_checkpoint_backward_against_the_formula(fp8, n, F):
+    g = gen(43)
+    (qa, sa), (qb, sb) = ref.quantize(np64(torch.randn(n, F, generator=g) * 4)), ref.quantize(np64(torch.randn(n, F, generator=g)))
+    dh = torch.randn(n, F, generator=g).to(BF)
+    t = [x.cuda() for x in (*ref.to_torch(qa, sa), *ref.to_torch(qb, sb), dh)]
+    da, db, h = (torch.empty(n, F, dtype=BF, device="cuda") for _ in range(3))
+    fp8.checkpoint_backward(*t, da, db, h)
+    a, b, do = ref.dequantize(qa, sa), ref.dequantize(qb, sb), np64(dh)
+    sig = 1 / (1 + np.exp(-a))
+    # sigma is good to 2^-20 relative; silu' = sigma (1 + a (1 - sigma)), whose terms may cancel
+    mag = sig * (1 + np.abs(a) * (1 - sig) + np.abs(a) * sig * 2)
+    close(np64(da), do * b * sig * (1 + a * (1 - sig)), np.abs(do * b) * (mag * 2.0 ** -19 + H[BF] * np.abs(sig * (1 + a * (1 - sig)))), "da")
+    for got, want in ((db, do * a * sig), (h, a * sig * b)):
+        close(np64(got), want, np.abs(want) * (H[BF] + 2.0 ** -19))
+    da2, db2 = t[4].clone(), torch.empty_like(db)
+    fp8.checkpoint_backward(*t[:4], da2, da2, db2)  # in place of dh, without h
+    assert torch.equal(da2, da) and torch.equal(db2, db)
+
+
+def test_checkpoint_backward_against_differences(fp8):
+    """Central differences of sum(dh * silu(a) * b) in 64 bits at the values the checkpoint holds;
+    da, db are bf16: half a step, 2^-8, and 1e-6 for the differences."""
+    g, n, F = gen(44), 3, 64
+    (qa, sa), (qb, sb) = ref.quantize(np64(torch.randn(n, F, generator=g))), ref.quantize(np64(torch.randn(n, F, generator=g)))
+    dh = torch.randn(n, F, generator=g).to(BF)
+    da, db = (torch.empty(n, F, dtype=BF, device="cuda") for _ in range(2))
+    fp8.checkpoint_backward(*[x.cuda() for x in (*ref.to_torch(qa, sa), *ref.to_torch(qb, sb), dh)], da, db)
+    a, b, do, e = ref.dequantize(qa, sa), ref.dequantize(qb, sb), np64(dh), 1e-4
+    num_a = do * (ref.silu(a + e) - ref.silu(a - e)) * b / (2 * e)
+    num_b = do * ref.silu(a)
+    close(np64(da), num_a, H[BF] * np.abs(num_a) + 1e-6)
+    close(np64(db), num_b, H[BF] * np.abs(num_b) + 1e-6)
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+def test_other_streams_and_graph_capture(fp8):
+    """The whole serving chain on a side stream, then captured into a CUDA graph and replayed on
+    new inputs: the same bits as the eager calls."""
+    n, d, F, E = 96, 256, 384, 4
+    g = torch.Generator("cuda").manual_seed(9)
+    x, res = (torch.randn(n, d, generator=g, device="cuda").to(BF) for _ in range(2))
+    w, gates = torch.rand(d, generator=g, device="cuda"), torch.rand(n, generator=g, device="cuda")
+    ws = []
+    for r, c in ((F, d), (F, d), (d, F)):
+        q, s = f8(E, r, c), u8(E, -(-r // 128), fp8.scale_cols(c))
+        fp8.quantize_weights(torch.randn(E, r, c, generator=g, device="cuda") * c ** -0.5, q, s)
+        ws += [q, s]
+    seg = torch.tensor([10, 0, 80, 6], dtype=torch.int32, device="cuda")
+    plan = fp8.Fp8ExpertPlan(n, d, E, 1, F)
+    wsp, q, s, y, r = plan.new_workspace(), f8(n, d), u8(n, 4), torch.empty_like(x), torch.empty_like(x)
+
+    def chain(stream=None):
+        fp8.rmsnorm(x, w, res, r, q=q, scales=s, stream=stream)
+        plan.forward(seg, q, s, gates, *ws, y, wsp, stream=stream)
+
+    chain()
+    torch.cuda.synchronize()
+    first = y.clone()
+    y.zero_()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    chain(side)
+    side.synchronize()
+    assert torch.equal(first, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    x.copy_(torch.randn(n, d, generator=g, device="cuda"))
+    graph.replay()
+    torch.cuda.synchronize()
+    replayed = y.clone()
+    chain()
+    torch.cuda.synchronize()
+    assert torch.equal(replayed, y) and not torch.equal(first, y)
+    assert plan.device_status(wsp) == 0

@@ -1,0 +1,177 @@
+"""Refusals and host logic of the 8-bit operators, without a GPU: every bad argument is turned
+down on the host before any CUDA call (the fake addresses are never dereferenced)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as ref
+
+
+@pytest.fixture(scope="module")
+def fp8():
+    from top_routing_grouped_gb300 import build as b
+    if not b.up_to_date():
+        b.build()
+    from top_routing_grouped_gb300 import fp8 as m
+    return m
+
+
+P = ctypes.c_void_p
+A = [P(4096 * (i + 1)) for i in range(16)]
+INVALID, UNSUPPORTED = 1, 2
+
+
+def test_scale_cols(fp8):
+    for c in (1, 127, 128, 129, 512, 513, 2048, 2064, 4096):
+        assert fp8.scale_cols(c) == ref.scale_cols(c) and fp8.scale_cols(c) % 4 == 0
+        assert -(-c // 128) <= fp8.scale_cols(c) < -(-c // 128) + 4
+    assert fp8.scale_cols(0) == 0 and fp8.scale_cols(-5) == 0
+
+
+def test_reference_rounding_is_torchs():
+    """The reference's e4m3 rounding against torch's conversion, over every value and midpoint."""
+    v = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    v = v[torch.isfinite(v)].unique()
+    mid = (v[1:] + v[:-1]) / 2
+    for t in (v, mid, mid * 1.0001, mid * 0.9999):
+        np.testing.assert_array_equal(ref.round_e4m3(t.double().numpy()), t.to(torch.float8_e4m3fn).double().numpy())
+    b = ref.scale_byte(np.array([0.0, 448.0, 448.0001, 1.0, np.inf, 2.0 ** -140, 3.4e38]))
+    assert b.tolist() == [0, 127, 128, 119, 255, 0, 247]
+
+
+def test_quantize_refusals(fp8):
+    L = fp8._lib
+    ok = dict(x=A[0], t=0, rows=4, cols=64, ld=64, br=1, er=4, q=A[1], s=A[2])
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return L.moe_fp8_quantize(a["x"], a["t"], a["rows"], a["cols"], a["ld"], a["br"], a["er"], a["q"], a["s"], None)
+
+    for kw in (dict(x=None), dict(q=None), dict(s=None), dict(t=5), dict(rows=-1), dict(cols=0), dict(ld=63), dict(br=64),
+               dict(x=P(4098)), dict(q=P(4104)), dict(s=P(4097)), dict(br=128, er=0), dict(br=128, er=3)):
+        assert call(**kw) == INVALID, kw
+    assert call(rows=1 << 40) == UNSUPPORTED
+    assert call(rows=0, x=None, q=None, s=None) == 0  # nothing to do
+
+
+def test_rmsnorm_refusals(fp8):
+    L = fp8._lib
+    ok = dict(x=A[0], r=A[1], w=A[2], t=1, rows=4, d=64, ldx=64, ldr=64, eps=1e-6, ro=A[3], o=A[4], q=A[5], s=A[6], rs=A[7])
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return L.moe_rmsnorm(a["x"], a["r"], a["w"], a["t"], a["rows"], a["d"], a["ldx"], a["ldr"], a["eps"], a["ro"], a["o"],
+                             a["q"], a["s"], a["rs"], None)
+
+    for kw in (dict(x=None), dict(t=2), dict(rows=-1), dict(d=0), dict(ldx=60), dict(ldr=60), dict(eps=-1.0),
+               dict(eps=float("nan")), dict(eps=float("inf")), dict(q=None), dict(s=None), dict(x=P(4097)), dict(o=P(4097)),
+               dict(q=P(4100)), dict(rs=P(4100)), dict(w=P(4100)), dict(ro=None, o=None, q=None, s=None, rs=None),
+               dict(ro=A[0], ldx=80), dict(ro=A[1], ldr=80)):
+        assert call(**kw) == INVALID, kw
+    assert call(d=60000, ldx=60000, ldr=60000) == UNSUPPORTED
+    assert call(rows=0) == 0
+
+
+def test_rmsnorm_backward_refusals(fp8):
+    L = fp8._lib
+    assert fp8._rmsnorm_ws(0, 64) == 0 and fp8._rmsnorm_ws(-1, 64) == 0 and fp8._rmsnorm_ws(1000, 64) >= 64 * 4
+    need = fp8._rmsnorm_ws(1000, 64)
+    ok = dict(do=A[0], dt=0, r=A[1], w=A[2], rs=A[3], dr=A[4], t=1, rows=1000, d=64, ld=64, dx=A[5], dw=A[6], ws=A[7], n=need)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return L.moe_rmsnorm_backward(a["do"], a["dt"], a["r"], a["w"], a["rs"], a["dr"], a["t"], a["rows"], a["d"], a["ld"],
+                                      a["dx"], a["dw"], a["ws"], a["n"], None)
+
+    for kw in (dict(do=None), dict(r=None), dict(rs=None), dict(dx=None), dict(dt=3), dict(t=-1), dict(rows=-1), dict(d=0),
+               dict(ld=10), dict(ws=None), dict(ws=P(4224)), dict(n=need - 1), dict(dw=P(4100)), dict(do=P(4098))):
+        assert call(**kw) == INVALID, kw
+    assert call(d=60000, ld=60000) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(max_rows=0), "MOE_ERR_INVALID_ARG"), (dict(K=0), "MOE_ERR_INVALID_ARG"), (dict(n=0), "MOE_ERR_INVALID_ARG"),
+    (dict(n_experts=0), "MOE_ERR_INVALID_ARG"), (dict(n_experts=129, n_sources=2), "MOE_ERR_INVALID_ARG"),
+    (dict(path="tc1"), "MOE_ERR_INVALID_ARG"), (dict(K=72), "MOE_ERR_UNSUPPORTED"), (dict(n=100), "MOE_ERR_UNSUPPORTED"),
+    (dict(max_rows=1 << 31), "MOE_ERR_UNSUPPORTED"), (dict(n=1 << 30, n_experts=2), "MOE_ERR_UNSUPPORTED"),
+])
+def test_plan_refusals(fp8, kw, status):
+    a = dict(max_rows=64, K=64, n=64, n_experts=2, n_sources=1, path="auto", **{})
+    a.update(kw)
+    with pytest.raises(fp8.MoEError) as ei:
+        fp8.Fp8MatmulPlan(a["max_rows"], a["K"], a["n"], n_experts=a["n_experts"], n_sources=a["n_sources"], path=a["path"])
+    assert status in str(ei.value)
+    with pytest.raises(fp8.MoEError) as ei:
+        fp8.Fp8ExpertPlan(a["max_rows"], a["K"], a["n_experts"], a["n_sources"], a["n"], path=a["path"])
+    assert status in str(ei.value)
+
+
+def test_simt_plans_take_any_size(fp8):
+    assert fp8.Fp8MatmulPlan(3, 5, 7, path="simt").workspace_bytes > 0
+    assert fp8.Fp8ExpertPlan(3, 5, 2, 1, 7, path="simt").workspace_bytes > 0
+
+
+def test_product_refusals(fp8):
+    L = fp8._lib
+    p, e = fp8.Fp8MatmulPlan(64, 64, 64, n_experts=2), fp8.Fp8ExpertPlan(64, 64, 2, 1, 64)
+    n = p.workspace_bytes
+    args = dict(seg=A[0], a=A[1], sa=A[2], w=A[3], sw=A[4], out=A[5], ws=A[6], n=n)
+
+    def call(h=p.handle, **kw):
+        a = {**args, **kw}
+        return L.moe_fp8_matmul(h, a["seg"], a["a"], a["sa"], a["w"], a["sw"], a["out"], a["ws"], a["n"], None)
+
+    for name in ("seg", "a", "sa", "w", "sw", "out"):
+        assert call(**{name: None}) == INVALID and call(**{name: P(4104)}) == INVALID, name
+    assert call(ws=None) == INVALID and call(ws=P(4224)) == INVALID and call(n=n - 1) == INVALID
+    assert call(h=None) == INVALID and call(h=e.handle) == INVALID
+    ne = e.workspace_bytes
+    for i in range(11):
+        b = list(A[:11])
+        b[i] = None
+        assert L.moe_fp8_expert_forward(e.handle, *b, A[11], ne, None) == INVALID, i
+        b[i] = P(4104)
+        assert L.moe_fp8_expert_forward(e.handle, *b, A[11], ne, None) == INVALID, i
+    assert L.moe_fp8_expert_forward(e.handle, *A[:11], A[11], ne - 1, None) == INVALID
+    assert L.moe_fp8_expert_forward(p.handle, *A[:11], A[11], ne, None) == INVALID
+
+
+def test_checkpoint_refusals(fp8):
+    L = fp8._lib
+    for i in range(6):
+        b = list(A[:6])
+        b[i] = None
+        assert L.moe_checkpoint_save_rows(b[0], b[1], 4, 64, *b[2:], None) == INVALID, i
+        b[i] = P(4104)
+        assert L.moe_checkpoint_save_rows(b[0], b[1], 4, 64, *b[2:], None) == INVALID, i
+    for i in range(8):
+        b = list(A[:8])
+        b[i] = P(4104)
+        assert L.moe_checkpoint_backward_rows(*b[:5], 4, 64, *b[5:], None) == INVALID, i
+        b[i] = None
+        if i < 7:  # h may be missing
+            assert L.moe_checkpoint_backward_rows(*b[:5], 4, 64, *b[5:], None) == INVALID, i
+    assert L.moe_checkpoint_save_rows(*A[:2], -1, 64, *A[2:6], None) == INVALID
+    assert L.moe_checkpoint_save_rows(*A[:2], 4, 0, *A[2:6], None) == INVALID
+
+
+def test_binding_checks_types_shapes_and_layouts(fp8):
+    """The binding turns wrong tensors down before their addresses are used."""
+    x = torch.zeros(4, 64)
+    q, s = torch.zeros(4, 64, dtype=torch.uint8).view(fp8.E4M3), torch.zeros(4, 4, dtype=torch.uint8)
+    bad = [lambda: fp8.quantize(x.double(), q, s), lambda: fp8.quantize(x, q[:, :32], s), lambda: fp8.quantize(x, x, s),
+           lambda: fp8.quantize(x, q, s[:, :1]), lambda: fp8.quantize(x.t(), q.view(torch.uint8).t().contiguous().view(fp8.E4M3), s),
+           lambda: fp8.quantize(x[:1].expand(4, 64), q, s),
+           lambda: fp8.rmsnorm(x, torch.ones(63), out=x), lambda: fp8.rmsnorm(x, None, out=torch.zeros(64, 4).t()),
+           lambda: fp8.rmsnorm(x, None, residual=x.bfloat16(), out=x), lambda: fp8.rmsnorm(x.view(-1), None, out=x),
+           lambda: fp8.rmsnorm_backward(x[:3], x, None, torch.ones(4), x), lambda: fp8.rmsnorm_backward(x, x, None, torch.ones(3), x),
+           lambda: fp8.checkpoint_save(x, x, q, s, q, s), lambda: fp8.checkpoint_backward(q, s, q, s, x, x, x)]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"case {i} was taken")
+    plan = fp8.Fp8MatmulPlan(4, 64, 32)
+    with pytest.raises(ValueError):
+        plan.forward(None, q, s, torch.zeros(1, 32, 64).to(fp8.E4M3), s, torch.zeros(4, 32), torch.zeros(1 << 16, dtype=torch.uint8))

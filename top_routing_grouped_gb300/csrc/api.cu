@@ -588,7 +588,7 @@ moe_status moe_expert_forward(moe_plan_t plan, const int32_t* seg_counts, const 
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemsetAsync(ws.hdr, 0, moe::kHdrClearWords * sizeof(uint32_t), cs);
   if (e != cudaSuccess) return cuda_fail(e, "clearing the status word");
-  if ((e = moe::launch_seg_scan(s, ws, seg_counts, plan->n_seg, s.E, cs)) != cudaSuccess)
+  if ((e = moe::launch_seg_scan(s, ws, seg_counts, plan->n_seg, s.E, false, cs)) != cudaSuccess)
     return cuda_fail(e, "launching the segment scan");
   for (int mode = 1; mode <= 2; ++mode) {
     if (plan->pair)

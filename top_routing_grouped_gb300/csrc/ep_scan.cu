@@ -18,15 +18,16 @@ namespace moe {
 
 constexpr int kSegThreads = kMaxExperts;  // one thread per segment (W * E_l <= 256)
 
-// One CTA: segment counts (device input) -> counts, offsets, tile tables, header totals.  A
-// negative count or a total beyond the plan's row capacity is reported (MOE_ERR_INTERNAL, site
+// One CTA: segment counts (device input; null: one segment of all s.N rows) -> counts, offsets,
+// tile tables, header totals; with `clear` also the header's clear before them.  A negative count or a total beyond the plan's row capacity is reported (MOE_ERR_INTERNAL, site
 // 0x740) and leaves empty tile tables, so that no GEMM reads outside the buffers.
 __global__ void __launch_bounds__(kSegThreads) seg_scan_kernel(Shape s, Ws ws, const int32_t* seg_counts, int n_seg,
-                                                               int n_local) {
+                                                               int n_local, int clear) {
   __shared__ int cnt_s[kMaxExperts], offs_s[kMaxExperts];
   __shared__ int scratch[kTileScratchInts];
   const int i = threadIdx.x;
-  int cnt = i < n_seg ? seg_counts[i] : 0;
+  if (clear && i < kHdrClearWords) ws.hdr[i] = 0u;  // ordered before record_error by the barrier below
+  int cnt = i < n_seg ? (seg_counts ? seg_counts[i] : (int)s.N) : 0;
   const bool neg = cnt < 0;
   cnt_s[i] = neg ? 0 : cnt;
   if (__syncthreads_or(neg)) {
@@ -42,8 +43,9 @@ __global__ void __launch_bounds__(kSegThreads) seg_scan_kernel(Shape s, Ws ws, c
 }
 
 cudaError_t launch_seg_scan(const Shape& s, const Ws& ws, const int32_t* seg_counts, int n_seg, int n_local,
-                            cudaStream_t st) {
-  return launch_kernel(seg_scan_kernel, dim3(1), dim3(kSegThreads), 0, st, false, 1, s, ws, seg_counts, n_seg, n_local);
+                            bool clear, cudaStream_t st) {
+  return launch_kernel(seg_scan_kernel, dim3(1), dim3(kSegThreads), 0, st, false, 1, s, ws, seg_counts, n_seg, n_local,
+                       clear ? 1 : 0);
 }
 
 // aux = E * sum_e (count_e / (T k)) * (psum_e / T) from per-expert totals (counts and sums of

@@ -1,0 +1,565 @@
+// gemm_fp8_tc.cu -- the 8-bit grouped products on CTA pairs (2-SM tcgen05.mma with block
+// factors, kind::mxf8f6f4.block_scale).
+//
+//   out[p, n] = sum_j 2^(sA[p,j] + sW[n/128,j]) sum_{k in block j} A[p,k] W_e[n,k]   (j: 128 k's)
+//
+// A power-of-two factor for a block of 128 is the tensor core's own factor for a block of 32,
+// given four times: the MMA multiplies by both factors while it accumulates, so nothing is
+// rescaled between K blocks and the accumulator stays in TMEM over the whole sum.
+//
+// Tiles, ring and roles are those of gemm_tc2.cu: a cluster of two CTAs computes 256 x 256 with
+// one MMA stream issued by the leader, each CTA loads its own 128 rows of A and its half of the
+// 256 weight rows (SwiGLU: the leader W1's 128, the peer W3's), 128 k's (128 bytes) a stage, so a
+// stage is 32 KB and takes 512 clocks of MMA, as in bf16 with half the k's.
+//
+// Factors.  A 32-bit word holds a row's bytes of four K blocks, in the order the rows' scale
+// bytes lie in memory; the instruction descriptor picks the byte of the current block, so one
+// load of words serves 512 k's.  Warp 3 of each CTA gathers the words of its 128 rows and of the
+// tile's two blocks of weight rows into shared memory, the MMA thread copies them to TMEM
+// (tcgen05.cp, 32 lanes repeated over the four lane quarters; column c of a group of four belongs
+// to rows 32c..32c+31), ordered before the MMAs that it issues next.  Two sets of columns in TMEM
+// take turns; the shared words have one buffer, which is free again when the copy has run.
+//
+// TMEM.  The two sets take 32 columns, so the two accumulators of 256 columns overlap by 32: the
+// epilogue reads those columns first and hands them over before it goes on, and the next
+// tile's MMAs start then.
+//
+// SwiGLU epilogue: the 128 columns of a tile are one block of each hidden row.  Two warps share a
+// row's 128 values (64 each), agree on the largest one through shared memory, and write e4m3 and
+// one factor byte, so the hidden rows cost N*F bytes instead of 2*N*F twice.
+//
+// Waits are bounded (MOE_ERR_TIMEOUT, no trap); an abort raises the flag in both CTAs; the pair
+// meets at cluster barriers before TMEM is released.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "fp8_common.cuh"
+#include "gemm_tc.h"
+#include "tc_ptx.cuh"
+#include "tmap.h"
+
+namespace moe {
+namespace fp8 {
+namespace {
+
+constexpr int kBK = 128;  // bytes = k's per stage: one block of factors
+constexpr int kStages = 6;
+constexpr int kRowsPerCta = 128;
+constexpr int kMmaM = 256;
+constexpr int kMmaN = 256;
+constexpr int kMmaK = 32;
+constexpr int kABytes = kRowsPerCta * kBK;
+constexpr int kBHalfBytes = (kMmaN / 2) * kBK;
+constexpr int kStageBytes = kABytes + kBHalfBytes;
+constexpr int kThreads = 384;
+constexpr int kEpiWarp0 = 4;
+constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, one per half of the tile's columns
+
+// TMEM columns: accumulator i at 224 i (256 wide), factor set i at 480 + 16 i (4 of A, 8 of B)
+constexpr int kTmemCols = 512;
+constexpr int kAccStep = 224;
+constexpr int kSfCol = 480;
+constexpr int kSfStep = 16;
+
+constexpr int kSfBytes = 3 * 512;             // A's 128 rows, B's two blocks of 128 rows
+constexpr int kStgBlockBytes = 32 * 128;      // a store block: 32 rows of 128 bytes, swizzled
+constexpr int kStgBytes = kEpiWarps * kStgBlockBytes;
+
+struct Ctl {
+  uint64_t full[kStages];   // leader's: both CTAs' bytes of a stage
+  uint64_t empty[kStages];  // each CTA: stage free again (leader's multicast commit)
+  uint64_t tfull[2];        // each CTA: accumulator ready (leader's multicast commit)
+  uint64_t over;            // leader's: the columns the accumulators share have been read
+  uint64_t sf_full;         // leader's: both CTAs' factor words are in shared memory
+  uint64_t sf_empty;        // each CTA: the words have been copied (leader's multicast commit)
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t peer_tmem_base;
+  int abort;
+};
+
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kStgBytes + kSfBytes + sizeof(Ctl);
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 2-D tiled TMA store of a staged block (x = column, y = row), as a bulk group of its own
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int32_t x, int32_t y, uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(src)
+      : "memory");
+}
+// this thread's bulk groups have read their shared-memory source / are complete
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Named barrier of the two warps of one lane quarter, with the AND of a flag over them.
+__device__ __forceinline__ bool pair_bar_and(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// Instruction descriptor of kind::mxf8f6f4 with e4m3 A and B (both K-major), e8m0 factors, fp32
+// D: bits 4-5 B's factor byte, 7-9 / 10-12 the types (0 = e4m3), 17-22 N >> 3, 23 factor type
+// (1 = e8m0), 24-28 M >> 4, 29-30 A's factor byte.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, uint32_t byte) {
+  return (byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | (byte << 29);
+}
+
+__device__ __forceinline__ void mma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// 512 bytes (32 rows of 16) of each CTA's shared memory -> 4 columns of its TMEM, repeated in the
+// four lane quarters.
+__device__ __forceinline__ void tmem_cp_factors(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Descriptor of an unswizzled block of rows of 16 bytes: 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t desc_rows16(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+__device__ __forceinline__ void raise_abort(Ctl* ctl, uint32_t rank) {
+  ctl->abort = 1;
+  ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&ctl->abort), rank ^ 1u), 1u);
+}
+
+template <int kKind>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmB3, const __grid_constant__ CUtensorMap tmY, GemmArgs g, Ws ws,
+                    int64_t timeout_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stg_base = stages + kStages * kStageBytes;
+  uint8_t* sf_base = stg_base + kStgBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(sf_base + kSfBytes);
+  // SwiGLU stages four blocks; the warps' maxima lie behind them: [half][128 rows]
+  uint32_t* top_s = reinterpret_cast<uint32_t*>(stg_base + 4 * kStgBlockBytes);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cid = (int)ptx::cluster_id_x();
+  const int ncl = (int)ptx::cluster_count_x();
+
+  constexpr int bn = kKind == kSwiGLU ? kMmaN / 2 : kMmaN;  // output columns per tile
+  const int n_tiles = (g.n + bn - 1) / bn;
+  const int kblocks = (g.K + kBK - 1) / kBK;
+  const int sck = (int)(scale_cols(g.K) / 4);  // words of factors per row
+  const int nb = (g.n + kBlock - 1) / kBlock;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&ctl->full[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&ctl->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&ctl->tfull[i]), 1);
+    ptx::mbar_init(ptx::smem_u32(&ctl->over), 2 * kEpiWarps);
+    ptx::mbar_init(ptx::smem_u32(&ctl->sf_full), 2);
+    ptx::mbar_init(ptx::smem_u32(&ctl->sf_empty), 1);
+    ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
+    ctl->abort = 0;
+    ctl->peer_tmem_base = 0xFFFFFFFFu;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&tmA);
+    ptx::tma_prefetch_desc(&tmB);
+    if (kKind == kSwiGLU) ptx::tma_prefetch_desc(&tmB3);
+    ptx::tma_prefetch_desc(&tmY);
+  }
+  ptx::cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or load
+  if (warp == 2) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(&ctl->tmem_base), kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  if (threadIdx.x == 0) ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&ctl->peer_tmem_base), rank ^ 1u), tmem);
+  ptx::cluster_sync();
+  pdl_wait();  // the tile table and the A operand come from the previous kernels
+  pdl_launch_dependents();
+  int total = (int)ws.hdr[kHdrNumPairs] * n_tiles;
+  if (ctl->peer_tmem_base != tmem) {  // a pair's accumulators must sit at the same TMEM address
+    if (threadIdx.x == 0) record_error(ws, MOE_ERR_INTERNAL, 0x900u + kKind);
+    total = 0;
+  }
+  volatile int* abort_flag = &ctl->abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- TMA producer (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const CUtensorMap* bmap = (kKind == kSwiGLU && rank == 1) ? &tmB3 : &tmB;
+      for (int tile = cid; tile < total && ok; tile += ncl) {
+        const TileInfo ti = decode_pair_tile(ws, n_tiles, tile, (int)rank);
+        // a pair's second m-tile may not exist: its A rows are neither loaded nor waited for
+        const bool peer_rows = decode_pair_tile(ws, n_tiles, tile, 1).rows > 0;
+        const uint32_t bytes = peer_rows ? 2 * kStageBytes : 2 * kStageBytes - kABytes;
+        const int brow = ti.e * g.n + ti.n_idx * bn + (kKind == kSwiGLU ? 0 : (int)rank * (kMmaN / 2));
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!ptx::mbar_wait(ptx::smem_u32(&ctl->empty[stage]), phase ^ 1u, timeout_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_local = ptx::smem_u32(&ctl->full[stage]);
+          if (leader) ptx::mbar_arrive_expect_tx(full_local, bytes);
+          const uint32_t bar = ptx::mapa(full_local, 0);
+          const uint32_t sa = ptx::smem_u32(stages + (size_t)stage * kStageBytes);
+          if (ti.rows > 0) ptx::tma_load_2d_pair(sa, &tmA, kb * kBK, ti.row0, bar);
+          ptx::tma_load_2d_pair(sa + kABytes, bmap, kb * kBK, brow, bar);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        record_error(ws, MOE_ERR_TIMEOUT, 0x910u + kKind);
+        raise_abort(ctl, rank);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---------------------------------------------------------- MMA issuer (leader only)
+      int stage = 0, acc = 0, set = 0;
+      uint32_t phase = 0, over_phase = 0, sf_phase = 0;
+      bool ok = true, first = true;
+      const uint64_t sf_desc = desc_rows16(ptx::smem_u32(sf_base));
+      for (int tile = cid; tile < total && ok; tile += ncl) {
+        const uint32_t d_tmem = tmem + (uint32_t)(acc * kAccStep);
+        uint32_t sf = 0;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if ((kb & 3) == 0) {  // the words of the next four K blocks
+            if (!ptx::mbar_wait(ptx::smem_u32(&ctl->sf_full), sf_phase, timeout_ns, abort_flag)) {
+              ok = false;
+              break;
+            }
+            sf_phase ^= 1u;
+            ptx::tc_fence_after();
+            sf = tmem + (uint32_t)(kSfCol + set * kSfStep);
+            set ^= 1;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) tmem_cp_factors(sf + 4 * i, sf_desc + (uint64_t)(i * (512 >> 4)));
+            ptx::mma_commit_pair_multicast(ptx::smem_u32(&ctl->sf_empty), 0x3);
+          }
+          if (kb == 0 && !first) {  // the columns shared with the previous tile's accumulator
+            if (!ptx::mbar_wait(ptx::smem_u32(&ctl->over), over_phase, timeout_ns, abort_flag)) {
+              ok = false;
+              break;
+            }
+            over_phase ^= 1u;
+            ptx::tc_fence_after();
+          }
+          if (!ptx::mbar_wait(ptx::smem_u32(&ctl->full[stage]), phase, timeout_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sa = ptx::smem_u32(stages + (size_t)stage * kStageBytes);
+          const uint32_t sb = sa + kABytes;
+          const uint32_t idesc = idesc_mxf8(kMmaM, kMmaN, (uint32_t)(kb & 3));
+#pragma unroll
+          for (int ks = 0; ks < kBK / kMmaK; ++ks)
+            mma_mxf8_pair(d_tmem, ptx::desc_kmajor_sw128(sa + ks * kMmaK), ptx::desc_kmajor_sw128(sb + ks * kMmaK), idesc,
+                          sf, sf + 4, (kb | ks) != 0 ? 1u : 0u);
+          ptx::mma_commit_pair_multicast(ptx::smem_u32(&ctl->empty[stage]), 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::mma_commit_pair_multicast(ptx::smem_u32(&ctl->tfull[acc]), 0x3);
+        acc ^= 1;
+        first = false;
+      }
+      if (!ok) {
+        record_error(ws, MOE_ERR_TIMEOUT, 0x920u + kKind);
+        raise_abort(ctl, rank);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ factor words (both CTAs)
+    const uint32_t* sa32 = reinterpret_cast<const uint32_t*>(g.sa);
+    const uint32_t* sb32 = reinterpret_cast<const uint32_t*>(g.sb);
+    const uint32_t* sb3_32 = reinterpret_cast<const uint32_t*>(kKind == kSwiGLU ? g.sb3 : g.sb);
+    const uint32_t dst = ptx::smem_u32(sf_base) + (uint32_t)lane * 16;
+    const uint32_t bar = ptx::mapa(ptx::smem_u32(&ctl->sf_full), 0);
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = cid; tile < total && ok; tile += ncl) {
+      const TileInfo ti = decode_pair_tile(ws, n_tiles, tile, (int)rank);
+      int64_t ra[4];  // rows past the buffer belong to no output: any row's words do
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ra[c] = min((int64_t)ti.row0 + 32 * c + lane, g.rows - 1) * sck;
+      const int blk = ti.n_idx * (bn / kBlock);
+      const int64_t r0 = ((int64_t)ti.e * nb + blk) * sck;
+      const int64_t r1 = kKind == kSwiGLU ? r0 : ((int64_t)ti.e * nb + min(blk + 1, nb - 1)) * sck;
+      for (int gk = 0; gk < sck; ++gk) {
+        uint32_t a[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a[c] = __ldg(sa32 + ra[c] + gk);
+        const uint32_t b0 = __ldg(sb32 + r0 + gk), b1 = __ldg(sb3_32 + r1 + gk);
+        ok = ptx::mbar_wait(ptx::smem_u32(&ctl->sf_empty), phase ^ 1u, timeout_ns, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        phase ^= 1u;
+        st_shared_v4(dst, a[0], a[1], a[2], a[3]);
+        st_shared_v4(dst + 512, b0, b0, b0, b0);
+        st_shared_v4(dst + 1024, b1, b1, b1, b1);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(bar);
+      }
+    }
+    if (!ok && lane == 0) {
+      record_error(ws, MOE_ERR_TIMEOUT, 0x930u + kKind);
+      raise_abort(ctl, rank);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    const int r = q * 32 + lane;
+    const uint32_t over = ptx::mapa(ptx::smem_u32(&ctl->over), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int tile = cid; tile < total; tile += ncl) {
+      const TileInfo ti = decode_pair_tile(ws, n_tiles, tile, (int)rank);
+      ok = ptx::mbar_wait(ptx::smem_u32(&ctl->tfull[acc]), acc_phase, timeout_ns, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (kKind != kSwiGLU && !ok) break;
+      ptx::tc_fence_after();
+      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kAccStep);
+      // accumulator 0 shares its last 32 columns (the upper half's), accumulator 1 its first 32
+      const bool shares = acc == 1 - half;
+      const bool flip = acc == 0 && half == 1;  // the shared columns lie in the second piece: take it first
+      if (!shares) {
+        ptx::tc_fence_before();  // the loads of the accumulator before the last
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(over);
+      }
+      const bool valid = r < ti.rows;
+      const int64_t p = (int64_t)ti.row0 + r;
+      const int n0 = ti.n_idx * bn;
+      const int vw = ti.rows - q * 32;  // rows of this warp's 32 that belong to the tile's expert
+      if constexpr (kKind == kSwiGLU) {
+        // this warp's 64 hidden columns, 32 at a time
+        float h[2][32];
+        uint32_t top = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = half * 64 + ((u == 1) != flip ? 32 : 0);
+          uint32_t a[32], b[32];
+          ptx::tmem_ld_32cols(t_row + c, a);
+          ptx::tmem_ld_32cols(t_row + kMmaN / 2 + c, b);
+          ptx::tmem_ld_wait();
+          if (u == 0 && shares) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(over);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            h[u][i] = silu_exact(__uint_as_float(a[i])) * __uint_as_float(b[i]);
+            if (n0 + c + (i & ~15) >= g.n) h[u][i] = 0.f;  // columns past the expert (n is a multiple of 16)
+            top = max(top, abs_bits(h[u][i]));
+          }
+        }
+        top_s[half * kRowsPerCta + r] = top;
+        if (half == 0 && lane == 0) bulk_wait_read();  // the quarter's last store has left its block
+        if (!pair_bar_and(1 + q, ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sb = scale_byte(__uint_as_float(max(top, top_s[(half ^ 1) * kRowsPerCta + r])));
+        const float f = inv_scale_value(sb);
+        const uint32_t stg = ptx::smem_u32(stg_base) + (uint32_t)(q * kStgBlockBytes);
+        uint8_t* hrow = reinterpret_cast<uint8_t*>(g.out) + p * g.n + n0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = half * 64 + ((u == 1) != flip ? 32 : 0);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_e4m3x4(h[u][16 * v + 4 * i] * f, h[u][16 * v + 4 * i + 1] * f, h[u][16 * v + 4 * i + 2] * f,
+                                 h[u][16 * v + 4 * i + 3] * f);
+            const int j = c / 16 + v;
+            if (vw >= 32)
+              st_shared_v4(stg + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) * 16)), w[0], w[1], w[2], w[3]);
+            else if (valid && n0 + 16 * j < g.n)
+              *reinterpret_cast<uint4*>(hrow + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (half == 0 && valid) g.out_scales[p * scale_cols(g.n) + ti.n_idx] = (uint8_t)sb;
+        if (vw >= 32) fence_async();
+        pair_bar_and(1 + q, true);
+        if (vw >= 32 && half == 0 && lane == 0) tma_store_2d(&tmY, n0, ti.row0 + q * 32, stg);
+      } else {
+        const float gate = !valid ? 0.f : g.gate ? g.gate[p] : 1.f;
+        const uint32_t stg = ptx::smem_u32(stg_base) + (uint32_t)((warp - kEpiWarp0) * kStgBlockBytes);
+        constexpr int kCols = kKind == kOutBf16 ? 64 : 32;  // columns of a 128-byte store row
+        constexpr int kPieces = 128 / kCols;
+#pragma unroll 1
+        for (int u = 0; u < kPieces; ++u) {
+          const int c = half * 128 + (flip ? kPieces - 1 - u : u) * kCols;
+          uint32_t pk[32];
+          if constexpr (kKind == kOutBf16) {
+            uint32_t a[32], b[32];
+            ptx::tmem_ld_32cols(t_row + c, a);
+            ptx::tmem_ld_32cols(t_row + c + 32, b);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              pk[i] = pack_bf16x2(gate * __uint_as_float(a[2 * i]), gate * __uint_as_float(a[2 * i + 1]));
+              pk[16 + i] = pack_bf16x2(gate * __uint_as_float(b[2 * i]), gate * __uint_as_float(b[2 * i + 1]));
+            }
+          } else {
+            ptx::tmem_ld_32cols(t_row + c, pk);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) pk[i] = __float_as_uint(gate * __uint_as_float(pk[i]));
+          }
+          if (u == 0 && shares) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(over);
+          }
+          if (vw <= 0 || n0 + c >= g.n) continue;  // warp-uniform
+          if (vw >= 32) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(stg + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) * 16)), pk[4 * j], pk[4 * j + 1], pk[4 * j + 2],
+                           pk[4 * j + 3]);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) tma_store_2d(&tmY, n0 + c, ti.row0 + q * 32, stg);
+          } else if (valid) {
+            constexpr int kEsz = kKind == kOutBf16 ? 2 : 4;
+            uint4* d = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(g.out) + (p * g.n + n0 + c) * kEsz);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              if (n0 + c + v * (16 / kEsz) < g.n) d[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+          }
+        }
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    bulk_wait_all();  // the tiled stores this lane issued have been written
+    if (!ok && lane == 0) {
+      record_error(ws, MOE_ERR_TIMEOUT, 0x940u + kKind);
+      raise_abort(ctl, rank);
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  __syncthreads();
+  if (leader && warp == 1 && lane == 0) {
+    // every copy and MMA of this pair has finished with both CTAs' TMEM
+    ptx::mma_commit_pair(ptx::smem_u32(&ctl->drain));
+    ptx::mbar_wait(ptx::smem_u32(&ctl->drain), 0u, timeout_ns, nullptr);
+  }
+  __syncthreads();
+  ptx::cluster_sync();  // neither CTA issues loads or MMAs any more
+  if (*abort_flag && threadIdx.x == 0) {
+    // copies already in flight land within microseconds; give them 200 us before the
+    // shared memory they target goes away
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 200000ull) {
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  if (warp == 2) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+template <int kKind>
+cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, int num_sms, int64_t timeout_ns, bool pdl, cudaStream_t st) {
+  constexpr int kEsz = kKind == kSwiGLU ? 1 : kKind == kOutBf16 ? 2 : 4;
+  CUtensorMap mA, mB, mB3, mY;
+  cudaError_t e;
+  const uint64_t wrows = (uint64_t)g.E * (uint64_t)g.n;
+  if ((e = make_tmap_rows128(&mA, g.a, 1, (uint64_t)g.rows, (uint64_t)g.K, kRowsPerCta)) != cudaSuccess) return e;
+  if ((e = make_tmap_rows128(&mB, g.b, 1, wrows, (uint64_t)g.K, kMmaN / 2)) != cudaSuccess) return e;
+  if ((e = make_tmap_rows128(&mB3, kKind == kSwiGLU ? g.b3 : g.b, 1, wrows, (uint64_t)g.K, kMmaN / 2)) != cudaSuccess) return e;
+  if ((e = make_tmap_rows128(&mY, g.out, kEsz, (uint64_t)g.rows, (uint64_t)g.n, 32)) != cudaSuccess) return e;
+  auto kern = gemm_fp8_kernel<kKind>;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes)) != cudaSuccess) return e;
+  // as many pairs as can be resident at once (persistent loop over pair tiles)
+  int grid = num_sms & ~1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0 && 2 * clusters < grid)
+    grid = 2 * clusters;
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, st, pdl, 2, mA, mB, mB3, mY, g, ws,
+                       timeout_ns);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int num_sms, int64_t timeout_ns, bool pdl,
+                           cudaStream_t st) {
+  switch (kind) {
+    case kSwiGLU: return launch_kind<kSwiGLU>(g, ws, num_sms, timeout_ns, pdl, st);
+    case kOutBf16: return launch_kind<kOutBf16>(g, ws, num_sms, timeout_ns, pdl, st);
+    default: return launch_kind<kOutF32>(g, ws, num_sms, timeout_ns, pdl, st);
+  }
+}
+
+}  // namespace fp8
+}  // namespace moe

@@ -150,10 +150,11 @@ cudaError_t launch_permute(const Shape& s, const Ws& ws, const Weights& w, int n
 cudaError_t launch_gemm1_simt(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st);
 cudaError_t launch_gemm2_simt(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st);
 cudaError_t launch_combine(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st);
-// expert stage of expert parallelism: the tile table over received segments; the balancing
-// scalar from per-expert totals
+// expert stage of expert parallelism: the tile table over received segments (seg_counts null:
+// one segment of s.N rows; `clear`: the kernel clears the header first); the balancing scalar
+// from per-expert totals
 cudaError_t launch_seg_scan(const Shape& s, const Ws& ws, const int32_t* seg_counts, int n_seg, int n_local,
-                            cudaStream_t st);
+                            bool clear, cudaStream_t st);
 cudaError_t launch_aux_totals(int E, int k, int64_t T, const int32_t* counts, const float* psum, float* aux_out,
                               cudaStream_t st);
 

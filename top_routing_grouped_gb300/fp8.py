@@ -1,0 +1,233 @@
+"""ctypes binding of the 8-bit operators in libmoe.so (the C ABI in include/moe_fp8.h).
+
+Argument marshalling only, as in ``moe``: outputs and workspaces are the caller's tensors, and
+every call enqueues its kernels on the current stream (or ``stream``) and returns.  8-bit tensors
+are torch.float8_e4m3fn, their block factors torch.float8_e8m0fnu (or the bytes as uint8); a row
+of c values has ``scale_cols(c)`` factors.  A wrong type, shape or layout raises ValueError before
+the library is called; the library's own checks raise ``moe.MoEError``.
+"""
+import ctypes
+
+import torch
+
+from . import moe
+from .moe import MOE_BF16, MOE_F32, MOE_OK, MoEError, MoeExpertConfig, _lib, _PATHS
+
+_P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+_SCALES = (torch.float8_e8m0fnu, torch.uint8)
+E4M3 = torch.float8_e4m3fn
+
+
+class MoeFp8MatmulConfig(ctypes.Structure):
+    _fields_ = [("max_rows", _I64), ("k", _I32), ("n", _I32), ("n_experts", _I32), ("n_sources", _I32),
+                ("out_dtype", _I32), ("path", _I32), ("wait_timeout_ns", _I64)]
+
+
+def _declare(name, *argtypes, restype=ctypes.c_int):
+    f = getattr(_lib, name)
+    f.argtypes, f.restype = list(argtypes), restype
+    return f
+
+
+_scale_cols = _declare("moe_fp8_scale_cols", _I64, restype=_I64)
+_quantize = _declare("moe_fp8_quantize", _P, _I32, _I64, _I64, _I64, _I32, _I64, _P, _P, _P)
+_rmsnorm = _declare("moe_rmsnorm", _P, _P, _P, _I32, _I64, _I32, _I64, _I64, _F, _P, _P, _P, _P, _P, _P)
+_rmsnorm_ws = _declare("moe_rmsnorm_backward_workspace", _I64, _I32, restype=ctypes.c_size_t)
+_rmsnorm_bwd = _declare("moe_rmsnorm_backward", _P, _I32, _P, _P, _P, _P, _I32, _I64, _I32, _I64, _P, _P, _P,
+                        ctypes.c_size_t, _P)
+_matmul_plan = _declare("moe_fp8_matmul_plan", ctypes.POINTER(MoeFp8MatmulConfig), ctypes.POINTER(_P),
+                        ctypes.POINTER(ctypes.c_size_t))
+_matmul = _declare("moe_fp8_matmul", *[_P] * 8, ctypes.c_size_t, _P)
+_expert_plan = _declare("moe_fp8_expert_plan", ctypes.POINTER(MoeExpertConfig), ctypes.POINTER(_P),
+                        ctypes.POINTER(ctypes.c_size_t))
+_expert_forward = _declare("moe_fp8_expert_forward", *[_P] * 13, ctypes.c_size_t, _P)
+_plan_destroy = _declare("moe_fp8_plan_destroy", _P, restype=None)
+_device_status = _declare("moe_fp8_get_device_status", _P, _P, _P)
+_ckpt_save = _declare("moe_checkpoint_save_rows", _P, _P, _I64, _I32, _P, _P, _P, _P, _P)
+_ckpt_backward = _declare("moe_checkpoint_backward_rows", *[_P] * 5, _I64, _I32, _P, _P, _P, _P)
+
+
+def _check(status, where):
+    if status != MOE_OK:
+        raise MoEError(status, where)
+
+
+def _want(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _rows(t, shape, dtypes, name, optional=False):
+    """The address of a row-major contiguous tensor of this shape and type."""
+    if t is None:
+        _want(optional, name + " is missing")
+        return None
+    _want(t.dtype in dtypes and tuple(t.shape) == shape and t.is_contiguous(),
+          f"{name} must be a contiguous {shape} tensor of {' or '.join(str(d) for d in dtypes)}")
+    return t.data_ptr()
+
+
+def _pitched(t, shape, dtypes, name):
+    """(address, row pitch) of a 2-D tensor whose rows are contiguous."""
+    _want(t.dtype in dtypes and tuple(t.shape) == shape, f"{name} must be a {shape} tensor of {' or '.join(str(d) for d in dtypes)}")
+    pitch = t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+    _want((t.stride(1) == 1 or shape[1] == 1) and pitch >= shape[1], f"{name} must have contiguous, separate rows")
+    return t.data_ptr(), pitch
+
+
+def scale_cols(cols):
+    """Factors of a row of `cols` values: one for every 128, in whole words of four."""
+    return int(_scale_cols(int(cols)))
+
+
+def quantize(x, q, scales, stream=None):
+    """Rows x [n, c] (fp32 or bf16; any row pitch) into q [n, c] with scales [n, scale_cols(c)]."""
+    n, c = x.shape
+    px, ldx = _pitched(x, (n, c), tuple(_DTYPES), "x")
+    _check(_quantize(px, _DTYPES[x.dtype], n, c, ldx, 1, 0, _rows(q, (n, c), (E4M3,), "q"),
+                     _rows(scales, (n, scale_cols(c)), _SCALES, "scales"), _stream(stream)), "moe_fp8_quantize")
+
+
+def quantize_weights(w, q, scales, stream=None):
+    """Weights w [E, n, c] (fp32 or bf16) into q [E, n, c] with scales [E, ceil(n/128), scale_cols(c)]."""
+    E, n, c = w.shape
+    _check(_quantize(_rows(w, (E, n, c), tuple(_DTYPES), "w"), _DTYPES[w.dtype], E * n, c, c, 128, n,
+                     _rows(q, (E, n, c), (E4M3,), "q"),
+                     _rows(scales, (E, (n + 127) // 128, scale_cols(c)), _SCALES, "scales"), _stream(stream)),
+           "moe_fp8_quantize")
+
+
+def rmsnorm(x, weight, residual=None, residual_out=None, out=None, q=None, scales=None, rstd=None, eps=1e-6, stream=None):
+    """r = x + residual, n = r * rstd * weight into whichever outputs are given (moe_rmsnorm):
+    residual_out and out [T, d] in x's type, q e4m3 with scales, rstd [T] fp32.  x and residual may
+    have any row pitch; weight fp32 [d] or None for ones."""
+    _want(x.dim() == 2 and x.dtype in _DTYPES, "x must be a 2-D fp32 or bf16 tensor")
+    T, d = x.shape
+    t = (x.dtype,)
+    px, ldx = _pitched(x, (T, d), t, "x")
+    pr, ldr = (None, d) if residual is None else _pitched(residual, (T, d), t, "residual")
+    _check(_rmsnorm(px, pr, _rows(weight, (d,), (torch.float32,), "weight", True), _DTYPES[x.dtype], T, d, ldx, ldr, eps,
+                    _rows(residual_out, (T, d), t, "residual_out", True), _rows(out, (T, d), t, "out", True),
+                    _rows(q, (T, d), (E4M3,), "q", True),
+                    None if scales is None else _rows(scales, (T, scale_cols(d)), _SCALES, "scales"),
+                    _rows(rstd, (T,), (torch.float32,), "rstd", True), _stream(stream)), "moe_rmsnorm")
+
+
+def rmsnorm_backward_workspace(T, d, device="cuda"):
+    """The workspace of rmsnorm_backward for [T, d] (when dweight is wanted)."""
+    return torch.empty(max(1, int(_rmsnorm_ws(int(T), int(d)))), dtype=torch.uint8, device=device)
+
+
+def rmsnorm_backward(dout, r, weight, rstd, dx, dweight=None, workspace=None, dresidual=None, stream=None):
+    """dx and dweight from dout = dL/dn (fp32 or bf16) and what the forward kept: r (its
+    residual_out, or x without a residual; any row pitch) and rstd; dresidual is the gradient that
+    reaches r on its other way."""
+    _want(r.dim() == 2 and r.dtype in _DTYPES, "r must be a 2-D fp32 or bf16 tensor")
+    T, d = r.shape
+    t, f32 = (r.dtype,), (torch.float32,)
+    pr, ldr = _pitched(r, (T, d), t, "r")
+    pd = _rows(dout, (T, d), tuple(_DTYPES), "dout")
+    _check(_rmsnorm_bwd(pd, _DTYPES[dout.dtype], pr, _rows(weight, (d,), f32, "weight", True), _rows(rstd, (T,), f32, "rstd"),
+                        _rows(dresidual, (T, d), t, "dresidual", True), _DTYPES[r.dtype], T, d, ldr, _rows(dx, (T, d), t, "dx"),
+                        _rows(dweight, (d,), f32, "dweight", True), None if workspace is None else workspace.data_ptr(),
+                        0 if workspace is None else workspace.numel(), _stream(stream)), "moe_rmsnorm_backward")
+
+
+class _Fp8Plan:
+    def _make(self, make, cfg, where):
+        self._h = ctypes.c_void_p()
+        wsb = ctypes.c_size_t(0)
+        _check(make(ctypes.byref(cfg), ctypes.byref(self._h), ctypes.byref(wsb)), where)
+        self.workspace_bytes = wsb.value
+
+    def __del__(self):
+        if getattr(self, "_h", None) and self._h.value:
+            _plan_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    @property
+    def handle(self):
+        return self._h
+
+    def new_workspace(self, device="cuda"):
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+
+    def device_status(self, workspace, stream=None):
+        """Synchronises the stream; returns the status code (MOE_OK == 0)."""
+        return _device_status(self._h, workspace.data_ptr(), _stream(stream))
+
+
+class Fp8MatmulPlan(_Fp8Plan):
+    """out[p] = A[p] . W_e^T for rows grouped by expert (moe_fp8_matmul): K columns in, n out."""
+
+    def __init__(self, max_rows, K, n, n_experts=1, n_sources=1, out_dtype="bf16", path="auto", wait_timeout_ns=0):
+        self.out_dtype = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+        self.cfg = MoeFp8MatmulConfig(int(max_rows), int(K), int(n), int(n_experts), int(n_sources), _DTYPES[self.out_dtype],
+                                      _PATHS[path], int(wait_timeout_ns))
+        R, E = int(max_rows), int(n_experts)
+        self._make(_matmul_plan, self.cfg, "moe_fp8_matmul_plan")
+        self._a, self._sa = (R, int(K)), (R, scale_cols(K))
+        self._w, self._sw = (E, int(n), int(K)), (E, (int(n) + 127) // 128, scale_cols(K))
+        self._out, self._seg = (R, int(n)), (E * int(n_sources),)
+
+    def forward(self, seg_counts, a, a_scales, w, w_scales, out, workspace, stream=None):
+        """seg_counts: int32 rows of each (source, expert) segment, or None for one segment of
+        max_rows rows."""
+        _check(_matmul(self._h, _rows(seg_counts, self._seg, (torch.int32,), "seg_counts", True),
+                       _rows(a, self._a, (E4M3,), "a"), _rows(a_scales, self._sa, _SCALES, "a_scales"),
+                       _rows(w, self._w, (E4M3,), "w"), _rows(w_scales, self._sw, _SCALES, "w_scales"),
+                       _rows(out, self._out, (self.out_dtype,), "out"), workspace.data_ptr(), workspace.numel(),
+                       _stream(stream)), "moe_fp8_matmul")
+
+
+class Fp8ExpertPlan(_Fp8Plan):
+    """The expert stage in 8 bits (moe_fp8_expert_forward); the arguments are moe.ExpertPlan's."""
+
+    def __init__(self, max_rows, d, E_local, n_sources, F, path="auto", wait_timeout_ns=0):
+        R, d, E, W, F = int(max_rows), int(d), int(E_local), int(n_sources), int(F)
+        self.cfg = MoeExpertConfig(R, d, E, W, F, MOE_BF16, _PATHS[path], int(wait_timeout_ns))
+        self._make(_expert_plan, self.cfg, "moe_fp8_expert_plan")
+        self.max_rows, self.d, self.E_local, self.n_sources, self.F = R, d, E, W, F
+        self._x, self._sx = (R, d), (R, scale_cols(d))
+        self._w13, self._s13 = (E, F, d), (E, (F + 127) // 128, scale_cols(d))
+        self._w2, self._s2 = (E, d, F), (E, (d + 127) // 128, scale_cols(F))
+        self._seg = (E * W,)
+
+    def forward(self, seg_counts, x_rows, x_scales, gates, w1, s1, w3, s3, w2, s2, y_rows, workspace, stream=None):
+        _check(_expert_forward(self._h, _rows(seg_counts, self._seg, (torch.int32,), "seg_counts", True),
+                               _rows(x_rows, self._x, (E4M3,), "x_rows"), _rows(x_scales, self._sx, _SCALES, "x_scales"),
+                               _rows(gates, (self.max_rows,), (torch.float32,), "gates"),
+                               _rows(w1, self._w13, (E4M3,), "w1"), _rows(s1, self._s13, _SCALES, "s1"),
+                               _rows(w3, self._w13, (E4M3,), "w3"), _rows(s3, self._s13, _SCALES, "s3"),
+                               _rows(w2, self._w2, (E4M3,), "w2"), _rows(s2, self._s2, _SCALES, "s2"),
+                               _rows(y_rows, self._x, (torch.bfloat16,), "y_rows"), workspace.data_ptr(), workspace.numel(),
+                               _stream(stream)), "moe_fp8_expert_forward")
+
+
+def checkpoint_save(a, b, qa, sa, qb, sb, stream=None):
+    """The pre-activations a, b [n, F] (bf16) into 8 bits (moe_checkpoint_save_rows)."""
+    _want(a.dim() == 2, "a must be 2-D")
+    n, F = a.shape
+    s = (n, scale_cols(F))
+    bf = (torch.bfloat16,)
+    _check(_ckpt_save(_rows(a, (n, F), bf, "a"), _rows(b, (n, F), bf, "b"), n, F, _rows(qa, (n, F), (E4M3,), "qa"),
+                      _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), (E4M3,), "qb"), _rows(sb, s, _SCALES, "sb"),
+                      _stream(stream)), "moe_checkpoint_save_rows")
+
+
+def checkpoint_backward(qa, sa, qb, sb, dh, da, db, h=None, stream=None):
+    """The SwiGLU's backward out of the checkpoint (moe_checkpoint_backward_rows): da, db and, if
+    given, the hidden rows h, all [n, F] bf16, from dh."""
+    _want(qa.dim() == 2, "qa must be 2-D")
+    n, F = qa.shape
+    s = (n, scale_cols(F))
+    bf = (torch.bfloat16,)
+    _check(_ckpt_backward(_rows(qa, (n, F), (E4M3,), "qa"), _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), (E4M3,), "qb"),
+                          _rows(sb, s, _SCALES, "sb"), _rows(dh, (n, F), bf, "dh"), n, F, _rows(da, (n, F), bf, "da"),
+                          _rows(db, (n, F), bf, "db"), _rows(h, (n, F), bf, "h", True), _stream(stream)),
+           "moe_checkpoint_backward_rows")

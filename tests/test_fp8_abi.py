@@ -169,9 +169,11 @@ def test_binding_checks_types_shapes_and_layouts(fp8):
            lambda: fp8.rmsnorm_backward(x[:3], x, None, torch.ones(4), x), lambda: fp8.rmsnorm_backward(x, x, None, torch.ones(3), x),
            lambda: fp8.checkpoint_save(x, x, q, s, q, s), lambda: fp8.checkpoint_backward(q, s, q, s, x, x, x)]
     for i, f in enumerate(bad):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError) as ei:
             f()
-            pytest.fail(f"case {i} was taken")
+        assert "must be a" in str(ei.value) and "GPU" not in str(ei.value), i
+    with pytest.raises(ValueError, match="GPU memory"):  # nothing wrong but where the tensors are
+        fp8.quantize(x, q, s)
     plan = fp8.Fp8MatmulPlan(4, 64, 32)
     with pytest.raises(ValueError):
         plan.forward(None, q, s, torch.zeros(1, 32, 64).to(fp8.E4M3), s, torch.zeros(4, 32), torch.zeros(1 << 16, dtype=torch.uint8))

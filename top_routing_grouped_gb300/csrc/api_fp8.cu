@@ -154,7 +154,7 @@ moe_status begin(moe_fp8_plan_t plan, const int32_t* seg_counts, void* workspace
 }
 
 moe_status product(moe_fp8_plan_t plan, int kind, const fp8::GemmArgs& g, const Ws& ws, cudaStream_t st, const char* what) {
-  return cuda_status(plan->tc ? fp8::launch_gemm_tc(kind, g, ws, plan->num_sms, plan->timeout_ns, true, st)
+  return cuda_status(plan->tc ? fp8::launch_gemm_tc(kind, g, ws, plan->device, plan->num_sms, plan->timeout_ns, true, st)
                               : fp8::launch_gemm_simt(kind, g, ws, plan->num_sms, st),
                      what);
 }

@@ -45,8 +45,8 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
                                     int64_t ldr, void* dx, float* dweight, float* parts, cudaStream_t st);
 
 cudaError_t launch_gemm_simt(int kind, const GemmArgs& g, const Ws& ws, int num_sms, cudaStream_t st);
-cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int num_sms, int64_t timeout_ns, bool pdl,
-                           cudaStream_t st);
+cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns,
+                           bool pdl, cudaStream_t st);
 
 }  // namespace fp8
 }  // namespace moe

@@ -33,6 +33,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "fp8_common.cuh"
 #include "gemm_tc.h"
 #include "tc_ptx.cuh"
@@ -518,19 +520,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// CTAs of a persistent launch: as many pairs as can be resident at once.  The kernel's attribute
+// and the count are set and asked for once per kernel and device (a call of one token is shorter
+// than the two questions); two threads that come first may both ask and store the same answer.
 template <int kKind>
-cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, int num_sms, int64_t timeout_ns, bool pdl, cudaStream_t st) {
-  constexpr int kEsz = kKind == kSwiGLU ? 1 : kKind == kOutBf16 ? 2 : 4;
-  CUtensorMap mA, mB, mB3, mY;
-  cudaError_t e;
-  const uint64_t wrows = (uint64_t)g.E * (uint64_t)g.n;
-  if ((e = make_tmap_rows128(&mA, g.a, 1, (uint64_t)g.rows, (uint64_t)g.K, kRowsPerCta)) != cudaSuccess) return e;
-  if ((e = make_tmap_rows128(&mB, g.b, 1, wrows, (uint64_t)g.K, kMmaN / 2)) != cudaSuccess) return e;
-  if ((e = make_tmap_rows128(&mB3, kKind == kSwiGLU ? g.b3 : g.b, 1, wrows, (uint64_t)g.K, kMmaN / 2)) != cudaSuccess) return e;
-  if ((e = make_tmap_rows128(&mY, g.out, kEsz, (uint64_t)g.rows, (uint64_t)g.n, 32)) != cudaSuccess) return e;
+int persistent_grid(int device, int num_sms, cudaError_t* err) {
   auto kern = gemm_fp8_kernel<kKind>;
-  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes)) != cudaSuccess) return e;
-  // as many pairs as can be resident at once (persistent loop over pair tiles)
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  const bool keep = device >= 0 && device < kMaxDevices;
+  *err = cudaSuccess;
+  if (keep)
+    if (const int g = known[device].load(std::memory_order_acquire)) return g;
+  if ((*err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes)) != cudaSuccess) return 0;
   int grid = num_sms & ~1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
@@ -546,18 +548,37 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, int num_sms, int64_t ti
   int clusters = 0;
   if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0 && 2 * clusters < grid)
     grid = 2 * clusters;
+  if (keep) known[device].store(grid, std::memory_order_release);
+  return grid;
+}
+
+template <int kKind>
+cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns, bool pdl,
+                        cudaStream_t st) {
+  constexpr int kEsz = kKind == kSwiGLU ? 1 : kKind == kOutBf16 ? 2 : 4;
+  CUtensorMap mA, mB, mB3, mY;
+  cudaError_t e;
+  const uint64_t wrows = (uint64_t)g.E * (uint64_t)g.n;
+  if ((e = make_tmap_rows128(&mA, g.a, 1, (uint64_t)g.rows, (uint64_t)g.K, kRowsPerCta)) != cudaSuccess) return e;
+  if ((e = make_tmap_rows128(&mB, g.b, 1, wrows, (uint64_t)g.K, kMmaN / 2)) != cudaSuccess) return e;
+  mB3 = mB;
+  if (kKind == kSwiGLU && (e = make_tmap_rows128(&mB3, g.b3, 1, wrows, (uint64_t)g.K, kMmaN / 2)) != cudaSuccess) return e;
+  if ((e = make_tmap_rows128(&mY, g.out, kEsz, (uint64_t)g.rows, (uint64_t)g.n, 32)) != cudaSuccess) return e;
+  auto kern = gemm_fp8_kernel<kKind>;
+  const int grid = persistent_grid<kKind>(device, num_sms, &e);
+  if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, st, pdl, 2, mA, mB, mB3, mY, g, ws,
                        timeout_ns);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int num_sms, int64_t timeout_ns, bool pdl,
-                           cudaStream_t st) {
+cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns,
+                           bool pdl, cudaStream_t st) {
   switch (kind) {
-    case kSwiGLU: return launch_kind<kSwiGLU>(g, ws, num_sms, timeout_ns, pdl, st);
-    case kOutBf16: return launch_kind<kOutBf16>(g, ws, num_sms, timeout_ns, pdl, st);
-    default: return launch_kind<kOutF32>(g, ws, num_sms, timeout_ns, pdl, st);
+    case kSwiGLU: return launch_kind<kSwiGLU>(g, ws, device, num_sms, timeout_ns, pdl, st);
+    case kOutBf16: return launch_kind<kOutBf16>(g, ws, device, num_sms, timeout_ns, pdl, st);
+    default: return launch_kind<kOutF32>(g, ws, device, num_sms, timeout_ns, pdl, st);
   }
 }
 

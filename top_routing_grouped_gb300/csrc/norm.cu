@@ -142,8 +142,10 @@ cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* wei
                            float* rstd, cudaStream_t st) {
   const size_t smem = (size_t)d * sizeof(float);
   auto kern = bf16 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024 &&  // what a launch may have without asking
+      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return e;
   const int64_t grid = rows < (1 << 20) ? rows : 1 << 20;
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, false, 1, x, residual, weight, rows, d, ldx,
                        ldr, eps, residual_out, out, (uint8_t*)q, scales, rstd);
@@ -158,8 +160,10 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
   const size_t smem = (size_t)d * sizeof(float);
   auto kern = bf16 ? (dout_bf16 ? rmsnorm_backward_kernel<true, true> : rmsnorm_backward_kernel<true, false>)
                    : (dout_bf16 ? rmsnorm_backward_kernel<false, true> : rmsnorm_backward_kernel<false, false>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024 &&  // what a launch may have without asking
+      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return e;
   if (n > 0) {
     e = launch_kernel(kern, dim3((unsigned)n), dim3(kThreads), smem, st, false, 1, dout, r, weight, rstd, dresidual, rows,
                       d, ldr, dx, dweight ? parts : nullptr);

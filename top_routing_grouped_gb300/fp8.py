@@ -10,13 +10,13 @@ import ctypes
 
 import torch
 
-from . import moe
 from .moe import MOE_BF16, MOE_F32, MOE_OK, MoEError, MoeExpertConfig, _lib, _PATHS
 
 _P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 _SCALES = (torch.float8_e8m0fnu, torch.uint8)
 E4M3 = torch.float8_e4m3fn
+_FLOATS, _E4, _F32, _BF16 = tuple(_DTYPES), (E4M3,), (torch.float32,), (torch.bfloat16,)
 
 
 class MoeFp8MatmulConfig(ctypes.Structure):
@@ -30,7 +30,7 @@ def _declare(name, *argtypes, restype=ctypes.c_int):
     return f
 
 
-_scale_cols = _declare("moe_fp8_scale_cols", _I64, restype=_I64)
+_declare("moe_fp8_scale_cols", _I64, restype=_I64)
 _quantize = _declare("moe_fp8_quantize", _P, _I32, _I64, _I64, _I64, _I32, _I64, _P, _P, _P)
 _rmsnorm = _declare("moe_rmsnorm", _P, _P, _P, _I32, _I64, _I32, _I64, _I64, _F, _P, _P, _P, _P, _P, _P)
 _rmsnorm_ws = _declare("moe_rmsnorm_backward_workspace", _I64, _I32, restype=ctypes.c_size_t)
@@ -58,47 +58,67 @@ def _want(cond, what):
         raise ValueError(what)
 
 
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream  # an order cheaper than building a torch.cuda.Stream
 
 
-def _rows(t, shape, dtypes, name, optional=False):
+def _stream(stream, *tensors):
+    """The given stream, or the current one of the tensors' device; refuses tensors in host memory."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("every tensor must be in GPU memory")
+    return _raw_stream(tensors[0].get_device()) if stream is None else stream.cuda_stream
+
+
+# The checks below run on every call, and a call of a few rows takes the GPU two or three
+# microseconds: messages are put together only when a check has failed.
+
+def _refuse(name, shape, dtypes, how):
+    raise ValueError(f"{name} must be a {how} {tuple(shape)} tensor of {' or '.join(str(d) for d in dtypes)}")
+
+
+def _rows(t, shape, dtypes, name):
     """The address of a row-major contiguous tensor of this shape and type."""
-    if t is None:
-        _want(optional, name + " is missing")
-        return None
-    _want(t.dtype in dtypes and tuple(t.shape) == shape and t.is_contiguous(),
-          f"{name} must be a contiguous {shape} tensor of {' or '.join(str(d) for d in dtypes)}")
+    if t is None or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        _refuse(name, shape, dtypes, "contiguous")
     return t.data_ptr()
 
 
+def _maybe(t, shape, dtypes, name):
+    return None if t is None else _rows(t, shape, dtypes, name)
+
+
 def _pitched(t, shape, dtypes, name):
-    """(address, row pitch) of a 2-D tensor whose rows are contiguous."""
-    _want(t.dtype in dtypes and tuple(t.shape) == shape, f"{name} must be a {shape} tensor of {' or '.join(str(d) for d in dtypes)}")
-    pitch = t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
-    _want((t.stride(1) == 1 or shape[1] == 1) and pitch >= shape[1], f"{name} must have contiguous, separate rows")
+    """(address, row pitch) of a 2-D tensor whose rows are contiguous and separate."""
+    if t.dtype not in dtypes or t.shape != shape:
+        _refuse(name, shape, dtypes, "row-contiguous")
+    n, c = shape
+    pitch, step = t.stride()
+    if n <= 1 and pitch < c:
+        pitch = c
+    if (step != 1 and c > 1) or pitch < c:
+        _refuse(name, shape, dtypes, "row-contiguous")
     return t.data_ptr(), pitch
 
 
 def scale_cols(cols):
     """Factors of a row of `cols` values: one for every 128, in whole words of four."""
-    return int(_scale_cols(int(cols)))
+    return (int(cols) + 511) // 512 * 4 if cols > 0 else 0
 
 
 def quantize(x, q, scales, stream=None):
     """Rows x [n, c] (fp32 or bf16; any row pitch) into q [n, c] with scales [n, scale_cols(c)]."""
     n, c = x.shape
-    px, ldx = _pitched(x, (n, c), tuple(_DTYPES), "x")
-    _check(_quantize(px, _DTYPES[x.dtype], n, c, ldx, 1, 0, _rows(q, (n, c), (E4M3,), "q"),
-                     _rows(scales, (n, scale_cols(c)), _SCALES, "scales"), _stream(stream)), "moe_fp8_quantize")
+    px, ldx = _pitched(x, (n, c), _FLOATS, "x")
+    _check(_quantize(px, _DTYPES[x.dtype], n, c, ldx, 1, 0, _rows(q, (n, c), _E4, "q"),
+                     _rows(scales, (n, scale_cols(c)), _SCALES, "scales"), _stream(stream, x, q, scales)), "moe_fp8_quantize")
 
 
 def quantize_weights(w, q, scales, stream=None):
     """Weights w [E, n, c] (fp32 or bf16) into q [E, n, c] with scales [E, ceil(n/128), scale_cols(c)]."""
     E, n, c = w.shape
-    _check(_quantize(_rows(w, (E, n, c), tuple(_DTYPES), "w"), _DTYPES[w.dtype], E * n, c, c, 128, n,
-                     _rows(q, (E, n, c), (E4M3,), "q"),
-                     _rows(scales, (E, (n + 127) // 128, scale_cols(c)), _SCALES, "scales"), _stream(stream)),
+    _check(_quantize(_rows(w, (E, n, c), _FLOATS, "w"), _DTYPES[w.dtype], E * n, c, c, 128, n,
+                     _rows(q, (E, n, c), _E4, "q"),
+                     _rows(scales, (E, (n + 127) // 128, scale_cols(c)), _SCALES, "scales"), _stream(stream, w, q, scales)),
            "moe_fp8_quantize")
 
 
@@ -111,11 +131,11 @@ def rmsnorm(x, weight, residual=None, residual_out=None, out=None, q=None, scale
     t = (x.dtype,)
     px, ldx = _pitched(x, (T, d), t, "x")
     pr, ldr = (None, d) if residual is None else _pitched(residual, (T, d), t, "residual")
-    _check(_rmsnorm(px, pr, _rows(weight, (d,), (torch.float32,), "weight", True), _DTYPES[x.dtype], T, d, ldx, ldr, eps,
-                    _rows(residual_out, (T, d), t, "residual_out", True), _rows(out, (T, d), t, "out", True),
-                    _rows(q, (T, d), (E4M3,), "q", True),
-                    None if scales is None else _rows(scales, (T, scale_cols(d)), _SCALES, "scales"),
-                    _rows(rstd, (T,), (torch.float32,), "rstd", True), _stream(stream)), "moe_rmsnorm")
+    _check(_rmsnorm(px, pr, _maybe(weight, (d,), _F32, "weight"), _DTYPES[x.dtype], T, d, ldx, ldr, eps,
+                    _maybe(residual_out, (T, d), t, "residual_out"), _maybe(out, (T, d), t, "out"),
+                    _maybe(q, (T, d), _E4, "q"),
+                    _maybe(scales, (T, scale_cols(d)), _SCALES, "scales"),
+                    _maybe(rstd, (T,), _F32, "rstd"), _stream(stream, x, weight, residual, residual_out, out, q, scales, rstd)), "moe_rmsnorm")
 
 
 def rmsnorm_backward_workspace(T, d, device="cuda"):
@@ -129,13 +149,13 @@ def rmsnorm_backward(dout, r, weight, rstd, dx, dweight=None, workspace=None, dr
     reaches r on its other way."""
     _want(r.dim() == 2 and r.dtype in _DTYPES, "r must be a 2-D fp32 or bf16 tensor")
     T, d = r.shape
-    t, f32 = (r.dtype,), (torch.float32,)
+    t, f32 = (r.dtype,), _F32
     pr, ldr = _pitched(r, (T, d), t, "r")
-    pd = _rows(dout, (T, d), tuple(_DTYPES), "dout")
-    _check(_rmsnorm_bwd(pd, _DTYPES[dout.dtype], pr, _rows(weight, (d,), f32, "weight", True), _rows(rstd, (T,), f32, "rstd"),
-                        _rows(dresidual, (T, d), t, "dresidual", True), _DTYPES[r.dtype], T, d, ldr, _rows(dx, (T, d), t, "dx"),
-                        _rows(dweight, (d,), f32, "dweight", True), None if workspace is None else workspace.data_ptr(),
-                        0 if workspace is None else workspace.numel(), _stream(stream)), "moe_rmsnorm_backward")
+    pd = _rows(dout, (T, d), _FLOATS, "dout")
+    _check(_rmsnorm_bwd(pd, _DTYPES[dout.dtype], pr, _maybe(weight, (d,), f32, "weight"), _rows(rstd, (T,), f32, "rstd"),
+                        _maybe(dresidual, (T, d), t, "dresidual"), _DTYPES[r.dtype], T, d, ldr, _rows(dx, (T, d), t, "dx"),
+                        _maybe(dweight, (d,), f32, "dweight"), None if workspace is None else workspace.data_ptr(),
+                        0 if workspace is None else workspace.numel(), _stream(stream, dout, r, weight, rstd, dx, dweight, workspace, dresidual)), "moe_rmsnorm_backward")
 
 
 class _Fp8Plan:
@@ -159,7 +179,7 @@ class _Fp8Plan:
 
     def device_status(self, workspace, stream=None):
         """Synchronises the stream; returns the status code (MOE_OK == 0)."""
-        return _device_status(self._h, workspace.data_ptr(), _stream(stream))
+        return _device_status(self._h, workspace.data_ptr(), _stream(stream, workspace))
 
 
 class Fp8MatmulPlan(_Fp8Plan):
@@ -178,11 +198,11 @@ class Fp8MatmulPlan(_Fp8Plan):
     def forward(self, seg_counts, a, a_scales, w, w_scales, out, workspace, stream=None):
         """seg_counts: int32 rows of each (source, expert) segment, or None for one segment of
         max_rows rows."""
-        _check(_matmul(self._h, _rows(seg_counts, self._seg, (torch.int32,), "seg_counts", True),
-                       _rows(a, self._a, (E4M3,), "a"), _rows(a_scales, self._sa, _SCALES, "a_scales"),
-                       _rows(w, self._w, (E4M3,), "w"), _rows(w_scales, self._sw, _SCALES, "w_scales"),
+        _check(_matmul(self._h, _maybe(seg_counts, self._seg, (torch.int32,), "seg_counts"),
+                       _rows(a, self._a, _E4, "a"), _rows(a_scales, self._sa, _SCALES, "a_scales"),
+                       _rows(w, self._w, _E4, "w"), _rows(w_scales, self._sw, _SCALES, "w_scales"),
                        _rows(out, self._out, (self.out_dtype,), "out"), workspace.data_ptr(), workspace.numel(),
-                       _stream(stream)), "moe_fp8_matmul")
+                       _stream(stream, a, a_scales, w, w_scales, out, workspace, seg_counts)), "moe_fp8_matmul")
 
 
 class Fp8ExpertPlan(_Fp8Plan):
@@ -199,14 +219,14 @@ class Fp8ExpertPlan(_Fp8Plan):
         self._seg = (E * W,)
 
     def forward(self, seg_counts, x_rows, x_scales, gates, w1, s1, w3, s3, w2, s2, y_rows, workspace, stream=None):
-        _check(_expert_forward(self._h, _rows(seg_counts, self._seg, (torch.int32,), "seg_counts", True),
-                               _rows(x_rows, self._x, (E4M3,), "x_rows"), _rows(x_scales, self._sx, _SCALES, "x_scales"),
-                               _rows(gates, (self.max_rows,), (torch.float32,), "gates"),
-                               _rows(w1, self._w13, (E4M3,), "w1"), _rows(s1, self._s13, _SCALES, "s1"),
-                               _rows(w3, self._w13, (E4M3,), "w3"), _rows(s3, self._s13, _SCALES, "s3"),
-                               _rows(w2, self._w2, (E4M3,), "w2"), _rows(s2, self._s2, _SCALES, "s2"),
-                               _rows(y_rows, self._x, (torch.bfloat16,), "y_rows"), workspace.data_ptr(), workspace.numel(),
-                               _stream(stream)), "moe_fp8_expert_forward")
+        _check(_expert_forward(self._h, _maybe(seg_counts, self._seg, (torch.int32,), "seg_counts"),
+                               _rows(x_rows, self._x, _E4, "x_rows"), _rows(x_scales, self._sx, _SCALES, "x_scales"),
+                               _rows(gates, (self.max_rows,), _F32, "gates"),
+                               _rows(w1, self._w13, _E4, "w1"), _rows(s1, self._s13, _SCALES, "s1"),
+                               _rows(w3, self._w13, _E4, "w3"), _rows(s3, self._s13, _SCALES, "s3"),
+                               _rows(w2, self._w2, _E4, "w2"), _rows(s2, self._s2, _SCALES, "s2"),
+                               _rows(y_rows, self._x, _BF16, "y_rows"), workspace.data_ptr(), workspace.numel(),
+                               _stream(stream, x_rows, x_scales, gates, w1, s1, w3, s3, w2, s2, y_rows, workspace, seg_counts)), "moe_fp8_expert_forward")
 
 
 def checkpoint_save(a, b, qa, sa, qb, sb, stream=None):
@@ -214,10 +234,9 @@ def checkpoint_save(a, b, qa, sa, qb, sb, stream=None):
     _want(a.dim() == 2, "a must be 2-D")
     n, F = a.shape
     s = (n, scale_cols(F))
-    bf = (torch.bfloat16,)
-    _check(_ckpt_save(_rows(a, (n, F), bf, "a"), _rows(b, (n, F), bf, "b"), n, F, _rows(qa, (n, F), (E4M3,), "qa"),
-                      _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), (E4M3,), "qb"), _rows(sb, s, _SCALES, "sb"),
-                      _stream(stream)), "moe_checkpoint_save_rows")
+    _check(_ckpt_save(_rows(a, (n, F), _BF16, "a"), _rows(b, (n, F), _BF16, "b"), n, F, _rows(qa, (n, F), _E4, "qa"),
+                      _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), _E4, "qb"), _rows(sb, s, _SCALES, "sb"),
+                      _stream(stream, a, b, qa, sa, qb, sb)), "moe_checkpoint_save_rows")
 
 
 def checkpoint_backward(qa, sa, qb, sb, dh, da, db, h=None, stream=None):
@@ -226,8 +245,7 @@ def checkpoint_backward(qa, sa, qb, sb, dh, da, db, h=None, stream=None):
     _want(qa.dim() == 2, "qa must be 2-D")
     n, F = qa.shape
     s = (n, scale_cols(F))
-    bf = (torch.bfloat16,)
-    _check(_ckpt_backward(_rows(qa, (n, F), (E4M3,), "qa"), _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), (E4M3,), "qb"),
-                          _rows(sb, s, _SCALES, "sb"), _rows(dh, (n, F), bf, "dh"), n, F, _rows(da, (n, F), bf, "da"),
-                          _rows(db, (n, F), bf, "db"), _rows(h, (n, F), bf, "h", True), _stream(stream)),
+    _check(_ckpt_backward(_rows(qa, (n, F), _E4, "qa"), _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), _E4, "qb"),
+                          _rows(sb, s, _SCALES, "sb"), _rows(dh, (n, F), _BF16, "dh"), n, F, _rows(da, (n, F), _BF16, "da"),
+                          _rows(db, (n, F), _BF16, "db"), _maybe(h, (n, F), _BF16, "h"), _stream(stream, qa, sa, qb, sb, dh, da, db, h)),
            "moe_checkpoint_backward_rows")

@@ -216,7 +216,7 @@ moe_status moe_rmsnorm(const void* x, const void* residual, const float* weight,
 
 size_t moe_rmsnorm_backward_workspace(int64_t rows, int32_t d) {
   if (rows < 0 || d < 1) return 0;
-  return ((size_t)fp8::rmsnorm_backward_parts(rows) * (size_t)d * sizeof(float) + 255) / 256 * 256;
+  return ((size_t)fp8::rmsnorm_backward_parts(rows, d) * (size_t)d * sizeof(float) + 255) / 256 * 256;
 }
 
 moe_status moe_rmsnorm_backward(const void* dout, int32_t dout_dtype, const void* r, const float* weight,

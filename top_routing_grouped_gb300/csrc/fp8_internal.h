@@ -39,7 +39,7 @@ cudaError_t launch_checkpoint_backward(const void* qa, const uint8_t* sa, const 
 cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* weight, bool bf16, int64_t rows, int d,
                            int64_t ldx, int64_t ldr, float eps, void* residual_out, void* out, void* q, uint8_t* scales,
                            float* rstd, cudaStream_t st);
-int rmsnorm_backward_parts(int64_t rows);  // partial sums of dweight
+int rmsnorm_backward_parts(int64_t rows, int d);  // partial sums of dweight
 cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void* r, const float* weight,
                                     const float* rstd, const void* dresidual, bool bf16, int64_t rows, int d,
                                     int64_t ldr, void* dx, float* dweight, float* parts, cudaStream_t st);

@@ -7,8 +7,17 @@
 //   dweight = sum_t dn xhat
 //
 // Both read and write each value once: HBM bounds them (one row: the launch does).
+//
+// A row is held in registers by W warps, eight values a thread and piece, V pieces a thread; the
+// CTAs are persistent and a row's loads are issued before the row before it is reduced, so the
+// loads of one row run under the reduction and the stores of another.  Rows of whole 16-byte
+// vectors give a thread 8 consecutive columns (kVec); others give it every 32nd of 256, so that
+// single loads and stores of a warp still touch consecutive addresses.
 #include "device_common.cuh"
 #include "fp8_common.cuh"
+#include "fp8_vec.cuh"
+
+#include <string.h>
 
 namespace moe {
 namespace fp8 {
@@ -16,6 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRegCols = 8192;  // 512 threads, two pieces each
 
 template <bool kBf16>
 __device__ __forceinline__ float ld(const void* p, int64_t i) {
@@ -47,6 +57,270 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   __syncthreads();
   return s;
 }
+
+// ---------------------------------------------------------------- rows in registers
+
+// Columns of piece u of this thread: kVec: column(u) .. column(u) + 7; else 32 apart within each
+// of two blocks of 128.
+template <bool kVec, int W>
+struct Cols {
+  int warp, lane;  // warp within the row's W warps
+  __device__ __forceinline__ int first(int u) const {
+    return kVec ? (u * W * 32 + warp * 32 + lane) * 8 : (u * W + warp) * 256 + lane;
+  }
+  __device__ __forceinline__ int col(int u, int j) const { return first(u) + (kVec ? j : 32 * j); }
+};
+
+// Eight values of a row as they lie in memory.
+template <bool kBf16, bool kVec>
+struct Piece {
+  uint32_t w[kBf16 && kVec ? 4 : 8];
+  template <int W>
+  __device__ __forceinline__ void load(const void* row, const Cols<kVec, W>& cs, int u, int d) {
+    if constexpr (kVec) {
+      const int c = cs.first(u);
+      Raw8<kBf16> r;
+      if (c < d) r.load(row, c);
+      else r.zero();
+      memcpy(w, r.w, sizeof w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = cs.col(u, j);
+        w[j] = c >= d ? 0u : kBf16 ? (uint32_t)reinterpret_cast<const uint16_t*>(row)[c] << 16
+                                   : reinterpret_cast<const uint32_t*>(row)[c];
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (kBf16 && kVec) return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    return __uint_as_float(w[j]);
+  }
+};
+
+template <bool kBf16, bool kVec, int W>
+__device__ __forceinline__ void store8(void* row, const Cols<kVec, W>& cs, int u, int d, const float (&v)[8]) {
+  if constexpr (kVec) {
+    const int c = cs.first(u);
+    if (c >= d) return;
+    if constexpr (kBf16) {
+      *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(row) + c) = pack_bf16x8(v);
+    } else {
+      float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(row) + c);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (cs.col(u, j) < d) st<kBf16>(row, cs.col(u, j), v[j]);
+  }
+}
+
+template <bool kVec, int W>
+__device__ __forceinline__ void load_weight(const float* weight, const Cols<kVec, W>& cs, int u, int d, float (&v)[8]) {
+  if (!weight) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 1.f;
+  } else {
+    Piece<false, kVec> p;
+    p.load(weight, cs, u, d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p.get(j);
+  }
+}
+
+// Sum over the row's W warps, the same bits in every thread.  `red` [2][W]: calls take turns
+// (`turn`), so one barrier a call is enough.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* red, int turn, int warp, int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (W > 1) {
+    red += turn * W;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v += red[w];
+  }
+  return v;
+}
+
+// R rows a CTA (R > 1 only with one warp a row).
+template <bool kBf16, bool kVec, int V, int W, int R>
+__global__ void __launch_bounds__(32 * W * R)
+    rmsnorm_reg_kernel(const void* x, const void* residual, const float* weight, int64_t rows, int d, int64_t ldx,
+                       int64_t ldr, float eps, void* residual_out, void* out, uint8_t* q, uint8_t* scales, float* rstd) {
+  __shared__ float red[2 * W];
+  constexpr int kEsz = kBf16 ? 2 : 4;
+  const int lane = threadIdx.x & 31;
+  const Cols<kVec, W> cs{(int)(threadIdx.x >> 5) % W, lane};
+  const int64_t sc = scale_cols(d), step = (int64_t)gridDim.x * R;
+  const int nb = (d + kBlock - 1) / kBlock;
+  float wt[V][8];
+#pragma unroll
+  for (int u = 0; u < V; ++u) load_weight(weight, cs, u, d, wt[u]);
+  Piece<kBf16, kVec> px[V], pr[V];
+  auto fetch = [&](int64_t t) {
+    const char* xr = reinterpret_cast<const char*>(x) + t * ldx * kEsz;
+    const char* rr = reinterpret_cast<const char*>(residual) + t * ldr * kEsz;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      px[u].load(xr, cs, u, d);
+      if (residual) pr[u].load(rr, cs, u, d);
+    }
+  };
+  int64_t t = (int64_t)blockIdx.x * R + (R > 1 ? threadIdx.x >> 5 : 0);
+  if (t < rows) fetch(t);
+  for (int turn = 0; t < rows; t += step, turn ^= 1) {
+    float v[V][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[u][j] = px[u].get(j);
+        if (residual) v[u][j] = rounded<kBf16>(v[u][j] + pr[u].get(j));
+        ss += v[u][j] * v[u][j];  // zero past the row's end
+      }
+    }
+    if (t + step < rows) fetch(t + step);
+    if (residual_out) {
+      char* ro = reinterpret_cast<char*>(residual_out) + t * d * kEsz;
+#pragma unroll
+      for (int u = 0; u < V; ++u) store8<kBf16>(ro, cs, u, d, v[u]);
+    }
+    const float inv = 1.f / sqrtf(row_sum<W>(ss, red, turn, cs.warp, lane) / (float)d + eps);
+    if (rstd && cs.warp == 0 && lane == 0) rstd[t] = inv;
+    if (!out && !q) continue;
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = v[u][j] * inv * wt[u][j];
+    if (out) {
+      char* o = reinterpret_cast<char*>(out) + t * d * kEsz;
+#pragma unroll
+      for (int u = 0; u < V; ++u) store8<kBf16>(o, cs, u, d, v[u]);
+    }
+    if (!q) continue;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      if constexpr (kVec) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, abs_bits(cs.first(u) < d ? v[u][j] : 0.f));
+        const uint32_t b = scale_byte(__uint_as_float(half_warp_max(top)));
+        const float f = inv_scale_value(b);
+        const int c = cs.first(u);
+        if (c < d) {
+          *reinterpret_cast<uint2*>(q + t * d + c) = make_uint2(pack_e4m3x4(v[u][0] * f, v[u][1] * f, v[u][2] * f, v[u][3] * f),
+                                                                pack_e4m3x4(v[u][4] * f, v[u][5] * f, v[u][6] * f, v[u][7] * f));
+          if ((lane & 15) == 0) scales[t * sc + c / kBlock] = (uint8_t)b;
+        }
+      } else {
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb) {  // the piece's two blocks
+          uint32_t top = 0;
+#pragma unroll
+          for (int j = 4 * hb; j < 4 * hb + 4; ++j) top = max(top, abs_bits(cs.col(u, j) < d ? v[u][j] : 0.f));
+          const uint32_t b = scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
+          const float f = inv_scale_value(b);
+#pragma unroll
+          for (int j = 4 * hb; j < 4 * hb + 4; ++j)
+            if (cs.col(u, j) < d) q[t * d + cs.col(u, j)] = (uint8_t)pack_e4m3x2(v[u][j] * f, 0.f);
+          const int blk = (u * W + cs.warp) * 2 + hb;
+          if (lane == 0 && blk < nb) scales[t * sc + blk] = (uint8_t)b;
+        }
+      }
+    }
+    if (cs.warp == 0 && lane < sc - nb) scales[t * sc + nb + lane] = 0;  // the row's padding bytes
+  }
+}
+
+// The CTA's sum of dweight stays in registers over its rows and leaves as one row of `parts`.
+template <bool kBf16, bool kDoutBf16, bool kVec, int V, int W, int R>
+__global__ void __launch_bounds__(32 * W * R)
+    rmsnorm_backward_reg_kernel(const void* dout, const void* r, const float* weight, const float* rstd,
+                                const void* dresidual, int64_t rows, int d, int64_t ldr, void* dx, float* parts) {
+  __shared__ float red[2 * W];
+  constexpr int kEsz = kBf16 ? 2 : 4, kDsz = kDoutBf16 ? 2 : 4;
+  const int lane = threadIdx.x & 31;
+  const Cols<kVec, W> cs{(int)(threadIdx.x >> 5) % W, lane};
+  const int64_t step = (int64_t)gridDim.x * R;
+  float wt[V][8], dw[V][8];
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    load_weight(weight, cs, u, d, wt[u]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[u][j] = 0.f;
+  }
+  Piece<kDoutBf16, kVec> pd[V];
+  Piece<kBf16, kVec> pr[V], ps[V];
+  float inv = 0.f;
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      pd[u].load(reinterpret_cast<const char*>(dout) + t * d * kDsz, cs, u, d);
+      pr[u].load(reinterpret_cast<const char*>(r) + t * ldr * kEsz, cs, u, d);
+      if (dresidual) ps[u].load(reinterpret_cast<const char*>(dresidual) + t * d * kEsz, cs, u, d);
+    }
+    inv = rstd[t];
+  };
+  int64_t t = (int64_t)blockIdx.x * R + (R > 1 ? threadIdx.x >> 5 : 0);
+  if (t < rows) fetch(t);
+  for (int turn = 0; t < rows; t += step, turn ^= 1) {
+    float g[V][8], xh[V][8], s[V][8];
+    const float iv = inv;
+    float dot = 0.f;
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float dn = pd[u].get(j);
+        xh[u][j] = pr[u].get(j) * iv;
+        s[u][j] = dresidual ? ps[u].get(j) : 0.f;
+        g[u][j] = dn * wt[u][j];
+        dw[u][j] += dn * xh[u][j];
+        dot += g[u][j] * xh[u][j];
+      }
+    if (t + step < rows) fetch(t + step);
+    const float m = row_sum<W>(dot, red, turn, cs.warp, lane) / (float)d;
+    char* o = reinterpret_cast<char*>(dx) + t * d * kEsz;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = iv * (g[u][j] - xh[u][j] * m) + s[u][j];
+      store8<kBf16>(o, cs, u, d, v);
+    }
+  }
+  if (!parts) return;
+  if constexpr (R > 1) {  // the CTA's R rows (one warp each, V = 1) in order
+    __shared__ float all[R][256];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = cs.col(0, j);
+      if (c < 256) all[threadIdx.x >> 5][c] = dw[0][j];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += 32 * W * R) {
+      float a = 0.f;
+#pragma unroll
+      for (int w = 0; w < R; ++w) a += all[w][c];
+      parts[(int64_t)blockIdx.x * d + c] = a;
+    }
+  } else {
+    float* o = parts + (int64_t)blockIdx.x * d;
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (cs.col(u, j) < d) o[cs.col(u, j)] = dw[u][j];
+  }
+}
+
+// ---------------------------------------------------------------- rows too long for registers
 
 // One CTA per row, the row in shared memory between the sum and the scaling; any d, pitch and
 // alignment.
@@ -126,20 +400,79 @@ __global__ void __launch_bounds__(kThreads)
     for (int c = threadIdx.x; c < d; c += kThreads) parts[(int64_t)blockIdx.x * d + c] = dw_s[c];
 }
 
+// dweight[c] = the n partial sums of column c: 32 columns a CTA, each warp an eighth of the parts
+// in order, then the eight in order.
 __global__ void __launch_bounds__(kThreads) dweight_sum_kernel(const float* parts, int n, int d, float* dweight) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
+  __shared__ float all[kWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   pdl_wait();
-  if (c >= d) return;
   float s = 0.f;
-  for (int p = 0; p < n; ++p) s += parts[(int64_t)p * d + c];
-  dweight[c] = s;
+  if (c < d) {
+    const int end = (int)((int64_t)n * (warp + 1) / kWarps);
+#pragma unroll 8
+    for (int p = (int)((int64_t)n * warp / kWarps); p < end; ++p) s += parts[(int64_t)p * d + c];
+  }
+  all[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < d) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += all[w][lane];
+    dweight[c] = s;
+  }
 }
 
 }  // namespace
 
+// Persistent CTAs: what 152 SMs hold of CTAs of this many threads (at about 64 registers a thread).
+static int resident(int threads) { return 152 * (1024 / threads); }
+
+struct NormArgs {
+  const void *x, *residual;
+  const float* weight;
+  int64_t rows;
+  int d;
+  int64_t ldx, ldr;
+  float eps;
+  void *residual_out, *out;
+  uint8_t *q, *scales;
+  float* rstd;
+};
+
+template <bool kBf16, bool kVec, int V, int W, int R>
+static cudaError_t norm_reg(const NormArgs& a, cudaStream_t st) {
+  const int64_t want = (a.rows + R - 1) / R;
+  const int64_t grid = want < resident(32 * W * R) ? want : resident(32 * W * R);
+  return launch_kernel(rmsnorm_reg_kernel<kBf16, kVec, V, W, R>, dim3((unsigned)grid), dim3(32 * W * R), 0, st, false, 1, a.x,
+                       a.residual, a.weight, a.rows, a.d, a.ldx, a.ldr, a.eps, a.residual_out, a.out, a.q, a.scales, a.rstd);
+}
+
+// The fewest threads that hold the row at eight values a thread (two pieces above 4096 columns);
+// rows of up to 256 take a warp each.
+template <bool kBf16, bool kVec>
+static cudaError_t norm_width(const NormArgs& a, cudaStream_t st) {
+  if (a.d <= 256) return norm_reg<kBf16, kVec, 1, 1, 8>(a, st);
+  if (a.d <= 1024) return norm_reg<kBf16, kVec, 1, 4, 1>(a, st);
+  if (a.d <= 2048) return norm_reg<kBf16, kVec, 1, 8, 1>(a, st);
+  if (a.d <= 4096) return norm_reg<kBf16, kVec, 1, 16, 1>(a, st);
+  return norm_reg<kBf16, kVec, 2, 16, 1>(a, st);
+}
+
+// Rows on whole 16-byte vectors.
+static bool vectors(const void* p, bool bf16, int64_t ld) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (bf16 ? 8 : 4) == 0);
+}
+
 cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* weight, bool bf16, int64_t rows, int d,
                            int64_t ldx, int64_t ldr, float eps, void* residual_out, void* out, void* q, uint8_t* scales,
                            float* rstd, cudaStream_t st) {
+  if (d <= kMaxRegCols) {
+    const NormArgs a{x, residual, weight, rows, d, ldx, ldr, eps, residual_out, out, (uint8_t*)q, scales, rstd};
+    const bool vec = d % 8 == 0 && vectors(x, bf16, ldx) && vectors(residual, bf16, ldr) && vectors(residual_out, bf16, d) &&
+                     vectors(out, bf16, d);
+    return bf16 ? (vec ? norm_width<true, true>(a, st) : norm_width<true, false>(a, st))
+                : (vec ? norm_width<false, true>(a, st) : norm_width<false, false>(a, st));
+  }
   const size_t smem = (size_t)d * sizeof(float);
   auto kern = bf16 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>;
   cudaError_t e = cudaSuccess;
@@ -151,26 +484,71 @@ cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* wei
                        ldr, eps, residual_out, out, (uint8_t*)q, scales, rstd);
 }
 
-int rmsnorm_backward_parts(int64_t rows) { return (int)(rows < 304 ? rows : 304); }
+// Rows a CTA sums dweight over before it writes a partial: enough CTAs to fill the GPU, but
+// partials of a few rows each at least, which are written and read again.  The count depends on
+// the shape alone, and so does the order of the sum.
+int rmsnorm_backward_parts(int64_t rows, int d) {
+  const int per_cta = d <= 256 ? 8 : 1;
+  const int64_t most = resident(d <= 256 ? 256 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= kMaxRegCols ? 512 : 256);
+  const int64_t want = (rows + 2 * per_cta - 1) / (2 * per_cta);
+  return (int)(want < most ? want : most);
+}
+
+struct NormBwdArgs {
+  const void *dout, *r;
+  const float *weight, *rstd;
+  const void* dresidual;
+  int64_t rows;
+  int d;
+  int64_t ldr;
+  void* dx;
+  float* parts;
+};
+
+template <bool kBf16, bool kDoutBf16, bool kVec, int V, int W, int R>
+static cudaError_t norm_bwd_reg(const NormBwdArgs& a, cudaStream_t st) {
+  return launch_kernel(rmsnorm_backward_reg_kernel<kBf16, kDoutBf16, kVec, V, W, R>,
+                       dim3((unsigned)rmsnorm_backward_parts(a.rows, a.d)), dim3(32 * W * R), 0, st, false, 1, a.dout, a.r,
+                       a.weight, a.rstd, a.dresidual, a.rows, a.d, a.ldr, a.dx, a.parts);
+}
+
+template <bool kBf16, bool kDoutBf16, bool kVec>
+static cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t st) {
+  if (a.d <= 256) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 1, 8>(a, st);
+  if (a.d <= 1024) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 4, 1>(a, st);
+  if (a.d <= 2048) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 8, 1>(a, st);
+  if (a.d <= 4096) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 16, 1>(a, st);
+  return norm_bwd_reg<kBf16, kDoutBf16, kVec, 2, 16, 1>(a, st);
+}
+
+template <bool kVec>
+static cudaError_t norm_bwd_types(const NormBwdArgs& a, bool bf16, bool dout_bf16, cudaStream_t st) {
+  return bf16 ? (dout_bf16 ? norm_bwd_width<true, true, kVec>(a, st) : norm_bwd_width<true, false, kVec>(a, st))
+              : (dout_bf16 ? norm_bwd_width<false, true, kVec>(a, st) : norm_bwd_width<false, false, kVec>(a, st));
+}
 
 cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void* r, const float* weight,
                                     const float* rstd, const void* dresidual, bool bf16, int64_t rows, int d,
                                     int64_t ldr, void* dx, float* dweight, float* parts, cudaStream_t st) {
-  const int n = rmsnorm_backward_parts(rows);
-  const size_t smem = (size_t)d * sizeof(float);
-  auto kern = bf16 ? (dout_bf16 ? rmsnorm_backward_kernel<true, true> : rmsnorm_backward_kernel<true, false>)
-                   : (dout_bf16 ? rmsnorm_backward_kernel<false, true> : rmsnorm_backward_kernel<false, false>);
+  const int n = rmsnorm_backward_parts(rows, d);
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024 &&  // what a launch may have without asking
-      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-    return e;
-  if (n > 0) {
-    e = launch_kernel(kern, dim3((unsigned)n), dim3(kThreads), smem, st, false, 1, dout, r, weight, rstd, dresidual, rows,
-                      d, ldr, dx, dweight ? parts : nullptr);
-    if (e != cudaSuccess) return e;
+  if (n > 0 && d <= kMaxRegCols) {
+    const NormBwdArgs a{dout, r, weight, rstd, dresidual, rows, d, ldr, dx, dweight ? parts : nullptr};
+    const bool vec = d % 8 == 0 && vectors(dout, dout_bf16, d) && vectors(r, bf16, ldr) && vectors(dresidual, bf16, d) &&
+                     vectors(dx, bf16, d);
+    e = vec ? norm_bwd_types<true>(a, bf16, dout_bf16, st) : norm_bwd_types<false>(a, bf16, dout_bf16, st);
+  } else if (n > 0) {
+    const size_t smem = (size_t)d * sizeof(float);
+    auto kern = bf16 ? (dout_bf16 ? rmsnorm_backward_kernel<true, true> : rmsnorm_backward_kernel<true, false>)
+                     : (dout_bf16 ? rmsnorm_backward_kernel<false, true> : rmsnorm_backward_kernel<false, false>);
+    if (smem > 48 * 1024 &&  // what a launch may have without asking
+        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+      return e;
+    e = launch_kernel(kern, dim3((unsigned)n), dim3(kThreads), smem, st, false, 1, dout, r, weight, rstd, dresidual, rows, d,
+                      ldr, dx, dweight ? parts : nullptr);
   }
-  if (!dweight) return cudaSuccess;
-  return launch_kernel(dweight_sum_kernel, dim3((unsigned)((d + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, n > 0, 1,
+  if (e != cudaSuccess || !dweight) return e;
+  return launch_kernel(dweight_sum_kernel, dim3((unsigned)((d + 31) / 32)), dim3(kThreads), 0, st, n > 0, 1,
                        (const float*)parts, n, d, dweight);
 }
 

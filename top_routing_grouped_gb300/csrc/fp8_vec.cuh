@@ -22,6 +22,21 @@ struct Raw8 {
     w[0] = make_uint4(0, 0, 0, 0);
     if constexpr (!kBf16) w[1] = w[0];
   }
+  // the largest |value|, as fp32 bits (NaN above infinity above every number): bf16 two at a time
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if constexpr (kBf16) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = __vmaxu2(m, u[j] & 0x7fff7fffu);
+      return max(m & 0xffff0000u, m << 16);
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, u[j] & 0x7fffffffu);
+      return m;
+    }
+  }
   __device__ __forceinline__ Eight get() const {
     Eight r;
     const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
@@ -32,9 +47,11 @@ struct Raw8 {
   }
 };
 
+// Largest |.| over the half-warp (each half on its own: the halves may have diverged).
 __device__ __forceinline__ uint32_t half_warp_max(uint32_t v) {
+  const uint32_t mask = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 8; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(mask, v, o));
   return v;
 }
 

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(32 * W * R)
 
 // The CTA's sum of dweight stays in registers over its rows and leaves as one row of `parts`.
 template <bool kBf16, bool kDoutBf16, bool kVec, int V, int W, int R>
-__global__ void __launch_bounds__(32 * W * R)
+__global__ void __launch_bounds__(32 * W * R, kBf16 && kVec && V == 1 ? 1024 / (32 * W * R) : 1)
     rmsnorm_backward_reg_kernel(const void* dout, const void* r, const float* weight, const float* rstd,
                                 const void* dresidual, int64_t rows, int d, int64_t ldr, void* dx, float* parts) {
   __shared__ float red[2 * W];
@@ -270,20 +270,24 @@ __global__ void __launch_bounds__(32 * W * R)
   int64_t t = (int64_t)blockIdx.x * R + (R > 1 ? threadIdx.x >> 5 : 0);
   if (t < rows) fetch(t);
   for (int turn = 0; t < rows; t += step, turn ^= 1) {
-    float g[V][8], xh[V][8], s[V][8];
+    // the row stays packed as it was loaded: unpacked twice it costs fewer registers than kept as
+    // fp32, and two CTAs of 512 threads fit an SM
+    Piece<kDoutBf16, kVec> cd[V];
+    Piece<kBf16, kVec> cr[V], cres[V];
     const float iv = inv;
     float dot = 0.f;
 #pragma unroll
-    for (int u = 0; u < V; ++u)
+    for (int u = 0; u < V; ++u) {
+      cd[u] = pd[u];
+      cr[u] = pr[u];
+      cres[u] = ps[u];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float dn = pd[u].get(j);
-        xh[u][j] = pr[u].get(j) * iv;
-        s[u][j] = dresidual ? ps[u].get(j) : 0.f;
-        g[u][j] = dn * wt[u][j];
-        dw[u][j] += dn * xh[u][j];
-        dot += g[u][j] * xh[u][j];
+        const float dx_hat = cd[u].get(j) * (cr[u].get(j) * iv);
+        dw[u][j] += dx_hat;
+        dot += dx_hat * wt[u][j];
       }
+    }
     if (t + step < rows) fetch(t + step);
     const float m = row_sum<W>(dot, red, turn, cs.warp, lane) / (float)d;
     char* o = reinterpret_cast<char*>(dx) + t * d * kEsz;
@@ -291,7 +295,10 @@ __global__ void __launch_bounds__(32 * W * R)
     for (int u = 0; u < V; ++u) {
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = iv * (g[u][j] - xh[u][j] * m) + s[u][j];
+      for (int j = 0; j < 8; ++j) {
+        v[j] = iv * (cd[u].get(j) * wt[u][j] - cr[u].get(j) * iv * m);
+        if (dresidual) v[j] += cres[u].get(j);
+      }
       store8<kBf16>(o, cs, u, d, v);
     }
   }

@@ -74,20 +74,24 @@ __global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const void* x
 
 // ---- eight columns a thread -------------------------------------------------------------------
 // With rows of whole 16-byte vectors a thread takes 8 consecutive columns and a half-warp a block
-// of 128: loads of 16 bytes a lane, and the block's maximum in four shuffles.  A thread requests
-// its kUnroll blocks before it uses the first, which keeps enough bytes in flight for HBM
-// (blocks are dealt to half-warps in order, so a warp's loads stay contiguous).
-constexpr int kUnroll = 4;
+// of 128: loads of 16 bytes a lane, and the block's maximum in four shuffles.  A thread keeps its
+// columns and goes down the rows, so that its addresses advance by constants: with an index
+// divided into row and block at every step these kernels were bound by integer instructions, not
+// by HBM.  The next row's loads are issued before the present row is worked on.
+#ifndef QR
+#define QR 6
+#endif
+constexpr int kResident = 152 * QR;  // CTAs
 
-// Block `i` of a tensor of nb blocks a row.
-struct BlockAt {
-  int64_t row;
+// The threads of a pass over `per_pass` rows, 16 * nb to a row (nb blocks).
+struct Lanes {
+  int64_t row;  // this thread's first row; at or past the end: none
+  int col;      // its first column (the last block may end before it)
   int blk;
 };
-__device__ __forceinline__ BlockAt block_at(int64_t i, uint32_t nb) {
-  // a 32-bit division where the index allows it
-  if (i >> 32 == 0) return {(int64_t)((uint32_t)i / nb), (int)((uint32_t)i % nb)};
-  return {i / nb, (int)(i % nb)};
+__device__ __forceinline__ Lanes lanes(int64_t rows, int per_pass, int nb) {
+  const uint32_t s = blockIdx.x * kThreads + threadIdx.x, w = (uint32_t)nb * 16, r = s / w, c = s % w;
+  return {(int)r < per_pass ? (int64_t)r : rows, (int)(c * 8), (int)(c / 16)};
 }
 
 // blockIdx.y picks one of two tensors of the same shape (the checkpoint's a and b).
@@ -98,47 +102,36 @@ struct QuantizeJob {
 };
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) quantize_rows_vec_kernel(QuantizeJob job, int64_t rows, int cols, int64_t ldx) {
+__global__ void __launch_bounds__(kThreads) quantize_rows_vec_kernel(QuantizeJob job, int64_t rows, int cols, int64_t ldx,
+                                                                     int per_pass) {
   const bool second = blockIdx.y != 0;
-  const void* x = second ? job.x[1] : job.x[0];
-  uint8_t* q = second ? job.q[1] : job.q[0];
-  uint8_t* scales = second ? job.scales[1] : job.scales[0];
+  const int nb = (cols + kBlock - 1) / kBlock, sc = (int)scale_cols(cols);
+  const Lanes at = lanes(rows, per_pass, nb);
+  const bool in = at.col < cols;
   const int l16 = threadIdx.x & 15;
-  const uint32_t nb = (uint32_t)((cols + kBlock - 1) / kBlock);
-  const int64_t sc = scale_cols(cols), n = rows * nb;
-  // a CTA's share: kUnroll runs of kThreads / 16 consecutive blocks
-  for (int64_t base = (int64_t)blockIdx.x * kUnroll * (kThreads / 16) + threadIdx.x / 16; base < (n + 1) / 2 * 2;  // the same for both halves of a warp
-       base += (int64_t)gridDim.x * kUnroll * (kThreads / 16)) {
-    Raw8<kBf16> raw[kUnroll];
-    BlockAt at[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = base + u * (kThreads / 16);
-      at[u] = block_at(i, nb);
-      const int c = at[u].blk * kBlock + l16 * 8;
-      if (i < n && c < cols) raw[u].load(x, at[u].row * ldx + c);
-      else raw[u].zero();
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t i = base + u * (kThreads / 16);
-      const int c = at[u].blk * kBlock + l16 * 8;
-      const Eight e = raw[u].get();
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, abs_bits(e.v[j]));
-      const uint32_t b = scale_byte(__uint_as_float(half_warp_max(top)));
-      const float f = inv_scale_value(b);
-      if (i < n) {
-        if (c < cols)
-          *reinterpret_cast<uint2*>(q + at[u].row * cols + c) =
-              make_uint2(pack_e4m3x4(e.v[0] * f, e.v[1] * f, e.v[2] * f, e.v[3] * f),
-                         pack_e4m3x4(e.v[4] * f, e.v[5] * f, e.v[6] * f, e.v[7] * f));
-        if (l16 == 0) scales[at[u].row * sc + at[u].blk] = (uint8_t)b;
-        // the row's padding bytes, by the other lanes of its last block
-        if (at[u].blk == (int)nb - 1 && l16 > 0 && nb - 1 + l16 < sc) scales[at[u].row * sc + nb - 1 + l16] = 0;
-      }
-    }
+  const char* x = reinterpret_cast<const char*>(second ? job.x[1] : job.x[0]) + (at.row * ldx + at.col) * (kBf16 ? 2 : 4);
+  uint8_t* q = (second ? job.q[1] : job.q[0]) + at.row * cols + at.col;
+  uint8_t* s = (second ? job.scales[1] : job.scales[0]) + at.row * sc + at.blk;
+  const int64_t dx = per_pass * ldx * (kBf16 ? 2 : 4), dq = (int64_t)per_pass * cols, ds = (int64_t)per_pass * sc;
+  // the row's padding bytes are written by the other lanes of its last block
+  const bool pad = at.blk == nb - 1 && l16 > 0 && nb - 1 + l16 < sc;
+  Raw8<kBf16> raw;
+  raw.zero();
+  if (in && at.row < rows) raw.load(x, 0);
+  for (int64_t row = at.row; row < rows; row += per_pass) {
+    const Raw8<kBf16> now = raw;
+    x += dx;
+    if (in && row + per_pass < rows) raw.load(x, 0);
+    const uint32_t b = scale_byte(__uint_as_float(half_warp_max(now.top())));
+    const float f = inv_scale_value(b);
+    const Eight e = now.get();
+    if (in)
+      *reinterpret_cast<uint2*>(q) = make_uint2(pack_e4m3x4(e.v[0] * f, e.v[1] * f, e.v[2] * f, e.v[3] * f),
+                                                pack_e4m3x4(e.v[4] * f, e.v[5] * f, e.v[6] * f, e.v[7] * f));
+    if (l16 == 0) *s = (uint8_t)b;
+    if (pad) s[l16] = 0;
+    q += dq;
+    s += ds;
   }
 }
 
@@ -150,53 +143,46 @@ __device__ __forceinline__ void swiglu_backward(float a, float b, float g, float
   h = u * b;
 }
 
-constexpr int kBwdUnroll = 2;
+constexpr int kBwdResident = 152 * 5;  // CTAs (48 registers); 20011 x 1072: 35.5 us, with 4 a SM 36.4, with 6 (two waves) 43
 
 __global__ void __launch_bounds__(kThreads)
     checkpoint_backward_vec_kernel(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
                                    const __nv_bfloat16* dh, int64_t rows, int F, __nv_bfloat16* da, __nv_bfloat16* db,
-                                   __nv_bfloat16* h) {
-  const int l16 = threadIdx.x & 15;
-  const uint32_t nb = (uint32_t)((F + kBlock - 1) / kBlock);
-  const int64_t sc = scale_cols(F), n = rows * nb;
-  for (int64_t base = (int64_t)blockIdx.x * kBwdUnroll * (kThreads / 16) + threadIdx.x / 16; base < n;
-       base += (int64_t)gridDim.x * kBwdUnroll * (kThreads / 16)) {
-    uint2 va[kBwdUnroll], vb[kBwdUnroll];
-    Raw8<true> g[kBwdUnroll];
-    float fa[kBwdUnroll], fb[kBwdUnroll];
-    int64_t o[kBwdUnroll];
-    bool in[kBwdUnroll];
+                                   __nv_bfloat16* h, int per_pass) {
+  const int nb = (F + kBlock - 1) / kBlock, sc = (int)scale_cols(F);
+  const Lanes at = lanes(rows, per_pass, nb);
+  if (at.col >= F) return;
+  int64_t o = at.row * F + at.col, os = at.row * sc + at.blk;
+  const int64_t step = (int64_t)per_pass * F, sstep = (int64_t)per_pass * sc;
+  uint2 va, vb;
+  Raw8<true> g;
+  uint32_t fa, fb;
+  auto fetch = [&](int64_t i, int64_t is) {
+    va = __ldcs(reinterpret_cast<const uint2*>(qa + i));
+    vb = __ldcs(reinterpret_cast<const uint2*>(qb + i));
+    g.load(dh, i);
+    fa = __ldg(sa + is);
+    fb = __ldg(sb + is);
+  };
+  if (at.row < rows) fetch(o, os);
+  for (int64_t row = at.row; row < rows; row += per_pass) {
+    const uint2 ca = va, cb = vb;
+    const Eight e = g.get();
+    const float sca = scale_value(fa), scb = scale_value(fb);
+    os += sstep;
+    if (row + per_pass < rows) fetch(o + step, os);
+    float oa[8], ob[8], oh[8];
 #pragma unroll
-    for (int u = 0; u < kBwdUnroll; ++u) {
-      const int64_t i = base + u * (kThreads / 16);
-      const BlockAt at = block_at(i, nb);
-      const int c = at.blk * kBlock + l16 * 8;
-      in[u] = i < n && c < F;
-      o[u] = at.row * F + c;
-      if (in[u]) {
-        va[u] = __ldcs(reinterpret_cast<const uint2*>(qa + o[u]));
-        vb[u] = __ldcs(reinterpret_cast<const uint2*>(qb + o[u]));
-        g[u].load(dh, o[u]);
-        fa[u] = scale_value(__ldg(sa + at.row * sc + at.blk));
-        fb[u] = scale_value(__ldg(sb + at.row * sc + at.blk));
-      }
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t wa = (j & 2 ? ca.y : ca.x) >> (16 * (j & 1)), wb = (j & 2 ? cb.y : cb.x) >> (16 * (j & 1));
+      const float2 a = unpack_e4m3x2(wa), b = unpack_e4m3x2(wb);
+      swiglu_backward(a.x * sca, b.x * scb, e.v[2 * j], oa[2 * j], ob[2 * j], oh[2 * j]);
+      swiglu_backward(a.y * sca, b.y * scb, e.v[2 * j + 1], oa[2 * j + 1], ob[2 * j + 1], oh[2 * j + 1]);
     }
-#pragma unroll
-    for (int u = 0; u < kBwdUnroll; ++u) {
-      if (!in[u]) continue;
-      const Eight e = g[u].get();
-      float oa[8], ob[8], oh[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t wa = (j & 2 ? va[u].y : va[u].x) >> (16 * (j & 1)), wb = (j & 2 ? vb[u].y : vb[u].x) >> (16 * (j & 1));
-        const float2 a = unpack_e4m3x2(wa), b = unpack_e4m3x2(wb);
-        swiglu_backward(a.x * fa[u], b.x * fb[u], e.v[2 * j], oa[2 * j], ob[2 * j], oh[2 * j]);
-        swiglu_backward(a.y * fa[u], b.y * fb[u], e.v[2 * j + 1], oa[2 * j + 1], ob[2 * j + 1], oh[2 * j + 1]);
-      }
-      *reinterpret_cast<uint4*>(da + o[u]) = pack_bf16x8(oa);
-      *reinterpret_cast<uint4*>(db + o[u]) = pack_bf16x8(ob);
-      if (h) *reinterpret_cast<uint4*>(h + o[u]) = pack_bf16x8(oh);
-    }
+    *reinterpret_cast<uint4*>(da + o) = pack_bf16x8(oa);
+    *reinterpret_cast<uint4*>(db + o) = pack_bf16x8(ob);
+    if (h) *reinterpret_cast<uint4*>(h + o) = pack_bf16x8(oh);
+    o += step;
   }
 }
 
@@ -237,11 +223,23 @@ static bool vectors(const void* x, bool bf16, int64_t cols, int64_t ldx) {
   return cols % 8 == 0 && ldx % (bf16 ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 && cols <= INT32_MAX - 512;
 }
 
+// CTAs of at most `resident`, and the rows that their threads cover at a time.
+struct Pass {
+  unsigned ctas;
+  int per_pass;
+};
+static Pass pass_of(int64_t rows, int64_t cols, int resident) {
+  const int64_t w = (cols + kBlock - 1) / kBlock * 16, want = (rows * w + kThreads - 1) / kThreads;
+  int64_t ctas = want < resident ? want : resident;
+  if (ctas * kThreads < w) ctas = (w + kThreads - 1) / kThreads;  // a row longer than that
+  return {(unsigned)ctas, (int)(ctas * kThreads / w)};
+}
+
 static cudaError_t quantize_vec(const QuantizeJob& job, int jobs, bool bf16, int64_t rows, int64_t cols, int64_t ldx,
                                 cudaStream_t st) {
-  const dim3 grid(grid_for(rows * ((cols + kBlock - 1) / kBlock), kUnroll * (kThreads / 16)), (unsigned)jobs);
-  return launch_kernel(bf16 ? quantize_rows_vec_kernel<true> : quantize_rows_vec_kernel<false>, grid, dim3(kThreads), 0, st,
-                       false, 1, job, rows, (int)cols, ldx);
+  const Pass p = pass_of(rows, cols, kResident / jobs);
+  return launch_kernel(bf16 ? quantize_rows_vec_kernel<true> : quantize_rows_vec_kernel<false>, dim3(p.ctas, (unsigned)jobs),
+                       dim3(kThreads), 0, st, false, 1, job, rows, (int)cols, ldx, p.per_pass);
 }
 
 cudaError_t launch_quantize_rows(const void* x, bool bf16, int64_t rows, int64_t cols, int64_t ldx, void* q,
@@ -270,11 +268,12 @@ cudaError_t launch_checkpoint_save(const void* a, const void* b, int64_t rows, i
 cudaError_t launch_checkpoint_backward(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb,
                                        const void* dh, int64_t rows, int F, void* da, void* db, void* h,
                                        cudaStream_t st) {
-  if (F % 8 == 0)
-    return launch_kernel(checkpoint_backward_vec_kernel,
-                         dim3(grid_for(rows * ((F + kBlock - 1) / kBlock), kBwdUnroll * (kThreads / 16))), dim3(kThreads), 0,
-                         st, false, 1, (const uint8_t*)qa, sa, (const uint8_t*)qb, sb, (const __nv_bfloat16*)dh, rows, F,
-                         (__nv_bfloat16*)da, (__nv_bfloat16*)db, (__nv_bfloat16*)h);
+  if (F % 8 == 0) {
+    const Pass p = pass_of(rows, F, kBwdResident);
+    return launch_kernel(checkpoint_backward_vec_kernel, dim3(p.ctas), dim3(kThreads), 0, st, false, 1, (const uint8_t*)qa, sa,
+                         (const uint8_t*)qb, sb, (const __nv_bfloat16*)dh, rows, F, (__nv_bfloat16*)da, (__nv_bfloat16*)db,
+                         (__nv_bfloat16*)h, p.per_pass);
+  }
   return launch_kernel(checkpoint_backward_kernel, dim3(grid_for(rows * ((F + kBlock - 1) / kBlock), kWarps)),
                        dim3(kThreads), 0, st, false, 1, (const uint8_t*)qa, sa, (const uint8_t*)qb, sb,
                        (const __nv_bfloat16*)dh, rows, F, (__nv_bfloat16*)da, (__nv_bfloat16*)db, (__nv_bfloat16*)h);

@@ -323,30 +323,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bar = ptx::mapa(ptx::smem_u32(&ctl->sf_full), 0);
     uint32_t phase = 0;
     bool ok = true;
-    for (int tile = cid; tile < total && ok; tile += ncl) {
+    // The words of the next group are requested before the present group's wait, across tiles too:
+    // a group of MMAs lasts about as long as one trip to L2.
+    int tile = cid, gk = 0;
+    int64_t ra[4], r0 = 0, r1 = 0;
+    auto locate = [&]() {
       const TileInfo ti = decode_pair_tile(ws, n_tiles, tile, (int)rank);
-      int64_t ra[4];  // rows past the buffer belong to no output: any row's words do
 #pragma unroll
-      for (int c = 0; c < 4; ++c) ra[c] = min((int64_t)ti.row0 + 32 * c + lane, g.rows - 1) * sck;
+      for (int c = 0; c < 4; ++c)  // rows past the buffer belong to no output: any row's words do
+        ra[c] = min((int64_t)ti.row0 + 32 * c + lane, g.rows - 1) * sck;
       const int blk = ti.n_idx * (bn / kBlock);
-      const int64_t r0 = ((int64_t)ti.e * nb + blk) * sck;
-      const int64_t r1 = kKind == kSwiGLU ? r0 : ((int64_t)ti.e * nb + min(blk + 1, nb - 1)) * sck;
-      for (int gk = 0; gk < sck; ++gk) {
-        uint32_t a[4];
+      r0 = ((int64_t)ti.e * nb + blk) * sck;
+      r1 = kKind == kSwiGLU ? r0 : ((int64_t)ti.e * nb + min(blk + 1, nb - 1)) * sck;
+    };
+    uint32_t a[4], b0, b1;
+    auto request = [&]() {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) a[c] = __ldg(sa32 + ra[c] + gk);
-        const uint32_t b0 = __ldg(sb32 + r0 + gk), b1 = __ldg(sb3_32 + r1 + gk);
-        ok = ptx::mbar_wait(ptx::smem_u32(&ctl->sf_empty), phase ^ 1u, timeout_ns, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        phase ^= 1u;
-        st_shared_v4(dst, a[0], a[1], a[2], a[3]);
-        st_shared_v4(dst + 512, b0, b0, b0, b0);
-        st_shared_v4(dst + 1024, b1, b1, b1, b1);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(bar);
+      for (int c = 0; c < 4; ++c) a[c] = __ldg(sa32 + ra[c] + gk);
+      b0 = __ldg(sb32 + r0 + gk);
+      b1 = __ldg(sb3_32 + r1 + gk);
+    };
+    if (tile < total) {
+      locate();
+      request();
+    }
+    while (tile < total) {
+      const uint32_t w[6] = {a[0], a[1], a[2], a[3], b0, b1};
+      if (++gk == sck) {
+        gk = 0;
+        tile += ncl;
+        if (tile < total) locate();
       }
+      if (tile < total) request();
+      ok = ptx::mbar_wait(ptx::smem_u32(&ctl->sf_empty), phase ^ 1u, timeout_ns, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      phase ^= 1u;
+      st_shared_v4(dst, w[0], w[1], w[2], w[3]);
+      st_shared_v4(dst + 512, w[4], w[4], w[4], w[4]);
+      st_shared_v4(dst + 1024, w[5], w[5], w[5], w[5]);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(bar);
     }
     if (!ok && lane == 0) {
       record_error(ws, MOE_ERR_TIMEOUT, 0x930u + kKind);

@@ -14,15 +14,15 @@
 //
 // Factors.  A 32-bit word holds a row's bytes of four K blocks, in the order the rows' scale
 // bytes lie in memory; the instruction descriptor picks the byte of the current block, so one
-// load of words serves 512 k's.  Warp 3 of each CTA gathers the words of its 128 rows and of the
-// tile's two blocks of weight rows into shared memory, the MMA thread copies them to TMEM
-// (tcgen05.cp, 32 lanes repeated over the four lane quarters; column c of a group of four belongs
-// to rows 32c..32c+31), ordered before the MMAs that it issues next.  Two sets of columns in TMEM
-// take turns; the shared words have one buffer, which is free again when the copy has run.
+// load of words serves 512 k's.  Four warps of each CTA, one for each TMEM lane quarter, gather the
+// words of the CTA's 128 rows and of the tile's two blocks of weight rows and store them to TMEM (the
+// same words in every quarter; column c of a group of four belongs to rows 32c..32c+31) up to four
+// groups ahead of the MMAs.  Copies from shared memory (tcgen05.cp) instead stood in the MMA pipe's
+// order and left it idle 11-16 % of the time.
 //
-// TMEM.  The two sets take 32 columns, so the two accumulators of 256 columns overlap by 32: the
-// epilogue reads those columns first and hands them over before it goes on, and the next
-// tile's MMAs start then.
+// TMEM.  The sets take 64 columns, so the two accumulators of 256 columns overlap by 64: the
+// epilogue warps that own those columns read them first and hand them over before they go on, and
+// the next tile's MMAs start then.
 //
 // SwiGLU epilogue: the 128 columns of a tile are one block of each hidden row.  Two warps share a
 // row's 128 values (64 each), agree on the largest one through shared memory, and write e4m3 and
@@ -32,6 +32,8 @@
 // meets at cluster barriers before TMEM is released.
 #include <cuda.h>
 #include <cuda_bf16.h>
+
+#include <stddef.h>
 
 #include <atomic>
 
@@ -53,17 +55,22 @@ constexpr int kMmaK = 32;
 constexpr int kABytes = kRowsPerCta * kBK;
 constexpr int kBHalfBytes = (kMmaN / 2) * kBK;
 constexpr int kStageBytes = kABytes + kBHalfBytes;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, one per half of the tile's columns
+constexpr int kSfWarp0 = 12;
+constexpr int kSfWarps = 4;   // one per TMEM lane quarter
+// Registers a thread: the launch gives every thread 128; the TMA / MMA warps and the factor warps
+// hand some to the epilogue (256 * 72 + 256 * 184 <= 512 * 128).
+constexpr int kRegsFew = 72, kRegsEpi = 184;
 
-// TMEM columns: accumulator i at 224 i (256 wide), factor set i at 480 + 16 i (4 of A, 8 of B)
+// TMEM columns: accumulator i at 192 i (256 wide), factor set i at 448 + 16 i (4 of A, 8 of B)
 constexpr int kTmemCols = 512;
-constexpr int kAccStep = 224;
-constexpr int kSfCol = 480;
+constexpr int kAccStep = 192;
+constexpr int kSfCol = 448;
 constexpr int kSfStep = 16;
+constexpr int kSfSets = 4;
 
-constexpr int kSfBytes = 3 * 512;             // A's 128 rows, B's two blocks of 128 rows
 constexpr int kStgBlockBytes = 32 * 128;      // a store block: 32 rows of 128 bytes, swizzled
 constexpr int kStgBytes = kEpiWarps * kStgBlockBytes;
 
@@ -71,16 +78,17 @@ struct Ctl {
   uint64_t full[kStages];   // leader's: both CTAs' bytes of a stage
   uint64_t empty[kStages];  // each CTA: stage free again (leader's multicast commit)
   uint64_t tfull[2];        // each CTA: accumulator ready (leader's multicast commit)
+  uint64_t tempty[2];       // leader's: both CTAs' epilogue warps have read the accumulator
   uint64_t over;            // leader's: the columns the accumulators share have been read
-  uint64_t sf_full;         // leader's: both CTAs' factor words are in shared memory
-  uint64_t sf_empty;        // each CTA: the words have been copied (leader's multicast commit)
+  uint64_t sf_full[kSfSets];   // leader's: both CTAs' factor words of a group are in TMEM
+  uint64_t sf_empty[kSfSets];  // each CTA: the group's MMAs have run (leader's multicast commit)
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t peer_tmem_base;
   int abort;
 };
 
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kStgBytes + kSfBytes + sizeof(Ctl);
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kStgBytes + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
@@ -126,6 +134,16 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, uint32_t byte) {
   return (byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | (byte << 29);
 }
 
+// One more in either factor byte.
+__host__ __device__ constexpr uint32_t idesc_byte() { return (1u << 4) | (1u << 29); }
+
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void mma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
@@ -136,15 +154,22 @@ __device__ __forceinline__ void mma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 }
 
-// 512 bytes (32 rows of 16) of each CTA's shared memory -> 4 columns of its TMEM, repeated in the
-// four lane quarters.
-__device__ __forceinline__ void tmem_cp_factors(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// This lane's words to 12 columns of its warp's TMEM lane quarter.
+__device__ __forceinline__ void tmem_st_factors(uint32_t taddr, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %5, %5, %5};" ::"r"(taddr), "r"(a[0]),
+               "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0)
+               : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr + 8), "r"(b1) : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Descriptor of an unswizzled block of rows of 16 bytes: 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t desc_rows16(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 __device__ __forceinline__ void raise_abort(Ctl* ctl, uint32_t rank) {
@@ -160,8 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stg_base = stages + kStages * kStageBytes;
-  uint8_t* sf_base = stg_base + kStgBytes;
-  Ctl* ctl = reinterpret_cast<Ctl*>(sf_base + kSfBytes);
+  Ctl* ctl = reinterpret_cast<Ctl*>(stg_base + kStgBytes);
   // SwiGLU stages four blocks; the warps' maxima lie behind them: [half][128 rows]
   uint32_t* top_s = reinterpret_cast<uint32_t*>(stg_base + 4 * kStgBlockBytes);
   const int warp = threadIdx.x >> 5;
@@ -182,10 +206,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&ctl->full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&ctl->empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&ctl->tfull[i]), 1);
-    ptx::mbar_init(ptx::smem_u32(&ctl->over), 2 * kEpiWarps);
-    ptx::mbar_init(ptx::smem_u32(&ctl->sf_full), 2);
-    ptx::mbar_init(ptx::smem_u32(&ctl->sf_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&ctl->tfull[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&ctl->tempty[i]), 2 * kEpiWarps);
+    }
+    ptx::mbar_init(ptx::smem_u32(&ctl->over), kEpiWarps);  // half of both CTAs' epilogue warps
+    for (int i = 0; i < kSfSets; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&ctl->sf_full[i]), 2 * kSfWarps);
+      ptx::mbar_init(ptx::smem_u32(&ctl->sf_empty[i]), 1);
+    }
     ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     ctl->peer_tmem_base = 0xFFFFFFFFu;
@@ -217,8 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   volatile int* abort_flag = &ctl->abort;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < kEpiWarp0) {
+    regs_dec<kRegsFew>();
+    if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- TMA producer (both CTAs)
       int stage = 0;
       uint32_t phase = 0;
@@ -251,76 +281,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         record_error(ws, MOE_ERR_TIMEOUT, 0x910u + kKind);
         raise_abort(ctl, rank);
       }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
       // ---------------------------------------------------------- MMA issuer (leader only)
+      // The whole warp runs the loop and one elected lane issues: with every operand the same in
+      // all lanes for the compiler to see, an MMA costs 39 clocks to issue; from a branch of one
+      // lane it cost 93, and issuing, at 680 clocks a stage, was what bound the kernel.
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int first_tile = __shfl_sync(0xffffffffu, cid, 0), stride = __shfl_sync(0xffffffffu, ncl, 0);
+      const int tiles_end = __shfl_sync(0xffffffffu, total, 0);
+      const uint64_t desc0 = ptx::desc_kmajor_sw128(__shfl_sync(0xffffffffu, ptx::smem_u32(stages), 0));
+      const uint32_t ctl0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ctl), 0);
+      const bool elected = elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ptx::mbar_wait(ctl0 + bar, parity, timeout_ns, abort_flag)) != 0;
+      };
       int stage = 0, acc = 0, set = 0;
-      uint32_t phase = 0, over_phase = 0, sf_phase = 0;
+      uint32_t phase = 0, acc_phase = 0, over_phase = 0, sf_phase = 0;
       bool ok = true, first = true;
-      const uint64_t sf_desc = desc_rows16(ptx::smem_u32(sf_base));
-      for (int tile = cid; tile < total && ok; tile += ncl) {
-        const uint32_t d_tmem = tmem + (uint32_t)(acc * kAccStep);
+      for (int tile = first_tile; tile < tiles_end && ok; tile += stride) {
+        // the accumulator before the last, and the columns shared with the last one, have been read
+        ok = wait(offsetof(Ctl, tempty) + 8 * acc, acc_phase ^ 1u) && (first || wait(offsetof(Ctl, over), over_phase));
+        if (!ok) break;
+        if (!first) over_phase ^= 1u;
+        first = false;
+        ptx::tc_fence_after();
+        const uint32_t d_tmem = tm + (uint32_t)(acc * kAccStep);
         uint32_t sf = 0;
         for (int kb = 0; kb < kblocks; ++kb) {
-          if ((kb & 3) == 0) {  // the words of the next four K blocks
-            if (!ptx::mbar_wait(ptx::smem_u32(&ctl->sf_full), sf_phase, timeout_ns, abort_flag)) {
-              ok = false;
-              break;
-            }
-            sf_phase ^= 1u;
-            ptx::tc_fence_after();
-            sf = tmem + (uint32_t)(kSfCol + set * kSfStep);
-            set ^= 1;
-#pragma unroll
-            for (int i = 0; i < 3; ++i) tmem_cp_factors(sf + 4 * i, sf_desc + (uint64_t)(i * (512 >> 4)));
-            ptx::mma_commit_pair_multicast(ptx::smem_u32(&ctl->sf_empty), 0x3);
+          if ((kb & 3) == 0) {  // a new group: its factors
+            if (!(ok = wait(offsetof(Ctl, sf_full) + 8 * set, sf_phase))) break;
+            sf = tm + (uint32_t)(kSfCol + set * kSfStep);
           }
-          if (kb == 0 && !first) {  // the columns shared with the previous tile's accumulator
-            if (!ptx::mbar_wait(ptx::smem_u32(&ctl->over), over_phase, timeout_ns, abort_flag)) {
-              ok = false;
-              break;
-            }
-            over_phase ^= 1u;
-            ptx::tc_fence_after();
-          }
-          if (!ptx::mbar_wait(ptx::smem_u32(&ctl->full[stage]), phase, timeout_ns, abort_flag)) {
-            ok = false;
-            break;
-          }
+          if (!(ok = wait(offsetof(Ctl, full) + 8 * stage, phase))) break;
           ptx::tc_fence_after();
-          const uint32_t sa = ptx::smem_u32(stages + (size_t)stage * kStageBytes);
-          const uint32_t sb = sa + kABytes;
-          const uint32_t idesc = idesc_mxf8(kMmaM, kMmaN, (uint32_t)(kb & 3));
+          const bool last_of_group = (kb & 3) == 3 || kb + 1 == kblocks;
+          if (elected) {
+            const uint64_t da = desc0 + (uint64_t)(stage * (kStageBytes >> 4)), db = da + (kABytes >> 4);
+            const uint32_t idesc = idesc_mxf8(kMmaM, kMmaN, 0) | (uint32_t)(kb & 3) * idesc_byte();
 #pragma unroll
-          for (int ks = 0; ks < kBK / kMmaK; ++ks)
-            mma_mxf8_pair(d_tmem, ptx::desc_kmajor_sw128(sa + ks * kMmaK), ptx::desc_kmajor_sw128(sb + ks * kMmaK), idesc,
-                          sf, sf + 4, (kb | ks) != 0 ? 1u : 0u);
-          ptx::mma_commit_pair_multicast(ptx::smem_u32(&ctl->empty[stage]), 0x3);
+            for (int ks = 0; ks < kBK / kMmaK; ++ks)
+              mma_mxf8_pair(d_tmem, da + ks * (kMmaK >> 4), db + ks * (kMmaK >> 4), idesc, sf, sf + 4, (kb | ks) != 0 ? 1u : 0u);
+            ptx::mma_commit_pair_multicast(ctl0 + offsetof(Ctl, empty) + 8 * stage, 0x3);
+            if (last_of_group) ptx::mma_commit_pair_multicast(ctl0 + offsetof(Ctl, sf_empty) + 8 * set, 0x3);
+          }
+          __syncwarp();
+          if (last_of_group && ++set == kSfSets) {
+            set = 0;
+            sf_phase ^= 1u;
+          }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        ptx::mma_commit_pair_multicast(ptx::smem_u32(&ctl->tfull[acc]), 0x3);
-        acc ^= 1;
-        first = false;
+        if (elected) ptx::mma_commit_pair_multicast(ctl0 + offsetof(Ctl, tfull) + 8 * acc, 0x3);
+        __syncwarp();
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
       }
-      if (!ok) {
+      if (!ok && elected) {
         record_error(ws, MOE_ERR_TIMEOUT, 0x920u + kKind);
         raise_abort(ctl, rank);
       }
+      // every MMA of this pair has finished with both CTAs' TMEM
+      if (elected) ptx::mma_commit_pair(ctl0 + offsetof(Ctl, drain));
+      __syncwarp();
+      ptx::mbar_wait(ctl0 + offsetof(Ctl, drain), 0u, timeout_ns, nullptr);
     }
     __syncwarp();
-  } else if (warp == 3) {
+  } else if (warp >= kSfWarp0) {
     // ------------------------------------------------------------ factor words (both CTAs)
+    regs_dec<kRegsFew>();
     const uint32_t* sa32 = reinterpret_cast<const uint32_t*>(g.sa);
     const uint32_t* sb32 = reinterpret_cast<const uint32_t*>(g.sb);
     const uint32_t* sb3_32 = reinterpret_cast<const uint32_t*>(kKind == kSwiGLU ? g.sb3 : g.sb);
-    const uint32_t dst = ptx::smem_u32(sf_base) + (uint32_t)lane * 16;
-    const uint32_t bar = ptx::mapa(ptx::smem_u32(&ctl->sf_full), 0);
+    const uint32_t dst = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kSfCol;
+    int set = 0;
     uint32_t phase = 0;
     bool ok = true;
     // The words of the next group are requested before the present group's wait, across tiles too:
@@ -348,30 +387,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       request();
     }
     while (tile < total) {
-      const uint32_t w[6] = {a[0], a[1], a[2], a[3], b0, b1};
+      const uint32_t w[4] = {a[0], a[1], a[2], a[3]}, w0 = b0, w1 = b1;
       if (++gk == sck) {
         gk = 0;
         tile += ncl;
         if (tile < total) locate();
       }
       if (tile < total) request();
-      ok = ptx::mbar_wait(ptx::smem_u32(&ctl->sf_empty), phase ^ 1u, timeout_ns, abort_flag);
+      ok = ptx::mbar_wait(ptx::smem_u32(&ctl->sf_empty[set]), phase ^ 1u, timeout_ns, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      phase ^= 1u;
-      st_shared_v4(dst, w[0], w[1], w[2], w[3]);
-      st_shared_v4(dst + 512, w[4], w[4], w[4], w[4]);
-      st_shared_v4(dst + 1024, w[5], w[5], w[5], w[5]);
-      fence_async();
+      ptx::tc_fence_after();
+      tmem_st_factors(dst + set * kSfStep, w, w0, w1);
+      ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(bar);
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->sf_full[set]), 0));
+      if (++set == kSfSets) {
+        set = 0;
+        phase ^= 1u;
+      }
     }
     if (!ok && lane == 0) {
       record_error(ws, MOE_ERR_TIMEOUT, 0x930u + kKind);
       raise_abort(ctl, rank);
     }
-  } else if (warp >= kEpiWarp0) {
+  } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
+    regs_inc<kRegsEpi>();
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const int r = q * 32 + lane;
     const uint32_t over = ptx::mapa(ptx::smem_u32(&ctl->over), 0);
@@ -385,39 +427,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kKind != kSwiGLU && !ok) break;
       ptx::tc_fence_after();
       const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kAccStep);
-      // accumulator 0 shares its last 32 columns (the upper half's), accumulator 1 its first 32
+      // accumulator 0 shares its last 64 columns (the upper half's), accumulator 1 its first 64
       const bool shares = acc == 1 - half;
       const bool flip = acc == 0 && half == 1;  // the shared columns lie in the second piece: take it first
-      if (!shares) {
-        ptx::tc_fence_before();  // the loads of the accumulator before the last
+      const uint32_t tempty = ptx::mapa(ptx::smem_u32(&ctl->tempty[acc]), 0);
+      auto arrive = [&](uint32_t bar) {  // after this warp's loads so far
+        ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(over);
-      }
+        if (lane == 0) ptx::mbar_arrive_cluster(bar);
+      };
       const bool valid = r < ti.rows;
       const int64_t p = (int64_t)ti.row0 + r;
       const int n0 = ti.n_idx * bn;
       const int vw = ti.rows - q * 32;  // rows of this warp's 32 that belong to the tile's expert
       if constexpr (kKind == kSwiGLU) {
-        // this warp's 64 hidden columns, 32 at a time
-        float h[2][32];
+        // This warp's 64 hidden columns: W1's products at c, W3's at 128 + c.  The side that lies in
+        // the shared columns is loaded first and whole, the other 32 columns at a time.
+        float h[64];
         uint32_t top = 0;
+        const int c0 = half * 64;
+        const uint32_t t_first = t_row + (flip ? kMmaN / 2 : 0) + c0, t_second = t_row + (flip ? 0 : kMmaN / 2) + c0;
+        uint32_t f0[32], f1[32];
+        ptx::tmem_ld_32cols(t_first, f0);
+        ptx::tmem_ld_32cols(t_first + 32, f1);
+        ptx::tmem_ld_wait();
+        if (shares) arrive(over);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int c = half * 64 + ((u == 1) != flip ? 32 : 0);
-          uint32_t a[32], b[32];
-          ptx::tmem_ld_32cols(t_row + c, a);
-          ptx::tmem_ld_32cols(t_row + kMmaN / 2 + c, b);
+          uint32_t s[32];
+          ptx::tmem_ld_32cols(t_second + 32 * u, s);
           ptx::tmem_ld_wait();
-          if (u == 0 && shares) {
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(over);
-          }
+          if (u == 1) arrive(tempty);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            h[u][i] = silu_exact(__uint_as_float(a[i])) * __uint_as_float(b[i]);
-            if (n0 + c + (i & ~15) >= g.n) h[u][i] = 0.f;  // columns past the expert (n is a multiple of 16)
-            top = max(top, abs_bits(h[u][i]));
+            const float x = __uint_as_float(u == 0 ? f0[i] : f1[i]), y = __uint_as_float(s[i]);
+            float v = silu_exact(flip ? y : x) * (flip ? x : y);
+            if (n0 + c0 + 32 * u + (i & ~15) >= g.n) v = 0.f;  // columns past the expert (n is a multiple of 16)
+            h[32 * u + i] = v;
+            top = max(top, abs_bits(v));
           }
         }
         top_s[half * kRowsPerCta + r] = top;
@@ -431,21 +478,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t stg = ptx::smem_u32(stg_base) + (uint32_t)(q * kStgBlockBytes);
         uint8_t* hrow = reinterpret_cast<uint8_t*>(g.out) + p * g.n + n0;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int c = half * 64 + ((u == 1) != flip ? 32 : 0);
+        for (int v = 0; v < 4; ++v) {
+          uint32_t w[4];
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_e4m3x4(h[u][16 * v + 4 * i] * f, h[u][16 * v + 4 * i + 1] * f, h[u][16 * v + 4 * i + 2] * f,
-                                 h[u][16 * v + 4 * i + 3] * f);
-            const int j = c / 16 + v;
-            if (vw >= 32)
-              st_shared_v4(stg + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) * 16)), w[0], w[1], w[2], w[3]);
-            else if (valid && n0 + 16 * j < g.n)
-              *reinterpret_cast<uint4*>(hrow + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int i = 0; i < 4; ++i)
+            w[i] = pack_e4m3x4(h[16 * v + 4 * i] * f, h[16 * v + 4 * i + 1] * f, h[16 * v + 4 * i + 2] * f,
+                               h[16 * v + 4 * i + 3] * f);
+          const int j = half * 4 + v;
+          if (vw >= 32)
+            st_shared_v4(stg + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) * 16)), w[0], w[1], w[2], w[3]);
+          else if (valid && n0 + 16 * j < g.n)
+            *reinterpret_cast<uint4*>(hrow + 16 * j) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         if (half == 0 && valid) g.out_scales[p * scale_cols(g.n) + ti.n_idx] = (uint8_t)sb;
         if (vw >= 32) fence_async();
@@ -476,11 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) pk[i] = __float_as_uint(gate * __uint_as_float(pk[i]));
           }
-          if (u == 0 && shares) {
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(over);
-          }
+          if (shares && u == 64 / kCols - 1) arrive(over);
+          if (u == kPieces - 1) arrive(tempty);
           if (vw <= 0 || n0 + c >= g.n) continue;  // warp-uniform
           if (vw >= 32) {
             if (lane == 0) bulk_wait_read();
@@ -514,12 +554,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  __syncthreads();
-  if (leader && warp == 1 && lane == 0) {
-    // every copy and MMA of this pair has finished with both CTAs' TMEM
-    ptx::mma_commit_pair(ptx::smem_u32(&ctl->drain));
-    ptx::mbar_wait(ptx::smem_u32(&ctl->drain), 0u, timeout_ns, nullptr);
-  }
   __syncthreads();
   ptx::cluster_sync();  // neither CTA issues loads or MMAs any more
   if (*abort_flag && threadIdx.x == 0) {

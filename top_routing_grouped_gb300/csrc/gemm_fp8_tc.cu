@@ -299,12 +299,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, acc_phase = 0, over_phase = 0, sf_phase = 0;
       bool ok = true, first = true;
       for (int tile = first_tile; tile < tiles_end && ok; tile += stride) {
-        // the accumulator before the last, and the columns shared with the last one, have been read
-        ok = wait(offsetof(Ctl, tempty) + 8 * acc, acc_phase ^ 1u) && (first || wait(offsetof(Ctl, over), over_phase));
-        if (!ok) break;
-        if (!first) over_phase ^= 1u;
-        first = false;
-        ptx::tc_fence_after();
         const uint32_t d_tmem = tm + (uint32_t)(acc * kAccStep);
         uint32_t sf = 0;
         for (int kb = 0; kb < kblocks; ++kb) {
@@ -313,6 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             sf = tm + (uint32_t)(kSfCol + set * kSfStep);
           }
           if (!(ok = wait(offsetof(Ctl, full) + 8 * stage, phase))) break;
+          if (kb == 0) {
+            // The accumulator before the last has been read, and so have the columns shared with the
+            // last one: waited for when all else is there, since the MMAs stand still until then.
+            ok = wait(offsetof(Ctl, tempty) + 8 * acc, acc_phase ^ 1u) && (first || wait(offsetof(Ctl, over), over_phase));
+            if (!ok) break;
+            if (!first) over_phase ^= 1u;
+            first = false;
+          }
           ptx::tc_fence_after();
           const bool last_of_group = (kb & 3) == 3 || kb + 1 == kblocks;
           if (elected) {

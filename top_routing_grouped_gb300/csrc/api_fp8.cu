@@ -12,6 +12,7 @@
 struct moe_fp8_plan_s {
   bool experts;  // the expert stage (else one product)
   bool tc;       // tensor-core kernels (MOE_PATH_AUTO)
+  bool few;      // ... those for few rows an expert
   int64_t rows;
   int k, n, E, n_seg, max_groups;  // expert stage: k = d, n = F
   int out_dtype;
@@ -88,6 +89,12 @@ moe_status bind_device(moe_fp8_plan_t plan) {
   return MOE_OK;
 }
 
+// Rows a segment on average, up to which the kernels that make the weights the MMA's rows are used.
+#ifndef FEW_ROWS
+#define FEW_ROWS 64
+#endif
+constexpr int64_t kFewRows = FEW_ROWS;
+
 moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E, int32_t W, int32_t out_dtype,
                      int32_t path, int64_t timeout_ns, moe_fp8_plan_t* plan, size_t* workspace_bytes) {
   *plan = nullptr;
@@ -106,6 +113,7 @@ moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E
   if (!p) return fail(MOE_ERR_INTERNAL, "out of host memory");
   p->experts = experts;
   p->tc = tc;
+  p->few = tc && rows <= kFewRows * (int64_t)E * W;
   p->rows = rows;
   p->k = k;
   p->n = n;
@@ -136,7 +144,7 @@ moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E
   return set_last_error(MOE_OK, "");
 }
 
-// Tile tables of this call's segments.
+// Tile tables of this call's segments (the kernels for few rows find theirs themselves).
 moe_status begin(moe_fp8_plan_t plan, const int32_t* seg_counts, void* workspace, cudaStream_t st, Ws* ws) {
   moe_status s = bind_device(plan);
   if (s != MOE_OK) return s;
@@ -147,16 +155,23 @@ moe_status begin(moe_fp8_plan_t plan, const int32_t* seg_counts, void* workspace
   ws->offsets = reinterpret_cast<int32_t*>(b + plan->offsets);
   ws->mt_desc = reinterpret_cast<int4*>(b + plan->mt_desc);
   ws->pr_desc = reinterpret_cast<int4*>(b + plan->pr_desc);
+  if (plan->few) return MOE_OK;
   Shape shape{};
   shape.N = plan->rows;
   shape.max_groups = plan->max_groups;
   return cuda_status(launch_seg_scan(shape, *ws, seg_counts, plan->n_seg, plan->E, true, st), "launching the segment scan");
 }
 
-moe_status product(moe_fp8_plan_t plan, int kind, const fp8::GemmArgs& g, const Ws& ws, cudaStream_t st, const char* what) {
-  return cuda_status(plan->tc ? fp8::launch_gemm_tc(kind, g, ws, plan->device, plan->num_sms, plan->timeout_ns, true, st)
-                              : fp8::launch_gemm_simt(kind, g, ws, plan->num_sms, st),
-                     what);
+moe_status product(moe_fp8_plan_t plan, int kind, const fp8::GemmArgs& g, const Ws& ws, const int32_t* seg_counts, bool first,
+                   cudaStream_t st, const char* what) {
+  cudaError_t e;
+  if (plan->few)
+    e = fp8::launch_gemm_few(kind, g, ws, seg_counts, plan->n_seg, first, plan->device, plan->num_sms, plan->timeout_ns, !first, st);
+  else if (plan->tc)
+    e = fp8::launch_gemm_tc(kind, g, ws, plan->device, plan->num_sms, plan->timeout_ns, true, st);
+  else
+    e = fp8::launch_gemm_simt(kind, g, ws, plan->num_sms, st);
+  return cuda_status(e, what);
 }
 
 moe_status check_workspace(moe_fp8_plan_t plan, const void* workspace, size_t bytes) {
@@ -281,7 +296,8 @@ moe_status moe_fp8_matmul(moe_fp8_plan_t plan, const int32_t* seg_counts, const 
   g.n = plan->n;
   g.K = plan->k;
   g.E = plan->E;
-  return product(plan, plan->out_dtype == MOE_BF16 ? fp8::kOutBf16 : fp8::kOutF32, g, ws, st, "launching the product");
+  return product(plan, plan->out_dtype == MOE_BF16 ? fp8::kOutBf16 : fp8::kOutF32, g, ws, seg_counts, true, st,
+                 "launching the product");
 }
 
 moe_status moe_fp8_expert_forward(moe_fp8_plan_t plan, const int32_t* seg_counts, const void* x_rows,
@@ -320,7 +336,7 @@ moe_status moe_fp8_expert_forward(moe_fp8_plan_t plan, const int32_t* seg_counts
   g.n = plan->n;
   g.K = plan->k;
   g.E = plan->E;
-  if ((s = product(plan, fp8::kSwiGLU, g, ws, st, "launching the SwiGLU product")) != MOE_OK) return s;
+  if ((s = product(plan, fp8::kSwiGLU, g, ws, seg_counts, true, st, "launching the SwiGLU product")) != MOE_OK) return s;
   g.a = b + plan->h;
   g.sa = b + plan->h_scales;
   g.b = static_cast<const uint8_t*>(w2);
@@ -332,7 +348,7 @@ moe_status moe_fp8_expert_forward(moe_fp8_plan_t plan, const int32_t* seg_counts
   g.out_scales = nullptr;
   g.n = plan->k;
   g.K = plan->n;
-  return product(plan, fp8::kOutBf16, g, ws, st, "launching the down-projection");
+  return product(plan, fp8::kOutBf16, g, ws, seg_counts, false, st, "launching the down-projection");
 }
 
 moe_status moe_fp8_get_device_status(moe_fp8_plan_t plan, const void* workspace, void* stream) {

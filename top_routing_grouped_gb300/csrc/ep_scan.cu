@@ -28,9 +28,14 @@ __global__ void __launch_bounds__(kSegThreads) seg_scan_kernel(Shape s, Ws ws, c
   const int i = threadIdx.x;
   if (clear && i < kHdrClearWords) ws.hdr[i] = 0u;  // ordered before record_error by the barrier below
   int cnt = i < n_seg ? (seg_counts ? seg_counts[i] : (int)s.N) : 0;
-  const bool neg = cnt < 0;
+  // a negative count, or a sum above the capacity (taken in 64 bits: it could wrap in 32)
+  __shared__ unsigned long long sum;
+  if (i == 0) sum = 0;
+  const bool neg = __syncthreads_or(cnt < 0) != 0;
+  if (!neg) atomicAdd(&sum, (unsigned long long)cnt);
   cnt_s[i] = neg ? 0 : cnt;
-  if (__syncthreads_or(neg)) {
+  __syncthreads();
+  if (neg || sum > (unsigned long long)s.N) {
     if (i == 0) {
       record_error(ws, MOE_ERR_INTERNAL, 0x740u);
       ws.hdr[kHdrNumGroups] = 0;

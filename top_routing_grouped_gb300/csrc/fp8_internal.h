@@ -47,6 +47,10 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
 cudaError_t launch_gemm_simt(int kind, const GemmArgs& g, const Ws& ws, int num_sms, cudaStream_t st);
 cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns,
                            bool pdl, cudaStream_t st);
+// Few rows an expert: finds its tiles from the segment counts itself (null: one segment); `first`:
+// the call's first launch, which sets the status word.
+cudaError_t launch_gemm_few(int kind, const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first,
+                            int device, int num_sms, int64_t timeout_ns, bool pdl, cudaStream_t st);
 
 }  // namespace fp8
 }  // namespace moe

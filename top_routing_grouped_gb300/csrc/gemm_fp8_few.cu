@@ -1,0 +1,572 @@
+// gemm_fp8_few.cu -- the 8-bit grouped products where an expert has few rows (decoding, short
+// batches): the same results as gemm_fp8_tc.cu, bound by reading the weights once.
+//
+//   out[p, n] = gate(p) * (A[p] . W_e[n])   and   h[p, n] = SiLU(A[p] . W1_e[n]) * (A[p] . W3_e[n])
+//
+// With a handful of rows a 256-row tile is padding, and an MMA of 256 rows takes as long for one of
+// them as for all.  Here the weights are the MMA's 128 rows and the activations its N columns
+// (16, 32 or 64), so D[m][t] is output column m of row t; an MMA takes 39-48 clocks, a stage of
+// 16 KB (SwiGLU: 32 KB) of weights a quarter of the time that HBM takes to deliver it.
+//
+// A unit of work is (segment, block of 128 weight rows, up to 64 of the segment's rows).  Every CTA
+// finds its units from the segment counts itself (a scan over at most 256 numbers), so a call needs no
+// kernel for tile tables.  When there are fewer units than SMs, a cluster of 2, 4 or 8 CTAs
+// shares a unit: each sums a part of K, and the first CTA adds the others' sums, which arrive in
+// its shared memory, in rank order.
+//
+// Roles of a CTA: a TMA thread (ring of stages), an MMA warp (one elected lane issues), four
+// epilogue warps and four warps that store the block factors to TMEM, as in gemm_fp8_tc.cu.  Waits are
+// bounded (MOE_ERR_TIMEOUT, no trap).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stddef.h>
+
+#include <atomic>
+
+#include "device_common.cuh"
+#include "fp8_common.cuh"
+#include "fp8_mma.cuh"
+#include "gemm_tc.h"
+#include "tc_ptx.cuh"
+#include "tmap.h"
+
+namespace moe {
+namespace fp8 {
+namespace {
+
+constexpr int kBK = 128;              // k's (bytes) per stage: one block of factors
+constexpr int kWRows = 128;           // weight rows per unit
+constexpr int kMaxTok = 64;           // activation rows per unit
+constexpr int kTokBox = 16;           // rows of one TMA box of activations
+constexpr int kWBytes = kWRows * kBK;
+constexpr int kMaxStages = 12;
+constexpr int kThreads = 384;
+constexpr int kEpiWarp0 = 4, kSfWarp0 = 8;
+constexpr int kEpiBar = 1;            // named barrier of the four epilogue warps
+
+// TMEM columns: accumulator (buffer b, matrix m) at 128 b + 64 m; factor set i at 256 + 16 i
+// (4 of W1 or W, 4 of W3, 4 of the activations)
+constexpr int kTmemCols = 512;
+constexpr int kSfCol = 256;
+constexpr int kSfStep = 16;
+constexpr int kSfSets = 8;
+
+struct Ctl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t tfull[2], tempty[2];
+  uint64_t sf_full[kSfSets], sf_empty[kSfSets];
+  uint64_t rfull;  // first CTA: the others' sums have arrived
+  uint64_t rfree;  // others: the first CTA has read this one's sums
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int bad;
+  uint32_t top[2][4][32];        // epilogue: largest hidden value of each warp and row
+  int row0[kMaxExperts + 1];     // first row of each segment
+  int unit0[kMaxExperts + 1];    // first unit of each segment
+  int64_t row_tot[8];  // the scans' warp totals
+  int unit_tot[8];
+};
+
+// The launch's sizes, chosen on the host.
+struct FewShape {
+  int n_seg;       // segments; segment s holds rows of expert s % E
+  int tok;         // rows per unit: a multiple of 16, at most 64
+  int stages;
+  int stage_bytes;
+  int recv_bytes;  // shared memory for one other CTA's sums
+  int split;       // CTAs of a cluster that share a unit
+  int first;       // this launch starts the call: it sets the status word
+};
+
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, int64_t timeout_ns, const volatile int* abort) {
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63u) == 0u && (*abort || (int64_t)(global_ns() - t0) > timeout_ns)) return false;
+  }
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Barrier of the 128 epilogue threads, with the AND of a flag over them.
+__device__ __forceinline__ bool epi_bar_and(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "n"(kEpiBar), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+struct Unit {
+  int e;       // weight expert
+  int n0;      // first weight row of the block
+  int row0;    // first activation row
+  int rows;    // activation rows, 1..tok
+};
+
+// Unit u: segments in order, in a segment the blocks of weight rows, in a block the groups of rows
+// (neighbouring CTAs then read the same weights, once from HBM).
+__device__ __forceinline__ Unit decode(const Ctl* ctl, const FewShape& f, int E, int u) {
+  int lo = 0, hi = f.n_seg - 1;  // the last segment whose first unit is at or below u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (ctl->unit0[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const int cnt = ctl->row0[lo + 1] - ctl->row0[lo], groups = (cnt + f.tok - 1) / f.tok, local = u - ctl->unit0[lo];
+  Unit r;
+  r.e = lo % E;
+  r.n0 = local / groups * kWRows;
+  const int g0 = local % groups * f.tok;
+  r.row0 = ctl->row0[lo] + g0;
+  r.rows = min(f.tok, cnt - g0);
+  return r;
+}
+
+// Inclusive scan over the first 256 threads (all threads call it).
+template <typename T>
+__device__ __forceinline__ T scan256(T v, T* warp_tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (warp < 8 && lane == 31) warp_tot[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < 8; ++w)
+    if (w < warp) v += warp_tot[w];
+  return v;
+}
+
+template <int kKind>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp8_few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                        const __grid_constant__ CUtensorMap tmW3, GemmArgs g, Ws ws, const int32_t* seg_counts, FewShape f,
+                        int64_t timeout_ns) {
+  constexpr int kMats = kKind == kSwiGLU ? 2 : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* recv = reinterpret_cast<float*>(stages + (size_t)f.stages * f.stage_bytes);
+  Ctl* ctl = reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(recv) + (size_t)(f.split - 1) * f.recv_bytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = f.split > 1 ? ptx::cluster_ctarank() : 0;
+  const int cid = (int)(blockIdx.x / f.split), ncl = (int)(gridDim.x / f.split);
+  const int nblk = (g.n + kWRows - 1) / kWRows;
+  const int kblocks = (g.K + kBK - 1) / kBK;
+  const int sck = (int)(scale_cols(g.K) / 4);
+  const int gk0 = sck * (int)rank / f.split, gk1 = sck * ((int)rank + 1) / f.split;  // this CTA's groups of four K blocks
+  const int kb0 = gk0 * 4, kb1 = min(gk1 * 4, kblocks);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < f.stages; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&ctl->full[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&ctl->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&ctl->tfull[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&ctl->tempty[i]), 4);
+    }
+    for (int i = 0; i < kSfSets; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&ctl->sf_full[i]), 4);
+      ptx::mbar_init(ptx::smem_u32(&ctl->sf_empty[i]), 1);
+    }
+    ptx::mbar_init(ptx::smem_u32(&ctl->rfull), f.split > 1 ? 4 * (f.split - 1) : 1);
+    ptx::mbar_init(ptx::smem_u32(&ctl->rfree), 4);
+    ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
+    ctl->abort = 0;
+    ctl->bad = 0;
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&tmX);
+    ptx::tma_prefetch_desc(&tmW);
+    if (kMats == 2) ptx::tma_prefetch_desc(&tmW3);
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  if (f.split > 1) ptx::cluster_sync();  // every CTA's barriers exist before another arrives on them
+  pdl_wait();  // the activations (and the counts) come from earlier kernels
+  pdl_launch_dependents();
+
+  // ---- the segments' first rows and units
+  int total;
+  {
+    const int i = threadIdx.x;
+    const int cnt = i < f.n_seg ? (seg_counts ? seg_counts[i] : (int)g.rows) : 0;
+    if (cnt < 0) ctl->bad = 1;
+    const int64_t rows = scan256((int64_t)cnt, ctl->row_tot);  // 64 bits: bad counts may sum to anything
+    if (i == f.n_seg - 1 && rows > g.rows) ctl->bad = 1;
+    __syncthreads();
+    const bool bad = ctl->bad != 0;
+    const int units = scan256(bad ? 0 : (cnt + f.tok - 1) / f.tok * nblk, ctl->unit_tot);
+    if (i < kMaxExperts) {
+      ctl->row0[i + 1] = bad ? 0 : (int)rows;
+      ctl->unit0[i + 1] = units;
+    }
+    if (i == 0) ctl->row0[0] = ctl->unit0[0] = 0;
+    __syncthreads();
+    total = ctl->unit0[f.n_seg];
+    if (f.first && blockIdx.x == 0 && i == 0) {
+      ws.hdr[kHdrWhere] = bad ? 0x950u : 0u;
+      ws.hdr[kHdrStatus] = bad ? (uint32_t)MOE_ERR_INTERNAL : 0u;
+    }
+  }
+  volatile int* abort_flag = &ctl->abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- TMA producer
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = cid; u < total && ok; u += ncl) {
+        const Unit un = decode(ctl, f, g.E, u);
+        const int boxes = (un.rows + kTokBox - 1) / kTokBox;
+        const uint32_t bytes = (uint32_t)(kMats * kWBytes + boxes * kTokBox * kBK);
+        const int wrow = un.e * g.n + un.n0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!ptx::mbar_wait(ptx::smem_u32(&ctl->empty[stage]), phase ^ 1u, timeout_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = ptx::smem_u32(&ctl->full[stage]);
+          const uint32_t s = ptx::smem_u32(stages + (size_t)stage * f.stage_bytes);
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+          ptx::tma_load_2d(s, &tmW, kb * kBK, wrow, bar);
+          if (kMats == 2) ptx::tma_load_2d(s + kWBytes, &tmW3, kb * kBK, wrow, bar);
+          for (int b = 0; b < boxes; ++b)
+            ptx::tma_load_2d(s + kMats * kWBytes + b * kTokBox * kBK, &tmX, kb * kBK, un.row0 + b * kTokBox, bar);
+          if (++stage == f.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        record_error(ws, MOE_ERR_TIMEOUT, 0x960u + kKind);
+        ctl->abort = 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (converged warp)
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t desc0 = ptx::desc_kmajor_sw128(__shfl_sync(0xffffffffu, ptx::smem_u32(stages), 0));
+    const uint32_t ctl0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ctl), 0);
+    const bool elected = elect_one();
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, ptx::mbar_wait(ctl0 + bar, parity, timeout_ns, abort_flag)) != 0;
+    };
+    int stage = 0, acc = 0, set = 0;
+    uint32_t phase = 0, acc_phase = 0, sf_phase = 0;
+    bool ok = true;
+    for (int u = cid; u < total && ok; u += ncl) {
+      const int cols = (__shfl_sync(0xffffffffu, decode(ctl, f, g.E, u).rows, 0) + 15) & ~15;
+      if (!(ok = wait(offsetof(Ctl, tempty) + 8 * acc, acc_phase ^ 1u))) break;
+      ptx::tc_fence_after();
+      const uint32_t d = tm + (uint32_t)(acc * 128);
+      uint32_t sf = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if ((kb & 3) == 0) {
+          if (!(ok = wait(offsetof(Ctl, sf_full) + 8 * set, sf_phase))) break;
+          sf = tm + (uint32_t)(kSfCol + set * kSfStep);
+        }
+        if (!(ok = wait(offsetof(Ctl, full) + 8 * stage, phase))) break;
+        ptx::tc_fence_after();
+        const bool last_of_group = (kb & 3) == 3 || kb + 1 == kb1;
+        if (elected) {
+          const uint64_t dw = desc0 + (uint64_t)(stage * (f.stage_bytes >> 4)), dx = dw + (kMats * kWBytes >> 4);
+          const uint32_t idesc = idesc_mxf8(kWRows, 0, 0) + (uint32_t)(kb & 3) * idesc_byte() + ((uint32_t)(cols >> 3) << 17);
+#pragma unroll
+          for (int m = 0; m < kMats; ++m)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_mxf8(d + 64 * m, dw + (m * kWBytes >> 4) + 2 * ks, dx + 2 * ks, idesc, sf + 4 * m, sf + 8,
+                       (kb != kb0 || ks != 0) ? 1u : 0u);
+          ptx::mma_commit(ctl0 + offsetof(Ctl, empty) + 8 * stage);
+          if (last_of_group) ptx::mma_commit(ctl0 + offsetof(Ctl, sf_empty) + 8 * set);
+          if (kb + 1 == kb1) ptx::mma_commit(ctl0 + offsetof(Ctl, tfull) + 8 * acc);
+        }
+        __syncwarp();
+        if (last_of_group && ++set == kSfSets) {
+          set = 0;
+          sf_phase ^= 1u;
+        }
+        if (++stage == f.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (!ok && elected) {
+      record_error(ws, MOE_ERR_TIMEOUT, 0x970u + kKind);
+      ctl->abort = 1;
+    }
+    // every MMA has finished before TMEM is released
+    if (elected) ptx::mma_commit(ctl0 + offsetof(Ctl, drain));
+    __syncwarp();
+    ptx::mbar_wait(ctl0 + offsetof(Ctl, drain), 0u, timeout_ns, nullptr);
+  } else if (warp >= kSfWarp0) {
+    // ------------------------------------------------------------ block factors
+    const uint32_t* sx32 = reinterpret_cast<const uint32_t*>(g.sa);
+    const uint32_t* sw32 = reinterpret_cast<const uint32_t*>(g.sb);
+    const uint32_t* sw3_32 = reinterpret_cast<const uint32_t*>(kMats == 2 ? g.sb3 : g.sb);
+    const uint32_t dst = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kSfCol;
+    int set = 0, u = cid, gk = gk0;
+    uint32_t phase = 0;
+    bool ok = true;
+    int64_t rx[2], rw = 0;
+    auto locate = [&]() {
+      const Unit un = decode(ctl, f, g.E, u);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) rx[c] = min((int64_t)un.row0 + 32 * c + lane, g.rows - 1) * sck;  // clamped: unused rows
+      rw = ((int64_t)un.e * nblk + un.n0 / kBlock) * sck;
+    };
+    uint32_t x[2], w0 = 0, w1 = 0;
+    auto request = [&]() {
+      x[0] = __ldg(sx32 + rx[0] + gk);
+      x[1] = __ldg(sx32 + rx[1] + gk);
+      w0 = __ldg(sw32 + rw + gk);
+      w1 = __ldg(sw3_32 + rw + gk);
+    };
+    if (u < total && gk0 < gk1) {
+      locate();
+      request();
+    }
+    while (u < total && gk0 < gk1) {
+      const uint32_t wx[4] = {x[0], x[1], x[1], x[1]}, v0 = w0, v1 = w1;
+      if (++gk == gk1) {
+        gk = gk0;
+        u += ncl;
+        if (u < total) locate();
+      }
+      if (u < total) request();
+      ok = ptx::mbar_wait(ptx::smem_u32(&ctl->sf_empty[set]), phase ^ 1u, timeout_ns, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      tmem_st_x4(dst + set * kSfStep, v0, v0, v0, v0);
+      tmem_st_x4(dst + set * kSfStep + 4, v1, v1, v1, v1);
+      tmem_st_x4(dst + set * kSfStep + 8, wx[0], wx[1], wx[2], wx[3]);
+      tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&ctl->sf_full[set]));
+      if (++set == kSfSets) {
+        set = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok && lane == 0) {
+      record_error(ws, MOE_ERR_TIMEOUT, 0x980u + kKind);
+      ctl->abort = 1;
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, m = q * 32 + lane;  // weight row of the block
+    const float* mine = recv + m;               // the others' sums: [rank - 1][matrix][column][128 rows]
+    const int recv_floats = f.recv_bytes / 4;
+    int acc = 0, turn = 0;
+    uint32_t acc_phase = 0, r_phase = 0;
+    bool ok = true;
+    for (int u = cid; u < total; u += ncl) {
+      const Unit un = decode(ctl, f, g.E, u);
+      ok = ptx::mbar_wait(ptx::smem_u32(&ctl->tfull[acc]), acc_phase, timeout_ns, abort_flag);
+      if (f.split > 1)
+        ok = ok && wait_cluster(ptx::smem_u32(rank == 0 ? &ctl->rfull : &ctl->rfree), rank == 0 ? r_phase : r_phase ^ 1u,
+                                timeout_ns, abort_flag);
+      ok = epi_bar_and(ok);  // the four warps go on or stop together
+      if (!ok) break;
+      ptx::tc_fence_after();
+      r_phase ^= 1u;
+      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 128);
+      const int col = un.n0 + m;
+      const bool in = col < g.n;
+      if (rank != 0) {
+        // this CTA's sums to the first CTA
+        const uint32_t dst = ptx::mapa(ptx::smem_u32(recv), 0) + (uint32_t)(((int)rank - 1) * f.recv_bytes + m * 4);
+        for (int mt = 0; mt < kMats; ++mt)
+          for (int c = 0; c < un.rows; c += 32) {
+            uint32_t v[32];
+            ptx::tmem_ld_32cols(t_row + 64 * mt + c, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c + i < un.rows) st_cluster_f32(dst + (uint32_t)((mt * f.tok + c + i) * 512), v[i]);
+          }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(ptx::smem_u32(&ctl->tempty[acc]));
+          ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfull), 0));
+        }
+      } else {
+        auto load = [&](int mt, int c, uint32_t(&v)[32]) {
+          ptx::tmem_ld_32cols(t_row + 64 * mt + c, v);
+          ptx::tmem_ld_wait();
+          for (int r = 0; r < f.split - 1; ++r)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c + i < un.rows)
+                v[i] = __float_as_uint(__uint_as_float(v[i]) + mine[r * recv_floats + (mt * f.tok + c + i) * 128]);
+        };
+        for (int c = 0; c < un.rows; c += 32) {
+          const int nt = min(32, un.rows - c);
+          const int64_t p0 = (int64_t)un.row0 + c;
+          if constexpr (kKind == kSwiGLU) {
+            uint32_t a[32], b[32];
+            load(0, c, a);
+            load(1, c, b);
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float h = silu_exact(__uint_as_float(a[i])) * __uint_as_float(b[i]);
+              a[i] = __float_as_uint(h);
+              if (i < nt) {  // the row's largest value over this warp's 32 columns, kept by lane i
+                const uint32_t t = __reduce_max_sync(0xffffffffu, in ? abs_bits(h) : 0u);
+                if (lane == i) top = t;
+              }
+            }
+            ctl->top[turn][q][lane] = top;
+            epi_bar_and(true);
+            const uint32_t* o = &ctl->top[turn][0][lane];
+            top = max(max(o[0], o[32]), max(o[64], o[96]));
+            turn ^= 1;
+            const uint32_t sb = scale_byte(__uint_as_float(top));
+            const float fac = inv_scale_value(sb);
+            if (q == 0 && lane < nt) g.out_scales[(p0 + lane) * scale_cols(g.n) + un.n0 / kBlock] = (uint8_t)sb;
+            uint8_t* out = reinterpret_cast<uint8_t*>(g.out) + p0 * g.n + col;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float fi = __shfl_sync(0xffffffffu, fac, i);
+              if (i < nt && in) out[(int64_t)i * g.n] = (uint8_t)pack_e4m3x2(__uint_as_float(a[i]) * fi, 0.f);
+            }
+          } else {
+            uint32_t v[32];
+            load(0, c, v);
+            const float gate = g.gate && lane < nt ? g.gate[p0 + lane] : 1.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float y = __shfl_sync(0xffffffffu, gate, i) * __uint_as_float(v[i]);
+              if (i < nt && in) store_act(g.out, kKind == kOutBf16, (p0 + i) * g.n + col, y);
+            }
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(ptx::smem_u32(&ctl->tempty[acc]));
+          for (int r = 1; r < f.split; ++r) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfree), (uint32_t)r));
+        }
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (!ok && lane == 0) {
+      record_error(ws, MOE_ERR_TIMEOUT, 0x990u + kKind);
+      ctl->abort = 1;
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    // copies already in flight land within microseconds; give them 200 us before the shared
+    // memory they target goes away
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 200000ull) {
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (f.split > 1) ptx::cluster_sync();  // no CTA's shared memory goes while another may still write to it
+  if (warp == 2) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+constexpr int kSmemMax = 232448;
+
+template <int kKind>
+cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first, int device,
+                        int num_sms, int64_t timeout_ns, bool pdl, cudaStream_t st) {
+  constexpr int kMats = kKind == kSwiGLU ? 2 : 1;
+  auto kern = gemm_fp8_few_kernel<kKind>;
+  cudaError_t e;
+  static std::atomic<uint64_t> asked{0};  // devices on which the kernel may use all shared memory
+  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+  if (!(asked.load(std::memory_order_acquire) & bit) || !bit) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess) return e;
+    asked.fetch_or(bit, std::memory_order_release);
+  }
+  FewShape f{};
+  f.n_seg = n_seg;
+  f.first = first ? 1 : 0;
+  f.tok = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : kMaxTok;
+  f.stage_bytes = kMats * kWBytes + f.tok * kBK;
+  f.recv_bytes = kMats * f.tok * kWRows * 4;
+  // Units, when the rows are spread as thin as they can be; clusters that leave no SM without a part
+  // of one.  K is split in whole groups of four blocks, and the others' sums need shared memory.
+  const int64_t nblk = (g.n + kWRows - 1) / kWRows, owners = g.rows < n_seg ? g.rows : n_seg;
+  const int64_t units = owners * nblk * (owners == 1 ? (g.rows + f.tok - 1) / f.tok : 1);
+  const int sck = (int)(scale_cols(g.K) / 4), fixed = 1024 + (int)sizeof(Ctl);
+  f.split = 1;
+  while (f.split < 8 && 2 * f.split * units <= num_sms && 2 * f.split <= sck &&
+         fixed + (2 * f.split - 1) * f.recv_bytes + 4 * f.stage_bytes <= kSmemMax)
+    f.split *= 2;
+  f.stages = (kSmemMax - fixed - (f.split - 1) * f.recv_bytes) / f.stage_bytes;
+  if (f.stages > kMaxStages) f.stages = kMaxStages;
+  const size_t smem = (size_t)fixed + (size_t)(f.split - 1) * f.recv_bytes + (size_t)f.stages * f.stage_bytes;
+  CUtensorMap mX, mW, mW3;
+  const uint64_t wrows = (uint64_t)g.E * (uint64_t)g.n;
+  if ((e = make_tmap_rows128(&mX, g.a, 1, (uint64_t)g.rows, (uint64_t)g.K, kTokBox)) != cudaSuccess) return e;
+  if ((e = make_tmap_rows128(&mW, g.b, 1, wrows, (uint64_t)g.K, kWRows)) != cudaSuccess) return e;
+  mW3 = mW;
+  if (kMats == 2 && (e = make_tmap_rows128(&mW3, g.b3, 1, wrows, (uint64_t)g.K, kWRows)) != cudaSuccess) return e;
+  const int64_t clusters = num_sms / f.split, most = (g.rows / f.tok + owners) * nblk;  // no more units than that
+  const int grid = (int)(clusters < most ? clusters : most) * f.split;
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, pdl, f.split, mX, mW, mW3, g, ws, seg_counts, f,
+                       timeout_ns);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_few(int kind, const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first,
+                            int device, int num_sms, int64_t timeout_ns, bool pdl, cudaStream_t st) {
+  switch (kind) {
+    case kSwiGLU: return launch_kind<kSwiGLU>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, pdl, st);
+    case kOutBf16: return launch_kind<kOutBf16>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, pdl, st);
+    default: return launch_kind<kOutF32>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, pdl, st);
+  }
+}
+
+}  // namespace fp8
+}  // namespace moe

@@ -38,6 +38,7 @@
 #include <atomic>
 
 #include "fp8_common.cuh"
+#include "fp8_mma.cuh"
 #include "gemm_tc.h"
 #include "tc_ptx.cuh"
 #include "tmap.h"
@@ -125,42 +126,6 @@ __device__ __forceinline__ bool pair_bar_and(int id, bool v) {
       : "r"(id), "r"((uint32_t)v)
       : "memory");
   return r != 0;
-}
-
-// Instruction descriptor of kind::mxf8f6f4 with e4m3 A and B (both K-major), e8m0 factors, fp32
-// D: bits 4-5 B's factor byte, 7-9 / 10-12 the types (0 = e4m3), 17-22 N >> 3, 23 factor type
-// (1 = e8m0), 24-28 M >> 4, 29-30 A's factor byte.
-__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, uint32_t byte) {
-  return (byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | (byte << 29);
-}
-
-// One more in either factor byte.
-__host__ __device__ constexpr uint32_t idesc_byte() { return (1u << 4) | (1u << 29); }
-
-// True in one lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
-__device__ __forceinline__ void mma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
-}
-
-// This lane's words to 12 columns of its warp's TMEM lane quarter.
-__device__ __forceinline__ void tmem_st_factors(uint32_t taddr, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %5, %5, %5};" ::"r"(taddr), "r"(a[0]),
-               "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0)
-               : "memory");
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr + 8), "r"(b1) : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 template <int kRegs>
@@ -400,7 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       ptx::tc_fence_after();
-      tmem_st_factors(dst + set * kSfStep, w, w0, w1);
+      tmem_st_x4(dst + set * kSfStep, w[0], w[1], w[2], w[3]);
+      tmem_st_x4(dst + set * kSfStep + 4, w0, w0, w0, w0);
+      tmem_st_x4(dst + set * kSfStep + 8, w1, w1, w1, w1);
+      tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->sf_full[set]), 0));

@@ -166,7 +166,7 @@ moe_status product(moe_fp8_plan_t plan, int kind, const fp8::GemmArgs& g, const 
                    cudaStream_t st, const char* what) {
   cudaError_t e;
   if (plan->few)
-    e = fp8::launch_gemm_few(kind, g, ws, seg_counts, plan->n_seg, first, plan->device, plan->num_sms, plan->timeout_ns, !first, st);
+    e = fp8::launch_gemm_few(kind, g, ws, seg_counts, plan->n_seg, first, plan->device, plan->num_sms, plan->timeout_ns, true, st);
   else if (plan->tc)
     e = fp8::launch_gemm_tc(kind, g, ws, plan->device, plan->num_sms, plan->timeout_ns, true, st);
   else

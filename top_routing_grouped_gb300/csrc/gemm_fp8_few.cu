@@ -60,12 +60,11 @@ struct Ctl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int bad;
-  uint32_t top[2][4][32];        // epilogue: largest hidden value of each warp and row
+  uint32_t top[2][4][8];         // epilogue: largest hidden value of each warp and row
   int row0[kMaxExperts + 1];     // first row of each segment
   int unit0[kMaxExperts + 1];    // first unit of each segment
   int64_t row_tot[8];  // the scans' warp totals
-  int unit_tot[8];
+  uint32_t unit_tot[8];
 };
 
 // The launch's sizes, chosen on the host.
@@ -113,6 +112,13 @@ __device__ __forceinline__ bool epi_bar_and(bool v) {
   return r != 0;
 }
 
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
+
 struct Unit {
   int e;       // weight expert
   int n0;      // first weight row of the block
@@ -137,22 +143,6 @@ __device__ __forceinline__ Unit decode(const Ctl* ctl, const FewShape& f, int E,
   r.row0 = ctl->row0[lo] + g0;
   r.rows = min(f.tok, cnt - g0);
   return r;
-}
-
-// Inclusive scan over the first 256 threads (all threads call it).
-template <typename T>
-__device__ __forceinline__ T scan256(T v, T* warp_tot) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
-  }
-  if (warp < 8 && lane == 31) warp_tot[warp] = v;
-  __syncthreads();
-  for (int w = 0; w < 8; ++w)
-    if (w < warp) v += warp_tot[w];
-  return v;
 }
 
 template <int kKind>
@@ -191,7 +181,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(ptx::smem_u32(&ctl->rfree), 4);
     ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
-    ctl->bad = 0;
     ptx::fence_mbar_init();
     ptx::tma_prefetch_desc(&tmX);
     ptx::tma_prefetch_desc(&tmW);
@@ -206,27 +195,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   if (f.split > 1) ptx::cluster_sync();  // every CTA's barriers exist before another arrives on them
-  pdl_wait();  // the activations (and the counts) come from earlier kernels
+  // The call's first launch waits here for the counts and the activations.  Its second one starts
+  // when the first does (as far as SMs are free): the counts are there then, and only what the first
+  // launch computes, the hidden rows and their factors, is waited for where it is read.
+  if (f.first) pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the segments' first rows and units
+  // ---- the segments' first rows and units: inclusive scans over the first 256 threads
   int total;
   {
     const int i = threadIdx.x;
     const int cnt = i < f.n_seg ? (seg_counts ? seg_counts[i] : (int)g.rows) : 0;
-    if (cnt < 0) ctl->bad = 1;
-    const int64_t rows = scan256((int64_t)cnt, ctl->row_tot);  // 64 bits: bad counts may sum to anything
-    if (i == f.n_seg - 1 && rows > g.rows) ctl->bad = 1;
+    int64_t rows = cnt < 0 ? (int64_t)1 << 40 : cnt;  // 64 bits: bad counts may sum to anything
+    uint32_t units = ((uint32_t)cnt + f.tok - 1) / f.tok * nblk;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, rows, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, units, o);
+      if (lane >= o) {
+        rows += x;
+        units += y;
+      }
+    }
+    if (warp < 8 && lane == 31) {
+      ctl->row_tot[warp] = rows;
+      ctl->unit_tot[warp] = units;
+    }
     __syncthreads();
-    const bool bad = ctl->bad != 0;
-    const int units = scan256(bad ? 0 : (cnt + f.tok - 1) / f.tok * nblk, ctl->unit_tot);
+    int64_t all = 0;
+    for (int w = 0; w < 8; ++w) {
+      if (w < warp) {
+        rows += ctl->row_tot[w];
+        units += ctl->unit_tot[w];
+      }
+      all += ctl->row_tot[w];
+    }
+    const bool bad = all > g.rows;
     if (i < kMaxExperts) {
-      ctl->row0[i + 1] = bad ? 0 : (int)rows;
-      ctl->unit0[i + 1] = units;
+      ctl->row0[i + 1] = (int)rows;
+      ctl->unit0[i + 1] = (int)units;
     }
     if (i == 0) ctl->row0[0] = ctl->unit0[0] = 0;
     __syncthreads();
-    total = ctl->unit0[f.n_seg];
+    total = bad ? 0 : ctl->unit0[f.n_seg];
     if (f.first && blockIdx.x == 0 && i == 0) {
       ws.hdr[kHdrWhere] = bad ? 0x950u : 0u;
       ws.hdr[kHdrStatus] = bad ? (uint32_t)MOE_ERR_INTERNAL : 0u;
@@ -237,30 +248,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------- TMA producer
+      // A fill is a K block of a unit.  The second launch of a call requests the weights of its
+      // first ring of fills before the first launch has ended, and the activations after.
+      struct Cursor {
+        int u, kb;
+        Unit un;
+      };
+      auto at = [&](int u) {
+        Cursor c{u, kb0, Unit{}};
+        if (u < total) c.un = decode(ctl, f, g.E, u);
+        return c;
+      };
+      auto next = [&](Cursor& c) {
+        if (++c.kb == kb1) c = at(c.u + ncl);
+      };
+      auto fill_weights = [&](const Cursor& c, int stage) {
+        const int boxes = (c.un.rows + kTokBox - 1) / kTokBox, wrow = c.un.e * g.n + c.un.n0;
+        const uint32_t bar = ptx::smem_u32(&ctl->full[stage]), s = ptx::smem_u32(stages + (size_t)stage * f.stage_bytes);
+        ptx::mbar_arrive_expect_tx(bar, (uint32_t)(kMats * kWBytes + boxes * kTokBox * kBK));
+        ptx::tma_load_2d(s, &tmW, c.kb * kBK, wrow, bar);
+        if (kMats == 2) ptx::tma_load_2d(s + kWBytes, &tmW3, c.kb * kBK, wrow, bar);
+      };
+      auto fill_rows = [&](const Cursor& c, int stage) {
+        const int boxes = (c.un.rows + kTokBox - 1) / kTokBox;
+        const uint32_t bar = ptx::smem_u32(&ctl->full[stage]), s = ptx::smem_u32(stages + (size_t)stage * f.stage_bytes);
+        for (int b = 0; b < boxes; ++b)
+          ptx::tma_load_2d(s + kMats * kWBytes + b * kTokBox * kBK, &tmX, c.kb * kBK, c.un.row0 + b * kTokBox, bar);
+      };
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = cid; u < total && ok; u += ncl) {
-        const Unit un = decode(ctl, f, g.E, u);
-        const int boxes = (un.rows + kTokBox - 1) / kTokBox;
-        const uint32_t bytes = (uint32_t)(kMats * kWBytes + boxes * kTokBox * kBK);
-        const int wrow = un.e * g.n + un.n0;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!ptx::mbar_wait(ptx::smem_u32(&ctl->empty[stage]), phase ^ 1u, timeout_ns, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = ptx::smem_u32(&ctl->full[stage]);
-          const uint32_t s = ptx::smem_u32(stages + (size_t)stage * f.stage_bytes);
-          ptx::mbar_arrive_expect_tx(bar, bytes);
-          ptx::tma_load_2d(s, &tmW, kb * kBK, wrow, bar);
-          if (kMats == 2) ptx::tma_load_2d(s + kWBytes, &tmW3, kb * kBK, wrow, bar);
-          for (int b = 0; b < boxes; ++b)
-            ptx::tma_load_2d(s + kMats * kWBytes + b * kTokBox * kBK, &tmX, kb * kBK, un.row0 + b * kTokBox, bar);
-          if (++stage == f.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+      Cursor c = at(cid);
+      if (!f.first) {
+        int ahead = 0;
+        for (Cursor w = c; ahead < f.stages && w.u < total; ++ahead, next(w)) fill_weights(w, ahead);
+        pdl_wait();
+        for (; stage < ahead; ++stage, next(c)) fill_rows(c, stage);
+        if (stage == f.stages) {
+          stage = 0;
+          phase = 1;
+        }
+      }
+      while (c.u < total) {
+        if (!ptx::mbar_wait(ptx::smem_u32(&ctl->empty[stage]), phase ^ 1u, timeout_ns, abort_flag)) {
+          ok = false;
+          break;
+        }
+        fill_weights(c, stage);
+        fill_rows(c, stage);
+        next(c);
+        if (++stage == f.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
       if (!ok) {
@@ -333,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_wait(ctl0 + offsetof(Ctl, drain), 0u, timeout_ns, nullptr);
   } else if (warp >= kSfWarp0) {
     // ------------------------------------------------------------ block factors
+    if (!f.first) pdl_wait();  // those of the hidden rows
     const uint32_t* sx32 = reinterpret_cast<const uint32_t*>(g.sa);
     const uint32_t* sw32 = reinterpret_cast<const uint32_t*>(g.sb);
     const uint32_t* sw3_32 = reinterpret_cast<const uint32_t*>(kMats == 2 ? g.sb3 : g.sb);
@@ -411,12 +451,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this CTA's sums to the first CTA
         const uint32_t dst = ptx::mapa(ptx::smem_u32(recv), 0) + (uint32_t)(((int)rank - 1) * f.recv_bytes + m * 4);
         for (int mt = 0; mt < kMats; ++mt)
-          for (int c = 0; c < un.rows; c += 32) {
-            uint32_t v[32];
-            ptx::tmem_ld_32cols(t_row + 64 * mt + c, v);
+#pragma unroll 1
+          for (int c = 0; c < un.rows; c += 8) {
+            uint32_t v[8];
+            tmem_ld_x8(t_row + 64 * mt + c, v);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 8; ++i)
               if (c + i < un.rows) st_cluster_f32(dst + (uint32_t)((mt * f.tok + c + i) * 512), v[i]);
           }
         ptx::tc_fence_before();
@@ -426,53 +467,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfull), 0));
         }
       } else {
-        auto load = [&](int mt, int c, uint32_t(&v)[32]) {
-          ptx::tmem_ld_32cols(t_row + 64 * mt + c, v);
+        // Eight rows at a time: code that is short enough to be fetched once (unrolled over 32 rows
+        // this part took 6 us for a single one, most of it instruction fetches).
+        auto load = [&](int mt, int c, float(&v)[8]) {
+          uint32_t w[8];
+          tmem_ld_x8(t_row + 64 * mt + c, w);
           ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+#pragma unroll 1
           for (int r = 0; r < f.split - 1; ++r)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i < un.rows)
-                v[i] = __float_as_uint(__uint_as_float(v[i]) + mine[r * recv_floats + (mt * f.tok + c + i) * 128]);
+            for (int i = 0; i < 8; ++i)
+              if (c + i < un.rows) v[i] += mine[r * recv_floats + (mt * f.tok + c + i) * 128];
         };
-        for (int c = 0; c < un.rows; c += 32) {
-          const int nt = min(32, un.rows - c);
+#pragma unroll 1
+        for (int c = 0; c < un.rows; c += 8) {
+          const int nt = un.rows - c;
           const int64_t p0 = (int64_t)un.row0 + c;
           if constexpr (kKind == kSwiGLU) {
-            uint32_t a[32], b[32];
+            float a[8], b[8];
             load(0, c, a);
             load(1, c, b);
             uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float h = silu_exact(__uint_as_float(a[i])) * __uint_as_float(b[i]);
-              a[i] = __float_as_uint(h);
-              if (i < nt) {  // the row's largest value over this warp's 32 columns, kept by lane i
-                const uint32_t t = __reduce_max_sync(0xffffffffu, in ? abs_bits(h) : 0u);
-                if (lane == i) top = t;
-              }
+            for (int i = 0; i < 8; ++i) {
+              a[i] = silu_exact(a[i]) * b[i];
+              // the row's largest value over this warp's 32 columns, kept by lane i
+              const uint32_t t = __reduce_max_sync(0xffffffffu, in ? abs_bits(a[i]) : 0u);
+              if (lane == i) top = t;
             }
-            ctl->top[turn][q][lane] = top;
+            if (lane < 8) ctl->top[turn][q][lane] = top;
             epi_bar_and(true);
-            const uint32_t* o = &ctl->top[turn][0][lane];
-            top = max(max(o[0], o[32]), max(o[64], o[96]));
+            const uint32_t* o = &ctl->top[turn][0][lane & 7];
+            top = max(max(o[0], o[8]), max(o[16], o[24]));
             turn ^= 1;
             const uint32_t sb = scale_byte(__uint_as_float(top));
             const float fac = inv_scale_value(sb);
-            if (q == 0 && lane < nt) g.out_scales[(p0 + lane) * scale_cols(g.n) + un.n0 / kBlock] = (uint8_t)sb;
+            if (q == 0 && lane < min(nt, 8)) g.out_scales[(p0 + lane) * scale_cols(g.n) + un.n0 / kBlock] = (uint8_t)sb;
             uint8_t* out = reinterpret_cast<uint8_t*>(g.out) + p0 * g.n + col;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const float fi = __shfl_sync(0xffffffffu, fac, i);
-              if (i < nt && in) out[(int64_t)i * g.n] = (uint8_t)pack_e4m3x2(__uint_as_float(a[i]) * fi, 0.f);
+              if (i < nt && in) out[(int64_t)i * g.n] = (uint8_t)pack_e4m3x2(a[i] * fi, 0.f);
             }
           } else {
-            uint32_t v[32];
+            float v[8];
             load(0, c, v);
-            const float gate = g.gate && lane < nt ? g.gate[p0 + lane] : 1.f;
+            const float gate = g.gate && lane < min(nt, 8) ? g.gate[p0 + lane] : 1.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float y = __shfl_sync(0xffffffffu, gate, i) * __uint_as_float(v[i]);
+            for (int i = 0; i < 8; ++i) {
+              const float y = __shfl_sync(0xffffffffu, gate, i) * v[i];
               if (i < nt && in) store_act(g.out, kKind == kOutBf16, (p0 + i) * g.n + col, y);
             }
           }
@@ -481,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(ptx::smem_u32(&ctl->tempty[acc]));
-          for (int r = 1; r < f.split; ++r) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfree), (uint32_t)r));
+          if (u + ncl < total)  // the others do not wait for this after their last unit
+            for (int r = 1; r < f.split; ++r) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfree), (uint32_t)r));
         }
       }
       if (++acc == 2) {
@@ -506,7 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (f.split > 1) ptx::cluster_sync();  // no CTA's shared memory goes while another may still write to it
+  // No CTA's shared memory goes while another may still write to it: nobody writes to one of the others
+  // that has finished all its units, so those leave (and make room for the next launch) at once.
+  if (f.split > 1 && (rank == 0 || *abort_flag)) ptx::cluster_sync();
   if (warp == 2) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);

@@ -262,6 +262,10 @@ PRODUCTS = [  # segments' rows, E, K, N
     ([300], 1, 1024, 1040), ([2177], 1, 144, 96), ([0, 5, 0, 130, 1], 5, 256, 160), ([0, 0, 0], 3, 64, 64),
     ([3, 0, 7, 40, 1, 0, 0, 200], 4, 528, 144),  # two sources
     ([257, 31, 33, 32], 4, 384, 512),
+    # more than one unit of work for each SM: the CTA-pair kernels on the "auto" path
+    ([1300], 1, 272, 2064), ([129, 0, 700, 300, 1], 5, 528, 1168), ([40, 128, 257, 3, 900, 255], 3, 2064, 816),
+    # more units than clusters, one of them with every kind of short group
+    ([65, 17, 0, 1, 64, 33, 16, 15], 8, 1552, 2320),
 ]
 
 
@@ -352,6 +356,7 @@ def test_bad_counts_are_reported_and_compute_nothing(fp8, path, seg):
 EXPERTS = [  # segments' rows, E, d, F
     ([1], 1, 16, 16), ([1, 1, 0, 1, 1], 5, 512, 256), ([0, 0, 0, 0], 2, 64, 64), ([130, 0, 257, 64], 4, 256, 272),
     ([33, 128, 0, 3, 300, 1], 3, 400, 144), ([2100], 1, 128, 400), ([20, 31, 32, 33, 0, 200, 90, 64], 8, 1024, 640),
+    ([900, 0, 257, 300], 4, 272, 1168), ([700, 33, 128, 1, 0, 513], 3, 1168, 400),  # CTA pairs on "auto"
 ]
 
 

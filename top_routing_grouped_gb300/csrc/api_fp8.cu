@@ -89,11 +89,17 @@ moe_status bind_device(moe_fp8_plan_t plan) {
   return MOE_OK;
 }
 
-// Rows a segment on average, up to which the kernels that make the weights the MMA's rows are used.
-#ifndef FEW_ROWS
-#define FEW_ROWS 64
-#endif
-constexpr int64_t kFewRows = FEW_ROWS;
+// Which tensor-core kernels.  Those that make the weights the MMA's rows read each weight tile once for
+// every 64 rows of a segment; the CTA pairs take 256 rows at the price of one.  Measured (experts;
+// time of the pairs / time of the others): 16 and 32 rows a segment 1.2-1.3 at every shape, 64 rows
+// 0.9 (8 experts of 8192) to 1.1 (32 of 2048), 128 rows 0.66-0.75.  With few segments the pairs also
+// leave SMs idle: dense products K x n of 2048 x 2048, 4096 x 4096 and 2048 x 8192 cross where the
+// others have more than one unit of work for each SM (1.5, 1.2 and 1.5 at 128 units; 0.94, 0.69 and
+// 0.96 at 192 to 256).
+bool use_few(int64_t rows, int64_t n_seg, int64_t widest_out) {
+  const int64_t blocks = (widest_out + 127) / 128;
+  return rows <= 48 * n_seg || ((rows + 63) / 64 + n_seg - 1) * blocks <= 152;
+}
 
 moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E, int32_t W, int32_t out_dtype,
                      int32_t path, int64_t timeout_ns, moe_fp8_plan_t* plan, size_t* workspace_bytes) {
@@ -113,7 +119,7 @@ moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E
   if (!p) return fail(MOE_ERR_INTERNAL, "out of host memory");
   p->experts = experts;
   p->tc = tc;
-  p->few = tc && rows <= kFewRows * (int64_t)E * W;
+  p->few = tc && use_few(rows, (int64_t)E * W, experts && k > n ? k : n);
   p->rows = rows;
   p->k = k;
   p->n = n;

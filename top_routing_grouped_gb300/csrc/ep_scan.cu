@@ -26,6 +26,8 @@ __global__ void __launch_bounds__(kSegThreads) seg_scan_kernel(Shape s, Ws ws, c
   __shared__ int cnt_s[kMaxExperts], offs_s[kMaxExperts];
   __shared__ int scratch[kTileScratchInts];
   const int i = threadIdx.x;
+  pdl_wait();  // earlier kernels may still read the tables and write the counts
+  pdl_launch_dependents();
   if (clear && i < kHdrClearWords) ws.hdr[i] = 0u;  // ordered before record_error by the barrier below
   int cnt = i < n_seg ? (seg_counts ? seg_counts[i] : (int)s.N) : 0;
   // a negative count, or a sum above the capacity (taken in 64 bits: it could wrap in 32)
@@ -49,7 +51,7 @@ __global__ void __launch_bounds__(kSegThreads) seg_scan_kernel(Shape s, Ws ws, c
 
 cudaError_t launch_seg_scan(const Shape& s, const Ws& ws, const int32_t* seg_counts, int n_seg, int n_local,
                             bool clear, cudaStream_t st) {
-  return launch_kernel(seg_scan_kernel, dim3(1), dim3(kSegThreads), 0, st, false, 1, s, ws, seg_counts, n_seg, n_local,
+  return launch_kernel(seg_scan_kernel, dim3(1), dim3(kSegThreads), 0, st, clear, 1, s, ws, seg_counts, n_seg, n_local,
                        clear ? 1 : 0);
 }
 

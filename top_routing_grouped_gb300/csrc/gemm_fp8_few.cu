@@ -14,7 +14,7 @@
 // shares a unit: each sums a part of K, and the first CTA adds the others' sums, which arrive in
 // its shared memory, in rank order.
 //
-// Roles of a CTA: a TMA thread (ring of stages), an MMA warp (one elected lane issues), four
+// Roles of a CTA: a TMA thread (ring of stages), an MMA warp (one elected lane issues), eight
 // epilogue warps and four warps that store the block factors to TMEM, as in gemm_fp8_tc.cu.  Waits are
 // bounded (MOE_ERR_TIMEOUT, no trap).
 #include <cuda.h>
@@ -40,9 +40,9 @@ constexpr int kMaxTok = 64;           // activation rows per unit
 constexpr int kTokBox = 16;           // rows of one TMA box of activations
 constexpr int kWBytes = kWRows * kBK;
 constexpr int kMaxStages = 12;
-constexpr int kThreads = 384;
-constexpr int kEpiWarp0 = 4, kSfWarp0 = 8;
-constexpr int kEpiBar = 1;            // named barrier of the four epilogue warps
+constexpr int kThreads = 512;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;  // two sets of four warps take turns with the rows, eight at a time
+constexpr int kSfWarp0 = 12;
 
 // TMEM columns: accumulator (buffer b, matrix m) at 128 b + 64 m; factor set i at 256 + 16 i
 // (4 of W1 or W, 4 of W3, 4 of the activations)
@@ -60,7 +60,7 @@ struct Ctl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  uint32_t top[2][4][8];         // epilogue: largest hidden value of each warp and row
+  uint32_t top[2][2][4][8];      // epilogue: [set][turn] largest hidden value of each warp and row
   int row0[kMaxExperts + 1];     // first row of each segment
   int unit0[kMaxExperts + 1];    // first unit of each segment
   int64_t row_tot[8];  // the scans' warp totals
@@ -98,8 +98,8 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Barrier of the 128 epilogue threads, with the AND of a flag over them.
-__device__ __forceinline__ bool epi_bar_and(bool v) {
+// Barrier of the 128 threads of an epilogue set, with the AND of a flag over them.
+__device__ __forceinline__ bool epi_bar_and(int set, bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -107,7 +107,7 @@ __device__ __forceinline__ bool epi_bar_and(bool v) {
       "barrier.cta.red.and.pred q, %1, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "n"(kEpiBar), "r"((uint32_t)v)
+      : "r"(1 + set), "r"((uint32_t)v)
       : "memory");
   return r != 0;
 }
@@ -171,14 +171,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(ptx::smem_u32(&ctl->tfull[i]), 1);
-      ptx::mbar_init(ptx::smem_u32(&ctl->tempty[i]), 4);
+      ptx::mbar_init(ptx::smem_u32(&ctl->tempty[i]), kEpiWarps);
     }
     for (int i = 0; i < kSfSets; ++i) {
       ptx::mbar_init(ptx::smem_u32(&ctl->sf_full[i]), 4);
       ptx::mbar_init(ptx::smem_u32(&ctl->sf_empty[i]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(&ctl->rfull), f.split > 1 ? 4 * (f.split - 1) : 1);
-    ptx::mbar_init(ptx::smem_u32(&ctl->rfree), 4);
+    ptx::mbar_init(ptx::smem_u32(&ctl->rfull), f.split > 1 ? kEpiWarps * (f.split - 1) : 1);
+    ptx::mbar_init(ptx::smem_u32(&ctl->rfree), kEpiWarps);
     ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
@@ -428,37 +428,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3, m = q * 32 + lane;  // weight row of the block
-    const float* mine = recv + m;               // the others' sums: [rank - 1][matrix][column][128 rows]
+    // A warp here runs alone on its scheduler for the most part, so what counts is the length of its
+    // instruction chain: rows eight at a time (short code, fetched once), two sets of warps.
+    const int q = warp & 3, set = (warp - kEpiWarp0) >> 2, m = q * 32 + lane;  // m: weight row of the block
+    const float* mine = recv + m;  // the others' sums: [rank - 1][matrix][row][128 weight rows]
     const int recv_floats = f.recv_bytes / 4;
+    const int64_t scn = scale_cols(g.n);
+    constexpr int kOsz = kKind == kSwiGLU ? 1 : kKind == kOutBf16 ? 2 : 4;
+    const int64_t pitch = (int64_t)g.n * kOsz;
     int acc = 0, turn = 0;
     uint32_t acc_phase = 0, r_phase = 0;
     bool ok = true;
     for (int u = cid; u < total; u += ncl) {
       const Unit un = decode(ctl, f, g.E, u);
+      const int col = un.n0 + m;
+      const bool in = col < g.n;
+      float gate0 = 1.f, gate1 = 1.f;  // of rows lane and lane + 32
+      if (kKind != kSwiGLU && rank == 0 && g.gate) {
+        if (lane < un.rows) gate0 = g.gate[un.row0 + lane];
+        if (lane + 32 < un.rows) gate1 = g.gate[un.row0 + lane + 32];
+      }
       ok = ptx::mbar_wait(ptx::smem_u32(&ctl->tfull[acc]), acc_phase, timeout_ns, abort_flag);
       if (f.split > 1)
         ok = ok && wait_cluster(ptx::smem_u32(rank == 0 ? &ctl->rfull : &ctl->rfree), rank == 0 ? r_phase : r_phase ^ 1u,
                                 timeout_ns, abort_flag);
-      ok = epi_bar_and(ok);  // the four warps go on or stop together
+      ok = epi_bar_and(set, ok);  // the set's four warps go on or stop together
       if (!ok) break;
       ptx::tc_fence_after();
       r_phase ^= 1u;
       const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 128);
-      const int col = un.n0 + m;
-      const bool in = col < g.n;
       if (rank != 0) {
-        // this CTA's sums to the first CTA
+        // this CTA's sums to the first CTA (rows past the unit's last fill the buffer, unread)
         const uint32_t dst = ptx::mapa(ptx::smem_u32(recv), 0) + (uint32_t)(((int)rank - 1) * f.recv_bytes + m * 4);
+#pragma unroll 1
         for (int mt = 0; mt < kMats; ++mt)
 #pragma unroll 1
-          for (int c = 0; c < un.rows; c += 8) {
+          for (int c = 8 * set; c < un.rows; c += 16) {
             uint32_t v[8];
             tmem_ld_x8(t_row + 64 * mt + c, v);
             ptx::tmem_ld_wait();
+            const uint32_t to = dst + (uint32_t)((mt * f.tok + c) * 512);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c + i < un.rows) st_cluster_f32(dst + (uint32_t)((mt * f.tok + c + i) * 512), v[i]);
+            for (int i = 0; i < 8; ++i) st_cluster_f32(to + 512 * i, v[i]);
           }
         ptx::tc_fence_before();
         __syncwarp();
@@ -467,58 +478,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfull), 0));
         }
       } else {
-        // Eight rows at a time: code that is short enough to be fetched once (unrolled over 32 rows
-        // this part took 6 us for a single one, most of it instruction fetches).
         auto load = [&](int mt, int c, float(&v)[8]) {
           uint32_t w[8];
           tmem_ld_x8(t_row + 64 * mt + c, w);
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+          const float* o = mine + (mt * f.tok + c) * 128;
 #pragma unroll 1
-          for (int r = 0; r < f.split - 1; ++r)
+          for (int r = 0; r < f.split - 1; ++r, o += recv_floats) {
+            float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c + i < un.rows) v[i] += mine[r * recv_floats + (mt * f.tok + c + i) * 128];
+            for (int i = 0; i < 8; ++i) x[i] = o[128 * i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += x[i];
+          }
         };
 #pragma unroll 1
-        for (int c = 0; c < un.rows; c += 8) {
+        for (int c = 8 * set; c < un.rows; c += 16) {
           const int nt = un.rows - c;
           const int64_t p0 = (int64_t)un.row0 + c;
+          uint8_t* out = reinterpret_cast<uint8_t*>(g.out) + p0 * pitch + (int64_t)col * kOsz;
           if constexpr (kKind == kSwiGLU) {
             float a[8], b[8];
             load(0, c, a);
             load(1, c, b);
             uint32_t top = 0;
 #pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] = silu_exact(a[i]) * b[i];
+#pragma unroll
             for (int i = 0; i < 8; ++i) {
-              a[i] = silu_exact(a[i]) * b[i];
               // the row's largest value over this warp's 32 columns, kept by lane i
               const uint32_t t = __reduce_max_sync(0xffffffffu, in ? abs_bits(a[i]) : 0u);
               if (lane == i) top = t;
             }
-            if (lane < 8) ctl->top[turn][q][lane] = top;
-            epi_bar_and(true);
-            const uint32_t* o = &ctl->top[turn][0][lane & 7];
+            if (lane < 8) ctl->top[set][turn][q][lane] = top;
+            epi_bar_and(set, true);
+            const uint32_t* o = &ctl->top[set][turn][0][lane & 7];
             top = max(max(o[0], o[8]), max(o[16], o[24]));
             turn ^= 1;
             const uint32_t sb = scale_byte(__uint_as_float(top));
             const float fac = inv_scale_value(sb);
-            if (q == 0 && lane < min(nt, 8)) g.out_scales[(p0 + lane) * scale_cols(g.n) + un.n0 / kBlock] = (uint8_t)sb;
-            uint8_t* out = reinterpret_cast<uint8_t*>(g.out) + p0 * g.n + col;
+            if (q == 0 && lane < min(nt, 8)) g.out_scales[(p0 + lane) * scn + un.n0 / kBlock] = (uint8_t)sb;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 8; ++i, out += pitch) {
               const float fi = __shfl_sync(0xffffffffu, fac, i);
-              if (i < nt && in) out[(int64_t)i * g.n] = (uint8_t)pack_e4m3x2(a[i] * fi, 0.f);
+              if (i < nt && in) *out = (uint8_t)pack_e4m3x2(a[i] * fi, 0.f);
             }
           } else {
             float v[8];
             load(0, c, v);
-            const float gate = g.gate && lane < min(nt, 8) ? g.gate[p0 + lane] : 1.f;
+            const float gates = c < 32 ? gate0 : gate1;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float y = __shfl_sync(0xffffffffu, gate, i) * v[i];
-              if (i < nt && in) store_act(g.out, kKind == kOutBf16, (p0 + i) * g.n + col, y);
+            for (int i = 0; i < 8; ++i, out += pitch) {
+              const float y = __shfl_sync(0xffffffffu, gates, (c + i) & 31) * v[i];
+              if (i < nt && in) store_act(out, kKind == kOutBf16, 0, y);
             }
           }
         }
@@ -552,9 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  // No CTA's shared memory goes while another may still write to it: nobody writes to one of the others
-  // that has finished all its units, so those leave (and make room for the next launch) at once.
-  if (f.split > 1 && (rank == 0 || *abort_flag)) ptx::cluster_sync();
+  // No CTA's shared memory goes while another may still write to it.  After an undisturbed run none
+  // does: the first CTA has received every sum, and the others have used every release but the last
+  // unit's, which is not sent; so they leave at once and make room for the next launch.
+  if (f.split > 1 && *abort_flag) ptx::cluster_sync();
   if (warp == 2) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);

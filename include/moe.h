@@ -69,6 +69,8 @@ typedef enum { MOE_PATH_AUTO = 0, MOE_PATH_SIMT = 1, MOE_PATH_TC_1SM = 2 } moe_p
 #define MOE_FLAG_TRAINING 8u     /* the forward also keeps what moe_backward needs (the two
                                     pre-activations of every routed row and the router softmax);
                                     bf16 tensor-core plans with bf16 output */
+#define MOE_FLAG_FP8_EXPERTS 16u /* the experts run in 8 bits (moe_fp8_forward in moe_fp8.h); bf16
+                                    inputs, MOE_PATH_AUTO, inference */
 #define MOE_FLAG_RENORM_GATES 4u /* variant: gates renormalised over the k chosen experts
                                     (gate[t,j] = p[t,idx[t,j]] / sum_j' p[t,idx[t,j']]) */
 

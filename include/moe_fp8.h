@@ -120,6 +120,16 @@ moe_status moe_fp8_expert_forward(moe_fp8_plan_t plan, const int32_t* seg_counts
                                   const void* w3, const uint8_t* w3_scales, const void* w2, const uint8_t* w2_scales,
                                   void* y_rows, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The whole layer with its experts in 8 bits, for a plan made by moe_plan with
+ * MOE_FLAG_FP8_EXPERTS: the router on x (bf16 [T, d]), the dispatch of the 8-bit rows x_q [T, d]
+ * with factors x_scales [T, moe_fp8_scale_cols(d)] (moe_rmsnorm writes both out of one read),
+ * the experts as in moe_fp8_expert_forward, and the combine into y [T, d] in the plan's
+ * out_dtype.  The workspace's views are those of moe_forward, but that xp and h hold e4m3. */
+moe_status moe_fp8_forward(moe_plan_t plan, const void* x, const void* x_q, const uint8_t* x_scales, const void* w_router,
+                           const float* router_bias, const void* w1, const uint8_t* w1_scales, const void* w3,
+                           const uint8_t* w3_scales, const void* w2, const uint8_t* w2_scales, void* y, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 void moe_fp8_plan_destroy(moe_fp8_plan_t plan);
 
 /* SYNCHRONISES `stream`, then reads the workspace's status word (as moe_get_device_status). */
@@ -135,6 +145,11 @@ moe_status moe_fp8_get_device_status(moe_fp8_plan_t plan, const void* workspace,
 moe_status moe_checkpoint_save_rows(const void* a, const void* b, int64_t rows, int32_t F, void* qa, uint8_t* sa,
                                     void* qb, uint8_t* sb, void* stream);
 
+/* The values that a checkpoint holds, a and b (exact in bf16), and h = silu(a) * b; outputs
+ * [rows, F] bf16, each NULL if not wanted. */
+moe_status moe_checkpoint_restore_rows(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb, int64_t rows,
+                                       int32_t F, void* a, void* b, void* h, void* stream);
+
 /* The SwiGLU's backward out of the checkpoint, with a, b the values it holds:
  *   da = dh * b * silu'(a),  db = dh * silu(a),  h = silu(a) * b
  * dh, da, db, h [rows, F] bf16, computed in fp32 and rounded once.  h (for the gradient of
@@ -142,6 +157,20 @@ moe_status moe_checkpoint_save_rows(const void* a, const void* b, int64_t rows, 
 moe_status moe_checkpoint_backward_rows(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb,
                                         const void* dh, int64_t rows, int32_t F, void* da, void* db, void* h,
                                         void* stream);
+
+/* Checkpoints of a training layer: L layers of one shape train with one workspace and L
+ * checkpoints, each a little over a quarter of what a forward leaves in the workspace for
+ * moe_backward.  After moe_forward, moe_checkpoint_save copies the routing and the router
+ * softmax and quantises the pre-activations; before moe_backward, moe_checkpoint_restore puts
+ * them back, rebuilds the hidden rows from them and the dispatched rows from x (the forward's
+ * input).  The backward is then that of the layer with the pre-activations as they were kept.
+ * moe_checkpoint_bytes: 0 for a plan without MOE_FLAG_TRAINING.  Checkpoint and workspace are
+ * 256-byte aligned device memory; both calls are asynchronous on `stream`. */
+size_t moe_checkpoint_bytes(moe_plan_t plan);
+moe_status moe_checkpoint_save(moe_plan_t plan, const void* workspace, size_t workspace_bytes, void* checkpoint,
+                               size_t checkpoint_bytes, void* stream);
+moe_status moe_checkpoint_restore(moe_plan_t plan, const void* x, const void* checkpoint, size_t checkpoint_bytes,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

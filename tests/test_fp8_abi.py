@@ -153,6 +153,14 @@ def test_checkpoint_refusals(fp8):
         b[i] = None
         if i < 7:  # h may be missing
             assert L.moe_checkpoint_backward_rows(*b[:5], 4, 64, *b[5:], None) == INVALID, i
+    for i in range(7):
+        b = list(A[:7])
+        b[i] = P(4104)
+        assert L.moe_checkpoint_restore_rows(*b[:4], 4, 64, *b[4:], None) == INVALID, i
+        b[i] = None
+        if i < 4:
+            assert L.moe_checkpoint_restore_rows(*b[:4], 4, 64, *b[4:], None) == INVALID, i
+    assert L.moe_checkpoint_restore_rows(*A[:4], 4, 64, None, None, None, None) == INVALID
     assert L.moe_checkpoint_save_rows(*A[:2], -1, 64, *A[2:6], None) == INVALID
     assert L.moe_checkpoint_save_rows(*A[:2], 4, 0, *A[2:6], None) == INVALID
 
@@ -177,3 +185,49 @@ def test_binding_checks_types_shapes_and_layouts(fp8):
     plan = fp8.Fp8MatmulPlan(4, 64, 32)
     with pytest.raises(ValueError):
         plan.forward(None, q, s, torch.zeros(1, 32, 64).to(fp8.E4M3), s, torch.zeros(4, 32), torch.zeros(1 << 16, dtype=torch.uint8))
+
+
+def test_layer_plan_and_forward_refusals(fp8):
+    from top_routing_grouped_gb300 import moe
+    L = fp8._lib
+    p = fp8.Fp8MoEPlan(64, 128, 8, 2, 128)
+    p16 = moe.MoEPlan(64, 128, 8, 2, 128)
+    assert p.workspace_bytes < p16.workspace_bytes
+    n = p.workspace_bytes
+
+    def call(args, h=p.handle, ws=A[14], n=n, bias=None):
+        return L.moe_fp8_forward(h, *args[:4], bias, *args[4:], ws, n, None)
+
+    for i in range(11):
+        b = list(A[:11])
+        b[i] = None
+        assert call(b) == INVALID, i
+        b[i] = P(4104)
+        assert call(b) == INVALID, i
+    good = list(A[:11])
+    assert call(good, h=p16.handle) == INVALID and call(good, h=None) == INVALID
+    assert call(good, ws=None) == INVALID and call(good, ws=P(4224)) == INVALID and call(good, n=n - 1) == INVALID
+    pb = fp8.Fp8MoEPlan(64, 128, 8, 2, 128, has_bias=True)
+    assert call(good, h=pb.handle, n=pb.workspace_bytes) == INVALID
+    # the bf16 entry points turn an 8-bit plan down
+    assert L.moe_forward(p.handle, A[0], A[1], None, A[2], A[3], A[4], A[5], A[6], n, None) == INVALID
+    for kw in (dict(dtype="f32"), dict(path="simt"), dict(path="tc1"), dict(training=True), dict(test_stall=True)):
+        with pytest.raises(moe.MoEError, match="UNSUPPORTED"):
+            moe.MoEPlan(64, 128, 8, 2, 128, **{"dtype": "bf16", **kw}, fp8_experts=True)
+
+
+def test_layer_checkpoint_refusals(fp8):
+    from top_routing_grouped_gb300 import moe
+    L = fp8._lib
+    plain, p = moe.MoEPlan(64, 128, 8, 2, 128), moe.MoEPlan(64, 128, 8, 2, 128, training=True)
+    assert L.moe_checkpoint_bytes(None) == 0 and L.moe_checkpoint_bytes(plain.handle) == 0
+    c, n = L.moe_checkpoint_bytes(p.handle), p.workspace_bytes
+    assert 2 * 64 * 2 * 128 < c < n
+    save = lambda h=p.handle, ws=A[0], n=n, ck=A[1], c=c: L.moe_checkpoint_save(h, ws, n, ck, c, None)
+    load = lambda h=p.handle, x=A[2], ws=A[0], n=n, ck=A[1], c=c: L.moe_checkpoint_restore(h, x, ck, c, ws, n, None)
+    for f in (save, load):
+        for kw in (dict(h=None), dict(h=plain.handle), dict(ws=None), dict(ws=P(4224)), dict(n=n - 1), dict(ck=None),
+                   dict(ck=P(4224)), dict(c=c - 1)):
+            assert f(**kw) == INVALID, kw
+    with pytest.raises(ValueError, match="training"):
+        fp8.LayerCheckpoint(plain, device="cpu")

@@ -10,6 +10,7 @@
 #include <string>
 
 #include "moe_internal.h"
+#include "fp8_internal.h"
 #include "gemm_bwd.h"
 #include "gemm_tc.h"
 
@@ -87,6 +88,7 @@ WsLayout ws_layout(const Shape& s) {
     return at;
   };
   const size_t esz = s.act_bf16 ? 2 : 4;
+  const size_t rsz = s.fp8 ? 1 : esz;  // xp and h
   const size_t N = (size_t)s.N, E = (size_t)s.E, nb = (size_t)s.nblk;
   L.hdr = take(64 * sizeof(uint32_t));
   L.aux = take(sizeof(float));
@@ -106,9 +108,13 @@ WsLayout ws_layout(const Shape& s) {
   L.gate_perm = take(N * 4);
   L.slot_pos = take(N * 4);
   L.logits = s.keep_logits ? take((size_t)s.T * E * 4) : 0;
-  L.xp = take(N * (size_t)s.d * esz);
-  L.h = take(N * (size_t)s.F * esz);
+  L.xp = take(N * (size_t)s.d * rsz);
+  L.h = take(N * (size_t)s.F * rsz);
   L.yp = take(N * (size_t)s.d * esz);
+  if (s.fp8) {
+    L.xs = take(N * (size_t)fp8::scale_cols(s.d));
+    L.hs = take(N * (size_t)fp8::scale_cols(s.F));
+  }
   if (s.training) {
     const size_t nt = 2 * (((size_t)s.F + 255) / 256), chunks = (size_t)dwr_chunks(s);
     L.a1 = take(N * (size_t)s.F * 2);
@@ -156,6 +162,10 @@ Ws ws_bind(const Shape& s, void* base) {
   w.xp = b + L.xp;
   w.h = b + L.h;
   w.yp = b + L.yp;
+  if (s.fp8) {
+    w.xs = reinterpret_cast<uint8_t*>(b + L.xs);
+    w.hs = reinterpret_cast<uint8_t*>(b + L.hs);
+  }
   if (s.training) {
     w.a1 = b + L.a1;
     w.a3 = b + L.a3;
@@ -239,7 +249,8 @@ moe_status moe_plan(const moe_config* cfg, moe_plan_t* plan, size_t* workspace_b
   if (c.has_router_bias != 0 && c.has_router_bias != 1) return fail(MOE_ERR_INVALID_ARG, "has_router_bias must be 0 or 1");
   if (c.path != MOE_PATH_AUTO && c.path != MOE_PATH_SIMT && c.path != MOE_PATH_TC_1SM)
     return fail(MOE_ERR_INVALID_ARG, "bad path");
-  if (c.flags & ~(MOE_FLAG_KEEP_LOGITS | MOE_FLAG_TEST_STALL | MOE_FLAG_RENORM_GATES | MOE_FLAG_TRAINING))
+  if (c.flags & ~(MOE_FLAG_KEEP_LOGITS | MOE_FLAG_TEST_STALL | MOE_FLAG_RENORM_GATES | MOE_FLAG_TRAINING |
+                  MOE_FLAG_FP8_EXPERTS))
     return fail(MOE_ERR_INVALID_ARG, "unknown flags");
   const int64_t N = c.T * (int64_t)c.top_k;
   if (N > (int64_t)INT32_MAX / 2 || N * (int64_t)(c.d_model > c.d_expert ? c.d_model : c.d_expert) > ((int64_t)1 << 40))
@@ -255,6 +266,10 @@ moe_status moe_plan(const moe_config* cfg, moe_plan_t* plan, size_t* workspace_b
     return fail(MOE_ERR_INVALID_ARG, "MOE_FLAG_TEST_STALL applies to the tensor-core path only");
   if ((c.flags & MOE_FLAG_TRAINING) && (!tc || c.out_dtype != MOE_BF16))
     return fail(MOE_ERR_UNSUPPORTED, "MOE_FLAG_TRAINING needs the tensor-core path (bf16 inputs) and bf16 output");
+  if ((c.flags & MOE_FLAG_FP8_EXPERTS) && (!bf16 || c.path != MOE_PATH_AUTO))
+    return fail(MOE_ERR_UNSUPPORTED, "MOE_FLAG_FP8_EXPERTS needs bf16 inputs and MOE_PATH_AUTO");
+  if ((c.flags & MOE_FLAG_FP8_EXPERTS) && (c.flags & (MOE_FLAG_TRAINING | MOE_FLAG_TEST_STALL)))
+    return fail(MOE_ERR_UNSUPPORTED, "MOE_FLAG_FP8_EXPERTS is for inference: not with MOE_FLAG_TRAINING or MOE_FLAG_TEST_STALL");
 
   moe_plan_s* p = new (std::nothrow) moe_plan_s();
   if (!p) return fail(MOE_ERR_INTERNAL, "out of host memory");
@@ -272,6 +287,7 @@ moe_status moe_plan(const moe_config* cfg, moe_plan_t* plan, size_t* workspace_b
   s.keep_logits = (c.flags & MOE_FLAG_KEEP_LOGITS) ? 1 : 0;
   s.renorm = (c.flags & MOE_FLAG_RENORM_GATES) ? 1 : 0;
   s.training = (c.flags & MOE_FLAG_TRAINING) ? 1 : 0;
+  s.fp8 = (c.flags & MOE_FLAG_FP8_EXPERTS) ? 1 : 0;
   s.act_bf16 = bf16 ? 1 : 0;
   s.out_bf16 = c.out_dtype == MOE_BF16 ? 1 : 0;
   // groups of up to kGroupM m-tiles per expert: sum_e ceil(mt_e / G) <= MT / G + E and
@@ -301,6 +317,7 @@ static moe_status check_forward_args(moe_plan_t plan, const void* x, const void*
                                      size_t workspace_bytes) {
   if (!plan) return fail(MOE_ERR_INVALID_ARG, "null plan");
   if (plan->expert_stage) return fail(MOE_ERR_INVALID_ARG, "an expert-stage plan runs only moe_expert_forward");
+  if (plan->shape.fp8) return fail(MOE_ERR_INVALID_ARG, "a plan with MOE_FLAG_FP8_EXPERTS runs only moe_fp8_forward");
   const void* ptrs[] = {x, w_router, w1, w3, w2, y};
   const char* names[] = {"x", "w_router", "w1", "w3", "w2", "y"};
   for (int i = 0; i < 6; ++i) {
@@ -393,6 +410,150 @@ moe_status moe_forward_host(moe_plan_t plan, const void* x_host, void* x_dev, co
   e = cudaMemcpyAsync(y_host, y_dev, ybytes, cudaMemcpyDeviceToHost, cs);
   if (e != cudaSuccess) return cuda_fail(e, "copying y to the host");
   return MOE_OK;
+}
+
+// The layer with its experts in 8 bits: the router, the scan and the combine of moe_forward around
+// the dispatch and the products of 8-bit rows.
+moe_status moe_fp8_forward(moe_plan_t plan, const void* x, const void* x_q, const uint8_t* x_scales, const void* w_router,
+                           const float* router_bias, const void* w1, const uint8_t* w1_scales, const void* w3,
+                           const uint8_t* w3_scales, const void* w2, const uint8_t* w2_scales, void* y, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!plan) return fail(MOE_ERR_INVALID_ARG, "null plan");
+  if (plan->expert_stage || !plan->shape.fp8)
+    return fail(MOE_ERR_INVALID_ARG, "moe_fp8_forward needs a plan made by moe_plan with MOE_FLAG_FP8_EXPERTS");
+  const void* ptrs[] = {x, x_q, x_scales, w_router, w1, w1_scales, w3, w3_scales, w2, w2_scales, y};
+  const char* names[] = {"x", "x_q", "x_scales", "w_router", "w1", "w1_scales", "w3", "w3_scales", "w2", "w2_scales", "y"};
+  for (int i = 0; i < 11; ++i) {
+    if (!ptrs[i]) return fail(MOE_ERR_INVALID_ARG, "%s is null", names[i]);
+    if (!aligned(ptrs[i], 16)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
+  }
+  if (plan->shape.has_bias && (!router_bias || !aligned(router_bias, 16)))
+    return fail(MOE_ERR_INVALID_ARG, "router_bias must be a 16-byte aligned pointer (plan has a bias)");
+  if (!workspace || !aligned(workspace, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (workspace_bytes < plan->layout.total)
+    return fail(MOE_ERR_INVALID_ARG, "workspace too small: %zu < %zu", workspace_bytes, plan->layout.total);
+  moe_status st = bind_device(plan);
+  if (st != MOE_OK) return st;
+  const moe::Shape& s = plan->shape;
+  const moe::Ws ws = moe::ws_bind(s, workspace);
+  const moe::Weights w{x, w_router, s.has_bias ? router_bias : nullptr, nullptr, nullptr, nullptr, y};
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if ((st = run_stage(plan, 0, w, workspace, cs)) != MOE_OK) return st;
+  cudaError_t e = moe::launch_permute_fp8(s, ws, x_q, x_scales, plan->num_sms, true, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the dispatch of 8-bit rows");
+  moe::fp8::GemmArgs g{};
+  g.a = static_cast<const uint8_t*>(ws.xp);
+  g.sa = ws.xs;
+  g.b = static_cast<const uint8_t*>(w1);
+  g.sb = w1_scales;
+  g.b3 = static_cast<const uint8_t*>(w3);
+  g.sb3 = w3_scales;
+  g.out = ws.h;
+  g.out_scales = ws.hs;
+  g.rows = s.N;
+  g.n = s.F;
+  g.K = s.d;
+  g.E = s.E;
+  const bool few = moe::fp8::use_few(s.N, s.E, s.d > s.F ? s.d : s.F);
+  auto product = [&](int kind) {
+    return few ? moe::fp8::launch_gemm_few(kind, g, ws, ws.counts, s.E, false, plan->device, plan->num_sms, plan->timeout_ns, true, cs)
+               : moe::fp8::launch_gemm_tc(kind, g, ws, plan->device, plan->num_sms, plan->timeout_ns, true, cs);
+  };
+  if ((e = product(moe::fp8::kSwiGLU)) != cudaSuccess) return cuda_fail(e, "launching the SwiGLU product");
+  g.a = static_cast<const uint8_t*>(ws.h);
+  g.sa = ws.hs;
+  g.b = static_cast<const uint8_t*>(w2);
+  g.sb = w2_scales;
+  g.b3 = nullptr;
+  g.sb3 = nullptr;
+  g.gate = ws.gate_perm;
+  g.out = ws.yp;
+  g.out_scales = nullptr;
+  g.n = s.d;
+  g.K = s.F;
+  if ((e = product(moe::fp8::kOutBf16)) != cudaSuccess) return cuda_fail(e, "launching the down-projection");
+  return run_stage(plan, 4, w, workspace, cs);
+}
+
+// A checkpoint: the workspace's routing part as it lies, the router softmax, and the two
+// pre-activations in 8 bits.
+namespace {
+struct CkptLayout {
+  size_t routing, probs, qa, sa, qb, sb, total;
+};
+size_t routing_bytes(const moe::Shape& s, const moe::WsLayout& L) { return s.keep_logits ? L.logits : L.xp; }
+CkptLayout ckpt_layout(const moe::Shape& s, const moe::WsLayout& L) {
+  CkptLayout c{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = round_up(off + bytes, 256);
+    return at;
+  };
+  const size_t N = (size_t)s.N;
+  c.routing = take(routing_bytes(s, L));
+  c.probs = take((size_t)s.T * (size_t)s.E * 4);
+  c.qa = take(N * (size_t)s.F);
+  c.sa = take(N * (size_t)moe::fp8::scale_cols(s.F));
+  c.qb = take(N * (size_t)s.F);
+  c.sb = take(N * (size_t)moe::fp8::scale_cols(s.F));
+  c.total = off;
+  return c;
+}
+moe_status check_ckpt(moe_plan_t plan, const void* workspace, size_t workspace_bytes, const void* ckpt, size_t ckpt_bytes) {
+  if (!plan) return fail(MOE_ERR_INVALID_ARG, "null plan");
+  if (plan->expert_stage || !plan->shape.training)
+    return fail(MOE_ERR_INVALID_ARG, "a checkpoint needs a plan made with MOE_FLAG_TRAINING");
+  if (!workspace || !aligned(workspace, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (!ckpt || !aligned(ckpt, 256)) return fail(MOE_ERR_INVALID_ARG, "the checkpoint must be 256-byte aligned");
+  if (workspace_bytes < plan->layout.total)
+    return fail(MOE_ERR_INVALID_ARG, "workspace too small: %zu < %zu", workspace_bytes, plan->layout.total);
+  const size_t need = ckpt_layout(plan->shape, plan->layout).total;
+  if (ckpt_bytes < need) return fail(MOE_ERR_INVALID_ARG, "checkpoint too small: %zu < %zu", ckpt_bytes, need);
+  return bind_device(plan);
+}
+}  // namespace
+
+size_t moe_checkpoint_bytes(moe_plan_t plan) {
+  return !plan || plan->expert_stage || !plan->shape.training ? 0 : ckpt_layout(plan->shape, plan->layout).total;
+}
+
+moe_status moe_checkpoint_save(moe_plan_t plan, const void* workspace, size_t workspace_bytes, void* ckpt, size_t ckpt_bytes,
+                               void* stream) {
+  moe_status st = check_ckpt(plan, workspace, workspace_bytes, ckpt, ckpt_bytes);
+  if (st != MOE_OK) return st;
+  const moe::Shape& s = plan->shape;
+  const CkptLayout c = ckpt_layout(s, plan->layout);
+  const moe::Ws ws = moe::ws_bind(s, const_cast<void*>(workspace));
+  uint8_t* b = static_cast<uint8_t*>(ckpt);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(b + c.routing, workspace, routing_bytes(s, plan->layout), cudaMemcpyDeviceToDevice, cs);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(b + c.probs, ws.probs, (size_t)s.T * (size_t)s.E * 4, cudaMemcpyDeviceToDevice, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "copying the routing");
+  e = moe::fp8::launch_checkpoint_save(ws.a1, ws.a3, s.N, s.F, b + c.qa, b + c.sa, b + c.qb, b + c.sb, cs);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "launching the checkpoint");
+}
+
+moe_status moe_checkpoint_restore(moe_plan_t plan, const void* x, const void* ckpt, size_t ckpt_bytes, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  moe_status st = check_ckpt(plan, workspace, workspace_bytes, ckpt, ckpt_bytes);
+  if (st != MOE_OK) return st;
+  if (!x || !aligned(x, 16)) return fail(MOE_ERR_INVALID_ARG, "x must be a 16-byte aligned pointer");
+  const moe::Shape& s = plan->shape;
+  const CkptLayout c = ckpt_layout(s, plan->layout);
+  const moe::Ws ws = moe::ws_bind(s, workspace);
+  const uint8_t* b = static_cast<const uint8_t*>(ckpt);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(workspace, b + c.routing, routing_bytes(s, plan->layout), cudaMemcpyDeviceToDevice, cs);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(ws.probs, b + c.probs, (size_t)s.T * (size_t)s.E * 4, cudaMemcpyDeviceToDevice, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "copying the routing");
+  e = moe::fp8::launch_checkpoint_restore(b + c.qa, b + c.sa, b + c.qb, b + c.sb, s.N, s.F, ws.a1, ws.a3, ws.h, cs);
+  if (e != cudaSuccess) return cuda_fail(e, "launching the restore");
+  const moe::Weights w{x, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+  e = moe::launch_permute(s, ws, w, plan->num_sms, false, cs);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "launching the dispatch");
 }
 
 static constexpr const char* kBwdStageNames[] = {"gather_dy", "bwd_dh_swiglu", "bwd_dx_gemm", "bwd_dw13", "bwd_dw2",

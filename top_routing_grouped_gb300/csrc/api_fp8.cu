@@ -23,6 +23,24 @@ struct moe_fp8_plan_s {
   int num_sms = 0;
 };
 
+namespace moe {
+namespace fp8 {
+
+// Which tensor-core kernels.  Those that make the weights the MMA's rows read each weight tile once for
+// every 64 rows of a segment; the CTA pairs take 256 rows at the price of one.  Measured (experts;
+// time of the pairs / time of the others): 16 and 32 rows a segment 1.2-1.3 at every shape, 64 rows
+// 0.9 (8 experts of 8192) to 1.1 (32 of 2048), 128 rows 0.66-0.75.  With few segments the pairs also
+// leave SMs idle: dense products K x n of 2048 x 2048, 4096 x 4096 and 2048 x 8192 cross where the
+// others have more than one unit of work for each SM (1.5, 1.2 and 1.5 at 128 units; 0.94, 0.69 and
+// 0.96 at 192 to 256).
+bool use_few(int64_t rows, int64_t n_seg, int64_t widest_out) {
+  const int64_t blocks = (widest_out + 127) / 128;
+  return rows <= 48 * n_seg || ((rows + 63) / 64 + n_seg - 1) * blocks <= 152;
+}
+
+}  // namespace fp8
+}  // namespace moe
+
 namespace {
 
 using namespace moe;
@@ -89,18 +107,6 @@ moe_status bind_device(moe_fp8_plan_t plan) {
   return MOE_OK;
 }
 
-// Which tensor-core kernels.  Those that make the weights the MMA's rows read each weight tile once for
-// every 64 rows of a segment; the CTA pairs take 256 rows at the price of one.  Measured (experts;
-// time of the pairs / time of the others): 16 and 32 rows a segment 1.2-1.3 at every shape, 64 rows
-// 0.9 (8 experts of 8192) to 1.1 (32 of 2048), 128 rows 0.66-0.75.  With few segments the pairs also
-// leave SMs idle: dense products K x n of 2048 x 2048, 4096 x 4096 and 2048 x 8192 cross where the
-// others have more than one unit of work for each SM (1.5, 1.2 and 1.5 at 128 units; 0.94, 0.69 and
-// 0.96 at 192 to 256).
-bool use_few(int64_t rows, int64_t n_seg, int64_t widest_out) {
-  const int64_t blocks = (widest_out + 127) / 128;
-  return rows <= 48 * n_seg || ((rows + 63) / 64 + n_seg - 1) * blocks <= 152;
-}
-
 moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E, int32_t W, int32_t out_dtype,
                      int32_t path, int64_t timeout_ns, moe_fp8_plan_t* plan, size_t* workspace_bytes) {
   *plan = nullptr;
@@ -119,7 +125,7 @@ moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E
   if (!p) return fail(MOE_ERR_INTERNAL, "out of host memory");
   p->experts = experts;
   p->tc = tc;
-  p->few = tc && use_few(rows, (int64_t)E * W, experts && k > n ? k : n);
+  p->few = tc && fp8::use_few(rows, (int64_t)E * W, experts && k > n ? k : n);
   p->rows = rows;
   p->k = k;
   p->n = n;
@@ -380,6 +386,19 @@ moe_status moe_checkpoint_save_rows(const void* a, const void* b, int64_t rows, 
   if ((s = check(ptrs)) != MOE_OK) return s;
   return cuda_status(fp8::launch_checkpoint_save(a, b, rows, F, qa, sa, qb, sb, static_cast<cudaStream_t>(stream)),
                      "launching the checkpoint");
+}
+
+moe_status moe_checkpoint_restore_rows(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb, int64_t rows,
+                                       int32_t F, void* a, void* b, void* h, void* stream) {
+  moe_status s = check_sizes(rows, F, F);
+  if (s != MOE_OK) return s;
+  if (rows == 0) return set_last_error(MOE_OK, "");
+  const Ptr ptrs[] = {{qa, "qa", 16, false}, {sa, "sa", 16, false}, {qb, "qb", 16, false}, {sb, "sb", 16, false},
+                      {a, "a", 16, true},    {b, "b", 16, true},    {h, "h", 16, true}};
+  if ((s = check(ptrs)) != MOE_OK) return s;
+  if (!a && !b && !h) return fail(MOE_ERR_INVALID_ARG, "no output is wanted");
+  return cuda_status(fp8::launch_checkpoint_restore(qa, sa, qb, sb, rows, F, a, b, h, static_cast<cudaStream_t>(stream)),
+                     "launching the restore");
 }
 
 moe_status moe_checkpoint_backward_rows(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb,

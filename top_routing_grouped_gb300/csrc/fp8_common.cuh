@@ -56,10 +56,22 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
 // NaNs are the largest.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// SiLU(a) = a / (1 + e^-a).  The hidden rows are rounded to e4m3 right after this, where an
-// error of the hardware tanh (2^-11) would move about one value in 128 to its neighbour; this
-// form is good to a few fp32 steps.  For a -> -inf: e^-a = inf and the quotient is -0.
-__device__ __forceinline__ float silu_exact(float a) { return __fdividef(a, 1.f + __expf(-a)); }
+// sigma(a) = 1 / (1 + e^-a) and 1 - sigma(a), from z = e^-|a|: the quotients' denominator 1 + z lies
+// in [1, 2], so nothing overflows or is flushed for any a, and either value is good to a few fp32
+// steps.
+__device__ __forceinline__ void sigmoid_pair(float a, float& s, float& one_minus_s) {
+  const float z = __expf(-fabsf(a)), r = __fdividef(1.f, 1.f + z), zr = z * r;
+  s = a >= 0.f ? r : zr;
+  one_minus_s = a >= 0.f ? zr : r;
+}
+
+// SiLU(a) = a sigma(a).  The hidden rows are rounded to e4m3 right after this, where an error of the
+// hardware tanh (2^-11) would move about one value in 128 to its neighbour.
+__device__ __forceinline__ float silu_exact(float a) {
+  float s, c;
+  sigmoid_pair(a, s, c);
+  return a * s;
+}
 
 }  // namespace fp8
 }  // namespace moe

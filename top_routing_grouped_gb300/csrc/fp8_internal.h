@@ -36,6 +36,9 @@ cudaError_t launch_checkpoint_backward(const void* qa, const uint8_t* sa, const 
                                        const void* dh, int64_t rows, int F, void* da, void* db, void* h,
                                        cudaStream_t st);
 
+cudaError_t launch_checkpoint_restore(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb, int64_t rows,
+                                      int F, void* a, void* b, void* h, cudaStream_t st);
+
 cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* weight, bool bf16, int64_t rows, int d,
                            int64_t ldx, int64_t ldr, float eps, void* residual_out, void* out, void* q, uint8_t* scales,
                            float* rstd, cudaStream_t st);
@@ -47,6 +50,8 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
 cudaError_t launch_gemm_simt(int kind, const GemmArgs& g, const Ws& ws, int num_sms, cudaStream_t st);
 cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns,
                            bool pdl, cudaStream_t st);
+// Which of the two sets of tensor-core kernels: see api_fp8.cu.
+bool use_few(int64_t rows, int64_t n_seg, int64_t widest_out);
 // Few rows an expert: finds its tiles from the segment counts itself (null: one segment); `first`:
 // the call's first launch, which sets the status word.
 cudaError_t launch_gemm_few(int kind, const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first,

@@ -8,7 +8,7 @@
 //
 // One warp per token: the row is read once with 16-byte vector loads (issued first), the k
 // destinations are computed by lanes 0..k-1 and broadcast, and the row is written k times
-// (x is read once).
+// (x is read once).  An 8-bit row brings its block factors, a few words, along.
 #include "device_common.cuh"
 
 namespace moe {
@@ -16,12 +16,22 @@ namespace moe {
 constexpr int kPermWarps = 8;
 constexpr int kPermVec = 8;  // 16-byte vectors per lane in flight (a 4 KB row per warp)
 
-__global__ void __launch_bounds__(kPermWarps * 32) permute_kernel(Shape s, Ws ws, Weights w) {
+// What moves: rows of `vecs` 16-byte vectors and, where `words` > 0, that many 32-bit words beside
+// each of them.
+struct PermuteRows {
+  const void* src;
+  void* dst;
+  int vecs;
+  const uint32_t* src_words;
+  uint32_t* dst_words;
+  int words;
+};
+
+__global__ void __launch_bounds__(kPermWarps * 32) permute_kernel(Shape s, Ws ws, PermuteRows r) {
   const int lane = threadIdx.x & 31;
   const int64_t warp = (int64_t)blockIdx.x * kPermWarps + (threadIdx.x >> 5);
   const int64_t nwarps = (int64_t)gridDim.x * kPermWarps;
-  const int esz = s.act_bf16 ? 2 : 4;
-  const int vecs = s.d * esz / 16;  // 16-byte vectors per row (d * esz is a multiple of 16)
+  const int vecs = r.vecs;
   const int k = s.k;
   pdl_wait();  // bases of the scan, ranks and choices of the router
   pdl_launch_dependents();
@@ -29,7 +39,7 @@ __global__ void __launch_bounds__(kPermWarps * 32) permute_kernel(Shape s, Ws ws
   for (int64_t t = warp; t < s.T; t += nwarps) {
     // the row's first 32 x 8 vectors are requested before the routing lookups, so that the
     // two latencies overlap
-    const int4* src = reinterpret_cast<const int4*>(reinterpret_cast<const char*>(w.x) + t * (int64_t)s.d * esz);
+    const int4* src = reinterpret_cast<const int4*>(r.src) + t * vecs;
     int4 buf[kPermVec];
 #pragma unroll
     for (int u = 0; u < kPermVec; ++u) {
@@ -57,7 +67,7 @@ __global__ void __launch_bounds__(kPermWarps * 32) permute_kernel(Shape s, Ws ws
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j) dst[j] = __shfl_sync(0xffffffffu, my_p, j);
 
-    int4* xp = reinterpret_cast<int4*>(ws.xp);
+    int4* xp = reinterpret_cast<int4*>(r.dst);
     for (int v0 = 0;;) {
 #pragma unroll
       for (int j = 0; j < kMaxTopK; ++j) {
@@ -77,14 +87,33 @@ __global__ void __launch_bounds__(kPermWarps * 32) permute_kernel(Shape s, Ws ws
         if (v < vecs) buf[u] = __ldcs(src + v);
       }
     }
+    for (int i = lane; i < r.words; i += 32) {
+      const uint32_t f = __ldcs(r.src_words + t * r.words + i);
+#pragma unroll
+      for (int j = 0; j < kMaxTopK; ++j)
+        if (j < k && dst[j] >= 0) r.dst_words[dst[j] * r.words + i] = f;
+    }
   }
 }
 
-cudaError_t launch_permute(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st) {
+static cudaError_t launch(const Shape& s, const Ws& ws, const PermuteRows& r, int num_sms, bool pdl, cudaStream_t st) {
   int64_t blocks = (s.T + kPermWarps - 1) / kPermWarps;
   const int64_t cap = (int64_t)num_sms * 8;
   if (blocks > cap) blocks = cap;
-  return launch_kernel(permute_kernel, dim3((unsigned)blocks), dim3(kPermWarps * 32), 0, st, pdl, 1, s, ws, w);
+  return launch_kernel(permute_kernel, dim3((unsigned)blocks), dim3(kPermWarps * 32), 0, st, pdl, 1, s, ws, r);
+}
+
+cudaError_t launch_permute(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st) {
+  // d times the element's size is a multiple of 16
+  return launch(s, ws, PermuteRows{w.x, ws.xp, s.d * (s.act_bf16 ? 2 : 4) / 16, nullptr, nullptr, 0}, num_sms, pdl, st);
+}
+
+cudaError_t launch_permute_fp8(const Shape& s, const Ws& ws, const void* x, const uint8_t* xs, int num_sms, bool pdl,
+                               cudaStream_t st) {
+  const int words = (s.d + 511) / 512;  // four block factors a word
+  return launch(s, ws,
+                PermuteRows{x, ws.xp, s.d / 16, reinterpret_cast<const uint32_t*>(xs), reinterpret_cast<uint32_t*>(ws.xs), words},
+                num_sms, pdl, st);
 }
 
 }  // namespace moe

@@ -135,16 +135,32 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_vec_kernel(QuantizeJob
 
 // da = dh b silu'(a), db = dh silu(a), h = silu(a) b of one value.
 __device__ __forceinline__ void swiglu_backward(float a, float b, float g, float& da, float& db, float& h) {
-  const float s = __fdividef(1.f, 1.f + __expf(-a)), u = a * s;
-  da = g * b * (s + u * (1.f - s));
+  float s, c;
+  sigmoid_pair(a, s, c);
+  const float u = a * s;
+  da = g * b * (s + u * c);
   db = g * u;
   h = u * b;
 }
 
+template <bool kBackward>
+__device__ __forceinline__ void one(float a, float b, float g, float& oa, float& ob, float& oh) {
+  if constexpr (kBackward) {
+    swiglu_backward(a, b, g, oa, ob, oh);
+  } else {
+    oa = a;  // e4m3 times a power of two: exact in bf16
+    ob = b;
+    oh = silu_exact(a) * b;
+  }
+}
+
 constexpr int kBwdResident = 152 * 5;  // CTAs (48 registers); 20011 x 1072: 35.5 us, with 4 a SM 36.4, with 6 (two waves) 43
 
+// kBackward: da, db and h from dh; else the values themselves, a and b, and h.  Every output but
+// da and db may be null.
+template <bool kBackward>
 __global__ void __launch_bounds__(kThreads)
-    checkpoint_backward_vec_kernel(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
+    checkpoint_vec_kernel(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
                                    const __nv_bfloat16* dh, int64_t rows, int F, __nv_bfloat16* da, __nv_bfloat16* db,
                                    __nv_bfloat16* h, int per_pass) {
   const int nb = (F + kBlock - 1) / kBlock, sc = (int)scale_cols(F);
@@ -154,11 +170,12 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t step = (int64_t)per_pass * F, sstep = (int64_t)per_pass * sc;
   uint2 va, vb;
   Raw8<true> g;
+  g.zero();
   uint32_t fa, fb;
   auto fetch = [&](int64_t i, int64_t is) {
     va = __ldcs(reinterpret_cast<const uint2*>(qa + i));
     vb = __ldcs(reinterpret_cast<const uint2*>(qb + i));
-    g.load(dh, i);
+    if (kBackward) g.load(dh, i);
     fa = __ldg(sa + is);
     fb = __ldg(sb + is);
   };
@@ -174,19 +191,20 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = 0; j < 4; ++j) {
       const uint32_t wa = (j & 2 ? ca.y : ca.x) >> (16 * (j & 1)), wb = (j & 2 ? cb.y : cb.x) >> (16 * (j & 1));
       const float2 a = unpack_e4m3x2(wa), b = unpack_e4m3x2(wb);
-      swiglu_backward(a.x * sca, b.x * scb, e.v[2 * j], oa[2 * j], ob[2 * j], oh[2 * j]);
-      swiglu_backward(a.y * sca, b.y * scb, e.v[2 * j + 1], oa[2 * j + 1], ob[2 * j + 1], oh[2 * j + 1]);
+      one<kBackward>(a.x * sca, b.x * scb, e.v[2 * j], oa[2 * j], ob[2 * j], oh[2 * j]);
+      one<kBackward>(a.y * sca, b.y * scb, e.v[2 * j + 1], oa[2 * j + 1], ob[2 * j + 1], oh[2 * j + 1]);
     }
-    *reinterpret_cast<uint4*>(da + o) = pack_bf16x8(oa);
-    *reinterpret_cast<uint4*>(db + o) = pack_bf16x8(ob);
+    if (kBackward || da) *reinterpret_cast<uint4*>(da + o) = pack_bf16x8(oa);
+    if (kBackward || db) *reinterpret_cast<uint4*>(db + o) = pack_bf16x8(ob);
     if (h) *reinterpret_cast<uint4*>(h + o) = pack_bf16x8(oh);
     o += step;
   }
 }
 
-// SwiGLU backward out of the checkpoint; a warp per block of 128 columns of a row.
+// The same for rows of any length; a warp per block of 128 columns of a row.
+template <bool kBackward>
 __global__ void __launch_bounds__(kThreads)
-    checkpoint_backward_kernel(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
+    checkpoint_kernel(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
                                const __nv_bfloat16* dh, int64_t rows, int F, __nv_bfloat16* da, __nv_bfloat16* db,
                                __nv_bfloat16* h) {
   const int lane = threadIdx.x & 31;
@@ -199,11 +217,12 @@ __global__ void __launch_bounds__(kThreads)
       const int64_t c = blk * kBlock + j * 32 + lane;
       if (c >= F) continue;
       const int64_t o = row * F + c;
-      const float a = unpack_e4m3x2(qa[o]).x * fa, b = unpack_e4m3x2(qb[o]).x * fb, g = __bfloat162float(dh[o]);
+      const float a = unpack_e4m3x2(qa[o]).x * fa, b = unpack_e4m3x2(qb[o]).x * fb;
+      const float g = kBackward ? __bfloat162float(dh[o]) : 0.f;
       float oa, ob, oh;
-      swiglu_backward(a, b, g, oa, ob, oh);
-      da[o] = __float2bfloat16_rn(oa);
-      db[o] = __float2bfloat16_rn(ob);
+      one<kBackward>(a, b, g, oa, ob, oh);
+      if (kBackward || da) da[o] = __float2bfloat16_rn(oa);
+      if (kBackward || db) db[o] = __float2bfloat16_rn(ob);
       if (h) h[o] = __float2bfloat16_rn(oh);
     }
   }
@@ -263,18 +282,29 @@ cudaError_t launch_checkpoint_save(const void* a, const void* b, int64_t rows, i
   return e != cudaSuccess ? e : launch_quantize_rows(b, true, rows, F, F, qb, sb, st);
 }
 
-cudaError_t launch_checkpoint_backward(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb,
-                                       const void* dh, int64_t rows, int F, void* da, void* db, void* h,
-                                       cudaStream_t st) {
+template <bool kBackward>
+static cudaError_t checkpoint(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb, const void* dh,
+                              int64_t rows, int F, void* da, void* db, void* h, cudaStream_t st) {
   if (F % 8 == 0) {
     const Pass p = pass_of(rows, F, kBwdResident);
-    return launch_kernel(checkpoint_backward_vec_kernel, dim3(p.ctas), dim3(kThreads), 0, st, false, 1, (const uint8_t*)qa, sa,
+    return launch_kernel(checkpoint_vec_kernel<kBackward>, dim3(p.ctas), dim3(kThreads), 0, st, false, 1, (const uint8_t*)qa, sa,
                          (const uint8_t*)qb, sb, (const __nv_bfloat16*)dh, rows, F, (__nv_bfloat16*)da, (__nv_bfloat16*)db,
                          (__nv_bfloat16*)h, p.per_pass);
   }
-  return launch_kernel(checkpoint_backward_kernel, dim3(grid_for(rows * ((F + kBlock - 1) / kBlock), kWarps)),
-                       dim3(kThreads), 0, st, false, 1, (const uint8_t*)qa, sa, (const uint8_t*)qb, sb,
-                       (const __nv_bfloat16*)dh, rows, F, (__nv_bfloat16*)da, (__nv_bfloat16*)db, (__nv_bfloat16*)h);
+  return launch_kernel(checkpoint_kernel<kBackward>, dim3(grid_for(rows * ((F + kBlock - 1) / kBlock), kWarps)), dim3(kThreads),
+                       0, st, false, 1, (const uint8_t*)qa, sa, (const uint8_t*)qb, sb, (const __nv_bfloat16*)dh, rows, F,
+                       (__nv_bfloat16*)da, (__nv_bfloat16*)db, (__nv_bfloat16*)h);
+}
+
+cudaError_t launch_checkpoint_backward(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb,
+                                       const void* dh, int64_t rows, int F, void* da, void* db, void* h,
+                                       cudaStream_t st) {
+  return checkpoint<true>(qa, sa, qb, sb, dh, rows, F, da, db, h, st);
+}
+
+cudaError_t launch_checkpoint_restore(const void* qa, const uint8_t* sa, const void* qb, const uint8_t* sb, int64_t rows,
+                                      int F, void* a, void* b, void* h, cudaStream_t st) {
+  return checkpoint<false>(qa, sa, qb, sb, nullptr, rows, F, a, b, h, st);
 }
 
 }  // namespace fp8

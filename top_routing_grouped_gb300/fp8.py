@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from .moe import MOE_BF16, MOE_F32, MOE_OK, MoEError, MoeExpertConfig, _lib, _PATHS
+from .moe import MOE_BF16, MOE_F32, MOE_OK, MoEError, MoeExpertConfig, MoEPlan, _lib, _PATHS
 
 _P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
@@ -44,6 +44,11 @@ _expert_plan = _declare("moe_fp8_expert_plan", ctypes.POINTER(MoeExpertConfig), 
 _expert_forward = _declare("moe_fp8_expert_forward", *[_P] * 13, ctypes.c_size_t, _P)
 _plan_destroy = _declare("moe_fp8_plan_destroy", _P, restype=None)
 _device_status = _declare("moe_fp8_get_device_status", _P, _P, _P)
+_layer_forward = _declare("moe_fp8_forward", *[_P] * 14, ctypes.c_size_t, _P)
+_ckpt_restore_rows = _declare("moe_checkpoint_restore_rows", *[_P] * 4, _I64, _I32, _P, _P, _P, _P)
+_layer_ckpt_bytes = _declare("moe_checkpoint_bytes", _P, restype=ctypes.c_size_t)
+_layer_ckpt_save = _declare("moe_checkpoint_save", _P, _P, ctypes.c_size_t, _P, ctypes.c_size_t, _P)
+_layer_ckpt_restore = _declare("moe_checkpoint_restore", _P, _P, _P, ctypes.c_size_t, _P, ctypes.c_size_t, _P)
 _ckpt_save = _declare("moe_checkpoint_save_rows", _P, _P, _I64, _I32, _P, _P, _P, _P, _P)
 _ckpt_backward = _declare("moe_checkpoint_backward_rows", *[_P] * 5, _I64, _I32, _P, _P, _P, _P)
 
@@ -229,6 +234,53 @@ class Fp8ExpertPlan(_Fp8Plan):
                                _stream(stream, x_rows, x_scales, gates, w1, s1, w3, s3, w2, s2, y_rows, workspace, seg_counts)), "moe_fp8_expert_forward")
 
 
+class Fp8MoEPlan(MoEPlan):
+    """The whole layer with its experts in 8 bits (moe_fp8_forward): the arguments are MoEPlan's."""
+
+    def __init__(self, T, d, E, k, F, out_dtype="bf16", tau=1.0, has_bias=False, keep_logits=False, wait_timeout_ns=0,
+                 renorm_gates=False):
+        super().__init__(T, d, E, k, F, dtype="bf16", out_dtype=out_dtype, tau=tau, has_bias=has_bias, keep_logits=keep_logits,
+                         wait_timeout_ns=wait_timeout_ns, renorm_gates=renorm_gates, fp8_experts=True)
+        T, d, E, F = self.T, self.d, self.E, self.F
+        self._x, self._sx, self._wr = (T, d), (T, scale_cols(d)), (E, d)
+        self._w13, self._s13 = (E, F, d), (E, (F + 127) // 128, scale_cols(d))
+        self._w2, self._s2 = (E, d, F), (E, (d + 127) // 128, scale_cols(F))
+
+    def forward(self, x, x_q, x_scales, w_router, bias, w1, s1, w3, s3, w2, s2, y, workspace, stream=None):
+        """x (bf16) for the router, x_q with x_scales for the experts: both as rmsnorm writes them."""
+        _check(_layer_forward(self._h, _rows(x, self._x, _BF16, "x"), _rows(x_q, self._x, _E4, "x_q"),
+                              _rows(x_scales, self._sx, _SCALES, "x_scales"), _rows(w_router, self._wr, _BF16, "w_router"),
+                              _maybe(bias, (self.E,), _F32, "bias"),
+                              _rows(w1, self._w13, _E4, "w1"), _rows(s1, self._s13, _SCALES, "s1"),
+                              _rows(w3, self._w13, _E4, "w3"), _rows(s3, self._s13, _SCALES, "s3"),
+                              _rows(w2, self._w2, _E4, "w2"), _rows(s2, self._s2, _SCALES, "s2"),
+                              _rows(y, self._x, (self.out_dtype,), "y"), workspace.data_ptr(), workspace.numel(),
+                              _stream(stream, x, x_q, x_scales, w_router, bias, w1, s1, w3, s3, w2, s2, y, workspace)),
+               "moe_fp8_forward")
+
+
+class LayerCheckpoint:
+    """What one training forward of `plan` (a MoEPlan with training=True) has to leave for its backward,
+    with the pre-activations in 8 bits, so that the layers of a stack can share a workspace:
+    save(workspace) after plan.forward, restore(x, workspace) before plan.backward."""
+
+    def __init__(self, plan, device="cuda"):
+        self.plan = plan
+        n = int(_layer_ckpt_bytes(plan.handle))
+        _want(n > 0, "checkpoints need a plan with training=True")
+        self.data = torch.empty(n, dtype=torch.uint8, device=device)
+
+    def save(self, workspace, stream=None):
+        _check(_layer_ckpt_save(self.plan.handle, workspace.data_ptr(), workspace.numel(), self.data.data_ptr(),
+                                self.data.numel(), _stream(stream, workspace, self.data)), "moe_checkpoint_save")
+
+    def restore(self, x, workspace, stream=None):
+        p = self.plan
+        _check(_layer_ckpt_restore(p.handle, _rows(x, (p.T, p.d), (p.act_dtype,), "x"), self.data.data_ptr(), self.data.numel(),
+                                   workspace.data_ptr(), workspace.numel(), _stream(stream, x, workspace, self.data)),
+               "moe_checkpoint_restore")
+
+
 def checkpoint_save(a, b, qa, sa, qb, sb, stream=None):
     """The pre-activations a, b [n, F] (bf16) into 8 bits (moe_checkpoint_save_rows)."""
     _want(a.dim() == 2, "a must be 2-D")
@@ -237,6 +289,18 @@ def checkpoint_save(a, b, qa, sa, qb, sb, stream=None):
     _check(_ckpt_save(_rows(a, (n, F), _BF16, "a"), _rows(b, (n, F), _BF16, "b"), n, F, _rows(qa, (n, F), _E4, "qa"),
                       _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), _E4, "qb"), _rows(sb, s, _SCALES, "sb"),
                       _stream(stream, a, b, qa, sa, qb, sb)), "moe_checkpoint_save_rows")
+
+
+def checkpoint_restore(qa, sa, qb, sb, a=None, b=None, h=None, stream=None):
+    """The values of a checkpoint and h = silu(a) * b into whichever of a, b, h are given, [n, F] bf16
+    (moe_checkpoint_restore_rows)."""
+    _want(qa.dim() == 2, "qa must be 2-D")
+    n, F = qa.shape
+    s = (n, scale_cols(F))
+    _check(_ckpt_restore_rows(_rows(qa, (n, F), _E4, "qa"), _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), _E4, "qb"),
+                              _rows(sb, s, _SCALES, "sb"), n, F, _maybe(a, (n, F), _BF16, "a"), _maybe(b, (n, F), _BF16, "b"),
+                              _maybe(h, (n, F), _BF16, "h"), _stream(stream, qa, sa, qb, sb, a, b, h)),
+           "moe_checkpoint_restore_rows")
 
 
 def checkpoint_backward(qa, sa, qb, sb, dh, da, db, h=None, stream=None):

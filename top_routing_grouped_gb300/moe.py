@@ -18,6 +18,7 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_PATH_AUTO, MOE_PATH_SIMT, MOE_PATH_TC_1SM = 0, 1, 2
 _PATHS = {"auto": MOE_PATH_AUTO, "simt": MOE_PATH_SIMT, "tc1": MOE_PATH_TC_1SM}
 MOE_FLAG_KEEP_LOGITS, MOE_FLAG_TEST_STALL, MOE_FLAG_RENORM_GATES, MOE_FLAG_TRAINING = 1, 2, 4, 8
+MOE_FLAG_FP8_EXPERTS = 16
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build()")
@@ -123,11 +124,12 @@ class MoEPlan:
 
     def __init__(self, T, d, E, k, F, dtype="bf16", out_dtype=None, tau=1.0, has_bias=False,
                  path="auto", keep_logits=False, test_stall=False, wait_timeout_ns=0, renorm_gates=False,
-                 training=False):
+                 training=False, fp8_experts=False):
         act = MOE_BF16 if dtype == "bf16" else MOE_F32
         out = act if out_dtype is None else (MOE_BF16 if out_dtype == "bf16" else MOE_F32)
         flags = ((MOE_FLAG_KEEP_LOGITS if keep_logits else 0) | (MOE_FLAG_TEST_STALL if test_stall else 0)
-                 | (MOE_FLAG_RENORM_GATES if renorm_gates else 0) | (MOE_FLAG_TRAINING if training else 0))
+                 | (MOE_FLAG_RENORM_GATES if renorm_gates else 0) | (MOE_FLAG_TRAINING if training else 0)
+                 | (MOE_FLAG_FP8_EXPERTS if fp8_experts else 0))
         self.renorm_gates = bool(renorm_gates)
         self.cfg = MoeConfig(int(T), int(d), int(E), int(k), int(F), act, out, float(tau),
                              1 if has_bias else 0, _PATHS[path],
@@ -231,6 +233,7 @@ class MoEPlan:
             return workspace[off:off + nbytes].view(dtype).view(*shape)
 
         i32, f32, act = torch.int32, torch.float32, self.act_dtype
+        row = torch.float8_e4m3fn if self.cfg.flags & MOE_FLAG_FP8_EXPERTS else act
         return dict(
             status=view(v.status, i32, (8,)), aux=view(v.aux, f32, (1,)),
             topk_idx=view(v.topk_idx, i32, (self.T, self.k)), topk_gate=view(v.topk_gate, f32, (self.T, self.k)),
@@ -238,8 +241,8 @@ class MoEPlan:
             expert_offsets=view(v.expert_offsets, i32, (self.E + 1,)),
             perm_src=view(v.perm_src, i32, (N,)), perm_slot=view(v.perm_slot, i32, (N,)),
             gate_perm=view(v.gate_perm, f32, (N,)), slot_pos=view(v.slot_pos, i32, (N,)),
-            logits=view(v.logits, f32, (self.T, self.E)), xp=view(v.xp, act, (N, self.d)),
-            h=view(v.h, act, (N, self.F)), yp=view(v.yp, act, (N, self.d)),
+            logits=view(v.logits, f32, (self.T, self.E)), xp=view(v.xp, row, (N, self.d)),
+            h=view(v.h, row, (N, self.F)), yp=view(v.yp, act, (N, self.d)),
             expert_psum=view(v.expert_psum, f32, (self.E,)))
 
 

@@ -20,6 +20,8 @@ struct moe_plan_s {
   moe::WsLayout layout;
   bool tc;          // tensor-core router and expert GEMMs (bf16 layers, not MOE_PATH_SIMT)
   bool pair;        // expert GEMMs on CTA pairs (MOE_PATH_AUTO)
+  bool fp8 = false; // experts in 8 bits (MOE_FLAG_FP8_EXPERTS): xp and h hold e4m3, with factors at xs and hs
+  size_t xs = 0, hs = 0;
   int device = -1;  // device the cached attributes belong to
   int num_sms = 0;
   int64_t timeout_ns;
@@ -79,7 +81,8 @@ moe_status bind_device(moe_plan_t plan) {
 
 namespace moe {
 
-WsLayout ws_layout(const Shape& s) {
+// fp8_xs, fp8_hs: null, or where an 8-bit plan's block factors of xp and h lie.
+static WsLayout layout(const Shape& s, size_t* fp8_xs, size_t* fp8_hs) {
   WsLayout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -88,7 +91,7 @@ WsLayout ws_layout(const Shape& s) {
     return at;
   };
   const size_t esz = s.act_bf16 ? 2 : 4;
-  const size_t rsz = s.fp8 ? 1 : esz;  // xp and h
+  const size_t rsz = fp8_xs ? 1 : esz;  // xp and h
   const size_t N = (size_t)s.N, E = (size_t)s.E, nb = (size_t)s.nblk;
   L.hdr = take(64 * sizeof(uint32_t));
   L.aux = take(sizeof(float));
@@ -111,9 +114,9 @@ WsLayout ws_layout(const Shape& s) {
   L.xp = take(N * (size_t)s.d * rsz);
   L.h = take(N * (size_t)s.F * rsz);
   L.yp = take(N * (size_t)s.d * esz);
-  if (s.fp8) {
-    L.xs = take(N * (size_t)fp8::scale_cols(s.d));
-    L.hs = take(N * (size_t)fp8::scale_cols(s.F));
+  if (fp8_xs) {
+    *fp8_xs = take(N * (size_t)fp8::scale_cols(s.d));
+    *fp8_hs = take(N * (size_t)fp8::scale_cols(s.F));
   }
   if (s.training) {
     const size_t nt = 2 * (((size_t)s.F + 255) / 256), chunks = (size_t)dwr_chunks(s);
@@ -137,8 +140,9 @@ WsLayout ws_layout(const Shape& s) {
   return L;
 }
 
-Ws ws_bind(const Shape& s, void* base) {
-  const WsLayout L = ws_layout(s);
+WsLayout ws_layout(const Shape& s) { return layout(s, nullptr, nullptr); }
+
+static Ws bind(const Shape& s, const WsLayout& L, void* base) {
   char* b = static_cast<char*>(base);
   Ws w{};
   w.hdr = reinterpret_cast<uint32_t*>(b + L.hdr);
@@ -162,10 +166,6 @@ Ws ws_bind(const Shape& s, void* base) {
   w.xp = b + L.xp;
   w.h = b + L.h;
   w.yp = b + L.yp;
-  if (s.fp8) {
-    w.xs = reinterpret_cast<uint8_t*>(b + L.xs);
-    w.hs = reinterpret_cast<uint8_t*>(b + L.hs);
-  }
   if (s.training) {
     w.a1 = b + L.a1;
     w.a3 = b + L.a3;
@@ -185,6 +185,8 @@ Ws ws_bind(const Shape& s, void* base) {
   }
   return w;
 }
+
+Ws ws_bind(const Shape& s, void* base) { return bind(s, ws_layout(s), base); }
 
 const Shape* plan_shape(moe_plan_t plan) { return &plan->shape; }
 bool plan_is_layer(moe_plan_t plan) { return plan && !plan->expert_stage; }
@@ -287,13 +289,13 @@ moe_status moe_plan(const moe_config* cfg, moe_plan_t* plan, size_t* workspace_b
   s.keep_logits = (c.flags & MOE_FLAG_KEEP_LOGITS) ? 1 : 0;
   s.renorm = (c.flags & MOE_FLAG_RENORM_GATES) ? 1 : 0;
   s.training = (c.flags & MOE_FLAG_TRAINING) ? 1 : 0;
-  s.fp8 = (c.flags & MOE_FLAG_FP8_EXPERTS) ? 1 : 0;
   s.act_bf16 = bf16 ? 1 : 0;
   s.out_bf16 = c.out_dtype == MOE_BF16 ? 1 : 0;
   // groups of up to kGroupM m-tiles per expert: sum_e ceil(mt_e / G) <= MT / G + E and
   // MT = sum_e ceil(count_e / 128) <= N / 128 + E
   s.max_groups = (int)(N / ((int64_t)moe::kTileM * moe::kGroupM) + 2 * (int64_t)c.n_experts + 2);
-  p->layout = moe::ws_layout(s);
+  p->fp8 = (c.flags & MOE_FLAG_FP8_EXPERTS) != 0;
+  p->layout = p->fp8 ? moe::layout(s, &p->xs, &p->hs) : moe::ws_layout(s);
   p->tc = tc;
   p->pair = tc && c.path == MOE_PATH_AUTO;
   p->timeout_ns = c.wait_timeout_ns > 0 ? c.wait_timeout_ns : 2000000000LL;
@@ -317,7 +319,7 @@ static moe_status check_forward_args(moe_plan_t plan, const void* x, const void*
                                      size_t workspace_bytes) {
   if (!plan) return fail(MOE_ERR_INVALID_ARG, "null plan");
   if (plan->expert_stage) return fail(MOE_ERR_INVALID_ARG, "an expert-stage plan runs only moe_expert_forward");
-  if (plan->shape.fp8) return fail(MOE_ERR_INVALID_ARG, "a plan with MOE_FLAG_FP8_EXPERTS runs only moe_fp8_forward");
+  if (plan->fp8) return fail(MOE_ERR_INVALID_ARG, "a plan with MOE_FLAG_FP8_EXPERTS runs only moe_fp8_forward");
   const void* ptrs[] = {x, w_router, w1, w3, w2, y};
   const char* names[] = {"x", "w_router", "w1", "w3", "w2", "y"};
   for (int i = 0; i < 6; ++i) {
@@ -334,7 +336,7 @@ static moe_status check_forward_args(moe_plan_t plan, const void* x, const void*
 
 static moe_status run_stage(moe_plan_t plan, int32_t stage, const moe::Weights& w, void* workspace, cudaStream_t st) {
   const moe::Shape& s = plan->shape;
-  const moe::Ws ws = moe::ws_bind(s, workspace);
+  const moe::Ws ws = moe::bind(s, plan->layout, workspace);
   // every stage after the router is chained to its predecessor (programmatic dependent launch)
   const bool pdl = stage > 0;
   cudaError_t e = cudaSuccess;
@@ -419,7 +421,7 @@ moe_status moe_fp8_forward(moe_plan_t plan, const void* x, const void* x_q, cons
                            const uint8_t* w3_scales, const void* w2, const uint8_t* w2_scales, void* y, void* workspace,
                            size_t workspace_bytes, void* stream) {
   if (!plan) return fail(MOE_ERR_INVALID_ARG, "null plan");
-  if (plan->expert_stage || !plan->shape.fp8)
+  if (plan->expert_stage || !plan->fp8)
     return fail(MOE_ERR_INVALID_ARG, "moe_fp8_forward needs a plan made by moe_plan with MOE_FLAG_FP8_EXPERTS");
   const void* ptrs[] = {x, x_q, x_scales, w_router, w1, w1_scales, w3, w3_scales, w2, w2_scales, y};
   const char* names[] = {"x", "x_q", "x_scales", "w_router", "w1", "w1_scales", "w3", "w3_scales", "w2", "w2_scales", "y"};
@@ -435,21 +437,23 @@ moe_status moe_fp8_forward(moe_plan_t plan, const void* x, const void* x_q, cons
   moe_status st = bind_device(plan);
   if (st != MOE_OK) return st;
   const moe::Shape& s = plan->shape;
-  const moe::Ws ws = moe::ws_bind(s, workspace);
+  const moe::Ws ws = moe::bind(s, plan->layout, workspace);
   const moe::Weights w{x, w_router, s.has_bias ? router_bias : nullptr, nullptr, nullptr, nullptr, y};
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if ((st = run_stage(plan, 0, w, workspace, cs)) != MOE_OK) return st;
-  cudaError_t e = moe::launch_permute_fp8(s, ws, x_q, x_scales, plan->num_sms, true, cs);
+  uint8_t* xs = static_cast<uint8_t*>(workspace) + plan->xs;
+  uint8_t* hs = static_cast<uint8_t*>(workspace) + plan->hs;
+  cudaError_t e = moe::fp8::launch_permute(s, ws, x_q, x_scales, xs, plan->num_sms, true, cs);
   if (e != cudaSuccess) return cuda_fail(e, "launching the dispatch of 8-bit rows");
   moe::fp8::GemmArgs g{};
   g.a = static_cast<const uint8_t*>(ws.xp);
-  g.sa = ws.xs;
+  g.sa = xs;
   g.b = static_cast<const uint8_t*>(w1);
   g.sb = w1_scales;
   g.b3 = static_cast<const uint8_t*>(w3);
   g.sb3 = w3_scales;
   g.out = ws.h;
-  g.out_scales = ws.hs;
+  g.out_scales = hs;
   g.rows = s.N;
   g.n = s.F;
   g.K = s.d;
@@ -461,7 +465,7 @@ moe_status moe_fp8_forward(moe_plan_t plan, const void* x, const void* x_q, cons
   };
   if ((e = product(moe::fp8::kSwiGLU)) != cudaSuccess) return cuda_fail(e, "launching the SwiGLU product");
   g.a = static_cast<const uint8_t*>(ws.h);
-  g.sa = ws.hs;
+  g.sa = hs;
   g.b = static_cast<const uint8_t*>(w2);
   g.sb = w2_scales;
   g.b3 = nullptr;
@@ -524,7 +528,7 @@ moe_status moe_checkpoint_save(moe_plan_t plan, const void* workspace, size_t wo
   if (st != MOE_OK) return st;
   const moe::Shape& s = plan->shape;
   const CkptLayout c = ckpt_layout(s, plan->layout);
-  const moe::Ws ws = moe::ws_bind(s, const_cast<void*>(workspace));
+  const moe::Ws ws = moe::bind(s, plan->layout, const_cast<void*>(workspace));
   uint8_t* b = static_cast<uint8_t*>(ckpt);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemcpyAsync(b + c.routing, workspace, routing_bytes(s, plan->layout), cudaMemcpyDeviceToDevice, cs);
@@ -542,7 +546,7 @@ moe_status moe_checkpoint_restore(moe_plan_t plan, const void* x, const void* ck
   if (!x || !aligned(x, 16)) return fail(MOE_ERR_INVALID_ARG, "x must be a 16-byte aligned pointer");
   const moe::Shape& s = plan->shape;
   const CkptLayout c = ckpt_layout(s, plan->layout);
-  const moe::Ws ws = moe::ws_bind(s, workspace);
+  const moe::Ws ws = moe::bind(s, plan->layout, workspace);
   const uint8_t* b = static_cast<const uint8_t*>(ckpt);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemcpyAsync(workspace, b + c.routing, routing_bytes(s, plan->layout), cudaMemcpyDeviceToDevice, cs);
@@ -582,7 +586,7 @@ moe_status moe_backward_stage(moe_plan_t plan, int32_t stage, const void* x, con
   if (stage < 0 || stage >= kNumBwdStages) return fail(MOE_ERR_INVALID_ARG, "backward stage %d out of range", stage);
   if ((st = bind_device(plan)) != MOE_OK) return st;
   const moe::Shape& s = plan->shape;
-  const moe::Ws ws = moe::ws_bind(s, workspace);
+  const moe::Ws ws = moe::bind(s, plan->layout, workspace);
   const moe::Weights w{x, w_router, plan->shape.has_bias ? router_bias : nullptr, w1, w3, w2, nullptr};
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool pdl = stage > 0;  // chained to the previous backward kernel
@@ -646,7 +650,7 @@ moe_status moe_aux_loss(moe_plan_t plan, const void* workspace, float* aux_out, 
 moe_status moe_workspace_views(moe_plan_t plan, void* workspace, moe_views* v) {
   if (!plan || !workspace || !v) return fail(MOE_ERR_INVALID_ARG, "null argument");
   if (plan->expert_stage) return fail(MOE_ERR_INVALID_ARG, "an expert-stage plan's workspace has no views");
-  const moe::Ws w = moe::ws_bind(plan->shape, workspace);
+  const moe::Ws w = moe::bind(plan->shape, plan->layout, workspace);
   v->status = w.hdr + moe::kHdrStatus;
   v->aux = w.aux;
   v->topk_idx = w.topk_idx;
@@ -749,7 +753,7 @@ moe_status moe_expert_forward(moe_plan_t plan, const int32_t* seg_counts, const 
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemsetAsync(ws.hdr, 0, moe::kHdrClearWords * sizeof(uint32_t), cs);
   if (e != cudaSuccess) return cuda_fail(e, "clearing the status word");
-  if ((e = moe::launch_seg_scan(s, ws, seg_counts, plan->n_seg, s.E, false, cs)) != cudaSuccess)
+  if ((e = moe::launch_seg_scan(s, ws, seg_counts, plan->n_seg, s.E, cs)) != cudaSuccess)
     return cuda_fail(e, "launching the segment scan");
   for (int mode = 1; mode <= 2; ++mode) {
     if (plan->pair)

@@ -171,7 +171,7 @@ moe_status begin(moe_fp8_plan_t plan, const int32_t* seg_counts, void* workspace
   Shape shape{};
   shape.N = plan->rows;
   shape.max_groups = plan->max_groups;
-  return cuda_status(launch_seg_scan(shape, *ws, seg_counts, plan->n_seg, plan->E, true, st), "launching the segment scan");
+  return cuda_status(fp8::launch_segments(shape, *ws, seg_counts, plan->n_seg, plan->E, st), "launching the segment scan");
 }
 
 moe_status product(moe_fp8_plan_t plan, int kind, const fp8::GemmArgs& g, const Ws& ws, const int32_t* seg_counts, bool first,

@@ -12,6 +12,7 @@
 // rows of one expert that came from different sources never share a tile, and nothing is
 // copied into expert order first.
 #include "device_common.cuh"
+#include "fp8_internal.h"
 #include "tile_tables.cuh"
 
 namespace moe {
@@ -50,10 +51,16 @@ __global__ void __launch_bounds__(kSegThreads) seg_scan_kernel(Shape s, Ws ws, c
 }
 
 cudaError_t launch_seg_scan(const Shape& s, const Ws& ws, const int32_t* seg_counts, int n_seg, int n_local,
-                            bool clear, cudaStream_t st) {
-  return launch_kernel(seg_scan_kernel, dim3(1), dim3(kSegThreads), 0, st, clear, 1, s, ws, seg_counts, n_seg, n_local,
-                       clear ? 1 : 0);
+                            cudaStream_t st) {
+  return launch_kernel(seg_scan_kernel, dim3(1), dim3(kSegThreads), 0, st, false, 1, s, ws, seg_counts, n_seg, n_local, 0);
 }
+
+namespace fp8 {
+cudaError_t launch_segments(const Shape& s, const Ws& ws, const int32_t* seg_counts, int n_seg, int n_experts,
+                            cudaStream_t st) {
+  return launch_kernel(seg_scan_kernel, dim3(1), dim3(kSegThreads), 0, st, true, 1, s, ws, seg_counts, n_seg, n_experts, 1);
+}
+}  // namespace fp8
 
 // aux = E * sum_e (count_e / (T k)) * (psum_e / T) from per-expert totals (counts and sums of
 // the softmax over every token of every rank), reduced over the same fixed tree as the

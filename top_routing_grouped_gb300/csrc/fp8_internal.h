@@ -47,6 +47,12 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
                                     const float* rstd, const void* dresidual, bool bf16, int64_t rows, int d,
                                     int64_t ldr, void* dx, float* dweight, float* parts, cudaStream_t st);
 
+// Segment counts (null: one segment of s.N rows) -> tile tables; clears the status word first.
+cudaError_t launch_segments(const Shape& s, const Ws& ws, const int32_t* seg_counts, int n_seg, int n_experts,
+                            cudaStream_t st);
+// Dispatch of 8-bit rows x [T, d] with their factors xs into ws.xp and xs_out.
+cudaError_t launch_permute(const Shape& s, const Ws& ws, const void* x, const uint8_t* xs, uint8_t* xs_out, int num_sms,
+                           bool pdl, cudaStream_t st);
 cudaError_t launch_gemm_simt(int kind, const GemmArgs& g, const Ws& ws, int num_sms, cudaStream_t st);
 cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns,
                            bool pdl, cudaStream_t st);

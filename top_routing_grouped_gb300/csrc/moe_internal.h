@@ -32,7 +32,6 @@ struct Shape {
   int training;   // the forward keeps what the backward needs (pre-activations, softmax)
   int act_bf16;   // x and weights are bf16 (else fp32)
   int out_bf16;   // y is bf16 (else fp32)
-  int fp8;        // the experts run in 8 bits: xp and h are e4m3 with factors xs and hs
   int max_groups; // bound on the scheduling groups (sizes the tile descriptors)
 };
 
@@ -63,8 +62,6 @@ struct Ws {
   void* xp;             // [N, d]
   void* h;              // [N, F]
   void* yp;             // [N, d] gate * expert output of routed row p (expert order)
-  uint8_t* xs;          // 8-bit experts: block factors of xp, [N, scale columns of d]
-  uint8_t* hs;          // ... and of h, [N, scale columns of F]
   // training (forward keeps, backward uses)
   void* a1;             // [N, F] bf16: W1_e . x of each routed row
   void* a3;             // [N, F] bf16: W3_e . x
@@ -90,7 +87,7 @@ struct Ws {
 struct WsLayout {
   size_t hdr, aux, blk_cnt, blk_psum, local_rank, topk_idx, topk_gate, counts, offsets, ptot, blk_base,
       mt_desc, pr_desc, perm_src, perm_slot, gate_perm, slot_pos, logits, xp, h,
-      yp, xs, hs, a1, a3, probs, dyp, dop, dab, dab_tail, dop_tail, dgp, dxslot, dlogit, dl_hi, dl_lo, dwr_part, dwr_part_b, total;
+      yp, a1, a3, probs, dyp, dop, dab, dab_tail, dop_tail, dgp, dxslot, dlogit, dl_hi, dl_lo, dwr_part, dwr_part_b, total;
 };
 
 // Columns of the bf16 dlogit terms: E rounded up to 64 (a whole 128-byte TMA box).
@@ -150,17 +147,13 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
 // Kernel launchers (each returns the launch's cudaError_t).  `pdl`: see launch_kernel.
 cudaError_t launch_route_simt(const Shape& s, const Ws& ws, const Weights& w, cudaStream_t st);
 cudaError_t launch_permute(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st);
-// the same of 8-bit rows x [T, d] with their factors xs
-cudaError_t launch_permute_fp8(const Shape& s, const Ws& ws, const void* x, const uint8_t* xs, int num_sms, bool pdl,
-                               cudaStream_t st);
 cudaError_t launch_gemm1_simt(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st);
 cudaError_t launch_gemm2_simt(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st);
 cudaError_t launch_combine(const Shape& s, const Ws& ws, const Weights& w, int num_sms, bool pdl, cudaStream_t st);
-// expert stage of expert parallelism: the tile table over received segments (seg_counts null:
-// one segment of s.N rows; `clear`: the kernel clears the header first); the balancing scalar
-// from per-expert totals
+// expert stage of expert parallelism: the tile table over received segments; the balancing
+// scalar from per-expert totals
 cudaError_t launch_seg_scan(const Shape& s, const Ws& ws, const int32_t* seg_counts, int n_seg, int n_local,
-                            bool clear, cudaStream_t st);
+                            cudaStream_t st);
 cudaError_t launch_aux_totals(int E, int k, int64_t T, const int32_t* counts, const float* psum, float* aux_out,
                               cudaStream_t st);
 

@@ -10,6 +10,7 @@
 // destinations are computed by lanes 0..k-1 and broadcast, and the row is written k times
 // (x is read once).  An 8-bit row brings its block factors, a few words, along.
 #include "device_common.cuh"
+#include "fp8_internal.h"
 
 namespace moe {
 
@@ -108,12 +109,14 @@ cudaError_t launch_permute(const Shape& s, const Ws& ws, const Weights& w, int n
   return launch(s, ws, PermuteRows{w.x, ws.xp, s.d * (s.act_bf16 ? 2 : 4) / 16, nullptr, nullptr, 0}, num_sms, pdl, st);
 }
 
-cudaError_t launch_permute_fp8(const Shape& s, const Ws& ws, const void* x, const uint8_t* xs, int num_sms, bool pdl,
-                               cudaStream_t st) {
-  const int words = (s.d + 511) / 512;  // four block factors a word
+namespace fp8 {
+cudaError_t launch_permute(const Shape& s, const Ws& ws, const void* x, const uint8_t* xs, uint8_t* xs_out, int num_sms,
+                           bool pdl, cudaStream_t st) {
+  const int words = (int)(scale_cols(s.d) / 4);
   return launch(s, ws,
-                PermuteRows{x, ws.xp, s.d / 16, reinterpret_cast<const uint32_t*>(xs), reinterpret_cast<uint32_t*>(ws.xs), words},
+                PermuteRows{x, ws.xp, s.d / 16, reinterpret_cast<const uint32_t*>(xs), reinterpret_cast<uint32_t*>(xs_out), words},
                 num_sms, pdl, st);
 }
+}  // namespace fp8
 
 }  // namespace moe

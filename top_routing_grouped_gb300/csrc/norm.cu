@@ -11,8 +11,9 @@
 // A row is held in registers by W warps, eight values a thread and piece, V pieces a thread; the
 // CTAs are persistent and a row's loads are issued before the row before it is reduced, so the
 // loads of one row run under the reduction and the stores of another.  Rows of whole 16-byte
-// vectors give a thread 8 consecutive columns (kVec); others give it every 32nd of 256, so that
-// single loads and stores of a warp still touch consecutive addresses.
+// vectors give a thread 8 consecutive columns (kVec); others give it four pairs of columns 64 apart,
+// so that a warp's loads and stores of a pair (of single values, where the width is odd) still
+// touch consecutive addresses.
 #include "device_common.cuh"
 #include "fp8_common.cuh"
 #include "fp8_vec.cuh"
@@ -60,23 +61,23 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
 
 // ---------------------------------------------------------------- rows in registers
 
-// Columns of piece u of this thread: kVec: column(u) .. column(u) + 7; else 32 apart within each
-// of two blocks of 128.
-template <bool kVec, int W>
+// Columns of piece u of this thread: kVec: first(u) .. first(u) + 7; else four pairs, two in each of
+// two blocks of 128.
+template <bool kVec>
 struct Cols {
-  int warp, lane;  // warp within the row's W warps
+  int W, warp, lane;  // warps of a row, this one among them
+  bool even;          // not kVec: pairs lie on whole pairs in memory
   __device__ __forceinline__ int first(int u) const {
-    return kVec ? (u * W * 32 + warp * 32 + lane) * 8 : (u * W + warp) * 256 + lane;
+    return kVec ? ((u * W + warp) * 32 + lane) * 8 : (u * W + warp) * 256 + 2 * lane;
   }
-  __device__ __forceinline__ int col(int u, int j) const { return first(u) + (kVec ? j : 32 * j); }
+  __device__ __forceinline__ int col(int u, int j) const { return first(u) + (kVec ? j : 64 * (j / 2) + (j & 1)); }
 };
 
 // Eight values of a row as they lie in memory.
 template <bool kBf16, bool kVec>
 struct Piece {
-  uint32_t w[kBf16 && kVec ? 4 : 8];
-  template <int W>
-  __device__ __forceinline__ void load(const void* row, const Cols<kVec, W>& cs, int u, int d) {
+  uint32_t w[kBf16 ? 4 : 8];  // bf16: two to a word
+  __device__ __forceinline__ void load(const void* row, const Cols<kVec>& cs, int u, int d) {
     if constexpr (kVec) {
       const int c = cs.first(u);
       Raw8<kBf16> r;
@@ -85,21 +86,36 @@ struct Piece {
       memcpy(w, r.w, sizeof w);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = cs.col(u, j);
-        w[j] = c >= d ? 0u : kBf16 ? (uint32_t)reinterpret_cast<const uint16_t*>(row)[c] << 16
-                                   : reinterpret_cast<const uint32_t*>(row)[c];
+      for (int j = 0; j < 4; ++j) {
+        const int c = cs.col(u, 2 * j);
+        if constexpr (kBf16) {
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
+          if (cs.even)
+            w[j] = c < d ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+          else
+            w[j] = (c < d ? p[0] : 0u) | (c + 1 < d ? (uint32_t)p[1] << 16 : 0u);
+        } else {
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + c;
+          if (cs.even) {
+            const uint2 v = c < d ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
+            w[2 * j] = v.x;
+            w[2 * j + 1] = v.y;
+          } else {
+            w[2 * j] = c < d ? p[0] : 0u;
+            w[2 * j + 1] = c + 1 < d ? p[1] : 0u;
+          }
+        }
       }
     }
   }
   __device__ __forceinline__ float get(int j) const {
-    if constexpr (kBf16 && kVec) return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    if constexpr (kBf16) return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
     return __uint_as_float(w[j]);
   }
 };
 
-template <bool kBf16, bool kVec, int W>
-__device__ __forceinline__ void store8(void* row, const Cols<kVec, W>& cs, int u, int d, const float (&v)[8]) {
+template <bool kBf16, bool kVec>
+__device__ __forceinline__ void store8(void* row, const Cols<kVec>& cs, int u, int d, const float (&v)[8]) {
   if constexpr (kVec) {
     const int c = cs.first(u);
     if (c >= d) return;
@@ -112,52 +128,74 @@ __device__ __forceinline__ void store8(void* row, const Cols<kVec, W>& cs, int u
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (cs.col(u, j) < d) st<kBf16>(row, cs.col(u, j), v[j]);
+    for (int j = 0; j < 8; j += 2) {
+      const int c = cs.col(u, j);
+      if (cs.even) {
+        if (c >= d) continue;
+        if constexpr (kBf16)
+          *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(row) + c) = __floats2bfloat162_rn(v[j], v[j + 1]);
+        else
+          *reinterpret_cast<float2*>(reinterpret_cast<float*>(row) + c) = make_float2(v[j], v[j + 1]);
+      } else {
+        if (c < d) st<kBf16>(row, c, v[j]);
+        if (c + 1 < d) st<kBf16>(row, c + 1, v[j + 1]);
+      }
+    }
   }
 }
 
-template <bool kVec, int W>
-__device__ __forceinline__ void load_weight(const float* weight, const Cols<kVec, W>& cs, int u, int d, float (&v)[8]) {
+// The weight is on a 16-byte boundary whatever the rows are on.
+template <bool kVec>
+__device__ __forceinline__ void load_weight(const float* weight, const Cols<kVec>& cs, int u, int d, float (&v)[8]) {
   if (!weight) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 1.f;
-  } else {
-    Piece<false, kVec> p;
-    p.load(weight, cs, u, d);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = p.get(j);
+    return;
   }
+  Cols<kVec> c = cs;
+  c.even = (d & 1) == 0;
+  Piece<false, kVec> p;
+  p.load(weight, c, u, d);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = p.get(j);
 }
 
-// Sum over the row's W warps, the same bits in every thread.  `red` [2][W]: calls take turns
-// (`turn`), so one barrier a call is enough.
-template <int W>
-__device__ __forceinline__ float row_sum(float v, float* red, int turn, int warp, int lane) {
+// Sum over the row's W <= 16 warps, the same bits in every thread.  `red` [2][16], zero where no warp
+// writes: calls take turns (`turn`), so one barrier a call is enough.
+__device__ __forceinline__ float row_sum(float v, float* red, int turn, int W, int warp, int lane) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (W > 1) {
-    red += turn * W;
+  if (W > 1) {
+    red += turn * 16;
     if (lane == 0) red[warp] = v;
     __syncthreads();
+    const float4* r4 = reinterpret_cast<const float4*>(red);
     v = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += red[w];
+    for (int w = 0; w < 4; ++w) {
+      const float4 x = r4[w];
+      v += (x.x + x.y) + (x.z + x.w);
+    }
   }
   return v;
 }
 
-// R rows a CTA (R > 1 only with one warp a row).
-template <bool kBf16, bool kVec, int V, int W, int R>
-__global__ void __launch_bounds__(32 * W * R)
+// R = 1: a row a CTA; R > 1: a row a warp.
+template <bool kBf16, bool kVec, int V, int R>
+__global__ void __launch_bounds__(R > 1 ? 32 * R : 512)
     rmsnorm_reg_kernel(const void* x, const void* residual, const float* weight, int64_t rows, int d, int64_t ldx,
-                       int64_t ldr, float eps, void* residual_out, void* out, uint8_t* q, uint8_t* scales, float* rstd) {
-  __shared__ float red[2 * W];
+                       int64_t ldr, float eps, void* residual_out, void* out, uint8_t* q, uint8_t* scales, float* rstd, int even) {
+  __shared__ __align__(16) float red[2 * 16];
+  if (R == 1) {
+    if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
+    __syncthreads();
+  }
   constexpr int kEsz = kBf16 ? 2 : 4;
   const int lane = threadIdx.x & 31;
-  const Cols<kVec, W> cs{(int)(threadIdx.x >> 5) % W, lane};
+  const Cols<kVec> cs{R > 1 ? 1 : (int)(blockDim.x >> 5), R > 1 ? 0 : (int)(threadIdx.x >> 5), lane, even != 0};
   const int64_t sc = scale_cols(d), step = (int64_t)gridDim.x * R;
   const int nb = (d + kBlock - 1) / kBlock;
+  pdl_wait();  // an earlier kernel may write any of the inputs
   float wt[V][8];
 #pragma unroll
   for (int u = 0; u < V; ++u) load_weight(weight, cs, u, d, wt[u]);
@@ -191,7 +229,7 @@ __global__ void __launch_bounds__(32 * W * R)
 #pragma unroll
       for (int u = 0; u < V; ++u) store8<kBf16>(ro, cs, u, d, v[u]);
     }
-    const float inv = 1.f / sqrtf(row_sum<W>(ss, red, turn, cs.warp, lane) / (float)d + eps);
+    const float inv = 1.f / sqrtf(row_sum(ss, red, turn, cs.W, cs.warp, lane) / (float)d + eps);
     if (rstd && cs.warp == 0 && lane == 0) rstd[t] = inv;
     if (!out && !q) continue;
 #pragma unroll
@@ -227,9 +265,18 @@ __global__ void __launch_bounds__(32 * W * R)
           const uint32_t b = scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
           const float f = inv_scale_value(b);
 #pragma unroll
-          for (int j = 4 * hb; j < 4 * hb + 4; ++j)
-            if (cs.col(u, j) < d) q[t * d + cs.col(u, j)] = (uint8_t)pack_e4m3x2(v[u][j] * f, 0.f);
-          const int blk = (u * W + cs.warp) * 2 + hb;
+          for (int j = 4 * hb; j < 4 * hb + 4; j += 2) {
+            const int cc = cs.col(u, j);
+            const uint32_t e2 = pack_e4m3x2(v[u][j] * f, v[u][j + 1] * f);
+            uint8_t* o = q + t * d + cc;
+            if (cs.even) {
+              if (cc < d) *reinterpret_cast<uint16_t*>(o) = (uint16_t)e2;
+            } else {
+              if (cc < d) o[0] = (uint8_t)e2;
+              if (cc + 1 < d) o[1] = (uint8_t)(e2 >> 8);
+            }
+          }
+          const int blk = (u * cs.W + cs.warp) * 2 + hb;
           if (lane == 0 && blk < nb) scales[t * sc + blk] = (uint8_t)b;
         }
       }
@@ -239,15 +286,21 @@ __global__ void __launch_bounds__(32 * W * R)
 }
 
 // The CTA's sum of dweight stays in registers over its rows and leaves as one row of `parts`.
-template <bool kBf16, bool kDoutBf16, bool kVec, int V, int W, int R>
-__global__ void __launch_bounds__(32 * W * R, kBf16 && kVec && V == 1 ? 1024 / (32 * W * R) : 1)
+template <bool kBf16, bool kDoutBf16, bool kVec, int V, int R>
+__global__ void __launch_bounds__(R > 1 ? 32 * R : 512, kBf16 && kVec && V == 1 ? (R > 1 ? 4 : 2) : 1)
     rmsnorm_backward_reg_kernel(const void* dout, const void* r, const float* weight, const float* rstd,
-                                const void* dresidual, int64_t rows, int d, int64_t ldr, void* dx, float* parts) {
-  __shared__ float red[2 * W];
+                                const void* dresidual, int64_t rows, int d, int64_t ldr, void* dx, float* parts, int even) {
+  __shared__ __align__(16) float red[2 * 16];
+  if (R == 1) {
+    if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
+    __syncthreads();
+  }
   constexpr int kEsz = kBf16 ? 2 : 4, kDsz = kDoutBf16 ? 2 : 4;
   const int lane = threadIdx.x & 31;
-  const Cols<kVec, W> cs{(int)(threadIdx.x >> 5) % W, lane};
+  const Cols<kVec> cs{R > 1 ? 1 : (int)(blockDim.x >> 5), R > 1 ? 0 : (int)(threadIdx.x >> 5), lane, even != 0};
   const int64_t step = (int64_t)gridDim.x * R;
+  pdl_wait();
+  pdl_launch_dependents();
   float wt[V][8], dw[V][8];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
@@ -289,7 +342,7 @@ __global__ void __launch_bounds__(32 * W * R, kBf16 && kVec && V == 1 ? 1024 / (
       }
     }
     if (t + step < rows) fetch(t + step);
-    const float m = row_sum<W>(dot, red, turn, cs.warp, lane) / (float)d;
+    const float m = row_sum(dot, red, turn, cs.W, cs.warp, lane) / (float)d;
     char* o = reinterpret_cast<char*>(dx) + t * d * kEsz;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
@@ -311,7 +364,7 @@ __global__ void __launch_bounds__(32 * W * R, kBf16 && kVec && V == 1 ? 1024 / (
       if (c < 256) all[threadIdx.x >> 5][c] = dw[0][j];
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < d; c += 32 * W * R) {
+    for (int c = threadIdx.x; c < d; c += 32 * R) {
       float a = 0.f;
 #pragma unroll
       for (int w = 0; w < R; ++w) a += all[w][c];
@@ -407,32 +460,44 @@ __global__ void __launch_bounds__(kThreads)
     for (int c = threadIdx.x; c < d; c += kThreads) parts[(int64_t)blockIdx.x * d + c] = dw_s[c];
 }
 
-// dweight[c] = the n partial sums of column c: 32 columns a CTA, each warp an eighth of the parts
-// in order, then the eight in order.
-__global__ void __launch_bounds__(kThreads) dweight_sum_kernel(const float* parts, int n, int d, float* dweight) {
-  __shared__ float all[kWarps][32];
+// dweight[c] = the n partial sums of column c: 32 columns a CTA, each of its 32 warps a
+// thirty-second of the parts in order, then the 32 in order.
+__global__ void __launch_bounds__(1024) dweight_sum_kernel(const float* parts, int n, int d, float* dweight) {
+  __shared__ float all[32][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   pdl_wait();
   float s = 0.f;
   if (c < d) {
-    const int end = (int)((int64_t)n * (warp + 1) / kWarps);
+    const int end = (int)((int64_t)n * (warp + 1) / 32);
 #pragma unroll 8
-    for (int p = (int)((int64_t)n * warp / kWarps); p < end; ++p) s += parts[(int64_t)p * d + c];
+    for (int p = (int)((int64_t)n * warp / 32); p < end; ++p) s += parts[(int64_t)p * d + c];
   }
   all[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < d) {
     s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += all[w][lane];
+    for (int w = 0; w < 32; ++w) s += all[w][lane];
     dweight[c] = s;
   }
 }
 
 }  // namespace
 
-// Persistent CTAs: what 152 SMs hold of CTAs of this many threads (at about 64 registers a thread).
-static int resident(int threads) { return 152 * (1024 / threads); }
+// Threads of a CTA for a row of d columns held in registers: a warp for every 256 columns, two pieces
+// a thread above 4096.
+static int pieces(int d) { return d <= 4096 ? 1 : 2; }
+static int row_threads(int d) {
+  if (d <= 256) return 256;  // eight rows of a warp each
+  const int per_warp = 256 * pieces(d);
+  return (d + per_warp - 1) / per_warp * 32;
+}
+
+// Persistent CTAs: what 152 SMs hold of them, at about 64 registers a thread, 128 with two pieces.
+static int resident(int d) {
+  const int threads = row_threads(d), most = pieces(d) == 1 ? 1024 : 512;
+  return 152 * (most / threads);
+}
 
 struct NormArgs {
   const void *x, *residual;
@@ -446,28 +511,26 @@ struct NormArgs {
   float* rstd;
 };
 
-template <bool kBf16, bool kVec, int V, int W, int R>
-static cudaError_t norm_reg(const NormArgs& a, cudaStream_t st) {
+template <bool kBf16, bool kVec, int V, int R>
+static cudaError_t norm_reg(const NormArgs& a, bool even, cudaStream_t st) {
+  const int threads = row_threads(a.d);
   const int64_t want = (a.rows + R - 1) / R;
-  const int64_t grid = want < resident(32 * W * R) ? want : resident(32 * W * R);
-  return launch_kernel(rmsnorm_reg_kernel<kBf16, kVec, V, W, R>, dim3((unsigned)grid), dim3(32 * W * R), 0, st, false, 1, a.x,
-                       a.residual, a.weight, a.rows, a.d, a.ldx, a.ldr, a.eps, a.residual_out, a.out, a.q, a.scales, a.rstd);
+  const int64_t grid = want < resident(a.d) ? want : resident(a.d);
+  return launch_kernel(rmsnorm_reg_kernel<kBf16, kVec, V, R>, dim3((unsigned)grid), dim3(threads), 0, st, true, 1, a.x,
+                       a.residual, a.weight, a.rows, a.d, a.ldx, a.ldr, a.eps, a.residual_out, a.out, a.q, a.scales, a.rstd,
+                       even ? 1 : 0);
 }
 
-// The fewest threads that hold the row at eight values a thread (two pieces above 4096 columns);
-// rows of up to 256 take a warp each.
 template <bool kBf16, bool kVec>
-static cudaError_t norm_width(const NormArgs& a, cudaStream_t st) {
-  if (a.d <= 256) return norm_reg<kBf16, kVec, 1, 1, 8>(a, st);
-  if (a.d <= 1024) return norm_reg<kBf16, kVec, 1, 4, 1>(a, st);
-  if (a.d <= 2048) return norm_reg<kBf16, kVec, 1, 8, 1>(a, st);
-  if (a.d <= 4096) return norm_reg<kBf16, kVec, 1, 16, 1>(a, st);
-  return norm_reg<kBf16, kVec, 2, 16, 1>(a, st);
+static cudaError_t norm_width(const NormArgs& a, bool even, cudaStream_t st) {
+  if (a.d <= 256) return norm_reg<kBf16, kVec, 1, 8>(a, even, st);
+  return pieces(a.d) == 1 ? norm_reg<kBf16, kVec, 1, 1>(a, even, st) : norm_reg<kBf16, kVec, 2, 1>(a, even, st);
 }
 
-// Rows on whole 16-byte vectors.
-static bool vectors(const void* p, bool bf16, int64_t ld) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % (bf16 ? 8 : 4) == 0);
+// Rows that lie on whole groups of `n` values (8: vectors, 2: pairs); a missing tensor does.
+static bool on(int n, const void* p, bool bf16, int64_t ld) {
+  const int per = n == 8 && !bf16 ? 4 : n;  // eight fp32 are two vectors
+  return !p || (reinterpret_cast<uintptr_t>(p) % (per * (bf16 ? 2 : 4)) == 0 && ld % per == 0);
 }
 
 cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* weight, bool bf16, int64_t rows, int d,
@@ -475,10 +538,12 @@ cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* wei
                            float* rstd, cudaStream_t st) {
   if (d <= kMaxRegCols) {
     const NormArgs a{x, residual, weight, rows, d, ldx, ldr, eps, residual_out, out, (uint8_t*)q, scales, rstd};
-    const bool vec = d % 8 == 0 && vectors(x, bf16, ldx) && vectors(residual, bf16, ldr) && vectors(residual_out, bf16, d) &&
-                     vectors(out, bf16, d);
-    return bf16 ? (vec ? norm_width<true, true>(a, st) : norm_width<true, false>(a, st))
-                : (vec ? norm_width<false, true>(a, st) : norm_width<false, false>(a, st));
+    auto all = [&](int n) {
+      return d % n == 0 && on(n, x, bf16, ldx) && on(n, residual, bf16, ldr) && on(n, residual_out, bf16, d) && on(n, out, bf16, d);
+    };
+    const bool vec = all(8), even = all(2);
+    return bf16 ? (vec ? norm_width<true, true>(a, even, st) : norm_width<true, false>(a, even, st))
+                : (vec ? norm_width<false, true>(a, even, st) : norm_width<false, false>(a, even, st));
   }
   const size_t smem = (size_t)d * sizeof(float);
   auto kern = bf16 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>;
@@ -496,7 +561,7 @@ cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* wei
 // the shape alone, and so does the order of the sum.
 int rmsnorm_backward_parts(int64_t rows, int d) {
   const int per_cta = d <= 256 ? 8 : 1;
-  const int64_t most = resident(d <= 256 ? 256 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= kMaxRegCols ? 512 : 256);
+  const int64_t most = d <= kMaxRegCols ? resident(d) : 152 * 2;
   const int64_t want = (rows + 2 * per_cta - 1) / (2 * per_cta);
   return (int)(want < most ? want : most);
 }
@@ -512,26 +577,24 @@ struct NormBwdArgs {
   float* parts;
 };
 
-template <bool kBf16, bool kDoutBf16, bool kVec, int V, int W, int R>
-static cudaError_t norm_bwd_reg(const NormBwdArgs& a, cudaStream_t st) {
-  return launch_kernel(rmsnorm_backward_reg_kernel<kBf16, kDoutBf16, kVec, V, W, R>,
-                       dim3((unsigned)rmsnorm_backward_parts(a.rows, a.d)), dim3(32 * W * R), 0, st, false, 1, a.dout, a.r,
-                       a.weight, a.rstd, a.dresidual, a.rows, a.d, a.ldr, a.dx, a.parts);
+template <bool kBf16, bool kDoutBf16, bool kVec, int V, int R>
+static cudaError_t norm_bwd_reg(const NormBwdArgs& a, bool even, cudaStream_t st) {
+  return launch_kernel(rmsnorm_backward_reg_kernel<kBf16, kDoutBf16, kVec, V, R>,
+                       dim3((unsigned)rmsnorm_backward_parts(a.rows, a.d)), dim3(row_threads(a.d)), 0, st, true, 1, a.dout, a.r,
+                       a.weight, a.rstd, a.dresidual, a.rows, a.d, a.ldr, a.dx, a.parts, even ? 1 : 0);
 }
 
 template <bool kBf16, bool kDoutBf16, bool kVec>
-static cudaError_t norm_bwd_width(const NormBwdArgs& a, cudaStream_t st) {
-  if (a.d <= 256) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 1, 8>(a, st);
-  if (a.d <= 1024) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 4, 1>(a, st);
-  if (a.d <= 2048) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 8, 1>(a, st);
-  if (a.d <= 4096) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 16, 1>(a, st);
-  return norm_bwd_reg<kBf16, kDoutBf16, kVec, 2, 16, 1>(a, st);
+static cudaError_t norm_bwd_width(const NormBwdArgs& a, bool even, cudaStream_t st) {
+  if (a.d <= 256) return norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 8>(a, even, st);
+  return pieces(a.d) == 1 ? norm_bwd_reg<kBf16, kDoutBf16, kVec, 1, 1>(a, even, st)
+                          : norm_bwd_reg<kBf16, kDoutBf16, kVec, 2, 1>(a, even, st);
 }
 
 template <bool kVec>
-static cudaError_t norm_bwd_types(const NormBwdArgs& a, bool bf16, bool dout_bf16, cudaStream_t st) {
-  return bf16 ? (dout_bf16 ? norm_bwd_width<true, true, kVec>(a, st) : norm_bwd_width<true, false, kVec>(a, st))
-              : (dout_bf16 ? norm_bwd_width<false, true, kVec>(a, st) : norm_bwd_width<false, false, kVec>(a, st));
+static cudaError_t norm_bwd_types(const NormBwdArgs& a, bool bf16, bool dout_bf16, bool even, cudaStream_t st) {
+  return bf16 ? (dout_bf16 ? norm_bwd_width<true, true, kVec>(a, even, st) : norm_bwd_width<true, false, kVec>(a, even, st))
+              : (dout_bf16 ? norm_bwd_width<false, true, kVec>(a, even, st) : norm_bwd_width<false, false, kVec>(a, even, st));
 }
 
 cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void* r, const float* weight,
@@ -541,9 +604,11 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
   cudaError_t e = cudaSuccess;
   if (n > 0 && d <= kMaxRegCols) {
     const NormBwdArgs a{dout, r, weight, rstd, dresidual, rows, d, ldr, dx, dweight ? parts : nullptr};
-    const bool vec = d % 8 == 0 && vectors(dout, dout_bf16, d) && vectors(r, bf16, ldr) && vectors(dresidual, bf16, d) &&
-                     vectors(dx, bf16, d);
-    e = vec ? norm_bwd_types<true>(a, bf16, dout_bf16, st) : norm_bwd_types<false>(a, bf16, dout_bf16, st);
+    auto all = [&](int k) {
+      return d % k == 0 && on(k, dout, dout_bf16, d) && on(k, r, bf16, ldr) && on(k, dresidual, bf16, d) && on(k, dx, bf16, d);
+    };
+    const bool vec = all(8), even = all(2);
+    e = vec ? norm_bwd_types<true>(a, bf16, dout_bf16, even, st) : norm_bwd_types<false>(a, bf16, dout_bf16, even, st);
   } else if (n > 0) {
     const size_t smem = (size_t)d * sizeof(float);
     auto kern = bf16 ? (dout_bf16 ? rmsnorm_backward_kernel<true, true> : rmsnorm_backward_kernel<true, false>)
@@ -555,7 +620,7 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
                       ldr, dx, dweight ? parts : nullptr);
   }
   if (e != cudaSuccess || !dweight) return e;
-  return launch_kernel(dweight_sum_kernel, dim3((unsigned)((d + 31) / 32)), dim3(kThreads), 0, st, n > 0, 1,
+  return launch_kernel(dweight_sum_kernel, dim3((unsigned)((d + 31) / 32)), dim3(1024), 0, st, n > 0, 1,
                        (const float*)parts, n, d, dweight);
 }
 

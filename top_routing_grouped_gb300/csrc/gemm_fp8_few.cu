@@ -14,6 +14,11 @@
 // shares a unit: each sums a part of K, and the first CTA adds the others' sums, which arrive in
 // its shared memory, in rank order.
 //
+// What bounds it: HBM while the weights stream (1500 rows over 128 experts of 2048 x 1024: 128 us,
+// 6.2 TB/s of weights, rows and results); with one unit for each SM the fixed part counts, about 5 us of
+// a launch (one token of 64 experts of 4096 x 2048: 26 us for 101 MB; 13 x 2064 x 8208: 7.7 us for
+// 17 MB).  The CTA pairs take 171, 43 and 15 us for the three.
+//
 // Roles of a CTA: a TMA thread (ring of stages), an MMA warp (one elected lane issues), eight
 // epilogue warps and four warps that store the block factors to TMEM, as in gemm_fp8_tc.cu.  Waits are
 // bounded (MOE_ERR_TIMEOUT, no trap).

@@ -17,8 +17,7 @@
 // load of words serves 512 k's.  Four warps of each CTA, one for each TMEM lane quarter, gather the
 // words of the CTA's 128 rows and of the tile's two blocks of weight rows and store them to TMEM (the
 // same words in every quarter; column c of a group of four belongs to rows 32c..32c+31) up to four
-// groups ahead of the MMAs.  Copies from shared memory (tcgen05.cp) instead stood in the MMA pipe's
-// order and left it idle 11-16 % of the time.
+// groups ahead of the MMAs (two sets instead of four: 5-7 % slower).
 //
 // TMEM.  The sets take 64 columns, so the two accumulators of 256 columns overlap by 64: the
 // epilogue warps that own those columns read them first and hand them over before they go on, and
@@ -27,6 +26,20 @@
 // SwiGLU epilogue: the 128 columns of a tile are one block of each hidden row.  Two warps share a
 // row's 128 values (64 each), agree on the largest one through shared memory, and write e4m3 and
 // one factor byte, so the hidden rows cost N*F bytes instead of 2*N*F twice.
+//
+// What bounds it.  At the full MMA rate the ring alone moves 64 bytes a clock into shared memory and
+// the MMAs read 64 out of it, all that it has; the output tiles pass through it too (staging, TMA
+// store).  Counted in clocks on 8192 x 8192 x 2048 (64 K blocks a tile) the MMAs run 87 % of the time
+// and 98 % in a build without loads, hand-over and stores; on 8192 x 2048 x 8192 (16 K blocks a tile) 73 %:
+// handing over the shared columns costs about 700 clocks of 11400 a tile (2000 in a build without
+// loads), the output's way through shared memory 1300.  Times: 98 us for 8192 x 2048 x 8192 (2.8
+// PFLOP/s), 88 us for 8192 x 4096 x 4096 (3.1), 2.4 ms for 131072 rows of 64 experts of 4096 x 2048 (2.75,
+// at 1.55 GHz under the power cap).
+//
+// Tried and dropped: 224-wide tiles, whose accumulators share no columns (the ring's time per K block
+// does not shrink with the tile: 98 -> 106 us); the output stored from registers, 32 bytes a lane
+// (99 -> 106 us); five stages and two store blocks a warp, L2 eviction priorities for A and the output
+// (no difference beyond noise).
 //
 // Waits are bounded (MOE_ERR_TIMEOUT, no trap); an abort raises the flag in both CTAs; the pair
 // meets at cluster barriers before TMEM is released.

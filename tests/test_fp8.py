@@ -338,19 +338,24 @@ def test_matmul_nan_and_extreme_factors_stay_in_their_rows(fp8, path):
 
 
 @pytest.mark.parametrize("path", ["simt", "auto"])
-@pytest.mark.parametrize("seg", [[5, -1, 3], [60, 30, 11]], ids=["negative", "too many"])
-def test_bad_counts_are_reported_and_compute_nothing(fp8, path, seg):
-    n, K, N = 100, 128, 64
-    (qa, sa), (qw, sw) = make_rows(n, K, 29), make_weights(3, N, K, 30)
-    plan = fp8.Fp8MatmulPlan(n, K, N, n_experts=3, path=path)
+@pytest.mark.parametrize("n, N", [(100, 64), (3000, 1040)], ids=["few rows", "many"])
+@pytest.mark.parametrize("seg", [[5, -1, 3], [0.6, 0.3, 0.2], [1 << 30] * 4, [0x7FFFFFFF, 0x7FFFFFFF, 2]],
+                         ids=["negative", "too many", "wraps to 0", "wraps to 0 again"])
+def test_bad_counts_are_reported_and_compute_nothing(fp8, path, n, N, seg):
+    K, E = 128, len(seg)
+    seg = [int(c * n) if isinstance(c, float) else c for c in seg]
+    (qa, sa), (qw, sw) = make_rows(n, K, 29), make_weights(E, N, K, 30)
+    plan = fp8.Fp8MatmulPlan(n, K, N, n_experts=E, path=path)
     o, ws = torch.full((n, N), 5.0, dtype=BF, device="cuda"), plan.new_workspace()
     t = [x.cuda() for x in (*ref.to_torch(qa, sa), *ref.to_torch(qw, sw))]
     plan.forward(torch.tensor(seg, dtype=torch.int32, device="cuda"), *t, o, ws)
     from top_routing_grouped_gb300 import moe
     assert plan.device_status(ws) == moe.MOE_ERR_INTERNAL
     assert (o == 5).all()
-    plan.forward(torch.tensor([50, 30, 20], dtype=torch.int32, device="cuda"), *t, o, ws)  # the next call is clean
-    assert plan.device_status(ws) == 0
+    good = torch.zeros(E, dtype=torch.int32)
+    good[0], good[1] = n - 30, 30
+    plan.forward(good.cuda(), *t, o, ws)  # the next call is clean
+    assert plan.device_status(ws) == 0 and not (o == 5).all(1).any()
 
 
 EXPERTS = [  # segments' rows, E, d, F

@@ -119,7 +119,7 @@ moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E
   if (tc && (k % 16 != 0 || n % 16 != 0))
     return fail(MOE_ERR_UNSUPPORTED, "the tensor-core path needs multiples of 16 columns (use MOE_PATH_SIMT)");
   const int64_t widest = k > n ? k : n;
-  if (rows > INT32_MAX / 2 || rows > ((int64_t)1 << 40) / widest || (int64_t)E * widest > INT32_MAX / 2)
+  if (rows > INT32_MAX / 2 || rows > ((int64_t)1 << 40) / widest || (int64_t)E * widest > INT32_MAX / 8)
     return fail(MOE_ERR_UNSUPPORTED, "too many rows or weight rows");
   moe_fp8_plan_s* p = new (std::nothrow) moe_fp8_plan_s();
   if (!p) return fail(MOE_ERR_INTERNAL, "out of host memory");

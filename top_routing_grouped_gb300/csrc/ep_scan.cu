@@ -20,8 +20,9 @@ namespace moe {
 constexpr int kSegThreads = kMaxExperts;  // one thread per segment (W * E_l <= 256)
 
 // One CTA: segment counts (device input; null: one segment of all s.N rows) -> counts, offsets,
-// tile tables, header totals; with `clear` also the header's clear before them.  A negative count or a total beyond the plan's row capacity is reported (MOE_ERR_INTERNAL, site
-// 0x740) and leaves empty tile tables, so that no GEMM reads outside the buffers.
+// tile tables, header totals; with `clear` also the header's clear before them.  A negative count
+// or a total beyond the plan's row capacity is reported (MOE_ERR_INTERNAL, site 0x740) and leaves
+// empty tile tables, so that no GEMM reads outside the buffers.
 __global__ void __launch_bounds__(kSegThreads) seg_scan_kernel(Shape s, Ws ws, const int32_t* seg_counts, int n_seg,
                                                                int n_local, int clear) {
   __shared__ int cnt_s[kMaxExperts], offs_s[kMaxExperts];

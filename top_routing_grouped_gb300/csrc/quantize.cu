@@ -133,6 +133,49 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_vec_kernel(QuantizeJob
   }
 }
 
+// Weights on whole vectors: a CTA holds its 128 x 128 block in registers (a thread eight rows' eight
+// columns) between the maximum and the rounding, and reads it once.
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads) quantize_blocks_vec_kernel(const void* x, int cols, int64_t ldx,
+                                                                       int64_t expert_rows, int64_t n_blocks, uint8_t* q,
+                                                                       uint8_t* scales) {
+  __shared__ uint32_t top_s[kWarps];
+  const int64_t sc = scale_cols(cols), nb = (expert_rows + kBlock - 1) / kBlock;
+  const int l16 = threadIdx.x & 15, r16 = threadIdx.x >> 4;
+  for (int64_t i = blockIdx.x; i < n_blocks; i += gridDim.x) {
+    const int64_t e = i / (nb * sc), r0 = i / sc % nb * kBlock;
+    const int c = (int)(i % sc) * kBlock + l16 * 8;
+    Raw8<kBf16> raw[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t r = r0 + 16 * j + r16;
+      raw[j].zero();
+      if (r < expert_rows && c < cols) raw[j].load(x, (e * expert_rows + r) * ldx + c);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, raw[j].top());
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) top_s[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = max(top, top_s[w]);
+    const uint32_t b = scale_byte(__uint_as_float(top));
+    const float f = inv_scale_value(b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t r = r0 + 16 * j + r16;
+      const Eight v = raw[j].get();
+      if (r < expert_rows && c < cols)
+        *reinterpret_cast<uint2*>(q + (e * expert_rows + r) * cols + c) =
+            make_uint2(pack_e4m3x4(v.v[0] * f, v.v[1] * f, v.v[2] * f, v.v[3] * f),
+                       pack_e4m3x4(v.v[4] * f, v.v[5] * f, v.v[6] * f, v.v[7] * f));
+    }
+    if (threadIdx.x == 0) scales[i] = (uint8_t)b;
+    __syncthreads();  // top_s is read before the next block overwrites it
+  }
+}
+
 // da = dh b silu'(a), db = dh silu(a), h = silu(a) b of one value.
 __device__ __forceinline__ void swiglu_backward(float a, float b, float g, float& da, float& db, float& h) {
   float s, c;
@@ -270,6 +313,9 @@ cudaError_t launch_quantize_rows(const void* x, bool bf16, int64_t rows, int64_t
 cudaError_t launch_quantize_blocks(const void* x, bool bf16, int64_t rows, int64_t cols, int64_t ldx,
                                    int64_t expert_rows, void* q, uint8_t* scales, cudaStream_t st) {
   const int64_t n = rows / expert_rows * ((expert_rows + kBlock - 1) / kBlock) * scale_cols(cols);
+  if (vectors(x, bf16, cols, ldx))
+    return launch_kernel(bf16 ? quantize_blocks_vec_kernel<true> : quantize_blocks_vec_kernel<false>, dim3(grid_for(n, 1)),
+                         dim3(kThreads), 0, st, false, 1, x, (int)cols, ldx, expert_rows, n, (uint8_t*)q, scales);
   return launch_kernel(quantize_blocks_kernel, dim3(grid_for(n, 1)), dim3(kThreads), 0, st, false, 1, x, bf16 ? 1 : 0,
                        cols, ldx, expert_rows, n, (uint8_t*)q, scales);
 }

@@ -165,26 +165,50 @@ def test_checkpoint_refusals(fp8):
     assert L.moe_checkpoint_save_rows(*A[:2], 4, 0, *A[2:6], None) == INVALID
 
 
+class OnGpu(torch.Tensor):
+    """A host tensor that says it lies in GPU memory: what the binding turns down for other reasons."""
+    is_cuda = True
+
+
 def test_binding_checks_types_shapes_and_layouts(fp8):
     """The binding turns wrong tensors down before their addresses are used."""
-    x = torch.zeros(4, 64)
-    q, s = torch.zeros(4, 64, dtype=torch.uint8).view(fp8.E4M3), torch.zeros(4, 4, dtype=torch.uint8)
+    g = lambda t: t.as_subclass(OnGpu)
+    x = g(torch.zeros(4, 64))
+    q, s = g(torch.zeros(4, 64, dtype=torch.uint8).view(fp8.E4M3)), g(torch.zeros(4, 4, dtype=torch.uint8))
+    one = g(torch.ones(4))
     bad = [lambda: fp8.quantize(x.double(), q, s), lambda: fp8.quantize(x, q[:, :32], s), lambda: fp8.quantize(x, x, s),
-           lambda: fp8.quantize(x, q, s[:, :1]), lambda: fp8.quantize(x.t(), q.view(torch.uint8).t().contiguous().view(fp8.E4M3), s),
+           lambda: fp8.quantize(x, q, s[:, :1]), lambda: fp8.quantize(x, q, None),
+           lambda: fp8.quantize(x.t(), g(torch.zeros(64, 4, dtype=torch.uint8).view(fp8.E4M3)), s),
            lambda: fp8.quantize(x[:1].expand(4, 64), q, s),
-           lambda: fp8.rmsnorm(x, torch.ones(63), out=x), lambda: fp8.rmsnorm(x, None, out=torch.zeros(64, 4).t()),
+           lambda: fp8.rmsnorm(x, g(torch.ones(63)), out=x), lambda: fp8.rmsnorm(x, None, out=g(torch.zeros(64, 4)).t()),
            lambda: fp8.rmsnorm(x, None, residual=x.bfloat16(), out=x), lambda: fp8.rmsnorm(x.view(-1), None, out=x),
-           lambda: fp8.rmsnorm_backward(x[:3], x, None, torch.ones(4), x), lambda: fp8.rmsnorm_backward(x, x, None, torch.ones(3), x),
-           lambda: fp8.checkpoint_save(x, x, q, s, q, s), lambda: fp8.checkpoint_backward(q, s, q, s, x, x, x)]
+           lambda: fp8.rmsnorm_backward(x[:3], x, None, one, x), lambda: fp8.rmsnorm_backward(x, x, None, one[:3], x),
+           lambda: fp8.checkpoint_save(x, x, q, s, q, s), lambda: fp8.checkpoint_backward(q, s, q, s, x, x, x),
+           lambda: fp8.checkpoint_restore(q, s, q, s, x)]
     for i, f in enumerate(bad):
         with pytest.raises(ValueError) as ei:
             f()
-        assert "must be a" in str(ei.value) and "GPU" not in str(ei.value), i
-    with pytest.raises(ValueError, match="GPU memory"):  # nothing wrong but where the tensors are
-        fp8.quantize(x, q, s)
+        assert "must be a" in str(ei.value), i
     plan = fp8.Fp8MatmulPlan(4, 64, 32)
-    with pytest.raises(ValueError):
-        plan.forward(None, q, s, torch.zeros(1, 32, 64).to(fp8.E4M3), s, torch.zeros(4, 32), torch.zeros(1 << 16, dtype=torch.uint8))
+    w, out = g(torch.zeros(1, 32, 64).to(fp8.E4M3)), g(torch.zeros(4, 32, dtype=torch.bfloat16))
+    sw, ws = g(torch.zeros(1, 1, 4, dtype=torch.uint8)), g(torch.zeros(1 << 16, dtype=torch.uint8))
+    for args in ((None, q, s, w, s, out, ws), (None, q, s, w, sw, out.float(), ws), (one, q, s, w, sw, out, ws),
+                 (None, q[:3], s, w, sw, out, ws), (None, q, s, w, sw, out, ws.float())):
+        with pytest.raises(ValueError):
+            plan.forward(*args)
+
+
+def test_binding_refuses_host_memory(fp8):
+    """Nothing wrong but where a tensor lies."""
+    x, q, s = torch.zeros(4, 64), torch.zeros(4, 64, dtype=torch.uint8).view(fp8.E4M3), torch.zeros(4, 4, dtype=torch.uint8)
+    g = lambda t: t.as_subclass(OnGpu)
+    for args in ((x, g(q), g(s)), (g(x), q, g(s)), (g(x), g(q), s)):
+        with pytest.raises(ValueError, match="GPU memory"):
+            fp8.quantize(*args)
+    with pytest.raises(ValueError, match="GPU memory"):
+        fp8.rmsnorm(g(x), torch.ones(64), out=g(x))
+    with pytest.raises(ValueError, match="GPU memory"):
+        fp8.rmsnorm_backward(g(x), g(x), None, g(torch.ones(4)), g(x), g(torch.ones(64)), torch.zeros(4096, dtype=torch.uint8))
 
 
 def test_layer_plan_and_forward_refusals(fp8):

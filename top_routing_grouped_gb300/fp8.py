@@ -66,26 +66,20 @@ def _want(cond, what):
 _raw_stream = torch._C._cuda_getCurrentRawStream  # an order cheaper than building a torch.cuda.Stream
 
 
-def _stream(stream, *tensors):
-    """The given stream, or the current one of the tensors' device; refuses tensors in host memory."""
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("every tensor must be in GPU memory")
-    return _raw_stream(tensors[0].get_device()) if stream is None else stream.cuda_stream
-
-
 # The checks below run on every call, and a call of a few rows takes the GPU two or three
 # microseconds: messages are put together only when a check has failed.
 
-def _refuse(name, shape, dtypes, how):
+def _refuse(t, shape, dtypes, name, how):
+    if t is not None and not t.is_cuda:
+        raise ValueError(f"{name} must be in GPU memory")
     raise ValueError(f"{name} must be a {how} {tuple(shape)} tensor of {' or '.join(str(d) for d in dtypes)}")
 
 
 def _rows(t, shape, dtypes, name):
-    """The address of a row-major contiguous tensor of this shape and type."""
-    if t is None or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
-        _refuse(name, shape, dtypes, "contiguous")
-    return t.data_ptr()
+    """The address of a row-major contiguous GPU tensor of this shape and type."""
+    if t is not None and t.dtype in dtypes and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, shape, dtypes, name, "contiguous")
 
 
 def _maybe(t, shape, dtypes, name):
@@ -93,16 +87,26 @@ def _maybe(t, shape, dtypes, name):
 
 
 def _pitched(t, shape, dtypes, name):
-    """(address, row pitch) of a 2-D tensor whose rows are contiguous and separate."""
-    if t.dtype not in dtypes or t.shape != shape:
-        _refuse(name, shape, dtypes, "row-contiguous")
-    n, c = shape
-    pitch, step = t.stride()
-    if n <= 1 and pitch < c:
-        pitch = c
-    if (step != 1 and c > 1) or pitch < c:
-        _refuse(name, shape, dtypes, "row-contiguous")
-    return t.data_ptr(), pitch
+    """(address, row pitch) of a 2-D GPU tensor whose rows are contiguous and separate."""
+    if t.dtype in dtypes and t.shape == shape and t.is_cuda:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        pitch, step = t.stride()
+        if (step == 1 or shape[1] == 1) and (pitch >= shape[1] or shape[0] == 1):
+            return t.data_ptr(), max(pitch, shape[1])
+    _refuse(t, shape, dtypes, name, "row-contiguous")
+
+
+def _bytes(t):
+    """The address of a workspace or checkpoint."""
+    if t.dtype is not torch.uint8 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspaces and checkpoints must be contiguous uint8 tensors in GPU memory")
+    return t.data_ptr()
+
+
+def _stream(stream, t):
+    """The given stream, or the current one of t's device."""
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def scale_cols(cols):
@@ -115,7 +119,7 @@ def quantize(x, q, scales, stream=None):
     n, c = x.shape
     px, ldx = _pitched(x, (n, c), _FLOATS, "x")
     _check(_quantize(px, _DTYPES[x.dtype], n, c, ldx, 1, 0, _rows(q, (n, c), _E4, "q"),
-                     _rows(scales, (n, scale_cols(c)), _SCALES, "scales"), _stream(stream, x, q, scales)), "moe_fp8_quantize")
+                     _rows(scales, (n, scale_cols(c)), _SCALES, "scales"), _stream(stream, x)), "moe_fp8_quantize")
 
 
 def quantize_weights(w, q, scales, stream=None):
@@ -123,7 +127,7 @@ def quantize_weights(w, q, scales, stream=None):
     E, n, c = w.shape
     _check(_quantize(_rows(w, (E, n, c), _FLOATS, "w"), _DTYPES[w.dtype], E * n, c, c, 128, n,
                      _rows(q, (E, n, c), _E4, "q"),
-                     _rows(scales, (E, (n + 127) // 128, scale_cols(c)), _SCALES, "scales"), _stream(stream, w, q, scales)),
+                     _rows(scales, (E, (n + 127) // 128, scale_cols(c)), _SCALES, "scales"), _stream(stream, w)),
            "moe_fp8_quantize")
 
 
@@ -140,7 +144,7 @@ def rmsnorm(x, weight, residual=None, residual_out=None, out=None, q=None, scale
                     _maybe(residual_out, (T, d), t, "residual_out"), _maybe(out, (T, d), t, "out"),
                     _maybe(q, (T, d), _E4, "q"),
                     _maybe(scales, (T, scale_cols(d)), _SCALES, "scales"),
-                    _maybe(rstd, (T,), _F32, "rstd"), _stream(stream, x, weight, residual, residual_out, out, q, scales, rstd)), "moe_rmsnorm")
+                    _maybe(rstd, (T,), _F32, "rstd"), _stream(stream, x)), "moe_rmsnorm")
 
 
 def rmsnorm_backward_workspace(T, d, device="cuda"):
@@ -159,8 +163,8 @@ def rmsnorm_backward(dout, r, weight, rstd, dx, dweight=None, workspace=None, dr
     pd = _rows(dout, (T, d), _FLOATS, "dout")
     _check(_rmsnorm_bwd(pd, _DTYPES[dout.dtype], pr, _maybe(weight, (d,), f32, "weight"), _rows(rstd, (T,), f32, "rstd"),
                         _maybe(dresidual, (T, d), t, "dresidual"), _DTYPES[r.dtype], T, d, ldr, _rows(dx, (T, d), t, "dx"),
-                        _maybe(dweight, (d,), f32, "dweight"), None if workspace is None else workspace.data_ptr(),
-                        0 if workspace is None else workspace.numel(), _stream(stream, dout, r, weight, rstd, dx, dweight, workspace, dresidual)), "moe_rmsnorm_backward")
+                        _maybe(dweight, (d,), f32, "dweight"), None if workspace is None else _bytes(workspace),
+                        0 if workspace is None else workspace.numel(), _stream(stream, dout)), "moe_rmsnorm_backward")
 
 
 class _Fp8Plan:
@@ -184,7 +188,7 @@ class _Fp8Plan:
 
     def device_status(self, workspace, stream=None):
         """Synchronises the stream; returns the status code (MOE_OK == 0)."""
-        return _device_status(self._h, workspace.data_ptr(), _stream(stream, workspace))
+        return _device_status(self._h, _bytes(workspace), _stream(stream, workspace))
 
 
 class Fp8MatmulPlan(_Fp8Plan):
@@ -206,8 +210,8 @@ class Fp8MatmulPlan(_Fp8Plan):
         _check(_matmul(self._h, _maybe(seg_counts, self._seg, (torch.int32,), "seg_counts"),
                        _rows(a, self._a, _E4, "a"), _rows(a_scales, self._sa, _SCALES, "a_scales"),
                        _rows(w, self._w, _E4, "w"), _rows(w_scales, self._sw, _SCALES, "w_scales"),
-                       _rows(out, self._out, (self.out_dtype,), "out"), workspace.data_ptr(), workspace.numel(),
-                       _stream(stream, a, a_scales, w, w_scales, out, workspace, seg_counts)), "moe_fp8_matmul")
+                       _rows(out, self._out, (self.out_dtype,), "out"), _bytes(workspace), workspace.numel(),
+                       _stream(stream, a)), "moe_fp8_matmul")
 
 
 class Fp8ExpertPlan(_Fp8Plan):
@@ -230,8 +234,8 @@ class Fp8ExpertPlan(_Fp8Plan):
                                _rows(w1, self._w13, _E4, "w1"), _rows(s1, self._s13, _SCALES, "s1"),
                                _rows(w3, self._w13, _E4, "w3"), _rows(s3, self._s13, _SCALES, "s3"),
                                _rows(w2, self._w2, _E4, "w2"), _rows(s2, self._s2, _SCALES, "s2"),
-                               _rows(y_rows, self._x, _BF16, "y_rows"), workspace.data_ptr(), workspace.numel(),
-                               _stream(stream, x_rows, x_scales, gates, w1, s1, w3, s3, w2, s2, y_rows, workspace, seg_counts)), "moe_fp8_expert_forward")
+                               _rows(y_rows, self._x, _BF16, "y_rows"), _bytes(workspace), workspace.numel(),
+                               _stream(stream, x_rows)), "moe_fp8_expert_forward")
 
 
 class Fp8MoEPlan(MoEPlan):
@@ -254,8 +258,8 @@ class Fp8MoEPlan(MoEPlan):
                               _rows(w1, self._w13, _E4, "w1"), _rows(s1, self._s13, _SCALES, "s1"),
                               _rows(w3, self._w13, _E4, "w3"), _rows(s3, self._s13, _SCALES, "s3"),
                               _rows(w2, self._w2, _E4, "w2"), _rows(s2, self._s2, _SCALES, "s2"),
-                              _rows(y, self._x, (self.out_dtype,), "y"), workspace.data_ptr(), workspace.numel(),
-                              _stream(stream, x, x_q, x_scales, w_router, bias, w1, s1, w3, s3, w2, s2, y, workspace)),
+                              _rows(y, self._x, (self.out_dtype,), "y"), _bytes(workspace), workspace.numel(),
+                              _stream(stream, x)),
                "moe_fp8_forward")
 
 
@@ -271,13 +275,13 @@ class LayerCheckpoint:
         self.data = torch.empty(n, dtype=torch.uint8, device=device)
 
     def save(self, workspace, stream=None):
-        _check(_layer_ckpt_save(self.plan.handle, workspace.data_ptr(), workspace.numel(), self.data.data_ptr(),
-                                self.data.numel(), _stream(stream, workspace, self.data)), "moe_checkpoint_save")
+        _check(_layer_ckpt_save(self.plan.handle, _bytes(workspace), workspace.numel(), _bytes(self.data),
+                                self.data.numel(), _stream(stream, workspace)), "moe_checkpoint_save")
 
     def restore(self, x, workspace, stream=None):
         p = self.plan
-        _check(_layer_ckpt_restore(p.handle, _rows(x, (p.T, p.d), (p.act_dtype,), "x"), self.data.data_ptr(), self.data.numel(),
-                                   workspace.data_ptr(), workspace.numel(), _stream(stream, x, workspace, self.data)),
+        _check(_layer_ckpt_restore(p.handle, _rows(x, (p.T, p.d), (p.act_dtype,), "x"), _bytes(self.data), self.data.numel(),
+                                   _bytes(workspace), workspace.numel(), _stream(stream, x)),
                "moe_checkpoint_restore")
 
 
@@ -288,7 +292,7 @@ def checkpoint_save(a, b, qa, sa, qb, sb, stream=None):
     s = (n, scale_cols(F))
     _check(_ckpt_save(_rows(a, (n, F), _BF16, "a"), _rows(b, (n, F), _BF16, "b"), n, F, _rows(qa, (n, F), _E4, "qa"),
                       _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), _E4, "qb"), _rows(sb, s, _SCALES, "sb"),
-                      _stream(stream, a, b, qa, sa, qb, sb)), "moe_checkpoint_save_rows")
+                      _stream(stream, a)), "moe_checkpoint_save_rows")
 
 
 def checkpoint_restore(qa, sa, qb, sb, a=None, b=None, h=None, stream=None):
@@ -299,7 +303,7 @@ def checkpoint_restore(qa, sa, qb, sb, a=None, b=None, h=None, stream=None):
     s = (n, scale_cols(F))
     _check(_ckpt_restore_rows(_rows(qa, (n, F), _E4, "qa"), _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), _E4, "qb"),
                               _rows(sb, s, _SCALES, "sb"), n, F, _maybe(a, (n, F), _BF16, "a"), _maybe(b, (n, F), _BF16, "b"),
-                              _maybe(h, (n, F), _BF16, "h"), _stream(stream, qa, sa, qb, sb, a, b, h)),
+                              _maybe(h, (n, F), _BF16, "h"), _stream(stream, qa)),
            "moe_checkpoint_restore_rows")
 
 
@@ -311,5 +315,5 @@ def checkpoint_backward(qa, sa, qb, sb, dh, da, db, h=None, stream=None):
     s = (n, scale_cols(F))
     _check(_ckpt_backward(_rows(qa, (n, F), _E4, "qa"), _rows(sa, s, _SCALES, "sa"), _rows(qb, (n, F), _E4, "qb"),
                           _rows(sb, s, _SCALES, "sb"), _rows(dh, (n, F), _BF16, "dh"), n, F, _rows(da, (n, F), _BF16, "da"),
-                          _rows(db, (n, F), _BF16, "db"), _maybe(h, (n, F), _BF16, "h"), _stream(stream, qa, sa, qb, sb, dh, da, db, h)),
+                          _rows(db, (n, F), _BF16, "db"), _maybe(h, (n, F), _BF16, "h"), _stream(stream, qa)),
            "moe_checkpoint_backward_rows")

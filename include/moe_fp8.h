@@ -98,7 +98,7 @@ typedef struct {
   int32_t n_sources;       /* W; W * E <= 256 */
   int32_t out_dtype;       /* moe_dtype of the output rows */
   int32_t path;            /* MOE_PATH_AUTO (K, n multiples of 16) or MOE_PATH_SIMT (any size) */
-  int64_t wait_timeout_ns; /* bound on any device-side wait; <= 0 selects 2 s */
+  int64_t wait_timeout_ns; /* bound on any device-side wait, 1 ms at least; <= 0 selects 2 s */
 } moe_fp8_matmul_config;
 
 /* out[p] = A[p] . W_e^T for the rows p of expert e.  A [R, K] with scales 1 x 128; W

@@ -132,7 +132,7 @@ moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E
   p->E = E;
   p->n_seg = E * W;
   p->out_dtype = out_dtype;
-  p->timeout_ns = timeout_ns > 0 ? timeout_ns : 2000000000LL;
+  p->timeout_ns = timeout_ns <= 0 ? 2000000000LL : timeout_ns < (int64_t)fp8::kMinTimeoutNs ? (int64_t)fp8::kMinTimeoutNs : timeout_ns;
   // groups of up to kGroupM m-tiles per segment, as moe_plan bounds them per expert
   p->max_groups = (int)(rows / ((int64_t)kTileM * kGroupM) + 2 * (int64_t)p->n_seg + 2);
   size_t off = 0;
@@ -156,7 +156,7 @@ moe_status make_plan(bool experts, int64_t rows, int32_t k, int32_t n, int32_t E
   return set_last_error(MOE_OK, "");
 }
 
-// Tile tables of this call's segments (the kernels for few rows find theirs themselves).
+// Tile tables of this call's segments (the tensor-core kernels find their tiles themselves).
 moe_status begin(moe_fp8_plan_t plan, const int32_t* seg_counts, void* workspace, cudaStream_t st, Ws* ws) {
   moe_status s = bind_device(plan);
   if (s != MOE_OK) return s;
@@ -167,7 +167,7 @@ moe_status begin(moe_fp8_plan_t plan, const int32_t* seg_counts, void* workspace
   ws->offsets = reinterpret_cast<int32_t*>(b + plan->offsets);
   ws->mt_desc = reinterpret_cast<int4*>(b + plan->mt_desc);
   ws->pr_desc = reinterpret_cast<int4*>(b + plan->pr_desc);
-  if (plan->few) return MOE_OK;
+  if (plan->tc) return MOE_OK;
   Shape shape{};
   shape.N = plan->rows;
   shape.max_groups = plan->max_groups;
@@ -177,12 +177,11 @@ moe_status begin(moe_fp8_plan_t plan, const int32_t* seg_counts, void* workspace
 moe_status product(moe_fp8_plan_t plan, int kind, const fp8::GemmArgs& g, const Ws& ws, const int32_t* seg_counts, bool first,
                    cudaStream_t st, const char* what) {
   cudaError_t e;
-  if (plan->few)
-    e = fp8::launch_gemm_few(kind, g, ws, seg_counts, plan->n_seg, first, plan->device, plan->num_sms, plan->timeout_ns, true, st);
-  else if (plan->tc)
-    e = fp8::launch_gemm_tc(kind, g, ws, plan->device, plan->num_sms, plan->timeout_ns, true, st);
-  else
+  if (!plan->tc)
     e = fp8::launch_gemm_simt(kind, g, ws, plan->num_sms, st);
+  else
+    e = (plan->few ? fp8::launch_gemm_few : fp8::launch_gemm_tc)(kind, g, ws, seg_counts, plan->n_seg, first, plan->device,
+                                                                 plan->num_sms, plan->timeout_ns, st);
   return cuda_status(e, what);
 }
 

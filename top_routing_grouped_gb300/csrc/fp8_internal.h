@@ -8,6 +8,7 @@ namespace moe {
 namespace fp8 {
 
 constexpr int kBlock = 128;  // values per scale
+constexpr uint64_t kMinTimeoutNs = 1000000;  // the shortest limit of a device-side wait
 __host__ __device__ inline int64_t scale_cols(int64_t cols) { return (cols + 511) / 512 * 4; }
 
 // One grouped product as its kernels see it.
@@ -47,21 +48,24 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
                                     const float* rstd, const void* dresidual, bool bf16, int64_t rows, int d,
                                     int64_t ldr, void* dx, float* dweight, float* parts, cudaStream_t st);
 
-// Segment counts (null: one segment of s.N rows) -> tile tables; clears the status word first.
+// MOE_PATH_SIMT: segment counts (null: one segment of s.N rows) -> tile tables; clears the status
+// word first.
 cudaError_t launch_segments(const Shape& s, const Ws& ws, const int32_t* seg_counts, int n_seg, int n_experts,
                             cudaStream_t st);
 // Dispatch of 8-bit rows x [T, d] with their factors xs into ws.xp and xs_out.
 cudaError_t launch_permute(const Shape& s, const Ws& ws, const void* x, const uint8_t* xs, uint8_t* xs_out, int num_sms,
                            bool pdl, cudaStream_t st);
 cudaError_t launch_gemm_simt(int kind, const GemmArgs& g, const Ws& ws, int num_sms, cudaStream_t st);
-cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns,
-                           bool pdl, cudaStream_t st);
+// The tensor-core products find their tiles from the segment counts themselves (null: one segment);
+// `first`: the call's first launch, which sets the status word and waits for all earlier kernels (the
+// second waits for the first's results alone).
+cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first,
+                           int device, int num_sms, int64_t timeout_ns, cudaStream_t st);
 // Which of the two sets of tensor-core kernels: see api_fp8.cu.
 bool use_few(int64_t rows, int64_t n_seg, int64_t widest_out);
-// Few rows an expert: finds its tiles from the segment counts itself (null: one segment); `first`:
-// the call's first launch, which sets the status word.
+// ... for few rows an expert.
 cudaError_t launch_gemm_few(int kind, const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first,
-                            int device, int num_sms, int64_t timeout_ns, bool pdl, cudaStream_t st);
+                            int device, int num_sms, int64_t timeout_ns, cudaStream_t st);
 
 }  // namespace fp8
 }  // namespace moe

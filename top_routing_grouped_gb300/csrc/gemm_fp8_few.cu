@@ -31,6 +31,7 @@
 #include "device_common.cuh"
 #include "fp8_common.cuh"
 #include "fp8_mma.cuh"
+#include "fp8_units.cuh"
 #include "gemm_tc.h"
 #include "tc_ptx.cuh"
 #include "tmap.h"
@@ -66,10 +67,7 @@ struct Ctl {
   uint32_t tmem_base;
   int abort;
   uint32_t top[2][2][4][8];      // epilogue: [set][turn] largest hidden value of each warp and row
-  int row0[kMaxExperts + 1];     // first row of each segment
-  int unit0[kMaxExperts + 1];    // first unit of each segment
-  int64_t row_tot[8];  // the scans' warp totals
-  uint32_t unit_tot[8];
+  Segments seg;
 };
 
 // The launch's sizes, chosen on the host.
@@ -134,18 +132,13 @@ struct Unit {
 // Unit u: segments in order, in a segment the blocks of weight rows, in a block the groups of rows
 // (neighbouring CTAs then read the same weights, once from HBM).
 __device__ __forceinline__ Unit decode(const Ctl* ctl, const FewShape& f, int E, int u) {
-  int lo = 0, hi = f.n_seg - 1;  // the last segment whose first unit is at or below u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (ctl->unit0[mid] <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  const int cnt = ctl->row0[lo + 1] - ctl->row0[lo], groups = (cnt + f.tok - 1) / f.tok, local = u - ctl->unit0[lo];
+  const int sg = segment_of(&ctl->seg, f.n_seg, u);
+  const int cnt = ctl->seg.row0[sg + 1] - ctl->seg.row0[sg], groups = (cnt + f.tok - 1) / f.tok, local = u - ctl->seg.unit0[sg];
   Unit r;
-  r.e = lo % E;
+  r.e = sg % E;
   r.n0 = local / groups * kWRows;
   const int g0 = local % groups * f.tok;
-  r.row0 = ctl->row0[lo] + g0;
+  r.row0 = ctl->seg.row0[sg] + g0;
   r.rows = min(f.tok, cnt - g0);
   return r;
 }
@@ -206,48 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (f.first) pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the segments' first rows and units: inclusive scans over the first 256 threads
-  int total;
-  {
-    const int i = threadIdx.x;
-    const int cnt = i < f.n_seg ? (seg_counts ? seg_counts[i] : (int)g.rows) : 0;
-    int64_t rows = cnt < 0 ? (int64_t)1 << 40 : cnt;  // 64 bits: bad counts may sum to anything
-    uint32_t units = ((uint32_t)cnt + f.tok - 1) / f.tok * nblk;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, rows, o);
-      const uint32_t y = __shfl_up_sync(0xffffffffu, units, o);
-      if (lane >= o) {
-        rows += x;
-        units += y;
-      }
-    }
-    if (warp < 8 && lane == 31) {
-      ctl->row_tot[warp] = rows;
-      ctl->unit_tot[warp] = units;
-    }
-    __syncthreads();
-    int64_t all = 0;
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) {
-        rows += ctl->row_tot[w];
-        units += ctl->unit_tot[w];
-      }
-      all += ctl->row_tot[w];
-    }
-    const bool bad = all > g.rows;
-    if (i < kMaxExperts) {
-      ctl->row0[i + 1] = (int)rows;
-      ctl->unit0[i + 1] = (int)units;
-    }
-    if (i == 0) ctl->row0[0] = ctl->unit0[0] = 0;
-    __syncthreads();
-    total = bad ? 0 : ctl->unit0[f.n_seg];
-    if (f.first && blockIdx.x == 0 && i == 0) {
-      ws.hdr[kHdrWhere] = bad ? 0x950u : 0u;
-      ws.hdr[kHdrStatus] = bad ? (uint32_t)MOE_ERR_INTERNAL : 0u;
-    }
-  }
+  int total = scan_segments(&ctl->seg, seg_counts, f.n_seg, g.rows, [&](int cnt) { return (cnt + f.tok - 1) / f.tok * nblk; });
+  if (f.first) begin_status(ws, total < 0, 0x950u);
+  total = max(total, 0);
   volatile int* abort_flag = &ctl->abort;
 
   if (warp == 0) {
@@ -585,7 +539,7 @@ constexpr int kSmemMax = 232448;
 
 template <int kKind>
 cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first, int device,
-                        int num_sms, int64_t timeout_ns, bool pdl, cudaStream_t st) {
+                        int num_sms, int64_t timeout_ns, cudaStream_t st) {
   constexpr int kMats = kKind == kSwiGLU ? 2 : 1;
   auto kern = gemm_fp8_few_kernel<kKind>;
   cudaError_t e;
@@ -621,18 +575,18 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_coun
   if (kMats == 2 && (e = make_tmap_rows128(&mW3, g.b3, 1, wrows, (uint64_t)g.K, kWRows)) != cudaSuccess) return e;
   const int64_t clusters = num_sms / f.split, most = (g.rows / f.tok + owners) * nblk;  // no more units than that
   const int grid = (int)(clusters < most ? clusters : most) * f.split;
-  return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, pdl, f.split, mX, mW, mW3, g, ws, seg_counts, f,
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, true, f.split, mX, mW, mW3, g, ws, seg_counts, f,
                        timeout_ns);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_few(int kind, const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first,
-                            int device, int num_sms, int64_t timeout_ns, bool pdl, cudaStream_t st) {
+                            int device, int num_sms, int64_t timeout_ns, cudaStream_t st) {
   switch (kind) {
-    case kSwiGLU: return launch_kind<kSwiGLU>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, pdl, st);
-    case kOutBf16: return launch_kind<kOutBf16>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, pdl, st);
-    default: return launch_kind<kOutF32>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, pdl, st);
+    case kSwiGLU: return launch_kind<kSwiGLU>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, st);
+    case kOutBf16: return launch_kind<kOutBf16>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, st);
+    default: return launch_kind<kOutF32>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, st);
   }
 }
 

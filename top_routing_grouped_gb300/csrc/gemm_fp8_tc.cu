@@ -32,9 +32,9 @@
 // store).  Counted in clocks on 8192 x 8192 x 2048 (64 K blocks a tile) the MMAs run 87 % of the time
 // and 98 % in a build without loads, hand-over and stores; on 8192 x 2048 x 8192 (16 K blocks a tile) 73 %:
 // handing over the shared columns costs about 700 clocks of 11400 a tile (2000 in a build without
-// loads), the output's way through shared memory 1300.  Times: 98 us for 8192 x 2048 x 8192 (2.8
-// PFLOP/s), 88 us for 8192 x 4096 x 4096 (3.1), 2.4 ms for 131072 rows of 64 experts of 4096 x 2048 (2.75,
-// at 1.55 GHz under the power cap).
+// loads), the output's way through shared memory 1300.  Times: 93 us for 8192 x 2048 x 8192 (2.95
+// PFLOP/s; 98 us while a kernel of its own built the tile tables), 84 us for 8192 x 4096 x 4096 (3.25),
+// 2.4 ms for 131072 rows of 64 experts of 4096 x 2048 (2.76, at 1.55 GHz under the power cap).
 //
 // Tried and dropped: 224-wide tiles, whose accumulators share no columns (the ring's time per K block
 // does not shrink with the tile: 98 -> 106 us); the output stored from registers, 32 bytes a lane
@@ -52,6 +52,7 @@
 
 #include "fp8_common.cuh"
 #include "fp8_mma.cuh"
+#include "fp8_units.cuh"
 #include "gemm_tc.h"
 #include "tc_ptx.cuh"
 #include "tmap.h"
@@ -100,9 +101,10 @@ struct Ctl {
   uint32_t tmem_base;
   uint32_t peer_tmem_base;
   int abort;
+  Segments seg;
 };
 
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + kStgBytes + sizeof(Ctl);
+constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + kStgBytes + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
@@ -150,6 +152,24 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// Tile u of the segments: up to 16 m-tiles of a segment form a group whose tiles share a few weight
+// tiles at a time (pairs of m-tiles fastest, then the weight tile, then the group), as in the bf16
+// kernels' tables.  The m-tile of CTA `rank` of the pair; rows <= 0: there is none.
+__device__ __forceinline__ int pairs_of(int cnt) { return ((cnt + kTileM - 1) / kTileM + 1) / 2; }
+__device__ __forceinline__ TileInfo decode(const Segments* sg, int n_seg, int E, int n_tiles, int u, int rank) {
+  constexpr int kPairs = kGroupM / 2;
+  const int s = segment_of(sg, n_seg, u), row0 = sg->row0[s], cnt = sg->row0[s + 1] - row0;
+  const int local = u - sg->unit0[s], grp = local / (kPairs * n_tiles), rem = local - grp * kPairs * n_tiles;
+  const int gp = min(kPairs, pairs_of(cnt) - grp * kPairs);
+  TileInfo ti;
+  ti.e = s % E;
+  ti.n_idx = rem / gp;
+  const int m0 = grp * kGroupM * kTileM + (2 * (rem % gp) + rank) * kTileM;
+  ti.row0 = row0 + m0;
+  ti.rows = min(kTileM, cnt - m0);
+  return ti;
+}
+
 __device__ __forceinline__ void raise_abort(Ctl* ctl, uint32_t rank) {
   ctl->abort = 1;
   ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&ctl->abort), rank ^ 1u), 1u);
@@ -159,9 +179,9 @@ template <int kKind>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmB3, const __grid_constant__ CUtensorMap tmY, GemmArgs g, Ws ws,
-                    int64_t timeout_ns) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+                    const int32_t* seg_counts, int n_seg, int first, int64_t timeout_ns) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* stages = smem_raw;  // the swizzled boxes need 1024-byte boundaries (checked below)
   uint8_t* stg_base = stages + kStages * kStageBytes;
   Ctl* ctl = reinterpret_cast<Ctl*>(stg_base + kStgBytes);
   // SwiGLU stages four blocks; the warps' maxima lie behind them: [half][128 rows]
@@ -215,11 +235,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctl->tmem_base;
   if (threadIdx.x == 0) ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&ctl->peer_tmem_base), rank ^ 1u), tmem);
   ptx::cluster_sync();
-  pdl_wait();  // the tile table and the A operand come from the previous kernels
+  // The call's first launch waits here for the counts and the activations; its second one waits for
+  // the hidden rows alone, once it has found its tiles.
+  if (first) pdl_wait();
+  int total = scan_segments(&ctl->seg, seg_counts, n_seg, g.rows, [&](int cnt) { return pairs_of(cnt) * n_tiles; });
+  if (first) begin_status(ws, total < 0, 0x900u);
+  total = max(total, 0);
+  if (!first) pdl_wait();
   pdl_launch_dependents();
-  int total = (int)ws.hdr[kHdrNumPairs] * n_tiles;
-  if (ctl->peer_tmem_base != tmem) {  // a pair's accumulators must sit at the same TMEM address
-    if (threadIdx.x == 0) record_error(ws, MOE_ERR_INTERNAL, 0x900u + kKind);
+  // a pair's accumulators must sit at the same TMEM address, the ring on its boundary
+  if (ctl->peer_tmem_base != tmem || (ptx::smem_u32(stages) & 1023u) != 0) {
+    if (threadIdx.x == 0) {
+      const uint64_t t0 = global_ns();  // not before CTA 0 has set the status word
+      while (global_ns() - t0 < kMinTimeoutNs) {
+      }
+      record_error(ws, MOE_ERR_INTERNAL, 0x908u + kKind);
+    }
     total = 0;
   }
   volatile int* abort_flag = &ctl->abort;
@@ -233,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const CUtensorMap* bmap = (kKind == kSwiGLU && rank == 1) ? &tmB3 : &tmB;
       for (int tile = cid; tile < total && ok; tile += ncl) {
-        const TileInfo ti = decode_pair_tile(ws, n_tiles, tile, (int)rank);
+        const TileInfo ti = decode(&ctl->seg, n_seg, g.E, n_tiles, tile, (int)rank);
         // a pair's second m-tile may not exist: its A rows are neither loaded nor waited for
-        const bool peer_rows = decode_pair_tile(ws, n_tiles, tile, 1).rows > 0;
+        const bool peer_rows = decode(&ctl->seg, n_seg, g.E, n_tiles, tile, 1).rows > 0;
         const uint32_t bytes = peer_rows ? 2 * kStageBytes : 2 * kStageBytes - kABytes;
         const int brow = ti.e * g.n + ti.n_idx * bn + (kKind == kSwiGLU ? 0 : (int)rank * (kMmaN / 2));
         for (int kb = 0; kb < kblocks; ++kb) {
@@ -347,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tile = cid, gk = 0;
     int64_t ra[4], r0 = 0, r1 = 0;
     auto locate = [&]() {
-      const TileInfo ti = decode_pair_tile(ws, n_tiles, tile, (int)rank);
+      const TileInfo ti = decode(&ctl->seg, n_seg, g.E, n_tiles, tile, (int)rank);
 #pragma unroll
       for (int c = 0; c < 4; ++c)  // rows past the buffer belong to no output: any row's words do
         ra[c] = min((int64_t)ti.row0 + 32 * c + lane, g.rows - 1) * sck;
@@ -404,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int tile = cid; tile < total; tile += ncl) {
-      const TileInfo ti = decode_pair_tile(ws, n_tiles, tile, (int)rank);
+      const TileInfo ti = decode(&ctl->seg, n_seg, g.E, n_tiles, tile, (int)rank);
       ok = ptx::mbar_wait(ptx::smem_u32(&ctl->tfull[acc]), acc_phase, timeout_ns, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (kKind != kSwiGLU && !ok) break;
@@ -588,8 +619,8 @@ int persistent_grid(int device, int num_sms, cudaError_t* err) {
 }
 
 template <int kKind>
-cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns, bool pdl,
-                        cudaStream_t st) {
+cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first, int device,
+                        int num_sms, int64_t timeout_ns, cudaStream_t st) {
   constexpr int kEsz = kKind == kSwiGLU ? 1 : kKind == kOutBf16 ? 2 : 4;
   CUtensorMap mA, mB, mB3, mY;
   cudaError_t e;
@@ -602,18 +633,18 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, int device, int num_sms
   auto kern = gemm_fp8_kernel<kKind>;
   const int grid = persistent_grid<kKind>(device, num_sms, &e);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, st, pdl, 2, mA, mB, mB3, mY, g, ws,
-                       timeout_ns);
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, st, true, 2, mA, mB, mB3, mY, g, ws, seg_counts,
+                       n_seg, first ? 1 : 0, timeout_ns);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, int device, int num_sms, int64_t timeout_ns,
-                           bool pdl, cudaStream_t st) {
+cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first,
+                           int device, int num_sms, int64_t timeout_ns, cudaStream_t st) {
   switch (kind) {
-    case kSwiGLU: return launch_kind<kSwiGLU>(g, ws, device, num_sms, timeout_ns, pdl, st);
-    case kOutBf16: return launch_kind<kOutBf16>(g, ws, device, num_sms, timeout_ns, pdl, st);
-    default: return launch_kind<kOutF32>(g, ws, device, num_sms, timeout_ns, pdl, st);
+    case kSwiGLU: return launch_kind<kSwiGLU>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, st);
+    case kOutBf16: return launch_kind<kOutBf16>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, st);
+    default: return launch_kind<kOutF32>(g, ws, seg_counts, n_seg, first, device, num_sms, timeout_ns, st);
   }
 }
 

@@ -70,8 +70,8 @@ moe_status moe_rmsnorm(const void* x, const void* residual, const float* weight,
  *   dweight = sum_t dout[t] * xhat[t]                             [d] fp32, may be NULL
  * dx is the gradient of x and of the residual alike, and may be dresidual itself.  The sum
  * over rows is taken in a fixed order (results do not depend on timing).  workspace: device,
- * 256-byte aligned, moe_rmsnorm_backward_workspace(rows, d) bytes (needed when dweight is
- * wanted). */
+ * 256-byte aligned, moe_rmsnorm_backward_workspace(rows, d) bytes (when dweight is wanted; may
+ * be NULL where that is 0, as with few rows). */
 size_t moe_rmsnorm_backward_workspace(int64_t rows, int32_t d);
 moe_status moe_rmsnorm_backward(const void* dout, int32_t dout_dtype, const void* r, const float* weight,
                                 const float* rstd, const void* dresidual, int32_t dtype, int64_t rows, int32_t d,

@@ -193,7 +193,8 @@ def test_rmsnorm_special_rows(fp8):
 
 
 @pytest.mark.parametrize("dtype, dout", [(F32, F32), (BF, F32), (BF, BF), (F32, BF)], ids=lambda t: str(t)[6:])
-@pytest.mark.parametrize("n, d, pad, dres, weight", [(1, 1, 0, False, True), (1, 4096, 0, True, True), (300, 1000, 5, True, True),
+@pytest.mark.parametrize("n, d, pad, dres, weight", [(1, 1, 0, False, True), (1, 4096, 0, True, True), (512, 264, 0, True, True),
+                                                     (513, 264, 0, True, True), (300, 1000, 5, True, True),
                                                      (2000, 136, 0, False, False), (700, 2048, 8, True, True),
                                                      (3, 12345, 0, True, True)])
 def test_rmsnorm_backward_against_the_formula(fp8, dtype, dout, n, d, pad, dres, weight):
@@ -266,6 +267,10 @@ PRODUCTS = [  # segments' rows, E, K, N
     ([1300], 1, 272, 2064), ([129, 0, 700, 300, 1], 5, 528, 1168), ([40, 128, 257, 3, 900, 255], 3, 2064, 816),
     # more units than clusters, one of them with every kind of short group
     ([65, 17, 0, 1, 64, 33, 16, 15], 8, 1552, 2320),
+    # K split over clusters of four that take two units each (one segment needs two groups of rows)
+    ([95, 1], 2, 2064, 2432),
+    # ... over clusters of eight, and a K whose last group of four blocks is short
+    ([7], 1, 4176, 144),
 ]
 
 

@@ -259,9 +259,9 @@ moe_status moe_rmsnorm_backward(const void* dout, int32_t dout_dtype, const void
                       {rstd, "rstd", 16, !any},                {dresidual, "dresidual", a, true}, {dx, "dx", a, !any},
                       {dweight, "dweight", 16, true}};
   if ((s = check(ptrs)) != MOE_OK) return s;
-  if (dweight && any) {
+  const size_t need = moe_rmsnorm_backward_workspace(rows, d);
+  if (dweight && need > 0) {
     if (!workspace || !aligned(workspace, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-    const size_t need = moe_rmsnorm_backward_workspace(rows, d);
     if (workspace_bytes < need) return fail(MOE_ERR_INVALID_ARG, "workspace too small: %zu < %zu", workspace_bytes, need);
   }
   return cuda_status(fp8::launch_rmsnorm_backward(dout, dout_dtype == MOE_BF16, r, weight, rstd, dresidual,

@@ -287,11 +287,35 @@ __global__ void __launch_bounds__(R > 1 ? 32 * R : 512)
   }
 }
 
-// The CTA's sum of dweight stays in registers over its rows and leaves as one row of `parts`.
+// dweight of 32 columns over all rows by one CTA: a warp takes every nth row, the warps' sums are
+// added in order.
+template <bool kBf16, bool kDoutBf16>
+__device__ __forceinline__ void column_sums(const void* dout, const void* r, const float* rstd, int rows, int d, int64_t ldr,
+                                            int c0, float* dweight, float (*all)[32]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = blockDim.x >> 5, c = c0 + lane;
+  float s = 0.f;
+  if (c < d) {
+#pragma unroll 8
+    for (int t = warp; t < rows; t += n)
+      s += ld<kDoutBf16>(dout, (int64_t)t * d + c) * (ld<kBf16>(r, t * ldr + c) * rstd[t]);
+  }
+  all[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < d) {
+    s = all[0][lane];
+    for (int w = 1; w < n; ++w) s += all[w][lane];
+    dweight[c] = s;
+  }
+}
+
+// The CTA's sum of dweight stays in registers over its rows and leaves as one row of `parts`.  With
+// few rows (`parts` null) the CTAs past the first `row_ctas` sum the columns instead, out of L2, and
+// the call needs no second kernel.
 template <bool kBf16, bool kDoutBf16, bool kVec, int V, int R>
 __global__ void __launch_bounds__(R > 1 ? 32 * R : 512, kBf16 && kVec && V == 1 ? (R > 1 ? 4 : 2) : 1)
     rmsnorm_backward_reg_kernel(const void* dout, const void* r, const float* weight, const float* rstd,
-                                const void* dresidual, int64_t rows, int d, int64_t ldr, void* dx, float* parts, int even) {
+                                const void* dresidual, int64_t rows, int d, int64_t ldr, void* dx, float* parts, int even,
+                                int row_ctas, float* dweight) {
   __shared__ __align__(16) float red[2 * 16];
   if (R == 1) {
     if (threadIdx.x < 32) red[threadIdx.x] = 0.f;
@@ -300,9 +324,14 @@ __global__ void __launch_bounds__(R > 1 ? 32 * R : 512, kBf16 && kVec && V == 1 
   constexpr int kEsz = kBf16 ? 2 : 4, kDsz = kDoutBf16 ? 2 : 4;
   const int lane = threadIdx.x & 31;
   const Cols<kVec> cs{R > 1 ? 1 : (int)(blockDim.x >> 5), R > 1 ? 0 : (int)(threadIdx.x >> 5), lane, even != 0};
-  const int64_t step = (int64_t)gridDim.x * R;
+  const int64_t step = (int64_t)row_ctas * R;
   pdl_wait();
   pdl_launch_dependents();
+  if (blockIdx.x >= row_ctas) {
+    __shared__ float all[16][32];
+    column_sums<kBf16, kDoutBf16>(dout, r, rstd, (int)rows, d, ldr, ((int)blockIdx.x - row_ctas) * 32, dweight, all);
+    return;
+  }
   float wt[V][8], dw[V][8];
 #pragma unroll
   for (int u = 0; u < V; ++u) {
@@ -558,15 +587,21 @@ cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* wei
                        ldr, eps, residual_out, out, (uint8_t*)q, scales, rstd);
 }
 
+// Up to this many rows, a call is one kernel: the columns' sums read the rows again, from L2 (300 x 1000
+// fp32: 4.6 us; with partial sums and a second kernel 5.5 us, and 2 us more of the host's).
+constexpr int kOneKernelRows = 512;
+static bool one_kernel(int64_t rows, int d) { return rows <= kOneKernelRows && d <= kMaxRegCols; }
+
 // Rows a CTA sums dweight over before it writes a partial: enough CTAs to fill the GPU, but
 // partials of a few rows each at least, which are written and read again.  The count depends on
 // the shape alone, and so does the order of the sum.
-int rmsnorm_backward_parts(int64_t rows, int d) {
+static int row_ctas(int64_t rows, int d) {
   const int per_cta = d <= 256 ? 8 : 1;
   const int64_t most = d <= kMaxRegCols ? resident(d) : 152 * 2;
   const int64_t want = (rows + 2 * per_cta - 1) / (2 * per_cta);
   return (int)(want < most ? want : most);
 }
+int rmsnorm_backward_parts(int64_t rows, int d) { return one_kernel(rows, d) ? 0 : row_ctas(rows, d); }
 
 struct NormBwdArgs {
   const void *dout, *r;
@@ -576,14 +611,16 @@ struct NormBwdArgs {
   int d;
   int64_t ldr;
   void* dx;
-  float* parts;
+  float* parts;    // more rows: partial sums
+  float* dweight;  // few rows: the sums
 };
 
 template <bool kBf16, bool kDoutBf16, bool kVec, int V, int R>
 static cudaError_t norm_bwd_reg(const NormBwdArgs& a, bool even, cudaStream_t st) {
-  return launch_kernel(rmsnorm_backward_reg_kernel<kBf16, kDoutBf16, kVec, V, R>,
-                       dim3((unsigned)rmsnorm_backward_parts(a.rows, a.d)), dim3(row_threads(a.d)), 0, st, true, 1, a.dout, a.r,
-                       a.weight, a.rstd, a.dresidual, a.rows, a.d, a.ldr, a.dx, a.parts, even ? 1 : 0);
+  const int n = row_ctas(a.rows, a.d), cols = a.dweight ? (a.d + 31) / 32 : 0;
+  return launch_kernel(rmsnorm_backward_reg_kernel<kBf16, kDoutBf16, kVec, V, R>, dim3((unsigned)(n + cols)),
+                       dim3(row_threads(a.d)), 0, st, true, 1, a.dout, a.r, a.weight, a.rstd, a.dresidual, a.rows, a.d, a.ldr,
+                       a.dx, a.parts, even ? 1 : 0, n, a.dweight);
 }
 
 template <bool kBf16, bool kDoutBf16, bool kVec>
@@ -602,10 +639,12 @@ static cudaError_t norm_bwd_types(const NormBwdArgs& a, bool bf16, bool dout_bf1
 cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void* r, const float* weight,
                                     const float* rstd, const void* dresidual, bool bf16, int64_t rows, int d,
                                     int64_t ldr, void* dx, float* dweight, float* parts, cudaStream_t st) {
-  const int n = rmsnorm_backward_parts(rows, d);
+  const int n = row_ctas(rows, d);
+  const bool one = one_kernel(rows, d);
   cudaError_t e = cudaSuccess;
   if (n > 0 && d <= kMaxRegCols) {
-    const NormBwdArgs a{dout, r, weight, rstd, dresidual, rows, d, ldr, dx, dweight ? parts : nullptr};
+    const NormBwdArgs a{dout, r, weight, rstd, dresidual, rows, d, ldr, dx, dweight && !one ? parts : nullptr,
+                        one ? dweight : nullptr};
     auto all = [&](int k) {
       return d % k == 0 && on(k, dout, dout_bf16, d) && on(k, r, bf16, ldr) && on(k, dresidual, bf16, d) && on(k, dx, bf16, d);
     };
@@ -621,7 +660,7 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
     e = launch_kernel(kern, dim3((unsigned)n), dim3(kThreads), smem, st, false, 1, dout, r, weight, rstd, dresidual, rows, d,
                       ldr, dx, dweight ? parts : nullptr);
   }
-  if (e != cudaSuccess || !dweight) return e;
+  if (e != cudaSuccess || !dweight || (one && n > 0)) return e;
   return launch_kernel(dweight_sum_kernel, dim3((unsigned)((d + 31) / 32)), dim3(1024), 0, st, n > 0, 1,
                        (const float*)parts, n, d, dweight);
 }

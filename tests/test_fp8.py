@@ -267,8 +267,8 @@ PRODUCTS = [  # segments' rows, E, K, N
     ([1300], 1, 272, 2064), ([129, 0, 700, 300, 1], 5, 528, 1168), ([40, 128, 257, 3, 900, 255], 3, 2064, 816),
     # more units than clusters, one of them with every kind of short group
     ([65, 17, 0, 1, 64, 33, 16, 15], 8, 1552, 2320),
-    # K split over clusters of four that take two units each (one segment needs two groups of rows)
-    ([95, 1], 2, 2064, 2432),
+    # K split over pairs of CTAs that take two units each (two segments need two groups of rows)
+    ([97, 97, 1], 3, 1040, 3184), ([96, 95, 20], 3, 528, 272),
     # ... over clusters of eight, and a K whose last group of four blocks is short
     ([7], 1, 4176, 144),
 ]

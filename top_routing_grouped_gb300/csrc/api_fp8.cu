@@ -27,15 +27,16 @@ namespace moe {
 namespace fp8 {
 
 // Which tensor-core kernels.  Those that make the weights the MMA's rows read each weight tile once for
-// every 64 rows of a segment; the CTA pairs take 256 rows at the price of one.  Measured (experts;
-// time of the pairs / time of the others): 16 and 32 rows a segment 1.2-1.3 at every shape, 64 rows
-// 0.9 (8 experts of 8192) to 1.1 (32 of 2048), 128 rows 0.66-0.75.  With few segments the pairs also
-// leave SMs idle: dense products K x n of 2048 x 2048, 4096 x 4096 and 2048 x 8192 cross where the
-// others have more than one unit of work for each SM (1.5, 1.2 and 1.5 at 128 units; 0.94, 0.69 and
-// 0.96 at 192 to 256).
+// every 96 rows of a segment; the CTA pairs take 256 rows at the price of one.  Measured (experts;
+// time of the pairs / time of the others, for 8 experts of 2048 x 8192, 32 of 2048 x 2048, 64 of
+// 4096 x 2048): 16 rows a segment 1.20-1.22, 48 rows 1.15-1.16, 64 rows 1.10-1.12, 80 rows 1.02-1.05, 96 rows
+// (half the segments need a second pass) 0.70-0.92, 128 rows 0.57-0.68.  With few segments the pairs also
+// leave SMs idle: dense products K x n of 2048 x 2048, 4096 x 4096 and 2048 x 8192 cross where the others
+// have a unit of work for half of the SMs (64 units: 0.99, 1.02, 0.99; 96 to 128 units: 0.87, 0.75, 0.88; one
+// row: 2.2, 1.95, 1.5).
 bool use_few(int64_t rows, int64_t n_seg, int64_t widest_out) {
   const int64_t blocks = (widest_out + 127) / 128;
-  return rows <= 48 * n_seg || ((rows + 63) / 64 + n_seg - 1) * blocks <= 152;
+  return rows <= 72 * n_seg || ((rows + 95) / 96 + n_seg - 1) * blocks <= 76;
 }
 
 }  // namespace fp8

@@ -5,10 +5,10 @@
 //
 // With a handful of rows a 256-row tile is padding, and an MMA of 256 rows takes as long for one of
 // them as for all.  Here the weights are the MMA's 128 rows and the activations its N columns
-// (16, 32 or 64), so D[m][t] is output column m of row t; an MMA takes 39-48 clocks, a stage of
-// 16 KB (SwiGLU: 32 KB) of weights a quarter of the time that HBM takes to deliver it.
+// (16 to 96), so D[m][t] is output column m of row t; an MMA takes 39-56 clocks, a stage of
+// 16 KB (SwiGLU: 32 KB) of weights a third of the time that HBM takes to deliver it.
 //
-// A unit of work is (segment, block of 128 weight rows, up to 64 of the segment's rows).  Every CTA
+// A unit of work is (segment, block of 128 weight rows, up to 96 of the segment's rows).  Every CTA
 // finds its units from the segment counts itself (a scan over at most 256 numbers), so a call needs no
 // kernel for tile tables.  When there are fewer units than SMs, a cluster of 2, 4 or 8 CTAs
 // shares a unit: each sums a part of K, and the first CTA adds the others' sums, which arrive in
@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kBK = 128;              // k's (bytes) per stage: one block of factors
 constexpr int kWRows = 128;           // weight rows per unit
-constexpr int kMaxTok = 64;           // activation rows per unit
+constexpr int kMaxTok = 96;           // activation rows per unit: two buffers of two matrices, and factors, fill TMEM
 constexpr int kTokBox = 16;           // rows of one TMA box of activations
 constexpr int kWBytes = kWRows * kBK;
 constexpr int kMaxStages = 12;
@@ -50,10 +50,10 @@ constexpr int kThreads = 512;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;  // two sets of four warps take turns with the rows, eight at a time
 constexpr int kSfWarp0 = 12;
 
-// TMEM columns: accumulator (buffer b, matrix m) at 128 b + 64 m; factor set i at 256 + 16 i
+// TMEM columns: accumulator (buffer b, matrix m) at 192 b + 96 m; factor set i at 384 + 16 i
 // (4 of W1 or W, 4 of W3, 4 of the activations)
 constexpr int kTmemCols = 512;
-constexpr int kSfCol = 256;
+constexpr int kSfCol = 4 * kMaxTok;
 constexpr int kSfStep = 16;
 constexpr int kSfSets = 8;
 
@@ -73,7 +73,7 @@ struct Ctl {
 // The launch's sizes, chosen on the host.
 struct FewShape {
   int n_seg;       // segments; segment s holds rows of expert s % E
-  int tok;         // rows per unit: a multiple of 16, at most 64
+  int tok;         // rows per unit: a multiple of 16, at most kMaxTok
   int stages;
   int stage_bytes;
   int recv_bytes;  // shared memory for one other CTA's sums
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cols = (__shfl_sync(0xffffffffu, decode(ctl, f, g.E, u).rows, 0) + 15) & ~15;
       if (!(ok = wait(offsetof(Ctl, tempty) + 8 * acc, acc_phase ^ 1u))) break;
       ptx::tc_fence_after();
-      const uint32_t d = tm + (uint32_t)(acc * 128);
+      const uint32_t d = tm + (uint32_t)(acc * 2 * kMaxTok);
       uint32_t sf = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if ((kb & 3) == 0) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int m = 0; m < kMats; ++m)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_mxf8(d + 64 * m, dw + (m * kWBytes >> 4) + 2 * ks, dx + 2 * ks, idesc, sf + 4 * m, sf + 8,
+              mma_mxf8(d + kMaxTok * m, dw + (m * kWBytes >> 4) + 2 * ks, dx + 2 * ks, idesc, sf + 4 * m, sf + 8,
                        (kb != kb0 || ks != 0) ? 1u : 0u);
           ptx::mma_commit(ctl0 + offsetof(Ctl, empty) + 8 * stage);
           if (last_of_group) ptx::mma_commit(ctl0 + offsetof(Ctl, sf_empty) + 8 * set);
@@ -339,17 +339,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     int set = 0, u = cid, gk = gk0;
     uint32_t phase = 0;
     bool ok = true;
-    int64_t rx[2], rw = 0;
+    int64_t rx[3], rw = 0;
     auto locate = [&]() {
       const Unit un = decode(ctl, f, g.E, u);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) rx[c] = min((int64_t)un.row0 + 32 * c + lane, g.rows - 1) * sck;  // clamped: unused rows
+      for (int c = 0; c < 3; ++c) rx[c] = min((int64_t)un.row0 + 32 * c + lane, g.rows - 1) * sck;  // clamped: unused rows
       rw = ((int64_t)un.e * nblk + un.n0 / kBlock) * sck;
     };
-    uint32_t x[2], w0 = 0, w1 = 0;
+    uint32_t x[3], w0 = 0, w1 = 0;
     auto request = [&]() {
-      x[0] = __ldg(sx32 + rx[0] + gk);
-      x[1] = __ldg(sx32 + rx[1] + gk);
+#pragma unroll
+      for (int c = 0; c < 3; ++c) x[c] = __ldg(sx32 + rx[c] + gk);
       w0 = __ldg(sw32 + rw + gk);
       w1 = __ldg(sw3_32 + rw + gk);
     };
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       request();
     }
     while (u < total && gk0 < gk1) {
-      const uint32_t wx[4] = {x[0], x[1], x[1], x[1]}, v0 = w0, v1 = w1;
+      const uint32_t wx[4] = {x[0], x[1], x[2], x[2]}, v0 = w0, v1 = w1;
       if (++gk == gk1) {
         gk = gk0;
         u += ncl;
@@ -402,10 +402,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit un = decode(ctl, f, g.E, u);
       const int col = un.n0 + m;
       const bool in = col < g.n;
-      float gate0 = 1.f, gate1 = 1.f;  // of rows lane and lane + 32
+      float gate0 = 1.f, gate1 = 1.f, gate2 = 1.f;  // of rows lane, lane + 32 and lane + 64
       if (kKind != kSwiGLU && rank == 0 && g.gate) {
         if (lane < un.rows) gate0 = g.gate[un.row0 + lane];
         if (lane + 32 < un.rows) gate1 = g.gate[un.row0 + lane + 32];
+        if (lane + 64 < un.rows) gate2 = g.gate[un.row0 + lane + 64];
       }
       ok = ptx::mbar_wait(ptx::smem_u32(&ctl->tfull[acc]), acc_phase, timeout_ns, abort_flag);
       if (f.split > 1)
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       r_phase ^= 1u;
-      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 128);
+      const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * kMaxTok);
       if (rank != 0) {
         // this CTA's sums to the first CTA (rows past the unit's last fill the buffer, unread)
         const uint32_t dst = ptx::mapa(ptx::smem_u32(recv), 0) + (uint32_t)(((int)rank - 1) * f.recv_bytes + m * 4);
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 8 * set; c < un.rows; c += 16) {
             uint32_t v[8];
-            tmem_ld_x8(t_row + 64 * mt + c, v);
+            tmem_ld_x8(t_row + kMaxTok * mt + c, v);
             ptx::tmem_ld_wait();
             const uint32_t to = dst + (uint32_t)((mt * f.tok + c) * 512);
 #pragma unroll
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         auto load = [&](int mt, int c, float(&v)[8]) {
           uint32_t w[8];
-          tmem_ld_x8(t_row + 64 * mt + c, w);
+          tmem_ld_x8(t_row + kMaxTok * mt + c, w);
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             float v[8];
             load(0, c, v);
-            const float gates = c < 32 ? gate0 : gate1;
+            const float gates = c < 32 ? gate0 : c < 64 ? gate1 : gate2;
 #pragma unroll
             for (int i = 0; i < 8; ++i, out += pitch) {
               const float y = __shfl_sync(0xffffffffu, gates, (c + i) & 31) * v[i];
@@ -552,7 +553,7 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_coun
   FewShape f{};
   f.n_seg = n_seg;
   f.first = first ? 1 : 0;
-  f.tok = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : kMaxTok;
+  f.tok = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : kMaxTok;
   f.stage_bytes = kMats * kWBytes + f.tok * kBK;
   f.recv_bytes = kMats * f.tok * kWRows * 4;
   // Units, when the rows are spread as thin as they can be; clusters that leave no SM without a part

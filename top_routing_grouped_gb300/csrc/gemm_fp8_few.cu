@@ -19,7 +19,7 @@
 // a launch (one token of 64 experts of 4096 x 2048: 26 us for 101 MB; 13 x 2064 x 8208: 7.7 us for
 // 17 MB).  The CTA pairs take 171, 43 and 15 us for the three.
 //
-// Roles of a CTA: a TMA thread (ring of stages), an MMA warp (one elected lane issues), eight
+// Roles of a CTA: three TMA warps (ring of stages), an MMA warp (one elected lane issues), eight
 // epilogue warps and four warps that store the block factors to TMEM, as in gemm_fp8_tc.cu.  Waits are
 // bounded (MOE_ERR_TIMEOUT, no trap).
 #include <cuda.h>
@@ -204,67 +204,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   total = max(total, 0);
   volatile int* abort_flag = &ctl->abort;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- TMA producer
-      // A fill is a K block of a unit.  The second launch of a call requests the weights of its
-      // first ring of fills before the first launch has ended, and the activations after.
-      struct Cursor {
-        int u, kb;
-        Unit un;
-      };
-      auto at = [&](int u) {
-        Cursor c{u, kb0, Unit{}};
-        if (u < total) c.un = decode(ctl, f, g.E, u);
-        return c;
-      };
-      auto next = [&](Cursor& c) {
-        if (++c.kb == kb1) c = at(c.u + ncl);
-      };
-      auto fill_weights = [&](const Cursor& c, int stage) {
-        const int boxes = (c.un.rows + kTokBox - 1) / kTokBox, wrow = c.un.e * g.n + c.un.n0;
-        const uint32_t bar = ptx::smem_u32(&ctl->full[stage]), s = ptx::smem_u32(stages + (size_t)stage * f.stage_bytes);
-        ptx::mbar_arrive_expect_tx(bar, (uint32_t)(kMats * kWBytes + boxes * kTokBox * kBK));
-        ptx::tma_load_2d(s, &tmW, c.kb * kBK, wrow, bar);
-        if (kMats == 2) ptx::tma_load_2d(s + kWBytes, &tmW3, c.kb * kBK, wrow, bar);
-      };
-      auto fill_rows = [&](const Cursor& c, int stage) {
-        const int boxes = (c.un.rows + kTokBox - 1) / kTokBox;
-        const uint32_t bar = ptx::smem_u32(&ctl->full[stage]), s = ptx::smem_u32(stages + (size_t)stage * f.stage_bytes);
-        for (int b = 0; b < boxes; ++b)
-          ptx::tma_load_2d(s + kMats * kWBytes + b * kTokBox * kBK, &tmX, c.kb * kBK, c.un.row0 + b * kTokBox, bar);
-      };
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      Cursor c = at(cid);
-      if (!f.first) {
-        int ahead = 0;
-        for (Cursor w = c; ahead < f.stages && w.u < total; ++ahead, next(w)) fill_weights(w, ahead);
-        pdl_wait();
-        for (; stage < ahead; ++stage, next(c)) fill_rows(c, stage);
-        if (stage == f.stages) {
-          stage = 0;
-          phase = 1;
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ TMA producers
+    // Warp 0 loads W (W1), warp 2 W3, warp 3 the activations, each converged with one elected lane
+    // issuing: a load costs its warp about 200 clocks, and one lane that issued all of a stage's took
+    // as long to fill the ring for the first time as HBM.  In a call's second launch the weights are
+    // requested before the first launch has ended.
+    if (!f.first && warp == 3) pdl_wait();
+    const CUtensorMap* map = warp == 0 ? &tmW : warp == 2 ? &tmW3 : &tmX;
+    const uint32_t ctl0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ctl), 0);
+    const uint32_t dst0 = __shfl_sync(0xffffffffu, ptx::smem_u32(stages), 0) + (uint32_t)(warp == 0 ? 0 : warp == 2 ? kWBytes : kMats * kWBytes);
+    const bool elected = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = cid; u < total && ok && (kMats == 2 || warp != 2); u += ncl) {
+      const Unit un = decode(ctl, f, g.E, u);
+      const int boxes = __shfl_sync(0xffffffffu, (un.rows + kTokBox - 1) / kTokBox, 0);
+      const uint32_t bytes = (uint32_t)(kMats * kWBytes + boxes * kTokBox * kBK);
+      const int y = __shfl_sync(0xffffffffu, warp == 3 ? un.row0 : un.e * g.n + un.n0, 0), n = warp == 3 ? boxes : 1;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(ctl0 + (uint32_t)offsetof(Ctl, empty) + 8 * stage, phase ^ 1u, timeout_ns,
+                                                    abort_flag)) != 0;
+        if (!ok) break;
+        if (elected) {
+          const uint32_t bar = ctl0 + (uint32_t)offsetof(Ctl, full) + 8 * stage, dst = dst0 + (uint32_t)(stage * f.stage_bytes);
+          if (warp == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+          for (int b = 0; b < n; ++b) ptx::tma_load_2d(dst + b * kTokBox * kBK, map, kb * kBK, y + b * kTokBox, bar);
         }
-      }
-      while (c.u < total) {
-        if (!ptx::mbar_wait(ptx::smem_u32(&ctl->empty[stage]), phase ^ 1u, timeout_ns, abort_flag)) {
-          ok = false;
-          break;
-        }
-        fill_weights(c, stage);
-        fill_rows(c, stage);
-        next(c);
+        __syncwarp();
         if (++stage == f.stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      if (!ok) {
-        record_error(ws, MOE_ERR_TIMEOUT, 0x960u + kKind);
-        ctl->abort = 1;
-      }
+    }
+    if (!ok && elected) {
+      record_error(ws, MOE_ERR_TIMEOUT, 0x960u + kKind);
+      ctl->abort = 1;
     }
     __syncwarp();
   } else if (warp == 1) {

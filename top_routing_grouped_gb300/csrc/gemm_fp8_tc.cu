@@ -28,18 +28,18 @@
 // one factor byte, so the hidden rows cost N*F bytes instead of 2*N*F twice.
 //
 // What bounds it.  At the full MMA rate the ring alone moves 64 bytes a clock into shared memory and
-// the MMAs read 64 out of it, all that it has; the output tiles pass through it too (staging, TMA
-// store).  Counted in clocks on 8192 x 8192 x 2048 (64 K blocks a tile) the MMAs run 87 % of the time
-// and 98 % in a build without loads, hand-over and stores; on 8192 x 2048 x 8192 (16 K blocks a tile) 73 %:
-// handing over the shared columns costs about 700 clocks of 11400 a tile (2000 in a build without
-// loads), the output's way through shared memory 1300.  Times: 93 us for 8192 x 2048 x 8192 (2.95
-// PFLOP/s; 98 us while a kernel of its own built the tile tables), 84 us for 8192 x 4096 x 4096 (3.25),
-// 2.4 ms for 131072 rows of 64 experts of 4096 x 2048 (2.76, at 1.55 GHz under the power cap).
+// the MMAs read 64 out of it, all that it has; the output tiles pass through it too (staging, TMA store:
+// 1000 clocks a tile).  Counted in clocks, the MMAs run 91 % of the time from a CTA's first to its last on
+// 8192 x 8192 x 2048 (64 K blocks a tile) and 80 % on 8192 x 2048 x 8192 (16 K blocks), where handing over the
+// shared columns costs about 700 of 10200 clocks a tile.  Before the first MMA go some 5000 clocks, half
+// of them until the tiles are found, half for the first loads.  Times: 86 us for 8192 x 2048 x 8192
+// (3.2 PFLOP/s), 80 us for 8192 x 4096 x 4096 (3.4), 11 us for 2048 x 2048 x 2048, 2.27 ms for 131072 rows of
+// 64 experts of 4096 x 2048 (2.9, at 1.55 GHz under the power cap).
 //
 // Tried and dropped: 224-wide tiles, whose accumulators share no columns (the ring's time per K block
-// does not shrink with the tile: 98 -> 106 us); the output stored from registers, 32 bytes a lane
-// (99 -> 106 us); five stages and two store blocks a warp, L2 eviction priorities for A and the output
-// (no difference beyond noise).
+// does not shrink with the tile: 98 -> 106 us); the output stored from registers, 32 bytes a lane, and
+// five stages and two store blocks a warp, and L2 eviction priorities for A and the output (no
+// difference beyond noise).
 //
 // Waits are bounded (MOE_ERR_TIMEOUT, no trap); an abort raises the flag in both CTAs; the pair
 // meets at cluster barriers before TMEM is released.
@@ -166,9 +166,11 @@ __device__ __forceinline__ TileInfo decode(const Segments* sg, int n_seg, int E,
   ti.n_idx = rem / gp;
   const int m0 = grp * kGroupM * kTileM + (2 * (rem % gp) + rank) * kTileM;
   ti.row0 = row0 + m0;
-  ti.rows = min(kTileM, cnt - m0);
+  ti.rows = cnt - m0;  // to the end of its segment: may be above kTileM, or below 1 for a pair's second tile
   return ti;
 }
+
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 
 __device__ __forceinline__ void raise_abort(Ctl* ctl, uint32_t rank) {
   ctl->abort = 1;
@@ -199,7 +201,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int sck = (int)(scale_cols(g.K) / 4);  // words of factors per row
   const int nb = (g.n + kBlock - 1) / kBlock;
 
-  if (threadIdx.x == 0) {
+  // Setting up takes microseconds where its steps wait for one another: warp 8 makes the barriers and warp 9,
+  // once the peer has started, takes TMEM, while the others wait for the previous kernel or find the tiles.
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  if (threadIdx.x == 8 * 32) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(ptx::smem_u32(&ctl->full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&ctl->empty[i]), 1);
@@ -215,34 +220,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
-    ctl->peer_tmem_base = 0xFFFFFFFFu;
     ptx::fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) {
+  if (threadIdx.x == 10 * 32) {
     ptx::tma_prefetch_desc(&tmA);
     ptx::tma_prefetch_desc(&tmB);
     if (kKind == kSwiGLU) ptx::tma_prefetch_desc(&tmB3);
     ptx::tma_prefetch_desc(&tmY);
   }
-  ptx::cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or load
-  if (warp == 2) {
+  cluster_wait();
+  if (warp == 9) {
     ptx::tmem_alloc_pair(ptx::smem_u32(&ctl->tmem_base), kTmemCols);
     ptx::tmem_relinquish_pair();
+    if (lane == 0) ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&ctl->peer_tmem_base), rank ^ 1u), ctl->tmem_base);
   }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
-  if (threadIdx.x == 0) ptx::st_cluster_u32(ptx::mapa(ptx::smem_u32(&ctl->peer_tmem_base), rank ^ 1u), tmem);
-  ptx::cluster_sync();
+  asm volatile("barrier.cluster.arrive;" ::: "memory");  // both CTAs' barriers exist before any load or cross-CTA arrive
   // The call's first launch waits here for the counts and the activations; its second one waits for
-  // the hidden rows alone, once it has found its tiles.
-  if (first) pdl_wait();
+  // the hidden rows alone, once it has found its tiles, as does a call without counts.
+  const bool counts_ready = !first || seg_counts == nullptr;
+  if (!counts_ready) pdl_wait();
   int total = scan_segments(&ctl->seg, seg_counts, n_seg, g.rows, [&](int cnt) { return pairs_of(cnt) * n_tiles; });
+  if (counts_ready) pdl_wait();
   if (first) begin_status(ws, total < 0, 0x900u);
   total = max(total, 0);
-  if (!first) pdl_wait();
   pdl_launch_dependents();
+  cluster_wait();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
   // a pair's accumulators must sit at the same TMEM address, the ring on its boundary
   if (ctl->peer_tmem_base != tmem || (ptx::smem_u32(stages) & 1023u) != 0) {
     if (threadIdx.x == 0) {
@@ -257,36 +261,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kEpiWarp0) {
     regs_dec<kRegsFew>();
-    if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------- TMA producer (both CTAs)
+    if (warp == 0 || warp == 2) {
+      // ---------------------------------------------------------- TMA producers (both CTAs)
+      // Warp 0 loads A, warp 2 the weights; the warps run converged and one elected lane issues (205
+      // clocks for a wait, an arrive and a load; 337 for one lane in a branch of its own, close to
+      // the 512 that a stage's MMAs take).
+      const bool a_side = warp == 0;
+      const CUtensorMap* map = a_side ? &tmA : (kKind == kSwiGLU && rank == 1) ? &tmB3 : &tmB;
+      const uint32_t ctl0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ctl), 0);
+      const uint32_t bar0 = __shfl_sync(0xffffffffu, ptx::mapa(ctl0 + (uint32_t)offsetof(Ctl, full), 0), 0);
+      const uint32_t dst0 = __shfl_sync(0xffffffffu, ptx::smem_u32(stages), 0) + (a_side ? 0u : (uint32_t)kABytes);
+      const int first_tile = __shfl_sync(0xffffffffu, cid, 0), stride = __shfl_sync(0xffffffffu, ncl, 0);
+      const int tiles_end = __shfl_sync(0xffffffffu, total, 0);
+      const bool elected = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      const CUtensorMap* bmap = (kKind == kSwiGLU && rank == 1) ? &tmB3 : &tmB;
-      for (int tile = cid; tile < total && ok; tile += ncl) {
+      for (int tile = first_tile; tile < tiles_end && ok; tile += stride) {
         const TileInfo ti = decode(&ctl->seg, n_seg, g.E, n_tiles, tile, (int)rank);
-        // a pair's second m-tile may not exist: its A rows are neither loaded nor waited for
-        const bool peer_rows = decode(&ctl->seg, n_seg, g.E, n_tiles, tile, 1).rows > 0;
-        const uint32_t bytes = peer_rows ? 2 * kStageBytes : 2 * kStageBytes - kABytes;
+        // a pair's second m-tile may not exist: its A rows are neither loaded nor waited for (the leader's
+        // view; its peer expects nothing)
+        const uint32_t bytes = ti.rows > kTileM ? 2 * kStageBytes : 2 * kStageBytes - kABytes;
         const int brow = ti.e * g.n + ti.n_idx * bn + (kKind == kSwiGLU ? 0 : (int)rank * (kMmaN / 2));
+        const int y = __shfl_sync(0xffffffffu, a_side ? ti.row0 : brow, 0);
+        const bool load = !a_side || ti.rows > 0;
         for (int kb = 0; kb < kblocks; ++kb) {
-          if (!ptx::mbar_wait(ptx::smem_u32(&ctl->empty[stage]), phase ^ 1u, timeout_ns, abort_flag)) {
-            ok = false;
-            break;
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(ctl0 + (uint32_t)offsetof(Ctl, empty) + 8 * stage, phase ^ 1u,
+                                                      timeout_ns, abort_flag)) != 0;
+          if (!ok) break;
+          if (elected) {
+            if (a_side && leader) ptx::mbar_arrive_expect_tx(ctl0 + (uint32_t)offsetof(Ctl, full) + 8 * stage, bytes);
+            if (load) ptx::tma_load_2d_pair(dst0 + stage * kStageBytes, map, kb * kBK, y, bar0 + 8 * stage);
           }
-          const uint32_t full_local = ptx::smem_u32(&ctl->full[stage]);
-          if (leader) ptx::mbar_arrive_expect_tx(full_local, bytes);
-          const uint32_t bar = ptx::mapa(full_local, 0);
-          const uint32_t sa = ptx::smem_u32(stages + (size_t)stage * kStageBytes);
-          if (ti.rows > 0) ptx::tma_load_2d_pair(sa, &tmA, kb * kBK, ti.row0, bar);
-          ptx::tma_load_2d_pair(sa + kABytes, bmap, kb * kBK, brow, bar);
+          __syncwarp();
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (!ok) {
+      if (!ok && elected) {
         record_error(ws, MOE_ERR_TIMEOUT, 0x910u + kKind);
         raise_abort(ctl, rank);
       }
@@ -398,28 +412,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       request();
     }
     while (tile < total) {
-      const uint32_t w[4] = {a[0], a[1], a[2], a[3]}, w0 = b0, w1 = b1;
+      ok = ptx::mbar_wait(ptx::smem_u32(&ctl->sf_empty[set]), phase ^ 1u, timeout_ns, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      tmem_st_x4(dst + set * kSfStep, a[0], a[1], a[2], a[3]);
+      tmem_st_x4(dst + set * kSfStep + 4, b0, b0, b0, b0);
+      tmem_st_x4(dst + set * kSfStep + 8, b1, b1, b1, b1);
+      tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_relaxed_cluster(ptx::mapa(ptx::smem_u32(&ctl->sf_full[set]), 0));
+      if (++set == kSfSets) {
+        set = 0;
+        phase ^= 1u;
+      }
       if (++gk == sck) {
         gk = 0;
         tile += ncl;
         if (tile < total) locate();
       }
       if (tile < total) request();
-      ok = ptx::mbar_wait(ptx::smem_u32(&ctl->sf_empty[set]), phase ^ 1u, timeout_ns, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      tmem_st_x4(dst + set * kSfStep, w[0], w[1], w[2], w[3]);
-      tmem_st_x4(dst + set * kSfStep + 4, w0, w0, w0, w0);
-      tmem_st_x4(dst + set * kSfStep + 8, w1, w1, w1, w1);
-      tmem_st_wait();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->sf_full[set]), 0));
-      if (++set == kSfSets) {
-        set = 0;
-        phase ^= 1u;
-      }
     }
     if (!ok && lane == 0) {
       record_error(ws, MOE_ERR_TIMEOUT, 0x930u + kKind);
@@ -448,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto arrive = [&](uint32_t bar) {  // after this warp's loads so far
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(bar);
+        if (lane == 0) arrive_relaxed_cluster(bar);
       };
       const bool valid = r < ti.rows;
       const int64_t p = (int64_t)ti.row0 + r;
@@ -568,8 +581,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  __syncthreads();
-  ptx::cluster_sync();  // neither CTA issues loads or MMAs any more
   if (*abort_flag && threadIdx.x == 0) {
     // copies already in flight land within microseconds; give them 200 us before the
     // shared memory they target goes away
@@ -578,9 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   ptx::tc_fence_before();
-  __syncthreads();
-  ptx::cluster_sync();
-  if (warp == 2) {
+  ptx::cluster_sync();  // neither CTA loads, computes or reads TMEM any more
+  if (warp == 9) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, kTmemCols);
   }

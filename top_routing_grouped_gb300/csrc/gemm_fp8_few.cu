@@ -514,6 +514,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kSmemMax = 232448;
+constexpr int kMaxSplit = 8;
+
+// Clusters of `split` CTAs, each CTA alone on its SM, that run at the same time.  A cluster lies within
+// a group of SMs that the hardware has, so this is less than SMs / split (152 SMs: 36 clusters of 4, 15 of 8).
+template <int kKind>
+int most_clusters(int device, int split) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices][kMaxSplit + 1];
+  const bool keep = device >= 0 && device < kMaxDevices;
+  if (keep)
+    if (const int n = known[device][split].load(std::memory_order_acquire)) return n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)split;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemMax;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_fp8_few_kernel<kKind>, &cfg) != cudaSuccess || n < 1) n = 1;
+  if (keep) known[device][split].store(n, std::memory_order_release);
+  return n;
+}
 
 template <int kKind>
 cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first, int device,
@@ -533,15 +560,17 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_coun
   f.tok = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : kMaxTok;
   f.stage_bytes = kMats * kWBytes + f.tok * kBK;
   f.recv_bytes = kMats * f.tok * kWRows * 4;
-  // Units, when the rows are spread as thin as they can be; clusters that leave no SM without a part
-  // of one.  K is split in whole groups of four blocks, and the others' sums need shared memory.
+  // Units, when the rows are spread as thin as they can be; clusters that run all of them at once.  K is
+  // split in whole groups of four blocks (of the splits with the same longest part the smallest), and
+  // the others' sums need shared memory.
   const int64_t nblk = (g.n + kWRows - 1) / kWRows, owners = g.rows < n_seg ? g.rows : n_seg;
   const int64_t units = owners * nblk * (owners == 1 ? (g.rows + f.tok - 1) / f.tok : 1);
   const int sck = (int)(scale_cols(g.K) / 4), fixed = 1024 + (int)sizeof(Ctl);
   f.split = 1;
-  while (f.split < 8 && 2 * f.split * units <= num_sms && 2 * f.split <= sck &&
-         fixed + (2 * f.split - 1) * f.recv_bytes + 4 * f.stage_bytes <= kSmemMax)
-    f.split *= 2;
+  for (int s = 2; s <= kMaxSplit && s <= sck && s * units <= num_sms; ++s) {
+    if (fixed + (s - 1) * f.recv_bytes + 4 * f.stage_bytes > kSmemMax || units > most_clusters<kKind>(device, s)) break;
+    if ((sck + s - 1) / s < (sck + f.split - 1) / f.split) f.split = s;
+  }
   f.stages = (kSmemMax - fixed - (f.split - 1) * f.recv_bytes) / f.stage_bytes;
   if (f.stages > kMaxStages) f.stages = kMaxStages;
   const size_t smem = (size_t)fixed + (size_t)(f.split - 1) * f.recv_bytes + (size_t)f.stages * f.stage_bytes;

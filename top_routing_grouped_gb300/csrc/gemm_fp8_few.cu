@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int gk0 = sck * (int)rank / f.split, gk1 = sck * ((int)rank + 1) / f.split;  // this CTA's groups of four K blocks
   const int kb0 = gk0 * 4, kb1 = min(gk1 * 4, kblocks);
 
-  if (threadIdx.x == 0) {
+  // Warp 8 makes the barriers and warp 12 takes TMEM while warps 0-7 wait for the counts and find the units.
+  if (threadIdx.x == 8 * 32) {
     for (int i = 0; i < f.stages; ++i) {
       ptx::mbar_init(ptx::smem_u32(&ctl->full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&ctl->empty[i]), 1);
@@ -180,19 +181,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
+  }
+  if (threadIdx.x == 9 * 32) {
     ptx::tma_prefetch_desc(&tmX);
     ptx::tma_prefetch_desc(&tmW);
     if (kMats == 2) ptx::tma_prefetch_desc(&tmW3);
   }
-  if (warp == 2) {
+  if (f.split > 1) asm volatile("barrier.cluster.arrive;" ::: "memory");
+  if (warp == kSfWarp0) {
     ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), kTmemCols);
     ptx::tmem_relinquish();
+    ptx::tc_fence_before();
   }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
-  if (f.split > 1) ptx::cluster_sync();  // every CTA's barriers exist before another arrives on them
   // The call's first launch waits here for the counts and the activations.  Its second one starts
   // when the first does (as far as SMs are free): the counts are there then, and only what the first
   // launch computes, the hidden rows and their factors, is waited for where it is read.
@@ -202,6 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int total = scan_segments(&ctl->seg, seg_counts, f.n_seg, g.rows, [&](int cnt) { return (cnt + f.tok - 1) / f.tok * nblk; });
   if (f.first) begin_status(ws, total < 0, 0x950u);
   total = max(total, 0);
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;  // made visible by the scan's barriers, as the barriers are
+  if (f.split > 1) asm volatile("barrier.cluster.wait;" ::: "memory");  // every CTA's barriers exist before another arrives on them
   volatile int* abort_flag = &ctl->abort;
 
   if (warp == 0 || warp == 2 || warp == 3) {
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // does: the first CTA has received every sum, and the others have used every release but the last
   // unit's, which is not sent; so they leave at once and make room for the next launch.
   if (f.split > 1 && *abort_flag) ptx::cluster_sync();
-  if (warp == 2) {
+  if (warp == kSfWarp0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }

@@ -296,6 +296,31 @@ def test_matmul(fp8, path, out, seg, E, K, N):
     assert (np64(o)[m:] == 77).all(), "rows past the segments are not written"
 
 
+CLUSTERS = [  # K split over clusters of 3, 5, 6, 7 and 8 CTAs, which take two or three units each
+    ([5000, 9], 2, 1424, 128), ([4000, 0, 1900], 3, 4624, 128), ([2600, 17], 2, 2832, 96), ([2500, 3], 2, 7168, 64),
+    ([2100, 95, 5], 3, 4096, 112),
+]
+
+
+@pytest.mark.parametrize("seg, E, K, N", CLUSTERS, ids=lambda v: str(v))
+def test_matmul_clusters_take_several_units(fp8, seg, E, K, N):
+    test_matmul(fp8, "auto", BF, seg, E, K, N)
+
+
+@pytest.mark.parametrize("K", [512, 1536, 2560, 8192])
+def test_matmul_rows_sum_alike_wherever_they_stand(fp8, K):
+    """Equal rows give equal bits, whichever CTA of a cluster adds their parts."""
+    n, N = 83, 160
+    (qa, sa), (qw, sw) = make_rows(1, K, 51), make_weights(1, N, K, 52)
+    plan = fp8.Fp8MatmulPlan(n, K, N, out_dtype="f32")
+    o, ws = torch.empty(n, N, device="cuda"), plan.new_workspace()
+    (ta, tsa), (tw, tsw) = ref.to_torch(qa, sa), ref.to_torch(qw, sw)
+    rows = lambda x: x.expand(n, -1).contiguous().cuda()
+    plan.forward(None, rows(ta.view(torch.uint8)).view(ta.dtype), rows(tsa), tw.cuda(), tsw.cuda(), o, ws)
+    assert plan.device_status(ws) == 0
+    assert (o == o[0]).all()
+
+
 @pytest.mark.parametrize("path", ["simt", "auto"])
 def test_matmul_whole_buffer_without_counts(fp8, path):
     n, K, N = 200, 256, 320
@@ -422,6 +447,10 @@ def test_experts(fp8, path, seg, E, d, F):
         return
     want, tol = expert_rows(ref.dequantize(qx, sx)[:m], (q1, s1), (q3, s3), (q2, s2), np64(gates)[:m], ref.row_experts(seg, E))
     close(np64(y)[:m], want, tol, "y")
+
+
+def test_experts_clusters_take_several_units(fp8):
+    test_experts(fp8, "auto", [97] * 27 + [2] * 11, 38, 1024, 256)
 
 
 def test_experts_paths_agree_on_a_larger_layer(fp8):

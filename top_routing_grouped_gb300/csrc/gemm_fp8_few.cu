@@ -10,9 +10,10 @@
 //
 // A unit of work is (segment, block of 128 weight rows, up to 96 of the segment's rows).  Every CTA
 // finds its units from the segment counts itself (a scan over at most 256 numbers), so a call needs no
-// kernel for tile tables.  When there are fewer units than SMs, a cluster of 2, 4 or 8 CTAs
-// shares a unit: each sums a part of K, and the first CTA adds the others' sums, which arrive in
-// its shared memory, in rank order.
+// kernel for tile tables.  When there are fewer units than SMs, a cluster of up to 8 CTAs shares a
+// unit: each sums a part of K, and the unit's rows are dealt out to the CTAs, eight at a time; for its
+// rows a CTA adds the others' sums, which arrive in its shared memory, in rank order.  (With all rows
+// summed by the first CTA 96 x 8192 x 2048 took 13.4 us, not 9.7.)
 //
 // What bounds it: HBM while the weights stream (1500 rows over 128 experts of 2048 x 1024: 128 us,
 // 6.2 TB/s of weights, rows and results); with one unit for each SM the fixed part counts, about 5 us of
@@ -61,8 +62,8 @@ struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2];
   uint64_t sf_full[kSfSets], sf_empty[kSfSets];
-  uint64_t rfull;  // first CTA: the others' sums have arrived
-  uint64_t rfree;  // others: the first CTA has read this one's sums
+  uint64_t rfull;  // the others' sums for this CTA's rows have arrived
+  uint64_t rfree;  // the others have read this CTA's sums of the unit before
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -76,8 +77,9 @@ struct FewShape {
   int tok;         // rows per unit: a multiple of 16, at most kMaxTok
   int stages;
   int stage_bytes;
-  int recv_bytes;  // shared memory for one other CTA's sums
   int split;       // CTAs of a cluster that share a unit
+  int part;        // rows of a unit that fall to one of them at most, a multiple of 8
+  int recv_bytes;  // shared memory for one other CTA's sums: [matrix][part][128 weight rows]
   int first;       // this launch starts the call: it sets the status word
 };
 
@@ -143,23 +145,25 @@ __device__ __forceinline__ Unit decode(const Ctl* ctl, const FewShape& f, int E,
   return r;
 }
 
-template <int kKind>
+// kSplit: a unit is shared by a cluster (its code costs the others 0.2 us a launch where it is merely there).
+template <int kKind, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_fp8_few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmW3, GemmArgs g, Ws ws, const int32_t* seg_counts, FewShape f,
                         int64_t timeout_ns) {
   constexpr int kMats = kKind == kSwiGLU ? 2 : 1;
+  const int split = kSplit ? f.split : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* recv = reinterpret_cast<float*>(stages + (size_t)f.stages * f.stage_bytes);
-  Ctl* ctl = reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(recv) + (size_t)(f.split - 1) * f.recv_bytes);
+  Ctl* ctl = reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(recv) + (size_t)(split - 1) * f.recv_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = f.split > 1 ? ptx::cluster_ctarank() : 0;
-  const int cid = (int)(blockIdx.x / f.split), ncl = (int)(gridDim.x / f.split);
+  const uint32_t rank = kSplit ? ptx::cluster_ctarank() : 0;
+  const int cid = (int)blockIdx.x / split, ncl = (int)gridDim.x / split;
   const int nblk = (g.n + kWRows - 1) / kWRows;
   const int kblocks = (g.K + kBK - 1) / kBK;
   const int sck = (int)(scale_cols(g.K) / 4);
-  const int gk0 = sck * (int)rank / f.split, gk1 = sck * ((int)rank + 1) / f.split;  // this CTA's groups of four K blocks
+  const int gk0 = sck * (int)rank / split, gk1 = sck * ((int)rank + 1) / split;  // this CTA's groups of four K blocks
   const int kb0 = gk0 * 4, kb1 = min(gk1 * 4, kblocks);
 
   // Warp 8 makes the barriers and warp 12 takes TMEM while warps 0-7 wait for the counts and find the units.
@@ -176,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&ctl->sf_full[i]), 4);
       ptx::mbar_init(ptx::smem_u32(&ctl->sf_empty[i]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(&ctl->rfull), f.split > 1 ? kEpiWarps * (f.split - 1) : 1);
-    ptx::mbar_init(ptx::smem_u32(&ctl->rfree), kEpiWarps);
+    ptx::mbar_init(ptx::smem_u32(&ctl->rfull), kSplit ? kEpiWarps * (split - 1) : 1);
+    ptx::mbar_init(ptx::smem_u32(&ctl->rfree), kSplit ? kEpiWarps * (split - 1) : 1);
     ptx::mbar_init(ptx::smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tma_prefetch_desc(&tmW);
     if (kMats == 2) ptx::tma_prefetch_desc(&tmW3);
   }
-  if (f.split > 1) asm volatile("barrier.cluster.arrive;" ::: "memory");
+  if (kSplit) asm volatile("barrier.cluster.arrive;" ::: "memory");
   if (warp == kSfWarp0) {
     ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), kTmemCols);
     ptx::tmem_relinquish();
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   total = max(total, 0);
   ptx::tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;  // made visible by the scan's barriers, as the barriers are
-  if (f.split > 1) asm volatile("barrier.cluster.wait;" ::: "memory");  // every CTA's barriers exist before another arrives on them
+  if (kSplit) asm volatile("barrier.cluster.wait;" ::: "memory");  // every CTA's barriers exist before another arrives on them
   volatile int* abort_flag = &ctl->abort;
 
   if (warp == 0 || warp == 2 || warp == 3) {
@@ -370,72 +374,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A warp here runs alone on its scheduler for the most part, so what counts is the length of its
     // instruction chain: rows eight at a time (short code, fetched once), two sets of warps.
     const int q = warp & 3, set = (warp - kEpiWarp0) >> 2, m = q * 32 + lane;  // m: weight row of the block
-    const float* mine = recv + m;  // the others' sums: [rank - 1][matrix][row][128 weight rows]
-    const int recv_floats = f.recv_bytes / 4;
+    // Rows 8 gi .. 8 gi + 7 fall to CTA gi % split, which counts them its group gi / split; a set takes
+    // every other one of these counts.  Where the others' sums land: [other CTA, this one left out].
+    const float* mine = recv + m;
+    const int recv_floats = f.recv_bytes / 4, me = (int)rank;
     const int64_t scn = scale_cols(g.n);
     constexpr int kOsz = kKind == kSwiGLU ? 1 : kKind == kOutBf16 ? 2 : 4;
     const int64_t pitch = (int64_t)g.n * kOsz;
     int acc = 0, turn = 0;
-    uint32_t acc_phase = 0, r_phase = 0;
+    uint32_t acc_phase = 0, full_phase = 0, free_phase = 0;
     bool ok = true;
     for (int u = cid; u < total; u += ncl) {
       const Unit un = decode(ctl, f, g.E, u);
       const int col = un.n0 + m;
       const bool in = col < g.n;
       float gate0 = 1.f, gate1 = 1.f, gate2 = 1.f;  // of rows lane, lane + 32 and lane + 64
-      if (kKind != kSwiGLU && rank == 0 && g.gate) {
+      if (kKind != kSwiGLU && g.gate) {
         if (lane < un.rows) gate0 = g.gate[un.row0 + lane];
         if (lane + 32 < un.rows) gate1 = g.gate[un.row0 + lane + 32];
         if (lane + 64 < un.rows) gate2 = g.gate[un.row0 + lane + 64];
       }
       ok = ptx::mbar_wait(ptx::smem_u32(&ctl->tfull[acc]), acc_phase, timeout_ns, abort_flag);
-      if (f.split > 1)
-        ok = ok && wait_cluster(ptx::smem_u32(rank == 0 ? &ctl->rfull : &ctl->rfree), rank == 0 ? r_phase : r_phase ^ 1u,
-                                timeout_ns, abort_flag);
+      if (kSplit && u != cid) {
+        ok = ok && wait_cluster(ptx::smem_u32(&ctl->rfree), free_phase, timeout_ns, abort_flag);
+        free_phase ^= 1u;
+      }
       ok = epi_bar_and(set, ok);  // the set's four warps go on or stop together
       if (!ok) break;
       ptx::tc_fence_after();
-      r_phase ^= 1u;
       const uint32_t t_row = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * 2 * kMaxTok);
-      if (rank != 0) {
-        // this CTA's sums to the first CTA (rows past the unit's last fill the buffer, unread)
-        const uint32_t dst = ptx::mapa(ptx::smem_u32(recv), 0) + (uint32_t)(((int)rank - 1) * f.recv_bytes + m * 4);
+      const int owners = min(split, (un.rows + 7) / 8);  // CTAs that have rows of this unit
+      if constexpr (kSplit) {
+        const uint32_t base = ptx::smem_u32(recv) + (uint32_t)(m * 4);
 #pragma unroll 1
-        for (int mt = 0; mt < kMats; ++mt)
+        for (int li = set; 8 * li * split < un.rows; li += 2)
 #pragma unroll 1
-          for (int c = 8 * set; c < un.rows; c += 16) {
-            uint32_t v[8];
-            tmem_ld_x8(t_row + kMaxTok * mt + c, v);
-            ptx::tmem_ld_wait();
-            const uint32_t to = dst + (uint32_t)((mt * f.tok + c) * 512);
+          for (int to = 0; to < split; ++to) {
+            const int c = 8 * (li * split + to);
+            if (to == me || c >= un.rows) continue;
+            const uint32_t dst = ptx::mapa(base + (uint32_t)((me - (me > to)) * f.recv_bytes + li * 8 * 512), (uint32_t)to);
+#pragma unroll 1
+            for (int mt = 0; mt < kMats; ++mt) {
+              uint32_t v[8];
+              tmem_ld_x8(t_row + kMaxTok * mt + c, v);
+              ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) st_cluster_f32(to + 512 * i, v[i]);
+              for (int i = 0; i < 8; ++i) st_cluster_f32(dst + (uint32_t)(mt * f.part * 512) + 512 * i, v[i]);
+            }
           }
-        ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(ptx::smem_u32(&ctl->tempty[acc]));
-          ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfull), 0));
+        if (lane < owners && lane != me) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfull), (uint32_t)lane));
+        if (me < owners) {
+          ok = wait_cluster(ptx::smem_u32(&ctl->rfull), full_phase, timeout_ns, abort_flag);
+          full_phase ^= 1u;
+          ok = epi_bar_and(set, ok);
+          if (!ok) break;
         }
-      } else {
+      }
+      {
         auto load = [&](int mt, int c, float(&v)[8]) {
           uint32_t w[8];
           tmem_ld_x8(t_row + kMaxTok * mt + c, w);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-          const float* o = mine + (mt * f.tok + c) * 128;
+          for (int i = 0; i < 8; ++i) v[i] = kSplit ? 0.f : __uint_as_float(w[i]);
+          if constexpr (kSplit) {
+            const float* o = mine + (mt * f.part + 8 * (c / 8 / split)) * 128;
 #pragma unroll 1
-          for (int r = 0; r < f.split - 1; ++r, o += recv_floats) {
-            float x[8];
+            for (int r = 0; r < split; ++r) {  // in rank order, whichever CTA adds
+              float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = o[128 * i];
+              for (int i = 0; i < 8; ++i) x[i] = r == me ? __uint_as_float(w[i]) : o[128 * i];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += x[i];
+              for (int i = 0; i < 8; ++i) v[i] += x[i];
+              if (r != me) o += recv_floats;
+            }
           }
         };
 #pragma unroll 1
-        for (int c = 8 * set; c < un.rows; c += 16) {
+        for (int c = 8 * (set * split + me); c < un.rows; c += 16 * split) {
           const int nt = un.rows - c;
           const int64_t p0 = (int64_t)un.row0 + c;
           uint8_t* out = reinterpret_cast<uint8_t*>(g.out) + p0 * pitch + (int64_t)col * kOsz;
@@ -478,11 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(ptx::smem_u32(&ctl->tempty[acc]));
-          if (u + ncl < total)  // the others do not wait for this after their last unit
-            for (int r = 1; r < f.split; ++r) ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfree), (uint32_t)r));
-        }
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&ctl->tempty[acc]));
+        // Read: the others may send the next unit's sums (after the last unit no one waits for this).  One
+        // that has no rows of the next unit may arrive for that too before all others' arrivals for this
+        // one have landed here; it has seen them, so the sums were read by then.
+        if (kSplit && lane < split && lane != me && u + ncl < total)
+          ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&ctl->rfree), (uint32_t)lane));
       }
       if (++acc == 2) {
         acc = 0;
@@ -507,9 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   // No CTA's shared memory goes while another may still write to it.  After an undisturbed run none
-  // does: the first CTA has received every sum, and the others have used every release but the last
-  // unit's, which is not sent; so they leave at once and make room for the next launch.
-  if (f.split > 1 && *abort_flag) ptx::cluster_sync();
+  // does: a CTA has waited for all sums of its rows, and for every release but the last unit's, which
+  // is not sent; so it leaves at once and makes room for the next launch.
+  if (kSplit && *abort_flag) ptx::cluster_sync();
   if (warp == kSfWarp0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
@@ -540,7 +558,7 @@ int most_clusters(int device, int split) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, gemm_fp8_few_kernel<kKind>, &cfg) != cudaSuccess || n < 1) n = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, gemm_fp8_few_kernel<kKind, true>, &cfg) != cudaSuccess || n < 1) n = 1;
   if (keep) known[device][split].store(n, std::memory_order_release);
   return n;
 }
@@ -549,12 +567,13 @@ template <int kKind>
 cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first, int device,
                         int num_sms, int64_t timeout_ns, cudaStream_t st) {
   constexpr int kMats = kKind == kSwiGLU ? 2 : 1;
-  auto kern = gemm_fp8_few_kernel<kKind>;
   cudaError_t e;
-  static std::atomic<uint64_t> asked{0};  // devices on which the kernel may use all shared memory
+  static std::atomic<uint64_t> asked{0};  // devices on which the kernels may use all shared memory
   const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
   if (!(asked.load(std::memory_order_acquire) & bit) || !bit) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)) != cudaSuccess) return e;
+    constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if ((e = cudaFuncSetAttribute(gemm_fp8_few_kernel<kKind, false>, kAttr, kSmemMax)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(gemm_fp8_few_kernel<kKind, true>, kAttr, kSmemMax)) != cudaSuccess) return e;
     asked.fetch_or(bit, std::memory_order_release);
   }
   FewShape f{};
@@ -562,7 +581,9 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_coun
   f.first = first ? 1 : 0;
   f.tok = g.rows <= 16 ? 16 : g.rows <= 32 ? 32 : g.rows <= 64 ? 64 : kMaxTok;
   f.stage_bytes = kMats * kWBytes + f.tok * kBK;
-  f.recv_bytes = kMats * f.tok * kWRows * 4;
+  // rows of a CTA in a cluster of s, and the shared memory for the others' sums of them
+  auto part = [&](int s) { return (f.tok / 8 + s - 1) / s * 8; };
+  auto recv = [&](int s) { return s == 1 ? 0 : kMats * part(s) * kWRows * 4; };
   // Units, when the rows are spread as thin as they can be; clusters that run all of them at once.  K is
   // split in whole groups of four blocks (of the splits with the same longest part the smallest), and
   // the others' sums need shared memory.
@@ -571,9 +592,11 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_coun
   const int sck = (int)(scale_cols(g.K) / 4), fixed = 1024 + (int)sizeof(Ctl);
   f.split = 1;
   for (int s = 2; s <= kMaxSplit && s <= sck && s * units <= num_sms; ++s) {
-    if (fixed + (s - 1) * f.recv_bytes + 4 * f.stage_bytes > kSmemMax || units > most_clusters<kKind>(device, s)) break;
+    if (fixed + (s - 1) * recv(s) + 4 * f.stage_bytes > kSmemMax || units > most_clusters<kKind>(device, s)) break;
     if ((sck + s - 1) / s < (sck + f.split - 1) / f.split) f.split = s;
   }
+  f.part = part(f.split);
+  f.recv_bytes = recv(f.split);
   f.stages = (kSmemMax - fixed - (f.split - 1) * f.recv_bytes) / f.stage_bytes;
   if (f.stages > kMaxStages) f.stages = kMaxStages;
   const size_t smem = (size_t)fixed + (size_t)(f.split - 1) * f.recv_bytes + (size_t)f.stages * f.stage_bytes;
@@ -585,6 +608,7 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_coun
   if (kMats == 2 && (e = make_tmap_rows128(&mW3, g.b3, 1, wrows, (uint64_t)g.K, kWRows)) != cudaSuccess) return e;
   const int64_t clusters = num_sms / f.split, most = (g.rows / f.tok + owners) * nblk;  // no more units than that
   const int grid = (int)(clusters < most ? clusters : most) * f.split;
+  auto kern = f.split > 1 ? gemm_fp8_few_kernel<kKind, true> : gemm_fp8_few_kernel<kKind, false>;
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, true, f.split, mX, mW, mW3, g, ws, seg_counts, f,
                        timeout_ns);
 }

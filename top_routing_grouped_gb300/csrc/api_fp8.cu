@@ -29,13 +29,13 @@ namespace fp8 {
 // Which tensor-core kernels.  Those that make the weights the MMA's rows read each weight tile once for
 // every 96 rows of a segment; the CTA pairs take 256 rows at the price of one.  Measured (experts;
 // time of the pairs / time of the others, for 8 experts of 2048 x 8192, 32 of 2048 x 2048, 64 of
-// 4096 x 2048): 16 rows a segment 1.07-1.11, 48 rows 1.04-1.09, 64 rows 1.03-1.09, 80 rows 1.02-1.06 (0.92 and
-// 0.98 for 4 of 2048 x 1024 and 8 of 1024 x 1024), 96 rows (half the segments need a second pass) 0.82-1.00, 128
-// rows 0.79-0.83.  With few units of work (block of weight rows x group of rows) the pairs also leave SMs
-// idle.  One segment: the others win as long as all units run at once (dense products K x n of 2048 x
-// 2048, 4096 x 4096, 2048 x 8192, 512 x 4096: 64 units 0.99-1.24, 96 to 128 units 1.00-1.12, 192 units 0.55-0.89; one row
-// 1.3-1.8).  Several, of uneven counts: up to half of the SMs (2 of 2048 x 2048: 48 units 0.99-1.01, 64 0.96, 80
-// to 112 0.83).
+// 4096 x 2048): 16 rows a segment 1.07-1.11, 48 rows 1.04-1.08, 64 rows 1.03-1.06, 80 rows 1.01-1.04 (0.95
+// for 4 of 2048 x 1024), 96 rows (half the segments need a second pass) 0.82-1.00, 128 rows 0.81-0.83.
+// With few units of work (block of weight rows x group of rows) the pairs also leave SMs idle.  One
+// segment: the others win as long as all units run at once (dense products K x n of 2048 x 2048, 4096 x
+// 4096, 2048 x 8192, 512 x 4096, 8192 x 2048: 48 to 64 units 1.1-1.5, 96 to 128 units 1.02-1.27, 192 units
+// 0.58-0.93; one row 1.3-2.7).  Several, of uneven counts: up to half of the SMs (4 of 512 x 512 and 2 of 2048 x
+// 2048: 48 to 64 units 0.92-1.07, 100 0.99; 3 of 1024 x 2048: 80 units 0.99).
 bool use_few(int64_t rows, int64_t n_seg, int64_t widest_out) {
   const int64_t units = ((rows + 95) / 96 + n_seg - 1) * ((widest_out + 127) / 128);
   return rows <= 72 * n_seg || units <= (n_seg == 1 ? 152 : 76);

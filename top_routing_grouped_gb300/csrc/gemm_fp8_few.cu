@@ -15,10 +15,12 @@
 // rows a CTA adds the others' sums, which arrive in its shared memory, in rank order.  (With all rows
 // summed by the first CTA 96 x 8192 x 2048 took 13.4 us, not 9.7.)
 //
-// What bounds it: HBM while the weights stream (1500 rows over 128 experts of 2048 x 1024: 128 us,
-// 6.2 TB/s of weights, rows and results); with one unit for each SM the fixed part counts, about 5 us of
-// a launch (one token of 64 experts of 4096 x 2048: 26 us for 101 MB; 13 x 2064 x 8208: 7.7 us for
-// 17 MB).  The CTA pairs take 171, 43 and 15 us for the three.
+// What bounds it: HBM while the weights stream (1500 rows over 128 experts of 2048 x 1024: 126 us,
+// 6.3 TB/s of weights, rows and results); with one unit for each SM the fixed part counts, about 5 us of
+// a launch (one token of 64 experts of 4096 x 2048: 24.3 us for 101 MB; 13 x 2064 x 8208: 7.3 us for
+// 17 MB).  The CTA pairs take 141, 34 and 9.8 us for the three.  In the token's call HBM stands still for some
+// 3.5 us between the two products (epilogue, launch, set-up); fetching the second one's first weights
+// to L2 meanwhile gained nothing (24 MB: 25.4 -> 26.2 us, 12 MB: 25.2), nor did two CTAs an SM.
 //
 // Roles of a CTA: three TMA warps (ring of stages), an MMA warp (one elected lane issues), eight
 // epilogue warps and four warps that store the block factors to TMEM, as in gemm_fp8_tc.cu.  Waits are
@@ -584,11 +586,12 @@ cudaError_t launch_kind(const GemmArgs& g, const Ws& ws, const int32_t* seg_coun
   // rows of a CTA in a cluster of s, and the shared memory for the others' sums of them
   auto part = [&](int s) { return (f.tok / 8 + s - 1) / s * 8; };
   auto recv = [&](int s) { return s == 1 ? 0 : kMats * part(s) * kWRows * 4; };
-  // Units, when the rows are spread as thin as they can be; clusters that run all of them at once.  K is
-  // split in whole groups of four blocks (of the splits with the same longest part the smallest), and
-  // the others' sums need shared memory.
+  // Units, when the segments differ by no more than a quarter; clusters that run all of them at once (a second
+  // unit of a cluster waits for the first one's epilogue).  K is split in whole groups of four blocks (of
+  // the splits with the same longest part the smallest), and the others' sums need shared memory.
   const int64_t nblk = (g.n + kWRows - 1) / kWRows, owners = g.rows < n_seg ? g.rows : n_seg;
-  const int64_t units = owners * nblk * (owners == 1 ? (g.rows + f.tok - 1) / f.tok : 1);
+  const int64_t top_rows = owners == 1 ? g.rows : (5 * g.rows + 4 * owners - 1) / (4 * owners);
+  const int64_t units = owners * nblk * ((top_rows + f.tok - 1) / f.tok);
   const int sck = (int)(scale_cols(g.K) / 4), fixed = 1024 + (int)sizeof(Ctl);
   f.split = 1;
   for (int s = 2; s <= kMaxSplit && s <= sck && s * units <= num_sms; ++s) {

@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
+  __syncthreads();  // no warp of this CTA issues a copy any more
   if (*abort_flag && threadIdx.x == 0) {
     // copies already in flight land within microseconds; give them 200 us before the
     // shared memory they target goes away

@@ -1,8 +1,9 @@
 """Build libmoe.so (the CUDA library behind include/moe.h) in-tree, for sm_103a only.
 
 Each .cu in csrc/ is compiled to an object in parallel, then linked with the CUDA runtime
-into ``top_routing_grouped_gb300/libmoe.so``.  The result is git-ignored; it is rebuilt
-wherever it is used (the GPU host is a different architecture from the build host).
+into ``top_routing_grouped_gb300/libmoe.so``; csrc/binding.cpp becomes the Python module
+``_fp8`` beside it.  The results are git-ignored; they are rebuilt wherever they are used (the GPU
+host is a different architecture from the build host).
 """
 import concurrent.futures as cf
 import glob
@@ -10,10 +11,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libmoe.so")
+BINDING = os.path.join(HERE, "_fp8.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 GENCODE = "arch=compute_103a,code=sm_103a"
 
@@ -36,18 +39,49 @@ def sources():
 
 def headers():
     return sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  [os.path.join(os.path.dirname(HERE), "include", "moe.h")])
+                  [os.path.join(os.path.dirname(HERE), "include", h) for h in ("moe.h", "moe_fp8.h")])
+
+
+def binding_source():
+    return os.path.join(CSRC, "binding.cpp")
 
 
 def up_to_date(out=OUT):
-    if not os.path.exists(out):
+    outs = [out, BINDING] if out == OUT else [out]
+    if not all(os.path.exists(o) for o in outs):
         return False
-    t = os.path.getmtime(out)
-    return all(os.path.getmtime(f) <= t for f in sources() + headers())
+    t = min(os.path.getmtime(o) for o in outs)
+    return all(os.path.getmtime(f) <= t for f in sources() + headers() + [binding_source()])
+
+
+def run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def compile_binding(obj):
+    """csrc/binding.cpp against the torch that imports it; links in link_binding."""
+    import torch
+    t = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+         *(f"-I{d}" for d in (t, os.path.join(t, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda)),
+         "-c", binding_source(), "-o", obj], "g++ on binding.cpp")
+    return obj
+
+
+def link_binding(obj):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    run(["g++", "-shared", obj, "-o", BINDING + ".tmp", f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+         "-lc10_cuda", f"-L{HERE}", "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"], "linking binding.cpp")
+    os.replace(BINDING + ".tmp", BINDING)
 
 
 def build(out=OUT, verbose=False, extra=(), jobs=None):
-    """Compile every csrc/*.cu and link ``out``.  Returns the library path."""
+    """Compile every csrc/*.cu and link ``out``, and for the package's own library the binding of the
+    8-bit operators.  Returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
     flags = common_flags(extra)
@@ -65,14 +99,15 @@ def build(out=OUT, verbose=False, extra=(), jobs=None):
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding, os.path.join(BUILD_DIR, "binding.o")) if out == OUT else None
         objs = list(ex.map(compile_one, srcs))
     tmp = out + ".tmp"
     cmd = [cc, "-gencode", GENCODE, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp, "-lcudart"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    run(cmd, "link")
     os.replace(tmp, out)
+    if binding:
+        link_binding(binding.result())
     return out
 
 

@@ -449,6 +449,24 @@ def test_experts(fp8, path, seg, E, d, F):
     close(np64(y)[:m], want, tol, "y")
 
 
+@pytest.mark.parametrize("path, seg", [("simt", [40]), ("auto", [40]), ("auto", [300])])
+def test_experts_at_the_ends_of_silu(fp8, path, seg):
+    """Pre-activations from -300 to 300: SiLU is a itself, or so small that it leaves fp32's normal range."""
+    d, F, n = 128, 2048, sum(seg)
+    (qx, sx) = make_rows(n, d, 61, std=64.0)
+    (q1, s1), (q3, s3), (q2, s2) = make_weights(1, F, d, 62), make_weights(1, F, d, 63), make_weights(1, d, F, 64)
+    gates = torch.rand(n, generator=gen(65))
+    a = ref.matmul(ref.dequantize(qx, sx), ref.dequantize_w(q1, s1), np.zeros(n, int))[0]
+    assert a.min() < -200 and a.max() > 200
+    plan = fp8.Fp8ExpertPlan(n, d, 1, 1, F, path=path)
+    ws, y = plan.new_workspace(), torch.empty(n, d, dtype=BF, device="cuda")
+    t = [x.cuda() for p in ((q1, s1), (q3, s3), (q2, s2)) for x in ref.to_torch(*p)]
+    plan.forward(None, *(x.cuda() for x in ref.to_torch(qx, sx)), gates.cuda(), *t, y, ws)
+    assert plan.device_status(ws) == 0
+    want, tol = expert_rows(ref.dequantize(qx, sx), (q1, s1), (q3, s3), (q2, s2), np64(gates), np.zeros(n, int))
+    close(np64(y), want, tol, "y")
+
+
 def test_experts_clusters_take_several_units(fp8):
     test_experts(fp8, "auto", [97] * 27 + [2] * 11, 38, 1024, 256)
 

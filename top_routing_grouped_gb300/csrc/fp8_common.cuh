@@ -65,12 +65,24 @@ __device__ __forceinline__ void sigmoid_pair(float a, float& s, float& one_minus
   one_minus_s = a >= 0.f ? zr : r;
 }
 
-// SiLU(a) = a sigma(a).  The hidden rows are rounded to e4m3 right after this, where an error of the
-// hardware tanh (2^-11) would move about one value in 128 to its neighbour.
+// SiLU(a) = a sigma(a), good to a few fp32 steps for every a.
 __device__ __forceinline__ float silu_exact(float a) {
   float s, c;
   sigmoid_pair(a, s, c);
   return a * s;
+}
+
+// The same for the hidden rows, in five instructions: a / (1 + 2^(-a log2 e)), but that it is 0 below
+// a = -87, where e^a leaves fp32's normal range (SiLU is at most 1e-36 there, far below what a's own
+// rounding moves it by).  With K of one or two blocks the epilogue is what bounds the product, and
+// with silu_exact, twice as many instructions, the experts of 128 x 3024 took 235 us, not 166.  The rows are
+// rounded to e4m3 right after this: an error of the hardware tanh (2^-11) would move about one value in
+// 128 to its neighbour.
+__device__ __forceinline__ float silu_hidden(float a) {
+  float z, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(a * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + z));
+  return a * r;
 }
 
 }  // namespace fp8

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             load(1, c, b);
             uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = silu_exact(a[i]) * b[i];
+            for (int i = 0; i < 8; ++i) a[i] = silu_hidden(a[i]) * b[i];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               // the row's largest value over this warp's 32 columns, kept by lane i

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_simt_kernel(GemmArgs g, Ws 
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          h[j] = n0 + lane + 32 * j < g.n ? silu_exact(acc[0][i][j]) * acc[1][i][j] : 0.f;
+          h[j] = n0 + lane + 32 * j < g.n ? silu_hidden(acc[0][i][j]) * acc[1][i][j] : 0.f;
           top = max(top, abs_bits(h[j]));
         }
         const uint32_t sb = scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));

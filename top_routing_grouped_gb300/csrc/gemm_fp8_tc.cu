@@ -32,9 +32,10 @@
 // 1000 clocks a tile).  Counted in clocks, the MMAs run 91 % of the time from a CTA's first to its last on
 // 8192 x 8192 x 2048 (64 K blocks a tile) and 80 % on 8192 x 2048 x 8192 (16 K blocks), where handing over the
 // shared columns costs about 700 of 10200 clocks a tile.  Before the first MMA go some 5000 clocks, half
-// of them until the tiles are found, half for the first loads.  Times: 86 us for 8192 x 2048 x 8192
-// (3.2 PFLOP/s), 80 us for 8192 x 4096 x 4096 (3.4), 11 us for 2048 x 2048 x 2048, 2.27 ms for 131072 rows of
-// 64 experts of 4096 x 2048 (2.9, at 1.55 GHz under the power cap).
+// of them until the tiles are found, half for the first loads.  With one to four K blocks a tile the
+// SwiGLU epilogue bounds it, some 4000 clocks a tile (51482 rows of 32 experts of 128 x 3024: 165 us).
+// Times: 85 us for 8192 x 2048 x 8192 (3.2 PFLOP/s), 80 us for 8192 x 4096 x 4096 (3.4), 11 us for 2048 x
+// 2048 x 2048, 2.24 ms for 131072 rows of 64 experts of 4096 x 2048 (2.95, at 1.55 GHz under the power cap).
 //
 // Tried and dropped: 224-wide tiles, whose accumulators share no columns (the ring's time per K block
 // does not shrink with the tile: 98 -> 106 us); the output stored from registers, 32 bytes a lane, and
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float x = __uint_as_float(u == 0 ? f0[i] : f1[i]), y = __uint_as_float(s[i]);
-            float v = silu_exact(flip ? y : x) * (flip ? x : y);
+            float v = silu_hidden(flip ? y : x) * (flip ? x : y);
             if (n0 + c0 + 32 * u + (i & ~15) >= g.n) v = 0.f;  // columns past the expert (n is a multiple of 16)
             h[32 * u + i] = v;
             top = max(top, abs_bits(v));

@@ -650,6 +650,40 @@ def test_layer_in_8_bits(fp8, T, d, E, k, F, bias, renorm):
     assert torch.equal(plan.aux_loss(ws), p16.aux_loss(w16))
 
 
+@pytest.mark.parametrize("T, d, E, k, F", [(1, 1024, 16, 4, 256), (1, 256, 8, 2, 128), (300, 256, 16, 2, 128), (1100, 256, 4, 2, 1152)])
+def test_layer_takes_the_gates_of_its_own_call(fp8, T, d, E, k, F):
+    """Calls one after another in one workspace, each with a router of its own (other experts, other gates) and
+    with NaN where the gates of the call before were: every call's expert rows are those of its own routing, and
+    the same call gives the same bits whatever ran before it."""
+    g = gen(71)
+    x = torch.randn(T, d, generator=g).to(BF).cuda()
+    xq, xs = f8(T, d), u8(T, fp8.scale_cols(d))
+    fp8.quantize(x, xq, xs)
+    w = [make_weights(E, r, c, 72 + i) for i, (r, c) in enumerate(((F, d), (F, d), (d, F)))]
+    tw = [v.cuda() for p in w for v in ref.to_torch(*p)]
+    routers = [(torch.randn(E, d, generator=g) * d ** -0.5 * s).to(BF).cuda() for s in (1.0, 4.0, 0.25)]
+    plan = fp8.Fp8MoEPlan(T, d, E, k, F, tau=0.7)
+    ws, y = plan.new_workspace(), torch.empty(T, d, dtype=BF, device="cuda")
+    first = []
+    for wr in routers:
+        plan.views(ws)["gate_perm"].fill_(float("nan"))
+        plan.forward(x, xq, xs, wr, None, *tw, y, ws)
+        assert plan.device_status(ws) == 0
+        v = plan.views(ws)
+        src, gate = v["perm_src"].cpu().numpy(), np64(v["gate_perm"])
+        np.testing.assert_array_equal(gate, np64(v["topk_gate"]).reshape(-1)[v["perm_slot"].cpu().numpy()])
+        ex = np.repeat(np.arange(E), v["expert_counts"].cpu().numpy())
+        want, tol = expert_rows(ref.dequantize(np64(xq), np64(xs))[src], *w, gate, ex)
+        close(np64(v["yp"]), want, tol, "expert rows")
+        first.append((y.clone(), v["yp"].clone()))
+    for i in 20 * [0, 1, 2, 1]:
+        plan.views(ws)["gate_perm"].fill_(float("nan"))
+        plan.forward(x, xq, xs, routers[i], None, *tw, y, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y, first[i][0]) and torch.equal(plan.views(ws)["yp"], first[i][1])
+    assert plan.device_status(ws) == 0
+
+
 def training_layer(moe, T, d, E, k, F, x, w, wr):
     plan = moe.MoEPlan(T, d, E, k, F, training=True)
     ws, y = plan.new_workspace(), torch.empty(T, d, dtype=BF, device="cuda")

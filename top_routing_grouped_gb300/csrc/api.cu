@@ -459,7 +459,8 @@ moe_status moe_fp8_forward(moe_plan_t plan, const void* x, const void* x_q, cons
   g.K = s.d;
   g.E = s.E;
   const bool few = moe::fp8::use_few(s.N, s.E, s.d > s.F ? s.d : s.F);
-  // not the call's first launches: the router has cleared the status word and counted the rows
+  // not the call's first launches: the router has cleared the status word and counted the rows.  The
+  // dispatch writes the rows, their factors and the gates, and may still run when either product starts.
   auto product = [&](int kind) {
     return (few ? moe::fp8::launch_gemm_few : moe::fp8::launch_gemm_tc)(kind, g, ws, ws.counts, s.E, false, plan->device,
                                                                         plan->num_sms, plan->timeout_ns, cs);

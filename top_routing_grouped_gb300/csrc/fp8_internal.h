@@ -57,8 +57,9 @@ cudaError_t launch_permute(const Shape& s, const Ws& ws, const void* x, const ui
                            bool pdl, cudaStream_t st);
 cudaError_t launch_gemm_simt(int kind, const GemmArgs& g, const Ws& ws, int num_sms, cudaStream_t st);
 // The tensor-core products find their tiles from the segment counts themselves (null: one segment);
-// `first`: the call's first launch, which sets the status word and waits for all earlier kernels (the
-// second waits for the first's results alone).
+// `first`: the call's first launch, which sets the status word and waits for all earlier kernels before it
+// reads anything.  The others read the counts before they wait, and the weights; a's rows and factors
+// and the gates after it, whichever earlier kernel of the call writes them.
 cudaError_t launch_gemm_tc(int kind, const GemmArgs& g, const Ws& ws, const int32_t* seg_counts, int n_seg, bool first,
                            int device, int num_sms, int64_t timeout_ns, cudaStream_t st);
 // Which of the two sets of tensor-core kernels: see api_fp8.cu.

@@ -199,9 +199,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
-  // The call's first launch waits here for the counts and the activations.  Its second one starts
-  // when the first does (as far as SMs are free): the counts are there then, and only what the first
-  // launch computes, the hidden rows and their factors, is waited for where it is read.
+  // The call's first launch waits here for the counts and the activations.  Another one starts as soon as
+  // the launch before it has (as far as SMs are free), and that may be one which has waited for nothing
+  // itself: in the layer the dispatch may still run then.  So only what the caller gives (weights and
+  // their factors) and what was there before the dispatch started (the counts) is read before a wait;
+  // rows, their factors and gates are read after one.
   if (f.first) pdl_wait();
   pdl_launch_dependents();
 
@@ -375,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     // A warp here runs alone on its scheduler for the most part, so what counts is the length of its
     // instruction chain: rows eight at a time (short code, fetched once), two sets of warps.
+    if (!f.first) pdl_wait();  // the dispatch writes the layer's gates
     const int q = warp & 3, set = (warp - kEpiWarp0) >> 2, m = q * 32 + lane;  // m: weight row of the block
     // Rows 8 gi .. 8 gi + 7 fall to CTA gi % split, which counts them its group gi / split; a set takes
     // every other one of these counts.  Where the others' sums land: [other CTA, this one left out].

@@ -124,7 +124,8 @@ moe_status moe_fp8_expert_forward(moe_fp8_plan_t plan, const int32_t* seg_counts
  * MOE_FLAG_FP8_EXPERTS: the router on x (bf16 [T, d]), the dispatch of the 8-bit rows x_q [T, d]
  * with factors x_scales [T, moe_fp8_scale_cols(d)] (moe_rmsnorm writes both out of one read),
  * the experts as in moe_fp8_expert_forward, and the combine into y [T, d] in the plan's
- * out_dtype.  The workspace's views are those of moe_forward, but that xp and h hold e4m3. */
+ * out_dtype.  The workspace's views are those of moe_forward, but that xp and h hold e4m3.  The
+ * plan's wait_timeout_ns is 1 ms at least, as in moe_fp8_matmul_config. */
 moe_status moe_fp8_forward(moe_plan_t plan, const void* x, const void* x_q, const uint8_t* x_scales, const void* w_router,
                            const float* router_bias, const void* w1, const uint8_t* w1_scales, const void* w3,
                            const uint8_t* w3_scales, const void* w2, const uint8_t* w2_scales, void* y, void* workspace,

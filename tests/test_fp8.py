@@ -684,6 +684,30 @@ def test_layer_takes_the_gates_of_its_own_call(fp8, T, d, E, k, F):
     assert plan.device_status(ws) == 0
 
 
+@pytest.mark.parametrize("T, d, E, k, F", [(1, 4096, 16, 4, 2048), (300, 1024, 16, 2, 512), (3000, 512, 4, 2, 1152)])
+def test_layer_with_the_shortest_limit(fp8, T, d, E, k, F):
+    """A limit below the shortest one, 1 ms, is that one, and it runs only while a wait can end: the second
+    product, which starts as early as the first, does not report the time until the first has ended."""
+    g = torch.Generator("cuda").manual_seed(81)
+    x = torch.randn(T, d, generator=g, device="cuda").to(BF)
+    xq, xs = f8(T, d), u8(T, fp8.scale_cols(d))
+    fp8.quantize(x, xq, xs)
+    tw = []
+    for r, c in ((F, d), (F, d), (d, F)):
+        q, s = f8(E, r, c), u8(E, -(-r // 128), fp8.scale_cols(c))
+        fp8.quantize_weights(torch.randn(E, r, c, generator=g, device="cuda") * c ** -0.5, q, s)
+        tw += [q, s]
+    wr = (torch.randn(E, d, generator=g, device="cuda") * d ** -0.5).to(BF)
+    ys = []
+    for limit in (1, 0):
+        plan = fp8.Fp8MoEPlan(T, d, E, k, F, wait_timeout_ns=limit)
+        ws, y = plan.new_workspace(), torch.empty(T, d, dtype=BF, device="cuda")
+        plan.forward(x, xq, xs, wr, None, *tw, y, ws)
+        assert plan.device_status(ws) == 0
+        ys.append(y)
+    assert torch.equal(*ys)
+
+
 def training_layer(moe, T, d, E, k, F, x, w, wr):
     plan = moe.MoEPlan(T, d, E, k, F, training=True)
     ws, y = plan.new_workspace(), torch.empty(T, d, dtype=BF, device="cuda")

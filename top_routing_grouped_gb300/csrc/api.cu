@@ -299,6 +299,7 @@ moe_status moe_plan(const moe_config* cfg, moe_plan_t* plan, size_t* workspace_b
   p->tc = tc;
   p->pair = tc && c.path == MOE_PATH_AUTO;
   p->timeout_ns = c.wait_timeout_ns > 0 ? c.wait_timeout_ns : 2000000000LL;
+  if (p->fp8 && p->timeout_ns < (int64_t)moe::fp8::kMinTimeoutNs) p->timeout_ns = (int64_t)moe::fp8::kMinTimeoutNs;
   *plan = p;
   *workspace_bytes = p->layout.total;
   g_last_error.clear();

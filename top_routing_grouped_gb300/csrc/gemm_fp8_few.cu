@@ -219,8 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ TMA producers
     // Warp 0 loads W (W1), warp 2 W3, warp 3 the activations, each converged with one elected lane
     // issuing: a load costs its warp about 200 clocks, and one lane that issued all of a stage's took
-    // as long to fill the ring for the first time as HBM.  In a call's second launch the weights are
-    // requested before the first launch has ended.
+    // as long to fill the ring for the first time as HBM.  In a call's second launch the weights that fill the
+    // ring once are requested before the first launch has ended; the wait for it comes before the first
+    // wait for an MMA, whose limit would else run while nothing can have happened yet.
     if (!f.first && warp == 3) pdl_wait();
     const CUtensorMap* map = warp == 0 ? &tmW : warp == 2 ? &tmW3 : &tmX;
     const uint32_t ctl0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ctl), 0);
@@ -247,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == f.stages) {
           stage = 0;
           phase ^= 1u;
+          if (!f.first) pdl_wait();  // returns at once after the first time
         }
       }
     }
@@ -257,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (converged warp)
+    if (!f.first) pdl_wait();  // its limits run from here
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t desc0 = ptx::desc_kmajor_sw128(__shfl_sync(0xffffffffu, ptx::smem_u32(stages), 0));
     const uint32_t ctl0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ctl), 0);
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     // A warp here runs alone on its scheduler for the most part, so what counts is the length of its
     // instruction chain: rows eight at a time (short code, fetched once), two sets of warps.
-    if (!f.first) pdl_wait();  // the dispatch writes the layer's gates
+    if (!f.first) pdl_wait();  // the dispatch writes the layer's gates; and the limits of the waits run from here
     const int q = warp & 3, set = (warp - kEpiWarp0) >> 2, m = q * 32 + lane;  // m: weight row of the block
     // Rows 8 gi .. 8 gi + 7 fall to CTA gi % split, which counts them its group gi / split; a set takes
     // every other one of these counts.  Where the others' sums land: [other CTA, this one left out].

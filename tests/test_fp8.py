@@ -247,6 +247,51 @@ def test_rmsnorm_backward_against_differences(fp8):
         assert abs((f(X, W + step) - f(X, W - step)) / (2 * h) - float(dw[j])) < 1e-5
 
 
+def test_norms_of_several_widths_from_two_threads(fp8):
+    """Rows too long for registers, of two widths, from two threads at once: every call is launched, with the bits
+    of a call alone.  Each thread has its own stream and tensors."""
+    import threading
+
+    def work(d, n=3):
+        g = torch.Generator("cuda").manual_seed(d)
+        x, do = (torch.randn(n, d, generator=g, device="cuda") for _ in range(2))
+        e = lambda: torch.empty(n, d, device="cuda")
+        out, dx, rstd, dw = e(), e(), torch.empty(n, device="cuda"), torch.empty(d, device="cuda")
+        ws = fp8.rmsnorm_backward_workspace(n, d)
+        def once(stream):
+            fp8.rmsnorm(x, None, out=out, rstd=rstd, stream=stream)
+            fp8.rmsnorm_backward(do, x, None, rstd, dx, dw, ws, stream=stream)
+        return once, (out, dx, rstd, dw)
+
+    jobs = {d: work(d) for d in (20000, 49152)}
+    torch.cuda.synchronize()
+    alone, errors = {}, []
+    for d, (once, outs) in jobs.items():
+        once(None)
+        torch.cuda.synchronize()
+        alone[d] = [t.clone() for t in outs]
+        for t in outs:
+            t.zero_()
+    torch.cuda.synchronize()
+
+    def loop(once):
+        stream = torch.cuda.Stream()
+        try:
+            for _ in range(2000):
+                once(stream)
+            stream.synchronize()
+        except Exception as e:  # shown by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=loop, args=(once,)) for once, _ in jobs.values()]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors, errors
+    for d, (_, outs) in jobs.items():
+        for a, b in zip(alone[d], outs):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ products
 
 def make_rows(n, c, seed, std=1.0):

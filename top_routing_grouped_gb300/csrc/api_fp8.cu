@@ -83,9 +83,6 @@ moe_status check(const Ptr (&ptrs)[N]) {
 bool is_dtype(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
 size_t esize(int32_t t) { return t == MOE_BF16 ? 2 : 4; }
 
-// The largest width whose rows the norms hold in shared memory.
-constexpr int32_t kMaxNormCols = 49152;
-
 moe_status check_sizes(int64_t rows, int64_t cols, int64_t ld) {
   if (rows < 0 || cols < 1) return fail(MOE_ERR_INVALID_ARG, "rows must be >= 0 and columns >= 1");
   if (ld < cols) return fail(MOE_ERR_INVALID_ARG, "a row pitch is below the row's length");
@@ -227,7 +224,7 @@ moe_status moe_rmsnorm(const void* x, const void* residual, const float* weight,
   moe_status s = check_sizes(rows, d, ldx);
   if (s != MOE_OK) return s;
   if (residual && ldr < d) return fail(MOE_ERR_INVALID_ARG, "a row pitch is below the row's length");
-  if (d > kMaxNormCols) return fail(MOE_ERR_UNSUPPORTED, "d must be <= %d", kMaxNormCols);
+  if (d > fp8::kMaxNormCols) return fail(MOE_ERR_UNSUPPORTED, "d must be <= %d", fp8::kMaxNormCols);
   if (rows == 0) return set_last_error(MOE_OK, "");
   if (!q != !scales) return fail(MOE_ERR_INVALID_ARG, "q and scales go together");
   if (!residual_out && !out && !q && !rstd) return fail(MOE_ERR_INVALID_ARG, "no output is wanted");
@@ -255,7 +252,7 @@ moe_status moe_rmsnorm_backward(const void* dout, int32_t dout_dtype, const void
   if (!is_dtype(dtype) || !is_dtype(dout_dtype)) return fail(MOE_ERR_INVALID_ARG, "bad dtype");
   moe_status s = check_sizes(rows, d, ldr);
   if (s != MOE_OK) return s;
-  if (d > kMaxNormCols) return fail(MOE_ERR_UNSUPPORTED, "d must be <= %d", kMaxNormCols);
+  if (d > fp8::kMaxNormCols) return fail(MOE_ERR_UNSUPPORTED, "d must be <= %d", fp8::kMaxNormCols);
   const size_t a = esize(dtype);
   const bool any = rows > 0;
   const Ptr ptrs[] = {{dout, "dout", esize(dout_dtype), !any}, {r, "r", a, !any},          {weight, "weight", 16, true},

@@ -9,6 +9,7 @@ namespace fp8 {
 
 constexpr int kBlock = 128;  // values per scale
 constexpr uint64_t kMinTimeoutNs = 1000000;  // the shortest limit of a device-side wait
+constexpr int kMaxNormCols = 49152;  // the widest row that the norms hold in shared memory
 __host__ __device__ inline int64_t scale_cols(int64_t cols) { return (cols + 511) / 512 * 4; }
 
 // One grouped product as its kernels see it.

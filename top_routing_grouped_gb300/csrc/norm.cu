@@ -22,6 +22,8 @@
 
 #include <string.h>
 
+#include <atomic>
+
 namespace moe {
 namespace fp8 {
 namespace {
@@ -564,6 +566,21 @@ static bool on(int n, const void* p, bool bf16, int64_t ld) {
   return !p || (reinterpret_cast<uintptr_t>(p) % (per * (bf16 ? 2 : 4)) == 0 && ld % per == 0);
 }
 
+// Lets a kernel that keeps a row in shared memory have as much of it as the widest row takes.  Set to that
+// once per kernel and device and never lowered: the attribute belongs to the process, and another thread may
+// stand between a call that has set its own row's size and its launch.
+template <typename Kern>
+static cudaError_t allow_widest_row(Kern kern, std::atomic<uint64_t>& asked) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+  if (bit && (asked.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxNormCols * (int)sizeof(float));
+  if (e == cudaSuccess) asked.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* weight, bool bf16, int64_t rows, int d,
                            int64_t ldx, int64_t ldr, float eps, void* residual_out, void* out, void* q, uint8_t* scales,
                            float* rstd, cudaStream_t st) {
@@ -578,10 +595,9 @@ cudaError_t launch_rmsnorm(const void* x, const void* residual, const float* wei
   }
   const size_t smem = (size_t)d * sizeof(float);
   auto kern = bf16 ? rmsnorm_kernel<true> : rmsnorm_kernel<false>;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024 &&  // what a launch may have without asking
-      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-    return e;
+  static std::atomic<uint64_t> asked[2];
+  const cudaError_t e = allow_widest_row(kern, asked[bf16]);
+  if (e != cudaSuccess) return e;
   const int64_t grid = rows < (1 << 20) ? rows : 1 << 20;
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), smem, st, false, 1, x, residual, weight, rows, d, ldx,
                        ldr, eps, residual_out, out, (uint8_t*)q, scales, rstd);
@@ -654,9 +670,8 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
     const size_t smem = (size_t)d * sizeof(float);
     auto kern = bf16 ? (dout_bf16 ? rmsnorm_backward_kernel<true, true> : rmsnorm_backward_kernel<true, false>)
                      : (dout_bf16 ? rmsnorm_backward_kernel<false, true> : rmsnorm_backward_kernel<false, false>);
-    if (smem > 48 * 1024 &&  // what a launch may have without asking
-        (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
-      return e;
+    static std::atomic<uint64_t> asked[2][2];
+    if ((e = allow_widest_row(kern, asked[bf16][dout_bf16])) != cudaSuccess) return e;
     e = launch_kernel(kern, dim3((unsigned)n), dim3(kThreads), smem, st, false, 1, dout, r, weight, rstd, dresidual, rows, d,
                       ldr, dx, dweight ? parts : nullptr);
   }

@@ -68,7 +68,8 @@ moe_status moe_rmsnorm(const void* x, const void* residual, const float* weight,
  *   g = dout * weight,  xhat = r * rstd
  *   dx[t]   = rstd (g - xhat * mean_j(g xhat)) + dresidual        [rows, d] in `dtype`
  *   dweight = sum_t dout[t] * xhat[t]                             [d] fp32, may be NULL
- * dx is the gradient of x and of the residual alike, and may be dresidual itself.  The sum
+ * dx is the gradient of x and of the residual alike.  It may be dresidual, dout (where both have one
+ * type) or r (where ldr is d) itself; a dx that overlaps one of them otherwise is refused.  The sum
  * over rows is taken in a fixed order (results do not depend on timing).  workspace: device,
  * 256-byte aligned, moe_rmsnorm_backward_workspace(rows, d) bytes (when dweight is wanted; may
  * be NULL where that is 0, as with few rows). */

@@ -223,6 +223,33 @@ def test_rmsnorm_backward_against_the_formula(fp8, dtype, dout, n, d, pad, dres,
         assert torch.equal(dr, dx)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("n, d", [(1, 4096), (300, 1000), (512, 264), (512, 97), (513, 264), (2000, 136), (300, 5000), (3, 12345)])
+def test_rmsnorm_backward_in_place(fp8, dtype, n, d):
+    """dx over dout, over r or over all three: the bits of the call with a tensor of its own, dweight among them."""
+    g = gen(16)
+    r, dn, dr = ((torch.randn(n, d, generator=g) * 2).to(dtype).cuda() for _ in range(3))
+    w = (1 + 0.2 * torch.randn(d, generator=g)).cuda()
+    rstd = (r.double().square().mean(1) + 1e-5).rsqrt().float()
+    ws = fp8.rmsnorm_backward_workspace(n, d)
+
+    def call(dn, r, dx, dr):
+        dw = torch.full((d,), 77.0, device="cuda")
+        fp8.rmsnorm_backward(dn, r, w, rstd, dx, dw, ws, dresidual=dr)
+        return dx, dw
+
+    want = call(dn, r, torch.empty_like(r), dr)
+    for over in ("dn", "r"):
+        for _ in range(10):
+            t = dict(dn=dn.clone(), r=r.clone())
+            got = call(t["dn"], t["r"], t[over], dr)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), over
+    both = r.clone()  # one tensor for everything
+    want = call(r, r, torch.empty_like(r), r)
+    got = call(both, both, both, both)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_rmsnorm_backward_against_differences(fp8):
     """Central differences of the 64-bit forward, through the kernel's gradients of fp32 inputs.
     With steps of 1e-4 the differences' own error is about 1e-8 of third derivatives of order one;

@@ -91,6 +91,36 @@ def test_rmsnorm_backward_refusals(fp8):
     assert call(d=60000, ld=60000) == UNSUPPORTED
 
 
+def test_rmsnorm_backward_refuses_overlaps(fp8):
+    """dx may be dresidual, dout or r itself (seen where the call stops at a workspace that is too small, its last
+    check); anything else that shares a byte with one of them is turned down by name."""
+    L = fp8._lib
+    rows, d, at = 1000, 64, 1 << 24
+    size = {0: 4, 1: 2}
+
+    def call(t=1, dt=1, ld=d, **kw):
+        p = dict(do=1 << 28, r=2 << 28, dr=3 << 28, dx=at)
+        p.update(kw)
+        st = L.moe_rmsnorm_backward(P(p["do"]), dt, P(p["r"]), None, A[3], P(p["dr"]), t, rows, d, ld, P(p["dx"]), A[6], A[7], 0, None)
+        return st, L.moe_last_error().decode()
+
+    fine = (INVALID, "workspace too small")
+    for kw in (dict(), dict(do=at), dict(r=at), dict(dr=at), dict(do=at, r=at, dr=at), dict(do=at, dt=0, t=0)):
+        st, why = call(**kw)
+        assert (st, why[:19]) == fine, (kw, why)
+    for t in (0, 1):
+        bytes_ = rows * d * size[t]
+        for name, word in (("do", "dout"), ("r", "r"), ("dr", "dresidual")):
+            for off in (16, d * size[t], bytes_ - 16, -16, 16 - bytes_):
+                st, why = call(t=t, dt=t, **{name: at + off})
+                assert st == INVALID and why.startswith(f"dx overlaps {word}:"), (t, name, off, why)
+            for off in (bytes_, -bytes_):
+                st, why = call(t=t, dt=t, **{name: at + off})
+                assert (st, why[:19]) == fine, (t, name, off, why)
+    assert call(do=at, dt=0)[1].startswith("dx overlaps dout")   # another type
+    assert call(r=at, ld=80)[1].startswith("dx overlaps r:")     # another pitch
+
+
 @pytest.mark.parametrize("kw, status", [
     (dict(max_rows=0), "MOE_ERR_INVALID_ARG"), (dict(K=0), "MOE_ERR_INVALID_ARG"), (dict(n=0), "MOE_ERR_INVALID_ARG"),
     (dict(n_experts=0), "MOE_ERR_INVALID_ARG"), (dict(n_experts=129, n_sources=2), "MOE_ERR_INVALID_ARG"),

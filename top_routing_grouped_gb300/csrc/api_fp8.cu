@@ -80,6 +80,12 @@ moe_status check(const Ptr (&ptrs)[N]) {
   return MOE_OK;
 }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+
 bool is_dtype(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
 size_t esize(int32_t t) { return t == MOE_BF16 ? 2 : 4; }
 
@@ -259,6 +265,16 @@ moe_status moe_rmsnorm_backward(const void* dout, int32_t dout_dtype, const void
                       {rstd, "rstd", 16, !any},                {dresidual, "dresidual", a, true}, {dx, "dx", a, !any},
                       {dweight, "dweight", 16, true}};
   if ((s = check(ptrs)) != MOE_OK) return s;
+  if (any) {  // in place only where every row of dx lies on its own row of the input
+    const size_t row = (size_t)d * a, bytes = (size_t)rows * row;
+    const size_t dout_bytes = (size_t)rows * (size_t)d * esize(dout_dtype), r_bytes = (size_t)(rows - 1) * (size_t)ldr * a + row;
+    if (overlap(dx, bytes, dout, dout_bytes) && !(dx == dout && dtype == dout_dtype))
+      return fail(MOE_ERR_INVALID_ARG, "dx overlaps dout: it may only be dout itself, of its type");
+    if (overlap(dx, bytes, r, r_bytes) && !(dx == r && ldr == d))
+      return fail(MOE_ERR_INVALID_ARG, "dx overlaps r: it may only be r itself, with a pitch of d");
+    if (dresidual && overlap(dx, bytes, dresidual, bytes) && dx != dresidual)
+      return fail(MOE_ERR_INVALID_ARG, "dx overlaps dresidual: it may only be dresidual itself");
+  }
   const size_t need = moe_rmsnorm_backward_workspace(rows, d);
   if (dweight && need > 0) {
     if (!workspace || !aligned(workspace, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");

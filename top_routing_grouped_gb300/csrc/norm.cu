@@ -627,16 +627,17 @@ struct NormBwdArgs {
   int d;
   int64_t ldr;
   void* dx;
+  int ctas;        // those that take rows
   float* parts;    // more rows: partial sums
   float* dweight;  // few rows: the sums
 };
 
 template <bool kBf16, bool kDoutBf16, bool kVec, int V, int R>
 static cudaError_t norm_bwd_reg(const NormBwdArgs& a, bool even, cudaStream_t st) {
-  const int n = row_ctas(a.rows, a.d), cols = a.dweight ? (a.d + 31) / 32 : 0;
-  return launch_kernel(rmsnorm_backward_reg_kernel<kBf16, kDoutBf16, kVec, V, R>, dim3((unsigned)(n + cols)),
+  const int cols = a.dweight ? (a.d + 31) / 32 : 0;
+  return launch_kernel(rmsnorm_backward_reg_kernel<kBf16, kDoutBf16, kVec, V, R>, dim3((unsigned)(a.ctas + cols)),
                        dim3(row_threads(a.d)), 0, st, true, 1, a.dout, a.r, a.weight, a.rstd, a.dresidual, a.rows, a.d, a.ldr,
-                       a.dx, a.parts, even ? 1 : 0, n, a.dweight);
+                       a.dx, a.parts, even ? 1 : 0, a.ctas, a.dweight);
 }
 
 template <bool kBf16, bool kDoutBf16, bool kVec>
@@ -659,13 +660,23 @@ cudaError_t launch_rmsnorm_backward(const void* dout, bool dout_bf16, const void
   const bool one = one_kernel(rows, d);
   cudaError_t e = cudaSuccess;
   if (n > 0 && d <= kMaxRegCols) {
-    const NormBwdArgs a{dout, r, weight, rstd, dresidual, rows, d, ldr, dx, dweight && !one ? parts : nullptr,
-                        one ? dweight : nullptr};
+    NormBwdArgs a{dout, r, weight, rstd, dresidual, rows, d, ldr, dx, n, dweight && !one ? parts : nullptr,
+                  one ? dweight : nullptr};
     auto all = [&](int k) {
       return d % k == 0 && on(k, dout, dout_bf16, d) && on(k, r, bf16, ldr) && on(k, dresidual, bf16, d) && on(k, dx, bf16, d);
     };
     const bool vec = all(8), even = all(2);
-    e = vec ? norm_bwd_types<true>(a, bf16, dout_bf16, even, st) : norm_bwd_types<false>(a, bf16, dout_bf16, even, st);
+    auto launch = [&]() {
+      return vec ? norm_bwd_types<true>(a, bf16, dout_bf16, even, st) : norm_bwd_types<false>(a, bf16, dout_bf16, even, st);
+    };
+    if (a.dweight && (dx == dout || dx == r)) {
+      // in place: the columns' sums read what the rows' CTAs overwrite, so they go first, by themselves
+      a.ctas = 0;
+      if ((e = launch()) != cudaSuccess) return e;
+      a.ctas = n;
+      a.dweight = nullptr;
+    }
+    e = launch();
   } else if (n > 0) {
     const size_t smem = (size_t)d * sizeof(float);
     auto kern = bf16 ? (dout_bf16 ? rmsnorm_backward_kernel<true, true> : rmsnorm_backward_kernel<true, false>)

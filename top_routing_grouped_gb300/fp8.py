@@ -107,7 +107,7 @@ def rmsnorm_backward_workspace(T, d, device="cuda"):
 def rmsnorm_backward(dout, r, weight, rstd, dx, dweight=None, workspace=None, dresidual=None, stream=None):
     """dx and dweight from dout = dL/dn (fp32 or bf16) and what the forward kept: r (its
     residual_out, or x without a residual; any row pitch) and rstd; dresidual is the gradient that
-    reaches r on its other way."""
+    reaches r on its other way.  dx may be dresidual, dout or r itself."""
     _check(_fp8.rmsnorm_backward(dout, r, weight, rstd, dx, dweight, workspace, dresidual, stream), "moe_rmsnorm_backward")
 
 

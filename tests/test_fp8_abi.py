@@ -241,6 +241,83 @@ def test_binding_refuses_host_memory(fp8):
         fp8.rmsnorm_backward(g(x), g(x), None, g(torch.ones(4)), g(x), g(torch.ones(64)), torch.zeros(4096, dtype=torch.uint8))
 
 
+class Elsewhere(torch.Tensor):
+    """A tensor without memory that lies on the given device for the binding too."""
+    @staticmethod
+    def __new__(cls, shape, dtype, device):
+        return torch.Tensor._make_wrapper_subclass(cls, shape, dtype=dtype, device=device)
+
+    @classmethod
+    def __torch_dispatch__(cls, f, types, args=(), kwargs=None):
+        raise NotImplementedError(f)
+
+
+class FakeStream:
+    cuda_stream, device_index = 0, 1
+
+
+def binding_calls(fp8):
+    """(name, function of a list of tensors and a stream, the tensors' shapes and types) of every call of the
+    binding that takes tensors."""
+    from top_routing_grouped_gb300 import moe
+    f32, bf, f8, u8, i32 = torch.float32, torch.bfloat16, fp8.E4M3, torch.uint8, torch.int32
+    T, d, E, F = 4, 64, 2, 32
+    x, q, s = ((T, d), f32), ((T, d), f8), ((T, 4), u8)
+    b, v, w, ws = ((T, d), bf), ((d,), f32), ((E, 1, 4), u8), ((1 << 20,), u8)
+    up, down = ((E, F, d), f8), ((E, d, F), f8)
+    mm, ex = fp8.Fp8MatmulPlan(T, d, F, n_experts=E), fp8.Fp8ExpertPlan(T, d, E, 1, F)
+    layer = fp8.Fp8MoEPlan(T, 128, 8, 2, 128, has_bias=True)
+    lq, lw, lc = ((T, 128), f8), ((8, 128, 128), f8), ((8, 1, 4), u8)
+    lx = ((T, 128), bf)
+    return [
+        ("quantize", fp8.quantize, [x, q, s]),
+        ("quantize_weights", fp8.quantize_weights, [((E, F, d), f32), up, w]),
+        ("rmsnorm", lambda x, w, r, ro, o, q, s, rs, stream: fp8.rmsnorm(x, w, r, ro, o, q, s, rs, stream=stream),
+         [x, v, x, x, x, q, s, ((T,), f32)]),
+        ("rmsnorm_backward", fp8.rmsnorm_backward, [x, x, v, ((T,), f32), x, v, ws, x]),
+        ("matmul", mm.forward, [((E,), i32), q, s, up, w, ((T, F), bf), ws]),
+        ("experts", ex.forward, [((E,), i32), q, s, ((T,), f32), up, w, up, w, down, w, b, ws]),
+        ("layer", layer.forward, [lx, lq, s, ((8, 128), bf), ((8,), f32), lw, lc, lw, lc, lw, lc, lx, ws]),
+        ("checkpoint_save", fp8.checkpoint_save, [b, b, q, s, q, s]),
+        ("checkpoint_restore", fp8.checkpoint_restore, [q, s, q, s, b, b, b]),
+        ("checkpoint_backward", fp8.checkpoint_backward, [q, s, q, s, b, b, b, b]),
+    ]
+
+
+@pytest.mark.parametrize("i", range(10))
+def test_binding_refuses_each_tensor_elsewhere(fp8, i):
+    """Nothing wrong but where one tensor lies, each in turn: in host memory, or on another GPU than the rest; or
+    the stream's device."""
+    name, f, tensors = binding_calls(fp8)[i]
+    for j, (shape, dtype) in enumerate(tensors):
+        on = lambda device: [Elsewhere(*t, device if k == j else "cuda:0") for k, t in enumerate(tensors)]
+        host = on("cuda:0")
+        host[j] = torch.zeros(shape, dtype=torch.uint8 if dtype.itemsize == 1 else dtype).view(dtype)
+        with pytest.raises(ValueError, match="must be in GPU memory"):
+            f(*host, stream=None)
+        with pytest.raises(ValueError, match="must be on the device of the tensors before it"):
+            f(*on("cuda:1"), stream=None)
+    with pytest.raises(ValueError, match="stream must be on the tensors' device"):
+        f(*[Elsewhere(*t, "cuda:0") for t in tensors], stream=FakeStream())
+
+
+def test_layer_checkpoint_refuses_other_devices(fp8):
+    from top_routing_grouped_gb300 import moe
+    p = moe.MoEPlan(64, 128, 8, 2, 128, training=True)
+    c = fp8.LayerCheckpoint(p, device="cpu")
+    tensor = lambda n, device, dtype=torch.uint8: Elsewhere(n, dtype, device)
+    ws = lambda device: tensor((p.workspace_bytes,), device)
+    with pytest.raises(ValueError, match="GPU memory"):
+        c.save(ws("cuda:0"))
+    c.data = tensor((c.data.numel(),), "cuda:0")
+    x = lambda device: tensor((64, 128), device, torch.bfloat16)
+    for f in (lambda: c.save(ws("cuda:1")), lambda: c.restore(x("cuda:1"), ws("cuda:0")), lambda: c.restore(x("cuda:0"), ws("cuda:1")),
+              lambda: c.save(ws("cuda:0"), stream=FakeStream()), lambda: c.restore(x("cuda:0"), ws("cuda:0"), stream=FakeStream()),
+              lambda: fp8.Fp8MatmulPlan(4, 64, 32).device_status(ws("cuda:0"), stream=FakeStream())):
+        with pytest.raises(ValueError, match="one device"):
+            f()
+
+
 def test_layer_plan_and_forward_refusals(fp8):
     from top_routing_grouped_gb300 import moe
     L = fp8._lib

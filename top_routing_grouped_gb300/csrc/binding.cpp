@@ -9,11 +9,14 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
 #include <initializer_list>
+#include <memory>
+#include <optional>
 #include <string>
 
 #include "../../include/moe_fp8.h"
@@ -72,13 +75,45 @@ const Tensor& matrix(PyObject* o, unsigned types, const char* what) {
   return *t;
 }
 
+int64_t integer(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PyError{};
+  return v;
+}
+
+template <typename P>
+P handle(PyObject* o) {
+  void* p = PyLong_AsVoidPtr(o);
+  if (!p && PyErr_Occurred()) throw PyError{};
+  return static_cast<P>(p);
+}
+
+struct Release {
+  void operator()(PyObject* o) const { Py_DECREF(o); }
+};
+
+std::unique_ptr<PyObject, Release> attribute(PyObject* o, const char* name) {
+  PyObject* v = PyObject_GetAttrString(o, name);
+  if (!v) throw PyError{};
+  return std::unique_ptr<PyObject, Release>(v);
+}
+
 // A call's arguments.  Types, shapes and layouts are checked as the arguments are taken; where the
-// tensors lie, at the end (stream).
+// tensors lie, at the end (stream), which also makes their device the current one for the call.
 struct Args {
-  const char* on_host = nullptr;  // the first tensor outside GPU memory
+  const char* on_host = nullptr;    // the first tensor outside GPU memory
+  const char* elsewhere = nullptr;  // the first one on another GPU than those before it
+  c10::DeviceIndex device = -1;     // theirs
+  std::optional<c10::cuda::CUDAGuard> guard;
 
   void* address(const Tensor& t, const char* name) {
-    if (!t.is_cuda() && !on_host) on_host = name;
+    if (!t.is_cuda()) {
+      if (!on_host) on_host = name;
+    } else if (device < 0) {
+      device = (c10::DeviceIndex)t.get_device();
+    } else if (t.get_device() != device && !elsewhere) {
+      elsewhere = name;
+    }
     return t.data_ptr();
   }
 
@@ -121,31 +156,25 @@ struct Args {
     return o == Py_None ? nullptr : bytes(o, n);
   }
 
-  // The given torch.cuda.Stream, or (None) the current stream of the device of a tensor taken before.
-  void* stream(PyObject* o, PyObject* of) {
+  // The given torch.cuda.Stream, or (None) the current stream of the tensors' device.
+  void* stream(PyObject* o) {
     if (on_host) throw Refused{std::string(on_host) + " must be in GPU memory"};
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(THPVariable_Unpack(of).get_device()).stream();
-    PyObject* v = PyObject_GetAttrString(o, "cuda_stream");
-    if (!v) throw PyError{};
-    void* p = PyLong_AsVoidPtr(v);
-    Py_DECREF(v);
-    if (!p && PyErr_Occurred()) throw PyError{};
+    if (elsewhere) throw Refused{std::string(elsewhere) + " must be on the device of the tensors before it"};
+    if (o == Py_None) {
+      make_current();
+      return c10::cuda::getCurrentCUDAStream(device).stream();
+    }
+    void* p = handle<void*>(attribute(o, "cuda_stream").get());
+    if (PyObject_HasAttrString(o, "device_index") && integer(attribute(o, "device_index").get()) != device)
+      throw Refused{"the stream must be on the tensors' device"};
+    make_current();
     return p;
   }
+
+  void make_current() {
+    if (c10::cuda::device_count() > 1) guard.emplace(device);
+  }
 };
-
-int64_t integer(PyObject* o) {
-  const long long v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw PyError{};
-  return v;
-}
-
-template <typename P>
-P handle(PyObject* o) {
-  void* p = PyLong_AsVoidPtr(o);
-  if (!p && PyErr_Occurred()) throw PyError{};
-  return static_cast<P>(p);
-}
 
 // One Python function: kArgs arguments, body -> status.
 template <int kArgs, typename Body>
@@ -182,7 +211,7 @@ PyObject* quantize(ARGS) {  // x, q, scales, stream
     const int64_t n = x.size(0), c = x.size(1);
     int64_t ld;
     void *px = in.pitched(a[0], n, c, kFloats, "x", &ld), *q = in.rows(a[1], {n, c}, kE4m3, "q");
-    void *s = in.rows(a[2], {n, moe_fp8_scale_cols(c)}, kScales, "scales"), *st = in.stream(a[3], a[0]);
+    void *s = in.rows(a[2], {n, moe_fp8_scale_cols(c)}, kScales, "scales"), *st = in.stream(a[3]);
     const int32_t dt = moe_dtype_of(type_of(x));
     return unlocked([=] { return moe_fp8_quantize(px, dt, n, c, ld, 1, 0, q, U8(s), st); });
   });
@@ -194,7 +223,7 @@ PyObject* quantize_weights(ARGS) {  // w, q, scales, stream
     if (!w || w->dim() != 3) throw Refused{"w must be a 3-D fp32 or bf16 tensor"};
     const int64_t E = w->size(0), n = w->size(1), c = w->size(2);
     void *pw = in.rows(a[0], {E, n, c}, kFloats, "w"), *q = in.rows(a[1], {E, n, c}, kE4m3, "q");
-    void *s = in.rows(a[2], {E, (n + 127) / 128, moe_fp8_scale_cols(c)}, kScales, "scales"), *st = in.stream(a[3], a[0]);
+    void *s = in.rows(a[2], {E, (n + 127) / 128, moe_fp8_scale_cols(c)}, kScales, "scales"), *st = in.stream(a[3]);
     const int32_t dt = moe_dtype_of(type_of(*w));
     return unlocked([=] { return moe_fp8_quantize(pw, dt, E * n, c, c, 128, n, q, U8(s), st); });
   });
@@ -212,7 +241,7 @@ PyObject* rmsnorm(ARGS) {  // x, weight, residual, residual_out, out, q, scales,
     void* rs = in.maybe(a[7], {T}, kF32, "rstd");
     const double eps = PyFloat_AsDouble(a[8]);
     if (eps == -1.0 && PyErr_Occurred()) throw PyError{};
-    void* st = in.stream(a[9], a[0]);
+    void* st = in.stream(a[9]);
     if (d > INT32_MAX) throw Refused{"x has too many columns"};
     return unlocked([=] {
       return moe_rmsnorm(px, pr, FL(w), moe_dtype_of(t), T, (int32_t)d, ldx, ldr, (float)eps, ro, out, q, U8(s), FL(rs), st);
@@ -230,7 +259,7 @@ PyObject* rmsnorm_backward(ARGS) {  // dout, r, weight, rstd, dx, dweight, works
     void *w = in.maybe(a[2], {d}, kF32, "weight"), *rs = in.rows(a[3], {T}, kF32, "rstd"), *dres = in.maybe(a[7], {T, d}, t, "dresidual");
     void *dx = in.rows(a[4], {T, d}, t, "dx"), *dw = in.maybe(a[5], {d}, kF32, "dweight");
     size_t n;
-    void *ws = in.maybe_bytes(a[6], &n), *st = in.stream(a[8], a[0]);
+    void *ws = in.maybe_bytes(a[6], &n), *st = in.stream(a[8]);
     const int32_t ddt = moe_dtype_of(type_of(THPVariable_Unpack(a[0])));
     if (d > INT32_MAX) throw Refused{"r has too many columns"};
     return unlocked([=] {
@@ -249,7 +278,7 @@ PyObject* matmul(ARGS) {  // plan, (max_rows, K, n, E, segments, bf16 out), seg_
     void *sa = in.rows(a[2], {R, moe_fp8_scale_cols(K)}, kScales, "a_scales"), *w = in.rows(a[3], {E, N, K}, kE4m3, "w");
     void *sw = in.rows(a[4], {E, (N + 127) / 128, moe_fp8_scale_cols(K)}, kScales, "w_scales"), *out = in.rows(a[5], {R, N}, ot, "out");
     size_t n;
-    void *ws = in.bytes(a[6], &n), *st = in.stream(a[7], a[1]);
+    void *ws = in.bytes(a[6], &n), *st = in.stream(a[7]);
     return unlocked([=] { return moe_fp8_matmul(plan, static_cast<int32_t*>(seg), pa, U8(sa), w, U8(sw), out, ws, n, st); });
   });
 }
@@ -277,7 +306,7 @@ PyObject* experts(ARGS) {  // plan, (max_rows, d, E, segments, F), seg_counts, x
     void *sx = in.rows(a[2], {R, moe_fp8_scale_cols(d)}, kScales, "x_scales"), *g = in.rows(a[3], {R}, kF32, "gates");
     const Experts w(in, a + 4, E, d, F);
     size_t n;
-    void *y = in.rows(a[10], {R, d}, kBf16, "y_rows"), *ws = in.bytes(a[11], &n), *st = in.stream(a[12], a[1]);
+    void *y = in.rows(a[10], {R, d}, kBf16, "y_rows"), *ws = in.bytes(a[11], &n), *st = in.stream(a[12]);
     return unlocked([=] {
       return moe_fp8_expert_forward(plan, static_cast<int32_t*>(seg), x, U8(sx), FL(g), w.w1, U8(w.s1), w.w3, U8(w.s3), w.w2,
                                     U8(w.s2), y, ws, n, st);
@@ -296,7 +325,7 @@ PyObject* layer(ARGS) {  // plan, (T, d, E, F, bf16 out), x, x_q, x_scales, w_ro
     void* bias = in.maybe(a[4], {E}, kF32, "bias");
     const Experts w(in, a + 5, E, d, F);
     size_t n;
-    void *y = in.rows(a[11], {T, d}, ot, "y"), *ws = in.bytes(a[12], &n), *st = in.stream(a[13], a[0]);
+    void *y = in.rows(a[11], {T, d}, ot, "y"), *ws = in.bytes(a[12], &n), *st = in.stream(a[13]);
     return unlocked([=] {
       return moe_fp8_forward(plan, x, xq, U8(sx), wr, FL(bias), w.w1, U8(w.s1), w.w3, U8(w.s3), w.w2, U8(w.s2), y, ws, n, st);
     });
@@ -309,7 +338,7 @@ PyObject* checkpoint_save(ARGS) {  // a, b, qa, sa, qb, sb, stream
     const int64_t n = t.size(0), F = t.size(1), sc = moe_fp8_scale_cols(F);
     void *a = in.rows(p[0], {n, F}, kBf16, "a"), *b = in.rows(p[1], {n, F}, kBf16, "b");
     void *qa = in.rows(p[2], {n, F}, kE4m3, "qa"), *sa = in.rows(p[3], {n, sc}, kScales, "sa");
-    void *qb = in.rows(p[4], {n, F}, kE4m3, "qb"), *sb = in.rows(p[5], {n, sc}, kScales, "sb"), *st = in.stream(p[6], p[0]);
+    void *qb = in.rows(p[4], {n, F}, kE4m3, "qb"), *sb = in.rows(p[5], {n, sc}, kScales, "sb"), *st = in.stream(p[6]);
     if (F > INT32_MAX) throw Refused{"a has too many columns"};
     return unlocked([=] { return moe_checkpoint_save_rows(a, b, n, (int32_t)F, qa, U8(sa), qb, U8(sb), st); });
   });
@@ -336,7 +365,7 @@ PyObject* checkpoint_restore(ARGS) {  // qa, sa, qb, sb, a, b, h, stream
   return call<8>(args, nargs, [](Args& in, PyObject* const* p) {
     const Kept k(in, p);
     void *a = in.maybe(p[4], {k.n, k.F}, kBf16, "a"), *b = in.maybe(p[5], {k.n, k.F}, kBf16, "b");
-    void *h = in.maybe(p[6], {k.n, k.F}, kBf16, "h"), *st = in.stream(p[7], p[0]);
+    void *h = in.maybe(p[6], {k.n, k.F}, kBf16, "h"), *st = in.stream(p[7]);
     return unlocked(
         [=] { return moe_checkpoint_restore_rows(k.qa, U8(k.sa), k.qb, U8(k.sb), k.n, (int32_t)k.F, a, b, h, st); });
   });
@@ -346,7 +375,7 @@ PyObject* checkpoint_backward(ARGS) {  // qa, sa, qb, sb, dh, da, db, h, stream
   return call<9>(args, nargs, [](Args& in, PyObject* const* p) {
     const Kept k(in, p);
     void *dh = in.rows(p[4], {k.n, k.F}, kBf16, "dh"), *da = in.rows(p[5], {k.n, k.F}, kBf16, "da");
-    void *db = in.rows(p[6], {k.n, k.F}, kBf16, "db"), *h = in.maybe(p[7], {k.n, k.F}, kBf16, "h"), *st = in.stream(p[8], p[0]);
+    void *db = in.rows(p[6], {k.n, k.F}, kBf16, "db"), *h = in.maybe(p[7], {k.n, k.F}, kBf16, "h"), *st = in.stream(p[8]);
     return unlocked(
         [=] { return moe_checkpoint_backward_rows(k.qa, U8(k.sa), k.qb, U8(k.sb), dh, k.n, (int32_t)k.F, da, db, h, st); });
   });

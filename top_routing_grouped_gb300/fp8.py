@@ -4,8 +4,9 @@ Argument marshalling only, as in ``moe``: outputs and workspaces are the caller'
 every call enqueues its kernels on the current stream (or ``stream``) and returns.  The checks of
 the calls that run once a layer or more are compiled (``_fp8``, csrc/binding.cpp).  8-bit tensors
 are torch.float8_e4m3fn, their block factors torch.float8_e8m0fnu (or the bytes as uint8); a row
-of c values has ``scale_cols(c)`` factors.  A wrong type, shape or layout raises ValueError before
-the library is called; the library's own checks raise ``moe.MoEError``.
+of c values has ``scale_cols(c)`` factors.  A wrong type, shape or layout, a tensor outside GPU memory and
+tensors (or a stream) of more than one device raise ValueError before the library is called; the library's
+own checks raise ``moe.MoEError``.  The tensors' device is made current for the call.
 """
 import ctypes
 
@@ -72,6 +73,14 @@ def _bytes(t):
     return t.data_ptr()
 
 
+def _one_device(*ts, stream=None):
+    """The one device of these tensors and of the stream, made current for the call."""
+    d = ts[0].get_device()
+    if any(t.get_device() != d for t in ts) or (stream is not None and stream.device_index != d):
+        raise ValueError("all tensors and the stream must be on one device")
+    return torch.cuda.device(d)
+
+
 def _stream(stream, t):
     """The given stream, or the current one of t's device."""
     return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
@@ -132,7 +141,9 @@ class _Fp8Plan:
 
     def device_status(self, workspace, stream=None):
         """Synchronises the stream; returns the status code (MOE_OK == 0)."""
-        return _device_status(self._h, _bytes(workspace), _stream(stream, workspace))
+        p = _bytes(workspace)
+        with _one_device(workspace, stream=stream):
+            return _device_status(self._h, p, _stream(stream, workspace))
 
 
 class Fp8MatmulPlan(_Fp8Plan):
@@ -201,14 +212,16 @@ class LayerCheckpoint:
                          f"x must be a contiguous {(p.T, p.d)} tensor of {p.act_dtype}")
 
     def save(self, workspace, stream=None):
-        _check(_layer_ckpt_save(self.plan.handle, _bytes(workspace), workspace.numel(), _bytes(self.data),
-                                self.data.numel(), _stream(stream, workspace)), "moe_checkpoint_save")
+        ws, data = _bytes(workspace), _bytes(self.data)
+        with _one_device(workspace, self.data, stream=stream):
+            _check(_layer_ckpt_save(self.plan.handle, ws, workspace.numel(), data, self.data.numel(),
+                                    _stream(stream, workspace)), "moe_checkpoint_save")
 
     def restore(self, x, workspace, stream=None):
-        p = self.plan
-        _check(_layer_ckpt_restore(p.handle, self._rows(x), _bytes(self.data), self.data.numel(),
-                                   _bytes(workspace), workspace.numel(), _stream(stream, x)),
-               "moe_checkpoint_restore")
+        px, ws, data = self._rows(x), _bytes(workspace), _bytes(self.data)
+        with _one_device(x, workspace, self.data, stream=stream):
+            _check(_layer_ckpt_restore(self.plan.handle, px, data, self.data.numel(), ws, workspace.numel(),
+                                       _stream(stream, x)), "moe_checkpoint_restore")
 
 
 def checkpoint_save(a, b, qa, sa, qb, sb, stream=None):

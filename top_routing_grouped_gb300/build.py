@@ -7,11 +7,13 @@ host is a different architecture from the build host).
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -46,8 +48,23 @@ def binding_source():
     return os.path.join(CSRC, "binding.cpp")
 
 
+def binding_lacks():
+    """What this machine lacks for the binding of the 8-bit operators, or None.  The library needs none of it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return "torch"
+    root = os.path.dirname(spec.origin)
+    if not shutil.which("g++"):
+        return "g++"
+    for f in (os.path.join(sysconfig.get_paths()["include"], "Python.h"), os.path.join(root, "include", "ATen", "core", "Tensor.h"),
+              os.path.join(root, "lib", "libc10_cuda.so")):
+        if not os.path.exists(f):
+            return f
+    return None
+
+
 def up_to_date(out=OUT):
-    outs = [out, BINDING] if out == OUT else [out]
+    outs = [out, BINDING] if out == OUT and not binding_lacks() else [out]
     if not all(os.path.exists(o) for o in outs):
         return False
     t = min(os.path.getmtime(o) for o in outs)
@@ -81,7 +98,8 @@ def link_binding(obj):
 
 def build(out=OUT, verbose=False, extra=(), jobs=None):
     """Compile every csrc/*.cu and link ``out``, and for the package's own library the binding of the
-    8-bit operators.  Returns the library path."""
+    8-bit operators (where the machine has what that needs; else a warning says what it lacks, and importing
+    ``fp8`` fails).  Returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
     flags = common_flags(extra)
@@ -98,9 +116,14 @@ def build(out=OUT, verbose=False, extra=(), jobs=None):
             print(r.stdout + r.stderr, flush=True)
         return obj
 
+    lacks = binding_lacks() if out == OUT else None
+    if lacks:
+        warnings.warn(f"the binding of the 8-bit operators is not built: {lacks} is missing")
+        if os.path.exists(BINDING):
+            os.remove(BINDING)  # of another library
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(compile_binding, os.path.join(BUILD_DIR, "binding.o")) if out == OUT else None
+        binding = ex.submit(compile_binding, os.path.join(BUILD_DIR, "binding.o")) if out == OUT and not lacks else None
         objs = list(ex.map(compile_one, srcs))
     tmp = out + ".tmp"
     cmd = [cc, "-gencode", GENCODE, "-shared", "-Xcompiler", "-fPIC", *objs, "-o", tmp, "-lcudart"]

@@ -13,7 +13,12 @@ import ctypes
 import torch
 
 from .moe import MOE_BF16, MOE_F32, MOE_OK, MoEError, MoeExpertConfig, MoEPlan, _lib, _PATHS
-from . import _fp8  # after torch and libmoe.so, which it is linked with
+
+try:
+    from . import _fp8  # after torch and libmoe.so, which it is linked with
+except ImportError as e:
+    raise ImportError("the binding of the 8-bit operators (_fp8.so) is missing or does not load: build it with "
+                      "__graft_entry__.build(), where g++ and the headers of Python and torch are") from e
 
 _P, _I32, _I64, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}

@@ -539,6 +539,33 @@ def test_experts_at_the_ends_of_silu(fp8, path, seg):
     close(np64(y), want, tol, "y")
 
 
+# One or few rows and a K of several groups of four blocks: the SwiGLU product's units are shared by clusters of
+# 2, 3, 8 and 8 CTAs (16 rows a unit), 8 (32 rows) and 2 and 3 (64 rows).
+SPLIT_EXPERTS = [([1], 1, 1024, 256), ([1, 0, 1, 1, 1], 5, 1040, 272), ([1, 1, 0, 1], 2, 4096, 256), ([0, 13, 1], 3, 4096, 400),
+                 ([20, 0, 5], 3, 4096, 256), ([50, 3], 2, 1024, 144), ([33, 20, 1], 3, 2320, 256)]
+
+
+@pytest.mark.parametrize("seg, E, d, F", SPLIT_EXPERTS, ids=lambda v: str(v))
+def test_experts_hidden_rows_summed_by_clusters(fp8, seg, E, d, F):
+    test_experts(fp8, "auto", seg, E, d, F)
+
+
+@pytest.mark.parametrize("d", [1024, 4096])
+def test_layer_in_8_bits_of_one_wide_token(fp8, d):
+    test_layer_in_8_bits(fp8, 1, d, 8, 2, 256, False, False)
+
+
+# Clusters of 3 to 8 CTAs, some of which take a second unit: the estimate of the units counts one group of rows
+# a segment, and two of the three segments have two.
+SECOND_UNITS = [(3, 1296, 1408), (4, 1920, 1024), (5, 2320, 896), (6, 2832, 752), (7, 3472, 640), (8, 4000, 624)]
+
+
+@pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("split, K, N", SECOND_UNITS)
+def test_matmul_clusters_take_a_second_unit(fp8, out, split, K, N):
+    test_matmul(fp8, "auto", out, [97, 97, 1], 3, K, N)
+
+
 def test_experts_clusters_take_several_units(fp8):
     test_experts(fp8, "auto", [97] * 27 + [2] * 11, 38, 1024, 256)
 

@@ -570,6 +570,36 @@ def test_experts_clusters_take_several_units(fp8):
     test_experts(fp8, "auto", [97] * 27 + [2] * 11, 38, 1024, 256)
 
 
+@pytest.mark.parametrize("path, least", [("simt", 90), ("auto", 87)])
+@pytest.mark.parametrize("n", [3, 33, 300])
+def test_experts_of_hidden_rows_that_are_all_small(fp8, path, least, n):
+    """Pre-activations at the lower end of SiLU, so that nothing larger in a block hides them: a is -80 to
+    -least, the same for all hidden columns of a row, and b is 2^14 of either sign (all exact).  The exponential is good
+    to 2 + 1.17 |a| steps of 2^-23, and to half a subnormal step of 2^-149 of its 2^-130 at least: 2^-16 in all.
+    A hidden value within twice that of a border may take the neighbouring e4m3, a step of 2^-3."""
+    d, F = 128, 256
+    a = -(80 + np.arange(n) * (least - 80) // max(1, n - 1)).astype(np.float64)
+    x = np.zeros((n, d))
+    x[:, 0], x[:, 1], x[:, 2] = 10, -a - 80, 1
+    w1, w3, w2 = np.zeros((1, F, d)), np.zeros((1, F, d)), np64(torch.randn(1, d, F, generator=gen(67)) * 16)
+    w1[:, :, 0], w1[:, :, 1] = -8, -1
+    w3[:, :, 2] = 2.0 ** 14 * (1 - 2 * (np.arange(F) % 3 == 0))
+    qx, w = ref.quantize(x), [ref.quantize_weights(v) for v in (w1, w3, w2)]
+    held, ex = ref.dequantize(*qx), np.zeros(n, int)
+    np.testing.assert_array_equal(ref.matmul(held, ref.dequantize_w(*w[0]), ex)[0], np.repeat(a[:, None], F, 1))
+    plan = fp8.Fp8ExpertPlan(n, d, 1, 1, F, path=path)
+    ws, y = plan.new_workspace(), torch.empty(n, d, dtype=BF, device="cuda")
+    t = [v.cuda() for p in w for v in ref.to_torch(*p)]
+    plan.forward(None, *(v.cuda() for v in ref.to_torch(*qx)), torch.ones(n, device="cuda"), *t, y, ws)
+    assert plan.device_status(ws) == 0
+    want, tol = expert_rows(held, *w, np.ones(n), ex)
+    h = np.abs(ref.silu(a))[:, None] * np.full((1, F), 2.0 ** 14)
+    f = np.repeat(ref.scale_value(ref.quantize(h)[1][:, :F // 128]), 128, 1)
+    near = ref.round_e4m3(h * (1 - 2.0 ** -15) / f) != ref.round_e4m3(h * (1 + 2.0 ** -15) / f)
+    close(np64(y), want, tol + ref.matmul(near * 2.0 ** -3 * h, np.abs(ref.dequantize_w(*w[2])), ex)[0], "y")
+    assert (np.abs(np64(y)).max(1) > 0).all()
+
+
 def test_experts_paths_agree_on_a_larger_layer(fp8):
     """The tensor-core and SIMT paths on 3000 rows of 16 experts: both round the same sums to the
     same 8 bits but for values at a border, and y to bf16: 2-norm of the difference within 2^-8."""

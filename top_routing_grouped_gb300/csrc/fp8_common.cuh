@@ -57,27 +57,30 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint32_t v) {
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // sigma(a) = 1 / (1 + e^-a) and 1 - sigma(a), from z = e^-|a|: the quotients' denominator 1 + z lies
-// in [1, 2], so nothing overflows or is flushed for any a, and either value is good to a few fp32
-// steps.
+// in [1, 2], so nothing overflows for any a.  The larger of the two is good to a few fp32 steps; the smaller
+// one, z r, has z's relative error, which grows with |a| (__expf: 2 + 1.17 |a| steps, 1e-5 at |a| = 80; the
+// results are rounded to bf16, 2^-8), and is 0 where e^-|a| is, past |a| = 104.
 __device__ __forceinline__ void sigmoid_pair(float a, float& s, float& one_minus_s) {
   const float z = __expf(-fabsf(a)), r = __fdividef(1.f, 1.f + z), zr = z * r;
   s = a >= 0.f ? r : zr;
   one_minus_s = a >= 0.f ? zr : r;
 }
 
-// SiLU(a) = a sigma(a), good to a few fp32 steps for every a.
+// SiLU(a) = a sigma(a), as good as sigma(a).
 __device__ __forceinline__ float silu_exact(float a) {
   float s, c;
   sigmoid_pair(a, s, c);
   return a * s;
 }
 
-// The same for the hidden rows, in five instructions: a / (1 + 2^(-a log2 e)), but that it is 0 below
-// a = -87, where e^a leaves fp32's normal range (SiLU is at most 1e-36 there, far below what a's own
-// rounding moves it by).  With K of one or two blocks the epilogue is what bounds the product, and
-// with silu_exact, twice as many instructions, the experts of 128 x 3024 took 235 us, not 166.  The rows are
-// rounded to e4m3 right after this: an error of the hardware tanh (2^-11) would move about one value in
-// 128 to its neighbour.
+// The same for the tensor-core kernels' hidden rows, in five instructions: a / (1 + 2^(-a log2 e)).  Down to
+// a = -87 it is as good as silu_exact; below it is 0, since the reciprocal of what is past 2^126 leaves
+// fp32's normal range, while SiLU is there at most 87.4 * 2^-126 = 1.03e-36 in magnitude.  (The quotient in
+// plain fp32 is 0 from -88.8 on, where e^-a overflows.)  That can be seen in a hidden row whose 128 values of a block are
+// all so small, nowhere else: beside any larger value they round to 0.  With K of one or two blocks the
+// epilogue is what bounds the product, and with silu_exact, twice as many instructions, the experts of 128 x
+// 3024 took 235 us, not 166.  The rows are rounded to e4m3 right after this: an error of the hardware tanh
+// (2^-11) would move about one value in 128 to its neighbour.
 __device__ __forceinline__ float silu_hidden(float a) {
   float z, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(a * -1.4426950408889634f));

@@ -2,6 +2,8 @@
 // cross-check of the tensor-core kernels.  An e4m3 times its power of two is exact in fp32, as is
 // the product of two; the sums are fp32 in ascending k.
 //
+// SiLU is silu_exact here, not the tensor-core kernels' shorter form.
+//
 // A CTA computes 32 rows x 128 columns (SwiGLU: of both products, so that a row's block of 128
 // hidden values, which shares a factor, lies in one warp): lane l of warp w has rows 4w..4w+3 and
 // columns l, l + 32, l + 64, l + 96.
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) gemm_fp8_simt_kernel(GemmArgs g, Ws 
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          h[j] = n0 + lane + 32 * j < g.n ? silu_hidden(acc[0][i][j]) * acc[1][i][j] : 0.f;
+          h[j] = n0 + lane + 32 * j < g.n ? silu_exact(acc[0][i][j]) * acc[1][i][j] : 0.f;
           top = max(top, abs_bits(h[j]));
         }
         const uint32_t sb = scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));

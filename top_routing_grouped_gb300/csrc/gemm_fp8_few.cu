@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t x[3], w0 = 0, w1 = 0;
     auto request = [&]() {
 #pragma unroll
-      for (int c = 0; c < 3; ++c) x[c] = __ldg(sx32 + rx[c] + gk);
+      for (int c = 0; c < 3; ++c) x[c] = sx32[rx[c] + gk];  // not __ldg: written while this kernel already runs
       w0 = __ldg(sw32 + rw + gk);
       w1 = __ldg(sw3_32 + rw + gk);
     };

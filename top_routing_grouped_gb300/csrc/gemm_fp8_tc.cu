@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t a[4], b0, b1;
     auto request = [&]() {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) a[c] = __ldg(sa32 + ra[c] + gk);
+      for (int c = 0; c < 4; ++c) a[c] = sa32[ra[c] + gk];  // not __ldg: written while this kernel already runs
       b0 = __ldg(sb32 + r0 + gk);
       b1 = __ldg(sb3_32 + r1 + gk);
     };

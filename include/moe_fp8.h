@@ -162,8 +162,8 @@ moe_status moe_checkpoint_backward_rows(const void* qa, const uint8_t* sa, const
                                         void* stream);
 
 /* Checkpoints of a training layer: L layers of one shape train with one workspace and L
- * checkpoints, each a little over a quarter of what a forward leaves in the workspace for
- * moe_backward.  After moe_forward, moe_checkpoint_save copies the routing and the router
+ * checkpoints.  A checkpoint has 2 F (1 + 1/32) bytes a routed row and the routing, where a forward leaves
+ * 6 F + 2 d for moe_backward: a little over a quarter at F = d, a fifth at F = d / 2.  After moe_forward, moe_checkpoint_save copies the routing and the router
  * softmax and quantises the pre-activations; before moe_backward, moe_checkpoint_restore puts
  * them back, rebuilds the hidden rows from them and the dispatched rows from x (the forward's
  * input).  The backward is then that of the layer with the pre-activations as they were kept.

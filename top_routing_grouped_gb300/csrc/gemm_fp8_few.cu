@@ -15,9 +15,9 @@
 // rows a CTA adds the others' sums, which arrive in its shared memory, in rank order.  (With all rows
 // summed by the first CTA 96 x 8192 x 2048 took 13.4 us, not 9.7.)
 //
-// What bounds it: HBM while the weights stream (1500 rows over 128 experts of 2048 x 1024: 126 us,
-// 6.3 TB/s of weights, rows and results); with one unit for each SM the fixed part counts, about 5 us of
-// a launch (one token of 64 experts of 4096 x 2048: 24.3 us for 101 MB; 13 x 2064 x 8208: 7.3 us for
+// What bounds it: HBM while the weights stream (1500 rows over 128 experts of 2048 x 1024: 129 us,
+// 6.1 TB/s of weights, rows and results); with one unit for each SM the fixed part counts, about 5 us of
+// a launch (one token of 64 experts of 4096 x 2048: 25.1 us for 101 MB; 13 x 2064 x 8208: 7.4 us for
 // 17 MB).  The CTA pairs take 141, 34 and 9.8 us for the three.  In the token's call HBM stands still for some
 // 3.5 us between the two products (epilogue, launch, set-up); fetching the second one's first weights
 // to L2 meanwhile gained nothing (24 MB: 25.4 -> 26.2 us, 12 MB: 25.2), nor did two CTAs an SM.

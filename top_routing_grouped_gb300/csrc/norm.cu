@@ -7,8 +7,11 @@
 //   dweight = sum_t dn xhat
 //
 // Both read and write each value once: HBM bounds them (one row: the launch does).  32768 x 4096 bf16
-// with residual, bf16 and e4m3 outputs: 190 us, 6.3 TB/s; backward from fp32 gradients: 211 us, 6.3
-// TB/s; one row of 4096: 2.1 us.
+// with residual, bf16 and e4m3 outputs: 192 us, 6.3 TB/s; backward from fp32 gradients: 201 us, 6.7
+// TB/s; one row of 4096: 2.1 us.  By width (2^25 values, bf16, residual; forward / backward in TB/s): 1000 to 4096
+// columns 5.0-6.2 / 5.8-6.0 (2500: 5.4 / 3.8), 4100 to 8192 3.9-5.6 / 4.6-5.2 (one CTA of 288 to 512 threads an
+// SM), off whole pairs 2.1 / 1.8 at 257 and 3.3 / 2.7 at 2001, 64 and 128 columns 2.0-3.9 / 2.4-4.4, and past 8192,
+// where a row goes through shared memory in single values, 1.5 / 0.8 at 12288 and 1.1 / 0.8 at 16384.
 //
 // A row is held in registers by W warps, eight values a thread and piece, V pieces a thread; the
 // CTAs are persistent and a row's loads are issued before the row before it is reduced, so the
@@ -526,7 +529,9 @@ static int row_threads(int d) {
   return (d + per_warp - 1) / per_warp * 32;
 }
 
-// Persistent CTAs: what 152 SMs hold of them, at about 64 registers a thread, 128 with two pieces.
+// Persistent CTAs: what 152 SMs hold of them at 64 registers a thread, 128 with two pieces.  The forward's kernels
+// and the backward's for bf16 on whole vectors have that (60 to 70; with two pieces 96 to 126); the other backward kernels
+// take 87 to 113 with one piece, so that part of their grid waits for the rest.
 static int resident(int d) {
   const int threads = row_threads(d), most = pieces(d) == 1 ? 1024 : 512;
   return 152 * (most / threads);

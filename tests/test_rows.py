@@ -1,0 +1,302 @@
+"""Rows sorted by expert and back with gates applied, and the gradients, on the GPU against plain 64-bit
+references.
+
+Tolerances.  Sorts and gathers move values: compared bit for bit.  A sum of n products in fp32, in any order,
+is off by at most (n + 1) roundings of 2^-24 of the sum of the terms' magnitudes; storing a value of type t adds
+half a step of it, H[t]."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+H = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+F8 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def rows():
+    from top_routing_grouped_gb300 import rows as m
+    return m
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def np64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def choice(T, k, E, seed, drop=0.0, hot=0.0):
+    """Experts of each slot (the same one may come twice), some dropped, some all for expert E // 2."""
+    g = gen(seed)
+    idx = torch.randint(0, E, (T, k), generator=g)
+    idx = torch.where(torch.rand(T, k, generator=g) < hot, E // 2, idx)
+    gone = torch.tensor([-1, E, -2 ** 31, 2 ** 31 - 1])[torch.randint(0, 4, (T, k), generator=g)]
+    return torch.where(torch.rand(T, k, generator=g) < drop, gone, idx)
+
+
+def sorted_ref(idx, E):
+    flat = idx.reshape(-1).numpy().astype(np.int64)
+    ok = (flat >= 0) & (flat < E)
+    order = np.argsort(np.where(ok, flat, E), kind="stable")[:ok.sum()]
+    pos, row_slot = np.full(flat.size, -1, np.int32), np.full(flat.size, -1, np.int32)
+    pos[order] = np.arange(order.size)
+    row_slot[:order.size] = order
+    return np.bincount(flat[ok], minlength=E).astype(np.int32), pos.reshape(idx.shape), row_slot
+
+
+def full(*shape, dtype=torch.int32, value=77):
+    return torch.full(shape, value, dtype=dtype, device="cuda")
+
+
+def as_bytes(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy()
+
+
+# T, k, E, drop, hot
+SORTS = [(1, 1, 1, 0, 0), (1, 4, 64, 0, 0), (1, 64, 1024, 0.2, 0), (7, 3, 5, 0.5, 0), (33, 8, 128, 0, 0.7), (300, 2, 8, 1.0, 0),
+         (1029, 8, 128, 0.5, 0.2), (2048, 8, 256, 0, 0), (2049, 8, 256, 0, 0), (5000, 4, 60, 0.1, 0), (70000, 1, 3, 0, 0),
+         (4111, 64, 1024, 0.3, 0.1), (40000, 6, 1, 0, 0), (150001, 2, 33, 0.9, 0.5)]
+
+
+@pytest.mark.parametrize("T, k, E, drop, hot", SORTS)
+@pytest.mark.parametrize("wide", [False, True])
+def test_sort(rows, T, k, E, drop, hot, wide):
+    idx = choice(T, k, E, T + k, drop, hot)
+    if wide:  # values that agree with an expert's number in their low half
+        idx = torch.where(idx < 0, idx + (1 << 32), idx)
+    counts, pos, row_slot = full(E), full(T, k), full(T * k)
+    rows.sort(idx.to("cuda") if wide else idx.to(torch.int32).to("cuda"), counts, pos, row_slot, rows.dispatch_workspace(T, k, E))
+    for got, want in zip((counts, pos, row_slot), sorted_ref(idx, E)):
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
+
+
+def test_sort_without_row_slot_and_of_no_tokens(rows):
+    idx = choice(50, 4, 9, 1).to(torch.int32)
+    counts, pos = full(9), full(50, 4)
+    rows.sort(idx.cuda(), counts, pos)
+    np.testing.assert_array_equal(pos.cpu().numpy(), sorted_ref(idx, 9)[1])
+    rows.sort(torch.empty(0, 4, dtype=torch.int64, device="cuda"), counts, full(0, 4))
+    assert counts.cpu().tolist() == [0] * 9
+
+
+def source(T, d, dtype, seed, lay="plain"):
+    raw = torch.randint(0, 256, (T, (d + 24) * dtype.itemsize), generator=gen(seed), dtype=torch.int64).to(torch.uint8)
+    wide = raw.cuda().view(dtype)  # any bits: NaNs and infinities among them
+    return {"plain": wide[:, :d].contiguous(), "pitched": wide[:, :d], "shifted": wide[:, 1:d + 1]}[lay]
+
+
+# T, k, E, d, dtype, layout, drop
+DISPATCHES = [(1, 4, 64, 4096, F8, "plain", 0), (1, 1, 1, 1, F8, "plain", 0), (3, 2, 4, 16384, F32, "plain", 0), (13, 8, 32, 2048, BF, "plain", 0),
+              (1029, 8, 128, 2050, BF, "pitched", 0.5), (257, 5, 7, 333, BF, "shifted", 0.1), (64, 3, 60, 1000, F32, "shifted", 0),
+              (100, 2, 8, 129, F8, "shifted", 0.3), (3000, 8, 32, 264, F8, "plain", 0.2), (2600, 8, 256, 72, F32, "pitched", 0.75),
+              (17, 64, 300, 520, BF, "plain", 0), (9000, 2, 16, 20, BF, "plain", 0), (20, 2, 4, 40000, BF, "pitched", 0)]
+
+
+@pytest.mark.parametrize("T, k, E, d, dtype, lay, drop", DISPATCHES)
+def test_dispatch_and_gather(rows, T, k, E, d, dtype, lay, drop):
+    from top_routing_grouped_gb300 import fp8
+    idx, x = choice(T, k, E, d, drop), source(T, d, dtype, 3, lay)
+    gates = torch.rand(T, k, generator=gen(4)).cuda()
+    scaled = dtype is F8
+    sx = torch.randint(0, 256, (T, fp8.scale_cols(d)), generator=gen(5), dtype=torch.int64).to(torch.uint8).cuda() if scaled else None
+    counts_ref, pos_ref, slot_ref = sorted_ref(idx, E)
+    n = int(counts_ref.sum())
+    for R in {T * k, n, n // 2}:  # the last: rows past the buffer are left out
+        for call in ("dispatch", "gather"):
+            counts, pos, row_slot = full(E), full(T, k), full(T * k)
+            out, rg = full(R * d * dtype.itemsize, dtype=torch.uint8).view(dtype).view(R, d), full(R, dtype=F32)
+            rs = full(R, fp8.scale_cols(d), dtype=torch.uint8) if scaled else None
+            if call == "dispatch":
+                rows.dispatch(idx.to("cuda"), x, counts, pos, out, rows.dispatch_workspace(T, k, E), row_slot, sx, rs, gates, rg)
+                for got, want in zip((counts, pos, row_slot), (counts_ref, pos_ref, slot_ref)):
+                    np.testing.assert_array_equal(got.cpu().numpy(), want)
+            else:
+                rows.gather(torch.from_numpy(pos_ref).cuda(), x, out, sx, rs, gates, rg)
+            m = min(n, R)
+            token = slot_ref[:m] // k
+            np.testing.assert_array_equal(as_bytes(out[:m]), as_bytes(x)[token])
+            assert (as_bytes(out[m:]) == 77).all() and (rg[m:] == 77).all()  # left as they were
+            np.testing.assert_array_equal(rg[:m].cpu().numpy(), gates.cpu().numpy().reshape(-1)[slot_ref[:m]])
+            if scaled:
+                np.testing.assert_array_equal(rs[:m].cpu().numpy(), sx.cpu().numpy()[token])
+                assert (rs[m:] == 77).all()
+
+
+def positions(T, k, R, seed, bad=0.2):
+    """Different rows for the slots, some outside [0, R)."""
+    g = gen(seed)
+    pos = torch.randperm(max(R, T * k), generator=g)[:T * k].view(T, k).to(torch.int32)
+    out = torch.tensor([-1, R, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)[torch.randint(0, 4, (T, k), generator=g)]
+    return torch.where((torch.rand(T, k, generator=g) < bad) | (pos >= R), out, pos)
+
+
+# T, k, d, R, y's type, the other's type, offset in values of y and out
+COMBINES = [(1, 1, 1, 1, BF, BF, 0), (1, 8, 7552, 8, BF, F32, 0), (13, 8, 2048, 104, BF, BF, 0), (257, 4, 1000, 900, F32, F32, 0),
+            (300, 6, 2050, 1800, BF, BF, 0), (65, 2, 333, 130, F32, BF, 0), (40, 16, 264, 640, BF, BF, 1), (37, 64, 516, 2400, F32, F32, 1),
+            (20, 33, 72, 660, BF, F32, 4), (5000, 2, 40, 9000, F32, F32, 2), (3, 2, 20000, 6, BF, BF, 0), (9, 3, 64, 0, BF, BF, 0)]
+
+
+def at(t, offset):
+    """A contiguous copy of t that begins `offset` values past an aligned address."""
+    buf = torch.empty(t.numel() + offset, dtype=t.dtype, device="cuda")[offset:].view(t.shape)
+    return buf.copy_(t)
+
+
+@pytest.mark.parametrize("T, k, d, R, ty, to, offset", COMBINES)
+@pytest.mark.parametrize("gated, res", [(True, "other"), (False, None), (True, "self"), (False, "other")])
+def test_combine(rows, T, k, d, R, ty, to, offset, gated, res):
+    g = gen(d)
+    y, pos = at(torch.randn(R, d, generator=g).to(ty), offset), positions(T, k, R, 8)
+    gates = torch.randn(T, k, generator=g) if gated else None
+    r = at(torch.randn(T, d, generator=g).to(to), offset) if res else None
+    r64 = np64(r) if res else np.zeros((T, d))
+    out = r if res == "self" else at(torch.full((T, d), 77.0).to(to), offset)
+    rows.combine(y, pos.cuda(), out, gates=None if gates is None else gates.cuda(), residual=r)
+    ok = (pos >= 0) & (pos < R)
+    y64 = np64(y)[np.where(ok, pos, 0)] if R else np.zeros((T, k, d))
+    terms = np.where(ok.numpy()[:, :, None], y64 * (np64(gates)[:, :, None] if gated else 1.0), 0.0)
+    want = r64 + terms.sum(1)
+    tol = (k + 1) * 2.0 ** -24 * (np.abs(terms).sum(1) + np.abs(r64)) + H[to] * np.abs(want)
+    assert (np.abs(np64(out) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("T, k, d, R, ty, to, offset", COMBINES)
+@pytest.mark.parametrize("gated, wants", [(True, "both"), (False, "rows"), (True, "gates"), (True, "in place")])
+def test_combine_backward(rows, T, k, d, R, ty, to, offset, gated, wants):
+    g = gen(d + 1)
+    y, pos = at(torch.randn(R, d, generator=g).to(ty), offset), positions(T, k, R, 9)
+    gates = torch.randn(T, k, generator=g) if gated else None
+    dout = at(torch.randn(T, d, generator=g).to(to), offset)
+    y64, o64 = np64(y), np64(dout)
+    dy = {"gates": None, "in place": y}.get(wants, at(torch.full((R, d), 77.0).to(ty), offset))
+    dg = None if wants == "rows" else full(T, k, dtype=F32)
+    rows.combine_backward(dout, pos.cuda(), None if gates is None else gates.cuda(), y_rows=None if wants == "rows" else y, dy_rows=dy, dgates=dg)
+    ok = ((pos >= 0) & (pos < R)).numpy()
+    if dg is not None:
+        terms = np.where(ok[:, :, None], o64[:, None, :] * (y64[np.where(ok, pos, 0)] if R else 0.0), 0.0)
+        tol = (d + 1) * 2.0 ** -24 * np.abs(terms).sum(2)
+        assert (np.abs(np64(dg) - terms.sum(2)) <= tol).all()
+    if dy is not None:
+        want = np.full((R, d), 77.0) if wants != "in place" else y64.copy()
+        want[pos.numpy()[ok]] = ((np64(gates)[:, :, None] if gated else 1.0) * np.broadcast_to(o64[:, None, :], (T, k, d)))[ok]
+        assert (np.abs(np64(dy) - want) <= (2.0 ** -24 + H[ty]) * np.abs(want)).all()
+
+
+def test_gradients_are_those_of_differences(rows):
+    """<gradient, direction> against a central difference of the forward, for rows, gates and the tokens."""
+    T, k, E, d, step = 40, 3, 6, 24, 2.0 ** -4
+    idx, x = choice(T, k, E, 5, 0.2).cuda(), torch.randn(T, d, generator=gen(1)).cuda()
+    gates, dout = torch.rand(T, k, generator=gen(2)).cuda(), torch.randn(T, d, generator=gen(3)).cuda()
+    w = torch.randn(d, generator=gen(4)).cuda()
+    counts, pos, xr = full(E), full(T, k), torch.zeros(T * k, d, device="cuda")
+
+    def loss(x, gates):
+        """Rows to y = w x, back with gates: bilinear in x and gates, so that a central difference is exact."""
+        rows.dispatch(idx, x, counts, pos, xr)
+        out = torch.empty(T, d, device="cuda")
+        rows.combine(xr * w, pos, out, gates=gates, residual=x)
+        return float((out.double() * dout.double()).sum())
+
+    loss(x, gates)
+    dy, dg, dx = torch.zeros_like(xr), torch.empty_like(gates), torch.empty_like(x)
+    rows.combine_backward(dout, pos, gates, y_rows=xr * w, dy_rows=dy, dgates=dg)
+    rows.combine(dy * w, pos, dx, residual=dout)  # the dispatch's gradient, with the residual's
+    for name, at_, grad in (("x", x, dx), ("gates", gates, dg)):
+        way = torch.randn(at_.shape, generator=gen(6)).cuda()
+        args = [(x + s * step * way, gates) if name == "x" else (x, gates + s * step * way) for s in (1, -1)]
+        diff = (loss(*args[0]) - loss(*args[1])) / (2 * step)
+        # each loss is a sum of T d (k + 1) products, each with a few fp32 roundings
+        scale = float(dout.abs().double().sum()) * 8 * 2.0 ** -24 * (k + 3) / step * 4
+        assert abs(diff - float((grad.double() * way.double()).sum())) <= scale, name
+
+
+def test_captured_with_other_inputs_and_streams(rows):
+    """Two captured graphs that share a workspace, replayed on another stream with new contents."""
+    T, k, E, d = 9000, 2, 16, 64
+    ws = rows.dispatch_workspace(T, k, E)
+    sets = []
+    for s in range(2):
+        b = dict(idx=choice(T, k, E, s).to(torch.int32).cuda(), x=torch.randn(T, d, generator=gen(s)).cuda(), counts=full(E), pos=full(T, k),
+                 xr=torch.zeros(T * k, d, device="cuda"), out=torch.zeros(T, d, device="cuda"))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            rows.dispatch(b["idx"], b["x"], b["counts"], b["pos"], b["xr"], ws)
+            rows.combine(b["xr"], b["pos"], b["out"])
+        sets.append((b, g))
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for s, (b, g) in enumerate(sets):
+            b["idx"].copy_(choice(T, k, E, 10 + s).to(torch.int32))
+            b["x"].normal_()
+        for _ in range(3):
+            for _, g in sets:
+                g.replay()
+    side.synchronize()
+    for s, (b, _) in enumerate(sets):
+        counts, pos, _ = sorted_ref(choice(T, k, E, 10 + s), E)
+        np.testing.assert_array_equal(b["counts"].cpu().numpy(), counts)
+        np.testing.assert_array_equal(b["pos"].cpu().numpy(), pos)
+        assert torch.equal(b["out"], 2 * b["x"])  # both of its rows come back
+
+
+def test_same_results_every_time(rows):
+    T, k, E, d = 3000, 8, 64, 136
+    idx, y, dout = choice(T, k, E, 1, 0.1).cuda(), torch.randn(T * k, d, device="cuda"), torch.randn(T, d, device="cuda")
+    gates, ws, seen = torch.rand(T, k, device="cuda"), rows.dispatch_workspace(T, k, E), []
+    for _ in range(3):
+        counts, pos, out, dg = full(E), full(T, k), torch.zeros(T, d, device="cuda"), full(T, k, dtype=F32)
+        rows.sort(idx, counts, pos, None, ws)
+        rows.combine(y, pos, out, gates)
+        rows.combine_backward(dout, pos, gates, y_rows=y, dgates=dg)
+        seen.append((pos, out, dg))
+    assert all(torch.equal(a, b) for s in seen[1:] for a, b in zip(s, seen[0]))
+
+
+def test_a_gate_of_zero_keeps_what_the_formula_gives(rows):
+    """0 * infinity is NaN; a slot without a row is not read."""
+    y = torch.tensor([[float("inf"), 1.0], [2.0, 3.0]], device="cuda")
+    pos, gates, out = torch.tensor([[0, 1], [1, -1]], dtype=torch.int32, device="cuda"), torch.tensor([[0.0, 1.0], [2.0, float("nan")]], device="cuda"), torch.empty(2, 2, device="cuda")
+    rows.combine(y, pos, out, gates=gates)
+    assert torch.isnan(out[0, 0]) and out[0, 1] == 3 and out[1].tolist() == [4.0, 6.0]
+
+
+@pytest.mark.parametrize("T", [1, 50, 700])
+def test_the_expert_stage_on_sorted_rows_is_the_layer(rows, T):
+    """Another router's choice through the 8-bit expert stage: dispatch, experts, combine; against the rows one by one."""
+    from top_routing_grouped_gb300 import fp8
+    k, E, d, F = 3, 8, 256, 192
+    g = gen(T)
+    x = torch.randn(T, d, generator=g).to(BF).cuda()
+    idx, gates = choice(T, k, E, T, 0.2).to(torch.int32).cuda(), torch.rand(T, k, generator=g).cuda()
+    q, s = torch.empty(T, d, dtype=F8, device="cuda"), full(T, fp8.scale_cols(d), dtype=torch.uint8)
+    fp8.quantize(x, q, s)
+    w = []
+    for n, c in ((F, d), (F, d), (d, F)):
+        wq, ws = torch.empty(E, n, c, dtype=F8, device="cuda"), full(E, (n + 127) // 128, fp8.scale_cols(c), dtype=torch.uint8)
+        fp8.quantize_weights((torch.randn(E, n, c, generator=g) * c ** -0.5).cuda(), wq, ws)
+        w += [wq, ws]
+    R = T * k
+    plan = fp8.Fp8ExpertPlan(R, d, E, 1, F)
+    counts, pos, xr, xs = full(E), full(T, k), torch.zeros(R, d, device="cuda").to(F8), torch.zeros(R, fp8.scale_cols(d), dtype=torch.uint8, device="cuda")
+    y, rg, out, ones = torch.zeros(R, d, dtype=BF, device="cuda"), torch.zeros(R, device="cuda"), torch.empty(T, d, dtype=BF, device="cuda"), torch.ones(R, device="cuda")
+    rows.dispatch(idx, q, counts, pos, xr, rows.dispatch_workspace(T, k, E), x_scales=s, row_scales=xs, gates=gates, row_gates=rg)
+    ws = plan.new_workspace()
+    plan.forward(counts, xr, xs, ones, *w, y, ws)
+    rows.combine(y, pos, out, gates=gates, residual=x)
+    assert plan.device_status(ws) == 0
+    want = np64(x)
+    for j in range(k):  # every slot as its own batch of one row a token, sorted by hand
+        order = torch.argsort(idx[:, j], stable=True)
+        has = (idx[order, j] >= 0) & (idx[order, j] < E)
+        order = order[has]
+        if not order.numel():
+            continue
+        one = fp8.Fp8ExpertPlan(order.numel(), d, E, 1, F)
+        c, yy = torch.bincount(idx[order, j], minlength=E).to(torch.int32), torch.empty(order.numel(), d, dtype=BF, device="cuda")
+        one.forward(c, q[order].contiguous(), s[order].contiguous(), torch.ones(order.numel(), device="cuda"), *w, yy, one.new_workspace())
+        want[order.cpu().numpy()] += np64(gates[order, j])[:, None] * np64(yy)
+    # the same products, which may sum in another order: a hidden value at a border of e4m3 may fall to either side
+    assert np.linalg.norm(np64(out) - want) <= 1e-2 * np.linalg.norm(want)

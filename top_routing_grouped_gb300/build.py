@@ -41,7 +41,7 @@ def sources():
 
 def headers():
     return sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  [os.path.join(os.path.dirname(HERE), "include", h) for h in ("moe.h", "moe_fp8.h")])
+                  [os.path.join(os.path.dirname(HERE), "include", h) for h in ("moe.h", "moe_fp8.h", "moe_rows.h", "moe_optim.h")])
 
 
 def binding_source():

@@ -2,12 +2,11 @@
 // workspaces and launch sequences.
 #include <cuda_runtime.h>
 #include <math.h>
-#include <stdarg.h>
-#include <stdio.h>
 
 #include <new>
 
 #include "fp8_internal.h"
+#include "host_checks.h"
 
 struct moe_fp8_plan_s {
   bool experts;  // the expert stage (else one product)
@@ -47,47 +46,6 @@ bool use_few(int64_t rows, int64_t n_seg, int64_t widest_out) {
 namespace {
 
 using namespace moe;
-
-moe_status fail(moe_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-moe_status fail(moe_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  return set_last_error(st, buf);
-}
-
-moe_status cuda_status(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return MOE_OK;
-  return fail(MOE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-struct Ptr {
-  const void* p;
-  const char* name;
-  size_t align;
-  bool may_be_null;
-};
-template <size_t N>
-moe_status check(const Ptr (&ptrs)[N]) {
-  for (const Ptr& q : ptrs) {
-    if (!q.p && !q.may_be_null) return fail(MOE_ERR_INVALID_ARG, "%s is null", q.name);
-    if (!aligned(q.p, q.align)) return fail(MOE_ERR_INVALID_ARG, "%s is not %zu-byte aligned", q.name, q.align);
-  }
-  return MOE_OK;
-}
-
-// Whether [a, a + na) and [b, b + nb) share a byte.
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na && nb && x < y + nb && y < x + na;
-}
-
-bool is_dtype(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
-size_t esize(int32_t t) { return t == MOE_BF16 ? 2 : 4; }
 
 moe_status check_sizes(int64_t rows, int64_t cols, int64_t ld) {
   if (rows < 0 || cols < 1) return fail(MOE_ERR_INVALID_ARG, "rows must be >= 0 and columns >= 1");

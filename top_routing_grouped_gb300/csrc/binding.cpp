@@ -1,5 +1,6 @@
-// binding.cpp -- the Python module top_routing_grouped_gb300._fp8: the 8-bit operators' calls from torch
-// tensors (include/moe_fp8.h).  Each function checks types, shapes and layouts, as fp8.py documents them,
+// binding.cpp -- the Python module top_routing_grouped_gb300._fp8: the calls of the 8-bit operators
+// (include/moe_fp8.h), of the rows around an expert stage (moe_rows.h) and of the optimiser's step (moe_optim.h)
+// from torch tensors.  Each function checks types, shapes and layouts, as fp8.py, rows.py and optim.py document them,
 // takes the current stream where none is given, and calls the library without the interpreter's lock.
 //
 // A call of a few rows takes the GPU two to five microseconds.  Checked in Python and passed on by ctypes,
@@ -18,8 +19,11 @@
 #include <memory>
 #include <optional>
 #include <string>
+#include <vector>
 
 #include "../../include/moe_fp8.h"
+#include "../../include/moe_optim.h"
+#include "../../include/moe_rows.h"
 
 namespace {
 
@@ -31,7 +35,7 @@ struct Refused {  // -> ValueError
 struct PyError {};  // the Python error is already set
 
 // Types a tensor may have, in the order a message names them.
-enum : unsigned { kF32 = 1, kBf16 = 2, kE4m3 = 4, kE8m0 = 8, kU8 = 16, kI32 = 32 };
+enum : unsigned { kF32 = 1, kBf16 = 2, kE4m3 = 4, kE8m0 = 8, kU8 = 16, kI32 = 32, kI64 = 64 };
 constexpr unsigned kFloats = kF32 | kBf16, kScales = kE8m0 | kU8;
 
 unsigned type_of(const Tensor& t) {
@@ -42,6 +46,7 @@ unsigned type_of(const Tensor& t) {
     case at::ScalarType::Float8_e8m0fnu: return kE8m0;
     case at::ScalarType::Byte: return kU8;
     case at::ScalarType::Int: return kI32;
+    case at::ScalarType::Long: return kI64;
     default: return 0;
   }
 }
@@ -50,16 +55,16 @@ int32_t moe_dtype_of(unsigned type) { return type == kBf16 ? MOE_BF16 : MOE_F32;
 
 std::string names(unsigned types) {
   static constexpr const char* kNames[] = {"torch.float32", "torch.bfloat16", "torch.float8_e4m3fn", "torch.float8_e8m0fnu",
-                                           "torch.uint8", "torch.int32"};
+                                           "torch.uint8", "torch.int32", "torch.int64"};
   std::string s;
-  for (int i = 0; i < 6; ++i)
+  for (int i = 0; i < 7; ++i)
     if (types >> i & 1) s += (s.empty() ? "" : " or ") + std::string(kNames[i]);
   return s;
 }
 
 using Shape = std::initializer_list<int64_t>;
 
-[[noreturn]] void refuse(Shape shape, unsigned types, const char* name, const char* how) {
+[[noreturn]] void refuse(at::IntArrayRef shape, unsigned types, const char* name, const char* how) {
   std::string s;
   for (int64_t v : shape) s += (s.empty() ? "" : ", ") + std::to_string(v);
   if (shape.size() == 1) s += ",";
@@ -119,9 +124,12 @@ struct Args {
 
   // The address of a row-major contiguous tensor of this shape and one of these types.
   void* rows(PyObject* o, Shape shape, unsigned types, const char* name) {
+    return array(o, at::IntArrayRef(shape.begin(), shape.size()), types, name);
+  }
+
+  void* array(PyObject* o, at::IntArrayRef shape, unsigned types, const char* name) {
     const Tensor* t = tensor(o);
-    if (!t || !(type_of(*t) & types) || !t->sizes().equals(at::IntArrayRef(shape.begin(), shape.size())) || !t->is_contiguous())
-      refuse(shape, types, name, "contiguous");
+    if (!t || !(type_of(*t) & types) || !t->sizes().equals(shape) || !t->is_contiguous()) refuse(shape, types, name, "contiguous");
     return address(*t, name);
   }
 
@@ -132,8 +140,7 @@ struct Args {
   // The address and row pitch of a 2-D tensor whose rows are contiguous and separate.
   void* pitched(PyObject* o, int64_t n, int64_t c, unsigned types, const char* name, int64_t* ld) {
     const Tensor* t = tensor(o);
-    if (!t || !(type_of(*t) & types) || t->dim() != 2 || t->size(0) != n || t->size(1) != c)
-      refuse({n, c}, types, name, "row-contiguous");
+    if (!t || !(type_of(*t) & types) || t->dim() != 2 || t->size(0) != n || t->size(1) != c) refuse({n, c}, types, name, "row-contiguous");
     *ld = c;
     if (!t->is_contiguous()) {
       if ((t->stride(1) != 1 && c != 1) || (t->stride(0) < c && n != 1)) refuse({n, c}, types, name, "row-contiguous");
@@ -381,13 +388,220 @@ PyObject* checkpoint_backward(ARGS) {  // qa, sa, qb, sb, dh, da, db, h, stream
   });
 }
 
+// The rows that a dispatch moves: x, x_rows, x_scales, row_scales, gates, row_gates.
+struct Moved {
+  int64_t d, ldx, R, scale_bytes = 0;
+  int32_t elem_bytes;
+  void *x, *x_rows, *x_scales = nullptr, *row_scales = nullptr, *gates = nullptr, *row_gates = nullptr;
+  Moved(Args& in, int64_t T, int64_t k, PyObject* px, PyObject* po, PyObject* pxs, PyObject* prs, PyObject* pg, PyObject* prg) {
+    const Tensor &t = matrix(px, kFloats | kE4m3, "x must be a 2-D fp32, bf16 or e4m3 tensor"), &o = matrix(po, 0, "x_rows must be 2-D");
+    const unsigned type = type_of(t);
+    d = t.size(1);
+    R = o.size(0);
+    elem_bytes = type == kE4m3 ? 1 : type == kBf16 ? 2 : 4;
+    x = in.pitched(px, T, d, type, "x", &ldx);
+    x_rows = in.rows(po, {R, d}, type, "x_rows");
+    if ((pxs == Py_None) != (prs == Py_None)) throw Refused{"x_scales and row_scales go together"};
+    if ((pg == Py_None) != (prg == Py_None)) throw Refused{"gates and row_gates go together"};
+    if (pxs != Py_None) {
+      if (type != kE4m3) throw Refused{"only e4m3 rows have scales"};
+      scale_bytes = moe_fp8_scale_cols(d);
+      x_scales = in.rows(pxs, {T, scale_bytes}, kScales, "x_scales");
+      row_scales = in.rows(prs, {R, scale_bytes}, kScales, "row_scales");
+    }
+    if (pg != Py_None) {
+      gates = in.rows(pg, {T, k}, kF32, "gates");
+      row_gates = in.rows(prg, {R}, kF32, "row_gates");
+    }
+  }
+};
+
+// The sort's arrays: idx, counts, slot_pos, row_slot.
+struct Sorted {
+  int64_t T, k, E;
+  int32_t idx_bytes;
+  void *idx, *counts, *slot_pos, *row_slot;
+  Sorted(Args& in, PyObject* pi, PyObject* pc, PyObject* ps, PyObject* pr) {
+    const Tensor &t = matrix(pi, kI32 | kI64, "idx must be a 2-D int32 or int64 tensor"), *c = tensor(pc);
+    if (!c || c->dim() != 1) throw Refused{"counts must be a 1-D int32 tensor"};
+    T = t.size(0);
+    k = t.size(1);
+    E = c->size(0);
+    if (k > INT32_MAX || E > INT32_MAX) throw Refused{"idx has too many columns, or counts too many values"};
+    idx_bytes = type_of(t) == kI64 ? 8 : 4;
+    idx = in.rows(pi, {T, k}, kI32 | kI64, "idx");
+    counts = in.rows(pc, {E}, kI32, "counts");
+    slot_pos = in.rows(ps, {T, k}, kI32, "slot_pos");
+    row_slot = in.maybe(pr, {T * k}, kI32, "row_slot");
+  }
+};
+
+#define I32(p) static_cast<int32_t*>(p)
+
+PyObject* rows_sort(ARGS) {  // idx, counts, slot_pos, row_slot, workspace, stream
+  return call<6>(args, nargs, [](Args& in, PyObject* const* p) {
+    const Sorted s(in, p[0], p[1], p[2], p[3]);
+    size_t n;
+    void *ws = in.maybe_bytes(p[4], &n), *st = in.stream(p[5]);
+    return unlocked([=] {
+      return moe_rows_sort(s.idx, s.idx_bytes, s.T, (int32_t)s.k, (int32_t)s.E, I32(s.counts), I32(s.slot_pos), I32(s.row_slot), ws, n, st);
+    });
+  });
+}
+
+PyObject* rows_gather(ARGS) {  // slot_pos, x, x_rows, x_scales, row_scales, gates, row_gates, stream
+  return call<8>(args, nargs, [](Args& in, PyObject* const* p) {
+    const Tensor& t = matrix(p[0], kI32, "slot_pos must be a 2-D int32 tensor");
+    const int64_t T = t.size(0), k = t.size(1);
+    if (k > INT32_MAX) throw Refused{"slot_pos has too many columns"};
+    void* pos = in.rows(p[0], {T, k}, kI32, "slot_pos");
+    const Moved m(in, T, k, p[1], p[2], p[3], p[4], p[5], p[6]);
+    void* st = in.stream(p[7]);
+    return unlocked([=] {
+      return moe_rows_gather(I32(pos), T, (int32_t)k, m.x, m.elem_bytes, m.d, m.ldx, m.R, m.x_rows, U8(m.x_scales), U8(m.row_scales),
+                             m.scale_bytes, FL(m.gates), FL(m.row_gates), st);
+    });
+  });
+}
+
+PyObject* rows_dispatch(ARGS) {  // idx, x, counts, slot_pos, x_rows, workspace, row_slot, x_scales, row_scales, gates, row_gates, stream
+  return call<12>(args, nargs, [](Args& in, PyObject* const* p) {
+    const Sorted s(in, p[0], p[2], p[3], p[6]);
+    const Moved m(in, s.T, s.k, p[1], p[4], p[7], p[8], p[9], p[10]);
+    size_t n;
+    void *ws = in.maybe_bytes(p[5], &n), *st = in.stream(p[11]);
+    return unlocked([=] {
+      return moe_rows_dispatch(s.idx, s.idx_bytes, s.T, (int32_t)s.k, (int32_t)s.E, I32(s.counts), I32(s.slot_pos), I32(s.row_slot), m.x,
+                               m.elem_bytes, m.d, m.ldx, m.R, m.x_rows, U8(m.x_scales), U8(m.row_scales), m.scale_bytes, FL(m.gates),
+                               FL(m.row_gates), ws, n, st);
+    });
+  });
+}
+
+PyObject* rows_combine(ARGS) {  // y_rows, slot_pos, out, gates, residual, stream
+  return call<6>(args, nargs, [](Args& in, PyObject* const* p) {
+    const Tensor &y = matrix(p[0], kFloats, "y_rows must be a 2-D fp32 or bf16 tensor"), &o = matrix(p[2], kFloats, "out must be a 2-D fp32 or bf16 tensor");
+    const Tensor& sp = matrix(p[1], kI32, "slot_pos must be a 2-D int32 tensor");
+    const int64_t R = y.size(0), d = y.size(1), T = sp.size(0), k = sp.size(1);
+    if (k > INT32_MAX) throw Refused{"slot_pos has too many columns"};
+    const unsigned ty = type_of(y), to = type_of(o);
+    void *py = in.rows(p[0], {R, d}, ty, "y_rows"), *pos = in.rows(p[1], {T, k}, kI32, "slot_pos"), *out = in.rows(p[2], {T, d}, to, "out");
+    void *g = in.maybe(p[3], {T, k}, kF32, "gates"), *res = in.maybe(p[4], {T, d}, to, "residual"), *st = in.stream(p[5]);
+    return unlocked(
+        [=] { return moe_rows_combine(py, moe_dtype_of(ty), R, I32(pos), FL(g), T, (int32_t)k, d, res, out, moe_dtype_of(to), st); });
+  });
+}
+
+PyObject* rows_combine_backward(ARGS) {  // dout, slot_pos, gates, y_rows, dy_rows, dgates, stream
+  return call<7>(args, nargs, [](Args& in, PyObject* const* p) {
+    const Tensor &o = matrix(p[0], kFloats, "dout must be a 2-D fp32 or bf16 tensor"), &sp = matrix(p[1], kI32, "slot_pos must be a 2-D int32 tensor");
+    const int64_t T = sp.size(0), k = sp.size(1), d = o.size(1);
+    if (k > INT32_MAX) throw Refused{"slot_pos has too many columns"};
+    PyObject* any = p[3] != Py_None ? p[3] : p[4];
+    if (any == Py_None) throw Refused{"y_rows or dy_rows is needed"};
+    const Tensor& y = matrix(any, kFloats, "y_rows and dy_rows must be 2-D fp32 or bf16 tensors");
+    const int64_t R = y.size(0);
+    const unsigned ty = type_of(y);
+    void *po = in.rows(p[0], {T, d}, kFloats, "dout"), *pos = in.rows(p[1], {T, k}, kI32, "slot_pos"), *g = in.maybe(p[2], {T, k}, kF32, "gates");
+    void *py = in.maybe(p[3], {R, d}, ty, "y_rows"), *dy = in.maybe(p[4], {R, d}, ty, "dy_rows"), *dg = in.maybe(p[5], {T, k}, kF32, "dgates");
+    void* st = in.stream(p[6]);
+    const int32_t dt = moe_dtype_of(type_of(o));
+    return unlocked(
+        [=] { return moe_rows_combine_backward(po, dt, I32(pos), FL(g), T, (int32_t)k, d, R, py, dy, moe_dtype_of(ty), FL(dg), st); });
+  });
+}
+
+// A Python sequence of n (n < 0: any number of) items.
+struct Items {
+  std::unique_ptr<PyObject, Release> seq;
+  Py_ssize_t n;
+  Items(PyObject* o, Py_ssize_t want, const char* name) : seq(PySequence_Fast(o, name)) {
+    if (!seq) {
+      PyErr_Clear();
+      throw Refused{std::string(name) + " must be a list"};
+    }
+    n = PySequence_Fast_GET_SIZE(seq.get());
+    if (want >= 0 && n != want) throw Refused{std::string(name) + " must have " + std::to_string(want) + " entries"};
+  }
+  PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq.get(), i); }
+};
+
+double real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PyError{};
+  return v;
+}
+
+// params, masters, grads, m, v, m_scales, v_scales, decays, lr, lr_device, beta1, beta2, eps, seed, grad_factor, steps, ticket, stream
+PyObject* adamw(ARGS) {
+  return call<18>(args, nargs, [](Args& in, PyObject* const* p) {
+    const Items ps(p[0], -1, "params");
+    const Items ws(p[1], ps.n, "masters"), gs(p[2], ps.n, "grads"), ms(p[3], ps.n, "m"), vs(p[4], ps.n, "v"), mss(p[5], ps.n, "m_scales"),
+        vss(p[6], ps.n, "v_scales"), ds(p[7], ps.n, "weight_decay");
+    std::vector<moe_adamw_tensor> list(ps.n);
+    for (Py_ssize_t i = 0; i < ps.n; ++i) {
+      moe_adamw_tensor& t = list[i];
+      const Tensor* q = tensor(ps[i]);
+      if (!q || !(type_of(*q) & kFloats) || !q->is_contiguous()) throw Refused{"params must be contiguous fp32 or bf16 tensors"};
+      const at::IntArrayRef shape = q->sizes();
+      const bool small = mss[i] != Py_None;
+      t.n = q->numel();
+      const int64_t blocks = (t.n + 127) / 128;
+      t.param = in.address(*q, "a parameter");
+      t.master = ws[i] == Py_None ? nullptr : FL(in.array(ws[i], shape, kF32, "a master"));
+      t.grad = in.array(gs[i], shape, kFloats, "a gradient");
+      t.m = in.array(ms[i], shape, small ? kE4m3 : kF32, "m");
+      t.v = in.array(vs[i], shape, small ? kE4m3 : kF32, "v");
+      t.m_scales = U8(in.maybe(mss[i], {blocks}, kScales, "m_scales"));
+      t.v_scales = U8(in.maybe(vss[i], {blocks}, kScales, "v_scales"));
+      t.weight_decay = (float)real(ds[i]);
+      t.param_dtype = moe_dtype_of(type_of(*q));
+      t.grad_dtype = moe_dtype_of(type_of(*tensor(gs[i])));
+    }
+    moe_adamw_config c{};
+    c.lr = real(p[8]);
+    c.lr_device = FL(in.maybe(p[9], {1}, kF32, "lr"));
+    c.beta1 = real(p[10]);
+    c.beta2 = real(p[11]);
+    c.eps = real(p[12]);
+    c.seed = PyLong_AsUnsignedLongLongMask(p[13]);
+    if (c.seed == (uint64_t)-1 && PyErr_Occurred()) throw PyError{};
+    float* factor = FL(in.maybe(p[14], {1}, kF32, "grad_factor"));
+    int64_t* steps = static_cast<int64_t*>(in.rows(p[15], {1}, kI64, "steps"));
+    uint32_t* ticket = reinterpret_cast<uint32_t*>(in.rows(p[16], {1}, kI32, "ticket"));
+    void* st = in.stream(p[17]);
+    if (ps.n > INT32_MAX) throw Refused{"too many tensors"};
+    return unlocked([&] { return moe_adamw(list.data(), (int32_t)list.size(), &c, factor, steps, ticket, st); });
+  });
+}
+
+PyObject* grad_norm(ARGS) {  // grads, norm, factor, max_norm, workspace, stream
+  return call<6>(args, nargs, [](Args& in, PyObject* const* p) {
+    const Items gs(p[0], -1, "grads");
+    std::vector<moe_grad_tensor> list(gs.n);
+    for (Py_ssize_t i = 0; i < gs.n; ++i) {
+      const Tensor* q = tensor(gs[i]);
+      if (!q || !(type_of(*q) & kFloats) || !q->is_contiguous()) throw Refused{"grads must be contiguous fp32 or bf16 tensors"};
+      list[i] = {in.address(*q, "a gradient"), q->numel(), moe_dtype_of(type_of(*q))};
+    }
+    float *norm = FL(in.rows(p[1], {1}, kF32, "norm")), *factor = FL(in.maybe(p[2], {1}, kF32, "factor"));
+    const float most = (float)real(p[3]);
+    size_t n;
+    void *ws = in.maybe_bytes(p[4], &n), *st = in.stream(p[5]);
+    if (gs.n > INT32_MAX) throw Refused{"too many tensors"};
+    return unlocked([&] { return moe_grad_norm(list.data(), (int32_t)list.size(), most, norm, factor, ws, n, st); });
+  });
+}
+
 #define FUNCTION(f) \
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr }
 PyMethodDef kFunctions[] = {FUNCTION(quantize),          FUNCTION(quantize_weights),   FUNCTION(rmsnorm),
                             FUNCTION(rmsnorm_backward),  FUNCTION(matmul),             FUNCTION(experts),
                             FUNCTION(layer),             FUNCTION(checkpoint_save),    FUNCTION(checkpoint_restore),
-                            FUNCTION(checkpoint_backward), {nullptr, nullptr, 0, nullptr}};
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fp8", "Calls of the 8-bit operators.", -1, kFunctions, nullptr, nullptr, nullptr,
+                            FUNCTION(checkpoint_backward), FUNCTION(rows_sort),    FUNCTION(rows_gather),
+                            FUNCTION(rows_dispatch),     FUNCTION(rows_combine),       FUNCTION(rows_combine_backward),
+                            FUNCTION(adamw),             FUNCTION(grad_norm),          {nullptr, nullptr, 0, nullptr}};
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fp8", "Calls of the 8-bit operators, the sorted rows and the optimiser's step.", -1, kFunctions, nullptr, nullptr, nullptr,
                        nullptr};
 
 }  // namespace

@@ -134,7 +134,7 @@ extern "C" {
 
 size_t moe_rows_workspace(int64_t T, int32_t k, int32_t n_experts) {
   if (T < 0 || k < 1 || k > rows::kMaxK || T > INT32_MAX / k || n_experts < 1 || n_experts > rows::kMaxSortExperts) return 0;
-  return rows::counts_first(T * k) ? ((size_t)rows::kCountBlocks * n_experts * sizeof(int32_t) + 255) / 256 * 256 : 0;
+  return rows::counts_first(T * k) ? ((size_t)rows::kCountBlocks * rows::count_pitch(n_experts) * sizeof(int32_t) + 255) / 256 * 256 : 0;
 }
 
 moe_status moe_rows_sort(const void* idx, int32_t idx_bytes, int64_t T, int32_t k, int32_t n_experts, int32_t* counts,

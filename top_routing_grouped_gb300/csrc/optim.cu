@@ -219,7 +219,7 @@ __device__ __forceinline__ float sqrt_fast(float x) {
 // ------------------------------------------------------------------ the step
 
 struct Step {
-  float lr, beta1, beta2, c1, c2, eps, log1, log2;  // c: 1 - beta, log: ln of beta
+  float lr, c1, c2, eps, log1, log2;  // c: 1 - beta, log: ln of beta
   const float* lr_device;
   const float* factor;
   int64_t* steps;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const float bc1 = -expm1f((float)taken * s.log1), bc2 = -expm1f((float)taken * s.log2);
     const float lr = s.lr_device ? *s.lr_device : s.lr;
     const float rate = lr / bc1, root = rsqrtf(bc2), keep = 1.f - lr * t.weight_decay;
-    const float b1 = s.beta1, b2 = s.beta2, c1 = s.c1, c2 = s.c2;
+    const float c1 = s.c1, c2 = s.c2;
     const uint32_t key = mix(mix(mix(mix(s.seed_low) + s.seed_high) + (uint32_t)taken) + (t.index_flags >> kIndexShift));
     for (int64_t i0 = begin; i0 < end; i0 += kTile) {
       const int64_t i = i0 + threadIdx.x * kPer;
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const float x = g.v[j] * f;
-        m.v[j] = fmaf(b1, m.v[j], c1 * x);
-        v.v[j] = fmaf(b2, v.v[j], c2 * x * x);
+        m.v[j] = fmaf(c1, x - m.v[j], m.v[j]);  // b1 m + c1 x, with one rounding of m's size
+        v.v[j] = fmaf(c2, fmaf(x, x, -v.v[j]), v.v[j]);
         r.v[j] = sqrt_fast(v.v[j]);
         w.v[j] = fmaf(keep, w.v[j], -rate * __fdividef(m.v[j], fmaf(r.v[j], root, s.eps)));
       }
@@ -427,8 +427,6 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   Step s{};
   s.lr = (float)cfg.lr;
   s.lr_device = cfg.lr_device;
-  s.beta1 = (float)cfg.beta1;
-  s.beta2 = (float)cfg.beta2;
   s.c1 = (float)(1 - cfg.beta1);
   s.c2 = (float)(1 - cfg.beta2);
   s.eps = (float)cfg.eps;

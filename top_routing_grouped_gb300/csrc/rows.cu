@@ -11,6 +11,10 @@ namespace rows {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kVecs = 128;             // vectors of a row that a warp moves at a time, four a lane
+constexpr int kMaxPositions = 4096;    // that a CTA keeps
+constexpr int kSortCtas = 152 * 2;
+constexpr int64_t kSortFew = 4096;
 constexpr unsigned kAll = 0xffffffffu;
 
 // ------------------------------------------------------------------ sort and gather
@@ -26,116 +30,63 @@ __device__ __forceinline__ int expert_of(const Args& a, int64_t slot) {
   }
 }
 
-// table[e] += the slots of expert e among [from, to), by all threads of the block; `also`: a second table
-// for those below `below`.  Lanes of one expert add once, together.
-template <bool kIdx64>
-__device__ __forceinline__ void count(const Args& a, int64_t from, int64_t to, int* table, int64_t below, int* also) {
+// The first expert's, second's ... slots among [from, to) by the block's threads: those below `split` into
+// `low`, the others into `high`.
+template <bool kIdx64, int kThreadsOf>
+__device__ __forceinline__ void count(const Args& a, int64_t from, int64_t to, int64_t split, int* low, int* high) {
   constexpr int kU = 8;  // loads in flight
-  for (int64_t i0 = from; i0 < to; i0 += kU * kThreads) {
+  for (int64_t i0 = from + threadIdx.x; i0 < to; i0 += kU * kThreadsOf) {
     int e[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int64_t i = i0 + u * kThreads + threadIdx.x;
+      const int64_t i = i0 + u * kThreadsOf;
       e[u] = i < to ? expert_of<kIdx64>(a, i) : -1;
     }
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t i = i0 + u * kThreads + threadIdx.x;
-      if (i0 + u * kThreads >= to) break;  // the same for the whole block
-      const unsigned same = __match_any_sync(kAll, e[u]);
-      const unsigned early = __ballot_sync(kAll, i < below) & same;
-      if (e[u] >= 0 && (int)(threadIdx.x & 31) == __ffs(same) - 1) {
-        atomicAdd(&table[e[u]], __popc(same));
-        if (also && early) atomicAdd(&also[e[u]], __popc(early));
-      }
-    }
+    for (int u = 0; u < kU; ++u)
+      if (e[u] >= 0) atomicAdd((i0 + u * kThreadsOf < split ? low : high) + e[u], 1);
   }
 }
 
-int64_t count_slots(int64_t N) { return (N + kCountBlocks - 1) / kCountBlocks; }
+// A block's own slots s0 .. s0 + own: each warp ranks a run of them, 32 at a time, behind the warps before it,
+// so that the order is that of the slots whatever the timing.
+template <bool kIdx64, int kW>
+struct Ranks {
+  static constexpr int kThreadsOf = kW * 32, kEach = (kMaxSortExperts + kThreadsOf - 1) / kThreadsOf;
+  int w0, w1;        // the warp's run
+  int e;             // the expert of its first 32 slots, and the lanes of the same one
+  unsigned same;
 
-// counted[b][e]: the slots of expert e in the b-th block of per_block slots.
-template <bool kIdx64>
-__global__ void __launch_bounds__(kThreads) count_kernel(Args a, int64_t per_block, int32_t* counted) {
-  extern __shared__ int table[];
-  for (int e = threadIdx.x; e < a.E; e += kThreads) table[e] = 0;
-  pdl_wait();
-  pdl_launch_dependents();
-  __syncthreads();
-  const int64_t N = a.T * a.k, from = blockIdx.x * per_block;
-  count<kIdx64>(a, from, min(from + per_block, N), table, 0, nullptr);
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kThreads) counted[(int64_t)blockIdx.x * a.E + e] = table[e];
-}
-
-// A counting sort in one pass, and the rows' way with it.  Each CTA takes `tokens` tokens (grid.y: a share
-// of their columns).  Where its slots' rows begin follows from the experts' totals and from the slots
-// before its own: of up to 16384 slots it counts them all by itself (64 KB out of L2, 1 us, where another launch
-// takes 2); of more it adds up what count_kernel counted in 64 blocks and counts the rest of its own
-// block.  Inside the CTA each warp ranks a run of slots, 32 at a time, behind the warps before it, so that
-// the order is that of the slots whatever the timing.
-template <typename V, bool kSort, bool kIdx64>
-__global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int64_t vecs_y, const int32_t* counted, int64_t per_block) {
-  extern __shared__ int shared[];
-  __shared__ int warp_sum[kWarps];
-  int* pos = shared;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
-  const int64_t t0 = (int64_t)blockIdx.x * tokens, s0 = t0 * a.k, N = a.T * a.k;
-  const int nt = (int)min((int64_t)tokens, a.T - t0), own = nt * a.k;
-  const bool first = blockIdx.y == 0;  // writes what does not depend on the columns
-
-  if constexpr (!kSort) {
-    pdl_wait();
-    pdl_launch_dependents();
-    for (int i = threadIdx.x; i < own; i += kThreads) {
-      const int p = a.slot_pos[s0 + i];
-      pos[i] = p;
-      if (first && a.gates && p >= 0 && p < a.R) a.row_gates[p] = a.gates[s0 + i];
-    }
-  } else {
-    int *total = shared + tokens * a.k, *before = total + E, *of_warp = before + E;  // [E], [E], [kWarps][E]
-    for (int e = threadIdx.x; e < (2 + kWarps) * E; e += kThreads) total[e] = 0;
-    pdl_wait();
-    pdl_launch_dependents();
-    __syncthreads();
-    if (counted) {
-      const int blocks = (int)((N + per_block - 1) / per_block), mine = (int)(s0 / per_block);
-      const int groups = E < kThreads ? kThreads / E : 1;
-      for (int i = threadIdx.x; i < groups * E; i += kThreads) {
-        const int e = i % E, g = i / E;
-        int all = 0, less = 0;
-#pragma unroll 8
-        for (int b = g; b < blocks; b += groups) {
-          const int c = counted[(int64_t)b * E + e];
-          all += c;
-          less += b < mine ? c : 0;
-        }
-        if (all) atomicAdd(&total[e], all);
-        if (less) atomicAdd(&before[e], less);
-      }
-      count<kIdx64>(a, mine * per_block, s0, before, 0, nullptr);
-    } else {
-      count<kIdx64>(a, 0, N, total, s0, before);
-    }
-    // its own slots, by warp
-    const int run = (own + kThreads - 1) / kThreads * 32, w0 = warp * run, w1 = min(w0 + run, own);
-    int* mine = of_warp + warp * E;
+  // table [kW][E], zeros: the warps' own counts, each by its warp.
+  __device__ __forceinline__ void count_own(const Args& a, int64_t s0, int own, int* table) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = (own + kThreadsOf - 1) / kThreadsOf * 32;
+    int* mine = table + warp * a.E;
+    w0 = warp * run;
+    w1 = min(w0 + run, own);
+    e = -1;
+    same = 0;
     for (int i0 = w0; i0 < w1; i0 += 32) {
-      const int e = i0 + lane < w1 ? expert_of<kIdx64>(a, s0 + i0 + lane) : -1;
-      const unsigned same = __match_any_sync(kAll, e);
-      if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+      const int x = i0 + lane < w1 ? expert_of<kIdx64>(a, s0 + i0 + lane) : -1;
+      const unsigned m = __match_any_sync(kAll, x);
+      if (x >= 0 && lane == __ffs(m) - 1) mine[x] += __popc(m);
+      if (i0 == w0) e = x, same = m;
       __syncwarp();
     }
+  }
+
+  // put(i, p) for each of the slots.  `before` and `rest` [E] hold each expert's slots before s0 and from there on;
+  // all(e, n) is called with each expert's number.  Returns the number of all rows.  Syncs the block first.
+  template <typename Put, typename All>
+  __device__ __forceinline__ int rank(const Args& a, int64_t s0, const int* before, const int* rest, int* table, Put put, All all) {
+    __shared__ int warp_sum[kW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
     __syncthreads();
-    if (first && blockIdx.x == 0)
-      for (int e = threadIdx.x; e < E; e += kThreads) a.counts[e] = total[e];
-    // exclusive scan of the totals: four experts a thread at most
-    const int each = (E + kThreads - 1) / kThreads;
-    int v[kMaxSortExperts / kThreads], sum = 0;
+    const int each = (E + kThreadsOf - 1) / kThreadsOf;
+    int v[kEach], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxSortExperts / kThreads; ++i) {
-      const int e = threadIdx.x * each + i;
-      v[i] = i < each && e < E ? total[e] : 0;
+    for (int i = 0; i < kEach; ++i) {
+      const int x = threadIdx.x * each + i;
+      v[i] = i < each && x < E ? before[x] + rest[x] : 0;
       sum += v[i];
     }
     int incl = sum;
@@ -148,70 +99,194 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
     __syncthreads();
     int at = incl - sum, kept = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) at += warp_sum[w];
-      kept += warp_sum[w];
+    for (int w = 0; w < kW; ++w) {
+      const int n = warp_sum[w];
+      at += w < warp ? n : 0;
+      kept += n;
     }
 #pragma unroll
-    for (int i = 0; i < kMaxSortExperts / kThreads; ++i) {
-      const int e = threadIdx.x * each + i;
-      if (i < each && e < E) {
-        int next = at + before[e];
+    for (int i = 0; i < kEach; ++i) {
+      const int x = threadIdx.x * each + i;
+      if (i < each && x < E) {
+        all(x, v[i]);
+        int n[kW], next = at + before[x];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const int n = of_warp[w * E + e];
-          of_warp[w * E + e] = next;
-          next += n;
+        for (int w = 0; w < kW; ++w) n[w] = table[w * E + x];
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          table[w * E + x] = next;
+          next += n[w];
         }
         at += v[i];
       }
     }
     __syncthreads();
+    int* mine = table + warp * E;
     for (int i0 = w0; i0 < w1; i0 += 32) {
       const int i = i0 + lane;
-      const int e = i < w1 ? expert_of<kIdx64>(a, s0 + i) : -1;
-      const unsigned same = __match_any_sync(kAll, e);
-      int p = -1;
-      if (e >= 0) p = mine[e] + __popc(same & ((1u << lane) - 1));
-      __syncwarp();
-      if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-      __syncwarp();
-      if (i < w1) {
-        pos[i] = p;
-        if (first) {
-          a.slot_pos[s0 + i] = p;
-          if (p >= 0) {
-            if (a.row_slot) a.row_slot[p] = (int)(s0 + i);
-            if (a.gates && p < a.R) a.row_gates[p] = a.gates[s0 + i];
-          }
-          if (a.row_slot && s0 + i >= kept) a.row_slot[s0 + i] = -1;
-        }
+      int x = e;
+      unsigned m = same;
+      if (i0 > w0) {
+        x = i < w1 ? expert_of<kIdx64>(a, s0 + i) : -1;
+        m = __match_any_sync(kAll, x);
       }
+      int p = -1;
+      if (x >= 0) p = mine[x] + __popc(m & ((1u << lane) - 1));
+      __syncwarp();
+      if (x >= 0 && lane == __ffs(m) - 1) mine[x] += __popc(m);
+      __syncwarp();
+      if (i < w1) put(i, p);
+    }
+    return kept;
+  }
+};
+
+// What a sort writes of slot s, whose row is p.
+__device__ __forceinline__ void write_slot(const Args& a, int64_t s, int p) {
+  a.slot_pos[s] = p;
+  if (p < 0) return;
+  if (a.row_slot) a.row_slot[p] = (int)s;
+  if (a.gates && p < a.R) a.row_gates[p] = a.gates[s];
+}
+
+// Many slots: blocks of them, one a CTA, are counted in one launch and ranked in a second one, whose CTAs each
+// add up the counts of the blocks before theirs.
+constexpr int kSortWarps = 16, kSortThreads = kSortWarps * 32;
+
+// Slots of a block: one for each thread, more where kCountBlocks blocks do not do.
+int64_t count_slots(int64_t N) {
+  const int64_t n = (N + kCountBlocks * 32 - 1) / (kCountBlocks * 32) * 32;
+  return n < kSortThreads ? kSortThreads : n;
+}
+
+template <bool kIdx64>
+__global__ void __launch_bounds__(kSortThreads) count_kernel(Args a, int64_t per_block, int32_t* counted) {
+  extern __shared__ int shared[];
+  const int pitch = count_pitch(a.E);
+  for (int e = threadIdx.x; e < pitch; e += kSortThreads) shared[e] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  __syncthreads();
+  const int64_t from = blockIdx.x * per_block, to = min(from + per_block, a.T * a.k);
+  count<kIdx64, kSortThreads>(a, from, to, to, shared, nullptr);
+  __syncthreads();
+  for (int e = threadIdx.x; e < pitch; e += kSortThreads) counted[(int64_t)blockIdx.x * pitch + e] = shared[e];
+}
+
+// Starts while count_kernel runs, which has waited for what was before it: the choice is there, only the counts
+// are not.
+template <bool kIdx64>
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(Args a, int64_t per_block, const int32_t* counted) {
+  extern __shared__ int shared[];
+  const int E = a.E, pitch = count_pitch(E), quads = pitch / 4;
+  int *before = shared, *rest = before + pitch, *table = rest + pitch;
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < 2 * pitch + kSortWarps * E; i += kSortThreads) shared[i] = 0;
+  __syncthreads();
+  const int64_t N = a.T * a.k, s0 = blockIdx.x * per_block;
+  const int own = (int)min(per_block, N - s0);
+  Ranks<kIdx64, kSortWarps> ranks;
+  ranks.count_own(a, s0, own, table);
+  pdl_wait();
+  const int groups = quads < kSortThreads ? kSortThreads / quads : 1;
+  for (int i = threadIdx.x; i < groups * quads; i += kSortThreads) {
+    const int q = i % quads;
+    int4 less = make_int4(0, 0, 0, 0), more = less;
+#pragma unroll 16
+    for (int b = i / quads; b < (int)gridDim.x; b += groups) {
+      const int4 c = *reinterpret_cast<const int4*>(counted + (int64_t)b * pitch + 4 * q);
+      int4& to = b < (int)blockIdx.x ? less : more;
+      to.x += c.x, to.y += c.y, to.z += c.z, to.w += c.w;
+    }
+    const int l[4] = {less.x, less.y, less.z, less.w}, m[4] = {more.x, more.y, more.z, more.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (l[j]) atomicAdd(&before[4 * q + j], l[j]);
+      if (m[j]) atomicAdd(&rest[4 * q + j], m[j]);
     }
   }
-  __syncthreads();
-  if (a.row_bytes == 0) return;
+  const int kept = ranks.rank(
+      a, s0, before, rest, table, [&](int i, int p) { write_slot(a, s0 + i, p); },
+      [&](int e, int n) {
+        if (blockIdx.x == 0) a.counts[e] = n;
+      });
+  if (a.row_slot)
+    for (int64_t p = max(s0, (int64_t)kept) + threadIdx.x; p < s0 + own; p += kSortThreads) a.row_slot[p] = -1;
+}
 
-  // the rows: a warp takes 32 kU vectors of one token, reads them once and writes them to each of its rows
-  constexpr int kU = 4;
+// The rows' way.  Each CTA takes `tokens` tokens (grid.y: a share of their columns).  With kSort, for few slots,
+// it first sorts them: each CTA counts all of them by itself, out of L2, and ranks its own.  A warp moves kVecs
+// vectors of a token at a time: it reads them once and writes them to each of the token's rows.  The first ones are
+// on their way while the positions are found; `early`: even while the previous kernel, a sort of the same call that
+// has waited for what was before it, ends.
+template <typename V, bool kSort, bool kIdx64>
+__global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int64_t vecs_y, bool early) {
+  extern __shared__ int shared[];
+  int* pos = shared;  // [tokens * k]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t0 = (int64_t)blockIdx.x * tokens, s0 = t0 * a.k;
+  const int nt = (int)min((int64_t)tokens, a.T - t0), own = nt * a.k;
+  const bool first = blockIdx.y == 0;  // writes what does not depend on the columns
+
+  constexpr int kU = kVecs / 32;
   const int64_t vecs = a.row_bytes / (int64_t)sizeof(V), v_first = blockIdx.y * vecs_y, v_end = min(v_first + vecs_y, vecs);
-  const int segs = (int)((v_end - v_first + 32 * kU - 1) / (32 * kU));
-  for (int unit = warp; unit < nt * segs; unit += kWarps) {
-    const int t = unit / segs;
-    const int64_t v0 = v_first + (int64_t)(unit - t * segs) * 32 * kU + lane;
+  const int segs = (int)((v_end - v_first + kVecs - 1) / kVecs), units = nt * segs;
+  int t, unit = warp;
+  int64_t v0;
+  V buf[kU];
+  const auto fetch = [&] {
+    t = unit / segs;
+    v0 = v_first + (int64_t)(unit - t * segs) * kVecs + lane;
     const V* src = reinterpret_cast<const V*>(a.x + (t0 + t) * a.ld_bytes);
-    V buf[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u)
       if (v0 + u * 32 < v_end) buf[u] = __ldcs(src + v0 + u * 32);
+  };
+
+  if constexpr (!kSort) {
+    if (early && unit < units) fetch();
+    pdl_wait();
+    pdl_launch_dependents();
+    if (!early && unit < units) fetch();
+    for (int i = threadIdx.x; i < own; i += kThreads) {
+      const int p = a.slot_pos[s0 + i];
+      pos[i] = p;
+      if (first && a.gates && p >= 0 && p < a.R) a.row_gates[p] = a.gates[s0 + i];
+    }
+  } else {
+    int *before = shared + tokens * a.k, *rest = before + a.E, *table = rest + a.E;
+    for (int i = threadIdx.x; i < (2 + kWarps) * a.E; i += kThreads) before[i] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (unit < units) fetch();
+    __syncthreads();
+    Ranks<kIdx64, kWarps> ranks;
+    ranks.count_own(a, s0, own, table);
+    count<kIdx64, kThreads>(a, 0, a.T * a.k, s0, before, rest);
+    const int kept = ranks.rank(
+        a, s0, before, rest, table,
+        [&](int i, int p) {
+          pos[i] = p;
+          if (first) write_slot(a, s0 + i, p);
+        },
+        [&](int e, int n) {
+          if (first && blockIdx.x == 0) a.counts[e] = n;
+        });
+    if (first && a.row_slot)
+      for (int64_t p = max(s0, (int64_t)kept) + threadIdx.x; p < s0 + own; p += kThreads) a.row_slot[p] = -1;
+  }
+  __syncthreads();
+  while (unit < units) {
     for (int j = 0; j < a.k; ++j) {
       const int p = pos[t * a.k + j];
       if (p < 0 || p >= a.R) continue;
       V* dst = reinterpret_cast<V*>(a.x_rows + p * a.row_bytes);
 #pragma unroll
       for (int u = 0; u < kU; ++u)
-        if (v0 + u * 32 < v_end) dst[v0 + u * 32] = buf[u];
+        if (v0 + u * 32 < v_end) __stcs(dst + v0 + u * 32, buf[u]);
     }
+    unit += kWarps;
+    if (unit < units) fetch();
   }
   if (a.words && first) {
     const int64_t n = nt * a.words;
@@ -227,50 +302,51 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
 }
 
 template <typename V, bool kSort, bool kIdx64>
-cudaError_t launch_as(const Args& a, int32_t* counted, cudaStream_t st) {
-  constexpr int64_t kCtas = 152 * 8;
-  const int64_t vecs = a.row_bytes / (int64_t)sizeof(V), segs = (vecs + 127) / 128;  // as the kernel's kU = 4 has them
-  // tokens a CTA: enough CTAs to fill the GPU several times, of eight warps' work each; a sort's shared
-  // memory holds 4096 positions.  Without rows to move: a slot for each thread.
-  int64_t tokens = (a.T + kCtas - 1) / kCtas;
-  const int64_t least = segs ? (8 + segs - 1) / segs : (kThreads + a.k - 1) / a.k;
-  if (tokens < least) tokens = least;
-  if (tokens > 4096 / a.k) tokens = 4096 / a.k;
+cudaError_t launch_as(const Args& a, bool early, cudaStream_t st) {
+  const int64_t vecs = a.row_bytes / (int64_t)sizeof(V), segs = (vecs + kVecs - 1) / kVecs;
+  // Tokens a CTA: a segment for each warp; where each CTA counts all slots, no more CTAs than kSortCtas.
+  int64_t tokens = segs ? (kWarps + segs - 1) / segs : (kThreads + a.k - 1) / a.k;
+  if (kSort && tokens < (a.T + kSortCtas - 1) / kSortCtas) tokens = (a.T + kSortCtas - 1) / kSortCtas;
+  if (tokens > kMaxPositions / a.k) tokens = kMaxPositions / a.k;
   if (tokens > a.T) tokens = a.T;
   const int64_t gx = (a.T + tokens - 1) / tokens;
   // columns of a few tokens' long rows are shared out
   int64_t gy = 1, vecs_y = vecs;
-  if (segs > 0 && gx < kCtas / 2) {
-    gy = (tokens * segs + 7) / 8;
-    if (gy > kCtas / 2 / gx) gy = kCtas / 2 / gx;
+  if (segs > 0 && gx < kSortCtas) {
+    gy = (tokens * segs + kWarps - 1) / kWarps;
+    if (gy > kSortCtas / gx) gy = kSortCtas / gx;
     if (gy > segs) gy = segs;
-    vecs_y = (segs + gy - 1) / gy * 128;
+    vecs_y = (segs + gy - 1) / gy * kVecs;
     gy = (vecs + vecs_y - 1) / vecs_y;
   }
-  size_t smem = (size_t)tokens * a.k * sizeof(int);
-  int64_t per_block = 0;
-  if constexpr (kSort) {
-    smem += (size_t)(2 + kWarps) * a.E * sizeof(int);
-    if (counted) {
-      per_block = count_slots(a.T * a.k);
-      const int64_t blocks = (a.T * a.k + per_block - 1) / per_block;
-      const cudaError_t e = launch_kernel(count_kernel<kIdx64>, dim3((unsigned)blocks), dim3(kThreads), (size_t)a.E * sizeof(int), st,
-                                          true, 1, a, per_block, counted);
-      if (e != cudaSuccess) return e;
-    }
-  }
+  const size_t smem = ((size_t)tokens * a.k + (kSort ? (size_t)(2 + kWarps) * a.E : 0)) * sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(rows_kernel<V, kSort, kIdx64>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
     if (e != cudaSuccess) return e;
   }
-  return launch_kernel(rows_kernel<V, kSort, kIdx64>, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), smem, st, true, 1, a,
-                       (int)tokens, vecs_y, (const int32_t*)counted, per_block);
+  return launch_kernel(rows_kernel<V, kSort, kIdx64>, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), smem, st, true, 1, a, (int)tokens,
+                       vecs_y, early);
 }
 
 template <typename V>
-cudaError_t launch_vec(const Args& a, int32_t* counted, cudaStream_t st) {
-  if (!a.idx) return launch_as<V, false, false>(a, nullptr, st);
-  return a.idx64 ? launch_as<V, true, true>(a, counted, st) : launch_as<V, true, false>(a, counted, st);
+cudaError_t launch_vec(const Args& a, bool sort, cudaStream_t st) {
+  if (!sort) return launch_as<V, false, false>(a, a.idx != nullptr, st);
+  return a.idx64 ? launch_as<V, true, true>(a, false, st) : launch_as<V, true, false>(a, false, st);
+}
+
+template <bool kIdx64>
+cudaError_t launch_sort(const Args& a, int32_t* counted, cudaStream_t st) {
+  const int64_t N = a.T * a.k, per_block = count_slots(N);
+  const dim3 grid((unsigned)((N + per_block - 1) / per_block)), block(kSortThreads);
+  const size_t pitch = (size_t)count_pitch(a.E) * sizeof(int);
+  cudaError_t e = launch_kernel(count_kernel<kIdx64>, grid, block, pitch, st, true, 1, a, per_block, counted);
+  if (e != cudaSuccess) return e;
+  const size_t smem = 2 * pitch + (size_t)kSortWarps * a.E * sizeof(int);
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(sort_kernel<kIdx64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 + kSortWarps) * kMaxSortExperts * sizeof(int));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(sort_kernel<kIdx64>, grid, block, smem, st, true, 1, a, per_block, (const int32_t*)counted);
 }
 
 // ------------------------------------------------------------------ combine
@@ -288,7 +364,7 @@ struct Values {
   }
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) reinterpret_cast<Part*>(p)[i] = part[i];
+    for (int i = 0; i < kParts; ++i) __stcs(reinterpret_cast<Part*>(p) + i, part[i]);
   }
   __device__ __forceinline__ float get(int i) const {
     const T v = reinterpret_cast<const T*>(part)[i];
@@ -303,7 +379,7 @@ struct Values {
 
 // One warp for 32 V columns of one token: up to four rows in flight, summed in the slots' order.
 template <typename Ty, typename To, int V>
-__global__ void __launch_bounds__(kThreads) combine_kernel(const Ty* y, int64_t R, const int32_t* slot_pos, const float* gates,
+__global__ void __launch_bounds__(kThreads, 6) combine_kernel(const Ty* y, int64_t R, const int32_t* slot_pos, const float* gates,
                                                            int64_t T, int k, int64_t d, unsigned segs, const To* residual, To* out) {
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -463,16 +539,23 @@ int values_at_once(int most, int64_t d, std::initializer_list<std::pair<const vo
 
 }  // namespace
 
-// One launch for all is the faster up to here (see rows_kernel).
-bool counts_first(int64_t N) { return N > 16384; }
+bool counts_first(int64_t N) { return N > kSortFew; }
 
-cudaError_t launch_rows(const Args& a, int32_t* counted, cudaStream_t st) {
+cudaError_t launch_rows(const Args& args, int32_t* counted, cudaStream_t st) {
+  Args a = args;
+  bool sort = a.idx != nullptr;
+  if (sort && counted) {
+    const cudaError_t e = a.idx64 ? launch_sort<true>(a, counted, st) : launch_sort<false>(a, counted, st);
+    if (e != cudaSuccess || a.row_bytes == 0) return e;
+    a.gates = nullptr;  // they are on their rows
+    sort = false;
+  }
   const uintptr_t b = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.x_rows) | (uintptr_t)a.row_bytes | (uintptr_t)a.ld_bytes;
-  if (b % 16 == 0) return launch_vec<uint4>(a, counted, st);
-  if (b % 8 == 0) return launch_vec<uint2>(a, counted, st);
-  if (b % 4 == 0) return launch_vec<uint32_t>(a, counted, st);
-  if (b % 2 == 0) return launch_vec<uint16_t>(a, counted, st);
-  return launch_vec<uint8_t>(a, counted, st);
+  if (b % 16 == 0) return launch_vec<uint4>(a, sort, st);
+  if (b % 8 == 0) return launch_vec<uint2>(a, sort, st);
+  if (b % 4 == 0) return launch_vec<uint32_t>(a, sort, st);
+  if (b % 2 == 0) return launch_vec<uint16_t>(a, sort, st);
+  return launch_vec<uint8_t>(a, sort, st);
 }
 
 using bf16 = __nv_bfloat16;

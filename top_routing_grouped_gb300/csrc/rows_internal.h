@@ -8,7 +8,8 @@ namespace rows {
 
 constexpr int kMaxK = 64;
 constexpr int kMaxSortExperts = 1024;
-constexpr int kCountBlocks = 64;  // blocks of slots that a sort's first launch counts
+constexpr int kCountBlocks = 152;  // most blocks of slots that a sort's first launch counts
+__host__ __device__ inline int count_pitch(int E) { return (E + 3) / 4 * 4; }  // words of a block's counts
 
 struct Args {
   const void* idx;  // null: the positions are given in slot_pos
@@ -26,7 +27,7 @@ struct Args {
   float* row_gates;
 };
 
-// Whether a sort of N slots counts them in a launch of its own, into [kCountBlocks, E] words.
+// Whether a sort of N slots counts them in a launch of its own, into [kCountBlocks, count_pitch(E)] words.
 bool counts_first(int64_t N);
 cudaError_t launch_rows(const Args& a, int32_t* counted, cudaStream_t st);
 

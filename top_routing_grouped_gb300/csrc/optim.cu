@@ -5,6 +5,9 @@
 // an argument of the kernel, so that a call needs no copy to the device.
 #include <math.h>
 
+#include <initializer_list>
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "fp8_common.cuh"
 #include "optim_internal.h"
@@ -13,10 +16,18 @@ namespace moe {
 namespace optim {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPer = 8;                    // consecutive values of a thread; 16 threads make a block of 128
-constexpr int kTile = kThreads * kPer;     // values of a CTA at a time
-constexpr int kChunk = 4 * kTile;          // values of a CTA
+constexpr int kPer = 8;  // consecutive values of a thread; 16 threads make a block of 128
+
+// The step's CTAs, for moments in 32 or in 8 bits: threads, CTAs an SM, values at a time (a tile) and the most tiles
+// (a power of two).  Moments in 32 bits: HBM does not wait for anyone (403 M values with masters: 1741 us with 256
+// threads, 3 CTAs and 2 to 4 tiles; 1730 with 2 CTAs, 1766 with 8 tiles, 1769-1790 with 128 threads).  In 8 bits the
+// warps an SM holds count (805 M values, no masters: 128 threads, 9 CTAs of 56 registers 1534 us, 8 of 64 1561, 7 of
+// 72 1595; 256 threads 4 CTAs 1571, 3 1696).
+template <bool kSmall>
+struct Shape {
+  static constexpr int kThreads = kSmall ? 128 : 256, kCtas = kSmall ? 9 : 3, kTile = kThreads * kPer, kTiles = kSmall ? 64 : 4;
+};
+constexpr int kMostChunk = Shape<true>::kTiles * Shape<true>::kTile, kLeastChunk = Shape<false>::kTiles * Shape<false>::kTile;
 constexpr unsigned kAll = 0xffffffffu;
 
 // ------------------------------------------------------------------ the lists
@@ -33,13 +44,16 @@ struct Entry {  // 72 bytes
 };
 enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kVec = 4, kIndexShift = 3 };  // kVec: every array on 16 bytes (8-bit ones: 8)
 
-// A launch's chunks are fewer than 2^31, whatever its tensors.
-static_assert((int64_t)kMostTensors * (kMostValues / kChunk) < INT32_MAX, "too many chunks");
+// A chunk, what a CTA takes of a tensor, has 1 to kTiles tiles: so many that there are kFewChunks of them and
+// more.  A launch's chunks are then fewer than 2^31, whatever its tensors.
+constexpr int64_t kFewChunks = 152 * 12;
+static_assert((int64_t)kMostTensors * (kMostValues / kLeastChunk) < INT32_MAX, "too many chunks");
 
 template <int kN>
 struct Batch {
   Entry e[kN];
   int n;
+  int chunk;               // values
   uint32_t first[kN + 1];  // the chunks before each tensor
 };
 
@@ -74,99 +88,36 @@ struct F8 {
   float v[kPer];
 };
 
-__device__ __forceinline__ F8 load_f32(const float* p, int left, bool vec) {
+// The first `left` of eight values from i on, the others 0.
+__device__ __forceinline__ F8 load(const void* p, int64_t i, bool bf16, int left) {
   F8 r;
-  if (vec && left >= kPer) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w, r.v[4] = b.x, r.v[5] = b.y, r.v[6] = b.z, r.v[7] = b.w;
-  } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) r.v[i] = i < left ? p[i] : 0.f;
-  }
+  for (int j = 0; j < kPer; ++j)
+    r.v[j] = j >= left ? 0.f : bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i + j] << 16) : static_cast<const float*>(p)[i + j];
   return r;
 }
 
-__device__ __forceinline__ F8 load_bf16(const uint16_t* p, int left, bool vec) {
+__device__ __forceinline__ F8 load_e4m3(const uint8_t* p, int left, float by) {
   F8 r;
-  if (vec && left >= kPer) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) r.v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) r.v[i] = i < left ? __uint_as_float((uint32_t)p[i] << 16) : 0.f;
-  }
+  for (int j = 0; j < kPer; ++j) r.v[j] = j < left ? fp8::unpack_e4m3x2(p[j]).x * by : 0.f;
   return r;
 }
 
-__device__ __forceinline__ F8 load(const void* p, int64_t i, bool bf16, int left, bool vec) {
-  return bf16 ? load_bf16(static_cast<const uint16_t*>(p) + i, left, vec) : load_f32(static_cast<const float*>(p) + i, left, vec);
-}
-
-__device__ __forceinline__ void store_f32(float* p, const F8& r, int left, bool vec) {
-  if (vec && left >= kPer) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(r.v[4], r.v[5], r.v[6], r.v[7]);
-  } else {
+__device__ __forceinline__ void store(float* p, int64_t i, const F8& r, int left) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < left) p[i] = r.v[i];
-  }
+  for (int j = 0; j < kPer; ++j)
+    if (j < left) p[i + j] = r.v[j];
 }
 
-__device__ __forceinline__ void store_bf16(uint16_t* p, const uint32_t (&w)[4], int left, bool vec) {
-  if (vec && left >= kPer) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < left) p[i] = (uint16_t)(w[i / 2] >> 16 * (i & 1));
-  }
-}
-
-__device__ __forceinline__ uint2 load_bytes(const uint8_t* p, int left, bool vec) {
-  if (vec && left >= kPer) return __ldcs(reinterpret_cast<const uint2*>(p));
-  uint32_t w[2] = {0, 0};
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (i < left) w[i / 4] |= (uint32_t)p[i] << 8 * (i % 4);
-  return make_uint2(w[0], w[1]);
-}
-
-__device__ __forceinline__ void store_bytes(uint8_t* p, uint2 w, int left, bool vec) {
-  if (vec && left >= kPer) {
-    *reinterpret_cast<uint2*>(p) = w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < left) p[i] = (uint8_t)((i < 4 ? w.x : w.y) >> 8 * (i % 4));
-  }
-}
-
-__device__ __forceinline__ F8 from_e4m3(uint2 w, float by) {
-  F8 r;
-#pragma unroll
-  for (int i = 0; i < kPer; i += 2) {
-    const float2 f = fp8::unpack_e4m3x2((i < 4 ? w.x : w.y) >> 8 * (i % 4));
-    r.v[i] = f.x * by;
-    r.v[i + 1] = f.y * by;
-  }
-  return r;
-}
-
-__device__ __forceinline__ uint2 to_e4m3(const F8& r) {
-  return make_uint2(fp8::pack_e4m3x4(r.v[0], r.v[1], r.v[2], r.v[3]), fp8::pack_e4m3x4(r.v[4], r.v[5], r.v[6], r.v[7]));
-}
-
-// The largest |.| of a block of 128, by its 16 threads, as fp32 bits (NaN above everything).
-__device__ __forceinline__ uint32_t top_of_block(const F8& r) {
+// The largest |.| of a block of 128, by its 16 threads (NaN above everything).
+__device__ __forceinline__ float top_of_block(const F8& r) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) m = max(m, fp8::abs_bits(r.v[i]));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
-  return m;
+  return __uint_as_float(m);
 }
 
 // ------------------------------------------------------------------ random words
@@ -185,6 +136,7 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 // e4m3 has three bits below the leading one down to 2^-6, and below that steps of 2^-9, which is what
 // [2^-6, 2^-5) has too: 2^-6 is added to such values, so that cutting fp32's last 20 bits off fits both.
 constexpr uint32_t kCut = 0xfff00000u;
+constexpr uint32_t kTop = 0x07e00000u;  // 448 * 2^-120
 __device__ __forceinline__ float lift(float u) { return u < 0x1p-6f ? 0x1p-6f : 0.f; }
 
 // u in [-448, 448] to an e4m3 value: up in magnitude where the bits that are cut, plus random ones, carry.
@@ -210,10 +162,83 @@ __device__ __forceinline__ uint32_t round_bf16(float v, uint32_t rnd) {
   return (u & 0x7f800000u) == 0x7f800000u ? u : u + (rnd & 0xffffu);
 }
 
+// sqrt and reciprocal to two steps of fp32; what is below 2^-126 counts as 0.
 __device__ __forceinline__ float sqrt_fast(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ------------------------------------------------------------------ two values an instruction
+
+// The step with 8-bit moments is bound by the instructions it issues before HBM is: its fp32 products and
+// sums are taken two at a time (the packed forms round as the plain ones do).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+
+// the larger of two, NaN where one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Four pairs of consecutive values.
+struct P4 {
+  float2 v[kPer / 2];
+};
+
+// The same as they lie in memory.
+template <int kBytes>
+struct Raw {
+  using Part = typename std::conditional<kBytes == 1, uint2, uint4>::type;
+  static constexpr int kParts = kBytes == 4 ? 2 : 1;
+  Part part[kParts];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const Part* q = reinterpret_cast<const Part*>(static_cast<const char*>(p) + i * kBytes);
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) part[j] = __ldcs(q + j);
+  }
+  __device__ __forceinline__ P4 get() const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(part);
+    P4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kBytes == 4) r.v[j] = make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+      else if constexpr (kBytes == 2) r.v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+      else r.v[j] = fp8::unpack_e4m3x2(w[j / 2] >> 16 * (j & 1));
+    }
+    return r;
+  }
+};
+
+__device__ __forceinline__ void store4_f32(float* p, const P4& r) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(r.v[0].x, r.v[0].y, r.v[1].x, r.v[1].y));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(r.v[2].x, r.v[2].y, r.v[3].x, r.v[3].y));
 }
 
 // ------------------------------------------------------------------ the step
@@ -228,104 +253,257 @@ struct Step {
   bool last;  // launch of the call
 };
 
-template <int kN>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Batch<kN> b, const __grid_constant__ Step s) {
+// What all values of a tensor have in common.
+struct Common {
+  float f, c1, c2, rate, root, eps, keep;  // rate = lr / (1 - beta1^t), root = 1 / sqrt(1 - beta2^t), keep = 1 - lr wd
+  uint32_t key;
+};
+
+enum : int { kF32 = 0, kBf16 = 1, kMaster = 2 };  // a parameter: fp32, bf16, bf16 with a master
+
+// The factors of a chunk's 8-bit moments are in shared memory meanwhile, m's and then v's, read and written with
+// whole sectors: stored and loaded a byte a block, in the loop, they took a third of the step's time.
+constexpr int kMostBlocks = kMostChunk / 128;
+
+// What a thread reads for eight values, all of them there and on whole vectors.
+template <int kParam, bool kGradBf16, bool kSmall>
+struct Read {
+  Raw<kGradBf16 ? 2 : 4> g;
+  Raw<kParam == kBf16 ? 2 : 4> w;
+  Raw<kSmall ? 1 : 4> m, v;
+  __device__ __forceinline__ void load(const Entry& t, int64_t i) {
+    g.load(t.grad, i);
+    w.load(kParam == kMaster ? t.master : t.param, i);
+    m.load(t.m, i);
+    v.load(t.v, i);
+  }
+};
+
+template <int kParam, bool kGradBf16, bool kSmall>
+__device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Common& k, const Read<kParam, kGradBf16, kSmall>& in,
+                                           uint8_t* factors) {
+  const P4 g = in.g.get();
+  P4 w = in.w.get(), m = in.m.get(), v = in.v.get(), r;
+  if constexpr (kSmall) {
+    const float2 fm = both(fp8::scale_value(factors[0])), fv = both(fp8::scale_value(factors[kMostBlocks]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m.v[j] = mul2(m.v[j], fm);
+      v.v[j] = mul2(v.v[j], fv);
+      v.v[j] = mul2(v.v[j], v.v[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = mul2(g.v[j], both(k.f));
+    m.v[j] = fma2(both(k.c1), add2(x, neg2(m.v[j])), m.v[j]);  // b1 m + c1 x, with one rounding of m's size
+    v.v[j] = fma2(both(k.c2), fma2(x, x, neg2(v.v[j])), v.v[j]);
+    r.v[j] = make_float2(sqrt_fast(v.v[j].x), sqrt_fast(v.v[j].y));
+    const float2 den = fma2(r.v[j], both(k.root), both(k.eps));
+    const float2 u = mul2(m.v[j], make_float2(rcp_fast(den.x), rcp_fast(den.y)));
+    w.v[j] = fma2(both(-k.rate), u, mul2(both(k.keep), w.v[j]));
+  }
+  uint32_t rnd[kPer];
+  if constexpr (kSmall || kParam == kBf16) {
+    rnd[0] = mix((uint32_t)(i >> 3) + k.key);
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) rnd[j] = rnd[j - 1] * 0x3C6EF375u + 0xA54FF53Bu;
+  }
+  if constexpr (kParam == kMaster) store4_f32(t.master + i, w);
+  if constexpr (kParam == kF32) {
+    store4_f32(static_cast<float*>(t.param) + i, w);
+  } else {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kParam == kMaster) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(w.v[j].x, w.v[j].y);
+        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {  // adds the words' low halves to the bits that are cut; infinities and NaN stay
+        asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;" : "=r"(o[j])
+            : "f"(w.v[j].y), "f"(w.v[j].x), "r"(__byte_perm(rnd[2 * j], rnd[2 * j + 1], 0x5410)));
+      }
+    }
+    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.param) + i), make_uint4(o[0], o[1], o[2], o[3]));
+  }
+  if constexpr (!kSmall) {
+    store4_f32(static_cast<float*>(t.m) + i, m);
+    store4_f32(static_cast<float*>(t.v) + i, v);
+  } else {
+    // The largest |m| and r of the block.  From the first exchange on even lanes have m's, odd ones r's, and find
+    // the factor of theirs.
+    float tm = 0.f, tr = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      tm = max_nan(max_nan(tm, fabsf(m.v[j].x)), fabsf(m.v[j].y));
+      tr = max_nan(max_nan(tr, r.v[j].x), r.v[j].y);
+    }
+    const bool odd = threadIdx.x & 1;
+    float top = max_nan(odd ? tr : tm, __shfl_xor_sync(kAll, odd ? tm : tr, 1));
+#pragma unroll
+    for (int o = 2; o < 16; o *= 2) top = max_nan(top, __shfl_xor_sync(kAll, top, o));
+    const uint32_t b = fp8::scale_byte(top);
+    if ((threadIdx.x & 14) == 0) factors[odd ? kMostBlocks : 0] = (uint8_t)b;
+    const float inv = fp8::inv_scale_value(b), other = __shfl_xor_sync(kAll, inv, 1);
+    const float2 im = both(odd ? other : inv), iv = both(odd ? inv : other);
+    // Times 2^-120 an e4m3 value has fp32's bits 27-20 for its own 7-0 but the sign's: its subnormals, below 2^-6,
+    // are fp32's.  So cutting fp32's last 20 bits off, after the random ones are added, rounds both alike.  Four
+    // bits up, the value is the top byte.
+    constexpr float kDown = 0x1p-120f, kUp = 0x1p120f;
+    uint32_t ym[kPer], yr[kPer];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 um = mul2(mul2(m.v[j], im), both(kDown)), ur = mul2(mul2(r.v[j], iv), both(kDown));
+      const float2 u2 = mul2(mul2(v.v[j], iv), iv);
+      const uint32_t bm[2] = {__float_as_uint(um.x), __float_as_uint(um.y)}, br[2] = {__float_as_uint(ur.x), __float_as_uint(ur.y)};
+      // m: (bits + (word >> 16 << 4)) << 4 and the sign
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ym[2 * j + h] = ((bm[h] << 4) + __byte_perm(rnd[2 * j + h], 0, 0x4324)) & 0x7fffffffu | bm[h] & 0x80000000u;
+      // r: between lo and hi, up where v lies above lo^2 + word (hi^2 - lo^2)
+      const uint32_t l0 = br[0] & kCut, l1 = br[1] & kCut;
+      const float2 lo = mul2(make_float2(__uint_as_float(l0), __uint_as_float(l1)), both(kUp));
+      const float2 hi = mul2(make_float2(__uint_as_float(l0 + 0x100000u), __uint_as_float(l1 + 0x100000u)), both(kUp));
+      const float2 lo2 = mul2(lo, lo), gap = fma2(hi, hi, neg2(lo2));
+      const float2 word = add2(make_float2(__uint_as_float(rnd[2 * j] >> 1 & 0x7fff80u | 0x3f800000u),
+                                           __uint_as_float(rnd[2 * j + 1] >> 1 & 0x7fff80u | 0x3f800000u)), both(-1.f));
+      const float2 border = fma2(word, gap, lo2);
+      // not to 0 with v > 0, not past 448
+      const bool up0 = u2.x > (l0 == 0 ? 0.f : border.x) && l0 < kTop, up1 = u2.y > (l1 == 0 ? 0.f : border.y) && l1 < kTop;
+      yr[2 * j] = (br[0] << 4) + (up0 ? 1u << 24 : 0u);
+      yr[2 * j + 1] = (br[1] << 4) + (up1 ? 1u << 24 : 0u);
+    }
+    const auto pack = [](const uint32_t* y) { return __byte_perm(__byte_perm(y[0], y[1], 0x0073), __byte_perm(y[2], y[3], 0x0073), 0x5410); };
+    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i), make_uint2(pack(ym), pack(ym + 4)));
+    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i), make_uint2(pack(yr), pack(yr + 4)));
+  }
+}
+
+// The same for values at a tensor's end, or off whole vectors: one by one.
+template <bool kSmall>
+__device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, const Common& k, uint8_t* factors) {
+  const int left = (int)max((int64_t)0, min(end - i, (int64_t)kPer));
+  const bool p_bf16 = t.index_flags & kParamBf16;
+  const F8 g = load(t.grad, i, t.index_flags & kGradBf16, left);
+  F8 w = t.master ? load(t.master, i, false, left) : load(t.param, i, p_bf16, left);
+  F8 m, v, r;
+  if constexpr (kSmall) {
+    m = load_e4m3(static_cast<const uint8_t*>(t.m) + i, left, fp8::scale_value(factors[0]));
+    v = load_e4m3(static_cast<const uint8_t*>(t.v) + i, left, fp8::scale_value(factors[kMostBlocks]));
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v.v[j] *= v.v[j];
+  } else {
+    m = load(t.m, i, false, left);
+    v = load(t.v, i, false, left);
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const float x = g.v[j] * k.f;
+    m.v[j] = fmaf(k.c1, x - m.v[j], m.v[j]);
+    v.v[j] = fmaf(k.c2, fmaf(x, x, -v.v[j]), v.v[j]);
+    r.v[j] = sqrt_fast(v.v[j]);
+    w.v[j] = fmaf(-k.rate, m.v[j] * rcp_fast(fmaf(r.v[j], k.root, k.eps)), k.keep * w.v[j]);
+  }
+  uint32_t rnd[kPer];
+  rnd[0] = mix((uint32_t)(i >> 3) + k.key);
+#pragma unroll
+  for (int j = 1; j < kPer; ++j) rnd[j] = rnd[j - 1] * 0x3C6EF375u + 0xA54FF53Bu;
+  if (t.master) store(t.master, i, w, left);
+  if (p_bf16) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (j < left) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(w.v[j]);
+        static_cast<uint16_t*>(t.param)[i + j] = t.master ? *reinterpret_cast<const uint16_t*>(&h) : (uint16_t)(round_bf16(w.v[j], rnd[j]) >> 16);
+      }
+  } else {
+    store(static_cast<float*>(t.param), i, w, left);
+  }
+  if constexpr (!kSmall) {
+    store(static_cast<float*>(t.m), i, m, left);
+    store(static_cast<float*>(t.v), i, v, left);
+    return;
+  }
+  const uint32_t bm = fp8::scale_byte(top_of_block(m)), bv = fp8::scale_byte(top_of_block(r));
+  const float im = fp8::inv_scale_value(bm), iv = fp8::inv_scale_value(bv);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (j < left) {
+      static_cast<uint8_t*>(t.m)[i + j] = (uint8_t)fp8::pack_e4m3x2(round_linear(m.v[j] * im, rnd[j]), 0.f);
+      static_cast<uint8_t*>(t.v)[i + j] = (uint8_t)fp8::pack_e4m3x2(round_root(r.v[j] * iv, v.v[j] * iv * iv, rnd[j]), 0.f);
+    }
+  if ((threadIdx.x & 15) == 0) {
+    factors[0] = (uint8_t)bm;
+    factors[kMostBlocks] = (uint8_t)bv;
+  }
+}
+
+template <int kParam, bool kGradBf16, bool kSmall>
+__device__ __forceinline__ void step_tiles(const Entry& t, int64_t from, int64_t to, const Common& k, uint8_t* factors) {
+  for (int64_t i = from + threadIdx.x * kPer; i < to; i += Shape<kSmall>::kTile) {
+    Read<kParam, kGradBf16, kSmall> in;
+    in.load(t, i);
+    step_whole(t, i, k, in, factors + (int)(i - from) / 128);
+  }
+}
+
+// One kernel for tensors with moments in 8 bits and one for those with 32, which takes more registers.
+template <int kN, bool kSmall>
+__global__ void __launch_bounds__(Shape<kSmall>::kThreads, Shape<kSmall>::kCtas) adamw_kernel(const __grid_constant__ Batch<kN> b,
+                                                                                              const __grid_constant__ Step s) {
+  constexpr int kThreads = Shape<kSmall>::kThreads, kTile = Shape<kSmall>::kTile;
+  __shared__ Common common;
+  __shared__ bool skip;
+  __shared__ uint8_t factors[kSmall ? 2 * kMostBlocks : 1];
   const int ti = owner(b, blockIdx.x);
   const Entry& t = b.e[ti];
-  const int64_t begin = (int64_t)(blockIdx.x - b.first[ti]) * kChunk, end = min(begin + kChunk, t.n);
-  const bool vec = t.index_flags & kVec, p_bf16 = t.index_flags & kParamBf16, g_bf16 = t.index_flags & kGradBf16;
-  const bool small = t.m_scales != nullptr;
+  const int64_t begin = (int64_t)(blockIdx.x - b.first[ti]) * b.chunk, end = min(begin + b.chunk, t.n);
+  int64_t taken;
+  bool raise = false;
   pdl_wait();
   pdl_launch_dependents();
 
-  const float f = s.factor ? *s.factor : 1.f;
-  const bool skip = !isfinite(f);
-  const int64_t taken = *s.steps + 1;
-  if (!skip) {
+  if (threadIdx.x == 0) {
+    const float f = s.factor ? *s.factor : 1.f;
+    taken = *static_cast<const volatile int64_t*>(s.steps) + 1;
+    const float lr = s.lr_device ? *s.lr_device : s.lr;
     // 1 - beta^t, without the cancellation for small t
     const float bc1 = -expm1f((float)taken * s.log1), bc2 = -expm1f((float)taken * s.log2);
-    const float lr = s.lr_device ? *s.lr_device : s.lr;
-    const float rate = lr / bc1, root = rsqrtf(bc2), keep = 1.f - lr * t.weight_decay;
-    const float c1 = s.c1, c2 = s.c2;
     const uint32_t key = mix(mix(mix(mix(s.seed_low) + s.seed_high) + (uint32_t)taken) + (t.index_flags >> kIndexShift));
-    for (int64_t i0 = begin; i0 < end; i0 += kTile) {
+    common = Common{f, s.c1, s.c2, lr / bc1, rsqrtf(bc2), s.eps, 1.f - lr * t.weight_decay, key};
+    skip = !isfinite(f);
+    // The CTA that reads the steps last, when no other one will, writes them at its end.
+    raise = s.last && atomicAdd(s.ticket, 1u) == gridDim.x - 1;
+  }
+  const int blocks = (int)((end - begin + 127) / 128);
+  const int64_t block0 = begin / 128;
+  if constexpr (kSmall)
+    for (int j = threadIdx.x; j < blocks; j += kThreads) {
+      factors[j] = t.m_scales[block0 + j];
+      factors[kMostBlocks + j] = t.v_scales[block0 + j];
+    }
+  __syncthreads();
+  const Common k = common;
+  const int64_t whole = t.index_flags & kVec ? begin + (end - begin) / kTile * kTile : begin;
+  if (!skip) {
+    const bool g = t.index_flags & kGradBf16;
+    if (t.master) g ? step_tiles<kMaster, true, kSmall>(t, begin, whole, k, factors) : step_tiles<kMaster, false, kSmall>(t, begin, whole, k, factors);
+    else if (t.index_flags & kParamBf16) g ? step_tiles<kBf16, true, kSmall>(t, begin, whole, k, factors) : step_tiles<kBf16, false, kSmall>(t, begin, whole, k, factors);
+    else g ? step_tiles<kF32, true, kSmall>(t, begin, whole, k, factors) : step_tiles<kF32, false, kSmall>(t, begin, whole, k, factors);
+    for (int64_t i0 = whole; i0 < end; i0 += kTile) {
       const int64_t i = i0 + threadIdx.x * kPer;
-      const int left = (int)max((int64_t)0, min(end - i, (int64_t)kPer));
-      F8 g = load(t.grad, i, g_bf16, left, vec);
-      F8 w = t.master ? load_f32(t.master + i, left, vec) : load(t.param, i, p_bf16, left, vec);
-      F8 m, v;
-      if (small) {
-        const int64_t blk = i >> 7;
-        const bool in = left > 0;
-        m = from_e4m3(load_bytes(static_cast<const uint8_t*>(t.m) + i, left, vec), fp8::scale_value(in ? t.m_scales[blk] : 0));
-        v = from_e4m3(load_bytes(static_cast<const uint8_t*>(t.v) + i, left, vec), fp8::scale_value(in ? t.v_scales[blk] : 0));
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) v.v[j] *= v.v[j];
-      } else {
-        m = load_f32(static_cast<const float*>(t.m) + i, left, vec);
-        v = load_f32(static_cast<const float*>(t.v) + i, left, vec);
-      }
-      F8 r;  // sqrt(v)
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float x = g.v[j] * f;
-        m.v[j] = fmaf(c1, x - m.v[j], m.v[j]);  // b1 m + c1 x, with one rounding of m's size
-        v.v[j] = fmaf(c2, fmaf(x, x, -v.v[j]), v.v[j]);
-        r.v[j] = sqrt_fast(v.v[j]);
-        w.v[j] = fmaf(keep, w.v[j], -rate * __fdividef(m.v[j], fmaf(r.v[j], root, s.eps)));
-      }
-      uint32_t rnd[kPer];
-      if (small || (p_bf16 && !t.master)) {
-        rnd[0] = mix((uint32_t)(i >> 3) + key);
-#pragma unroll
-        for (int j = 1; j < kPer; ++j) rnd[j] = rnd[j - 1] * 0x3C6EF375u + 0xA54FF53Bu;
-      }
-      if (t.master) store_f32(t.master + i, w, left, vec);
-      if (!p_bf16) {
-        store_f32(static_cast<float*>(t.param) + i, w, left, vec);
-      } else {
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (t.master) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(w.v[2 * j], w.v[2 * j + 1]);
-            o[j] = *reinterpret_cast<const uint32_t*>(&h);
-          } else {
-            o[j] = round_bf16(w.v[2 * j], rnd[2 * j]) >> 16 | (round_bf16(w.v[2 * j + 1], rnd[2 * j + 1]) & 0xffff0000u);
-          }
-        }
-        store_bf16(static_cast<uint16_t*>(t.param) + i, o, left, vec);
-      }
-      if (small) {
-        const uint32_t bm = fp8::scale_byte(__uint_as_float(top_of_block(m))), bv = fp8::scale_byte(__uint_as_float(top_of_block(r)));
-        const float im = fp8::inv_scale_value(bm), iv = fp8::inv_scale_value(bv);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          m.v[j] = round_linear(m.v[j] * im, rnd[j]);
-          r.v[j] = round_root(r.v[j] * iv, v.v[j] * iv * iv, rnd[j]);
-        }
-        store_bytes(static_cast<uint8_t*>(t.m) + i, to_e4m3(m), left, vec);
-        store_bytes(static_cast<uint8_t*>(t.v) + i, to_e4m3(r), left, vec);
-        if ((threadIdx.x & 15) == 0 && left > 0) {
-          t.m_scales[i >> 7] = (uint8_t)bm;
-          t.v_scales[i >> 7] = (uint8_t)bv;
-        }
-      } else {
-        store_f32(static_cast<float*>(t.m) + i, m, left, vec);
-        store_f32(static_cast<float*>(t.v) + i, v, left, vec);
+      step_rest<kSmall>(t, i, end, k, factors + (int)(i - begin) / 128);
+    }
+    if constexpr (kSmall) {
+      __syncthreads();
+      for (int j = threadIdx.x; j < blocks; j += kThreads) {
+        t.m_scales[block0 + j] = factors[j];
+        t.v_scales[block0 + j] = factors[kMostBlocks + j];
       }
     }
   }
-  // the CTA that is done last raises the step's number, when all have read it
-  if (s.last) {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
-      if (atomicAdd(s.ticket, 1u) == gridDim.x - 1) {
-        *s.ticket = 0;
-        if (!skip) *s.steps = taken;
-      }
-    }
+  if (raise) {
+    *s.ticket = 0;
+    if (!skip) *s.steps = taken;
   }
 }
 
@@ -336,20 +514,49 @@ __global__ void empty_step_kernel(const float* factor, int64_t* steps) {
   if (!factor || isfinite(*factor)) ++*steps;
 }
 
-template <int kN>
+template <int kN, bool kSmall>
 cudaError_t launch_list(const Entry* e, int n, const Step& s, cudaStream_t st) {
-  Batch<kN> b{};
+  constexpr int kTile = Shape<kSmall>::kTile;
+  Batch<kN> b;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) tiles += (e[i].n + kTile - 1) / kTile;
   b.n = n;
+  b.chunk = kTile;
+  while (b.chunk < Shape<kSmall>::kTiles * kTile && tiles * kTile >= 2 * kFewChunks * b.chunk) b.chunk *= 2;
+  b.first[0] = 0;
   for (int i = 0; i < n; ++i) {
     b.e[i] = e[i];
-    b.first[i + 1] = b.first[i] + (uint32_t)((e[i].n + kChunk - 1) / kChunk);
+    b.first[i + 1] = b.first[i] + (uint32_t)((e[i].n + b.chunk - 1) / b.chunk);
   }
-  return launch_kernel(adamw_kernel<kN>, dim3(b.first[n]), dim3(kThreads), 0, st, true, 1, b, s);
+  return launch_kernel(adamw_kernel<kN, kSmall>, dim3(b.first[n]), dim3(Shape<kSmall>::kThreads), 0, st, true, 1, b, s);
+}
+
+template <bool kSmall>
+cudaError_t launch_lists(const Entry* e, int n, const Step& s, cudaStream_t st) {
+  return n <= 24    ? launch_list<24, kSmall>(e, n, s, st)
+         : n <= 100 ? launch_list<100, kSmall>(e, n, s, st)
+                    : launch_list<kMostTensors, kSmall>(e, n, s, st);
 }
 
 // ------------------------------------------------------------------ the norm
 
+constexpr int kThreads = 256, kTile = kThreads * kPer;
 constexpr int kNormChunk = 8 * kTile;  // 64 values a thread are summed in fp32
+
+__device__ __forceinline__ F8 load_maybe(const GradEntry& e, int64_t i, int left) {
+  if (!e.vec || left < kPer) return load(e.g, i, e.bf16, left);
+  P4 p;
+  if (e.bf16) {
+    Raw<2> r;
+    r.load(e.g, i);
+    p = r.get();
+  } else {
+    Raw<4> r;
+    r.load(e.g, i);
+    p = r.get();
+  }
+  return {{p.v[0].x, p.v[0].y, p.v[1].x, p.v[1].y, p.v[2].x, p.v[2].y, p.v[3].x, p.v[3].y}};
+}
 
 // parts[CTA]: the sum of squares of its chunks, one in gridDim.x of all.
 template <int kN>
@@ -368,7 +575,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t i = i0 + u * kTile + threadIdx.x * kPer;
-        g[u] = load(e.g, i, e.bf16, (int)max((int64_t)0, min(end - i, (int64_t)kPer)), e.vec);
+        g[u] = load_maybe(e, i, (int)max((int64_t)0, min(end - i, (int64_t)kPer)));
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
@@ -407,8 +614,9 @@ __global__ void __launch_bounds__(1024) norm_end_kernel(const double* parts, int
 
 template <int kN>
 cudaError_t launch_norm_list(const GradEntry* e, int n, double* parts, int* used, cudaStream_t st) {
-  GradBatch<kN> b{};
+  GradBatch<kN> b;
   b.n = n;
+  b.first[0] = 0;
   for (int i = 0; i < n; ++i) {
     b.e[i] = e[i];
     b.first[i + 1] = b.first[i] + (uint32_t)((e[i].n + kNormChunk - 1) / kNormChunk);
@@ -437,25 +645,26 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   s.ticket = ticket;
   s.seed_low = (uint32_t)cfg.seed;
   s.seed_high = (uint32_t)(cfg.seed >> 32);
-  int last = -1;
-  for (int i = 0; i < n; ++i)
-    if (tensors[i].n > 0) last = i;
-  if (last < 0) return launch_kernel(empty_step_kernel, dim3(1), dim3(1), 0, st, true, 1, factor, steps);
+  int left[2] = {0, 0};  // tensors with moments in 32 bits, in 8
+  for (int i = 0; i < n; ++i) left[tensors[i].m_scales != nullptr] += tensors[i].n > 0;
+  if (left[0] + left[1] == 0) return launch_kernel(empty_step_kernel, dim3(1), dim3(1), 0, st, true, 1, factor, steps);
   Entry e[kMostTensors];
-  for (int i = 0; i <= last;) {
-    int m = 0;
-    for (; i <= last && m < kMostTensors; ++i) {
-      const moe_adamw_tensor& t = tensors[i];
-      if (t.n == 0) continue;
-      const uintptr_t moments = t.m_scales ? 8 : 16;
-      const bool vec = on(t.param, 16) && on(t.master, 16) && on(t.grad, 16) && on(t.m, moments) && on(t.v, moments);
-      e[m++] = {t.param, t.master, t.grad, t.m, t.v, t.m_scales, t.v_scales, t.n, t.weight_decay,
-                (uint32_t)i << kIndexShift | (t.param_dtype == MOE_BF16 ? kParamBf16 : 0) | (t.grad_dtype == MOE_BF16 ? kGradBf16 : 0) | (vec ? kVec : 0)};
+  for (const bool small : {true, false})
+    for (int i = 0; left[small] > 0;) {
+      int m = 0;
+      for (; i < n && m < kMostTensors; ++i) {
+        const moe_adamw_tensor& t = tensors[i];
+        if (t.n == 0 || (t.m_scales != nullptr) != small) continue;
+        const uintptr_t moments = small ? 8 : 16;
+        const bool vec = on(t.param, 16) && on(t.master, 16) && on(t.grad, 16) && on(t.m, moments) && on(t.v, moments);
+        e[m++] = {t.param, t.master, t.grad, t.m, t.v, t.m_scales, t.v_scales, t.n, t.weight_decay,
+                  (uint32_t)i << kIndexShift | (t.param_dtype == MOE_BF16 ? kParamBf16 : 0) | (t.grad_dtype == MOE_BF16 ? kGradBf16 : 0) | (vec ? kVec : 0)};
+      }
+      left[small] -= m;
+      s.last = left[0] + left[1] == 0;
+      const cudaError_t err = small ? launch_lists<true>(e, m, s, st) : launch_lists<false>(e, m, s, st);
+      if (err != cudaSuccess) return err;
     }
-    s.last = i > last;
-    const cudaError_t err = m <= 24 ? launch_list<24>(e, m, s, st) : m <= 100 ? launch_list<100>(e, m, s, st) : launch_list<kMostTensors>(e, m, s, st);
-    if (err != cudaSuccess) return err;
-  }
   return cudaSuccess;
 }
 

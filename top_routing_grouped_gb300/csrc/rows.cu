@@ -3,6 +3,10 @@
 // All of it moves rows: a few operations a byte, so HBM bounds the large calls and the launch the small ones.
 #include <cuda_bf16.h>
 
+#include <initializer_list>
+#include <type_traits>
+#include <utility>
+
 #include "device_common.cuh"
 #include "rows_internal.h"
 
@@ -351,7 +355,7 @@ cudaError_t launch_sort(const Args& a, int32_t* counted, cudaStream_t st) {
 
 // ------------------------------------------------------------------ combine
 
-// n values of type T on a boundary of n * sizeof(T) bytes (16 at most at a time), to and from fp32
+// n values of type T on a boundary of n * sizeof(T) bytes, 16 at most at a time, to and from fp32.
 template <typename T, int n>
 struct Values {
   static constexpr int kBytes = n * (int)sizeof(T) < 16 ? n * (int)sizeof(T) : 16, kParts = n * (int)sizeof(T) / kBytes;
@@ -377,23 +381,33 @@ struct Values {
   }
 };
 
-// One warp for 32 V columns of one token: up to four rows in flight, summed in the slots' order.
-template <typename Ty, typename To, int V>
-__global__ void __launch_bounds__(kThreads, 6) combine_kernel(const Ty* y, int64_t R, const int32_t* slot_pos, const float* gates,
-                                                           int64_t T, int k, int64_t d, unsigned segs, const To* residual, To* out) {
+// One warp for 32 V C columns of one token, C pieces of V a lane: kJ rows in flight at a time, summed in the
+// slots' order.  What counts is that a lane has 64 bytes of rows under way: for one slot a token, four pieces of
+// its row, not one of up to four rows (16384 x 2048 bf16: 36.8 -> KJ1 us); where rows lie on 4-byte boundaries
+// only, four pieces too (2048 x 2050, 16 slots: 43.5 -> ODD us).
+template <typename Ty, typename To, int V, int C, int kJ>
+__global__ void __launch_bounds__(kThreads, V * (int)sizeof(Ty) * C == 16 ? 6 : 4) combine_kernel(const Ty* y, int64_t R, const int32_t* slot_pos,
+                                                                               const float* gates, int64_t T, int k, int64_t d,
+                                                                               unsigned segs, const To* residual, To* out) {
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = unit <= 0xffffffffll ? (int64_t)((unsigned)unit / segs) : unit / segs;
   pdl_wait();
   pdl_launch_dependents();
   if (t >= T) return;
-  const int64_t c = ((unit - t * segs) * 32 + lane) * V;
-  const bool ok = c < d;
-  Values<To, V> res;
-  if (residual && ok) res.load(residual + t * d + c);
-  float acc[V];
+  const int64_t c = ((unit - t * segs) * 32 * C + lane) * V;
+  const auto col = [&](int x) { return c + x * 32 * V; };
+  Values<To, V> res[C];
+  if (residual) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int x = 0; x < C; ++x)
+      if (col(x) < d) res[x].load(residual + t * d + col(x));
+  }
+  float acc[C][V];
+#pragma unroll
+  for (int x = 0; x < C; ++x)
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[x][i] = 0.f;
   for (int j0 = 0; j0 < k; j0 += 32) {
     const int n = min(32, k - j0);
     int p = -1;
@@ -403,54 +417,60 @@ __global__ void __launch_bounds__(kThreads, 6) combine_kernel(const Ty* y, int64
       if (gates) g = gates[t * k + j0 + lane];
     }
     if (p >= R) p = -1;
-    for (int j = 0; j < n; j += 4) {
-      Values<Ty, V> row[4];
-      int at[4];
+    for (int j = 0; j < n; j += kJ) {
+      Values<Ty, V> row[kJ][C];
+      int at[kJ];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kJ; ++q) {
         at[q] = __shfl_sync(kAll, p, j + q);  // lanes past n hold -1
-        if (at[q] >= 0 && ok) row[q].load(y + at[q] * d + c);
+        if (at[q] < 0) continue;
+#pragma unroll
+        for (int x = 0; x < C; ++x)
+          if (col(x) < d) row[q][x].load(y + at[q] * d + col(x));
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < kJ; ++q) {
         const float gq = __shfl_sync(kAll, g, j + q);
-        if (at[q] >= 0) {
+        if (at[q] < 0) continue;
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(gq, row[q].get(i), acc[i]);
-        }
+        for (int x = 0; x < C; ++x)
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[x][i] = fmaf(gq, row[q][x].get(i), acc[x][i]);
       }
     }
   }
-  if (!ok) return;
-  Values<To, V> o;
 #pragma unroll
-  for (int i = 0; i < V; ++i) o.set(i, residual ? res.get(i) + acc[i] : acc[i]);
-  o.store(out + t * d + c);
+  for (int x = 0; x < C; ++x) {
+    if (col(x) >= d) continue;
+    Values<To, V> o;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.set(i, residual ? res[x].get(i) + acc[x][i] : acc[x][i]);
+    o.store(out + t * d + col(x));
+  }
 }
 
-template <typename Ty, typename To, int V>
+template <typename Ty, typename To, int V, int C, int kJ>
 cudaError_t combine_as(const void* y, int64_t R, const int32_t* slot_pos, const float* gates, int64_t T, int k, int64_t d,
                        const void* residual, void* out, cudaStream_t st) {
-  const int64_t segs = (d + 32 * V - 1) / (32 * V), blocks = (T * segs + kWarps - 1) / kWarps;
-  return launch_kernel(combine_kernel<Ty, To, V>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, 1, static_cast<const Ty*>(y), R,
-                       slot_pos, gates, T, k, d, (unsigned)segs, static_cast<const To*>(residual), static_cast<To*>(out));
+  const int64_t segs = (d + 32 * V * C - 1) / (32 * V * C), blocks = (T * segs + kWarps - 1) / kWarps;
+  return launch_kernel(combine_kernel<Ty, To, V, C, kJ>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, 1, static_cast<const Ty*>(y),
+                       R, slot_pos, gates, T, k, d, (unsigned)segs, static_cast<const To*>(residual), static_cast<To*>(out));
 }
 
-// The gradients: kPer warps a token, each lane V columns at a time of up to eight rows; the products with dout
-// are summed over the lanes, and over the warps in order.
-template <typename Td, typename Ty, int V>
+// The gradients: `per` warps a token, each lane C pieces of V columns at a time of up to kJ rows; the products with
+// dout are summed over the lanes, and over the warps in order.
+template <typename Td, typename Ty, int V, int C, int kJ>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Td* dout, const int32_t* slot_pos, const float* gates,
                                                                     int64_t T, int k, int64_t d, int64_t R, const Ty* y, Ty* dy,
                                                                     float* dgates, int per) {
-  constexpr int kRows = 8;
-  __shared__ float part[kWarps][kRows];
+  __shared__ float part[kWarps][kJ];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % per;
   const int64_t t = (int64_t)blockIdx.x * (kWarps / per) + warp / per;
   pdl_wait();
   pdl_launch_dependents();
   const bool has = t < T;
-  for (int j0 = 0; j0 < k; j0 += kRows) {
-    const int n = min(kRows, k - j0);
+  for (int j0 = 0; j0 < k; j0 += kJ) {
+    const int n = min(kJ, k - j0);
     int p = -1;
     float g = 1.f;
     if (has && lane < n) {
@@ -458,36 +478,45 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Td* do
       if (gates) g = gates[t * k + j0 + lane];
     }
     if (p >= R) p = -1;
-    int at[kRows];
-    float gate[kRows], dot[kRows];
+    int at[kJ];
+    float gate[kJ], dot[kJ];
 #pragma unroll
-    for (int q = 0; q < kRows; ++q) {
+    for (int q = 0; q < kJ; ++q) {
       at[q] = __shfl_sync(kAll, p, q);
       gate[q] = __shfl_sync(kAll, g, q);
       dot[q] = 0.f;
     }
     if (has) {
-      for (int64_t c = (mine * 32 + lane) * V; c < d; c += per * 32 * V) {
-        Values<Td, V> go;
-        go.load(dout + t * d + c);
-        Values<Ty, V> row[kRows];
+      for (int64_t c = (mine * 32 * C + lane) * V; c < d; c += per * 32 * V * C) {
+        const auto col = [&](int x) { return c + x * 32 * V; };
+        Values<Td, V> go[C];
+#pragma unroll
+        for (int x = 0; x < C; ++x)
+          if (col(x) < d) go[x].load(dout + t * d + col(x));
+        Values<Ty, V> row[kJ][C];
         if (dgates) {
 #pragma unroll
-          for (int q = 0; q < kRows; ++q)
-            if (at[q] >= 0) row[q].load(y + at[q] * d + c);
+          for (int q = 0; q < kJ; ++q)
+#pragma unroll
+            for (int x = 0; x < C; ++x)
+              if (at[q] >= 0 && col(x) < d) row[q][x].load(y + at[q] * d + col(x));
         }
 #pragma unroll
-        for (int q = 0; q < kRows; ++q) {
+        for (int q = 0; q < kJ; ++q) {
           if (at[q] < 0) continue;
-          if (dgates) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) dot[q] = fmaf(go.get(i), row[q].get(i), dot[q]);
-          }
-          if (dy) {
-            Values<Ty, V> o;
+          for (int x = 0; x < C; ++x) {
+            if (col(x) >= d) continue;
+            if (dgates) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) o.set(i, gate[q] * go.get(i));
-            o.store(dy + at[q] * d + c);
+              for (int i = 0; i < V; ++i) dot[q] = fmaf(go[x].get(i), row[q][x].get(i), dot[q]);
+            }
+            if (dy) {
+              Values<Ty, V> o;
+#pragma unroll
+              for (int i = 0; i < V; ++i) o.set(i, gate[q] * go[x].get(i));
+              o.store(dy + at[q] * d + col(x));
+            }
           }
         }
       }
@@ -495,13 +524,13 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Td* do
     if (dgates) {
       float sum = 0.f;
 #pragma unroll
-      for (int q = 0; q < kRows; ++q) {
+      for (int q = 0; q < kJ; ++q) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot[q] += __shfl_xor_sync(kAll, dot[q], o);
         if (lane == q) sum = dot[q];
       }
       if (per > 1) {
-        if (lane < kRows) part[warp][lane] = sum;
+        if (lane < kJ) part[warp][lane] = sum;
         __syncthreads();
         if (mine == 0 && lane < n) {
           sum = 0.f;
@@ -514,27 +543,28 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Td* do
   }
 }
 
-template <typename Td, typename Ty, int V>
+template <typename Td, typename Ty, int V, int C, int kJ>
 cudaError_t backward_as(const void* dout, const int32_t* slot_pos, const float* gates, int64_t T, int k, int64_t d, int64_t R,
                         const void* y, void* dy, float* dgates, cudaStream_t st) {
-  // warps a token: as many as have columns, until the GPU's warps have a token each
+  // warps a token: each has its columns in kTurns turns at most, as long as there are tokens for all
+  constexpr int kTurns = 4;
   int per = 1;
-  while (per < kWarps && (int64_t)per * 32 * V < d && T * per < 152 * 32) per *= 2;
+  while (per < kWarps && (int64_t)per * 32 * V * C * (T * per < 152 * 16 ? 1 : kTurns) < d) per *= 2;
   const int64_t blocks = (T + kWarps / per - 1) / (kWarps / per);
-  return launch_kernel(combine_backward_kernel<Td, Ty, V>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, 1,
+  return launch_kernel(combine_backward_kernel<Td, Ty, V, C, kJ>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, 1,
                        static_cast<const Td*>(dout), slot_pos, gates, T, k, d, R, static_cast<const Ty*>(y), static_cast<Ty*>(dy),
                        dgates, per);
 }
 
-// The most values, of `most`, that divide a row and that all these addresses are on boundaries of (16 bytes do
-// for more than 16).
+// How many values a lane takes at once: `most`, 2 or 1, so many that they divide a row and that all these addresses
+// are on boundaries of them (16 bytes do for more than 16).
 int values_at_once(int most, int64_t d, std::initializer_list<std::pair<const void*, int>> arrays) {
-  for (; most > 1; most /= 2) {
-    bool fits = d % most == 0;
-    for (const auto& [p, size] : arrays) fits = fits && reinterpret_cast<uintptr_t>(p) % (most * size < 16 ? most * size : 16) == 0;
-    if (fits) break;
+  for (const int v : {most, 2}) {
+    bool fits = d % v == 0;
+    for (const auto& [p, size] : arrays) fits = fits && reinterpret_cast<uintptr_t>(p) % (v * size < 16 ? v * size : 16) == 0;
+    if (fits) return v;
   }
-  return most;
+  return 1;
 }
 
 }  // namespace
@@ -566,11 +596,12 @@ cudaError_t launch_combine(const void* y, bool y_bf16, int64_t R, const int32_t*
   const auto with = [&](auto ty, auto to) {
     using Ty = decltype(ty);
     using To = decltype(to);
-    if constexpr (sizeof(Ty) == 2)
-      if (v == 8) return combine_as<Ty, To, 8>(y, R, slot_pos, gates, T, k, d, residual, out, st);
-    return v == 4   ? combine_as<Ty, To, 4>(y, R, slot_pos, gates, T, k, d, residual, out, st)
-           : v == 2 ? combine_as<Ty, To, 2>(y, R, slot_pos, gates, T, k, d, residual, out, st)
-                    : combine_as<Ty, To, 1>(y, R, slot_pos, gates, T, k, d, residual, out, st);
+    constexpr int kV = 16 / sizeof(Ty);
+    return v == 1   ? combine_as<Ty, To, 1, 2, 8>(y, R, slot_pos, gates, T, k, d, residual, out, st)
+           : v == 2 ? combine_as<Ty, To, 2, 2, 8>(y, R, slot_pos, gates, T, k, d, residual, out, st)
+           : k == 1 ? combine_as<Ty, To, kV, 4, 1>(y, R, slot_pos, gates, T, k, d, residual, out, st)
+           : k == 2 ? combine_as<Ty, To, kV, 2, 2>(y, R, slot_pos, gates, T, k, d, residual, out, st)
+                    : combine_as<Ty, To, kV, 1, 4>(y, R, slot_pos, gates, T, k, d, residual, out, st);
   };
   if (y_bf16) return out_bf16 ? with(bf16(), bf16()) : with(bf16(), float());
   return out_bf16 ? with(float(), bf16()) : with(float(), float());
@@ -582,11 +613,13 @@ cudaError_t launch_combine_backward(const void* dout, bool dout_bf16, const int3
   const auto with = [&](auto td, auto ty) {
     using Td = decltype(td);
     using Ty = decltype(ty);
-    if constexpr (sizeof(Ty) == 2)
-      if (v == 8) return backward_as<Td, Ty, 8>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st);
-    return v == 4   ? backward_as<Td, Ty, 4>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
-           : v == 2 ? backward_as<Td, Ty, 2>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
-                    : backward_as<Td, Ty, 1>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st);
+    constexpr int kV = 16 / sizeof(Ty);
+    return v == 1   ? backward_as<Td, Ty, 1, 4, 8>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
+           : v == 2 ? backward_as<Td, Ty, 2, 4, 8>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
+           : k == 1 ? backward_as<Td, Ty, kV, 4, 1>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
+           : k == 2 ? backward_as<Td, Ty, kV, 2, 2>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
+           : k <= 4 ? backward_as<Td, Ty, kV, 1, 4>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
+                    : backward_as<Td, Ty, kV, 1, 8>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st);
   };
   if (dout_bf16) return y_bf16 ? with(bf16(), bf16()) : with(bf16(), float());
   return y_bf16 ? with(float(), bf16()) : with(float(), float());

@@ -132,8 +132,8 @@ def test_grad_norm_refusals(lib):
     refused(call, ok, [dict(grad=None), dict(grad=A[0].value + 2), dict(n=-1), dict(n=(1 << 35) + 1), dict(dtype=2), dict(max_norm=0.0), dict(max_norm=float("nan")),
                        dict(max_norm=float("inf")), dict(norm=None), dict(norm=off(A[1], 2)), dict(factor=off(A[2], 1)), dict(factor=A[1]), dict(ws=None),
                        dict(ws=off(A[3], 64)), dict(wsb=100), dict(count=-1), dict(count=-2)])
-    assert [lib.moe_grad_norm_workspace(n) for n in (-1, 0, (1 << 20) + 1)] == [0, 0, 0]
-    assert lib.moe_grad_norm_workspace(421) == 2 * lib.moe_grad_norm_workspace(420)
+    assert [lib.moe_grad_norm_workspace(n) for n in (-1, (1 << 20) + 1)] == [0, 0]
+    assert lib.moe_grad_norm_workspace(0) == lib.moe_grad_norm_workspace(420) < lib.moe_grad_norm_workspace(421) <= 2 * lib.moe_grad_norm_workspace(420)
 
 
 def test_python_refusals(lib):

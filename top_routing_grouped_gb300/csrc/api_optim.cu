@@ -64,8 +64,9 @@ moe_status moe_adamw(const moe_adamw_tensor* tensors, int32_t n_tensors, const m
 
 size_t moe_grad_norm_workspace(int32_t n_tensors) {
   if (n_tensors < 0 || n_tensors > 1 << 20) return 0;
-  const size_t launches = (size_t)(n_tensors + optim::kMostTensors - 1) / optim::kMostTensors;  // a sum for each CTA of each
-  return (launches * optim::kNormCtas * sizeof(double) + 255) / 256 * 256;
+  // the ticket, and a sum for each CTA of each launch
+  const size_t launches = n_tensors == 0 ? 1 : (size_t)(n_tensors + optim::kMostTensors - 1) / optim::kMostTensors;
+  return ((1 + launches * optim::kNormCtas) * sizeof(double) + 255) / 256 * 256;
 }
 
 moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n_tensors, float max_norm, float* norm, float* factor, void* workspace,
@@ -83,9 +84,9 @@ moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n_tensors, floa
     if (t.n > 0 && (!t.grad || !aligned(t.grad, esize(t.dtype)))) return fail(MOE_ERR_INVALID_ARG, "tensor %d: grad is null or not aligned to its type", i);
   }
   const size_t need = moe_grad_norm_workspace(n_tensors);
-  if (need > 0 && (!workspace || !aligned(workspace, 256))) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (!workspace || !aligned(workspace, 256)) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if (workspace_bytes < need) return fail(MOE_ERR_INVALID_ARG, "workspace too small: %zu < %zu", workspace_bytes, need);
-  return cuda_status(optim::launch_grad_norm(tensors, n_tensors, max_norm, norm, factor, static_cast<double*>(workspace),
+  return cuda_status(optim::launch_grad_norm(tensors, n_tensors, max_norm, norm, factor, workspace,
                                              static_cast<cudaStream_t>(stream)),
                      "launching the norm");
 }

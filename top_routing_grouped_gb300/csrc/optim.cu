@@ -60,7 +60,7 @@ struct Batch {
 struct GradEntry {
   const void* g;
   int64_t n;
-  int bf16, vec;
+  bool bf16, vec;
 };
 
 template <int kN>
@@ -541,7 +541,7 @@ cudaError_t launch_lists(const Entry* e, int n, const Step& s, cudaStream_t st) 
 // ------------------------------------------------------------------ the norm
 
 constexpr int kThreads = 256, kTile = kThreads * kPer;
-constexpr int kNormChunk = 8 * kTile;  // 64 values a thread are summed in fp32
+constexpr int kNormChunk = 4 * kTile;  // 32 values a thread, all under way at once; a warp's are summed in fp32
 
 __device__ __forceinline__ F8 load_maybe(const GradEntry& e, int64_t i, int left) {
   if (!e.vec || left < kPer) return load(e.g, i, e.bf16, left);
@@ -558,10 +558,35 @@ __device__ __forceinline__ F8 load_maybe(const GradEntry& e, int64_t i, int left
   return {{p.v[0].x, p.v[0].y, p.v[1].x, p.v[1].y, p.v[2].x, p.v[2].y, p.v[3].x, p.v[3].y}};
 }
 
-// parts[CTA]: the sum of squares of its chunks, one in gridDim.x of all.
+// The sum of the warps' first lanes' values, in the block's first thread.  A sum in 64 bits takes a warp several times
+// as long as one in fp32, and they follow one another here: as few of them as can be.
+__device__ __forceinline__ double sum_of_warps(double v) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ double of_warp[kWarps];
+  __syncthreads();  // of_warp may still be read
+  if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < kWarps ? of_warp[threadIdx.x] : 0;
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  }
+  return v;
+}
+
+struct NormOut {
+  double* parts;     // of all launches; this one's are behind `before` others
+  uint32_t* ticket;  // null: not the last launch
+  int before;
+  float max_norm;
+  float *norm, *factor;
+};
+
+// parts[CTA]: the sum of squares of its chunks, one in gridDim.x of all.  Of the last launch the CTA that is done last
+// adds all parts up, in their order.
 template <int kN>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ GradBatch<kN> b, double* parts) {
-  __shared__ double of_warp[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ GradBatch<kN> b, const NormOut out) {
+  __shared__ bool ends;
   pdl_wait();
   pdl_launch_dependents();
   double total = 0;
@@ -569,51 +594,49 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     const int ti = owner(b, chunk);
     const GradEntry& e = b.e[ti];
     const int64_t begin = (int64_t)(chunk - b.first[ti]) * kNormChunk, end = min(begin + kNormChunk, e.n);
-    float sum[kPer] = {};
-    for (int64_t i0 = begin; i0 < end; i0 += 4 * kTile) {
-      F8 g[4];
+    F8 g[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int64_t i = i0 + u * kTile + threadIdx.x * kPer;
-        g[u] = load_maybe(e, i, (int)max((int64_t)0, min(end - i, (int64_t)kPer)));
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) sum[j] = fmaf(g[u].v[j], g[u].v[j], sum[j]);
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = begin + u * kTile + threadIdx.x * kPer;
+      g[u] = load_maybe(e, i, (int)max((int64_t)0, min(end - i, (int64_t)kPer)));
     }
-    total += (double)(((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7])));
+    float sum[kPer] = {};
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) sum[j] = fmaf(g[u].v[j], g[u].v[j], sum[j]);
+    float s = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    total += (double)s;
   }
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-  if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = total;
-  __syncthreads();
+  total = sum_of_warps(total);
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) total += of_warp[w];
-    parts[blockIdx.x] = total;
+    out.parts[out.before + blockIdx.x] = total;
+    ends = false;
+    if (out.ticket) {
+      __threadfence();  // the part is there before the ticket is
+      ends = atomicAdd(out.ticket, 1u) == gridDim.x - 1;
+    }
   }
-}
-
-__global__ void __launch_bounds__(1024) norm_end_kernel(const double* parts, int n, float max_norm, float* norm, float* factor) {
-  __shared__ double of_warp[32];
-  pdl_wait();
-  pdl_launch_dependents();
-  double total = 0;
-  for (int i = threadIdx.x; i < n; i += 1024) total += parts[i];
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-  if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = total;
   __syncthreads();
-  if (threadIdx.x >= 32) return;
-  total = of_warp[threadIdx.x];
+  if (!ends) return;
+  __threadfence();
+  total = 0;
+  for (int i = threadIdx.x; i < out.before + (int)gridDim.x; i += kThreads) total += __ldcg(out.parts + i);
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  total = sum_of_warps(total);
   if (threadIdx.x == 0) {
     const float r = (float)sqrt(total);
-    *norm = r;
-    if (factor) *factor = isfinite(r) ? (r > max_norm ? max_norm / r : 1.f) : __uint_as_float(0x7fffffffu);
+    *out.ticket = 0;
+    *out.norm = r;
+    if (out.factor) *out.factor = isfinite(r) ? (r > out.max_norm ? out.max_norm / r : 1.f) : __uint_as_float(0x7fffffffu);
   }
 }
 
 template <int kN>
-cudaError_t launch_norm_list(const GradEntry* e, int n, double* parts, int* used, cudaStream_t st) {
+cudaError_t launch_norm_list(const GradEntry* e, int n, NormOut& out, uint32_t* ticket, cudaStream_t st) {
   GradBatch<kN> b;
   b.n = n;
   b.first[0] = 0;
@@ -621,9 +644,11 @@ cudaError_t launch_norm_list(const GradEntry* e, int n, double* parts, int* used
     b.e[i] = e[i];
     b.first[i + 1] = b.first[i] + (uint32_t)((e[i].n + kNormChunk - 1) / kNormChunk);
   }
-  const unsigned grid = b.first[n] < (unsigned)kNormCtas ? b.first[n] : (unsigned)kNormCtas;
-  *used = (int)grid;
-  return launch_kernel(norm_kernel<kN>, dim3(grid), dim3(kThreads), 0, st, true, 1, b, parts);
+  const unsigned grid = b.first[n] > (unsigned)kNormCtas ? (unsigned)kNormCtas : b.first[n] > 0 ? b.first[n] : 1;
+  out.ticket = ticket;
+  const cudaError_t err = launch_kernel(norm_kernel<kN>, dim3(grid), dim3(kThreads), 0, st, true, 1, b, out);
+  out.before += (int)grid;
+  return err;
 }
 
 bool on(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -668,24 +693,25 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   return cudaSuccess;
 }
 
-cudaError_t launch_grad_norm(const moe_grad_tensor* tensors, int n, float max_norm, float* norm, float* factor, double* parts,
+cudaError_t launch_grad_norm(const moe_grad_tensor* tensors, int n, float max_norm, float* norm, float* factor, void* workspace,
                              cudaStream_t st) {
+  NormOut out{static_cast<double*>(workspace) + 1, nullptr, 0, max_norm, norm, factor};
   GradEntry e[kMostTensors];
-  int used = 0;
-  for (int i = 0; i < n;) {
+  int left = 0;  // tensors with values
+  for (int i = 0; i < n; ++i) left += tensors[i].n > 0;
+  int i = 0;
+  do {  // without values: one CTA that finds a sum of 0
     int m = 0;
     for (; i < n && m < kMostTensors; ++i) {
       const moe_grad_tensor& t = tensors[i];
-      if (t.n == 0) continue;
-      e[m++] = {t.grad, t.n, t.dtype == MOE_BF16, on(t.grad, 16)};
+      if (t.n > 0) e[m++] = {t.grad, t.n, t.dtype == MOE_BF16, on(t.grad, 16)};
     }
-    if (m == 0) continue;
-    int grid = 0;
-    const cudaError_t err = m <= 100 ? launch_norm_list<100>(e, m, parts + used, &grid, st) : launch_norm_list<kMostTensors>(e, m, parts + used, &grid, st);
+    left -= m;
+    uint32_t* ticket = left == 0 ? static_cast<uint32_t*>(workspace) : nullptr;
+    const cudaError_t err = m <= 100 ? launch_norm_list<100>(e, m, out, ticket, st) : launch_norm_list<kMostTensors>(e, m, out, ticket, st);
     if (err != cudaSuccess) return err;
-    used += grid;
-  }
-  return launch_kernel(norm_end_kernel, dim3(1), dim3(1024), 0, st, true, 1, (const double*)parts, used, max_norm, norm, factor);
+  } while (left > 0);
+  return cudaSuccess;
 }
 
 }  // namespace optim

@@ -33,8 +33,8 @@ class GradTensor(ctypes.Structure):
 
 
 def grad_norm_workspace(grads):
-    """The workspace of grad_norm for this list of tensors."""
-    return torch.empty(max(1, int(_norm_workspace(len(grads)))), dtype=torch.uint8, device=grads[0].device if grads else "cuda")
+    """The workspace of grad_norm for this list of tensors (zeros before the first call; the calls leave it ready)."""
+    return torch.zeros(int(_norm_workspace(len(grads))), dtype=torch.uint8, device=grads[0].device if grads else "cuda")
 
 
 def grad_norm(grads, norm, workspace, max_norm=1.0, factor=None, stream=None):

@@ -2,7 +2,9 @@
 with 8-bit activation checkpoints.
 
   python examples/moe_block.py serve     one batch and then single tokens through the stack
-  python examples/moe_block.py train     a few SGD steps on a regression target
+  python examples/moe_block.py train     a few steps on a regression target: SGD, or AdamW over all weights in one
+                                         call (--optimizer adamw: fp32 masters and moments; adamw8: moments in
+                                         8 bits and no masters), with the gradients clipped (--clip)
 
 Serving: each block's norm adds the block before's output to the stream and writes the
 normalised rows once in bf16 (the router's input) and once in e4m3 (the experts'); the experts'
@@ -16,7 +18,7 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from top_routing_grouped_gb300 import fp8, moe  # noqa: E402
+from top_routing_grouped_gb300 import fp8, moe, optim  # noqa: E402
 
 DEV = "cuda"
 E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
@@ -119,6 +121,27 @@ class Trainer:
         return grads[::-1], dr
 
 
+NAMES = ("router", "w1", "w3", "w2", "norm")
+
+
+class Adam:
+    """AdamW over the weights of all blocks: one call for the gradients' norm, one for the step."""
+
+    def __init__(self, weights, lr, bits, clip):
+        params = [getattr(w, n) for w in weights for n in NAMES]
+        wide = [n == "norm" for _ in weights for n in NAMES]  # norms: fp32, moments in 32 bits, no decay
+        self.opt = optim.AdamW(params, lr=lr, weight_decay=[0.0 if n else 0.01 for n in wide], bits=[32 if n else bits for n in wide],
+                               masters=[p.float() if bits == 32 and not n else None for p, n in zip(params, wide)])
+        self.clip, self.ws = clip, optim.grad_norm_workspace(params)
+        self.norm, self.factor = (torch.zeros(1, device=DEV) for _ in range(2))
+
+    def step(self, grads):
+        g = [gr[n] for gr in grads for n in NAMES]
+        if self.clip:
+            optim.grad_norm(g, self.norm, self.ws, max_norm=self.clip, factor=self.factor)
+        self.opt.step(g, grad_factor=self.factor if self.clip else None)
+
+
 def serve(a):
     g = torch.Generator(device=DEV).manual_seed(0)
     ws = [Weights(a.d, a.experts, a.hidden, g) for _ in range(a.layers)]
@@ -137,14 +160,18 @@ def train(a):
     x = torch.randn(a.tokens, a.d, generator=g, device=DEV).to(torch.bfloat16)
     target = torch.randn(a.tokens, a.d, generator=g, device=DEV)
     t = Trainer(ws, a.tokens, a.d, a.experts, a.k, a.hidden)
+    adam = None if a.optimizer == "sgd" else Adam(ws, a.lr, 8 if a.optimizer == "adamw8" else 32, a.clip)
     losses = []
     for _ in range(a.steps):
         out = t.forward(x)
         diff = out - target
         losses.append(float(0.5 * diff.square().sum(1).mean()))
         grads, _ = t.backward(diff / a.tokens)
+        if adam:
+            adam.step(grads)
+            continue
         for w, gr in zip(ws, grads):
-            for name in ("router", "w1", "w3", "w2", "norm"):
+            for name in NAMES:
                 p = getattr(w, name)
                 p.copy_((p.float() - a.lr * gr[name]).to(p.dtype))
     print(f"loss over {a.steps} steps: {losses[0]:.4f} -> {losses[-1]:.4f}; checkpoint {t.ckpt[0].data.numel() / 2**20:.1f} MiB "
@@ -162,8 +189,12 @@ def main(argv=None):
     ap.add_argument("--k", type=int, default=2)
     ap.add_argument("--hidden", type=int, default=512)
     ap.add_argument("--steps", type=int, default=8)
-    ap.add_argument("--lr", type=float, default=0.2)
+    ap.add_argument("--optimizer", choices=("sgd", "adamw", "adamw8"), default="sgd")
+    ap.add_argument("--lr", type=float, help="0.2 with SGD, 0.001 with AdamW")
+    ap.add_argument("--clip", type=float, default=0.0, help="AdamW: the most that the gradients' norm may be; 0: any")
     a = ap.parse_args(argv)
+    if a.lr is None:
+        a.lr = 0.2 if a.optimizer == "sgd" else 1e-3
     return serve(a) if a.what == "serve" else train(a)
 
 

@@ -34,8 +34,8 @@ def np64(t):
 
 # ------------------------------------------------------------------ references
 
-def words(n, seed, step, tensor):
-    """The random word of every value."""
+def words(n, seed, step, tensor, first=0):
+    """The random word of every value from `first` (a multiple of 8) on."""
     mask = (1 << 32) - 1
 
     def mix(x):
@@ -47,7 +47,7 @@ def words(n, seed, step, tensor):
     for part in (seed & mask, seed >> 32, step & mask, tensor):
         key = mix(np.array((int(key) + part) & mask, np.uint64))
     out = np.empty((-(-n // 8), 8), np.uint64)
-    out[:, 0] = mix((np.arange(len(out), dtype=np.uint64) + np.uint64(int(key))) & np.uint64(mask))
+    out[:, 0] = mix((np.arange(len(out), dtype=np.uint64) + np.uint64(first // 8 + int(key))) & np.uint64(mask))
     for j in range(1, 8):
         out[:, j] = (out[:, j - 1] * np.uint64(0x3C6EF375) + np.uint64(0xA54FF53B)) & np.uint64(mask)
     return out.reshape(-1)[:n].astype(np.int64)
@@ -91,7 +91,7 @@ def sr_r(v, w, e):
     return by * np.where(up | ((lo == 0) & (v > 0)), hi, lo)
 
 
-def check_step(before, after, grad, i, *, step, seed, f=1.0, lr=LR, b1=B1, b2=B2, eps=EPS, wd=0.01, optim=None):
+def check_step(before, after, grad, i, *, step, seed, f=1.0, lr=LR, b1=B1, b2=B2, eps=EPS, wd=0.01, optim=None, first=0):
     """One tensor of a step: before / after = (param, master, state) on the CPU."""
     p, w, st = before
     g = np64(grad).reshape(-1) * f
@@ -103,7 +103,7 @@ def check_step(before, after, grad, i, *, step, seed, f=1.0, lr=LR, b1=B1, b2=B2
     rate = lr / (1 - b1 ** step)
     tol = U * (4 * np.abs(x) + 30 * rate * mt / den) + 2.0 ** -149
     x = x * (1 - lr * wd) - rate * m / den
-    rnd = words(len(x), seed, step, i)
+    rnd = words(len(x), seed, step, i, first)
     got = np64(after[0]).reshape(-1)
     if w is not None:
         kept = np64(after[1]).reshape(-1)
@@ -361,6 +361,68 @@ def test_a_step_is_the_same_every_time_and_for_a_list_in_parts(optim):
         results.append([copy(x[0]) for x in made])
     for a, b in zip(*results):
         assert torch.equal(a[0], b[0]) and all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a[2], b[2]))
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_more_values_than_32_bits_count(optim, bits):
+    """The end of a tensor of 2^32 + 5000 values, and its beginning."""
+    n = 2 ** 32 + 5000
+    if torch.cuda.mem_get_info()[0] < n * 14:
+        pytest.skip("not enough memory")
+    p, g = torch.zeros(n, dtype=BF, device="cuda"), torch.zeros(n, dtype=BF, device="cuda")
+    opt = optim.AdamW([p], lr=LR, betas=(B1, B2), eps=EPS, weight_decay=0.01, bits=bits, steps=3, seed=11)
+    parts = []
+    for first in (0, 2 ** 31 - 4096, 2 ** 32 - 4096, n - 5000 // 128 * 128 - 8):
+        m = min(4096, n - first)
+        (pp, _, st), gg = make((m,), BF, BF, bits, False, first % 97, optim)
+        first = first // 128 * 128
+        sl = slice(first, first + m)
+        p[sl], g[sl] = pp, gg
+        views = [t[first // 128:first // 128 + -(-m // 128)] if t.dtype == torch.float8_e8m0fnu else t[sl] for t in opt.state[0]]
+        for v, t in zip(views, st):
+            v.view(torch.uint8).copy_(t.view(torch.uint8))
+        parts.append((first, (p[sl], None, tuple(views)), copy((p[sl], None, tuple(views))), g[sl]))
+    opt.step([g])
+    for first, after, before, gr in parts:
+        check_step(before, copy(after), gr, 0, step=4, seed=11, optim=optim, first=first)
+    assert int(torch.count_nonzero(p[8192:2 ** 31 - 8192])) == 0
+    norm = torch.zeros(1, device="cuda")
+    optim.grad_norm([g], norm, optim.grad_norm_workspace([g]))
+    want = sum(float(x[3].double().square().sum()) for x in parts) ** 0.5
+    assert abs(float(norm) - want) <= 1e-6 * want
+
+
+@gpu
+def test_two_steps_at_once_and_a_given_stream(optim):
+    """Two optimisers on two streams give what they give one after the other."""
+    results = []
+    for streams in ((None, None), (torch.cuda.Stream(), torch.cuda.Stream())):
+        made = [[make((200_001,), BF, F32, 8, False, 20 + j, optim), make((3000,), F32, F32, 32, False, 30 + j, optim)] for j in range(2)]
+        opts = [take(optim, [x[0] for x in mm], None, seed=j) for j, mm in enumerate(made)]
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for o, mm, s in zip(opts, made, streams):
+                o.step([x[1] for x in mm], stream=s)
+        torch.cuda.synchronize()
+        assert [int(o.steps) for o in opts] == [10, 10]
+        results.append([copy(x[0]) for mm in made for x in mm])
+    for a, b in zip(*results):
+        assert torch.equal(a[0], b[0]) and all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a[2], b[2]))
+
+
+@gpu
+@pytest.mark.parametrize("optimizer", ["adamw", "adamw8"])
+def test_example_trains_with_it(optimizer):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_block.py")
+    spec = importlib.util.spec_from_file_location("moe_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    losses = m.main(["train", "--tokens", "96", "--layers", "2", "--d", "128", "--experts", "4", "--hidden", "128", "--steps", "3", "--optimizer", optimizer,
+                     "--clip", "1.0"])
+    assert len(losses) == 3 and all(np.isfinite(v) for v in losses)
 
 
 # ------------------------------------------------------------------ the norm

@@ -242,6 +242,42 @@ def test_captured_with_other_inputs_and_streams(rows):
         assert torch.equal(b["out"], 2 * b["x"])  # both of its rows come back
 
 
+def test_two_at_once_and_a_given_stream(rows):
+    T, k, E, d = 9000, 2, 16, 64
+    sets = [dict(idx=choice(T, k, E, s).cuda(), x=torch.randn(T, d, generator=gen(s)).cuda(), counts=full(E), pos=full(T, k), ws=rows.dispatch_workspace(T, k, E),
+                 xr=torch.zeros(T * k, d, device="cuda"), out=torch.zeros(T, d, device="cuda"), stream=torch.cuda.Stream()) for s in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for b in sets:
+            rows.dispatch(b["idx"], b["x"], b["counts"], b["pos"], b["xr"], b["ws"], stream=b["stream"])
+            rows.combine(b["xr"], b["pos"], b["out"], stream=b["stream"])
+    torch.cuda.synchronize()
+    for s, b in enumerate(sets):
+        np.testing.assert_array_equal(b["pos"].cpu().numpy(), sorted_ref(choice(T, k, E, s), E)[1])
+        assert torch.equal(b["out"], 2 * b["x"])
+
+
+@pytest.mark.parametrize("d", [8192, 8190])
+def test_rows_past_32_bits(rows, d):
+    """Rows at the end of buffers of more than 2^31 values (2^32 bytes)."""
+    R = 2 ** 31 // d + 100
+    if torch.cuda.mem_get_info()[0] < 5 * R * d:
+        pytest.skip("not enough memory")
+    y, x = torch.zeros(R, d, dtype=BF, device="cuda"), torch.randn(3, d, generator=gen(1)).to(BF).cuda()
+    pos, gates = torch.tensor([[R - 1, 0], [R - 2, R // 2], [-1, 5]], dtype=torch.int32, device="cuda"), torch.rand(3, 2, generator=gen(2)).cuda()
+    rows.gather(pos, x, y)
+    for t, j in ((0, 0), (0, 1), (1, 0), (1, 1), (2, 1)):
+        assert torch.equal(y[int(pos[t, j])], x[t])
+    out = torch.empty(3, d, device="cuda")
+    rows.combine(y, pos, out)
+    assert torch.equal(out, x.float() * torch.tensor([2.0, 2.0, 1.0], device="cuda")[:, None])
+    dg = full(3, 2, dtype=F32)
+    rows.combine_backward(x.float(), pos, gates, y_rows=y, dy_rows=y, dgates=dg)
+    own = x.double().square().sum(1, keepdim=True) * torch.tensor([[1, 1], [1, 1], [0, 1]], device="cuda")
+    assert ((dg.double() - own).abs() <= (d + 1) * 2.0 ** -24 * own).all()
+    assert torch.equal(y[R - 1], (gates[0, 0] * x[0].float()).to(BF)) and torch.equal(y[R // 2], (gates[1, 1] * x[1].float()).to(BF))
+
+
 def test_same_results_every_time(rows):
     T, k, E, d = 3000, 8, 64, 136
     idx, y, dout = choice(T, k, E, 1, 0.1).cuda(), torch.randn(T * k, d, device="cuda"), torch.randn(T, d, device="cuda")

@@ -161,6 +161,13 @@ def test_python_refusals(lib):
     for bad in (dict(weight_decay=[0.1]), dict(masters=[None]), dict(bits=16), dict(state=[(p[0],)] * 2), dict(params=[])):
         with pytest.raises(ValueError):
             optim.AdamW(**{**dict(params=p), **bad})
+    flat = torch.zeros(100)
+    for bad in ([flat, flat], [flat[:60], flat[59:]]):
+        with pytest.raises(ValueError, match="overlap"):
+            optim.AdamW(bad)
+    with pytest.raises(ValueError, match="overlap"):
+        optim.AdamW([flat], state=[(torch.zeros(100), flat)])
+    optim.AdamW([flat[:60], flat[60:]])
     opt = optim.AdamW(p, bits=[32, 8])
     g = [torch.zeros(3, 5), torch.zeros(7)]
     for bad in (g[:1], [g[0].T, g[1]], [g[0].half(), g[1]], [None, g[1]], 3, g):

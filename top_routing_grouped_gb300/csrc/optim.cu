@@ -379,6 +379,8 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Comm
 }
 
 // The same for values at a tensor's end, or off whole vectors: one by one.
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <bool kSmall>
 __device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, const Common& k, uint8_t* factors) {
   const int left = (int)max((int64_t)0, min(end - i, (int64_t)kPer));
@@ -457,6 +459,16 @@ __global__ void __launch_bounds__(Shape<kSmall>::kThreads, Shape<kSmall>::kCtas)
   const int ti = owner(b, blockIdx.x);
   const Entry& t = b.e[ti];
   const int64_t begin = (int64_t)(blockIdx.x - b.first[ti]) * b.chunk, end = min(begin + b.chunk, t.n);
+  const int64_t whole = t.index_flags & kVec ? begin + (end - begin) / kTile * kTile : begin;
+  // the first tile is on its way to L2 while the kernel before ends and the first thread works (twelve small blocks, 60
+  // tensors: 29.0 -> 27.9 us)
+  if (const int64_t i = begin + threadIdx.x * kPer; i < whole) {
+    prefetch(static_cast<const char*>(t.grad) + i * (t.index_flags & kGradBf16 ? 2 : 4));
+    if (t.master) prefetch(t.master + i);
+    else prefetch(static_cast<const char*>(t.param) + i * (t.index_flags & kParamBf16 ? 2 : 4));
+    prefetch(static_cast<const char*>(t.m) + i * (kSmall ? 1 : 4));
+    prefetch(static_cast<const char*>(t.v) + i * (kSmall ? 1 : 4));
+  }
   int64_t taken;
   bool raise = false;
   pdl_wait();
@@ -483,7 +495,6 @@ __global__ void __launch_bounds__(Shape<kSmall>::kThreads, Shape<kSmall>::kCtas)
     }
   __syncthreads();
   const Common k = common;
-  const int64_t whole = t.index_flags & kVec ? begin + (end - begin) / kTile * kTile : begin;
   if (!skip) {
     const bool g = t.index_flags & kGradBf16;
     if (t.master) g ? step_tiles<kMaster, true, kSmall>(t, begin, whole, k, factors) : step_tiles<kMaster, false, kSmall>(t, begin, whole, k, factors);

@@ -23,13 +23,14 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // ------------------------------------------------------------------ sort and gather
 
+// Read out of L2, past L1: a kernel may do so before it has waited for the one before it (sort_kernel, rows_kernel).
 template <bool kIdx64>
 __device__ __forceinline__ int expert_of(const Args& a, int64_t slot) {
   if constexpr (kIdx64) {
-    const long long v = static_cast<const long long*>(a.idx)[slot];
+    const long long v = __ldcg(static_cast<const long long*>(a.idx) + slot);
     return (unsigned long long)v < (unsigned long long)a.E ? (int)v : -1;
   } else {
-    const int v = static_cast<const int*>(a.idx)[slot];
+    const int v = __ldcg(static_cast<const int*>(a.idx) + slot);
     return (unsigned)v < (unsigned)a.E ? v : -1;
   }
 }
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
     const V* src = reinterpret_cast<const V*>(a.x + (t0 + t) * a.ld_bytes);
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      if (v0 + u * 32 < v_end) buf[u] = __ldcs(src + v0 + u * 32);
+      if (v0 + u * 32 < v_end) buf[u] = __ldcg(src + v0 + u * 32);
   };
 
   if constexpr (!kSort) {

@@ -66,7 +66,7 @@ class AdamW:
     """AdamW over a list of parameters, in place (moe_adamw).  All that a step changes are tensors that the
     caller may keep and save: the parameters, ``masters``, ``state`` and ``steps``.
 
-    params: fp32 or bf16, contiguous, on one GPU.  masters: None, or a list with an fp32 tensor or None for each:
+    params: fp32 or bf16, contiguous, on one GPU; no two of them share memory.  masters: None, or a list with an fp32 tensor or None for each:
     a bf16 parameter with a master is rounded from it, one without is rounded stochastically.  weight_decay:
     one for all, or a list.  bits: 32 or 8, of the moments, one for all or a list; ignored with state, a list
     of what new_state makes.  steps: the steps taken so far, a number or an int64 tensor of shape (1,) on
@@ -87,6 +87,9 @@ class AdamW:
         self.weight_decay = tuple(float(v) for v in each(weight_decay))
         self.state = tuple(new_state(p, b) for p, b in zip(self.params, each(bits))) if state is None else each(tuple(map(tuple, state)))
         _want(all(len(s) in (2, 4) for s in self.state), "a state is (m, v) or (m, m_scales, r, r_scales)")
+        written = sorted((t.data_ptr(), t.numel() * t.element_size()) for t in (*self.params, *(w for w in self.masters if w is not None),
+                                                                                *(t for s in self.state for t in s)) if t.numel())
+        _want(all(a + n <= b for (a, n), (b, _) in zip(written, written[1:])), "two of the tensors that a step writes overlap")
         self.lr, self.betas, self.eps, self.seed = lr, (float(betas[0]), float(betas[1])), float(eps), int(seed)
         device = self.params[0].device
         self.steps = steps if isinstance(steps, torch.Tensor) else torch.full((1,), int(steps), dtype=torch.int64, device=device)

@@ -92,7 +92,14 @@ def source(T, d, dtype, seed, lay="plain"):
 DISPATCHES = [(1, 4, 64, 4096, F8, "plain", 0), (1, 1, 1, 1, F8, "plain", 0), (3, 2, 4, 16384, F32, "plain", 0), (13, 8, 32, 2048, BF, "plain", 0),
               (1029, 8, 128, 2050, BF, "pitched", 0.5), (257, 5, 7, 333, BF, "shifted", 0.1), (64, 3, 60, 1000, F32, "shifted", 0),
               (100, 2, 8, 129, F8, "shifted", 0.3), (3000, 8, 32, 264, F8, "plain", 0.2), (2600, 8, 256, 72, F32, "pitched", 0.75),
-              (17, 64, 300, 520, BF, "plain", 0), (9000, 2, 16, 20, BF, "plain", 0), (20, 2, 4, 40000, BF, "pitched", 0)]
+              (17, 64, 300, 520, BF, "plain", 0), (9000, 2, 16, 20, BF, "plain", 0), (20, 2, 4, 40000, BF, "pitched", 0),
+              # rows off 4-byte boundaries: shorter than a vector, a few of them, longer than a warp's share; few slots and many
+              (37, 3, 5, 3, F8, "plain", 0.1), (37, 3, 5, 15, F8, "plain", 0), (501, 3, 5, 17, F8, "shifted", 0), (45, 7, 9, 65, F8, "plain", 0),
+              (2000, 4, 9, 65, F8, "pitched", 0.1), (300, 2, 9, 4095, F8, "plain", 0), (3, 4, 8, 9001, F8, "plain", 0), (700, 8, 64, 2047, BF, "plain", 0.1),
+              (21, 2, 4, 1, BF, "shifted", 0), (1500, 4, 4, 7, BF, "plain", 0), (600, 9, 16, 129, BF, "pitched", 0),
+              # short rows, several a warp
+              (1, 1, 2, 16, F8, "plain", 0), (77, 5, 8, 64, F8, "plain", 0.2), (5001, 2, 8, 64, BF, "plain", 0.1), (901, 5, 8, 40, F32, "plain", 0),
+              (333, 16, 32, 128, F32, "pitched", 0), (90, 64, 100, 9, F32, "plain", 0.3)]
 
 
 @pytest.mark.parametrize("T, k, E, d, dtype, lay, drop", DISPATCHES)
@@ -136,7 +143,13 @@ def positions(T, k, R, seed, bad=0.2):
 # T, k, d, R, y's type, the other's type, offset in values of y and out
 COMBINES = [(1, 1, 1, 1, BF, BF, 0), (1, 8, 7552, 8, BF, F32, 0), (13, 8, 2048, 104, BF, BF, 0), (257, 4, 1000, 900, F32, F32, 0),
             (300, 6, 2050, 1800, BF, BF, 0), (65, 2, 333, 130, F32, BF, 0), (40, 16, 264, 640, BF, BF, 1), (37, 64, 516, 2400, F32, F32, 1),
-            (20, 33, 72, 660, BF, F32, 4), (5000, 2, 40, 9000, F32, F32, 2), (3, 2, 20000, 6, BF, BF, 0), (9, 3, 64, 0, BF, BF, 0)]
+            (20, 33, 72, 660, BF, F32, 4), (5000, 2, 40, 9000, F32, F32, 2), (3, 2, 20000, 6, BF, BF, 0), (9, 3, 64, 0, BF, BF, 0),
+            # short rows, several a warp, with fewer and more slots than lanes; every width of access
+            (1001, 1, 64, 1100, BF, BF, 0), (333, 2, 128, 700, BF, F32, 0), (77, 64, 8, 5000, BF, BF, 0), (50, 40, 96, 2100, F32, BF, 0), (129, 9, 7, 1200, BF, BF, 0),
+            (129, 9, 33, 1200, F32, F32, 0), (211, 5, 62, 1100, BF, F32, 0), (64, 17, 30, 1100, F32, BF, 1), (1, 1, 3, 1, F32, F32, 0),
+            # and long ones
+            (70, 1, 2051, 70, BF, F32, 0), (70, 2, 2046, 140, BF, BF, 0), (70, 4, 1027, 280, F32, F32, 0), (33, 5, 2052, 165, BF, BF, 0), (40, 3, 1026, 120, F32, F32, 2),
+            (300, 1, 4096, 300, F32, BF, 0), (300, 2, 4096, 600, BF, BF, 0)]
 
 
 def at(t, offset):

@@ -21,6 +21,43 @@ constexpr int kSortCtas = 152 * 2;
 constexpr int64_t kSortFew = 4096;
 constexpr unsigned kAll = 0xffffffffu;
 
+// ------------------------------------------------------------------ rows off 16-byte boundaries
+
+// Sixteen bytes from any address, out of the two 16-byte words of memory that they lie in; [lo, hi) is what may be
+// read.  Two loads and a shift: that pays for moving rows off 4-byte boundaries, not for others and not where the rows are
+// computed with (16384 tokens to 4 rows each; loads of the alignment's own size -> this: moving 4095 bytes 145 -> 74 us,
+// 2047 bf16 82 -> 71, 1023 fp32 59 -> 72; combining 2047 bf16 121 -> 138 us; its backward 153 -> 189).
+__device__ __forceinline__ uint4 load_any(const void* at, const void* lo, const void* hi) {
+  const char* p = static_cast<const char*>(at);
+  const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+  const char* base = p - off;
+  if (off == 0) return *reinterpret_cast<const uint4*>(base);
+  if (base < lo || base + 32 > hi) {  // at an array's ends
+    uint64_t w[2] = {0, 0};
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      const uint64_t v = (uint64_t)(uint8_t)p[i] << 8 * (i & 7);
+      w[0] |= i < 8 ? v : 0;
+      w[1] |= i < 8 ? 0 : v;
+    }
+    return make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
+  }
+  const uint4 a = reinterpret_cast<const uint4*>(base)[0], b = reinterpret_cast<const uint4*>(base)[1];
+  const bool two = off & 8, one = off & 4;
+  const uint32_t w0 = two ? a.z : a.x, w1 = two ? a.w : a.y, w2 = two ? b.x : a.z, w3 = two ? b.y : a.w, w4 = two ? b.z : b.x, w5 = two ? b.w : b.y;
+  const uint32_t x0 = one ? w1 : w0, x1 = one ? w2 : w1, x2 = one ? w3 : w2, x3 = one ? w4 : w3, x4 = one ? w5 : w4;
+  const int bits = off % 4 * 8;
+  return make_uint4(__funnelshift_r(x0, x1, bits), __funnelshift_r(x1, x2, bits), __funnelshift_r(x2, x3, bits), __funnelshift_r(x3, x4, bits));
+}
+
+// Lanes that share a token: all 32, or as few as hold a short row's `pieces`.  The kernels know 32 beforehand (kLanes;
+// 0: what they are given), which saves a third of the registers of some.
+int lanes_for(int64_t pieces) {
+  int n = 8;
+  while (n < 32 && n < pieces) n *= 2;
+  return n;
+}
+
 // ------------------------------------------------------------------ sort and gather
 
 // Read out of L2, past L1: a kernel may do so before it has waited for the one before it (sort_kernel, rows_kernel).
@@ -146,6 +183,7 @@ struct Ranks {
   }
 };
 
+
 // What a sort writes of slot s, whose row is p.
 __device__ __forceinline__ void write_slot(const Args& a, int64_t s, int p) {
   a.slot_pos[s] = p;
@@ -196,18 +234,30 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(Args a, int64_t per_
   const int groups = quads < kSortThreads ? kSortThreads / quads : 1;
   for (int i = threadIdx.x; i < groups * quads; i += kSortThreads) {
     const int q = i % quads;
-    int4 less = make_int4(0, 0, 0, 0), more = less;
-#pragma unroll 16
-    for (int b = i / quads; b < (int)gridDim.x; b += groups) {
-      const int4 c = *reinterpret_cast<const int4*>(counted + (int64_t)b * pitch + 4 * q);
-      int4& to = b < (int)blockIdx.x ? less : more;
-      to.x += c.x, to.y += c.y, to.z += c.z, to.w += c.w;
+    constexpr int kU = 10;  // loads under way: one after the other they cost 0.5 us each (16 us, not 7, for 256 experts)
+    int all[4] = {0, 0, 0, 0}, less[4] = {0, 0, 0, 0};
+    for (int b0 = i / quads; b0 < (int)gridDim.x; b0 += kU * groups) {
+      int4 c[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int b = b0 + u * groups;
+        c[u] = b < (int)gridDim.x ? *reinterpret_cast<const int4*>(counted + (int64_t)b * pitch + 4 * q) : make_int4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int v[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+        const bool ahead = b0 + u * groups < (int)blockIdx.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          all[j] += v[j];
+          less[j] += ahead ? v[j] : 0;
+        }
+      }
     }
-    const int l[4] = {less.x, less.y, less.z, less.w}, m[4] = {more.x, more.y, more.z, more.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (l[j]) atomicAdd(&before[4 * q + j], l[j]);
-      if (m[j]) atomicAdd(&rest[4 * q + j], m[j]);
+      if (less[j]) atomicAdd(&before[4 * q + j], less[j]);
+      if (all[j] != less[j]) atomicAdd(&rest[4 * q + j], all[j] - less[j]);
     }
   }
   const int kept = ranks.rank(
@@ -220,32 +270,40 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(Args a, int64_t per_
 }
 
 // The rows' way.  Each CTA takes `tokens` tokens (grid.y: a share of their columns).  With kSort, for few slots,
-// it first sorts them: each CTA counts all of them by itself, out of L2, and ranks its own.  A warp moves kVecs
-// vectors of a token at a time: it reads them once and writes them to each of the token's rows.  The first ones are
-// on their way while the positions are found; `early`: even while the previous kernel, a sort of the same call that
-// has waited for what was before it, ends.
-template <typename V, bool kSort, bool kIdx64>
-__global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int64_t vecs_y, bool early) {
+// it first sorts them: each CTA counts all of them by itself, out of L2, and ranks its own.  `lanes` lanes move up to
+// 4 * lanes vectors of a token at a time: they read them once and write them to each of the token's rows.  The
+// first ones are on their way while the positions are found; `early`: even while the previous kernel, a sort of the same
+// call that has waited for what was before it, ends.
+// kSize 0: all rows begin and end on boundaries of V.  Else they are values of kSize bytes, and each row is written
+// in whole 16-byte vectors of its own alignment, which are read from wherever they lie in x.
+template <typename V, int kSize, bool kSort, bool kIdx64, int kLanes>
+__global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int64_t vecs_y, bool early, int given_lanes) {
+  const int lanes = kLanes ? kLanes : given_lanes;
   extern __shared__ int shared[];
   int* pos = shared;  // [tokens * k]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x % lanes, warp = threadIdx.x >> 5, of_warp = 32 / lanes, mine = (threadIdx.x & 31) / lanes;
   const int64_t t0 = (int64_t)blockIdx.x * tokens, s0 = t0 * a.k;
   const int nt = (int)min((int64_t)tokens, a.T - t0), own = nt * a.k;
   const bool first = blockIdx.y == 0;  // writes what does not depend on the columns
 
   constexpr int kU = kVecs / 32;
   const int64_t vecs = a.row_bytes / (int64_t)sizeof(V), v_first = blockIdx.y * vecs_y, v_end = min(v_first + vecs_y, vecs);
-  const int segs = (int)((v_end - v_first + kVecs - 1) / kVecs), units = nt * segs;
+  const int segs = v_end == 0 && a.row_bytes > 0 ? 1 : (int)((v_end - v_first + lanes * kU - 1) / (lanes * kU)), units = (nt + of_warp - 1) / of_warp * segs;
   int t, unit = warp;
   int64_t v0;
   V buf[kU];
-  const auto fetch = [&] {
+  const auto place = [&] {
     t = unit / segs;
-    v0 = v_first + (int64_t)(unit - t * segs) * kVecs + lane;
+    v0 = v_first + (int64_t)(unit - t * segs) * lanes * kU + lane;
+    t = t * of_warp + mine;
+  };
+  const auto fetch = [&] {
+    place();
+    if (kSize != 0 || t >= nt) return;
     const V* src = reinterpret_cast<const V*>(a.x + (t0 + t) * a.ld_bytes);
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      if (v0 + u * 32 < v_end) buf[u] = __ldcg(src + v0 + u * 32);
+      if (v0 + u * lanes < v_end) buf[u] = __ldcg(src + v0 + u * lanes);
   };
 
   if constexpr (!kSort) {
@@ -281,14 +339,36 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
       for (int64_t p = max(s0, (int64_t)kept) + threadIdx.x; p < s0 + own; p += kThreads) a.row_slot[p] = -1;
   }
   __syncthreads();
+  const char* x_end = a.x + (a.T - 1) * a.ld_bytes + a.row_bytes;
   while (unit < units) {
-    for (int j = 0; j < a.k; ++j) {
+    for (int j = 0; t < nt && j < a.k; ++j) {
       const int p = pos[t * a.k + j];
       if (p < 0 || p >= a.R) continue;
-      V* dst = reinterpret_cast<V*>(a.x_rows + p * a.row_bytes);
+      char* row = a.x_rows + p * a.row_bytes;
+      if constexpr (kSize == 0) {
+        V* dst = reinterpret_cast<V*>(row);
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (v0 + u * 32 < v_end) __stcs(dst + v0 + u * 32, buf[u]);
+        for (int u = 0; u < kU; ++u)
+          if (v0 + u * lanes < v_end) __stcs(dst + v0 + u * lanes, buf[u]);
+      } else {
+        const char* src = a.x + (t0 + t) * a.ld_bytes;
+        const int head = (int)min(a.row_bytes, (int64_t)(-reinterpret_cast<uintptr_t>(row) & 15));  // bytes to its first boundary
+        const int64_t whole = (a.row_bytes - head) / 16, v_last = min(v_end, whole);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (v0 + u * lanes < v_last) buf[u] = load_any(src + head + 16 * (v0 + u * lanes), a.x, x_end);
+        if (v0 == lane) {  // and what lies before and behind the whole vectors, a value a lane
+          using Value = typename std::conditional<kSize == 2, uint16_t, uint8_t>::type;
+          const int64_t gap = 16 * whole;
+          for (int64_t i = lane * kSize; i < a.row_bytes - gap; i += lanes * kSize) {
+            const int64_t b = i < head ? i : i + gap;
+            *reinterpret_cast<Value*>(row + b) = *reinterpret_cast<const Value*>(src + b);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (v0 + u * lanes < v_last) __stcs(reinterpret_cast<uint4*>(row + head + 16 * (v0 + u * lanes)), buf[u]);
+      }
     }
     unit += kWarps;
     if (unit < units) fetch();
@@ -306,18 +386,20 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
   }
 }
 
-template <typename V, bool kSort, bool kIdx64>
+template <typename V, int kSize, bool kSort, bool kIdx64>
 cudaError_t launch_as(const Args& a, bool early, cudaStream_t st) {
-  const int64_t vecs = a.row_bytes / (int64_t)sizeof(V), segs = (vecs + kVecs - 1) / kVecs;
-  // Tokens a CTA: a segment for each warp; where each CTA counts all slots, no more CTAs than kSortCtas.
-  int64_t tokens = segs ? (kWarps + segs - 1) / segs : (kThreads + a.k - 1) / a.k;
+  const int64_t vecs = a.row_bytes / (int64_t)sizeof(V);
+  const int lanes = lanes_for(vecs);
+  const int64_t most_vecs = lanes * (kVecs / 32), segs = vecs == 0 && a.row_bytes > 0 ? 1 : (vecs + most_vecs - 1) / most_vecs;
+  // Tokens a CTA: a segment for each group of lanes; where each CTA counts all slots, no more CTAs than kSortCtas.
+  int64_t tokens = segs ? (kThreads / lanes + segs - 1) / segs : (kThreads + a.k - 1) / a.k;
   if (kSort && tokens < (a.T + kSortCtas - 1) / kSortCtas) tokens = (a.T + kSortCtas - 1) / kSortCtas;
   if (tokens > kMaxPositions / a.k) tokens = kMaxPositions / a.k;
   if (tokens > a.T) tokens = a.T;
   const int64_t gx = (a.T + tokens - 1) / tokens;
   // columns of a few tokens' long rows are shared out
   int64_t gy = 1, vecs_y = vecs;
-  if (segs > 0 && gx < kSortCtas) {
+  if (segs > 1 && gx < kSortCtas) {
     gy = (tokens * segs + kWarps - 1) / kWarps;
     if (gy > kSortCtas / gx) gy = kSortCtas / gx;
     if (gy > segs) gy = segs;
@@ -325,18 +407,19 @@ cudaError_t launch_as(const Args& a, bool early, cudaStream_t st) {
     gy = (vecs + vecs_y - 1) / vecs_y;
   }
   const size_t smem = ((size_t)tokens * a.k + (kSort ? (size_t)(2 + kWarps) * a.E : 0)) * sizeof(int);
+  const auto kernel = lanes == 32 ? rows_kernel<V, kSize, kSort, kIdx64, 32> : rows_kernel<V, kSize, kSort, kIdx64, 0>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<V, kSort, kIdx64>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
     if (e != cudaSuccess) return e;
   }
-  return launch_kernel(rows_kernel<V, kSort, kIdx64>, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), smem, st, true, 1, a, (int)tokens,
-                       vecs_y, early);
+  return launch_kernel(kernel, dim3((unsigned)gx, (unsigned)gy), dim3(kThreads), smem, st, true, 1, a, (int)tokens,
+                       vecs_y, early, lanes);
 }
 
-template <typename V>
+template <typename V, int kSize>
 cudaError_t launch_vec(const Args& a, bool sort, cudaStream_t st) {
-  if (!sort) return launch_as<V, false, false>(a, a.idx != nullptr, st);
-  return a.idx64 ? launch_as<V, true, true>(a, false, st) : launch_as<V, true, false>(a, false, st);
+  if (!sort) return launch_as<V, kSize, false, false>(a, a.idx != nullptr, st);
+  return a.idx64 ? launch_as<V, kSize, true, true>(a, false, st) : launch_as<V, kSize, true, false>(a, false, st);
 }
 
 template <bool kIdx64>
@@ -356,14 +439,14 @@ cudaError_t launch_sort(const Args& a, int32_t* counted, cudaStream_t st) {
 
 // ------------------------------------------------------------------ combine
 
-// n values of type T on a boundary of n * sizeof(T) bytes, 16 at most at a time, to and from fp32.
+// n values of type T, 16 bytes at most at a time, to and from fp32.
 template <typename T, int n>
 struct Values {
   static constexpr int kBytes = n * (int)sizeof(T) < 16 ? n * (int)sizeof(T) : 16, kParts = n * (int)sizeof(T) / kBytes;
   using Part = typename std::conditional<kBytes == 16, uint4,
                typename std::conditional<kBytes == 8, uint2, typename std::conditional<kBytes == 4, uint32_t, uint16_t>::type>::type>::type;
   Part part[kParts];
-  __device__ __forceinline__ void load(const T* p) {
+  __device__ __forceinline__ void load(const T* p) {  // on a boundary of kBytes
 #pragma unroll
     for (int i = 0; i < kParts; ++i) part[i] = __ldcs(reinterpret_cast<const Part*>(p) + i);
   }
@@ -382,24 +465,26 @@ struct Values {
   }
 };
 
-// One warp for 32 V C columns of one token, C pieces of V a lane: kJ rows in flight at a time, summed in the
-// slots' order.  What counts is that a lane has 64 bytes of rows under way: for one slot a token, four pieces of
-// its row, not one of up to four rows (16384 x 2048 bf16: 36.8 -> KJ1 us); where rows lie on 4-byte boundaries
-// only, four pieces too (2048 x 2050, 16 slots: 43.5 -> ODD us).
-template <typename Ty, typename To, int V, int C, int kJ>
-__global__ void __launch_bounds__(kThreads, V * (int)sizeof(Ty) * C == 16 ? 6 : 4) combine_kernel(const Ty* y, int64_t R, const int32_t* slot_pos,
-                                                                               const float* gates, int64_t T, int k, int64_t d,
-                                                                               unsigned segs, const To* residual, To* out) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+// `lanes` lanes for lanes * V * C columns of one token, C pieces of V a lane: kJ rows in flight at a time, summed in the
+// slots' order.  What counts is the bytes of rows that a lane has under way: for one slot a token, four pieces of its row,
+// not one of up to four rows (16384 x 2048 bf16: 36.8 -> 23.4 us); where rows lie on 4-byte boundaries, four or eight
+// pieces of four rows (4 slots of 2044 bf16: 124 -> 79 us, 1023 fp32 108 -> 65, 2047 bf16 206 -> 121).
+template <typename Ty, typename To, int V, int C, int kJ, int kLanes>
+__global__ void __launch_bounds__(kThreads, C == 1 && kLanes ? 6 : 4) combine_kernel(const Ty* y, int64_t R, const int32_t* slot_pos,
+                                                                                    const float* gates, int64_t T, int k, int64_t d,
+                                                                                    unsigned segs, int given_lanes, const To* residual,
+                                                                                    To* out) {
+  const int lanes = kLanes ? kLanes : given_lanes;
+  const int lane = threadIdx.x % lanes;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / lanes;
   const int64_t t = unit <= 0xffffffffll ? (int64_t)((unsigned)unit / segs) : unit / segs;
   pdl_wait();
   pdl_launch_dependents();
-  if (t >= T) return;
-  const int64_t c = ((unit - t * segs) * 32 * C + lane) * V;
-  const auto col = [&](int x) { return c + x * 32 * V; };
+  const bool has = t < T;
+  const int64_t piece = (unit - t * segs) * lanes * C + lane;
+  const auto col = [&](int x) { return (piece + x * lanes) * V; };
   Values<To, V> res[C];
-  if (residual) {
+  if (residual && has) {
 #pragma unroll
     for (int x = 0; x < C; ++x)
       if (col(x) < d) res[x].load(residual + t * d + col(x));
@@ -409,11 +494,11 @@ __global__ void __launch_bounds__(kThreads, V * (int)sizeof(Ty) * C == 16 ? 6 : 
   for (int x = 0; x < C; ++x)
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[x][i] = 0.f;
-  for (int j0 = 0; j0 < k; j0 += 32) {
-    const int n = min(32, k - j0);
+  for (int j0 = 0; j0 < k; j0 += lanes) {
+    const int n = min(lanes, k - j0);
     int p = -1;
     float g = 1.f;
-    if (lane < n) {
+    if (has && lane < n) {
       p = slot_pos[t * k + j0 + lane];
       if (gates) g = gates[t * k + j0 + lane];
     }
@@ -423,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, V * (int)sizeof(Ty) * C == 16 ? 6 : 
       int at[kJ];
 #pragma unroll
       for (int q = 0; q < kJ; ++q) {
-        at[q] = __shfl_sync(kAll, p, j + q);  // lanes past n hold -1
+        at[q] = __shfl_sync(kAll, p, j + q, lanes);  // lanes past n hold -1
         if (at[q] < 0) continue;
 #pragma unroll
         for (int x = 0; x < C; ++x)
@@ -431,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, V * (int)sizeof(Ty) * C == 16 ? 6 : 
       }
 #pragma unroll
       for (int q = 0; q < kJ; ++q) {
-        const float gq = __shfl_sync(kAll, g, j + q);
+        const float gq = __shfl_sync(kAll, g, j + q, lanes);
         if (at[q] < 0) continue;
 #pragma unroll
         for (int x = 0; x < C; ++x)
@@ -442,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, V * (int)sizeof(Ty) * C == 16 ? 6 : 
   }
 #pragma unroll
   for (int x = 0; x < C; ++x) {
-    if (col(x) >= d) continue;
+    if (!has || col(x) >= d) continue;
     Values<To, V> o;
 #pragma unroll
     for (int i = 0; i < V; ++i) o.set(i, residual ? res[x].get(i) + acc[x][i] : acc[x][i]);
@@ -450,23 +535,27 @@ __global__ void __launch_bounds__(kThreads, V * (int)sizeof(Ty) * C == 16 ? 6 : 
   }
 }
 
-template <typename Ty, typename To, int V, int C, int kJ>
+template <typename Ty, typename To, int V, int C, int kJ, int kLanes>
 cudaError_t combine_as(const void* y, int64_t R, const int32_t* slot_pos, const float* gates, int64_t T, int k, int64_t d,
                        const void* residual, void* out, cudaStream_t st) {
-  const int64_t segs = (d + 32 * V * C - 1) / (32 * V * C), blocks = (T * segs + kWarps - 1) / kWarps;
-  return launch_kernel(combine_kernel<Ty, To, V, C, kJ>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, 1, static_cast<const Ty*>(y),
-                       R, slot_pos, gates, T, k, d, (unsigned)segs, static_cast<const To*>(residual), static_cast<To*>(out));
+  const int64_t pieces = d / V;
+  const int lanes = kLanes ? kLanes : lanes_for((pieces + C - 1) / C);
+  const int64_t segs = (pieces + lanes * C - 1) / (lanes * C), of_block = kThreads / lanes, blocks = (T * segs + of_block - 1) / of_block;
+  return launch_kernel(combine_kernel<Ty, To, V, C, kJ, kLanes>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, 1,
+                       static_cast<const Ty*>(y), R, slot_pos, gates, T, k, d, (unsigned)segs, lanes, static_cast<const To*>(residual),
+                       static_cast<To*>(out));
 }
 
-// The gradients: `per` warps a token, each lane C pieces of V columns at a time of up to kJ rows; the products with
-// dout are summed over the lanes, and over the warps in order.
-template <typename Td, typename Ty, int V, int C, int kJ>
+// The gradients: `per` warps a token, or `lanes` lanes of one; each lane C pieces of V columns at a time of up to kJ rows;
+// the products with dout are summed over the lanes, and over the warps in order.
+template <typename Td, typename Ty, int V, int C, int kJ, int kLanes>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Td* dout, const int32_t* slot_pos, const float* gates,
                                                                     int64_t T, int k, int64_t d, int64_t R, const Ty* y, Ty* dy,
-                                                                    float* dgates, int per) {
+                                                                    float* dgates, int per, int given_lanes) {
   __shared__ float part[kWarps][kJ];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % per;
-  const int64_t t = (int64_t)blockIdx.x * (kWarps / per) + warp / per;
+  const int lanes = kLanes ? kLanes : given_lanes;
+  const int lane = threadIdx.x % lanes, warp = threadIdx.x >> 5, mine = warp % per;
+  const int64_t t = ((int64_t)blockIdx.x * (kWarps / per) + warp / per) * (32 / lanes) + (threadIdx.x & 31) / lanes;
   pdl_wait();
   pdl_launch_dependents();
   const bool has = t < T;
@@ -483,13 +572,13 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Td* do
     float gate[kJ], dot[kJ];
 #pragma unroll
     for (int q = 0; q < kJ; ++q) {
-      at[q] = __shfl_sync(kAll, p, q);
-      gate[q] = __shfl_sync(kAll, g, q);
+      at[q] = __shfl_sync(kAll, p, q, lanes);
+      gate[q] = __shfl_sync(kAll, g, q, lanes);
       dot[q] = 0.f;
     }
     if (has) {
-      for (int64_t c = (mine * 32 * C + lane) * V; c < d; c += per * 32 * V * C) {
-        const auto col = [&](int x) { return c + x * 32 * V; };
+      for (int64_t c = (mine * lanes * C + lane) * V; c < d; c += per * lanes * V * C) {
+        const auto col = [&](int x) { return c + x * lanes * V; };
         Values<Td, V> go[C];
 #pragma unroll
         for (int x = 0; x < C; ++x)
@@ -527,7 +616,8 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Td* do
 #pragma unroll
       for (int q = 0; q < kJ; ++q) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot[q] += __shfl_xor_sync(kAll, dot[q], o);
+        for (int o = 16; o > 0; o >>= 1)
+          if (o < lanes) dot[q] += __shfl_xor_sync(kAll, dot[q], o);
         if (lane == q) sum = dot[q];
       }
       if (per > 1) {
@@ -544,21 +634,22 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Td* do
   }
 }
 
-template <typename Td, typename Ty, int V, int C, int kJ>
+template <typename Td, typename Ty, int V, int C, int kJ, int kLanes>
 cudaError_t backward_as(const void* dout, const int32_t* slot_pos, const float* gates, int64_t T, int k, int64_t d, int64_t R,
                         const void* y, void* dy, float* dgates, cudaStream_t st) {
+  const int lanes = kLanes ? kLanes : lanes_for((d / V + C - 1) / C);
   // warps a token: each has its columns in kTurns turns at most, as long as there are tokens for all
   constexpr int kTurns = 4;
   int per = 1;
-  while (per < kWarps && (int64_t)per * 32 * V * C * (T * per < 152 * 16 ? 1 : kTurns) < d) per *= 2;
-  const int64_t blocks = (T + kWarps / per - 1) / (kWarps / per);
-  return launch_kernel(combine_backward_kernel<Td, Ty, V, C, kJ>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, 1,
+  while (lanes == 32 && per < kWarps && (int64_t)per * 32 * V * C * (T * per < 152 * 16 ? 1 : kTurns) < d) per *= 2;
+  const int64_t of_block = kThreads / (per * lanes), blocks = (T + of_block - 1) / of_block;
+  return launch_kernel(combine_backward_kernel<Td, Ty, V, C, kJ, kLanes>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, 1,
                        static_cast<const Td*>(dout), slot_pos, gates, T, k, d, R, static_cast<const Ty*>(y), static_cast<Ty*>(dy),
-                       dgates, per);
+                       dgates, per, lanes);
 }
 
-// How many values a lane takes at once: `most`, 2 or 1, so many that they divide a row and that all these addresses
-// are on boundaries of them (16 bytes do for more than 16).
+// How many values a lane takes at once: `most`, 2 or 1, so many that they divide a row and that all these arrays (address,
+// bytes a value) are on boundaries of them, 16 bytes doing for more than 16.
 int values_at_once(int most, int64_t d, std::initializer_list<std::pair<const void*, int>> arrays) {
   for (const int v : {most, 2}) {
     bool fits = d % v == 0;
@@ -582,11 +673,11 @@ cudaError_t launch_rows(const Args& args, int32_t* counted, cudaStream_t st) {
     sort = false;
   }
   const uintptr_t b = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.x_rows) | (uintptr_t)a.row_bytes | (uintptr_t)a.ld_bytes;
-  if (b % 16 == 0) return launch_vec<uint4>(a, sort, st);
-  if (b % 8 == 0) return launch_vec<uint2>(a, sort, st);
-  if (b % 4 == 0) return launch_vec<uint32_t>(a, sort, st);
-  if (b % 2 == 0) return launch_vec<uint16_t>(a, sort, st);
-  return launch_vec<uint8_t>(a, sort, st);
+  if (b % 16 == 0) return launch_vec<uint4, 0>(a, sort, st);
+  if (b % 8 == 0) return launch_vec<uint2, 0>(a, sort, st);
+  if (b % 4 == 0) return launch_vec<uint32_t, 0>(a, sort, st);
+  if (b % 2 == 0) return launch_vec<uint4, 2>(a, sort, st);
+  return launch_vec<uint4, 1>(a, sort, st);
 }
 
 using bf16 = __nv_bfloat16;
@@ -598,11 +689,15 @@ cudaError_t launch_combine(const void* y, bool y_bf16, int64_t R, const int32_t*
     using Ty = decltype(ty);
     using To = decltype(to);
     constexpr int kV = 16 / sizeof(Ty);
-    return v == 1   ? combine_as<Ty, To, 1, 2, 8>(y, R, slot_pos, gates, T, k, d, residual, out, st)
-           : v == 2 ? combine_as<Ty, To, 2, 2, 8>(y, R, slot_pos, gates, T, k, d, residual, out, st)
-           : k == 1 ? combine_as<Ty, To, kV, 4, 1>(y, R, slot_pos, gates, T, k, d, residual, out, st)
-           : k == 2 ? combine_as<Ty, To, kV, 2, 2>(y, R, slot_pos, gates, T, k, d, residual, out, st)
-                    : combine_as<Ty, To, kV, 1, 4>(y, R, slot_pos, gates, T, k, d, residual, out, st);
+    const bool wide = lanes_for(d / v) == 32;
+    const auto as = [&](auto f) { return f(y, R, slot_pos, gates, T, k, d, residual, out, st); };
+    if (v == kV)
+      return !wide    ? as(combine_as<Ty, To, kV, 1, 4, 0>)
+             : k == 1 ? as(combine_as<Ty, To, kV, 4, 1, 32>)
+             : k == 2 ? as(combine_as<Ty, To, kV, 2, 2, 32>)
+                      : as(combine_as<Ty, To, kV, 1, 4, 32>);
+    if (v == 2) return wide ? as(combine_as<Ty, To, 2, 4, 4, 32>) : as(combine_as<Ty, To, 2, 1, 4, 0>);
+    return wide ? as(combine_as<Ty, To, 1, 8, 4, 32>) : as(combine_as<Ty, To, 1, 1, 4, 0>);
   };
   if (y_bf16) return out_bf16 ? with(bf16(), bf16()) : with(bf16(), float());
   return out_bf16 ? with(float(), bf16()) : with(float(), float());
@@ -615,12 +710,16 @@ cudaError_t launch_combine_backward(const void* dout, bool dout_bf16, const int3
     using Td = decltype(td);
     using Ty = decltype(ty);
     constexpr int kV = 16 / sizeof(Ty);
-    return v == 1   ? backward_as<Td, Ty, 1, 4, 8>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
-           : v == 2 ? backward_as<Td, Ty, 2, 4, 8>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
-           : k == 1 ? backward_as<Td, Ty, kV, 4, 1>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
-           : k == 2 ? backward_as<Td, Ty, kV, 2, 2>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
-           : k <= 4 ? backward_as<Td, Ty, kV, 1, 4>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st)
-                    : backward_as<Td, Ty, kV, 1, 8>(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st);
+    const bool wide = lanes_for(d / v) == 32;
+    const auto as = [&](auto f) { return f(dout, slot_pos, gates, T, k, d, R, y, dy, dgates, st); };
+    if (v == kV)
+      return !wide    ? as(backward_as<Td, Ty, kV, 1, 4, 0>)
+             : k == 1 ? as(backward_as<Td, Ty, kV, 4, 1, 32>)
+             : k == 2 ? as(backward_as<Td, Ty, kV, 2, 2, 32>)
+             : k <= 4 ? as(backward_as<Td, Ty, kV, 1, 4, 32>)
+                      : as(backward_as<Td, Ty, kV, 1, 8, 32>);
+    if (v == 2) return !wide ? as(backward_as<Td, Ty, 2, 1, 4, 0>) : k <= 4 ? as(backward_as<Td, Ty, 2, 4, 4, 32>) : as(backward_as<Td, Ty, 2, 4, 8, 32>);
+    return !wide ? as(backward_as<Td, Ty, 1, 1, 4, 0>) : k <= 4 ? as(backward_as<Td, Ty, 1, 4, 4, 32>) : as(backward_as<Td, Ty, 1, 4, 8, 32>);
   };
   if (dout_bf16) return y_bf16 ? with(bf16(), bf16()) : with(bf16(), float());
   return y_bf16 ? with(float(), bf16()) : with(float(), float());

@@ -432,7 +432,7 @@ def test_example_trains_with_it(optimizer):
 @pytest.mark.parametrize("sizes", [[1], [0], [], [7, 0, 16383, 16384, 16385], [5] * 900, [3_000_001, 12], [40_000_000]])
 @pytest.mark.parametrize("offset", [0, 1])
 def test_grad_norm(optim, dtype, sizes, offset):
-    """Each square has one rounding and goes through 4 + 3 + 5 sums in fp32 at most, the rest are in 64 bits: the sum is
+    """Each square has one rounding and goes through 4 + 3 + 5 sums in fp32 at most, the rest have 48 bits or more: the sum is
     off by 13 u at most, the norm by half of that and its own rounding."""
     g = torch.Generator(device="cuda").manual_seed(4)
     ts = [(torch.randn(n + offset, generator=g, device="cuda") * 3).to(dtype)[offset:] for n in sizes]

@@ -552,21 +552,39 @@ cudaError_t launch_lists(const Entry* e, int n, const Step& s, cudaStream_t st) 
 // ------------------------------------------------------------------ the norm
 
 constexpr int kThreads = 256, kTile = kThreads * kPer;
-constexpr int kNormChunk = 4 * kTile;  // 32 values a thread, all under way at once; a warp's are summed in fp32
+constexpr int kNormTiles = 4, kNormChunk = kNormTiles * kTile;  // 32 values a thread, all under way at once
 
-__device__ __forceinline__ F8 load_maybe(const GradEntry& e, int64_t i, int left) {
-  if (!e.vec || left < kPer) return load(e.g, i, e.bf16, left);
-  P4 p;
-  if (e.bf16) {
-    Raw<2> r;
-    r.load(e.g, i);
-    p = r.get();
+// The sum of a warp's squares of a chunk, in fp32.
+template <bool kBf16>
+__device__ __forceinline__ float sum_of_squares(const GradEntry& e, int64_t begin, int64_t end) {
+  P4 g[kNormTiles];
+  if (e.vec && end - begin == kNormChunk) {
+    Raw<kBf16 ? 2 : 4> r[kNormTiles];
+#pragma unroll
+    for (int u = 0; u < kNormTiles; ++u) r[u].load(e.g, begin + u * kTile + threadIdx.x * kPer);
+#pragma unroll
+    for (int u = 0; u < kNormTiles; ++u) g[u] = r[u].get();
   } else {
-    Raw<4> r;
-    r.load(e.g, i);
-    p = r.get();
+#pragma unroll
+    for (int u = 0; u < kNormTiles; ++u) {
+      const int64_t i = begin + u * kTile + threadIdx.x * kPer;
+      const F8 r = load(e.g, i, kBf16, (int)max((int64_t)0, min(end - i, (int64_t)kPer)));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[u].v[j] = make_float2(r.v[2 * j], r.v[2 * j + 1]);
+    }
   }
-  return {{p.v[0].x, p.v[0].y, p.v[1].x, p.v[1].y, p.v[2].x, p.v[2].y, p.v[3].x, p.v[3].y}};
+  float2 sum[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sum[j] = mul2(g[0].v[j], g[0].v[j]);
+#pragma unroll
+  for (int u = 1; u < kNormTiles; ++u)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = fma2(g[u].v[j], g[u].v[j], sum[j]);
+  const float2 s = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+  float all = s.x + s.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
+  return all;
 }
 
 // The sum of the warps' first lanes' values, in the block's first thread.  A sum in 64 bits takes a warp several times
@@ -600,27 +618,18 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   __shared__ bool ends;
   pdl_wait();
   pdl_launch_dependents();
-  double total = 0;
+  float sum = 0.f, lost = 0.f;
   for (uint32_t chunk = blockIdx.x; chunk < b.first[b.n]; chunk += gridDim.x) {
     const int ti = owner(b, chunk);
     const GradEntry& e = b.e[ti];
     const int64_t begin = (int64_t)(chunk - b.first[ti]) * kNormChunk, end = min(begin + kNormChunk, e.n);
-    F8 g[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = begin + u * kTile + threadIdx.x * kPer;
-      g[u] = load_maybe(e, i, (int)max((int64_t)0, min(end - i, (int64_t)kPer)));
-    }
-    float sum[kPer] = {};
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) sum[j] = fmaf(g[u].v[j], g[u].v[j], sum[j]);
-    float s = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    total += (double)s;
+    const float v = e.bf16 ? sum_of_squares<true>(e, begin, end) : sum_of_squares<false>(e, begin, end);
+    // what the sum loses is kept beside it: as good as 64 bits, whose additions an SM has few units for
+    const float t = sum + v, part = t - sum;
+    lost += (sum - (t - part)) + (v - part);
+    sum = t;
   }
+  double total = isfinite(sum) ? (double)sum + (double)lost : (double)sum;
   total = sum_of_warps(total);
   if (threadIdx.x == 0) {
     out.parts[out.before + blockIdx.x] = total;

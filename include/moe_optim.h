@@ -5,7 +5,8 @@
  * One step of AdamW, with f the clipping factor, t the number of the step (1 the first):
  *   g = f * grad,   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
  *   p = p - lr wd p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
- * in fp32.  A parameter is fp32; or bf16 with an fp32 master, which the step is taken on and the
+ * in fp32; the square root and the quotient are good to two of its steps, and a v below 2^-126 counts as 0 in them.
+ * A parameter is fp32; or bf16 with an fp32 master, which the step is taken on and the
  * parameter rounded from (to nearest); or bf16 alone, rounded stochastically.
  *
  * Moments in 8 bits are m and r = sqrt(v), e4m3 values with an e8m0 factor for each 128 consecutive ones of
@@ -16,7 +17,7 @@
  * rounded to 0, so that no update is divided by eps alone.
  *
  * The random words are a hash of the seed, t, the tensor's index in the list and the value's index:
- * a step gives the same bits however it is launched.  With words of 32 bits,
+ * a step gives the same bits wherever its arrays lie and however it is launched.  With words of 32 bits,
  *   mix(x):  x *= 0x9E3779B1; x ^= x >> 16;  x *= 0x6A09E667; x ^= x >> 15;  x *= 0xBB67AE85; x ^= x >> 16
  *   key = mix(mix(mix(mix(seed_low) + seed_high) + t_low) + tensor)
  *   r_0 = mix(i / 8 + key),  r_{j+1} = r_j * 0x3C6EF375 + 0xA54FF53B,  the word of value i is r_{i mod 8}
@@ -51,7 +52,7 @@ typedef struct {
   double lr;              /* >= 0 */
   const float* lr_device; /* NULL, or a device value that is used for lr (a captured step reads it at each replay) */
   double beta1, beta2;    /* [0, 1); 1 - beta is taken in 64 bits */
-  double eps;             /* > 0, in fp32 too */
+  double eps;             /* >= 2^-126 */
   uint64_t seed;
 } moe_adamw_config;
 

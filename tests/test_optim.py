@@ -350,8 +350,26 @@ def test_small_moments_reach_the_right_value(optim):
 
 
 @gpu
-def test_a_step_is_the_same_every_time_and_for_a_list_in_parts(optim):
-    """The words go by the index in the list and not by the launch."""
+@pytest.mark.parametrize("ptype, master, bits", KINDS)
+@pytest.mark.parametrize("gtype", [F32, BF])
+def test_a_step_is_the_same_every_time_and_wherever_the_arrays_lie(optim, ptype, master, bits, gtype):
+    """Whole vectors and single values; a list that takes one launch and one that takes three, with the tensor at one place in it."""
+    results = []
+    for offset, others in ((0, 0), (0, 900), (1, 0)):
+        made = [make((9001,), ptype, gtype, bits, master, 7, optim, offset), make((2 ** 20,), ptype, gtype, bits, master, 8, optim, offset)]
+        more = [make((5,), BF, F32, 8, False, 9, optim) for _ in range(others)]
+        opt = take(optim, [x[0] for x in made + more], None, seed=3)
+        for _ in range(3):
+            opt.step([x[1] for x in made + more])
+        results.append([copy(x[0]) for x in made])
+    for other in results[1:]:
+        for a, b in zip(results[0], other):
+            assert torch.equal(a[0], b[0]) and (a[1] is None or torch.equal(a[1], b[1]))
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a[2], b[2]))
+
+
+@gpu
+def test_a_step_is_the_same_again(optim):
     results = []
     for _ in range(2):
         made = [make((9000,), BF, F32, 8, False, 7, optim), make((2 ** 20,), BF, F32, 8, False, 8, optim)]

@@ -116,7 +116,7 @@ def test_adamw_refusals(lib):
               dict(master=a[0] + 1996), dict(m=a[4] + 3996), dict(v=a[2]), dict(m_scales=a[5], v_scales=a[5] + 7), dict(m_scales=a[3] + 999, v_scales=a[5])):
         assert step(lib, t) == INVALID, t
     for c in (dict(lr=-1.0), dict(lr=nan), dict(lr=inf), dict(lr=1e39), dict(lr_device=a[6] + 2), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=nan),
-              dict(beta2=1.5), dict(eps=0.0), dict(eps=1e-60), dict(eps=inf), dict(eps=-1e-8)):
+              dict(beta2=1.5), dict(eps=0.0), dict(eps=1e-60), dict(eps=1e-39), dict(eps=inf), dict(eps=-1e-8)):
         assert step(lib, cfg=c) == INVALID, c
     for kw in (dict(factor=off(A[6], 1)), dict(steps=None), dict(steps=off(A[10], 4)), dict(ticket=None), dict(ticket=off(A[11], 2)), dict(n=-1), dict(no_cfg=True)):
         assert step(lib, **kw) == INVALID, kw

@@ -1,4 +1,5 @@
 // api_optim.cu -- the C ABI of the optimiser's step (include/moe_optim.h): argument checks and launches.
+#include <float.h>
 #include <math.h>
 
 #include "host_checks.h"
@@ -52,7 +53,7 @@ moe_status moe_adamw(const moe_adamw_tensor* tensors, int32_t n_tensors, const m
   if (!(cfg->lr >= 0) || !isfinite((float)cfg->lr)) return fail(MOE_ERR_INVALID_ARG, "lr must be finite and >= 0");
   if (!(cfg->beta1 >= 0 && cfg->beta1 < 1 && cfg->beta2 >= 0 && cfg->beta2 < 1))
     return fail(MOE_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
-  if (!((float)cfg->eps > 0.f) || !isfinite((float)cfg->eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be finite and above 0");
+  if (!((float)cfg->eps >= FLT_MIN) || !isfinite((float)cfg->eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be finite and at least 2^-126");
   const Ptr ptrs[] = {{cfg->lr_device, "lr_device", 4, true}, {grad_factor, "grad_factor", 4, true}, {steps, "steps", 8, false},
                       {ticket, "ticket", 4, false}};
   if ((s = check(ptrs)) != MOE_OK) return s;

@@ -1,7 +1,8 @@
 // optim.cu -- the gradients' norm and the step of AdamW over many tensors (include/moe_optim.h).
 //
-// Both go once over the data, so HBM bounds them: a step reads and writes, a value, 28 bytes (bf16 parameter
-// with a master, fp32 gradient and moments) down to 12 (8-bit moments, no master).  The tensors' list is
+// Both go once over the data, so HBM bounds them: a step reads and writes, a value, 30 bytes (bf16 parameter
+// with a master, fp32 gradient and moments) down to 10 (bf16 gradient, 8-bit moments, no master).  403 M values at 30
+// bytes take 1.75 ms, the norm of as many fp32 gradients 0.22 ms: both at the copy bandwidth.  The tensors' list is
 // an argument of the kernel, so that a call needs no copy to the device.
 #include <math.h>
 
@@ -19,15 +20,15 @@ namespace {
 constexpr int kPer = 8;  // consecutive values of a thread; 16 threads make a block of 128
 
 // The step's CTAs, for moments in 32 or in 8 bits: threads, CTAs an SM, values at a time (a tile) and the most tiles
-// (a power of two).  Moments in 32 bits: HBM does not wait for anyone (403 M values with masters: 1741 us with 256
-// threads, 3 CTAs and 2 to 4 tiles; 1730 with 2 CTAs, 1766 with 8 tiles, 1769-1790 with 128 threads).  In 8 bits the
-// warps an SM holds count (805 M values, no masters: 128 threads, 9 CTAs of 56 registers 1534 us, 8 of 64 1561, 7 of
+// (a power of two).  With moments in 32 bits HBM bounds the step whatever these are (403 M values with masters: 1741 us
+// with 256 threads, 3 CTAs and 4 tiles; 1730 with 2 CTAs, 1766 with 8 tiles, 1769-1790 with 128 threads).  With moments
+// in 8 bits the warps that an SM holds count (805 M values, no masters: 128 threads, 9 CTAs of 56 registers 1534 us, 8 of 64 1561, 7 of
 // 72 1595; 256 threads 4 CTAs 1571, 3 1696).
 template <bool kSmall>
-struct Shape {
-  static constexpr int kThreads = kSmall ? 128 : 256, kCtas = kSmall ? 9 : 3, kTile = kThreads * kPer, kTiles = kSmall ? 64 : 4;
+struct Ctas {
+  static constexpr int kThreads = kSmall ? 128 : 256, kOfSm = kSmall ? 9 : 3, kTile = kThreads * kPer, kTiles = kSmall ? 64 : 4;
 };
-constexpr int kMostChunk = Shape<true>::kTiles * Shape<true>::kTile, kLeastChunk = Shape<false>::kTiles * Shape<false>::kTile;
+constexpr int kMostChunk = Ctas<true>::kTiles * Ctas<true>::kTile, kLeastChunk = Ctas<false>::kTiles * Ctas<false>::kTile;
 constexpr unsigned kAll = 0xffffffffu;
 
 // ------------------------------------------------------------------ the lists
@@ -45,7 +46,8 @@ struct Entry {  // 72 bytes
 enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kVec = 4, kIndexShift = 3 };  // kVec: every array on 16 bytes (8-bit ones: 8)
 
 // A chunk, what a CTA takes of a tensor, has 1 to kTiles tiles: so many that there are kFewChunks of them and
-// more.  A launch's chunks are then fewer than 2^31, whatever its tensors.
+// more (34 M values with 8-bit moments: 219 us; half or a quarter as many chunks 250).  A launch's chunks are then fewer
+// than 2^31, whatever its tensors.
 constexpr int64_t kFewChunks = 152 * 12;
 static_assert((int64_t)kMostTensors * (kMostValues / kLeastChunk) < INT32_MAX, "too many chunks");
 
@@ -120,6 +122,16 @@ __device__ __forceinline__ float top_of_block(const F8& r) {
   return __uint_as_float(m);
 }
 
+// The scale byte of a block from its largest |m|, as fp8::scale_byte gives it; or, `root`, that of r = sqrt(v) from the
+// largest v: b - 127 is the least e with v <= 448^2 * 4^e, read off v's bits (448^2 = 1.53125 * 2^17), so that it does not
+// depend on how a root is rounded.  What counts as 0 gives 0, an infinity or NaN 255.
+__device__ __forceinline__ uint32_t block_byte(float top, bool root) {
+  const uint32_t u = __float_as_uint(top);
+  const int x = (int)(u >> 23), y = x + ((u & 0x7fffffu) > (root ? 0x440000u : 0x600000u) ? 1 : 0);
+  const int b = root ? (y + 111) >> 1 : max(y - 8, 0);
+  return x >= 255 ? 255u : x == 0 ? 0u : (uint32_t)b;
+}
+
 // ------------------------------------------------------------------ random words
 
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
@@ -147,16 +159,16 @@ __device__ __forceinline__ float round_linear(float u, uint32_t rnd) {
 }
 
 // r = sqrt(v), both times the block's factor (its square): to one of r's neighbours lo and hi so that the mean
-// of the square is v; with v > 0 not to 0.
+// of the square is v; with v > 0 not to 0, and not past 448.
 __device__ __forceinline__ float round_root(float u, float u2, uint32_t rnd) {
   const float c = lift(u);
   const uint32_t b = __float_as_uint(u + c) & kCut;
   const float lo = __uint_as_float(b) - c, hi = __uint_as_float(b + 0x100000u) - c, lo2 = lo * lo;
-  const bool up = (u2 - lo2) * 65536.f > (float)(rnd >> 8 & 0xffffu) * (fmaf(hi, hi, -lo2)) || (lo == 0.f && u2 > 0.f);
-  return up ? hi : lo;
+  const float border = fmaf((float)(rnd >> 8 & 0xffffu) * 0x1p-16f, fmaf(hi, hi, -lo2), lo2);
+  return u2 > (lo == 0.f ? 0.f : border) && lo < 448.f ? hi : lo;
 }
 
-// To bf16, the bits of two values in a word.
+// To bf16, in the upper half.
 __device__ __forceinline__ uint32_t round_bf16(float v, uint32_t rnd) {
   const uint32_t u = __float_as_uint(v);
   return (u & 0x7f800000u) == 0x7f800000u ? u : u + (rnd & 0xffffu);
@@ -176,8 +188,9 @@ __device__ __forceinline__ float rcp_fast(float x) {
 
 // ------------------------------------------------------------------ two values an instruction
 
-// The step with 8-bit moments is bound by the instructions it issues before HBM is: its fp32 products and
-// sums are taken two at a time (the packed forms round as the plain ones do).
+// The step with 8-bit moments is bound by the instructions it issues as much as by HBM (57 a value, 3.1 a cycle and SM;
+// 805 M values 1.55 ms, 92 % of the copy bandwidth with fp32 gradients, 74 % with bf16 ones): its fp32 products and sums
+// are taken two at a time (the packed forms round as the plain ones do).  With 104 a value it took 2.83 ms.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
   asm("{.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
@@ -265,7 +278,8 @@ enum : int { kF32 = 0, kBf16 = 1, kMaster = 2 };  // a parameter: fp32, bf16, bf
 // whole sectors: stored and loaded a byte a block, in the loop, they took a third of the step's time.
 constexpr int kMostBlocks = kMostChunk / 128;
 
-// What a thread reads for eight values, all of them there and on whole vectors.
+// What a thread reads for eight values, all of them there and on whole vectors.  Nothing is read ahead: more warps an SM
+// gain more than the registers that would take.
 template <int kParam, bool kGradBf16, bool kSmall>
 struct Read {
   Raw<kGradBf16 ? 2 : 4> g;
@@ -330,19 +344,19 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Comm
     store4_f32(static_cast<float*>(t.m) + i, m);
     store4_f32(static_cast<float*>(t.v) + i, v);
   } else {
-    // The largest |m| and r of the block.  From the first exchange on even lanes have m's, odd ones r's, and find
+    // The largest |m| and v of the block.  From the first exchange on even lanes have m's, odd ones v's, and find
     // the factor of theirs.
-    float tm = 0.f, tr = 0.f;
+    float tm = 0.f, tv = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       tm = max_nan(max_nan(tm, fabsf(m.v[j].x)), fabsf(m.v[j].y));
-      tr = max_nan(max_nan(tr, r.v[j].x), r.v[j].y);
+      tv = max_nan(max_nan(tv, v.v[j].x), v.v[j].y);
     }
     const bool odd = threadIdx.x & 1;
-    float top = max_nan(odd ? tr : tm, __shfl_xor_sync(kAll, odd ? tm : tr, 1));
+    float top = max_nan(odd ? tv : tm, __shfl_xor_sync(kAll, odd ? tm : tv, 1));
 #pragma unroll
     for (int o = 2; o < 16; o *= 2) top = max_nan(top, __shfl_xor_sync(kAll, top, o));
-    const uint32_t b = fp8::scale_byte(top);
+    const uint32_t b = block_byte(top, odd);
     if ((threadIdx.x & 14) == 0) factors[odd ? kMostBlocks : 0] = (uint8_t)b;
     const float inv = fp8::inv_scale_value(b), other = __shfl_xor_sync(kAll, inv, 1);
     const float2 im = both(odd ? other : inv), iv = both(odd ? inv : other);
@@ -425,7 +439,7 @@ __device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, c
     store(static_cast<float*>(t.v), i, v, left);
     return;
   }
-  const uint32_t bm = fp8::scale_byte(top_of_block(m)), bv = fp8::scale_byte(top_of_block(r));
+  const uint32_t bm = block_byte(top_of_block(m), false), bv = block_byte(top_of_block(v), true);
   const float im = fp8::inv_scale_value(bm), iv = fp8::inv_scale_value(bv);
 #pragma unroll
   for (int j = 0; j < kPer; ++j)
@@ -441,7 +455,7 @@ __device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, c
 
 template <int kParam, bool kGradBf16, bool kSmall>
 __device__ __forceinline__ void step_tiles(const Entry& t, int64_t from, int64_t to, const Common& k, uint8_t* factors) {
-  for (int64_t i = from + threadIdx.x * kPer; i < to; i += Shape<kSmall>::kTile) {
+  for (int64_t i = from + threadIdx.x * kPer; i < to; i += Ctas<kSmall>::kTile) {
     Read<kParam, kGradBf16, kSmall> in;
     in.load(t, i);
     step_whole(t, i, k, in, factors + (int)(i - from) / 128);
@@ -450,9 +464,9 @@ __device__ __forceinline__ void step_tiles(const Entry& t, int64_t from, int64_t
 
 // One kernel for tensors with moments in 8 bits and one for those with 32, which takes more registers.
 template <int kN, bool kSmall>
-__global__ void __launch_bounds__(Shape<kSmall>::kThreads, Shape<kSmall>::kCtas) adamw_kernel(const __grid_constant__ Batch<kN> b,
+__global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) adamw_kernel(const __grid_constant__ Batch<kN> b,
                                                                                               const __grid_constant__ Step s) {
-  constexpr int kThreads = Shape<kSmall>::kThreads, kTile = Shape<kSmall>::kTile;
+  constexpr int kThreads = Ctas<kSmall>::kThreads, kTile = Ctas<kSmall>::kTile;
   __shared__ Common common;
   __shared__ bool skip;
   __shared__ uint8_t factors[kSmall ? 2 * kMostBlocks : 1];
@@ -527,19 +541,19 @@ __global__ void empty_step_kernel(const float* factor, int64_t* steps) {
 
 template <int kN, bool kSmall>
 cudaError_t launch_list(const Entry* e, int n, const Step& s, cudaStream_t st) {
-  constexpr int kTile = Shape<kSmall>::kTile;
+  constexpr int kTile = Ctas<kSmall>::kTile;
   Batch<kN> b;
   int64_t tiles = 0;
   for (int i = 0; i < n; ++i) tiles += (e[i].n + kTile - 1) / kTile;
   b.n = n;
   b.chunk = kTile;
-  while (b.chunk < Shape<kSmall>::kTiles * kTile && tiles * kTile >= 2 * kFewChunks * b.chunk) b.chunk *= 2;
+  while (b.chunk < Ctas<kSmall>::kTiles * kTile && tiles * kTile >= 2 * kFewChunks * b.chunk) b.chunk *= 2;
   b.first[0] = 0;
   for (int i = 0; i < n; ++i) {
     b.e[i] = e[i];
     b.first[i + 1] = b.first[i] + (uint32_t)((e[i].n + b.chunk - 1) / b.chunk);
   }
-  return launch_kernel(adamw_kernel<kN, kSmall>, dim3(b.first[n]), dim3(Shape<kSmall>::kThreads), 0, st, true, 1, b, s);
+  return launch_kernel(adamw_kernel<kN, kSmall>, dim3(b.first[n]), dim3(Ctas<kSmall>::kThreads), 0, st, true, 1, b, s);
 }
 
 template <bool kSmall>

@@ -22,8 +22,8 @@ constexpr int kPer = 8;  // consecutive values of a thread; 16 threads make a bl
 // The step's CTAs, for moments in 32 or in 8 bits: threads, CTAs an SM, values at a time (a tile) and the most tiles
 // (a power of two).  With moments in 32 bits HBM bounds the step whatever these are (403 M values with masters: 1741 us
 // with 256 threads, 3 CTAs and 4 tiles; 1730 with 2 CTAs, 1766 with 8 tiles, 1769-1790 with 128 threads).  With moments
-// in 8 bits the warps that an SM holds count (805 M values, no masters: 128 threads, 9 CTAs of 56 registers 1534 us, 8 of 64 1561, 7 of
-// 72 1595; 256 threads 4 CTAs 1571, 3 1696).
+// in 8 bits the warps that an SM holds count (805 M values, no masters: 128 threads, 9 CTAs of 56 registers 1533 us, 8 of 64 1561, 7 of
+// 72 1595, 10 of 48 1612; 256 threads 4 CTAs 1571, 3 1696).
 template <bool kSmall>
 struct Ctas {
   static constexpr int kThreads = kSmall ? 128 : 256, kOfSm = kSmall ? 9 : 3, kTile = kThreads * kPer, kTiles = kSmall ? 64 : 4;
@@ -189,7 +189,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // ------------------------------------------------------------------ two values an instruction
 
 // The step with 8-bit moments is bound by the instructions it issues as much as by HBM (57 a value, 3.1 a cycle and SM;
-// 805 M values 1.55 ms, 92 % of the copy bandwidth with fp32 gradients, 74 % with bf16 ones): its fp32 products and sums
+// 805 M values 1.53 ms, 93 % of the copy bandwidth with fp32 gradients, 74 % with bf16 ones): its fp32 products and sums
 // are taken two at a time (the packed forms round as the plain ones do).  With 104 a value it took 2.83 ms.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -356,9 +356,9 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Comm
     float top = max_nan(odd ? tv : tm, __shfl_xor_sync(kAll, odd ? tm : tv, 1));
 #pragma unroll
     for (int o = 2; o < 16; o *= 2) top = max_nan(top, __shfl_xor_sync(kAll, top, o));
-    const uint32_t b = block_byte(top, odd);
+    const uint32_t b = block_byte(top, odd);  // 247 at most, or 255
     if ((threadIdx.x & 14) == 0) factors[odd ? kMostBlocks : 0] = (uint8_t)b;
-    const float inv = fp8::inv_scale_value(b), other = __shfl_xor_sync(kAll, inv, 1);
+    const float inv = __uint_as_float(b == 255u ? 0x7fffffffu : (254u - b) << 23), other = __shfl_xor_sync(kAll, inv, 1);
     const float2 im = both(odd ? other : inv), iv = both(odd ? inv : other);
     // Times 2^-120 an e4m3 value has fp32's bits 27-20 for its own 7-0 but the sign's: its subnormals, below 2^-6,
     // are fp32's.  So cutting fp32's last 20 bits off, after the random ones are added, rounds both alike.  Four

@@ -225,6 +225,23 @@ def test_step(optim, ptype, master, bits, gtype, offset):
 
 
 @gpu
+@pytest.mark.parametrize("betas", [(0.0, 0.0), (1e-9, 1e-9), (0.0, 0.999), (0.3, 0.6), (0.5, 0.5), (0.6, 0.4), (0.99, 0.9999)])
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_other_betas(optim, betas, bits, offset):
+    """Moments that are kept and much larger or smaller than what comes in; 1 - b has one rounding more where b is small."""
+    made = [make((5000,), BF, F32, bits, False, 3, optim, offset), make((300,), F32, BF, bits, False, 4, optim, offset)]
+    sets, grads = [x[0] for x in made], [x[1] for x in made]
+    for scale in (1.0, 2.0 ** -14, 2.0 ** 14):
+        now = [g * scale for g in grads] if not offset else [g.mul_(scale) for g in grads]
+        before = [copy(b) for b in sets]
+        opt = optim.AdamW([b[0] for b in sets], lr=0.02, betas=betas, eps=1e-5, state=[b[2] for b in sets], steps=2, seed=1)
+        opt.step(now)
+        for i, (b, s, gr) in enumerate(zip(before, sets, now)):
+            check_step(b, copy(s), gr, i, step=3, seed=1, lr=0.02, b1=betas[0], b2=betas[1], eps=1e-5, optim=optim)
+
+
+@gpu
 def test_mixed_list_of_many_tensors(optim):
     """More tensors than a launch takes, of all kinds, some without values."""
     made = [make((1 + 37 * i % 300,) if i % 50 else (0, 3), *((F32, F32, 32, False), (BF, F32, 8, False), (BF, BF, 32, True), (F32, BF, 8, False))[i % 4], i, optim)

@@ -183,6 +183,14 @@ def test_python_refusals(lib):
         optim.grad_norm(g, torch.zeros(1), torch.zeros(10, dtype=torch.uint8))
 
 
+def test_registers_leave_room_for_the_ctas(tmp_path):
+    from test_resources import REGISTERS, resources
+    found = resources("optim.cu", tmp_path)
+    for kernel, threads, ctas in (("adamw_kernelILi24ELb1E", 128, 9), ("adamw_kernelILi24ELb0E", 256, 3)):
+        regs = [r for n, r in found.items() if kernel in n]
+        assert regs and all(ctas * threads * (-(-r // 8) * 8) <= REGISTERS for r in regs), (kernel, regs)
+
+
 def test_state_values():
     """What moments() gives for a state in 8 bits."""
     from top_routing_grouped_gb300 import optim

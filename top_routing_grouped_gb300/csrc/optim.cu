@@ -189,7 +189,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // ------------------------------------------------------------------ two values an instruction
 
 // The step with 8-bit moments is bound by the instructions it issues as much as by HBM (57 a value, 3.1 a cycle and SM;
-// 805 M values 1.53 ms, 93 % of the copy bandwidth with fp32 gradients, 74 % with bf16 ones): its fp32 products and sums
+// 805 M values 1.54 ms, 93 % of the copy bandwidth with fp32 gradients, 74 % with bf16 ones): its fp32 products and sums
 // are taken two at a time (the packed forms round as the plain ones do).  With 104 a value it took 2.83 ms.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -257,7 +257,7 @@ __device__ __forceinline__ void store4_f32(float* p, const P4& r) {
 // ------------------------------------------------------------------ the step
 
 struct Step {
-  float lr, c1, c2, eps, log1, log2;  // c: 1 - beta, log: ln of beta
+  float lr, b1, b2, c1, c2, eps, log1, log2;  // b: beta, c: 1 - beta, log: ln of beta
   const float* lr_device;
   const float* factor;
   int64_t* steps;
@@ -270,6 +270,9 @@ struct Step {
 struct Common {
   float f, c1, c2, rate, root, eps, keep;  // rate = lr / (1 - beta1^t), root = 1 / sqrt(1 - beta2^t), keep = 1 - lr wd
   uint32_t key;
+  // Both betas are 0.5 or more, as they mostly are: m + c1 (x - m) then has one rounding of m's size.  Where a beta is
+  // small and m is large beside x, it would lose x; b1 m + c1 x does not.
+  bool slow;
 };
 
 enum : int { kF32 = 0, kBf16 = 1, kMaster = 2 };  // a parameter: fp32, bf16, bf16 with a master
@@ -294,8 +297,8 @@ struct Read {
 };
 
 template <int kParam, bool kGradBf16, bool kSmall>
-__device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Common& k, const Read<kParam, kGradBf16, kSmall>& in,
-                                           uint8_t* factors) {
+__device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Step& s, const Common& k,
+                                           const Read<kParam, kGradBf16, kSmall>& in, uint8_t* factors) {
   const P4 g = in.g.get();
   P4 w = in.w.get(), m = in.m.get(), v = in.v.get(), r;
   if constexpr (kSmall) {
@@ -307,11 +310,23 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Comm
       v.v[j] = mul2(v.v[j], v.v[j]);
     }
   }
+  if (k.slow) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = mul2(g.v[j], both(k.f));
+      m.v[j] = fma2(both(k.c1), add2(x, neg2(m.v[j])), m.v[j]);
+      v.v[j] = fma2(both(k.c2), fma2(x, x, neg2(v.v[j])), v.v[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = mul2(g.v[j], both(k.f));
+      m.v[j] = fma2(both(k.c1), x, mul2(both(s.b1), m.v[j]));
+      v.v[j] = fma2(mul2(both(k.c2), x), x, mul2(both(s.b2), v.v[j]));
+    }
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 x = mul2(g.v[j], both(k.f));
-    m.v[j] = fma2(both(k.c1), add2(x, neg2(m.v[j])), m.v[j]);  // b1 m + c1 x, with one rounding of m's size
-    v.v[j] = fma2(both(k.c2), fma2(x, x, neg2(v.v[j])), v.v[j]);
     r.v[j] = make_float2(sqrt_fast(v.v[j].x), sqrt_fast(v.v[j].y));
     const float2 den = fma2(r.v[j], both(k.root), both(k.eps));
     const float2 u = mul2(m.v[j], make_float2(rcp_fast(den.x), rcp_fast(den.y)));
@@ -396,7 +411,7 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Comm
 __device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <bool kSmall>
-__device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, const Common& k, uint8_t* factors) {
+__device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, const Step& s, const Common& k, uint8_t* factors) {
   const int left = (int)max((int64_t)0, min(end - i, (int64_t)kPer));
   const bool p_bf16 = t.index_flags & kParamBf16;
   const F8 g = load(t.grad, i, t.index_flags & kGradBf16, left);
@@ -414,8 +429,13 @@ __device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, c
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const float x = g.v[j] * k.f;
-    m.v[j] = fmaf(k.c1, x - m.v[j], m.v[j]);
-    v.v[j] = fmaf(k.c2, fmaf(x, x, -v.v[j]), v.v[j]);
+    if (k.slow) {
+      m.v[j] = fmaf(k.c1, x - m.v[j], m.v[j]);
+      v.v[j] = fmaf(k.c2, fmaf(x, x, -v.v[j]), v.v[j]);
+    } else {
+      m.v[j] = fmaf(k.c1, x, s.b1 * m.v[j]);
+      v.v[j] = fmaf(k.c2 * x, x, s.b2 * v.v[j]);
+    }
     r.v[j] = sqrt_fast(v.v[j]);
     w.v[j] = fmaf(-k.rate, m.v[j] * rcp_fast(fmaf(r.v[j], k.root, k.eps)), k.keep * w.v[j]);
   }
@@ -454,11 +474,11 @@ __device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, c
 }
 
 template <int kParam, bool kGradBf16, bool kSmall>
-__device__ __forceinline__ void step_tiles(const Entry& t, int64_t from, int64_t to, const Common& k, uint8_t* factors) {
+__device__ __forceinline__ void step_tiles(const Entry& t, int64_t from, int64_t to, const Step& s, const Common& k, uint8_t* factors) {
   for (int64_t i = from + threadIdx.x * kPer; i < to; i += Ctas<kSmall>::kTile) {
     Read<kParam, kGradBf16, kSmall> in;
     in.load(t, i);
-    step_whole(t, i, k, in, factors + (int)(i - from) / 128);
+    step_whole(t, i, s, k, in, factors + (int)(i - from) / 128);
   }
 }
 
@@ -495,7 +515,7 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
     // 1 - beta^t, without the cancellation for small t
     const float bc1 = -expm1f((float)taken * s.log1), bc2 = -expm1f((float)taken * s.log2);
     const uint32_t key = mix(mix(mix(mix(s.seed_low) + s.seed_high) + (uint32_t)taken) + (t.index_flags >> kIndexShift));
-    common = Common{f, s.c1, s.c2, lr / bc1, rsqrtf(bc2), s.eps, 1.f - lr * t.weight_decay, key};
+    common = Common{f, s.c1, s.c2, lr / bc1, rsqrtf(bc2), s.eps, 1.f - lr * t.weight_decay, key, s.c1 <= 0.5f && s.c2 <= 0.5f};
     skip = !isfinite(f);
     // The CTA that reads the steps last, when no other one will, writes them at its end.
     raise = s.last && atomicAdd(s.ticket, 1u) == gridDim.x - 1;
@@ -511,12 +531,12 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
   const Common k = common;
   if (!skip) {
     const bool g = t.index_flags & kGradBf16;
-    if (t.master) g ? step_tiles<kMaster, true, kSmall>(t, begin, whole, k, factors) : step_tiles<kMaster, false, kSmall>(t, begin, whole, k, factors);
-    else if (t.index_flags & kParamBf16) g ? step_tiles<kBf16, true, kSmall>(t, begin, whole, k, factors) : step_tiles<kBf16, false, kSmall>(t, begin, whole, k, factors);
-    else g ? step_tiles<kF32, true, kSmall>(t, begin, whole, k, factors) : step_tiles<kF32, false, kSmall>(t, begin, whole, k, factors);
+    if (t.master) g ? step_tiles<kMaster, true, kSmall>(t, begin, whole, s, k, factors) : step_tiles<kMaster, false, kSmall>(t, begin, whole, s, k, factors);
+    else if (t.index_flags & kParamBf16) g ? step_tiles<kBf16, true, kSmall>(t, begin, whole, s, k, factors) : step_tiles<kBf16, false, kSmall>(t, begin, whole, s, k, factors);
+    else g ? step_tiles<kF32, true, kSmall>(t, begin, whole, s, k, factors) : step_tiles<kF32, false, kSmall>(t, begin, whole, s, k, factors);
     for (int64_t i0 = whole; i0 < end; i0 += kTile) {
       const int64_t i = i0 + threadIdx.x * kPer;
-      step_rest<kSmall>(t, i, end, k, factors + (int)(i - begin) / 128);
+      step_rest<kSmall>(t, i, end, s, k, factors + (int)(i - begin) / 128);
     }
     if constexpr (kSmall) {
       __syncthreads();
@@ -694,6 +714,8 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   Step s{};
   s.lr = (float)cfg.lr;
   s.lr_device = cfg.lr_device;
+  s.b1 = (float)cfg.beta1;
+  s.b2 = (float)cfg.beta2;
   s.c1 = (float)(1 - cfg.beta1);
   s.c2 = (float)(1 - cfg.beta2);
   s.eps = (float)cfg.eps;

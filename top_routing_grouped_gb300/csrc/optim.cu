@@ -19,14 +19,17 @@ namespace {
 
 constexpr int kPer = 8;  // consecutive values of a thread; 16 threads make a block of 128
 
-// The step's CTAs, for moments in 32 or in 8 bits: threads, CTAs an SM, values at a time (a tile) and the most tiles
-// (a power of two).  With moments in 32 bits HBM bounds the step whatever these are (403 M values with masters: 1741 us
-// with 256 threads, 3 CTAs and 4 tiles; 1730 with 2 CTAs, 1766 with 8 tiles, 1769-1790 with 128 threads).  With moments
-// in 8 bits the warps that an SM holds count (805 M values, no masters: 128 threads, 9 CTAs of 56 registers 1533 us, 8 of 64 1561, 7 of
-// 72 1595, 10 of 48 1612; 256 threads 4 CTAs 1571, 3 1696).
+// The step's CTAs, for moments in 32 or in 8 bits: threads, CTAs an SM, values at a time (a tile).  A chunk, what a CTA
+// takes of a tensor, has 1 to kTiles tiles (a power of two), so many that there are kFew chunks and more.
+// With moments in 32 bits HBM bounds the step whatever these are (403 M values with masters: 1741 us with 256 threads,
+// 3 CTAs and 4 tiles; 1730 with 2 CTAs, 1766 with 8 tiles, 1769-1790 with 128 threads).  With moments in 8 bits the warps
+// that an SM holds count (805 M values, no masters: 128 threads, 9 CTAs of 56 registers 1533 us, 8 of 64 1561, 7 of 72 1595,
+// 10 of 48 1612; 256 threads 4 CTAs 1571, 3 1696), and how evenly it ends (kFew of 152 * 12, 24, 48: 131 M values 307, 288,
+// 286 us, 35 M 221, 209, 209; 64, 32 and 16 tiles within 1 %).
 template <bool kSmall>
 struct Ctas {
-  static constexpr int kThreads = kSmall ? 128 : 256, kOfSm = kSmall ? 9 : 3, kTile = kThreads * kPer, kTiles = kSmall ? 64 : 4;
+  static constexpr int kThreads = kSmall ? 128 : 256, kOfSm = kSmall ? 9 : 3, kTile = kThreads * kPer, kTiles = kSmall ? 32 : 4,
+                       kFew = 152 * (kSmall ? 48 : 12);
 };
 constexpr int kMostChunk = Ctas<true>::kTiles * Ctas<true>::kTile, kLeastChunk = Ctas<false>::kTiles * Ctas<false>::kTile;
 constexpr unsigned kAll = 0xffffffffu;
@@ -45,10 +48,7 @@ struct Entry {  // 72 bytes
 };
 enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kVec = 4, kIndexShift = 3 };  // kVec: every array on 16 bytes (8-bit ones: 8)
 
-// A chunk, what a CTA takes of a tensor, has 1 to kTiles tiles: so many that there are kFewChunks of them and
-// more (34 M values with 8-bit moments: 219 us; half or a quarter as many chunks 250).  A launch's chunks are then fewer
-// than 2^31, whatever its tensors.
-constexpr int64_t kFewChunks = 152 * 12;
+// A launch's chunks are fewer than 2^31, whatever its tensors.
 static_assert((int64_t)kMostTensors * (kMostValues / kLeastChunk) < INT32_MAX, "too many chunks");
 
 template <int kN>
@@ -189,7 +189,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
 // ------------------------------------------------------------------ two values an instruction
 
 // The step with 8-bit moments is bound by the instructions it issues as much as by HBM (57 a value, 3.1 a cycle and SM;
-// 805 M values 1.54 ms, 93 % of the copy bandwidth with fp32 gradients, 74 % with bf16 ones): its fp32 products and sums
+// 805 M values 1.53 ms, 93 % of the copy bandwidth with fp32 gradients, 78 % with bf16 ones): its fp32 products and sums
 // are taken two at a time (the packed forms round as the plain ones do).  With 104 a value it took 2.83 ms.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -567,7 +567,7 @@ cudaError_t launch_list(const Entry* e, int n, const Step& s, cudaStream_t st) {
   for (int i = 0; i < n; ++i) tiles += (e[i].n + kTile - 1) / kTile;
   b.n = n;
   b.chunk = kTile;
-  while (b.chunk < Ctas<kSmall>::kTiles * kTile && tiles * kTile >= 2 * kFewChunks * b.chunk) b.chunk *= 2;
+  while (b.chunk < Ctas<kSmall>::kTiles * kTile && tiles * kTile >= 2 * (int64_t)Ctas<kSmall>::kFew * b.chunk) b.chunk *= 2;
   b.first[0] = 0;
   for (int i = 0; i < n; ++i) {
     b.e[i] = e[i];

@@ -102,19 +102,24 @@ struct Ranks {
   int e;             // the expert of its first 32 slots, and the lanes of the same one
   unsigned same;
 
-  // table [kW][E], zeros: the warps' own counts, each by its warp.
-  __device__ __forceinline__ void count_own(const Args& a, int64_t s0, int own, int* table) {
+  // Asks for the first 32.
+  __device__ __forceinline__ void begin(const Args& a, int64_t s0, int own) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, run = (own + kThreadsOf - 1) / kThreadsOf * 32;
-    int* mine = table + warp * a.E;
     w0 = warp * run;
     w1 = min(w0 + run, own);
-    e = -1;
+    e = w0 + lane < w1 ? expert_of<kIdx64>(a, s0 + w0 + lane) : -1;
+  }
+
+  // table [kW][E], zeros: the warps' own counts, each by its warp.
+  __device__ __forceinline__ void count_own(const Args& a, int64_t s0, int* table) {
+    const int lane = threadIdx.x & 31;
+    int* mine = table + (threadIdx.x >> 5) * a.E;
     same = 0;
     for (int i0 = w0; i0 < w1; i0 += 32) {
-      const int x = i0 + lane < w1 ? expert_of<kIdx64>(a, s0 + i0 + lane) : -1;
+      const int x = i0 == w0 ? e : i0 + lane < w1 ? expert_of<kIdx64>(a, s0 + i0 + lane) : -1;
       const unsigned m = __match_any_sync(kAll, x);
       if (x >= 0 && lane == __ffs(m) - 1) mine[x] += __popc(m);
-      if (i0 == w0) e = x, same = m;
+      if (i0 == w0) same = m;
       __syncwarp();
     }
   }
@@ -187,11 +192,11 @@ struct Ranks {
 };
 
 // What a sort writes of slot s, whose row is p.
-__device__ __forceinline__ void write_slot(const Args& a, int64_t s, int p) {
+__device__ __forceinline__ void write_slot(const Args& a, int64_t s, int p, const float* gate) {
   a.slot_pos[s] = p;
   if (p < 0) return;
   if (a.row_slot) a.row_slot[p] = (int)s;
-  if (a.gates && p < a.R) a.row_gates[p] = a.gates[s];
+  if (a.gates && p < a.R) a.row_gates[p] = *gate;
 }
 
 // Many slots: blocks of them, one a CTA, are counted in one launch and ranked in a second one, whose CTAs each
@@ -231,7 +236,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(Args a, int64_t per_
   const int64_t N = a.T * a.k, s0 = blockIdx.x * per_block;
   const int own = (int)min(per_block, N - s0);
   Ranks<kIdx64, kSortWarps> ranks;
-  ranks.count_own(a, s0, own, table);
+  ranks.begin(a, s0, own);
+  ranks.count_own(a, s0, table);
   pdl_wait();
   const int groups = quads < kSortThreads ? kSortThreads / quads : 1;
   for (int i = threadIdx.x; i < groups * quads; i += kSortThreads) {
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(Args a, int64_t per_
     }
   }
   const int kept = ranks.rank(
-      a, s0, before, rest, table, [&](int i, int p) { write_slot(a, s0 + i, p); },
+      a, s0, before, rest, table, [&](int i, int p) { write_slot(a, s0 + i, p, a.gates + s0 + i); },
       [&](int e, int n) {
         if (blockIdx.x == 0) a.counts[e] = n;
       });
@@ -272,11 +278,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(Args a, int64_t per_
 }
 
 // The rows' way: bound by HBM (32768 rows of 4096 bf16 to four experts each, sorted: 203 us, 98 % of the copy
-// bandwidth; the sort is 6 us of it; small CTAs of a segment a warp, 27 tokens a CTA 230 us).  Each CTA takes `tokens` tokens (grid.y: a share of their columns).  With kSort, for few slots,
-// it first sorts them: each CTA counts all of them by itself, out of L2, and ranks its own.  `lanes` lanes move up to
-// 4 * lanes vectors of a token at a time: they read them once and write them to each of the token's rows.  The
-// first ones are on their way while the positions are found; `early`: even while the previous kernel, a sort of the same
-// call that has waited for what was before it, ends.
+// bandwidth; the sort is 6 us of it; small CTAs of a segment a warp, 27 tokens a CTA 230 us).  Each CTA takes `tokens`
+// tokens (grid.y: a share of their columns).  With kSort, for few slots, it first sorts them: each CTA counts all of
+// them by itself, out of L2, and ranks its own; up to 32 a warp compares with one another (a token to four experts of
+// 64, in a CUDA graph: 3.2 -> 2.3 us, the sort's outputs written behind the rows).  `lanes` lanes move up to 4 * lanes
+// vectors of a token at a time: they read them once and write them to each of the token's rows.  The first ones are on
+// their way while the positions are found; `early`: even while the previous kernel, a sort of the same call that has
+// waited for what was before it, ends.
 // kSize 0: all rows begin and end on boundaries of V.  Else they are values of kSize bytes, and each row is written
 // in whole 16-byte vectors of its own alignment, which are read from wherever they lie in x.
 template <typename V, int kSize, bool kSort, bool kIdx64, int kLanes>
@@ -309,6 +317,8 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
       if (v0 + u * lanes < v_end) buf[u] = __ldcg(src + v0 + u * lanes);
   };
 
+  int kept = 0;
+  float gate = 0.f;
   if constexpr (!kSort) {
     if (early && unit < units) fetch();
     pdl_wait();
@@ -321,25 +331,43 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
     }
   } else {
     int *before = shared + tokens * a.k, *rest = before + a.E, *table = rest + a.E;
-    for (int i = threadIdx.x; i < (2 + kWarps) * a.E; i += kThreads) before[i] = 0;
     pdl_wait();
     pdl_launch_dependents();
-    if (unit < units) fetch();
-    __syncthreads();
     Ranks<kIdx64, kWarps> ranks;
-    ranks.count_own(a, s0, own, table);
-    count<kIdx64, kThreads>(a, 0, a.T * a.k, s0, before, rest);
-    const int kept = ranks.rank(
-        a, s0, before, rest, table,
-        [&](int i, int p) {
-          pos[i] = p;
-          if (first) write_slot(a, s0 + i, p);
-        },
-        [&](int e, int n) {
-          if (first && blockIdx.x == 0) a.counts[e] = n;
-        });
-    if (first && a.row_slot)
-      for (int64_t p = max(s0, (int64_t)kept) + threadIdx.x; p < s0 + own; p += kThreads) a.row_slot[p] = -1;
+    const int N = (int)(a.T * a.k);
+    const bool counts = first && blockIdx.x == 0;
+    if (N <= 32) {  // a slot a lane: no shared memory but for the positions
+      const int at = threadIdx.x & 31, e = at < N ? expert_of<kIdx64>(a, at) : -1;
+      if (unit < units) fetch();
+      kept = __popc(__ballot_sync(kAll, e >= 0));
+      if (warp == 0) {
+        int p = 0;
+        for (int j = 0; j < N; ++j) {
+          const int f = __shfl_sync(kAll, e, j);
+          p += f >= 0 && (f < e || (f == e && j < at)) ? 1 : 0;
+        }
+        if (at >= s0 && at < s0 + own) pos[at - s0] = e >= 0 ? p : -1;
+      } else if (counts) {
+        for (int x0 = (warp - 1) * 32; x0 < a.E; x0 += (kWarps - 1) * 32) {
+          int n = 0;
+          for (int j = 0; j < N; ++j) n += __shfl_sync(kAll, e, j) == x0 + at ? 1 : 0;
+          if (x0 + at < a.E) a.counts[x0 + at] = n;
+        }
+      }
+    } else {
+      ranks.begin(a, s0, own);
+      for (int i = threadIdx.x; i < (2 + kWarps) * a.E; i += kThreads) before[i] = 0;
+      __syncthreads();
+      count<kIdx64, kThreads>(a, 0, N, s0, before, rest);
+      if (unit < units) fetch();
+      ranks.count_own(a, s0, table);
+      kept = ranks.rank(
+          a, s0, before, rest, table, [&](int i, int p) { pos[i] = p; },
+          [&](int e, int n) {
+            if (counts) a.counts[e] = n;
+          });
+    }
+    if (first && a.gates && threadIdx.x < own) gate = a.gates[s0 + threadIdx.x];
   }
   __syncthreads();
   const char* x_end = a.x + (a.T - 1) * a.ld_bytes + a.row_bytes;
@@ -376,6 +404,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
     unit += kWarps;
     if (unit < units) fetch();
   }
+  if (kSort && first)
+    for (int i = threadIdx.x; i < own; i += kThreads) {
+      write_slot(a, s0 + i, pos[i], i == threadIdx.x ? &gate : a.gates + s0 + i);
+      if (a.row_slot && s0 + i >= kept) a.row_slot[s0 + i] = -1;
+    }
   if (a.words && first) {
     const int64_t n = nt * a.words;
     for (int64_t i = threadIdx.x; i < n; i += kThreads) {

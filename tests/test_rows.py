@@ -132,7 +132,7 @@ def test_dispatch_and_gather(rows, T, k, E, d, dtype, lay, drop):
                 assert (rs[m:] == 77).all()
 
 
-@pytest.mark.parametrize("T, k", [(1, 31), (31, 1), (4, 8), (32, 1), (1, 32), (11, 3), (33, 1)])
+@pytest.mark.parametrize("T, k", [(1, 31), (31, 1), (4, 8), (32, 1), (1, 32), (11, 3), (33, 1), (23, 1), (1, 24), (3, 8), (24, 1), (5, 5)])
 @pytest.mark.parametrize("E, d, drop", [(1, 72, 0), (2, 8, 0.5), (31, 2048, 0.1), (225, 1001, 0.2), (1024, 20, 0), (6, 16, 1.0)])
 def test_dispatch_of_about_a_warp_of_slots(rows, T, k, E, d, drop):
     test_dispatch_and_gather(rows, T, k, E, d, BF, "plain", drop)

@@ -22,6 +22,9 @@ constexpr int kMaxPositions = 4096;    // that a CTA keeps
 // 4.6; 2000 tokens' two rows of 1000 fp32 are dispatched in 6.4 us, sorted first in 8.3.  With 152 or 608 CTAs: within 3 %.
 constexpr int64_t kSortFew = 4096;
 constexpr int kSortCtas = 152 * 2;
+// Up to kWarpSlots (32 at most) a warp compares with one another, a turn for each.  In a CUDA graph, against counting: 4 slots
+// 2.3 and 3.3 us, 16 slots 3.4 and 4.0, 24 slots 3.7 and 4.0, 32 slots 4.15 and 4.0.
+constexpr int kWarpSlots = 24;
 constexpr unsigned kAll = 0xffffffffu;
 
 // ------------------------------------------------------------------ rows off 16-byte boundaries
@@ -280,11 +283,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(Args a, int64_t per_
 // The rows' way: bound by HBM (32768 rows of 4096 bf16 to four experts each, sorted: 203 us, 98 % of the copy
 // bandwidth; the sort is 6 us of it; small CTAs of a segment a warp, 27 tokens a CTA 230 us).  Each CTA takes `tokens`
 // tokens (grid.y: a share of their columns).  With kSort, for few slots, it first sorts them: each CTA counts all of
-// them by itself, out of L2, and ranks its own; up to 32 a warp compares with one another (a token to four experts of
-// 64, in a CUDA graph: 3.2 -> 2.3 us, the sort's outputs written behind the rows).  `lanes` lanes move up to 4 * lanes
-// vectors of a token at a time: they read them once and write them to each of the token's rows.  The first ones are on
-// their way while the positions are found; `early`: even while the previous kernel, a sort of the same call that has
-// waited for what was before it, ends.
+// them by itself, out of L2, and ranks its own; a warp compares the fewest with one another.  The sort's outputs
+// are written behind the rows.  `lanes` lanes move up to 4 * lanes vectors of a token at a time: they read them once and
+// write them to each of the token's rows.  The first ones are on their way while the positions are found; `early`: even
+// while the previous kernel, a sort of the same call that has waited for what was before it, ends.
 // kSize 0: all rows begin and end on boundaries of V.  Else they are values of kSize bytes, and each row is written
 // in whole 16-byte vectors of its own alignment, which are read from wherever they lie in x.
 template <typename V, int kSize, bool kSort, bool kIdx64, int kLanes>
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(Args a, int tokens, int6
     Ranks<kIdx64, kWarps> ranks;
     const int N = (int)(a.T * a.k);
     const bool counts = first && blockIdx.x == 0;
-    if (N <= 32) {  // a slot a lane: no shared memory but for the positions
+    if (N <= kWarpSlots) {  // a slot a lane: no shared memory but for the positions
       const int at = threadIdx.x & 31, e = at < N ? expert_of<kIdx64>(a, at) : -1;
       if (unit < units) fetch();
       kept = __popc(__ballot_sync(kAll, e >= 0));

@@ -138,6 +138,12 @@ def test_dispatch_of_about_a_warp_of_slots(rows, T, k, E, d, drop):
     test_dispatch_and_gather(rows, T, k, E, d, BF, "plain", drop)
 
 
+@pytest.mark.parametrize("T, k", [(6143, 1), (1536, 4), (96, 64), (6145, 1), (1537, 4), (4095, 2), (97, 64)])
+@pytest.mark.parametrize("E, d, drop", [(3, 136, 0), (100, 33, 0.2), (1024, 72, 0.4)])
+def test_dispatch_of_a_few_thousand_slots(rows, T, k, E, d, drop):
+    test_dispatch_and_gather(rows, T, k, E, d, BF, "plain", drop)
+
+
 def positions(T, k, R, seed, bad=0.2):
     """Different rows for the slots, some outside [0, R)."""
     g = gen(seed)

@@ -18,9 +18,11 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 128;             // vectors of a row that a warp moves at a time, four a lane
 constexpr int kMaxPositions = 4096;    // that a CTA keeps
 // Up to kSortFew slots each CTA that moves rows counts them all by itself, with kSortCtas such CTAs at most; more are sorted
-// in launches of their own.  A sort of 4096 slots takes 3.7 us in one launch and 4.5 in two, of 8192 slots 5.1 and
-// 4.6; 2000 tokens' two rows of 1000 fp32 are dispatched in 6.4 us, sorted first in 8.3.  With 152 or 608 CTAs: within 3 %.
-constexpr int64_t kSortFew = 4096;
+// in launches of their own.  In CUDA graphs, one launch and two or three: 2000 tokens' two rows of 1000 bf16 5.1 and
+// 6.5 us, 1100 tokens' four of 2048 6.9 and 8.1, 1500 tokens' four of 2048 8.1 and 9.2, 760 tokens' eight of 1024 6.8 and 8.4;
+// 1029 tokens' eight of 2050 10.8 and 9.8, 4096 tokens' two of 512 6.7 and 6.4, 4000 tokens' four of 256 10.0 and 7.2.
+// With 152 CTAs: within 3 % up to 8192 slots but for one 10 % slower.
+constexpr int64_t kSortFew = 6144;
 constexpr int kSortCtas = 152 * 2;
 // Up to kWarpSlots (32 at most) a warp compares with one another, a turn for each.  In a CUDA graph, against counting: 4 slots
 // 2.3 and 3.3 us, 16 slots 3.4 and 4.0, 24 slots 3.7 and 4.0, 32 slots 4.15 and 4.0.

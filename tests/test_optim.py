@@ -500,3 +500,25 @@ def test_large_and_small_values(optim):
         optim.grad_norm(t, norm, optim.grad_norm_workspace(t), 1.0, factor)
         assert float(norm) == want or abs(float(norm) / want - 1) < 1e-5
         assert torch.isnan(factor) == (want == float("inf"))
+
+
+# ------------------------------------------------------------------ what all values of a step have in common
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+def test_all_blocks_of_a_step_take_the_same_number(optim, bits):
+    """Moments of zero and gradients of one: every value moves by one number, which hangs on the step's number alone (half as
+    many bits of 1 - 0.5^t from one to the next).  The number is raised while a step's thousands of CTAs run."""
+    n = 3_000_001
+    p, g = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    opt = optim.AdamW([p], lr=1.0, betas=(0.5, 0.5), weight_decay=0.0, bits=bits)
+    for _ in range(20):
+        for done in range(12):
+            p.zero_(), opt.steps.fill_(done)
+            for t in opt.state[0]:
+                t.view(torch.uint8).zero_()
+            opt.step([g])
+            low, high = torch.aminmax(p)
+            bc = 1 - 0.5 ** (done + 1)
+            assert float(low) == float(high), (done, float(low), float(high))
+            assert abs(float(low) + 0.5 / bc / (0.5 / bc) ** 0.5) < 1e-6 and int(opt.steps) == done + 1 and int(opt._ticket) == 0

@@ -482,6 +482,17 @@ __device__ __forceinline__ void step_tiles(const Entry& t, int64_t from, int64_t
   }
 }
 
+// The steps' number is read by every CTA of a call and raised by one of the last launch, after all have read it.  Each
+// draws a ticket once it has read the number, with release semantics (nothing else holds a read before an atomic on
+// another word); the CTA that draws the last one, and so knows that all have read, fences before it writes.  The draw
+// takes as long as what it waits for: the last warp does it behind the barrier (60 small tensors, clipped: 29.2 us;
+// before the barrier, or at the end, 30.6).
+__device__ __forceinline__ uint32_t draw(uint32_t* ticket) {
+  uint32_t n;
+  asm volatile("atom.release.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(ticket) : "memory");
+  return n;
+}
+
 // One kernel for tensors with moments in 8 bits and one for those with 32, which takes more registers.
 template <int kN, bool kSmall>
 __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) adamw_kernel(const __grid_constant__ Batch<kN> b,
@@ -489,6 +500,7 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
   constexpr int kThreads = Ctas<kSmall>::kThreads, kTile = Ctas<kSmall>::kTile;
   __shared__ Common common;
   __shared__ bool skip;
+  __shared__ int64_t taken;
   __shared__ uint8_t factors[kSmall ? 2 * kMostBlocks : 1];
   const int ti = owner(b, blockIdx.x);
   const Entry& t = b.e[ti];
@@ -503,7 +515,6 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
     prefetch(static_cast<const char*>(t.m) + i * (kSmall ? 1 : 4));
     prefetch(static_cast<const char*>(t.v) + i * (kSmall ? 1 : 4));
   }
-  int64_t taken;
   bool raise = false;
   pdl_wait();
   pdl_launch_dependents();
@@ -517,8 +528,6 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
     const uint32_t key = mix(mix(mix(mix(s.seed_low) + s.seed_high) + (uint32_t)taken) + (t.index_flags >> kIndexShift));
     common = Common{f, s.c1, s.c2, lr / bc1, rsqrtf(bc2), s.eps, 1.f - lr * t.weight_decay, key, s.c1 <= 0.5f && s.c2 <= 0.5f};
     skip = !isfinite(f);
-    // The CTA that reads the steps last, when no other one will, writes them at its end.
-    raise = s.last && atomicAdd(s.ticket, 1u) == gridDim.x - 1;
   }
   const int blocks = (int)((end - begin + 127) / 128);
   const int64_t block0 = begin / 128;
@@ -528,6 +537,7 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
       factors[kMostBlocks + j] = t.v_scales[block0 + j];
     }
   __syncthreads();
+  if (s.last && threadIdx.x == kThreads - 32) raise = draw(s.ticket) == gridDim.x - 1;
   const Common k = common;
   if (!skip) {
     const bool g = t.index_flags & kGradBf16;
@@ -547,6 +557,7 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
     }
   }
   if (raise) {
+    __threadfence();  // every CTA's read of the steps lies before what follows
     *s.ticket = 0;
     if (!skip) *s.steps = taken;
   }

@@ -195,6 +195,11 @@ def make(shape, ptype, gtype, bits, master, seed, optim, offset=0, spread=True):
     return (at(w.to(ptype).view(shape)), at(w.view(shape)) if master else None, state), at(gr.to(gtype).view(shape))
 
 
+def at_offset(t, offset):
+    """A copy on the GPU that begins `offset` values past an aligned address."""
+    return torch.empty(t.numel() + offset, dtype=t.dtype, device="cuda")[offset:].view(t.shape).copy_(t)
+
+
 def copy(b):
     return b[0].cpu().clone(), None if b[1] is None else b[1].cpu().clone(), tuple(t.view(torch.uint8).cpu().clone().view(t.dtype) for t in b[2])
 
@@ -500,6 +505,64 @@ def test_large_and_small_values(optim):
         optim.grad_norm(t, norm, optim.grad_norm_workspace(t), 1.0, factor)
         assert float(norm) == want or abs(float(norm) / want - 1) < 1e-5
         assert torch.isnan(factor) == (want == float("inf"))
+
+
+# ------------------------------------------------------------------ the decay
+
+@gpu
+@pytest.mark.parametrize("ptype, master, bits", [(F32, False, 32), (F32, False, 8), (BF, True, 32), (BF, True, 8)])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("lr, wd", [(1e-3, 0.1), (1e-4, 0.01), (1e-5, 0.1), (1e-5, 0.01), (5e-6, 0.01), (1e-6, 0.01), (1.0, 0.3), (1.0, 0.75), (0.5, 3.0), (1e-3, 0.0)])
+def test_a_decayed_value_has_one_rounding(optim, ptype, master, bits, offset, lr, wd):
+    """p (1 - lr wd) and the update, rounded once: half a step of the result, lr and wd with half a step of fp32 each (2 u of
+    the decay), the split of 1 - lr wd (2^-48; 2^-25 where it is below 1 / 2), 30 u of the update as above and two
+    more of it and of the decay's second part for their product and sum.  With moments, and with none."""
+    (p, w, st), g = make((9001,), ptype, F32, bits, master, 17, optim, offset)
+    for still in (False, True):
+        if still:
+            g.zero_()
+            for t in st:
+                t.view(torch.uint8).zero_()
+        x = np64(w if master else p)
+        before = copy((p, w, st))
+        m, v = (np64(t) for t in optim.moments(before[2]))
+        opt = optim.AdamW([p], lr=lr, betas=(B1, B2), eps=EPS, weight_decay=wd, masters=[w], state=[st], steps=50, seed=2)
+        opt.step([g])
+        g64 = np64(g)
+        mt, v = np.abs(B1 * m) + np.abs((1 - B1) * g64), B2 * v + (1 - B2) * g64 ** 2
+        m = B1 * m + (1 - B1) * g64
+        den, rate = np.sqrt(v / (1 - B2 ** 51)) + EPS, lr / (1 - B1 ** 51)
+        want = x * (1 - lr * wd) - rate * m / den
+        half = 2.0 ** -24 * np.exp2(np.floor(np.log2(np.maximum(np.abs(want), 2.0 ** -126))))
+        rest = 2.0 ** -25 if lr * wd > 0.5 else 2.0 ** -48
+        more = 2 * U * lr * wd * np.abs(x) + 32 * U * rate * mt / den + (rest + 2.0 ** -47) * np.abs(x) + 2.0 ** -149
+        got = np64(w if master else p)
+        assert (np.abs(got - want) <= half + 1.001 * more).all()
+        if master:
+            assert torch.equal(p, w.to(BF))
+
+
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("wd", [0.0, 0.01, 0.3, 2.0])
+@pytest.mark.parametrize("ptype, offset", [(F32, 0), (F32, 1), (BF, 0)])
+def test_an_infinite_parameter_stays(optim, bits, wd, ptype, offset):
+    """Where 1 - lr wd is above 0; the values beside it change as they would without it."""
+    n = 3001
+    values, infinite = torch.randn(n, generator=gen(5)).to(ptype), torch.zeros(n, dtype=torch.bool)
+    infinite[[3, 200, 2047, 2048, 3000]] = True
+    got = []
+    for with_it in (True, False):
+        p = at_offset(values, offset)
+        if with_it:
+            p[3], p[200], p[2047], p[2048], p[3000] = (float(s + "inf") for s in "+--+-")
+        was = p.clone()
+        opt = optim.AdamW([p], lr=0.1, weight_decay=wd, bits=bits, seed=4)
+        opt.step([torch.ones(n, device="cuda")])
+        if with_it:
+            assert torch.equal(p[infinite.cuda()], was[infinite.cuda()])
+        got.append(p.cpu())
+    assert torch.isfinite(got[1]).all() and torch.equal(got[0][~infinite], got[1][~infinite])
 
 
 # ------------------------------------------------------------------ what all values of a step have in common

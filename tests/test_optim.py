@@ -565,6 +565,34 @@ def test_an_infinite_parameter_stays(optim, bits, wd, ptype, offset):
     assert torch.isfinite(got[1]).all() and torch.equal(got[0][~infinite], got[1][~infinite])
 
 
+# ------------------------------------------------------------------ large gradients
+
+def below_overflow(v, w, e, sr_r=sr_r):
+    """sr_r, but not up to 2^64, whose square fp32 does not hold: 240 of 2^56 is the last value below."""
+    r = sr_r(v, w, e)
+    return np.where(r >= 2.0 ** 64, 240 * 2.0 ** 56, r)
+
+
+@gpu
+@pytest.mark.parametrize("offset", [0, 1])
+def test_a_rounded_v_is_finite_where_v_is(optim, offset, monkeypatch):
+    """v in [2.6e38, 3.4e38): in blocks of the factor 2^56 r lies between 224 and 256, the last with a square of 2^128."""
+    import sys
+    monkeypatch.setattr(sys.modules[__name__], "sr_r", below_overflow)
+    n = 4000
+    grad = at_offset((torch.linspace(2.6e38, 3.39e38, n, dtype=torch.float64) / 0.999).sqrt().float(), offset)
+    grad[1536:2048] *= 1e-3  # blocks of another factor
+    p = at_offset(torch.randn(n, generator=gen(1)), offset)
+    opt = optim.AdamW([p], lr=LR, betas=(0.3, 1e-3), bits=8, seed=6)
+    for step in (1, 2):
+        before = copy((p, None, opt.state[0]))
+        opt.step([grad])
+        after = copy((p, None, opt.state[0]))
+        assert all(torch.isfinite(t).all() for t in optim.moments(after[2]))
+        check_step(before, after, grad, 0, step=step, seed=6, b1=0.3, b2=1e-3, optim=optim)
+        grad.mul_(0.999)
+
+
 # ------------------------------------------------------------------ what all values of a step have in common
 
 @gpu

@@ -593,6 +593,29 @@ def test_a_rounded_v_is_finite_where_v_is(optim, offset, monkeypatch):
         grad.mul_(0.999)
 
 
+@gpu
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.9, 0.95), (0.99, 0.999999), (0.3, 0.999)])
+def test_gradients_up_to_where_v_overflows(optim, bits, offset, betas, monkeypatch):
+    """(1 - b2) g^2 below 3.4e38, g^2 far above it; one block of each size, two steps."""
+    import sys
+    monkeypatch.setattr(sys.modules[__name__], "sr_r", below_overflow)
+    most = 1.8e19 / (1 - betas[1]) ** 0.5  # its square times 1 - b2: 3.24e38
+    size = torch.tensor([1.0, 1e10, 1e18, 1.9e19, 3e19, 0.5 * most, 0.98 * most]).repeat_interleave(384)
+    p = at_offset(torch.randn(len(size), generator=gen(1)), offset)
+    grad = at_offset(size * (torch.rand(len(size), generator=gen(2)) * 0.02 + 0.98) * torch.where(torch.arange(len(size)) % 3 == 0, -1, 1), offset)
+    opt = optim.AdamW([p], lr=LR, betas=betas, bits=bits, seed=6)
+    for step in (1, 2):
+        before = copy((p, None, opt.state[0]))
+        if step == 2:
+            grad.mul_(0.1)
+        opt.step([grad])
+        after = copy((p, None, opt.state[0]))
+        assert torch.isfinite(p).all() and all(torch.isfinite(t).all() for t in optim.moments(after[2]))
+        check_step(before, after, grad, 0, step=step, seed=6, b1=betas[0], b2=betas[1], optim=optim)
+
+
 # ------------------------------------------------------------------ what all values of a step have in common
 
 @gpu

@@ -261,7 +261,8 @@ __device__ __forceinline__ void store4_f32(float* p, const P4& r) {
 // ------------------------------------------------------------------ the step
 
 struct Step {
-  float lr, b1, b2, c1, c2, eps, log1, log2;  // b: beta, c: 1 - beta, log: ln of beta
+  float lr, b1, b2, c1, c2, a, neg_a2, eps, log1, log2;  // b: beta, neg_a2: -a^2, log: ln of beta; the others: see Common
+  bool slow;
   const float* lr_device;
   const float* factor;
   int64_t* steps;
@@ -272,13 +273,15 @@ struct Step {
 
 // What all values of a tensor have in common.
 struct Common {
-  float f, c1, c2, rate, root, eps;  // rate = lr / (1 - beta1^t), root = 1 / sqrt(1 - beta2^t)
+  float fa, c1, c2, rate, root, eps;  // fa = f a, rate = lr / (1 - beta1^t), root = 1 / sqrt(1 - beta2^t)
   // 1 - lr wd = keep + rest.  One float alone is off by up to 2^-25, the same for all values and steps: 1.4 % of a decay of
   // 1e-6, 19 % of 1e-7.  keep is cut towards 0 and rest is not 0, so that an infinite parameter stays what it is.
   float keep, rest;
   uint32_t key;
-  // Both betas are 0.5 or more, as they mostly are: m + c1 (x - m) then has one rounding of m's size.  Where a beta is
-  // small and m is large beside x, it would lose x; b1 m + c1 x does not.
+  // Both betas are 0.5 or more, as they mostly are: m + (1 - b1) (x - m) then has one rounding of m's size.  Where a beta is
+  // small and m is large beside x, it would lose x; b1 m + (1 - b1) x does not.  In the first form x = f g is taken times
+  // a, the largest power of two with a^2 <= 1 - b2, and c1 and c2 are (1 - b1) / a and (1 - b2) / a^2: exact, and x^2
+  // overflows where (1 - b2) x^2 does, no sooner.  Else a = 1.
   bool slow;
 };
 
@@ -320,14 +323,14 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Step
   if (k.slow) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 x = mul2(g.v[j], both(k.f));
-      m.v[j] = fma2(both(k.c1), add2(x, neg2(m.v[j])), m.v[j]);
-      v.v[j] = fma2(both(k.c2), fma2(x, x, neg2(v.v[j])), v.v[j]);
+      const float2 x = mul2(g.v[j], both(k.fa));
+      m.v[j] = fma2(both(k.c1), fma2(m.v[j], both(-s.a), x), m.v[j]);
+      v.v[j] = fma2(both(k.c2), fma2(x, x, mul2(v.v[j], both(s.neg_a2))), v.v[j]);
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 x = mul2(g.v[j], both(k.f));
+      const float2 x = mul2(g.v[j], both(k.fa));
       m.v[j] = fma2(both(k.c1), x, mul2(both(s.b1), m.v[j]));
       v.v[j] = fma2(mul2(both(k.c2), x), x, mul2(both(s.b2), v.v[j]));
     }
@@ -437,10 +440,10 @@ __device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, c
   }
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const float x = g.v[j] * k.f;
+    const float x = g.v[j] * k.fa;
     if (k.slow) {
-      m.v[j] = fmaf(k.c1, x - m.v[j], m.v[j]);
-      v.v[j] = fmaf(k.c2, fmaf(x, x, -v.v[j]), v.v[j]);
+      m.v[j] = fmaf(k.c1, fmaf(m.v[j], -s.a, x), m.v[j]);
+      v.v[j] = fmaf(k.c2, fmaf(x, x, v.v[j] * s.neg_a2), v.v[j]);
     } else {
       m.v[j] = fmaf(k.c1, x, s.b1 * m.v[j]);
       v.v[j] = fmaf(k.c2 * x, x, s.b2 * v.v[j]);
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
     const float bc1 = -expm1f((float)taken * s.log1), bc2 = -expm1f((float)taken * s.log2);
     const uint32_t key = mix(mix(mix(mix(s.seed_low) + s.seed_high) + (uint32_t)taken) + (t.index_flags >> kIndexShift));
     const float keep = __fmaf_rz(-lr, t.weight_decay, 1.f), rest = fmaf(-lr, t.weight_decay, 1.f - keep);
-    common = Common{f, s.c1, s.c2, lr / bc1, rsqrtf(bc2), s.eps, keep, copysignf(fmaxf(fabsf(rest), 0x1p-126f), keep), key, s.c1 <= 0.5f && s.c2 <= 0.5f};
+    common = Common{f * s.a, s.c1, s.c2, lr / bc1, rsqrtf(bc2), s.eps, keep, copysignf(fmaxf(fabsf(rest), 0x1p-126f), keep), key, s.slow};
     skip = !isfinite(f);
   }
   const int blocks = (int)((end - begin + 127) / 128);
@@ -739,6 +742,11 @@ cudaError_t launch_adamw(const moe_adamw_tensor* tensors, int n, const moe_adamw
   s.b2 = (float)cfg.beta2;
   s.c1 = (float)(1 - cfg.beta1);
   s.c2 = (float)(1 - cfg.beta2);
+  s.slow = s.c1 <= 0.5f && s.c2 <= 0.5f;
+  s.a = s.slow ? ldexpf(1.f, (ilogbf(s.c2) - (ilogbf(s.c2) & 1)) / 2) : 1.f;
+  s.neg_a2 = -s.a * s.a;
+  s.c1 /= s.a;
+  s.c2 /= s.a * s.a;
   s.eps = (float)cfg.eps;
   s.log1 = (float)log(cfg.beta1);
   s.log2 = (float)log(cfg.beta2);

@@ -76,7 +76,8 @@ size_t moe_grad_norm_workspace(int32_t n_tensors);
 /* *norm = sqrt(sum over all values g^2) and, where factor is not NULL, *factor = min(1, max_norm / *norm), NaN
  * where the norm is infinite or NaN.  Squares are taken in fp32 (a |g| above 1.8e19 gives an infinite
  * norm, values below 1e-19 count with few bits or not at all), summed in fp32 over 1024 values at most, pairwise,
- * then with 48 bits or more, in an order that the sizes fix.  max_norm > 0.  workspace: 256-byte aligned; its first 4 bytes are 0
+ * then with 48 bits or more, in an order that the sizes fix; in 64 bits from the squares on where fp32 does not hold a sum.
+ * max_norm > 0.  workspace: 256-byte aligned; its first 4 bytes are 0
  * before the first call, and the calls leave them 0.  Calls in flight at the same time need workspaces of their own. */
 moe_status moe_grad_norm(const moe_grad_tensor* tensors, int32_t n_tensors, float max_norm, float* norm, float* factor,
                          void* workspace, size_t workspace_bytes, void* stream);

@@ -636,3 +636,22 @@ def test_all_blocks_of_a_step_take_the_same_number(optim, bits):
             bc = 1 - 0.5 ** (done + 1)
             assert float(low) == float(high), (done, float(low), float(high))
             assert abs(float(low) + 0.5 / bc / (0.5 / bc) ** 0.5) < 1e-6 and int(opt.steps) == done + 1 and int(opt._ticket) == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("size", [2.0 ** 40, 2.0 ** 50, 1e18, 1.5e19])
+def test_grad_norm_of_many_large_values(optim, dtype, offset, size):
+    """Squares that fp32 holds, sums that it does not; beside them a tensor that does not show, and one that is not finite.  As
+    in test_grad_norm: half of 13 u, and the norm's own rounding."""
+    ts = [at_offset((torch.randn(n, generator=gen(n)).clamp(-1.1, 1.1) * size).to(dtype), offset) for n in (77, 8192, 300_001, 5_000_000)]
+    ts.insert(2, torch.randn(100_000, device="cuda"))
+    norm, factor, ws = torch.zeros(1, device="cuda"), torch.zeros(1, device="cuda"), optim.grad_norm_workspace(ts)
+    want = float(sum(t.double().square().sum() for t in ts)) ** 0.5
+    optim.grad_norm(ts, norm, ws, 1.0, factor)
+    assert abs(float(norm) - want) <= 8 * U * want and abs(float(factor) * want - 1) <= 10 * U
+    for bad in (float("nan"), float("inf"), 3e19):
+        ts[3][4567] = bad
+        optim.grad_norm(ts, norm, ws, 1.0, factor)
+        assert not torch.isfinite(norm) and torch.isnan(factor)

@@ -645,6 +645,23 @@ __device__ __forceinline__ float sum_of_squares(const GradEntry& e, int64_t begi
   return all;
 }
 
+// The sum of a warp's squares of all its chunks in 64 bits, for what fp32 does not hold.
+template <int kN>
+__device__ __noinline__ double wide_sum_of_squares(const GradBatch<kN>& b) {
+  double all = 0;
+  for (uint32_t chunk = blockIdx.x; chunk < b.first[b.n]; chunk += gridDim.x) {
+    const int ti = owner(b, chunk);
+    const GradEntry& e = b.e[ti];
+    const int64_t begin = (int64_t)(chunk - b.first[ti]) * kNormChunk, end = min(begin + kNormChunk, e.n);
+    for (int64_t i = begin + threadIdx.x * kPer; i < end; i += kTile) {
+      const F8 r = load(e.g, i, e.bf16, (int)min(end - i, (int64_t)kPer));
+      for (int j = 0; j < kPer; ++j) all += (double)(r.v[j] * r.v[j]);
+    }
+  }
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kAll, all, o);
+  return all;
+}
+
 // The sum of the warps' first lanes' values, in the block's first thread.  A sum in 64 bits takes a warp several times
 // as long as one in fp32, and they follow one another here: as few of them as can be.
 __device__ __forceinline__ double sum_of_warps(double v) {
@@ -687,7 +704,8 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     lost += (sum - (t - part)) + (v - part);
     sum = t;
   }
-  double total = isfinite(sum) ? (double)sum + (double)lost : (double)sum;
+  double total = (double)sum + (double)lost;
+  if (!isfinite(sum)) total = wide_sum_of_squares(b);  // a warp's lanes have the same sum
   total = sum_of_warps(total);
   if (threadIdx.x == 0) {
     out.parts[out.before + blockIdx.x] = total;

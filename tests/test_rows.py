@@ -82,6 +82,28 @@ def test_sort_without_row_slot_and_of_no_tokens(rows):
     assert counts.cpu().tolist() == [0] * 9
 
 
+@pytest.mark.parametrize("T, k, E", [(6, 4, 9), (24, 1, 1024), (13, 2, 7), (500, 4, 60), (1536, 4, 3), (1537, 4, 128), (20000, 2, 33)])
+def test_an_index_counts_with_all_its_bits(rows, T, k, E):
+    """64-bit values whose low halves are experts' numbers have no row, on each of the sort's paths, alone and in a dispatch."""
+    g = gen(T)
+    idx = choice(T, k, E, T)
+    far = torch.tensor([1 << 32, -(1 << 32), 1 << 40, -(1 << 63), (1 << 62) + (1 << 33)])[torch.randint(0, 5, (T, k), generator=g)]
+    idx = torch.where(torch.rand(T, k, generator=g) < 0.4, idx + far, idx)
+    x, ws = torch.randn(T, 24, generator=g).cuda(), rows.dispatch_workspace(T, k, E)
+    want = sorted_ref(idx, E)
+    assert 0 < want[0].sum() < T * k
+    for call in ("sort", "dispatch"):
+        counts, pos, row_slot, out = full(E), full(T, k), full(T * k), torch.full((T * k, 24), 77.0, device="cuda")
+        if call == "sort":
+            rows.sort(idx.cuda(), counts, pos, row_slot, ws)
+        else:
+            rows.dispatch(idx.cuda(), x, counts, pos, out, ws, row_slot)
+            n = int(want[0].sum())
+            assert torch.equal(out[:n].cpu(), x.cpu()[want[2][:n] // k]) and (out[n:] == 77).all()
+        for got, w in zip((counts, pos, row_slot), want):
+            np.testing.assert_array_equal(got.cpu().numpy(), w)
+
+
 def source(T, d, dtype, seed, lay="plain"):
     raw = torch.randint(0, 256, (T, (d + 24) * dtype.itemsize), generator=gen(seed), dtype=torch.int64).to(torch.uint8)
     wide = raw.cuda().view(dtype)  # any bits: NaNs and infinities among them

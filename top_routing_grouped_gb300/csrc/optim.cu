@@ -149,10 +149,6 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 // [2^-6, 2^-5) has too: 2^-6 is added to such values, so that cutting fp32's last 20 bits off fits both.
 constexpr uint32_t kCut = 0xfff00000u;
 constexpr uint32_t kTop = 0x07e00000u;  // 448 * 2^-120
-// In blocks of the factor 2^56, the largest for r, 240 is the last value whose square is below 2^128: r is rounded up to
-// that at most.
-constexpr float kLargestInv = 0x1p-56f;
-constexpr uint32_t kLargestBytes = 0x77777777u;
 __device__ __forceinline__ float lift(float u) { return u < 0x1p-6f ? 0x1p-6f : 0.f; }
 
 // u in [-448, 448] to an e4m3 value: up in magnitude where the bits that are cut, plus random ones, carry.
@@ -163,13 +159,13 @@ __device__ __forceinline__ float round_linear(float u, uint32_t rnd) {
 }
 
 // r = sqrt(v), both times the block's factor (its square): to one of r's neighbours lo and hi so that the mean
-// of the square is v; with v > 0 not to 0, and not past `top`.
-__device__ __forceinline__ float round_root(float u, float u2, uint32_t rnd, float top) {
+// of the square is v; with v > 0 not to 0, and not past 448.
+__device__ __forceinline__ float round_root(float u, float u2, uint32_t rnd) {
   const float c = lift(u);
   const uint32_t b = __float_as_uint(u + c) & kCut;
   const float lo = __uint_as_float(b) - c, hi = __uint_as_float(b + 0x100000u) - c, lo2 = lo * lo;
   const float border = fmaf((float)(rnd >> 8 & 0xffffu) * 0x1p-16f, fmaf(hi, hi, -lo2), lo2);
-  return u2 > (lo == 0.f ? 0.f : border) && lo < top ? hi : lo;
+  return u2 > (lo == 0.f ? 0.f : border) && lo < 448.f ? hi : lo;
 }
 
 // To bf16, in the upper half.
@@ -413,9 +409,7 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Step
     }
     const auto pack = [](const uint32_t* y) { return __byte_perm(__byte_perm(y[0], y[1], 0x0073), __byte_perm(y[2], y[3], 0x0073), 0x5410); };
     __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i), make_uint2(pack(ym), pack(ym + 4)));
-    uint2 packed = make_uint2(pack(yr), pack(yr + 4));
-    if (iv.x == kLargestInv) packed = make_uint2(__vminu4(packed.x, kLargestBytes), __vminu4(packed.y, kLargestBytes));
-    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i), packed);
+    __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i), make_uint2(pack(yr), pack(yr + 4)));
   }
 }
 
@@ -477,7 +471,7 @@ __device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, c
   for (int j = 0; j < kPer; ++j)
     if (j < left) {
       static_cast<uint8_t*>(t.m)[i + j] = (uint8_t)fp8::pack_e4m3x2(round_linear(m.v[j] * im, rnd[j]), 0.f);
-      static_cast<uint8_t*>(t.v)[i + j] = (uint8_t)fp8::pack_e4m3x2(round_root(r.v[j] * iv, v.v[j] * iv * iv, rnd[j], iv == kLargestInv ? 240.f : 448.f), 0.f);
+      static_cast<uint8_t*>(t.v)[i + j] = (uint8_t)fp8::pack_e4m3x2(round_root(r.v[j] * iv, v.v[j] * iv * iv, rnd[j]), 0.f);
     }
   if ((threadIdx.x & 15) == 0) {
     factors[0] = (uint8_t)bm;
@@ -492,6 +486,14 @@ __device__ __forceinline__ void step_tiles(const Entry& t, int64_t from, int64_t
     in.load(t, i);
     step_whole(t, i, s, k, in, factors + (int)(i - from) / 128);
   }
+}
+
+// In blocks of r's largest factor, 2^56, 240 is the last value whose square is below 2^128: what was rounded up to 256 is
+// taken back, once the block is done (in the loop, where hardly any block needs it, that made the step with bf16
+// gradients 7 % slower).
+constexpr uint8_t kLargestFactor = 127 + 56, kLargestOfIt = 0x77;
+__device__ __noinline__ void keep_squares_finite(uint8_t* r, int n) {
+  for (int i = 0; i < n; ++i) r[i] = min(r[i], kLargestOfIt);
 }
 
 // The steps' number is read by every CTA of a call and raised by one of the last launch, after all have read it.  Each
@@ -566,6 +568,8 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
       for (int j = threadIdx.x; j < blocks; j += kThreads) {
         t.m_scales[block0 + j] = factors[j];
         t.v_scales[block0 + j] = factors[kMostBlocks + j];
+        if (factors[kMostBlocks + j] == kLargestFactor)
+          keep_squares_finite(static_cast<uint8_t*>(t.v) + begin + 128 * j, (int)min((int64_t)128, end - begin - 128 * j));
       }
     }
   }

@@ -25,7 +25,8 @@
 extern "C" {
 #endif
 
-/* Bytes of workspace that a sort of T tokens needs; 0 for sizes that no call takes. */
+/* Bytes of workspace that a sort of T tokens needs: 0 where it needs none (up to 6144 slots), and for sizes that no call
+ * takes. */
 size_t moe_rows_workspace(int64_t T, int32_t k, int32_t n_experts);
 
 /* counts [E], slot_pos [T, k] and row_slot [T k] (may be NULL) from idx [T, k], whose values have
@@ -42,7 +43,7 @@ moe_status moe_rows_gather(const int32_t* slot_pos, int64_t T, int32_t k, const 
                            int64_t ldx, int64_t R, void* x_rows, const uint8_t* x_scales, uint8_t* row_scales,
                            int64_t scale_bytes, const float* gates, float* row_gates, void* stream);
 
-/* moe_rows_sort and moe_rows_gather in one call: one launch for few slots, two else. */
+/* moe_rows_sort and moe_rows_gather in one call: one launch for few slots, three else. */
 moe_status moe_rows_dispatch(const void* idx, int32_t idx_bytes, int64_t T, int32_t k, int32_t n_experts, int32_t* counts,
                              int32_t* slot_pos, int32_t* row_slot, const void* x, int32_t elem_bytes, int64_t d,
                              int64_t ldx, int64_t R, void* x_rows, const uint8_t* x_scales, uint8_t* row_scales,

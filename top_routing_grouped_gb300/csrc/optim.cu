@@ -21,11 +21,11 @@ constexpr int kPer = 8;  // consecutive values of a thread; 16 threads make a bl
 
 // The step's CTAs, for moments in 32 or in 8 bits: threads, CTAs an SM, values at a time (a tile).  A chunk, what a CTA
 // takes of a tensor, has 1 to kTiles tiles (a power of two), so many that there are kFew chunks and more.
-// With moments in 32 bits HBM bounds the step whatever these are (403 M values with masters: 1741 us with 256 threads,
-// 3 CTAs and 4 tiles; 1730 with 2 CTAs, 1766 with 8 tiles, 1769-1790 with 128 threads).  With moments in 8 bits the warps
-// that an SM holds count (805 M values, no masters: 128 threads, 9 CTAs of 56 registers 1533 us, 8 of 64 1561, 7 of 72 1595,
-// 10 of 48 1612; 256 threads 4 CTAs 1571, 3 1696), and how evenly it ends (kFew of 152 * 12, 24, 48: 131 M values 307, 288,
-// 286 us, 35 M 221, 209, 209; 64, 32 and 16 tiles within 1 %).
+// With moments in 32 bits HBM bounds the step whatever these are (403 M values with masters: 1775 us with 256 threads,
+// 3 CTAs and 4 tiles; 1771 with 2 CTAs, 1781 with 8 tiles).  With moments in 8 bits the warps that an SM holds count (805 M
+// values, no masters: 128 threads, 9 CTAs of 56 registers 1545 us, although 172 bytes spill; 8 of 64 1567, 7 of 72 1615, 10 of
+// 48 1591; 256 threads 4 CTAs 1594, 3 1749), and how evenly it ends (kFew of 152 * 12, 24, 48: 131 M values 269, 269, 263 us,
+// 35 M 80, 78, 80; 64, 32 and 16 tiles within 1 %).
 template <bool kSmall>
 struct Ctas {
   static constexpr int kThreads = kSmall ? 128 : 256, kOfSm = kSmall ? 9 : 3, kTile = kThreads * kPer, kTiles = kSmall ? 32 : 4,
@@ -188,8 +188,8 @@ __device__ __forceinline__ float rcp_fast(float x) {
 
 // ------------------------------------------------------------------ two values an instruction
 
-// The step with 8-bit moments is bound by the instructions it issues as much as by HBM (57 a value, 3.1 a cycle and SM;
-// 805 M values 1.53 ms, 93 % of the copy bandwidth with fp32 gradients, 78 % with bf16 ones): its fp32 products and sums
+// The step with 8-bit moments is bound by the instructions it issues as much as by HBM (62 a value, 3.1 a cycle and SM;
+// 805 M values 1.54 ms, 93 % of the copy bandwidth with fp32 gradients, 78 % with bf16 ones): its fp32 products and sums
 // are taken two at a time (the packed forms round as the plain ones do).  With 104 a value it took 2.83 ms.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
@@ -413,9 +413,11 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Step
   }
 }
 
-// The same for values at a tensor's end, or off whole vectors: one by one.
 __device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// The same for values at a tensor's end, or off whole vectors: one by one, 2 to 3.5 times as long a value (100 M values with
+// masters and moments in 32 bits, each array one value off a 16-byte boundary: 935 us, on it 447; 134 M with moments in
+// 8 bits 943 and 270).
 template <bool kSmall>
 __device__ __noinline__ void step_rest(const Entry& t, int64_t i, int64_t end, const Step& s, const Common& k, uint8_t* factors) {
   const int left = (int)max((int64_t)0, min(end - i, (int64_t)kPer));
@@ -499,8 +501,8 @@ __device__ __noinline__ void keep_squares_finite(uint8_t* r, int n) {
 // The steps' number is read by every CTA of a call and raised by one of the last launch, after all have read it.  Each
 // draws a ticket once it has read the number, with release semantics (nothing else holds a read before an atomic on
 // another word); the CTA that draws the last one, and so knows that all have read, fences before it writes.  The draw
-// takes as long as what it waits for: the last warp does it behind the barrier (60 small tensors, clipped: 29.2 us;
-// before the barrier, or at the end, 30.6).
+// takes as long as what it waits for: the last warp does it behind the barrier (60 small tensors, clipped: 28.8 us;
+// before the barrier, or at the end, 1.4 us more).
 __device__ __forceinline__ uint32_t draw(uint32_t* ticket) {
   uint32_t n;
   asm volatile("atom.release.gpu.global.add.u32 %0, [%1], 1;" : "=r"(n) : "l"(ticket) : "memory");
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(Ctas<kSmall>::kThreads, Ctas<kSmall>::kOfSm) a
   const int64_t begin = (int64_t)(blockIdx.x - b.first[ti]) * b.chunk, end = min(begin + b.chunk, t.n);
   const int64_t whole = t.index_flags & kVec ? begin + (end - begin) / kTile * kTile : begin;
   // the first tile is on its way to L2 while the kernel before ends and the first thread works (twelve small blocks, 60
-  // tensors: 29.0 -> 27.9 us)
+  // tensors: 1.1 us of 29 less)
   if (const int64_t i = begin + threadIdx.x * kPer; i < whole) {
     prefetch(static_cast<const char*>(t.grad) + i * (t.index_flags & kGradBf16 ? 2 : 4));
     if (t.master) prefetch(t.master + i);

@@ -506,7 +506,8 @@ struct Values {
 };
 
 // Bound by HBM: 32768 tokens' four rows of 4096 bf16 and the stream back into it in 251 us, 95 % of the copy bandwidth (with
-// six CTAs an SM; four 302, eight, which spill, 356).
+// six CTAs an SM, for which 16 to 56 bytes spill; four 302, eight, for which more do, 356).  Of the others, one slot a token
+// spills 64 bytes, 128 from bf16 to fp32, and single values to bf16 28.
 // `lanes` lanes for lanes * V * C columns of one token, C pieces of V a lane: kJ rows in flight at a time, summed in the
 // slots' order.  What counts is the bytes of rows that a lane has under way: for one slot a token, four pieces of its row,
 // not one of up to four rows (16384 x 2048 bf16: 36.8 -> 23.4 us); where rows lie on 4-byte boundaries, four or eight

@@ -99,7 +99,7 @@ class AdamW:
                        [s[1] if q else None for s, q in zip(self.state, small)], [s[3] if q else None for s, q in zip(self.state, small)])
 
     def step(self, grads, lr=None, grad_factor=None, stream=None):
-        """One step with these gradients (fp32 or bf16, shaped as the parameters).  grad_factor: a tensor of shape (1,)
+        """One step with these gradients (fp32 or bf16, contiguous, shaped as the parameters).  grad_factor: a tensor of shape (1,)
         that every gradient is multiplied with (grad_norm's factor); where it is infinite or NaN nothing changes."""
         lr = self.lr if lr is None else lr
         host, device = (0.0, lr) if isinstance(lr, torch.Tensor) else (lr, None)

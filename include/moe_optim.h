@@ -5,7 +5,7 @@
  * One step of AdamW, with f the clipping factor, t the number of the step (1 the first):
  *   g = f * grad,   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
  *   p = p - lr wd p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
- * in fp32; the square root and the quotient are good to two of its steps, and a v below 2^-126 counts as 0 in them.
+ * in fp32, with 1 - lr wd taken to 2^-48; the square root and the quotient are good to two of its steps, and a v below 2^-126 counts as 0 in them.
  * Where (1 - b2) g^2 is 2^128 or more (|g| of 5.8e20 with a b2 of 0.999), v becomes infinite and the parameter may then become NaN.
  * A parameter is fp32; or bf16 with an fp32 master, which the step is taken on and the
  * parameter rounded from (to nearest); or bf16 alone, rounded stochastically.

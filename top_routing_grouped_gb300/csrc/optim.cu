@@ -383,7 +383,8 @@ __device__ __forceinline__ void step_whole(const Entry& t, int64_t i, const Step
     const float2 im = both(odd ? other : inv), iv = both(odd ? inv : other);
     // Times 2^-120 an e4m3 value has fp32's bits 27-20 for its own 7-0 but the sign's: its subnormals, below 2^-6,
     // are fp32's.  So cutting fp32's last 20 bits off, after the random ones are added, rounds both alike.  Four
-    // bits up, the value is the top byte.
+    // bits up, the value is the top byte.  (Below 2^-6 the product is rounded to 2^-29, a step's 2^-20: four bits more than
+    // the random ones.)
     constexpr float kDown = 0x1p-120f, kUp = 0x1p120f;
     uint32_t ym[kPer], yr[kPer];
 #pragma unroll
